@@ -220,6 +220,78 @@ SSD_API int ssd_conv1d_silu_backward(int64_t batch, int64_t seqlen, int64_t chan
                                      void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /*
+ * Linear attention with a decay for each head: for every batch row b and head
+ * h, with a = exp(log_decay[h]) and g = h / (H / G) the head's group,
+ *
+ *     S_t = a S_{t-1} + v_t k_t^T        ([dv x dk] state)
+ *     o_t = scale * S_t q_t
+ *
+ * from S_{-1} = state0 (or zeros), for t < n: n = lens[b] (clamped to
+ * [0, T]; NULL = T for every row).  Past a row's length o is zero, and the
+ * row's final state is the one after its last step (state0 where n = 0).
+ * Any T >= 1.  The operands' memory past a row's length is never used.
+ *
+ *   q, k          [B][T][G][dk]   `dtype`, steps and rows strided
+ *   v, dout       [B][T][H][dv]   `dtype`, steps and rows strided
+ *   o, dv         [B][T][H][dv]   `dtype`, dense
+ *   dq, dk        [B][T][G][dk]   `dtype`, dense
+ *   log_decay     [H]             fp32, <= 0 (-inf: no memory)
+ *   state0, state, dstate, dstate0  [B][H][dv][dk]  fp32, dense
+ *   lens          [B]             int32, device memory
+ *
+ * *_batch and *_step are the strides, in elements, of the first two
+ * dimensions of q, k, v and dout; they must be multiples of 16 bytes and not
+ * negative, so that views of one projection's output serve as operands (a
+ * stride of an extent of 1 is not used).  dk, dv: multiples of 8 in [8, 128].
+ * Pointers 16-byte aligned (lens 4), the workspace 256.  State and sums are
+ * fp32; deterministic, asynchronous and with the errors of ssd_forward.  The
+ * kernels' waits are bounded and report through ssd_device_status.
+ */
+typedef struct {
+  int64_t batch;    /* B in [1, 65535] */
+  int64_t seqlen;   /* T >= 1 */
+  int64_t nheads;   /* H in [1, 65535], a multiple of ngroups */
+  int64_t ngroups;  /* G >= 1 */
+  int64_t dk, dv;
+  int64_t q_batch, q_step, k_batch, k_step, v_batch, v_step;
+  int64_t dout_batch, dout_step; /* ssd_linattn_backward only */
+  float scale;
+  int32_t dtype;    /* ssd_dtype */
+} ssd_linattn_dims;
+
+/* Bytes of workspace of ssd_linattn_forward (which = 0) or
+ * ssd_linattn_backward (which = 1); 0 for dims the library rejects. */
+SSD_API size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* dims, int which);
+
+/* state0, lens, state (the final state) may be NULL. */
+SSD_API int ssd_linattn_forward(const ssd_linattn_dims* dims, const void* q, const void* k,
+                                const void* v, const float* log_decay, const float* state0,
+                                const int32_t* lens, void* o, float* state,
+                                void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* Gradients of L = sum(dout * o) + sum(dstate * state); dstate NULL = zero.
+ * state0, lens, dstate0 may be NULL.  Past a row's length the gradients are
+ * zero.  A group's dq and dk are summed over its heads in head order. */
+SSD_API int ssd_linattn_backward(const ssd_linattn_dims* dims, const void* q, const void* k,
+                                 const void* v, const float* log_decay, const float* state0,
+                                 const void* dout, const float* dstate, const int32_t* lens,
+                                 void* dq, void* dk, void* dv, float* dstate0,
+                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* The recurrence for one token of every row (dims->seqlen = 1; the step
+ * strides are not used): q, k [B][G][dk], v [B][H][dv], o [B][H][dv].
+ * decay_batch: 0, or H when log_decay is [B][H].  Row b's state is row
+ * slots[b] of state_in and state_out [nslots][H][dv][dk], or row b where
+ * slots is NULL (then nslots >= B); where slots[b] is outside [0, nslots) the
+ * row is idle: o is zero and no state is touched.  Two rows must not share a
+ * slot.  state_out may be state_in; otherwise the two must not overlap, and
+ * the rows that no slot names are not written. */
+SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const void* k,
+                             const void* v, const float* log_decay, int64_t decay_batch,
+                             const float* state_in, float* state_out, const int32_t* slots,
+                             int64_t nslots, void* o, void* cuda_stream);
+
+/*
  * Forward pass that allocates nothing (no counterpart on the pages: an
  * addition of this library for callers that cannot allocate).
  * Same inputs, outputs, layouts, errors and launch sequence as ssd_forward

@@ -10,7 +10,10 @@ from .build import build  # noqa: F401
 
 __all__ = ["build", "forward", "backward", "forward_raw", "backward_raw",
            "rmsnorm_gated_forward", "rmsnorm_gated_backward", "conv1d_silu_forward",
-           "conv1d_silu_backward", "workspace_bytes", "kernel_path", "launch_count"]
+           "conv1d_silu_backward", "workspace_bytes", "kernel_path", "launch_count",
+           "linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes"]
+
+_LAYER = ("linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes")
 
 
 def __getattr__(name):
@@ -19,4 +22,7 @@ def __getattr__(name):
                 "workspace_bytes", "kernel_path", "launch_count", "alloc_workspace", "dims_of"):
         from . import api
         return getattr(api, name)
+    if name in _LAYER:
+        from . import layer_api
+        return getattr(layer_api, name)
     raise AttributeError(name)

@@ -22,7 +22,8 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_forward", "ssd_backward", "ssd_last_error
            "ssd_selftest_wait_timeout", "ssd_forward_noalloc", "ssd_forward_raw",
            "ssd_backward_raw", "ssd_rmsnorm_gated_workspace_bytes", "ssd_rmsnorm_gated_forward",
            "ssd_rmsnorm_gated_backward", "ssd_conv1d_silu_workspace_bytes", "ssd_conv1d_silu_forward",
-           "ssd_conv1d_silu_backward")
+           "ssd_conv1d_silu_backward", "ssd_linattn_workspace_bytes", "ssd_linattn_forward",
+           "ssd_linattn_backward", "ssd_linattn_step")
 
 
 class SsdDims(ctypes.Structure):
@@ -31,6 +32,13 @@ class SsdDims(ctypes.Structure):
                 ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
                 ("chunk", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class LinattnDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in
+                 ("batch", "seqlen", "nheads", "ngroups", "dk", "dv", "q_batch", "q_step",
+                  "k_batch", "k_step", "v_batch", "v_step", "dout_batch", "dout_step")] +
+                [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)])
 
 
 class SsdError(RuntimeError):
@@ -81,6 +89,16 @@ def lib() -> ctypes.CDLL:
             L.ssd_rmsnorm_gated_backward.argtypes = [_I64, _I64, _I32, _VP, _VP, _VP, _F, _VP,
                                                      _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t,
                                                      _VP]
+            LD = ctypes.POINTER(LinattnDims)
+            L.ssd_linattn_workspace_bytes.restype = ctypes.c_size_t
+            L.ssd_linattn_workspace_bytes.argtypes = [LD, ctypes.c_int]
+            L.ssd_linattn_forward.restype = ctypes.c_int
+            L.ssd_linattn_forward.argtypes = [LD] + [_VP] * 9 + [ctypes.c_size_t, _VP]
+            L.ssd_linattn_backward.restype = ctypes.c_int
+            L.ssd_linattn_backward.argtypes = [LD] + [_VP] * 13 + [ctypes.c_size_t, _VP]
+            L.ssd_linattn_step.restype = ctypes.c_int
+            L.ssd_linattn_step.argtypes = [LD, _VP, _VP, _VP, _VP, _I64, _VP, _VP, _VP, _I64,
+                                           _VP, _VP]
             L.ssd_last_error.restype = ctypes.c_char_p
             L.ssd_last_error.argtypes = []
             L.ssd_kernel_launch_count.restype = ctypes.c_uint64

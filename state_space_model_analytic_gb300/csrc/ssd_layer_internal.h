@@ -1,0 +1,64 @@
+// Host-side descriptions of the layer operators' kernel calls (linear
+// attention, block norm, gradient clipping), shared by their C entry points
+// (ssd_layer_api.cu) and the kernel launchers.  Not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ssd {
+
+// One operand [B][T][heads][D]: the last two dimensions are dense, the others
+// have strides (in elements); head h of the walk reads head h / share.
+struct LaOperand {
+  const void* p;
+  long long batch, step;
+  int share;
+};
+
+// One walk over the steps of every (b, h): with a = e^{log_decay[h]} and the
+// steps of a row of length n taken in order (or from the last one back),
+//   o_i    = s_intra sum_{j <= i} a^{i-j} (q_i . k_j) v_j + s_carry a^{i+off} first q_i
+//   last   = a^n first + s_inject sum_j a^{n-1-j + (1-off)} v_j k_j^T
+// (i, j count in the order of the walk).  The forward is one walk; dq, dk and
+// dv are walks with the operands' roles exchanged, the last two backwards.
+struct LaWalk {
+  int B, T, H, dk, dv;
+  LaOperand q, k, v;
+  const float* log_decay;
+  const float* first;     // [B][H][dv][dk], or [B][H][dk][dv] if swapped; nullable
+  float* last;            // same layout; nullable
+  bool first_swapped;
+  const int* lens;        // [B], nullable
+  void* o;                // [B][T][H][dv], dense
+  bool o_f32;             // o is fp32 whatever the operands' type
+  float s_intra, s_carry, s_inject;
+  int off;
+  bool reverse;
+};
+
+cudaError_t la_walk(const LaWalk& w, bool bf16, cudaStream_t s);
+// out[b][t][g][:] = sum over the group's heads of part[b][t][h][:], in head order
+cudaError_t la_group_sum(long long rows, int G, int share, int D, bool bf16, const float* part,
+                         void* out, cudaStream_t s);
+
+struct LaStep {
+  int B, H, G, dk, dv;
+  const void *q, *k, *v;
+  long long q_batch, k_batch, v_batch;
+  const float* log_decay;
+  long long decay_batch;  // 0, or H: a decay for each row too
+  const float* state_in;
+  float* state_out;
+  const int* slots;       // [B] rows of the state, nullable
+  long long nslots;
+  void* o;
+  float scale;
+};
+cudaError_t la_step(const LaStep& p, bool bf16, cudaStream_t s);
+
+// The calling thread's last-error message (ssd_api.cu).
+void set_last_error(const char* msg);
+
+}  // namespace ssd

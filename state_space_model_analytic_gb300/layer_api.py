@@ -1,0 +1,211 @@
+"""Python front end of the layer operators: linear attention with a decay for
+each head.  Torch CUDA tensors in, torch tensors out; every step runs in the
+library's kernels behind the C ABI (include/ssd.h), on `stream` or the current
+stream.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _native as nat
+
+_IO_TYPES = {torch.float32: nat.SSD_F32, torch.bfloat16: nat.SSD_BF16}
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_handle(stream):
+    s = stream if stream is not None else torch.cuda.current_stream()
+    return s.cuda_stream or None
+
+
+def _keep(stream, *tensors):
+    """Memory that a call made on the current stream and uses on another one
+    is not handed out again before that other stream is done with it."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _expect(name, t, dtype, shape, device, dense=True):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _io_type(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (no CPU path exists)")
+    code = _IO_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+# ---- linear attention ------------------------------------------------------------
+
+def _rows_dense(name, t):
+    """The last two dimensions are dense: the others are passed as strides."""
+    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
+        raise ValueError(f"{name}: the last two dimensions must be contiguous")
+
+
+def _linattn_dims(q, k, v, scale, log_decay, decay_rows=False):
+    code = _io_type("q", q)
+    step = q.dim() == 3
+    if q.dim() != 4 and not (decay_rows and step):
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected "
+                         + ("[B, G, K]" if decay_rows else "[B, T, G, K]"))
+    if v.dim() != q.dim():
+        raise ValueError(f"v: {v.dim()} dimensions, expected {q.dim()}")
+    B, G, K = q.shape[0], q.shape[-2], q.shape[-1]
+    T = 1 if step else q.shape[1]
+    H, V = v.shape[-2], v.shape[-1]
+    dev = q.device
+    _expect("k", k, q.dtype, q.shape, dev, False)
+    _expect("v", v, q.dtype, (*q.shape[:-2], H, V), dev, False)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _rows_dense(name, t)
+    if not (decay_rows and log_decay.dim() == 2):
+        _expect("log_decay", log_decay, torch.float32, (H,), dev)
+    else:
+        _expect("log_decay", log_decay, torch.float32, (B, H), dev)
+    s = (lambda t: (t.stride(0), 0)) if step else (lambda t: (t.stride(0), t.stride(1)))
+    return nat.LinattnDims(B, T, H, G, K, V, *s(q), *s(k), *s(v), 0, 0, scale, code)
+
+
+def _linattn_checks(d, dev, states, lens):
+    shape = (d.batch, d.nheads, d.dv, d.dk)
+    for name, t in states:
+        if t is not None:
+            _expect(name, t, torch.float32, shape, dev)
+    if lens is not None:
+        _expect("lens", lens, torch.int32, (d.batch,), dev)
+    return shape
+
+
+def _linattn_workspace(d, which, workspace, dev):
+    if workspace is not None:
+        return workspace
+    n = nat.lib().ssd_linattn_workspace_bytes(d, which)
+    if n == 0:
+        raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "dims rejected")
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def linattn_workspace_bytes(q, k, v, log_decay, *, backward=False) -> int:
+    """Bytes of the `workspace` that linattn_forward (or _backward) takes."""
+    d = _linattn_dims(q, k, v, 1.0, log_decay)
+    n = nat.lib().ssd_linattn_workspace_bytes(d, int(backward))
+    if n == 0:
+        raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "dims rejected")
+    return n
+
+
+def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, want_state=True,
+                    out=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head over [B, T] steps:
+    S_t = exp(log_decay_h) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.
+
+    q, k [B,T,G,K], v [B,T,H,V] (fp32 or bf16; head h uses group h // (H/G);
+    the last two dimensions contiguous, the others may be strided); log_decay
+    [H] fp32, <= 0; state0 [B,H,V,K] fp32 or None (zeros); lens [B] int32 on
+    the device: row b has lens[b] steps (o is zero past them).  K and V are
+    multiples of 8 up to 128.  Returns (o [B,T,H,V], final state [B,H,V,K] or
+    None); out: dict of preallocated "o", "state"."""
+    d = _linattn_dims(q, k, v, scale, log_decay)
+    dev = q.device
+    out = {} if out is None else out
+    o, state = out.get("o"), out.get("state")
+    shape = _linattn_checks(d, dev, (("state0", state0), ("out state", state)), lens)
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    else:
+        _expect("out o", o, v.dtype, v.shape, dev)
+    if state is None and want_state:
+        state = torch.empty(shape, dtype=torch.float32, device=dev)
+    workspace = _linattn_workspace(d, 0, workspace, dev)
+    _keep(stream, o, state, workspace)
+    nat.check(nat.lib().ssd_linattn_forward(
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
+        _ptr(lens), o.data_ptr(), _ptr(state), workspace.data_ptr(), workspace.numel(),
+        _stream_handle(stream)))
+    return o, state
+
+
+def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, lens=None,
+                     want_dstate0=True, out=None, workspace=None, stream=None):
+    """Gradients of sum(do * o) + sum(dstate * state) of linattn_forward: dict
+    dq, dk, dv, dstate0 (or None).  do [B,T,H,V] may be strided like v;
+    dstate [B,H,V,K] fp32 or None (zero)."""
+    d = _linattn_dims(q, k, v, scale, log_decay)
+    dev = q.device
+    _expect("do", do, v.dtype, v.shape, dev, False)
+    _rows_dense("do", do)
+    d.dout_batch, d.dout_step = do.stride(0), do.stride(1)
+    g = dict(out) if out is not None else {}
+    shape = _linattn_checks(d, dev, (("state0", state0), ("dstate", dstate),
+                                     ("out dstate0", g.get("dstate0"))), lens)
+    for name, t in (("dq", q), ("dk", k), ("dv", v)):
+        if g.get(name) is None:
+            g[name] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+        else:
+            _expect("out " + name, g[name], t.dtype, t.shape, dev)
+    if not want_dstate0:
+        g["dstate0"] = None
+    elif g.get("dstate0") is None:
+        g["dstate0"] = torch.empty(shape, dtype=torch.float32, device=dev)
+    workspace = _linattn_workspace(d, 1, workspace, dev)
+    _keep(stream, workspace, *g.values())
+    nat.check(nat.lib().ssd_linattn_backward(
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
+        do.data_ptr(), _ptr(dstate), _ptr(lens), g["dq"].data_ptr(), g["dk"].data_ptr(),
+        g["dv"].data_ptr(), _ptr(g["dstate0"]), workspace.data_ptr(), workspace.numel(),
+        _stream_handle(stream)))
+    return g
+
+
+def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=None, out=None,
+                 stream=None):
+    """One token of every row: q, k [B,G,K], v [B,H,V]; log_decay [H], or
+    [B,H] for decays of the token; state [rows,H,V,K] fp32.  Row b's state is
+    state[slots[b]] (slots [B] int32 on the device, each row its own slot; one
+    outside the state's rows marks an idle row: its o is zero and no state
+    changes), or state[b] where slots is None.  The new states go to state_out
+    (may be `state` itself, the default is a new tensor, or `state` itself
+    with slots).  Returns (o [B,H,V], state_out).
+
+    A step of the SSD core's recurrence is this one with v = dt x, k = B,
+    q = C, log_decay = dt A, and D x added to o."""
+    d = _linattn_dims(q, k, v, scale, log_decay, True)
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [B, G, K]")
+    dev = q.device
+    rows = state.shape[0] if state.dim() else 0
+    _expect("state", state, torch.float32, (rows, d.nheads, d.dv, d.dk), dev)
+    if slots is not None:
+        _expect("slots", slots, torch.int32, (d.batch,), dev)
+    elif rows != d.batch:
+        raise ValueError(f"state: {rows} rows, expected {d.batch}")
+    if state_out is None:
+        state_out = torch.empty_like(state) if slots is None else state
+    else:
+        _expect("state_out", state_out, torch.float32, state.shape, dev)
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    else:
+        _expect("out", out, v.dtype, v.shape, dev)
+    _keep(stream, out, state_out)
+    nat.check(nat.lib().ssd_linattn_step(
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+        d.nheads if log_decay.dim() == 2 else 0, state.data_ptr(), state_out.data_ptr(),
+        _ptr(slots), rows, out.data_ptr(), _stream_handle(stream)))
+    return out, state_out

@@ -204,3 +204,24 @@ def conv_inputs(batch: int, seqlen: int, channels: int, d_conv: int, dtype: str,
     return {"x": round_to(x, dtype), "weight": round_to(w, "f32"), "bias": round_to(b, "f32"),
             "init_state": None if init is None else round_to(init, "f32"),
             "dout": round_to(g, dtype)}
+
+
+def linattn_inputs(batch: int, seqlen: int, heads: int, groups: int, dk: int, dv: int, dtype: str,
+                   seed: int, decays=None) -> dict:
+    """Linear-attention inputs: q, k [B,T,G,K], v, do [B,T,H,V] ~ N(0, 1)
+    rounded to the storage type; state0, dstate ~ N(0, 1) [B,H,V,K] fp32;
+    log_decay [H]: `decays` repeated over the heads, or log(1 - 2^-u), u ~
+    U[2, 8]."""
+    rng = np.random.Generator(np.random.PCG64(seed))
+    q = rng.standard_normal((batch, seqlen, groups, dk))
+    k = rng.standard_normal((batch, seqlen, groups, dk))
+    v = rng.standard_normal((batch, seqlen, heads, dv))
+    do = rng.standard_normal((batch, seqlen, heads, dv))
+    s0 = rng.standard_normal((batch, heads, dv, dk))
+    ds = rng.standard_normal((batch, heads, dv, dk))
+    u = rng.uniform(2.0, 8.0, size=(heads,))
+    la = np.log1p(-np.exp2(-u)) if decays is None else np.resize(np.asarray(decays, float), heads)
+    r = lambda a: round_to(a, dtype)
+    f = lambda a: round_to(a, "f32")
+    return {"q": r(q), "k": r(k), "v": r(v), "do": r(do), "state0": f(s0), "dstate": f(ds),
+            "log_decay": f(la)}

@@ -292,6 +292,76 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
                              int64_t nslots, void* o, void* cuda_stream);
 
 /*
+ * Norms before and after a block, with its gate and residual scale: after a
+ * block whose output is y,
+ *
+ *     u  = y * inv_y * w_post * silu(z)        inv_y = 1 / sqrt(mean(y^2) + eps)
+ *     r' = residual + res_scale * u
+ *     x  = r' * inv_r * w_pre                  inv_r = 1 / sqrt(mean(r'^2) + eps)
+ *
+ * r' is the new residual and x the next block's input, both formed in one
+ * pass in fp32 (x from the unrounded r') and rounded once.  z NULL: no gate
+ * (silu(z) = 1); res_scale NULL: 1.  The backward takes r' as the forward
+ * stored it, and dx, dnew (gradients that reach x and, on later paths, r';
+ * dnew NULL = 0), and returns
+ *   dresidual (= the whole gradient at r'), dy, dz, and summed over the rows
+ *   dw_post, dres_scale, dw_pre.
+ * dz is not written where z is NULL, dres_scale may be NULL.
+ *   y, z, x, dx, dy, dz                   [rows][width]  `dtype`
+ *   residual, r', dnew, dresidual         [rows][width]  `res_dtype`
+ *   w_post, res_scale, w_pre, dw_post, dres_scale, dw_pre   [width]  fp32
+ *   stats                                 [rows][2]      fp32: inv_y, inv_r
+ * y and z may be strided over the rows (y_stride, z_stride elements, at least
+ * width); everything else is dense.  width in [1, 8192]; any alignment to the
+ * elements' own size is accepted (16-byte aligned rows run fastest).
+ * res_dtype: `dtype` or SSD_F32.  stats: written by the forward (NULL = not),
+ * read by the backward (NULL = recomputed).  The workspace (256-byte aligned)
+ * is ssd_block_norm_workspace_bytes(rows, width) bytes (0 = rejected).
+ * Deterministic; errors as for ssd_forward.
+ */
+SSD_API size_t ssd_block_norm_workspace_bytes(int64_t rows, int64_t width);
+SSD_API int ssd_block_norm_forward(int64_t rows, int64_t width, int32_t dtype, int32_t res_dtype,
+                                   const void* residual, const void* y, int64_t y_stride,
+                                   const void* z, int64_t z_stride, const float* w_post,
+                                   const float* res_scale, const float* w_pre, float eps,
+                                   void* new_residual, void* x, float* stats, void* cuda_stream);
+SSD_API int ssd_block_norm_backward(int64_t rows, int64_t width, int32_t dtype, int32_t res_dtype,
+                                    const void* new_residual, const void* y, int64_t y_stride,
+                                    const void* z, int64_t z_stride, const float* w_post,
+                                    const float* res_scale, const float* w_pre, float eps,
+                                    const float* stats, const void* dx, const void* dnew,
+                                    void* dresidual, void* dy, void* dz, float* dw_post,
+                                    float* dres_scale, float* dw_pre,
+                                    void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * Global gradient norm over many tensors, and clipping by it:
+ *     n = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (n + eps)),
+ *     out = c * g
+ * tensors: a host array, read during the call.  out = g for clipping in
+ * place; otherwise the two must not overlap.  count 0 and tensors of 0
+ * elements are allowed; any alignment to the elements' own size.  max_norm >=
+ * 0 (infinity: out = g); eps >= 0.  The sum is exact to fp32 rounding for
+ * gradients of any finite magnitude (no overflow or underflow of the squares).
+ * A NaN anywhere makes n and every out NaN; an infinity makes n infinite and
+ * c = 0 (and the infinite elements NaN).  norm [1] fp32 receives n.  In place
+ * nothing is written where c = 1.  The workspace (256-byte aligned) is
+ * ssd_clip_workspace_bytes(tensors, count) bytes.  Deterministic: the order
+ * of the sums depends on the sizes alone.  Errors as for ssd_forward.
+ */
+typedef struct {
+  const void* g;
+  void* out;
+  int64_t numel;
+  int32_t dtype;    /* ssd_dtype of g and out */
+  int32_t reserved; /* must be 0 */
+} ssd_clip_tensor;
+SSD_API size_t ssd_clip_workspace_bytes(const ssd_clip_tensor* tensors, int64_t count);
+SSD_API int ssd_clip_grad_norm(const ssd_clip_tensor* tensors, int64_t count, float max_norm,
+                               float eps, float* norm, void* workspace, size_t workspace_bytes,
+                               void* cuda_stream);
+
+/*
  * Forward pass that allocates nothing (no counterpart on the pages: an
  * addition of this library for callers that cannot allocate).
  * Same inputs, outputs, layouts, errors and launch sequence as ssd_forward

@@ -11,9 +11,11 @@ from .build import build  # noqa: F401
 __all__ = ["build", "forward", "backward", "forward_raw", "backward_raw",
            "rmsnorm_gated_forward", "rmsnorm_gated_backward", "conv1d_silu_forward",
            "conv1d_silu_backward", "workspace_bytes", "kernel_path", "launch_count",
-           "linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes"]
+           "linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes",
+           "block_norm_forward", "block_norm_backward", "clip_grad_norm"]
 
-_LAYER = ("linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes")
+_LAYER = ("linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes",
+          "block_norm_forward", "block_norm_backward", "clip_grad_norm")
 
 
 def __getattr__(name):

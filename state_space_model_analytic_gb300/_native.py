@@ -23,7 +23,9 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_forward", "ssd_backward", "ssd_last_error
            "ssd_backward_raw", "ssd_rmsnorm_gated_workspace_bytes", "ssd_rmsnorm_gated_forward",
            "ssd_rmsnorm_gated_backward", "ssd_conv1d_silu_workspace_bytes", "ssd_conv1d_silu_forward",
            "ssd_conv1d_silu_backward", "ssd_linattn_workspace_bytes", "ssd_linattn_forward",
-           "ssd_linattn_backward", "ssd_linattn_step")
+           "ssd_linattn_backward", "ssd_linattn_step", "ssd_block_norm_workspace_bytes",
+           "ssd_block_norm_forward", "ssd_block_norm_backward", "ssd_clip_workspace_bytes",
+           "ssd_clip_grad_norm")
 
 
 class SsdDims(ctypes.Structure):
@@ -39,6 +41,11 @@ class LinattnDims(ctypes.Structure):
                  ("batch", "seqlen", "nheads", "ngroups", "dk", "dv", "q_batch", "q_step",
                   "k_batch", "k_step", "v_batch", "v_step", "dout_batch", "dout_step")] +
                 [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)])
+
+
+class ClipTensor(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class SsdError(RuntimeError):
@@ -99,6 +106,20 @@ def lib() -> ctypes.CDLL:
             L.ssd_linattn_step.restype = ctypes.c_int
             L.ssd_linattn_step.argtypes = [LD, _VP, _VP, _VP, _VP, _I64, _VP, _VP, _VP, _I64,
                                            _VP, _VP]
+            L.ssd_block_norm_workspace_bytes.restype = ctypes.c_size_t
+            L.ssd_block_norm_workspace_bytes.argtypes = [_I64, _I64]
+            L.ssd_block_norm_forward.restype = ctypes.c_int
+            L.ssd_block_norm_forward.argtypes = [_I64, _I64, _I32, _I32, _VP, _VP, _I64, _VP, _I64,
+                                                 _VP, _VP, _VP, _F, _VP, _VP, _VP, _VP]
+            L.ssd_block_norm_backward.restype = ctypes.c_int
+            L.ssd_block_norm_backward.argtypes = ([_I64, _I64, _I32, _I32, _VP, _VP, _I64, _VP,
+                                                   _I64, _VP, _VP, _VP, _F] + [_VP] * 10 +
+                                                  [ctypes.c_size_t, _VP])
+            CT = ctypes.c_void_p  # a packed array of ClipTensor
+            L.ssd_clip_workspace_bytes.restype = ctypes.c_size_t
+            L.ssd_clip_workspace_bytes.argtypes = [CT, _I64]
+            L.ssd_clip_grad_norm.restype = ctypes.c_int
+            L.ssd_clip_grad_norm.argtypes = [CT, _I64, _F, _F, _VP, _VP, ctypes.c_size_t, _VP]
             L.ssd_last_error.restype = ctypes.c_char_p
             L.ssd_last_error.argtypes = []
             L.ssd_kernel_launch_count.restype = ctypes.c_uint64

@@ -1,0 +1,397 @@
+// Norms before and after a block with its gate and residual scale, one pass
+// over the rows in each direction.  Per row, with mean over the width,
+//   iy = 1/sqrt(mean y^2 + eps),  n = y iy,  s = silu(z)
+//   r' = r + alpha n w_post s,    ir = 1/sqrt(mean r'^2 + eps),  x = r' ir w_pre
+// backward, from dx and dn (the gradient that reaches r' on later paths):
+//   t  = dx w_pre,  dr = dn + ir t - r' ir^3 mean(t r')
+//   e  = alpha dr,  dz = e n w_post silu'(z)
+//   q  = e s w_post,  dy = iy q - y iy^3 mean(q y)
+//   over the rows: c = sum dr n s,  dw_post = alpha c,  dalpha = w_post c,
+//   dw_pre = sum dx r' ir
+// (alpha and w_post are constants of a column, so one column sum serves both
+// of their gradients).
+//
+// Bound by memory: the forward moves r, y, z, r', x, the backward y, z, r',
+// dx, dn, dr, dy, dz, each once.  W warps hold a row, eight elements a lane in
+// registers (16-byte loads where the rows are aligned for it); a CTA of 256
+// threads or more walks groups of rows.
+#include <cuda_bf16.h>
+
+#include "ssd_common.cuh"
+#include "ssd_internal.h"
+#include "ssd_layer_internal.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kL = 8;  // elements of a lane
+
+template <int W>
+struct Shape {
+  static constexpr int kRows = W >= 8 ? 1 : 8 / W;  // rows of a CTA at a time
+  static constexpr int kThreads = kRows * W * 32;
+};
+
+// Column of element i of a lane (`lane` counts over the row's W warps): VEC
+// lanes hold 16-byte vectors that are contiguous over the lanes.
+template <typename T, bool VEC, int W>
+__device__ __forceinline__ int column(int lane, int i) {
+  constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;
+  return ((i / E) * W * 32 + lane) * E + i % E;
+}
+
+// v[i] = row[column(i)], zero past the width.  In the vector case the width is
+// a multiple of the vector; U: the type of the column rule (that of y), T: the
+// type of the row, whose vectors may be twice as long.
+template <typename U, bool VEC, int W, typename T>
+__device__ __forceinline__ void load_row(const T* row, int lane, int width, float (&v)[kL]) {
+  if constexpr (VEC) {
+    constexpr int E = 16 / (int)sizeof(U);
+#pragma unroll
+    for (int j = 0; j < kL; j += E) {
+      const int c = column<U, VEC, W>(lane, j);
+      if (c < width) {
+        if constexpr (sizeof(T) == 2) {
+          const uint4 q = *(const uint4*)(row + c);
+          const __nv_bfloat162* h = (const __nv_bfloat162*)&q;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __bfloat1622float2(h[i]);
+            v[j + 2 * i] = f.x;
+            v[j + 2 * i + 1] = f.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; i += 4) {
+            const float4 f = *(const float4*)(row + c + i);
+            v[j + i] = f.x; v[j + i + 1] = f.y; v[j + i + 2] = f.z; v[j + i + 3] = f.w;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[j + i] = 0.f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      const int c = column<U, VEC, W>(lane, i);
+      v[i] = c < width ? to_f32(row[c]) : 0.f;
+    }
+  }
+}
+
+template <typename U, bool VEC, int W, typename T>
+__device__ __forceinline__ void store_row(T* row, int lane, int width, const float (&v)[kL]) {
+  if constexpr (VEC) {
+    constexpr int E = 16 / (int)sizeof(U);
+#pragma unroll
+    for (int j = 0; j < kL; j += E) {
+      const int c = column<U, VEC, W>(lane, j);
+      if (c >= width) continue;
+      if constexpr (sizeof(T) == 2) {
+        uint4 q;
+        __nv_bfloat162* h = (__nv_bfloat162*)&q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+        *(uint4*)(row + c) = q;
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 4)
+          *(float4*)(row + c + i) = make_float4(v[j + i], v[j + i + 1], v[j + i + 2], v[j + i + 3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kL; ++i) {
+      const int c = column<U, VEC, W>(lane, i);
+      if (c < width) row[c] = from_f32<T>(v[i]);
+    }
+  }
+}
+
+// Sums of NV values over the W warps of a row, the warps' totals added in
+// order.  red: [2][rows][W][NV] floats, alternated by the caller (buf).
+template <int W, int NV>
+__device__ __forceinline__ void row_sums(float (&v)[NV], float* red, int buf, int group) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if constexpr (W > 1) {
+    const int warp = (threadIdx.x >> 5) % W;
+    float* r = red + ((buf * Shape<W>::kRows + group) * W) * NV;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) r[warp * NV + i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) t += r[j * NV + i];
+      v[i] = t;
+    }
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+template <typename T, typename TR, bool VEC, int W>
+__global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_fwd(BlockNorm p) {
+  constexpr int R = Shape<W>::kRows;
+  __shared__ float red[2 * 2 * R * W];
+  const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
+  const float inv_w = 1.f / (float)p.width;
+  const long long steps = (p.rows + R - 1) / R;
+  for (long long i = blockIdx.x; i < steps; i += gridDim.x) {
+    const long long row = i * R + group;
+    const bool in = row < p.rows;
+    const int width = in ? p.width : 0;
+    float y[kL], z[kL], r[kL], w[kL];
+    load_row<T, VEC, W>((const T*)p.y + row * p.y_stride, lane, width, y);
+    if (p.z) load_row<T, VEC, W>((const T*)p.z + row * p.z_stride, lane, width, z);
+    load_row<T, VEC, W>((const TR*)p.residual + row * p.width, lane, width, r);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int e = 0; e < kL; ++e) s[0] = fmaf(y[e], y[e], s[0]);
+    row_sums<W>(s, red, 0, group);
+    const float iy = 1.f / sqrtf(s[0] * inv_w + p.eps);
+    load_row<T, VEC, W>(p.w_post, lane, width, w);
+#pragma unroll
+    for (int e = 0; e < kL; ++e) y[e] *= iy * w[e];
+    if (p.z)
+#pragma unroll
+      for (int e = 0; e < kL; ++e) y[e] *= z[e] * sigmoid(z[e]);
+    if (p.res_scale) {
+      load_row<T, VEC, W>(p.res_scale, lane, width, w);
+#pragma unroll
+      for (int e = 0; e < kL; ++e) y[e] *= w[e];
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int e = 0; e < kL; ++e) {
+      r[e] += y[e];
+      s[0] = fmaf(r[e], r[e], s[0]);
+    }
+    row_sums<W>(s, red, 1, group);
+    const float ir = 1.f / sqrtf(s[0] * inv_w + p.eps);
+    store_row<T, VEC, W>((TR*)p.new_residual + row * p.width, lane, width, r);
+    load_row<T, VEC, W>(p.w_pre, lane, width, w);
+#pragma unroll
+    for (int e = 0; e < kL; ++e) r[e] *= ir * w[e];
+    store_row<T, VEC, W>((T*)p.x + row * p.width, lane, width, r);
+    if (p.stats && in && lane == 0) ((float2*)p.stats)[row] = make_float2(iy, ir);
+  }
+}
+
+// part: [grid][2][width] sums of dr n s and of dx r' ir over a CTA's rows.
+template <typename T, typename TR, bool VEC, int W>
+__global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(BlockNorm p) {
+  constexpr int R = Shape<W>::kRows;
+  __shared__ float red[2 * 3 * R * W];
+  extern __shared__ float cols[];  // [R][2][width], R > 1
+  const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
+  const float inv_w = 1.f / (float)p.width;
+  const long long steps = (p.rows + R - 1) / R;
+  float cp[kL], cq[kL];
+#pragma unroll
+  for (int e = 0; e < kL; ++e) cp[e] = cq[e] = 0.f;
+  for (long long i = blockIdx.x; i < steps; i += gridDim.x) {
+    const long long row = i * R + group;
+    const bool in = row < p.rows;
+    const int width = in ? p.width : 0;
+    float y[kL], z[kL], r[kL], dx[kL], dr[kL], w[kL];
+    load_row<T, VEC, W>((const T*)p.y + row * p.y_stride, lane, width, y);
+    if (p.z) load_row<T, VEC, W>((const T*)p.z + row * p.z_stride, lane, width, z);
+    load_row<T, VEC, W>((const TR*)p.residual + row * p.width, lane, width, r);
+    load_row<T, VEC, W>((const T*)p.dx + row * p.width, lane, width, dx);
+    if (p.dnew) load_row<T, VEC, W>((const TR*)p.dnew + row * p.width, lane, width, dr);
+    else
+#pragma unroll
+      for (int e = 0; e < kL; ++e) dr[e] = 0.f;
+    load_row<T, VEC, W>(p.w_pre, lane, width, w);
+    float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < kL; ++e) {
+      s[0] = fmaf(dx[e] * w[e], r[e], s[0]);
+      s[1] = fmaf(r[e], r[e], s[1]);
+      s[2] = fmaf(y[e], y[e], s[2]);
+    }
+    row_sums<W>(s, red, 0, group);
+    float ir, iy;
+    if (p.stats) {
+      const float2 st = in ? ((const float2*)p.stats)[row] : make_float2(0.f, 0.f);
+      iy = st.x;
+      ir = st.y;
+    } else {
+      ir = 1.f / sqrtf(s[1] * inv_w + p.eps);
+      iy = 1.f / sqrtf(s[2] * inv_w + p.eps);
+    }
+    const float kr = s[0] * inv_w * ir * ir * ir;
+#pragma unroll
+    for (int e = 0; e < kL; ++e) {
+      dr[e] += fmaf(ir * dx[e], w[e], -kr * r[e]);
+      cq[e] = fmaf(dx[e] * ir, r[e], cq[e]);
+    }
+    store_row<T, VEC, W>((TR*)p.dresidual + row * p.width, lane, width, dr);
+    // dx now holds dr n: n = y iy
+#pragma unroll
+    for (int e = 0; e < kL; ++e) dx[e] = dr[e] * y[e] * iy;
+    load_row<T, VEC, W>(p.w_post, lane, width, w);
+    if (p.res_scale) {
+      float al[kL];
+      load_row<T, VEC, W>(p.res_scale, lane, width, al);
+#pragma unroll
+      for (int e = 0; e < kL; ++e) w[e] *= al[e];
+    }
+    // w = alpha w_post
+    float t[1] = {0.f};
+    if (p.z) {
+      float dz[kL];
+#pragma unroll
+      for (int e = 0; e < kL; ++e) {
+        const float sg = sigmoid(z[e]);
+        dz[e] = dx[e] * w[e] * (sg * fmaf(z[e], 1.f - sg, 1.f));
+        const float g = z[e] * sg;
+        cp[e] = fmaf(dx[e], g, cp[e]);
+        dr[e] *= g * w[e];
+        t[0] = fmaf(dr[e], y[e], t[0]);
+      }
+      store_row<T, VEC, W>((T*)p.dz + row * p.width, lane, width, dz);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kL; ++e) {
+        cp[e] += dx[e];
+        dr[e] *= w[e];
+        t[0] = fmaf(dr[e], y[e], t[0]);
+      }
+    }
+    row_sums<W>(t, red + 3 * R * W, 0, group);
+    const float ky = t[0] * inv_w * iy * iy * iy;
+#pragma unroll
+    for (int e = 0; e < kL; ++e) dr[e] = fmaf(iy, dr[e], -ky * y[e]);
+    store_row<T, VEC, W>((T*)p.dy + row * p.width, lane, width, dr);
+  }
+  float* part = p.part + (size_t)blockIdx.x * 2 * p.width;
+  if constexpr (R == 1) {
+#pragma unroll
+    for (int e = 0; e < kL; ++e) {
+      const int c = column<T, VEC, W>(lane, e);
+      if (c < p.width) {
+        part[c] = cp[e];
+        part[p.width + c] = cq[e];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kL; ++e) {
+      const int c = column<T, VEC, W>(lane, e);
+      if (c < p.width) {
+        cols[(group * 2) * p.width + c] = cp[e];
+        cols[(group * 2 + 1) * p.width + c] = cq[e];
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.width; c += blockDim.x) {
+      float t = 0.f;
+      for (int g = 0; g < R; ++g) t += cols[g * 2 * p.width + c];
+      part[c] = t;
+    }
+  }
+}
+
+// The CTAs' partial rows summed in order: a CTA takes 32 columns, 32 slices of
+// the partials each, then the slices in order.
+constexpr int kSlices = 32;
+__global__ void __launch_bounds__(32 * kSlices) k_block_norm_dw(int ncta, BlockNorm p) {
+  __shared__ float sum[2][kSlices][33];
+  const int j = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + j;
+  float a = 0.f, b = 0.f;
+  if (c < p.width)
+    for (int i = sl; i < ncta; i += kSlices) {
+      a += p.part[(size_t)i * 2 * p.width + c];
+      b += p.part[((size_t)i * 2 + 1) * p.width + c];
+    }
+  sum[0][sl][j] = a;
+  sum[1][sl][j] = b;
+  __syncthreads();
+  if (sl == 0 && c < p.width) {
+    a = b = 0.f;
+    for (int i = 0; i < kSlices; ++i) {
+      a += sum[0][i][j];
+      b += sum[1][i][j];
+    }
+    p.dw_post[c] = p.res_scale ? a * p.res_scale[c] : a;
+    if (p.dres_scale) p.dres_scale[c] = a * p.w_post[c];
+    p.dw_pre[c] = b;
+  }
+}
+
+template <typename T, typename TR, bool VEC, int W>
+cudaError_t launch(const BlockNorm& p, bool backward, int* grid_out, cudaStream_t s) {
+  constexpr int R = Shape<W>::kRows;
+  const long long steps = (p.rows + R - 1) / R;
+  if (!backward) {
+    // CTAs that fit: up to 2048 threads an SM of 152
+    const long long cap = 152ll * (2048 / Shape<W>::kThreads);
+    LaunchScope ls("block_norm_fwd", s);
+    k_block_norm_fwd<T, TR, VEC, W>
+        <<<(unsigned)(steps < cap ? steps : cap), Shape<W>::kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  const int grid = (int)(steps < kBlockNormMaxCtas ? steps : kBlockNormMaxCtas);
+  *grid_out = grid;
+  const size_t smem = R > 1 ? (size_t)R * 2 * p.width * sizeof(float) : 0;
+  LaunchScope ls("block_norm_bwd", s);
+  k_block_norm_bwd<T, TR, VEC, W><<<grid, Shape<W>::kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, typename TR>
+cudaError_t launch_t(const BlockNorm& p, bool vec, bool backward, int* grid, cudaStream_t s) {
+  const int w = (p.width + 32 * kL - 1) / (32 * kL);  // warps that a row needs
+  if (vec) {
+    if (w <= 1) return launch<T, TR, true, 1>(p, backward, grid, s);
+    if (w <= 2) return launch<T, TR, true, 2>(p, backward, grid, s);
+    if (w <= 4) return launch<T, TR, true, 4>(p, backward, grid, s);
+    if (w <= 8) return launch<T, TR, true, 8>(p, backward, grid, s);
+    if (w <= 16) return launch<T, TR, true, 16>(p, backward, grid, s);
+    return launch<T, TR, true, 32>(p, backward, grid, s);
+  }
+  if (w <= 1) return launch<T, TR, false, 1>(p, backward, grid, s);
+  if (w <= 4) return launch<T, TR, false, 4>(p, backward, grid, s);
+  return launch<T, TR, false, 32>(p, backward, grid, s);
+}
+
+cudaError_t dispatch(const BlockNorm& p, bool bf16, bool res_bf16, bool backward, int* grid,
+                     cudaStream_t s) {
+  // 16-byte vectors need every row of every tensor to start on such a boundary
+  // and the width to be whole vectors
+  const int unit = bf16 ? 8 : 4;
+  bool vec = p.width % unit == 0 && p.y_stride % unit == 0 && (!p.z || p.z_stride % unit == 0);
+  const void* ptrs[] = {p.residual, p.y, p.z, p.w_post, p.res_scale, p.w_pre, p.new_residual,
+                        p.x, p.dx, p.dnew, p.dresidual, p.dy, p.dz};
+  for (const void* q : ptrs) vec = vec && ((uintptr_t)q & 15u) == 0;
+  if (!bf16) return launch_t<float, float>(p, vec, backward, grid, s);
+  if (res_bf16) return launch_t<__nv_bfloat16, __nv_bfloat16>(p, vec, backward, grid, s);
+  return launch_t<__nv_bfloat16, float>(p, vec, backward, grid, s);
+}
+
+}  // namespace
+
+cudaError_t block_norm_forward(const BlockNorm& p, bool bf16, bool res_bf16, cudaStream_t s) {
+  return dispatch(p, bf16, res_bf16, false, nullptr, s);
+}
+
+cudaError_t block_norm_backward(const BlockNorm& p, bool bf16, bool res_bf16, cudaStream_t s) {
+  int grid = 1;
+  const cudaError_t e = dispatch(p, bf16, res_bf16, true, &grid, s);
+  if (e != cudaSuccess) return e;
+  LaunchScope ls("block_norm_dw", s);
+  k_block_norm_dw<<<(p.width + 31) / 32, 32 * kSlices, 0, s>>>(grid, p);
+  return cudaGetLastError();
+}
+
+}  // namespace ssd

@@ -1,8 +1,10 @@
-// C ABI of the layer operators (linear attention): argument validation,
+// C ABI of the layer operators (linear attention, norms around a block,
+// gradient clipping): argument validation,
 // workspace carve-up and the launches of each call.  Declarations and
 // contracts: include/ssd.h.
 #include <cstdarg>
 #include <cstdio>
+#include <new>
 
 #include "../../include/ssd.h"
 #include "ssd_internal.h"
@@ -99,6 +101,73 @@ size_t la_part_bytes(const ssd_linattn_dims* d, int which) {
   return up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
 }
 
+int workspace_check(const char* who, const void* workspace, size_t bytes, size_t need) {
+  if (!workspace) return refuse(SSD_ERR_INVALID_ARG, "%s: workspace is NULL", who);
+  if ((uintptr_t)workspace & 255u)
+    return refuse(SSD_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", who);
+  if (bytes < need)
+    return refuse(SSD_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, bytes, need);
+  return SSD_OK;
+}
+
+// ---- norms around a block, gradient clipping -----------------------------------
+
+// A pointer to elements of a type, aligned to their own size.
+struct Sized {
+  const char* name;
+  const void* p;
+  int dtype;
+};
+int check_sized(const char* who, const Sized* need, int n_need, const Sized* may, int n_may) {
+  for (int i = 0; i < n_need; ++i)
+    if (!need[i].p) return refuse(SSD_ERR_INVALID_ARG, "%s: %s is NULL", who, need[i].name);
+  for (int i = 0; i < n_need + n_may; ++i) {
+    const Sized& q = i < n_need ? need[i] : may[i - n_need];
+    if ((uintptr_t)q.p & (q.dtype == SSD_BF16 ? 1u : 3u))
+      return refuse(SSD_ERR_ALIGNMENT, "%s: %s is not aligned to its elements", who, q.name);
+  }
+  return SSD_OK;
+}
+
+int norm_check(const char* who, int64_t rows, int64_t width, int32_t dtype, int32_t res_dtype,
+               int64_t y_stride, int64_t z_stride, float eps) {
+  if (rows < 1) return refuse(SSD_ERR_INVALID_ARG, "%s: rows must be >= 1", who);
+  if (dtype != SSD_F32 && dtype != SSD_BF16)
+    return refuse(SSD_ERR_INVALID_ARG, "%s: dtype %d is not SSD_F32 or SSD_BF16", who, (int)dtype);
+  if (res_dtype != SSD_F32 && res_dtype != dtype)
+    return refuse(SSD_ERR_INVALID_ARG, "%s: res_dtype must be dtype or SSD_F32", who);
+  if (width < 1 || width > 8192)
+    return refuse(SSD_ERR_UNSUPPORTED, "%s: width %lld must be in [1, 8192]", who, (long long)width);
+  if (y_stride < width || z_stride < width)
+    return refuse(SSD_ERR_INVALID_ARG, "%s: a row stride is smaller than the width", who);
+  if (!(eps >= 0.f)) return refuse(SSD_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  return SSD_OK;
+}
+
+// *used: tensors with elements, *bytes: of all of them
+int clip_check(const char* who, const ssd_clip_tensor* t, int64_t count, int* used, long long* bytes) {
+  if (count < 0 || count > (1 << 24) || (count && !t))
+    return refuse(SSD_ERR_INVALID_ARG, "%s: count must be in [0, 2^24] and tensors not NULL", who);
+  *used = 0;
+  *bytes = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const ssd_clip_tensor& x = t[i];
+    if (x.numel < 0 || x.numel > (1ll << 40) || x.reserved != 0 ||
+        (x.dtype != SSD_F32 && x.dtype != SSD_BF16))
+      return refuse(SSD_ERR_INVALID_ARG, "%s: tensor %lld: bad numel, dtype or reserved", who,
+                    (long long)i);
+    if (!x.numel) continue;
+    if (!x.g || !x.out)
+      return refuse(SSD_ERR_INVALID_ARG, "%s: tensor %lld: NULL pointer", who, (long long)i);
+    if ((((uintptr_t)x.g | (uintptr_t)x.out) & (x.dtype == SSD_BF16 ? 1u : 3u)) != 0)
+      return refuse(SSD_ERR_ALIGNMENT, "%s: tensor %lld is not aligned to its elements", who,
+                    (long long)i);
+    *used += 1;
+    *bytes += x.numel * (x.dtype == SSD_BF16 ? 2 : 4);
+  }
+  return SSD_OK;
+}
+
 }  // namespace
 }  // namespace ssd
 
@@ -123,12 +192,12 @@ int ssd_linattn_forward(const ssd_linattn_dims* d, const void* q, const void* k,
   set_last_error("");
   int rc = la_check(who, d);
   if (rc) return rc;
-  const Named need[] = {{"q", q}, {"k", k}, {"v", v}, {"o", o}, {"workspace", workspace}};
+  const Named need[] = {{"q", q}, {"k", k}, {"v", v}, {"o", o}};
   const Named may[] = {{"state0", state0}, {"state", state}};
-  if ((rc = check_pointers(who, need, 5, may, 2))) return rc;
+  if ((rc = check_pointers(who, need, 4, may, 2))) return rc;
   if (!log_decay) return refuse(SSD_ERR_INVALID_ARG, "%s: log_decay is NULL", who);
-  if (workspace_bytes < ssd_linattn_workspace_bytes(d, 0))
-    return refuse(SSD_ERR_INVALID_ARG, "%s: workspace too small", who);
+  if ((rc = workspace_check(who, workspace, workspace_bytes, ssd_linattn_workspace_bytes(d, 0))))
+    return rc;
   LaWalk w = la_base(d, log_decay, lens);
   w.dk = (int)d->dk;
   w.dv = (int)d->dv;
@@ -156,12 +225,12 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   int rc = la_check(who, d);
   if (rc) return rc;
   const Named need[] = {{"q", q},   {"k", k},   {"v", v},   {"dout", dout},
-                        {"dq", dq}, {"dk", dk}, {"dv", dv}, {"workspace", workspace}};
+                        {"dq", dq}, {"dk", dk}, {"dv", dv}};
   const Named may[] = {{"state0", state0}, {"dstate", dstate}, {"dstate0", dstate0}};
-  if ((rc = check_pointers(who, need, 8, may, 3))) return rc;
+  if ((rc = check_pointers(who, need, 7, may, 3))) return rc;
   if (!log_decay) return refuse(SSD_ERR_INVALID_ARG, "%s: log_decay is NULL", who);
-  if (workspace_bytes < ssd_linattn_workspace_bytes(d, 1))
-    return refuse(SSD_ERR_INVALID_ARG, "%s: workspace too small", who);
+  if ((rc = workspace_check(who, workspace, workspace_bytes, ssd_linattn_workspace_bytes(d, 1))))
+    return rc;
   LaOperand oq, ok, ov, og;
   if ((rc = la_operand(who, "q", d, q, d->q_batch, d->q_step, d->ngroups, d->dk, false, &oq)) ||
       (rc = la_operand(who, "k", d, k, d->k_batch, d->k_step, d->ngroups, d->dk, false, &ok)) ||
@@ -267,6 +336,148 @@ int ssd_linattn_step(const ssd_linattn_dims* d, const void* q, const void* k, co
   p.scale = d->scale;
   const cudaError_t e = la_step(p, d->dtype == SSD_BF16, (cudaStream_t)cuda_stream);
   return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
+// ---- norms around a block ------------------------------------------------------
+
+size_t ssd_block_norm_workspace_bytes(int64_t rows, int64_t width) {
+  set_last_error("");
+  if (rows < 1 || width < 1 || width > 8192) {
+    refuse(SSD_ERR_INVALID_ARG, "ssd_block_norm_workspace_bytes: rows >= 1 and width in [1, 8192]");
+    return 0;
+  }
+  return up256((size_t)kBlockNormMaxCtas * 2 * width * sizeof(float));
+}
+
+int ssd_block_norm_forward(int64_t rows, int64_t width, int32_t dtype, int32_t res_dtype,
+                           const void* residual, const void* y, int64_t y_stride, const void* z,
+                           int64_t z_stride, const float* w_post, const float* res_scale,
+                           const float* w_pre, float eps, void* new_residual, void* x,
+                           float* stats, void* cuda_stream) {
+  const char* who = "ssd_block_norm_forward";
+  set_last_error("");
+  int rc = norm_check(who, rows, width, dtype, res_dtype, y_stride, z ? z_stride : width, eps);
+  if (rc) return rc;
+  const Sized need[] = {{"residual", residual, res_dtype}, {"y", y, dtype}, {"w_post", w_post, 0},
+                        {"w_pre", w_pre, 0}, {"new_residual", new_residual, res_dtype},
+                        {"x", x, dtype}};
+  const Sized may[] = {{"z", z, dtype}, {"res_scale", res_scale, 0}};
+  if ((rc = check_sized(who, need, 6, may, 2))) return rc;
+  if (stats && ((uintptr_t)stats & 7u))
+    return refuse(SSD_ERR_ALIGNMENT, "%s: stats is not 8-byte aligned", who);
+  BlockNorm p = {};
+  p.rows = rows;
+  p.width = (int)width;
+  p.y_stride = y_stride;
+  p.z_stride = z_stride;
+  p.eps = eps;
+  p.residual = residual;
+  p.y = y;
+  p.z = z;
+  p.w_post = w_post;
+  p.res_scale = res_scale;
+  p.w_pre = w_pre;
+  p.new_residual = new_residual;
+  p.x = x;
+  p.stats = stats;
+  const cudaError_t e =
+      block_norm_forward(p, dtype == SSD_BF16, res_dtype == SSD_BF16, (cudaStream_t)cuda_stream);
+  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
+int ssd_block_norm_backward(int64_t rows, int64_t width, int32_t dtype, int32_t res_dtype,
+                            const void* new_residual, const void* y, int64_t y_stride,
+                            const void* z, int64_t z_stride, const float* w_post,
+                            const float* res_scale, const float* w_pre, float eps,
+                            const float* stats, const void* dx, const void* dnew, void* dresidual,
+                            void* dy, void* dz, float* dw_post, float* dres_scale, float* dw_pre,
+                            void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  const char* who = "ssd_block_norm_backward";
+  set_last_error("");
+  int rc = norm_check(who, rows, width, dtype, res_dtype, y_stride, z ? z_stride : width, eps);
+  if (rc) return rc;
+  const Sized need[] = {{"new_residual", new_residual, res_dtype}, {"y", y, dtype},
+                        {"w_post", w_post, 0}, {"w_pre", w_pre, 0}, {"dx", dx, dtype},
+                        {"dresidual", dresidual, res_dtype}, {"dy", dy, dtype},
+                        {"dw_post", dw_post, 0}, {"dw_pre", dw_pre, 0}};
+  const Sized may[] = {{"z", z, dtype}, {"res_scale", res_scale, 0}, {"dnew", dnew, res_dtype},
+                       {"dz", dz, dtype}, {"dres_scale", dres_scale, 0}};
+  if ((rc = check_sized(who, need, 9, may, 5))) return rc;
+  if (z && !dz) return refuse(SSD_ERR_INVALID_ARG, "%s: dz is NULL", who);
+  if (stats && ((uintptr_t)stats & 7u))
+    return refuse(SSD_ERR_ALIGNMENT, "%s: stats is not 8-byte aligned", who);
+  if ((rc = workspace_check(who, workspace, workspace_bytes,
+                            ssd_block_norm_workspace_bytes(rows, width))))
+    return rc;
+  BlockNorm p = {};
+  p.rows = rows;
+  p.width = (int)width;
+  p.y_stride = y_stride;
+  p.z_stride = z_stride;
+  p.eps = eps;
+  p.residual = new_residual;
+  p.y = y;
+  p.z = z;
+  p.w_post = w_post;
+  p.res_scale = res_scale;
+  p.w_pre = w_pre;
+  p.stats = const_cast<float*>(stats);
+  p.dx = dx;
+  p.dnew = dnew;
+  p.dresidual = dresidual;
+  p.dy = dy;
+  p.dz = dz;
+  p.dw_post = dw_post;
+  p.dres_scale = dres_scale;
+  p.dw_pre = dw_pre;
+  p.part = (float*)workspace;
+  const cudaError_t e =
+      block_norm_backward(p, dtype == SSD_BF16, res_dtype == SSD_BF16, (cudaStream_t)cuda_stream);
+  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
+// ---- gradient clipping -----------------------------------------------------------
+
+size_t ssd_clip_workspace_bytes(const ssd_clip_tensor* tensors, int64_t count) {
+  set_last_error("");
+  int used = 0;
+  long long bytes = 0;
+  if (clip_check("ssd_clip_workspace_bytes", tensors, count, &used, &bytes)) return 0;
+  const size_t launches = ((size_t)used + kClipTable - 1) / kClipTable;
+  return up256((launches ? launches : 1) * kClipMaxCtas * sizeof(double));
+}
+
+int ssd_clip_grad_norm(const ssd_clip_tensor* tensors, int64_t count, float max_norm, float eps,
+                       float* norm, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  const char* who = "ssd_clip_grad_norm";
+  set_last_error("");
+  int used = 0;
+  long long bytes = 0;
+  int rc = clip_check(who, tensors, count, &used, &bytes);
+  if (rc) return rc;
+  if (!norm) return refuse(SSD_ERR_INVALID_ARG, "%s: norm is NULL", who);
+  if ((uintptr_t)norm & 3u) return refuse(SSD_ERR_ALIGNMENT, "%s: norm is not 4-byte aligned", who);
+  if (!(max_norm >= 0.f) || !(eps >= 0.f))
+    return refuse(SSD_ERR_INVALID_ARG, "%s: max_norm and eps must be >= 0", who);
+  if ((rc = workspace_check(who, workspace, workspace_bytes,
+                            ssd_clip_workspace_bytes(tensors, count))))
+    return rc;
+  ClipEntry few[64];
+  ClipEntry* e = used <= 64 ? few : new (std::nothrow) ClipEntry[used];
+  if (!e) return refuse(SSD_ERR_INVALID_ARG, "%s: no host memory for %d tensors", who, used);
+  int n = 0;
+  for (int64_t i = 0; i < count; ++i)
+    if (tensors[i].numel)
+      e[n++] = ClipEntry{tensors[i].g, tensors[i].out, (long long)tensors[i].numel, 0,
+                         tensors[i].dtype == SSD_BF16};
+  // chunks: the least power of two from 4 KB up that makes at most four of
+  // them a CTA; a launch's chunk count stays an int
+  int shift = 12;
+  while ((bytes >> shift) > 4ll * kClipMaxCtas) ++shift;
+  const cudaError_t err = clip_grad_norm(e, used, shift, (double*)workspace, max_norm, eps, norm,
+                                         (cudaStream_t)cuda_stream);
+  if (e != few) delete[] e;
+  return err == cudaSuccess ? SSD_OK : cuda_refuse(err, who);
 }
 
 }  // extern "C"

@@ -58,6 +58,42 @@ struct LaStep {
 };
 cudaError_t la_step(const LaStep& p, bool bf16, cudaStream_t s);
 
+// Norms around a block (ssd_blocknorm.cu).  In the backward `residual` is the
+// forward's new residual.  part: [grid][2][width] column sums of the CTAs,
+// grid <= kBlockNormMaxCtas.
+constexpr int kBlockNormMaxCtas = 608;
+struct BlockNorm {
+  long long rows;
+  int width;
+  long long y_stride, z_stride;
+  float eps;
+  const void *residual, *y, *z;
+  const float *w_post, *res_scale, *w_pre;
+  void *new_residual, *x;
+  float* stats;
+  const void *dx, *dnew;
+  void *dresidual, *dy, *dz;
+  float *dw_post, *dres_scale, *dw_pre;
+  float* part;
+};
+cudaError_t block_norm_forward(const BlockNorm& p, bool bf16, bool res_bf16, cudaStream_t s);
+cudaError_t block_norm_backward(const BlockNorm& p, bool bf16, bool res_bf16, cudaStream_t s);
+
+// Gradient clipping (ssd_clip.cu): `count` tensors, none empty, cut into
+// chunks of 2^shift bytes; kClipTable tensors a launch, at most kClipMaxCtas
+// partial sums each.
+constexpr int kClipTable = 960;
+constexpr int kClipMaxCtas = 1216;
+struct ClipEntry {
+  const void* g;
+  void* out;
+  long long numel;
+  int first_chunk;  // set by the launcher
+  int bf16;
+};
+cudaError_t clip_grad_norm(const ClipEntry* e, int count, int shift, double* part, float max_norm,
+                           float eps, float* norm, cudaStream_t s);
+
 // The calling thread's last-error message (ssd_api.cu).
 void set_last_error(const char* msg);
 

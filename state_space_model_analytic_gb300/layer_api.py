@@ -1,5 +1,5 @@
 """Python front end of the layer operators: linear attention with a decay for
-each head.  Torch CUDA tensors in, torch tensors out; every step runs in the
+each head, norms around a block, gradient clipping.  Torch CUDA tensors in, torch tensors out; every step runs in the
 library's kernels behind the C ABI (include/ssd.h), on `stream` or the current
 stream.
 """
@@ -209,3 +209,147 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
         d.nheads if log_decay.dim() == 2 else 0, state.data_ptr(), state_out.data_ptr(),
         _ptr(slots), rows, out.data_ptr(), _stream_handle(stream)))
     return out, state_out
+
+
+# ---- norms around a block ----------------------------------------------------------
+
+def _rows_of(name, t, shape, dtype, dev):
+    """(tensor, stride of its rows): rows dense, the rows themselves evenly spaced."""
+    _expect(name, t, dtype, shape, dev, False)
+    width = shape[-1]
+    if t.is_contiguous():
+        return width
+    if t.stride(-1) == 1:
+        s = t.stride(-2)
+        n = s * t.shape[-2]
+        for i in range(t.dim() - 3, -1, -1):
+            if t.shape[i] > 1 and t.stride(i) != n:
+                break
+            n *= t.shape[i]
+        else:
+            if s >= width:
+                return s
+    raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+
+
+def _block_norm_args(residual, y, z, w_post, res_scale, w_pre):
+    code = _io_type("y", y)
+    dev, width = y.device, y.shape[-1]
+    if residual.dtype not in (y.dtype, torch.float32):
+        raise TypeError(f"residual: dtype {residual.dtype}, expected {y.dtype} or torch.float32")
+    _expect("residual", residual, residual.dtype, y.shape, dev)
+    ys = _rows_of("y", y, y.shape, y.dtype, dev) if y.dim() > 1 else width
+    if y.dim() == 1 and not y.is_contiguous():
+        raise ValueError("y: must be contiguous")
+    zs = 0
+    if z is not None:
+        zs = _rows_of("z", z, y.shape, y.dtype, dev) if y.dim() > 1 else width
+    for name, w in (("w_post", w_post), ("w_pre", w_pre), ("res_scale", res_scale)):
+        if w is not None:
+            _expect(name, w, torch.float32, (width,), dev)
+    rows = y.numel() // width if width else 0
+    return rows, width, code, _IO_TYPES[residual.dtype], ys, zs
+
+
+def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_stats=True, out=None,
+                       stream=None):
+    """After a block with output y: new = residual + res_scale * rmsnorm(y)
+    w_post silu(z), x = rmsnorm(new) w_pre over the last dimension (up to
+    8192).  z (the gate) and res_scale may be None.  y, z: fp32 or bf16, rows
+    evenly spaced; residual: their type or fp32.  Weights [width] fp32.
+    Returns (new residual, x, stats [..., 2] fp32 for the backward or None);
+    out: dict of preallocated "residual" (may be `residual` itself), "x"."""
+    rows, width, code, rcode, ys, zs = _block_norm_args(residual, y, z, w_post, res_scale, w_pre)
+    dev = y.device
+    out = {} if out is None else out
+    new, x = out.get("residual"), out.get("x")
+    if new is None:
+        new = torch.empty_like(residual)
+    else:
+        _expect("out residual", new, residual.dtype, y.shape, dev)
+    if x is None:
+        x = torch.empty(y.shape, dtype=y.dtype, device=dev)
+    else:
+        _expect("out x", x, y.dtype, y.shape, dev)
+    stats = torch.empty(*y.shape[:-1], 2, dtype=torch.float32, device=dev) if want_stats else None
+    _keep(stream, new, x, stats)
+    nat.check(nat.lib().ssd_block_norm_forward(
+        rows, width, code, rcode, residual.data_ptr(), y.data_ptr(), ys, _ptr(z), zs,
+        w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), new.data_ptr(),
+        x.data_ptr(), _ptr(stats), _stream_handle(stream)))
+    return new, x, stats
+
+
+def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, dnew=None,
+                        stats=None, *, out=None, workspace=None, stream=None):
+    """Gradients of sum(dx * x) + sum(dnew * new): dict dresidual, dy, dz (None
+    without z), dw_post, dres_scale, dw_pre.  new_residual is the forward's;
+    stats as the forward returned them, or None (recomputed)."""
+    rows, width, code, rcode, ys, zs = _block_norm_args(new_residual, y, z, w_post, res_scale,
+                                                        w_pre)
+    dev = y.device
+    _expect("dx", dx, y.dtype, y.shape, dev)
+    if dnew is not None:
+        _expect("dnew", dnew, new_residual.dtype, y.shape, dev)
+    if stats is not None:
+        _expect("stats", stats, torch.float32, (*y.shape[:-1], 2), dev)
+    g = dict(out) if out is not None else {}
+    for name, dt, shape in (("dresidual", new_residual.dtype, y.shape), ("dy", y.dtype, y.shape),
+                            ("dz", y.dtype, y.shape), ("dw_post", torch.float32, (width,)),
+                            ("dres_scale", torch.float32, (width,)),
+                            ("dw_pre", torch.float32, (width,))):
+        if (name == "dz" and z is None) or (name == "dres_scale" and res_scale is None):
+            g[name] = None
+        elif g.get(name) is None:
+            g[name] = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _expect("out " + name, g[name], dt, shape, dev)
+    if workspace is None:
+        n = nat.lib().ssd_block_norm_workspace_bytes(rows, width)
+        if n == 0:
+            raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "shape rejected")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _keep(stream, workspace, *g.values())
+    nat.check(nat.lib().ssd_block_norm_backward(
+        rows, width, code, rcode, new_residual.data_ptr(), y.data_ptr(), ys, _ptr(z), zs,
+        w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), _ptr(stats),
+        dx.data_ptr(), _ptr(dnew), g["dresidual"].data_ptr(), g["dy"].data_ptr(), _ptr(g["dz"]),
+        g["dw_post"].data_ptr(), _ptr(g["dres_scale"]), g["dw_pre"].data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream_handle(stream)))
+    return g
+
+
+# ---- gradient clipping ---------------------------------------------------------------
+
+def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, stream=None):
+    """Scales the gradients by min(1, max_norm / (n + eps)), n the square root
+    of the sum of all their squares; in place, or into the tensors of `out`
+    (same shapes and types).  grads: contiguous CUDA tensors, fp32 and bf16
+    mixed as they come, of any size.  Returns n, a 0-d fp32 tensor on the
+    device (nothing is synchronised).  A NaN in a gradient makes n and every
+    gradient NaN."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"out: {len(outs)} tensors, expected {len(grads)}")
+    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    table = (nat.ClipTensor * max(1, len(grads)))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        code = _io_type(f"grads[{i}]", g)
+        _expect(f"grads[{i}]", g, g.dtype, g.shape, dev)
+        if o is not g:
+            _expect(f"out[{i}]", o, g.dtype, g.shape, dev)
+        e = table[i]
+        e.g, e.out, e.numel, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), code
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    L = nat.lib()
+    if workspace is None:
+        n = L.ssd_clip_workspace_bytes(table, len(grads))
+        if n == 0:
+            raise nat.SsdError(nat.SSD_ERR_INVALID_ARG, nat.last_error() or "tensors rejected")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _keep(stream, norm, workspace)
+    nat.check(L.ssd_clip_grad_norm(table, len(grads), float(max_norm), float(eps), norm.data_ptr(),
+                                   workspace.data_ptr(), workspace.numel(),
+                                   _stream_handle(stream)))
+    return norm

@@ -5,10 +5,12 @@ Tolerances.  Every output is a sum of products; M is the same sum over
 magnitudes (the reference on |inputs|), an upper bound of the sum of the
 terms' magnitudes.  In fp32 storage an output accumulates n <= K + V + T
 rounded terms with rounded decays (a few 2^-24 each): |error| <=
-(n + 64) 2^-24 M.  In bf16 storage the chunk's scores are rounded once to bf16
-for the second product (2^-9 M at most), the output once (2^-9 |o|), and the
-state operand is carried in two bf16 parts or more (2^-17): |error| <= 1.1 *
-2^-8 M; the states, which are fp32 outputs, see only the last: 2^-16 M."""
+(n + 64) 2^-24 M.  In bf16 storage the chunk's
+scores are rounded once to bf16 for the second product and the output once,
+each by at most 2^-8 (8 significant bits) of terms that are together well
+below M, and the state operand is carried in two bf16 parts or more (2^-16):
+|error| <= 1.1 * 2^-8 M is allowed for all of it; the states, which are fp32
+outputs, see only the last: 2^-16 M."""
 import numpy as np
 import pytest
 

@@ -240,8 +240,8 @@ SSD_API int ssd_conv1d_silu_backward(int64_t batch, int64_t seqlen, int64_t chan
  *   lens          [B]             int32, device memory
  *
  * *_batch and *_step are the strides, in elements, of the first two
- * dimensions of q, k, v and dout; they must be multiples of 16 bytes and not
- * negative, so that views of one projection's output serve as operands (a
+ * dimensions of q, k, v and dout; they must be positive multiples of 16
+ * bytes, so that views of one projection's output serve as operands (a
  * stride of an extent of 1 is not used).  dk, dv: multiples of 8 in [8, 128].
  * Pointers 16-byte aligned (lens 4), the workspace 256.  State and sums are
  * fp32; deterministic, asynchronous and with the errors of ssd_forward.  The

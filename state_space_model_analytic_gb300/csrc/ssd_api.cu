@@ -10,6 +10,7 @@
 
 #include "../../include/ssd.h"
 #include "ssd_internal.h"
+#include "ssd_layer_internal.h"
 
 namespace ssd {
 
@@ -361,13 +362,15 @@ int ssd_force_kernel_path(int path) {
 
 int ssd_device_status(void) {
   g_err.clear();
-  unsigned int flag = 0, conv_flag = 0, tc64_flag = 0;
+  unsigned int flag = 0, conv_flag = 0, tc64_flag = 0, la_flag = 0;
   cudaError_t e = tc_read_and_clear_error(&flag);
   if (e == cudaSuccess) e = conv_read_and_clear_error(&conv_flag);
   if (e == cudaSuccess) e = tc64_read_and_clear_error(&tc64_flag);
+  if (e == cudaSuccess) e = la_read_and_clear_error(&la_flag);
   if (e != cudaSuccess) return cuda_fail(e, "ssd_device_status");
   flag |= conv_flag << 8;
   flag |= tc64_flag << 16;
+  flag |= la_flag << 24;
   if (flag) return fail(SSD_ERR_DEVICE_TIMEOUT, "a device-side wait gave up (flag 0x%x)", flag);
   return SSD_OK;
 }

@@ -74,8 +74,8 @@ int la_operand(const char* who, const char* name, const ssd_linattn_dims* d, con
   if (d->seqlen == 1 || one_step) step = heads * dim;
   if (d->batch == 1) batch = step * d->seqlen;
   const int64_t unit = d->dtype == SSD_BF16 ? 8 : 4;
-  if (step < 0 || batch < 0 || step % unit || batch % unit)
-    return refuse(SSD_ERR_INVALID_ARG, "%s: the strides of %s must be non-negative multiples of 16 bytes",
+  if (step <= 0 || batch <= 0 || step % unit || batch % unit)
+    return refuse(SSD_ERR_INVALID_ARG, "%s: the strides of %s must be positive multiples of 16 bytes",
                   who, name);
   if (step > (1ll << 36) || batch > (1ll << 36))
     return refuse(SSD_ERR_UNSUPPORTED, "%s: a stride of %s is too large", who, name);
@@ -94,6 +94,11 @@ LaWalk la_base(const ssd_linattn_dims* d, const float* log_decay, const int32_t*
   w.log_decay = log_decay;
   w.lens = lens;
   return w;
+}
+
+size_t la_scratch_bytes(const ssd_linattn_dims* d) {
+  return up256(sizeof(float) * la_scratch_floats((int)d->batch, (int)d->nheads, (int)d->seqlen,
+                                                 (int)d->dk, (int)d->dv, d->dtype == SSD_BF16));
 }
 
 size_t la_part_bytes(const ssd_linattn_dims* d, int which) {
@@ -182,7 +187,7 @@ size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* d, int which) {
     refuse(SSD_ERR_INVALID_ARG, "ssd_linattn_workspace_bytes: which must be 0 or 1");
     return 0;
   }
-  return 256 + la_part_bytes(d, which);
+  return 256 + la_part_bytes(d, which) + la_scratch_bytes(d);
 }
 
 int ssd_linattn_forward(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
@@ -211,7 +216,7 @@ int ssd_linattn_forward(const ssd_linattn_dims* d, const void* q, const void* k,
   w.s_intra = w.s_carry = d->scale;
   w.s_inject = 1.f;
   w.off = 1;
-  const cudaError_t e = la_walk(w, d->dtype == SSD_BF16, (cudaStream_t)cuda_stream);
+  const cudaError_t e = la_walk(w, d->dtype == SSD_BF16, (float*)workspace, (cudaStream_t)cuda_stream);
   return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
 }
 
@@ -241,7 +246,8 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   const bool bf16 = d->dtype == SSD_BF16;
   const int share = (int)(d->nheads / d->ngroups);
   const cudaStream_t s = (cudaStream_t)cuda_stream;
-  float* part = share > 1 ? (float*)workspace : nullptr;
+  float* scratch = (float*)workspace;
+  float* part = share > 1 ? (float*)((char*)workspace + la_scratch_bytes(d)) : nullptr;
   // dq: forward over (do, v, k), from the transposed state
   LaWalk w = la_base(d, log_decay, lens);
   w.dk = (int)d->dv;
@@ -256,7 +262,7 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   w.s_intra = w.s_carry = d->scale;
   w.s_inject = 1.f;
   w.off = 1;
-  cudaError_t e = la_walk(w, bf16, s);
+  cudaError_t e = la_walk(w, bf16, scratch, s);
   if (e != cudaSuccess) return cuda_refuse(e, who);
   if (part) {
     e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk, bf16, part, dq, s);
@@ -272,7 +278,7 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   w.s_inject = d->scale;
   w.off = 0;
   w.reverse = true;
-  e = la_walk(w, bf16, s);
+  e = la_walk(w, bf16, scratch, s);
   if (e != cudaSuccess) return cuda_refuse(e, who);
   if (part) {
     e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk, bf16, part, dk, s);
@@ -288,7 +294,7 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   w.last = dstate0;
   w.o = dv;
   w.o_f32 = false;
-  e = la_walk(w, bf16, s);
+  e = la_walk(w, bf16, scratch, s);
   return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
 }
 

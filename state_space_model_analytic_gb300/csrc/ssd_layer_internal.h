@@ -38,7 +38,14 @@ struct LaWalk {
   bool reverse;
 };
 
-cudaError_t la_walk(const LaWalk& w, bool bf16, cudaStream_t s);
+// scratch: la_scratch_floats() floats
+size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16);
+cudaError_t la_walk(const LaWalk& w, bool bf16, float* scratch, cudaStream_t s);
+// the bf16 walk on tensor cores (ssd_linattn_tc.cu)
+size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv);
+cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s);
+// reads and clears the kernels' device error word (a wait gave up)
+cudaError_t la_read_and_clear_error(unsigned int* out);
 // out[b][t][g][:] = sum over the group's heads of part[b][t][h][:], in head order
 cudaError_t la_group_sum(long long rows, int G, int share, int D, bool bf16, const float* part,
                          void* out, cudaStream_t s);

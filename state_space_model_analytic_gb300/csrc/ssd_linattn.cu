@@ -30,8 +30,8 @@ constexpr int kThreads = 256;
 
 // One CTA per (h, b).  Shared memory (fp32): q, k [C][dk + 1], v [C][dv + 1],
 // P [C][C + 1], S [dv][dk + 1].
-template <typename T, typename TO>
 __global__ void __launch_bounds__(kThreads) k_la_walk(LaWalk w) {
+  using T = float;
   extern __shared__ float sm[];
   const int dk = w.dk, dv = w.dv, lk = dk + 1, lv = dv + 1;
   float* Q = sm;
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(LaWalk w) {
   const T* qp = (const T*)w.q.p + b * w.q.batch + (long long)(h / w.q.share) * dk;
   const T* kp = (const T*)w.k.p + b * w.k.batch + (long long)(h / w.k.share) * dk;
   const T* vp = (const T*)w.v.p + b * w.v.batch + (long long)(h / w.v.share) * dv;
-  TO* op = (TO*)w.o + ((long long)b * w.T * w.H + h) * dv;
+  T* op = (T*)w.o + ((long long)b * w.T * w.H + h) * dv;
   const int nc = (len + kC - 1) / kC;
   for (int ci = 0; ci < nc; ++ci) {
     const int c = w.reverse ? nc - 1 - ci : ci;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(LaWalk w) {
       for (int j = 0; j < kC; ++j) s = fmaf(P[i * (kC + 1) + j], V[j * lv + v], s);
       for (int x = 0; x < dk; ++x) u = fmaf(S[v * lk + x], Q[i * lk + x], u);
       const int lead = (w.reverse ? n - 1 - i : i) + w.off;
-      op[(t0 + i) * w.H * dv + v] = from_f32<TO>(fmaf(w.s_carry * pw[lead], u, s));
+      op[(t0 + i) * w.H * dv + v] = fmaf(w.s_carry * pw[lead], u, s);
     }
     __syncthreads();
     const float an = decay_pow(la, (float)n);
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(LaWalk w) {
   }
   __syncthreads();
   for (long long i = t; i < (long long)(w.T - len) * dv; i += kThreads)
-    op[(len + i / dv) * w.H * dv + i % dv] = from_f32<TO>(0.f);
+    op[(len + i / dv) * w.H * dv + i % dv] = 0.f;
   if (w.last)
     for (int i = t; i < dv * dk; i += kThreads) {
       const int v = i / dk, k = i % dk;
@@ -180,24 +180,23 @@ cudaError_t step_t(const LaStep& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, typename TO>
-cudaError_t walk_t(const LaWalk& w, cudaStream_t s) {
+}  // namespace
+
+size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16) {
+  return bf16 ? la_tc_scratch_floats(B, H, T, dk, dv) : 0;
+}
+
+cudaError_t la_walk(const LaWalk& w, bool bf16, float* scratch, cudaStream_t s) {
+  if (bf16) return la_walk_tc(w, scratch, s);
   const size_t smem =
       sizeof(float) * ((size_t)2 * kC * (w.dk + 1) + (size_t)kC * (w.dv + 1) + kC * (kC + 1) +
                        (size_t)w.dv * (w.dk + 1));
-  cudaError_t e = cudaFuncSetAttribute(k_la_walk<T, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e =
+      cudaFuncSetAttribute(k_la_walk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(w.reverse ? "linattn_walk_back" : "linattn_walk", s);
-  k_la_walk<T, TO><<<dim3(w.H, w.B), kThreads, smem, s>>>(w);
+  k_la_walk<<<dim3(w.H, w.B), kThreads, smem, s>>>(w);
   return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t la_walk(const LaWalk& w, bool bf16, cudaStream_t s) {
-  if (!bf16) return walk_t<float, float>(w, s);
-  return w.o_f32 ? walk_t<__nv_bfloat16, float>(w, s) : walk_t<__nv_bfloat16, __nv_bfloat16>(w, s);
 }
 
 cudaError_t la_group_sum(long long rows, int G, int share, int D, bool bf16, const float* part,

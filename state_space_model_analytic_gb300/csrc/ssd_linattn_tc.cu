@@ -20,12 +20,13 @@
 // Bound by memory: a chunk moves dk, dk, dv, dv columns of 128 rows once, at
 // 45 GB/s an SM some 4100 cycles for dk = 128, dv = 64, against 1800 cycles of
 // products.  The work is split over warps so that these overlap with the
-// loads: warps 0-3 turn S into P and write o (thread = row), warps 4-7 build
-// the parts of w o V and carry X (thread = row k), one thread issues the TMA
-// loads of the next chunks, one the products.
+// loads: warps 0-7 turn S into P and write o (thread = row and half of the
+// columns), warps 8-15 build the parts of w o V and carry X (thread = row k
+// and half of the columns), one warp each issues the TMA loads of the next
+// chunks, the products of the output and those of the state.
 //
 // Rows past the end of a batch row (its length, or T) take part as zeros: TMA
-// fills what lies past T; between a shorter row's end and T warps 0-3 clear
+// fills what lies past T; between a shorter row's end and T warps 0-7 clear
 // the tile's rows before any product reads them.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -45,8 +46,9 @@ using namespace tc;
 namespace {
 
 constexpr int kQ = 128;
-constexpr int kThreads = 320;  // 4 + 4 warps, the loader and the issuer
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kThreads = 640;  // 8 + 8 warps, and four of which three issue loads and products
+constexpr long long kWaitClocks = 3000000000ll;
+constexpr uint64_t kWaitNs = 1000000000ull;  // at the end, for what is still in flight
 
 __device__ unsigned int g_la_error;
 
@@ -64,7 +66,6 @@ struct TcWalk {
   int first_swapped;
   const int* lens;
   void* o;
-  int o_f32;
   float s_intra, s_carry, s_inject;
   int off, reverse;
 };
@@ -87,14 +88,36 @@ __device__ __forceinline__ void tma_store_4d(const void* tmap, const void* src, 
       "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]: A's row i is lane i, two bf16 a column
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// The products are issued by one lane; the predicate is on the instruction and
+// not on a branch around it, so that the operands stay in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d_tmem, uint64_t a_desc,
+                                       uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+// the same with A in TMEM: its row i is lane i, two bf16 a column
+__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t issue, uint64_t* mbar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(mbar)),
+      "r"(issue)
       : "memory");
 }
 // 32 lanes x 16 columns of 32 bits from registers
@@ -109,22 +132,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// One arrival for the warp, after what its lanes did before (each lane has
+// issued the fences that its writes need).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f ? 1.f : expf(la * e); }
 
-// ---- shared memory -----------------------------------------------------------------
+// ---- shared memory and tensor memory --------------------------------------------
 
-// NS: stages of the loads; WH: buffers of half a chunk's scaled parts.  The
-// sums stay below the 227 KB of a CTA.
+// NS: stages of the loads; WH: buffers of half a chunk's scaled parts; NB: 16 KB
+// buffers that o is staged in.  The sums stay below the 227 KB of a CTA.
 template <int DK, int DV>
 struct Geom {
   static constexpr bool scale_k = DK < DV;
   static constexpr int DS = scale_k ? DK : DV;  // width of the scaled operand
   static constexpr int NS = DK + DV == 256 ? 1 : 2;
-  static constexpr int WH = DS == 64 && DK + DV != 192 ? 2 : DK < DV ? 2 : 1;
+  static constexpr int WH = DS == 64 && DK == 64 ? 2 : 1;
+  static constexpr int NB = DK == 128 && DV == 64 ? 1 : 2;
   static constexpr int QT = DK * 256, VT = DV * 256;  // bytes of 128 rows
   static constexpr int WP = DS * 128;                  // one part of half a chunk
   static constexpr int kQo = 0;
@@ -132,27 +172,38 @@ struct Geom {
   static constexpr int kVo = kKo + NS * QT;
   static constexpr int kWo = kVo + NS * VT;
   static constexpr int kXo = kWo + WH * 3 * WP;
-  static constexpr int kSo = kXo + DK * DV * 2;        // 16 KB staging of o
-  static constexpr int kBytes = kSo + 16384;
+  static constexpr int kSo = kXo + DK * DV * 2;
+  static constexpr int kBytes = kSo + NB * 16384;
   static constexpr size_t smem = kBytes + 1024;
+  // TMEM columns.  dv = 64 leaves room for P beside S (else P takes S's
+  // columns) and for the three parts' products side by side (else they are
+  // accumulated one after another).
+  static constexpr bool wide = DV == 64;
+  static constexpr int cS = 0, cP = wide ? 128 : 0, cO = wide ? 192 : 128, cC = cO + DV,
+                       cU = cC + DV;
 };
 
 struct Bars {
   uint64_t fullQ[2], fullK[2], fullV[2], emptyQ[2], emptyK[2], emptyV[2];
-  uint64_t s, p, o, ofree, x, xfree, w[2], wfree[2], u, fix, drain;
+  uint64_t s, p, o, x, xfree, w[2], wfree[2], u, fix, drain[2];
   uint32_t tmem;
   volatile int abort;
+  float pw[2 * 64 + 4];  // a^0 ... a^130
+  alignas(16) float col[32];
 };
 
-// Bounded wait that also ends when another role of the CTA has given up.
+// Bounded wait that also ends when another role of the CTA has given up.  The
+// bound is in SM clocks (about a second and a half): reading the nanosecond
+// timer takes about a microsecond, which every wait that is not over at once
+// would pay.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Bars* B) {
-  const uint64_t t0 = globaltimer_ns();
+  const long long t0 = clock64();
   for (;;) {
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (B->abort) return false;
-    if (globaltimer_ns() - t0 > kWaitNs) {
+    if (clock64() - t0 > kWaitClocks) {
       B->abort = 1;
       atomicOr(&g_la_error, 1u);
       return false;
@@ -177,8 +228,9 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     pack_bf16(f[6], f[7]));
 }
 
-// kStates: only the states (K, V, U, X), each segment from zero.
-template <int DK, int DV, bool kStates>
+// kStates: only the states (K, V, U, X), each segment from zero.  kF32: o is
+// fp32 (partial sums), else bf16.
+template <int DK, int DV, bool kStates, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   using G = Geom<DK, DV>;
@@ -199,6 +251,24 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   auto valid = [&](int c) { return min(kQ, len - c * kQ); };
   // rows of chunk c that lie past the row's end but not past T
   auto ragged = [&](int c) { return valid(c) < kQ && len < p.T; };
+  auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity, B)) != 0;
+  };
+
+  // zeros into a row of a stage: 64 bytes of each 128-byte row of each tile
+  auto clear_row = [&](int s, int row, int hf) {
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    const int at = row * 128 + hf * 64;
+#pragma unroll 1
+    for (int x = 0; x < 2 * DK / 128 * 4; ++x) {
+      const int o = (x >> 2) * 16384 + at + (x & 3) * 16;
+      if (!kStates) *(uint4*)(sm + G::kQo + s * G::QT + o) = z;
+      *(uint4*)(sm + G::kKo + s * G::QT + o) = z;
+    }
+#pragma unroll 1
+    for (int x = 0; x < 2 * DV / 128 * 4; ++x)
+      *(uint4*)(sm + G::kVo + s * G::VT + (x >> 2) * 16384 + at + (x & 3) * 16) = z;
+  };
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -206,35 +276,41 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       mbar_init(&B->fullK[i], 1);
       mbar_init(&B->fullV[i], 1);
       mbar_init(&B->emptyQ[i], 1);
-      mbar_init(&B->emptyK[i], 1);
-      mbar_init(&B->emptyV[i], 1);
-      mbar_init(&B->w[i], 128);
+      mbar_init(&B->emptyK[i], kStates ? 1 : 2);
+      mbar_init(&B->emptyV[i], kStates ? 1 : 2);
+      mbar_init(&B->w[i], 8);
       mbar_init(&B->wfree[i], 1);
+      mbar_init(&B->drain[i], 1);
     }
     mbar_init(&B->s, 1);
-    mbar_init(&B->p, 128);
+    mbar_init(&B->p, 8);
     mbar_init(&B->o, 1);
-    mbar_init(&B->ofree, 128);
-    mbar_init(&B->x, 128);
+    mbar_init(&B->x, 8);
     mbar_init(&B->xfree, 1);
     mbar_init(&B->u, 1);
-    mbar_init(&B->fix, 128);
-    mbar_init(&B->drain, 1);
+    mbar_init(&B->fix, 8);
     B->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  for (int i = tid; i < 131; i += kThreads) bars.pw[i] = decay_pow(la, (float)i);
+  if (tid >= 160 && tid < 192) {
+    const int j = tid - 160;
+    bars.col[j] = decay_pow(la, (float)(p.reverse ? j : 31 - j));
+  }
+  if (warp == 16) {
     tmem_alloc(&B->tmem, 512);
     tmem_relinquish();
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tS = B->tmem, tO = tS + 128, tC = tS + 256, tU = tS + 384;
+  const uint32_t tm = B->tmem;
+  const uint32_t tS = tm + G::cS, tP = tm + G::cP, tO = tm + G::cO, tC = tm + G::cC,
+                 tU = tm + G::cU;
 
-  if (warp == 8) {
+  if (warp == 19) {
     // ---- loads ----
-    if (tid == 8 * 32) {
+    if (tid == 19 * 32) {
       prefetch_tmap(&maps.q);
       prefetch_tmap(&maps.k);
       prefetch_tmap(&maps.v);
@@ -274,254 +350,293 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         }
       }
     }
-  } else if (warp == 9) {
-    // ---- products ----
-    if (tid == 9 * 32) {
-      const uint32_t id_s = idesc_bf16(128, 128, false, false);
-      const uint32_t id_x = idesc_bf16(128, DV, false, true);
-      const uint32_t id_u = idesc_bf16(128, DV, true, true);
-      for (int it = 0; it < nit; ++it) {
-        const int s = it % NS;
-        const uint32_t full = (it / NS) & 1, ph = it & 1;
-        const uint32_t aQ = smem_u32(sm + G::kQo + s * G::QT), aK = smem_u32(sm + G::kKo + s * G::QT);
-        const uint32_t aV = smem_u32(sm + G::kVo + s * G::VT), aX = smem_u32(sm + G::kXo);
-        if (!wait(&B->fullK[s], full, B)) break;
-        if (!kStates) {
-          if (!wait(&B->fullQ[s], full, B)) break;
-          if (ragged(chunk(it)) && !wait(&B->fix, 0, B)) break;
-          // S takes the columns of the previous chunk's P
-          if (it > 0 && !wait(&B->o, ph ^ 1, B)) break;
-          fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_bf16(tS, desc_sw128(aQ + off, 16, 1024), desc_sw128(aK + off, 16, 1024), id_s, kk > 0);
-          }
-          mma_commit(&B->s);
-          if (!wait(&B->x, ph, B)) break;
-          if (it > 0 && !wait(&B->ofree, ph ^ 1, B)) break;
-          fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_bf16(tC, desc_sw128(aQ + off, 16, 1024), desc_sw128(aX + kk * 2048, DK * 128, 1024),
-                     id_x, kk > 0);
-          }
-          mma_commit(&B->emptyQ[s]);
-          mma_commit(&B->xfree);
-        } else if (ragged(chunk(it)) && !wait(&B->fix, 0, B)) {
-          break;
-        }
-        if (!wait(&B->fullV[s], full, B)) break;
-        bool go = true;
+  } else if (warp == 17) {
+    // ---- products of the output: S, O, Oc ----
+    // The whole warp walks the loop (so that descriptors stay warp-uniform), one
+    // lane issues.  Descriptors of a tile differ in their start address alone
+    // (16-byte units): K-major steps of 16 are 2 units apart and 1024 units after
+    // every four, MN-major ones 128.
+    if (!kStates) {
+      const uint32_t lead = (tid & 31) == 0;
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t id_x = idesc_bf16(128, DV, false, true);
+      const uint64_t dQ0 = desc_sw128(smem_u32(sm + G::kQo), 16, 1024);
+      const uint64_t dK0 = desc_sw128(smem_u32(sm + G::kKo), 16, 1024);
+      const uint64_t dX = desc_sw128(smem_u32(sm + G::kXo), DK * 128, 1024);
+      const uint64_t dV0 = desc_sw128(smem_u32(sm + G::kVo), 16384, 1024);
+      // per turn: O and Oc of chunk it - 1, then S of chunk it
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const int u = 2 * it + half, wb = u % WH;
-          if (!wait(&B->w[wb], (u / WH) & 1, B)) {
-            go = false;
-            break;
-          }
+      for (int it = 0; it <= nit; ++it) {
+        if (it > 0) {
+          const int j = it - 1, s = j % NS;
+          const uint32_t ph = j & 1;
+          // P of this chunk (whose writers have read the last chunk's O and Oc)
+          if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], (j / NS) & 1)) break;
           fence_after_sync();
-          const uint32_t aW = smem_u32(sm + G::kWo + wb * 3 * G::WP);
-          // rows 64 half ... of the tile that is not scaled
-          const uint32_t aT = (G::scale_k ? aV : aK) + half * 8192;
+          const uint64_t dV = dV0 + s * (G::VT >> 4);
 #pragma unroll
-          for (int part = 0; part < 3; ++part)
+          for (int kk = 0; kk < 8; ++kk) mma_ts(lead, tO, tP + 8 * kk, dV + 128 * kk, id_x, kk > 0);
+          commit_if(lead, &B->emptyV[s]);
+          if (!all_wait(&B->x, ph)) break;
+          fence_after_sync();
+          const uint64_t dQ = dQ0 + s * (G::QT >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t dw = desc_sw128(aW + part * G::WP + kk * 2048, 8192, 1024);
-              const uint64_t dt = desc_sw128(aT + kk * 2048, 16384, 1024);
-              mma_bf16(tU, G::scale_k ? dw : dt, G::scale_k ? dt : dw, id_u,
-                       half + part + kk > 0);
-            }
-          mma_commit(&B->wfree[wb]);
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_ss(lead, tC, dQ + ((kk >> 2) * 1024 + (kk & 3) * 2), dX + 128 * kk, id_x, kk > 0);
+          commit_if(lead, &B->o);
+          commit_if(lead, &B->emptyQ[s]);
+          commit_if(lead, &B->xfree);
+          // (where S takes P's columns, the product that reads P comes first)
+          if (!G::wide && !all_wait(&B->o, ph)) break;
         }
-        if (!go) break;
-        mma_commit(&B->emptyK[s]);
-        mma_commit(&B->u);
-        if (kStates) {
-          mma_commit(&B->emptyV[s]);
-        } else {
-          if (!wait(&B->p, ph, B)) break;
+        if (it < nit) {
+          const int s = it % NS;
+          const uint32_t full = (it / NS) & 1;
+          if (!all_wait(&B->fullK[s], full) || !all_wait(&B->fullQ[s], full)) break;
+          if (ragged(chunk(it)) && !all_wait(&B->fix, 0)) break;
           fence_after_sync();
+          const uint64_t dQ = dQ0 + s * (G::QT >> 4), dK = dK0 + s * (G::QT >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tO, tS + kk * 8, desc_sw128(aV + kk * 2048, 16384, 1024), id_x, kk > 0);
-          mma_commit(&B->o);
-          mma_commit(&B->emptyV[s]);
+          for (int kk = 0; kk < DK / 16; ++kk) {
+            const int off = (kk >> 2) * 1024 + (kk & 3) * 2;
+            mma_ss(lead, tS, dQ + off, dK + off, id_s, kk > 0);
+          }
+          commit_if(lead, &B->s);
+          commit_if(lead, &B->emptyK[s]);
         }
       }
-      mma_commit(&B->drain);
-      mbar_wait(&B->drain, 0, kWaitNs);
+      commit_if(lead, &B->drain[0]);
+      mbar_wait(&B->drain[0], 0, kWaitNs);
+      __syncwarp();
     }
-  } else if (warp < 4) {
-    // ---- P and o: thread = row i of the chunk ----
-    const int row = tid, il = row & 31, ib = warp;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    // a^{|i-j|} of a column j of another 32-column block: a^(steps between the
-    // blocks' facing edges) split into a factor of the row and one of the
-    // column; inside the row's own block one factor per element
-    float col[32], diag[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      col[j] = decay_pow(la, (float)(p.reverse ? j : 31 - j));
-      const int d = p.reverse ? j - il : il - j;
-      diag[j] = d >= 0 ? p.s_intra * decay_pow(la, (float)d) : 0.f;
-    }
-    float near[3];
-#pragma unroll
-    for (int x = 0; x < 3; ++x)
-      near[x] = p.s_intra * decay_pow(la, (float)((p.reverse ? 32 - il : il + 1) + 32 * x));
-    // (after a wait that gave up the four warps still meet at their barriers,
-    // without touching the data)
-    bool ok = true;
+  } else if (warp == 18) {
+    // ---- products of the state: U ----
+    const uint32_t lead = (tid & 31) == 0;
+    constexpr uint32_t id_u = idesc_bf16(128, G::wide ? 192 : DV, true, true);
+    const uint64_t dT0 =
+        desc_sw128(smem_u32(sm + (G::scale_k ? G::kVo : G::kKo)), 16384, 1024);
+    const uint64_t dW0 = desc_sw128(smem_u32(sm + G::kWo), 8192, 1024);
     for (int it = 0; it < nit; ++it) {
+      const int s = it % NS;
+      const uint32_t full = (it / NS) & 1;
+      if (!all_wait(&B->fullK[s], full) || !all_wait(&B->fullV[s], full)) break;
+      if (ragged(chunk(it)) && !all_wait(&B->fix, 0)) break;
+      bool go = true;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int u = 2 * it + half, wb = u % WH;
+        go = go && all_wait(&B->w[wb], (u / WH) & 1);
+        if (!go) break;
+        fence_after_sync();
+        // rows 64 half ... of the tile that is not scaled
+        const uint64_t dT = dT0 + (s * ((G::scale_k ? G::VT : G::QT) >> 4) + half * 512);
+        const uint64_t dW = dW0 + wb * (3 * G::WP >> 4);
+        // dv = 64: the parts side by side, 3 x 64 columns; else one after another
+#pragma unroll
+        for (int part = 0; part < (G::wide ? 1 : 3); ++part)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t w = dW + (part * (G::WP >> 4) + kk * 128), x = dT + kk * 128;
+            mma_ss(lead, tU, G::scale_k ? w : x, G::scale_k ? x : w, id_u, half + part + kk > 0);
+          }
+        commit_if(lead, &B->wfree[wb]);
+      }
+      if (!go) break;
+      commit_if(lead, &B->u);
+      commit_if(lead, &B->emptyK[s]);
+      commit_if(lead, &B->emptyV[s]);
+    }
+    commit_if(lead, &B->drain[1]);
+    mbar_wait(&B->drain[1], 0, kWaitNs);
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---- P and o: thread = row i of the chunk and every second 32 columns ----
+    const int row = tid & 127, il = row & 31, ib = warp & 3, hf = warp >> 2;
+    const uint32_t lane_base = (uint32_t)(ib * 32) << 16;
+    // a^{|i-j|} inside the row's own 32 columns is 2^((i-j) la2), la2 of the walk's
+    // sign; bit j of `before`: step j has a part in the row.  (A decay below 2^-1e30 counts as that: its
+    // powers are 0 but for the power 0.)
+    const float la2 = fmaxf(la * 1.4426950408889634f, -1e30f) * (p.reverse ? -1.f : 1.f);
+    const float fil = (float)il;
+    const uint32_t before = p.reverse ? 0xffffffffu << il : 0xffffffffu >> (31 - il);
+    // (after a wait that gave up the warps still meet at their barriers, without
+    // touching the data)
+    bool ok = true;
+#pragma unroll 1
+    for (int it = 0; it < (kStates ? 0 : nit); ++it) {
       const int c = chunk(it), n = valid(c), s = it % NS;
       const uint32_t ph = it & 1;
       if (ragged(c)) {
         const uint32_t full = (it / NS) & 1;
-        ok = ok && wait(&B->fullK[s], full, B) && wait(&B->fullV[s], full, B) &&
-             (kStates || wait(&B->fullQ[s], full, B));
+        ok = __all_sync(0xffffffffu, ok && wait(&B->fullK[s], full, B) &&
+                                         wait(&B->fullV[s], full, B) &&
+                                         wait(&B->fullQ[s], full, B));
         if (ok) {
-          const uint4 z = make_uint4(0, 0, 0, 0);
-          if (row >= n) {
-            for (int x = 0; x < 2 * DK; x += 16) {
-              const int at = (x >> 7) * 16384 + row * 128 + (x & 127);
-              if (!kStates) *(uint4*)(sm + G::kQo + s * G::QT + at) = z;
-              *(uint4*)(sm + G::kKo + s * G::QT + at) = z;
-            }
-            for (int x = 0; x < 2 * DV; x += 16)
-              *(uint4*)(sm + G::kVo + s * G::VT + (x >> 7) * 16384 + row * 128 + (x & 127)) = z;
-          }
+          if (row >= n) clear_row(s, row, hf);
           fence_async_smem();
-          mbar_arrive(&B->fix);
+          warp_arrive(&B->fix);
         }
       }
-      if (kStates) continue;
       ok = __all_sync(0xffffffffu, ok && wait(&B->s, ph, B));
-      if (ok) {
-        fence_after_sync();
+      // a^{|i-j|}: inside the row's own 32-column block one factor an element;
+      // elsewhere the steps between the blocks' facing edges, split into a factor
+      // of the row and one of the column.  Blocks of later steps are zero.
+      fence_after_sync();
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        // (where P takes S's columns, a half's P overwrites S of its own blocks or
+        // of block 1, which the first half reads before the second half writes)
+        const int jb = G::wide ? 2 * x + hf : 2 * hf + x;
+        const int dist = p.reverse ? jb - ib : ib - jb;
+        uint32_t r[16];
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-          const int dist = p.reverse ? jb - ib : ib - jb;
-          uint32_t r[16];
-          if (dist < 0) {
+        for (int j = 0; j < 16; ++j) r[j] = 0;
+        float v[32];
+        if (ok && dist >= 0) {
+          tmem_ld32(tS + lane_base + jb * 32, v);
+          tmem_wait_ld();
+        }
+        if (!G::wide && x != hf) {
+          fence_before_sync();
+          if (hf == 0) named_arrive(2, 256);
+          else named_sync(2, 256);
+          fence_after_sync();
+        }
+        if (ok) {
+          if (dist == 0) {
+            // (selected, not multiplied by zero: a later step has no part in this
+            // row whatever its product is)
+            float fi = fil;  // (opaque: 32 factors are not to be kept from chunk to chunk)
+            uint32_t bm = before;
+            asm volatile("" : "+f"(fi), "+r"(bm));
 #pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = 0;
-          } else {
-            float v[32];
-            tmem_ld32(tS + lane_base + jb * 32, v);
-            tmem_wait_ld();
-            if (dist == 0) {
+            for (int j = 0; j < 32; ++j) {
+              const float e = ex2((fi - (float)j) * la2);
+              v[j] = ((bm >> j) & 1) ? v[j] * e : 0.f;
+            }
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float2 x = mul2(make_float2(v[2 * j], v[2 * j + 1]),
-                                make_float2(diag[2 * j], diag[2 * j + 1]));
-                // a step that comes later has no part, whatever its product is
-                if (p.reverse ? 2 * j < il : 2 * j > il) x.x = 0.f;
-                if (p.reverse ? 2 * j + 1 < il : 2 * j + 1 > il) x.y = 0.f;
-                r[j] = pack_bf16(x.x, x.y);
-              }
-            } else {
-              const float f = dist == 1 ? near[0] : dist == 2 ? near[1] : near[2];
+            for (int j = 0; j < 16; ++j) r[j] = pack_bf16(v[2 * j] * p.s_intra, v[2 * j + 1] * p.s_intra);
+          } else if (dist > 0) {
+            const float f = p.s_intra * bars.pw[(p.reverse ? 32 - il : il + 1) + 32 * (dist - 1)];
+            const float2 f2 = make_float2(f, f);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 x = mul2(mul2(make_float2(v[2 * j], v[2 * j + 1]), make_float2(f, f)),
-                                      make_float2(col[2 * j], col[2 * j + 1]));
-                r[j] = pack_bf16(x.x, x.y);
-              }
+            for (int j = 0; j < 8; ++j) {
+              const float4 g = *(const float4*)&bars.col[4 * j];
+              const float2 a0 = mul2(mul2(make_float2(v[4 * j], v[4 * j + 1]), f2), make_float2(g.x, g.y));
+              const float2 a1 = mul2(mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), f2), make_float2(g.z, g.w));
+              r[2 * j] = pack_bf16(a0.x, a0.y);
+              r[2 * j + 1] = pack_bf16(a1.x, a1.y);
             }
           }
-          tmem_st16(tS + lane_base + jb * 16, r);
+          tmem_st16(tP + lane_base + jb * 16, r);
         }
+      }
+      if (ok) {
         tmem_wait_st();
         fence_before_sync();
-        mbar_arrive(&B->p);
+        warp_arrive(&B->p);
       }
-      const int e = (p.reverse ? n - 1 - row : row) + p.off;
-      const float lead = row < n ? p.s_carry * decay_pow(la, (float)e) : 0.f;
+      const float lead = row < n ? p.s_carry * bars.pw[(p.reverse ? n - 1 - row : row) + p.off] : 0.f;
       ok = __all_sync(0xffffffffu, ok && wait(&B->o, ph, B));
       fence_after_sync();
-      uint8_t* st = sm + G::kSo;
+      // columns [c0, c0 + 16) of o
+      auto out16 = [&](int c0, float (&v)[16]) {
+        float y[16];
+        tmem_ld16(tO + lane_base + c0, v);
+        tmem_ld16(tC + lane_base + c0, y);
+        tmem_wait_ld();
+        const float2 l2 = make_float2(lead, lead);
 #pragma unroll
-      for (int x = 0; x < DV; x += 32) {
-        float v[32];
-        if (ok) {
-          float y[32];
-          tmem_ld32(tO + lane_base + x, v);
-          tmem_ld32(tC + lane_base + x, y);
-          tmem_wait_ld();
-          if (x == DV - 32) {
-            fence_before_sync();
-            mbar_arrive(&B->ofree);
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = row < n ? fmaf(lead, y[j], v[j]) : 0.f;
+        for (int j = 0; j < 16; j += 2) {
+          const float2 a = fma2(l2, make_float2(y[j], y[j + 1]), make_float2(v[j], v[j + 1]));
+          v[j] = row < n ? a.x : 0.f;
+          v[j + 1] = row < n ? a.y : 0.f;
         }
-        // 16 KB of staging: 64 columns of bf16, or 32 of fp32
-        if (p.o_f32 || x % 64 == 0) {
-          if (tid == 0) bulk_wait_read0();
-          named_sync(1, 128);
-        }
-        if (ok) {
-          if (p.o_f32) {
+      };
+      // staged in 128-byte rows: 64 columns of bf16 (both halves of the threads),
+      // or 32 of fp32 (one half; one after the other where there is one buffer)
+#pragma unroll 1
+      for (int x = 0; x < DV * (kF32 ? 2 / G::NB : 1) / 64; ++x) {
+        uint8_t* st = sm + G::kSo + (G::NB == 1 ? 0 : kF32 ? hf : x % 2) * 16384;
+        const bool turn = !kF32 || G::NB == 2 || x % 2 == hf;
+        const int x0 = kF32 && G::NB == 1 ? x * 32 : x * 64;  // first column of the round
+        if (tid == 0) bulk_wait_read0();
+        named_sync(1, 256);
+        if (ok && turn) {
+#pragma unroll 1
+          for (int z = 0; z < 2; ++z) {
+            float v[16];
+            const int ch = z * 16 + (kF32 && G::NB == 1 ? 0 : hf * 32);
+            out16(x0 + ch, v);
+            if (kF32) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *(float4*)(st + sw128(row, j)) =
-                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *(uint4*)(st + sw128(row, (x % 64) / 8 + j)) = pack8(v + 8 * j);
+              for (int j = 0; j < 4; ++j)
+                *(float4*)(st + sw128(row, z * 4 + j)) =
+                    make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            } else {
+              *(uint4*)(st + sw128(row, ch / 8)) = pack8(v);
+              *(uint4*)(st + sw128(row, ch / 8 + 1)) = pack8(v + 8);
+            }
           }
         }
-        if (p.o_f32 || x % 64 == 32) {
-          fence_async_smem();
-          named_sync(1, 128);
-          // (a box that starts past the width would start out of range)
-          const int x0 = p.o_f32 ? x : x - 32;
-          if (tid == 0 && ok && x0 < p.dv) {
-            tma_store_4d(&maps.o, st, x0, h, c * kQ, b);
-            bulk_commit();
-          }
+        fence_async_smem();
+        named_sync(1, 256);
+        // (a box that starts past the width would start out of range)
+        if (tid == 0 && ok) {
+          if (x0 < p.dv) tma_store_4d(&maps.o, sm + G::kSo + (kF32 ? 0 : G::NB == 1 ? 0 : x % 2) * 16384, x0, h, c * kQ, b);
+          if (kF32 && G::NB == 2 && x0 + 32 < p.dv)
+            tma_store_4d(&maps.o, sm + G::kSo + 16384, x0 + 32, h, c * kQ, b);
+          bulk_commit();
         }
       }
     }
     if (!kStates && tid == 0) bulk_wait0();
-  } else {
-    // ---- w o V (or K), X: thread = row j of a half, row k of the state ----
-    const int t = tid - 128, k = t;
-    const uint32_t lane_base = (uint32_t)((warp - 4) * 32) << 16;
+  } else if (warp < 16) {
+    // ---- w o V (or K): thread = row of a half and two 16-byte pieces of each 64
+    // columns; X: thread = row k of the state and every second 32 columns ----
+    const int t = tid - 256, k = t & 127, hf = t >> 7;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const bool mine = k < DK;
-    float X[DV];
+    constexpr int XN = DV / 2;  // column of X[i]: (i / 32) * 64 + hf * 32 + i % 32
+    float X[XN];
 #pragma unroll
-    for (int v = 0; v < DV; ++v) X[v] = 0.f;
+    for (int i = 0; i < XN; ++i) X[i] = 0.f;
     const size_t sbase = (((size_t)seg * p.B + b) * p.H + h) * p.dk * p.dv;
     if (!kStates && p.first && k < p.dk) {
       const float* f = p.first + sbase;
-      // (unrolled: X stays in registers)
 #pragma unroll
-      for (int v = 0; v < DV; ++v)
-        if (v < p.dv) X[v] = f[p.first_swapped ? (size_t)k * p.dv + v : (size_t)v * p.dk + k];
+      for (int i = 0; i < XN; ++i) {
+        const int v = (i / 32) * 64 + hf * 32 + i % 32;
+        if (v < p.dv) X[i] = f[p.first_swapped ? (size_t)k * p.dv + v : (size_t)v * p.dk + k];
+      }
     }
     auto put_x = [&] {
       if (mine)
 #pragma unroll
-        for (int v = 0; v < DV; v += 8)
-          *(uint4*)(sm + G::kXo + (v >> 6) * DK * 128 + sw128(k, (v & 63) >> 3)) = pack8(X + v);
+        for (int i = 0; i < XN; i += 8)
+          *(uint4*)(sm + G::kXo + (i / 32) * DK * 128 + sw128(k, hf * 4 + (i & 31) / 8)) = pack8(X + i);
       fence_async_smem();
-      mbar_arrive(&B->x);
-    };
-    if (!kStates && nit > 0) put_x();
-    auto all_wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait(bar, parity, B)) != 0;
+      warp_arrive(&B->x);
     };
     bool ok = true;
+#pragma unroll 1
     for (int it = 0; it < nit && ok; ++it) {
       const int c = chunk(it), n = valid(c), s = it % NS;
       const uint32_t full = (it / NS) & 1;
+      if (!kStates) {
+        if (it > 0 && !all_wait(&B->xfree, (it - 1) & 1)) break;
+        put_x();
+      }
       if (!all_wait(G::scale_k ? &B->fullK[s] : &B->fullV[s], full)) break;
-      if (ragged(c) && !all_wait(&B->fix, 0)) break;
+      if (ragged(c)) {
+        if (kStates) {  // (warps 0-7 do not follow a states walk's chunks)
+          if (!all_wait(G::scale_k ? &B->fullV[s] : &B->fullK[s], full)) break;
+          if (k >= n) clear_row(s, k, hf);
+          fence_async_smem();
+          warp_arrive(&B->fix);
+        }
+        if (!all_wait(&B->fix, 0)) break;
+      }
       const uint8_t* src = sm + (G::scale_k ? G::kKo + s * G::QT : G::kVo + s * G::VT);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
@@ -531,71 +646,80 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
           break;
         }
         const int r = t & 63, j = half * 64 + r;
-        const int e = (p.reverse ? j : n - 1 - j) + 1 - p.off;
-        const float w = j < n ? p.s_inject * decay_pow(la, (float)e) : 0.f;
+        const float w = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
+        const float2 w2 = make_float2(w, w);
         uint8_t* dst = sm + G::kWo + wb * 3 * G::WP;
-        // a thread takes half of the row: 32 columns of each 64
+#pragma unroll 1
+        for (int x = 0; x < G::DS / 64; ++x)
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            const int ch = (t >> 6) * 2 + q;
+            const uint4 in = *(const uint4*)(src + x * 16384 + sw128(j, ch));
+            float2 f[4];
+            unpack8(in, (float*)f);
 #pragma unroll
-        for (int x = 0; x < G::DS; x += 64)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int ch = (t >> 6) * 4 + q;
-            float f[8], m[8];
-            unpack8(*(const uint4*)(src + (x >> 6) * 16384 + sw128(j, ch)), f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= w;
+            for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
 #pragma unroll
             for (int part = 0; part < 3; ++part) {
-              const uint4 o = pack8(f);
-              *(uint4*)(dst + part * G::WP + (x >> 6) * 8192 + sw128(r, ch)) = o;
-              unpack8(o, m);
+              const uint4 o = pack8((const float*)f);
+              *(uint4*)(dst + part * G::WP + x * 8192 + sw128(r, ch)) = o;
+              float2 m[4];
+              unpack8(o, (float*)m);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] -= m[i];
+              for (int i = 0; i < 4; ++i) f[i] = fma2(m[i], make_float2(-1.f, -1.f), f[i]);
             }
           }
         fence_async_smem();
         fence_before_sync();
-        mbar_arrive(&B->w[wb]);
+        warp_arrive(&B->w[wb]);
       }
       if (!ok || !all_wait(&B->u, it & 1)) break;
       fence_after_sync();
-      const float an = decay_pow(la, (float)n);
+      const float an = bars.pw[n];
 #pragma unroll
-      for (int x = 0; x < DV; x += 32) {
-        float v[32];
-        tmem_ld32(tU + lane_base + x, v);
-        tmem_wait_ld();
+      for (int x = 0; x < XN / 16; ++x) {
+        const int col = (x / 2) * 64 + hf * 32 + (x & 1) * 16;
+        float v[16];
+        tmem_ld16(tU + lane_base + col, v);
+        if constexpr (G::wide) {
+          float m[16], l[16];
+          tmem_ld16(tU + lane_base + 64 + col, m);
+          tmem_ld16(tU + lane_base + 128 + col, l);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) X[x + i] = fmaf(an, X[x + i], v[i]);
+          for (int i = 0; i < 16; ++i) v[i] += m[i] + l[i];
+        } else {
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) X[16 * x + i] = fmaf(an, X[16 * x + i], v[i]);
       }
       fence_before_sync();
-      if (!kStates && it + 1 < nit) {
-        if (!all_wait(&B->xfree, it & 1)) break;
-        put_x();
-      }
     }
     if (p.last && k < p.dk) {
       float* l = p.last + sbase;
 #pragma unroll
-      for (int v = 0; v < DV; ++v)
-        if (v < p.dv) l[!kStates && p.first_swapped ? (size_t)k * p.dv + v : (size_t)v * p.dk + k] = X[v];
+      for (int i = 0; i < XN; ++i) {
+        const int v = (i / 32) * 64 + hf * 32 + i % 32;
+        if (v < p.dv) l[!kStates && p.first_swapped ? (size_t)k * p.dv + v : (size_t)v * p.dk + k] = X[i];
+      }
     }
   }
   if (!kStates) {
     // whole chunks of the segment past the row's end
     const int z0 = max(c1, c0) * kQ, z1 = min((c0 + p.seg_chunks) * kQ, p.T);
-    const int esz = p.o_f32 ? 4 : 2, row16 = p.dv * esz / 16;
-    for (long long i = tid; i < (long long)(z1 - z0) * row16; i += kThreads) {
-      const long long t = z0 + i / row16;
-      uint8_t* o = (uint8_t*)p.o + (((size_t)b * p.T + t) * p.H + h) * p.dv * esz;
-      *(uint4*)(o + (i % row16) * 16) = make_uint4(0, 0, 0, 0);
-    }
+    const int esz = kF32 ? 4 : 2, lane = tid & 31;
+    uint8_t* o = (uint8_t*)p.o + ((size_t)b * p.T * p.H + h) * p.dv * esz + lane * 16;
+    if (lane * 16 < p.dv * esz)
+#pragma unroll 1
+      for (int t = z0 + warp; t < z1; t += kThreads / 32)
+        *(uint4*)(o + (size_t)t * p.H * p.dv * esz) = make_uint4(0, 0, 0, 0);
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 16) {
     __syncwarp();
-    tmem_dealloc(tS, 512);
+    tmem_dealloc(tm, 512);
   }
 }
 
@@ -613,14 +737,22 @@ __global__ void __launch_bounds__(256) k_la_segments(const TcWalk p, float* seg,
   const size_t row = ((size_t)b * p.H + h) * n, stride = (size_t)p.B * p.H * n;
   const size_t at = row + (p.first_swapped ? (size_t)(i % p.dk) * p.dv + i / p.dk : (size_t)i);
   float x = first ? first[at] : 0.f;
-  for (int j = 0; j < p.nseg; ++j) {
-    const int s = p.reverse ? p.nseg - 1 - j : j;
-    const int span = p.seg_chunks * kQ;
-    const int steps = min(max(len - s * span, 0), span);
-    float* q = seg + s * stride + row + i;
-    const float local = *q;
-    *q = x;
-    x = fmaf(decay_pow(la, (float)steps), x, local);
+  const int span = p.seg_chunks * kQ;
+  for (int j0 = 0; j0 < p.nseg; j0 += 8) {
+    float local[8];  // read ahead: the loads do not wait for one another
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int s = p.reverse ? p.nseg - 1 - j0 - u : j0 + u;
+      local[u] = j0 + u < p.nseg ? seg[s * stride + row + i] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (j0 + u >= p.nseg) break;
+      const int s = p.reverse ? p.nseg - 1 - j0 - u : j0 + u;
+      const int steps = min(max(len - s * span, 0), span);
+      seg[s * stride + row + i] = x;
+      x = fmaf(decay_pow(la, (float)steps), x, local[u]);
+    }
   }
   if (last) last[at] = x;
 }
@@ -662,22 +794,23 @@ bool map_4d(CUtensorMap* m, const void* base, bool f32, int D, int heads, int T,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DK, int DV, bool kStates>
+template <int DK, int DV, bool kStates, bool kF32>
 cudaError_t launch(const Maps& m, const TcWalk& p, cudaStream_t s) {
   constexpr size_t smem = Geom<DK, DV>::smem;
   static_assert(smem + sizeof(Bars) <= 232448, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(k_la_walk_tc<DK, DV, kStates>,
+  cudaError_t e = cudaFuncSetAttribute(k_la_walk_tc<DK, DV, kStates, kF32>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(kStates ? "linattn_states" : p.reverse ? "linattn_walk_back" : "linattn_walk", s);
-  k_la_walk_tc<DK, DV, kStates><<<dim3(p.H, p.B, p.nseg), kThreads, smem, s>>>(m, p);
+  k_la_walk_tc<DK, DV, kStates, kF32><<<dim3(p.H, p.B, p.nseg), kThreads, smem, s>>>(m, p);
   return cudaGetLastError();
 }
 
-template <bool kStates>
+template <bool kStates, bool kF32>
 cudaError_t launch_d(const Maps& m, const TcWalk& p, cudaStream_t s) {
-  if (p.dk <= 64) return p.dv <= 64 ? launch<64, 64, kStates>(m, p, s) : launch<64, 128, kStates>(m, p, s);
-  return p.dv <= 64 ? launch<128, 64, kStates>(m, p, s) : launch<128, 128, kStates>(m, p, s);
+  if (p.dk <= 64)
+    return p.dv <= 64 ? launch<64, 64, kStates, kF32>(m, p, s) : launch<64, 128, kStates, kF32>(m, p, s);
+  return p.dv <= 64 ? launch<128, 64, kStates, kF32>(m, p, s) : launch<128, 128, kStates, kF32>(m, p, s);
 }
 
 }  // namespace
@@ -690,9 +823,9 @@ int la_tc_segments(int B, int H, int T) {
   auto waves = [&](long long n) { return (rows * n + sms - 1) / sms; };
   double best = (double)(waves(1) * nc);
   long long at = 1;
-  for (long long n = 2; n <= nc && n <= 64; ++n) {
+  for (long long n = 2; n <= nc && n <= 32; ++n) {
     const long long per = (nc + n - 1) / n;
-    const double cost = 1.5 * (double)(waves(n) * per) + 4.0;
+    const double cost = 1.5 * (double)(waves(n) * per) + 4.0 + 0.25 * (double)n;
     if (cost < best) {
       best = cost;
       at = n;
@@ -726,7 +859,6 @@ cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s) {
   p.log_decay = w.log_decay;
   p.lens = w.lens;
   p.o = w.o;
-  p.o_f32 = w.o_f32;
   p.s_intra = w.s_intra;
   p.s_carry = w.s_carry;
   p.s_inject = w.s_inject;
@@ -742,7 +874,7 @@ cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s) {
   p.first_swapped = w.first_swapped;
   if (n > 1) {
     p.last = scratch;
-    cudaError_t e = launch_d<true>(m, p, s);
+    cudaError_t e = launch_d<true, false>(m, p, s);
     if (e != cudaSuccess) return e;
     {
       LaunchScope ls("linattn_segments", s);
@@ -754,7 +886,7 @@ cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s) {
     p.first_swapped = 0;
     p.last = nullptr;
   }
-  return launch_d<false>(m, p, s);
+  return w.o_f32 ? launch_d<false, true>(m, p, s) : launch_d<false, false>(m, p, s);
 }
 
 cudaError_t la_read_and_clear_error(unsigned int* out) {

@@ -2,9 +2,9 @@
 // operands, fp32 state): the forward and, with exchanged roles, the gradients
 // (the formulas stand in ssd_linattn.cu).
 //
-// Chunks of 128 steps, one CTA per (head, row, segment of the row).  Per chunk,
-// with w_j the decay from step j to the chunk's end and X the state before it
-// ([dk][dv], rows k),
+// Chunks of 128 steps; one CTA per (head, 64 columns of v, row, segment of the
+// row).  Per chunk, with w_j the decay from step j to the chunk's end and X the
+// state before it ([dk][64], rows k),
 //   S  = Q K^T              128 x 128, masked and decayed into P (bf16, TMEM)
 //   O  = P V                A from TMEM
 //   Oc = Q X                X in bf16; o = O + lead_i Oc
@@ -13,17 +13,19 @@
 //
 // Precision.  P is rounded to bf16 once (the scores are the A operand of the
 // second product) and X once as an operand; the output is bf16 itself.  The
-// state is an fp32 result, so w o V is carried as three bf16 parts (hi, mid,
-// lo: 24 bits) and U is three products; the one of V and K that is narrower is
-// scaled.
+// state is an fp32 result, so w o V is carried exactly, as three bf16 parts of
+// 8 bits each, side by side in one product of 192 columns.
 //
-// Bound by memory: a chunk moves dk, dk, dv, dv columns of 128 rows once, at
-// 45 GB/s an SM some 4100 cycles for dk = 128, dv = 64, against 1800 cycles of
-// products.  The work is split over warps so that these overlap with the
-// loads: warps 0-7 turn S into P and write o (thread = row and half of the
-// columns), warps 8-15 build the parts of w o V and carry X (thread = row k
-// and half of the columns), one warp each issues the TMA loads of the next
-// chunks, the products of the output and those of the state.
+// Bound by memory: a chunk moves dk, dk, 64, 64 columns of 128 rows once, at
+// 45 GB/s an SM some 4100 cycles for dk = 128, against 1900 cycles of products
+// and 3200 of shared-memory traffic.  The work is split over warps so that it
+// overlaps with the loads and with itself: warps 0-7 turn S into P and write o
+// of the chunk before (thread = row and half of the columns), warps 8-15 build
+// the parts of w o V and carry X (thread = row k and half of the columns), one
+// warp each issues the TMA loads of the next chunks, the products of the
+// output and those of the state.  128 columns of v are two CTAs, which read q
+// and k twice (from L2) and form S twice: at 64 columns the accumulators leave
+// room for P beside S, so that S of the next chunk does not wait for P V.
 //
 // Rows past the end of a batch row (its length, or T) take part as zeros: TMA
 // fills what lies past T; between a shorter row's end and T warps 0-7 clear
@@ -129,13 +131,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 32 lanes x 8 columns
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -148,47 +157,44 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ void named_arrive(int id, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f ? 1.f : expf(la * e); }
 
 // ---- shared memory and tensor memory --------------------------------------------
 
-// NS: stages of the loads; WH: buffers of half a chunk's scaled parts; NB: 16 KB
+constexpr int kV = 64;      // columns of v of a CTA
+constexpr int kPiece = 32;  // steps of a piece of w o V
+constexpr int kDiagRow = 36;  // (16-byte pieces of 8 rows fall on all 32 banks)
+
+// NS: stages of the loads; NW: buffers of a piece's three parts; NB: 16 KB
 // buffers that o is staged in.  The sums stay below the 227 KB of a CTA.
-template <int DK, int DV>
+template <int DK, bool kStates>
 struct Geom {
-  static constexpr bool scale_k = DK < DV;
-  static constexpr int DS = scale_k ? DK : DV;  // width of the scaled operand
-  static constexpr int NS = DK + DV == 256 ? 1 : 2;
-  static constexpr int WH = DS == 64 && DK == 64 ? 2 : 1;
-  static constexpr int NB = DK == 128 && DV == 64 ? 1 : 2;
-  static constexpr int QT = DK * 256, VT = DV * 256;  // bytes of 128 rows
-  static constexpr int WP = DS * 128;                  // one part of half a chunk
+  static constexpr int NS = kStates ? 3 : 2;
+  static constexpr int NW = kStates || DK == 64 ? 4 : 2;
+  static constexpr int NB = kStates ? 0 : DK == 64 ? 2 : 1;
+  static constexpr int QT = DK * 256, VT = kV * 256;  // bytes of 128 rows
+  static constexpr int WP = kPiece * 128;              // one part of a piece
   static constexpr int kQo = 0;
-  static constexpr int kKo = kQo + NS * QT;
+  static constexpr int kKo = kStates ? 0 : NS * QT;
   static constexpr int kVo = kKo + NS * QT;
   static constexpr int kWo = kVo + NS * VT;
-  static constexpr int kXo = kWo + WH * 3 * WP;
-  static constexpr int kSo = kXo + DK * DV * 2;
-  static constexpr int kBytes = kSo + NB * 16384;
+  static constexpr int kXo = kWo + NW * 3 * WP;
+  static constexpr int kSo = kXo + (kStates ? 0 : DK * kV * 2);
+  static constexpr int kDo = kSo + NB * 16384;          // kDiagRow floats a row, 32 rows
+  static constexpr int kBytes = kDo + (kStates ? 0 : 32 * kDiagRow * 4);
   static constexpr size_t smem = kBytes + 1024;
-  // TMEM columns.  dv = 64 leaves room for P beside S (else P takes S's
-  // columns) and for the three parts' products side by side (else they are
-  // accumulated one after another).
-  static constexpr bool wide = DV == 64;
-  static constexpr int cS = 0, cP = wide ? 128 : 0, cO = wide ? 192 : 128, cC = cO + DV,
-                       cU = cC + DV;
 };
 
+// TMEM columns
+constexpr int cS = 0, cP = 128, cO = 192, cC = 256, cU = 320;
+
 struct Bars {
-  uint64_t fullQ[2], fullK[2], fullV[2], emptyQ[2], emptyK[2], emptyV[2];
-  uint64_t s, p, o, x, xfree, w[2], wfree[2], u, fix, drain[2];
+  uint64_t fullQ[3], fullK[3], fullV[3], emptyQ[3], emptyK[3], emptyV[3];
+  uint64_t w[4], wfree[4], s, sfree, p, o, ofree, x, xfree, u, fix, drain[2];
   uint32_t tmem;
   volatile int abort;
-  float pw[2 * 64 + 4];  // a^0 ... a^130
+  float pw[132];  // a^0 ... a^130
   alignas(16) float col[32];
 };
 
@@ -230,17 +236,19 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 
 // kStates: only the states (K, V, U, X), each segment from zero.  kF32: o is
 // fp32 (partial sums), else bf16.
-template <int DK, int DV, bool kStates, bool kF32>
+template <int DK, bool kStates, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
-  using G = Geom<DK, DV>;
-  constexpr int NS = G::NS, WH = G::WH;
+  using G = Geom<DK, kStates>;
+  constexpr int NS = G::NS, NW = G::NW;
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = align1024(raw);
   __shared__ Bars bars;
   Bars* B = &bars;
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int h = blockIdx.x, b = blockIdx.y, seg = blockIdx.z;
+  const int vblocks = (p.dv + kV - 1) / kV;
+  const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kV;
+  const int b = blockIdx.y, seg = blockIdx.z;
   const float la = p.log_decay[h];
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
@@ -254,7 +262,6 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   auto all_wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity, B)) != 0;
   };
-
   // zeros into a row of a stage: 64 bytes of each 128-byte row of each tile
   auto clear_row = [&](int s, int row, int hf) {
     const uint4 z = make_uint4(0, 0, 0, 0);
@@ -266,29 +273,33 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       *(uint4*)(sm + G::kKo + s * G::QT + o) = z;
     }
 #pragma unroll 1
-    for (int x = 0; x < 2 * DV / 128 * 4; ++x)
-      *(uint4*)(sm + G::kVo + s * G::VT + (x >> 2) * 16384 + at + (x & 3) * 16) = z;
+    for (int x = 0; x < 4; ++x) *(uint4*)(sm + G::kVo + s * G::VT + at + x * 16) = z;
   };
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NS; ++i) {
       mbar_init(&B->fullQ[i], 1);
       mbar_init(&B->fullK[i], 1);
       mbar_init(&B->fullV[i], 1);
       mbar_init(&B->emptyQ[i], 1);
       mbar_init(&B->emptyK[i], kStates ? 1 : 2);
       mbar_init(&B->emptyV[i], kStates ? 1 : 2);
+    }
+    for (int i = 0; i < NW; ++i) {
       mbar_init(&B->w[i], 8);
       mbar_init(&B->wfree[i], 1);
-      mbar_init(&B->drain[i], 1);
     }
     mbar_init(&B->s, 1);
+    mbar_init(&B->sfree, 8);
     mbar_init(&B->p, 8);
     mbar_init(&B->o, 1);
+    mbar_init(&B->ofree, 8);
     mbar_init(&B->x, 8);
     mbar_init(&B->xfree, 1);
     mbar_init(&B->u, 1);
     mbar_init(&B->fix, 8);
+    mbar_init(&B->drain[0], 1);
+    mbar_init(&B->drain[1], 1);
     B->abort = 0;
     fence_mbar_init();
   }
@@ -297,6 +308,13 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     const int j = tid - 160;
     bars.col[j] = decay_pow(la, (float)(p.reverse ? j : 31 - j));
   }
+  // s_intra a^{|i-j|} inside a 32 x 32 block on the diagonal, 0 for later steps
+  float* diag = (float*)(sm + G::kDo);
+  if (!kStates)
+    for (int i = tid; i < 1024; i += kThreads) {
+      const int d = p.reverse ? (i & 31) - (i >> 5) : (i >> 5) - (i & 31);
+      diag[(i >> 5) * kDiagRow + (i & 31)] = d >= 0 ? p.s_intra * decay_pow(la, (float)d) : 0.f;
+    }
   if (warp == 16) {
     tmem_alloc(&B->tmem, 512);
     tmem_relinquish();
@@ -305,8 +323,6 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   __syncthreads();
   fence_after_sync();
   const uint32_t tm = B->tmem;
-  const uint32_t tS = tm + G::cS, tP = tm + G::cP, tO = tm + G::cO, tC = tm + G::cC,
-                 tU = tm + G::cU;
 
   if (warp == 19) {
     // ---- loads ----
@@ -314,8 +330,9 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       prefetch_tmap(&maps.q);
       prefetch_tmap(&maps.k);
       prefetch_tmap(&maps.v);
-      int issued = 0;
-      for (int it = 0; it < nit; ++it) {
+      int it = 0;
+#pragma unroll 1
+      for (; it < nit; ++it) {
         const int s = it % NS, t0 = chunk(it) * kQ;
         const uint32_t free = ((it / NS) & 1) ^ 1;
         if (!wait(&B->emptyK[s], free, B)) break;
@@ -331,18 +348,15 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
             tma_load_4d(d + x * 256, &maps.q, x, h / p.qs, t0, b, &B->fullQ[s]);
         }
         if (!wait(&B->emptyV[s], free, B)) break;
-        d = sm + G::kVo + s * G::VT;
         mbar_expect_tx(&B->fullV[s], G::VT);
-        for (int x = 0; x < DV; x += 64)
-          tma_load_4d(d + x * 256, &maps.v, x, h / p.vs, t0, b, &B->fullV[s]);
-        issued = it + 1;
+        tma_load_4d(sm + G::kVo + s * G::VT, &maps.v, v0, h / p.vs, t0, b, &B->fullV[s]);
       }
       if (B->abort) {
         // no copy may be in flight when the CTA ends: those of the last stages
         // (a barrier that nothing was issued on in that phase runs out its limit)
-        for (int it = issued > NS ? issued - NS : 0; it <= issued && it < nit; ++it) {
-          const int s = it % NS;
-          const uint32_t ph = (it / NS) & 1;
+        for (int j = it > NS ? it - NS : 0; j <= it && j < nit; ++j) {
+          const int s = j % NS;
+          const uint32_t ph = (j / NS) & 1;
           const uint64_t lim = 50000000ull;
           mbar_wait(&B->fullK[s], ph, lim);
           if (!kStates) mbar_wait(&B->fullQ[s], ph, lim);
@@ -359,50 +373,51 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     if (!kStates) {
       const uint32_t lead = (tid & 31) == 0;
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t id_x = idesc_bf16(128, DV, false, true);
+      constexpr uint32_t id_x = idesc_bf16(128, kV, false, true);
       const uint64_t dQ0 = desc_sw128(smem_u32(sm + G::kQo), 16, 1024);
       const uint64_t dK0 = desc_sw128(smem_u32(sm + G::kKo), 16, 1024);
-      const uint64_t dX = desc_sw128(smem_u32(sm + G::kXo), DK * 128, 1024);
-      const uint64_t dV0 = desc_sw128(smem_u32(sm + G::kVo), 16384, 1024);
-      // per turn: O and Oc of chunk it - 1, then S of chunk it
+      const uint64_t dX = desc_sw128(smem_u32(sm + G::kXo), 16, 1024);
+      const uint64_t dV0 = desc_sw128(smem_u32(sm + G::kVo), 16, 1024);
+      // per turn: S of chunk it (once S of the last one is read), then Oc and O of
+      // chunk it - 1 (once those of the chunk before it are read)
 #pragma unroll 1
       for (int it = 0; it <= nit; ++it) {
-        if (it > 0) {
-          const int j = it - 1, s = j % NS;
-          const uint32_t ph = j & 1;
-          // P of this chunk (whose writers have read the last chunk's O and Oc)
-          if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], (j / NS) & 1)) break;
-          fence_after_sync();
-          const uint64_t dV = dV0 + s * (G::VT >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ts(lead, tO, tP + 8 * kk, dV + 128 * kk, id_x, kk > 0);
-          commit_if(lead, &B->emptyV[s]);
-          if (!all_wait(&B->x, ph)) break;
-          fence_after_sync();
-          const uint64_t dQ = dQ0 + s * (G::QT >> 4);
-#pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk)
-            mma_ss(lead, tC, dQ + ((kk >> 2) * 1024 + (kk & 3) * 2), dX + 128 * kk, id_x, kk > 0);
-          commit_if(lead, &B->o);
-          commit_if(lead, &B->emptyQ[s]);
-          commit_if(lead, &B->xfree);
-          // (where S takes P's columns, the product that reads P comes first)
-          if (!G::wide && !all_wait(&B->o, ph)) break;
-        }
         if (it < nit) {
           const int s = it % NS;
           const uint32_t full = (it / NS) & 1;
           if (!all_wait(&B->fullK[s], full) || !all_wait(&B->fullQ[s], full)) break;
           if (ragged(chunk(it)) && !all_wait(&B->fix, 0)) break;
+          if (it > 0 && !all_wait(&B->sfree, (it - 1) & 1)) break;
           fence_after_sync();
           const uint64_t dQ = dQ0 + s * (G::QT >> 4), dK = dK0 + s * (G::QT >> 4);
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk) {
             const int off = (kk >> 2) * 1024 + (kk & 3) * 2;
-            mma_ss(lead, tS, dQ + off, dK + off, id_s, kk > 0);
+            mma_ss(lead, tm + cS, dQ + off, dK + off, id_s, kk > 0);
           }
           commit_if(lead, &B->s);
           commit_if(lead, &B->emptyK[s]);
+        }
+        if (it > 0) {
+          const int j = it - 1, s = j % NS;
+          const uint32_t ph = j & 1;
+          if (!all_wait(&B->x, ph)) break;
+          if (j > 0 && !all_wait(&B->ofree, ph ^ 1)) break;
+          fence_after_sync();
+          const uint64_t dQ = dQ0 + s * (G::QT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_ss(lead, tm + cC, dQ + ((kk >> 2) * 1024 + (kk & 3) * 2), dX + 128 * kk, id_x, kk > 0);
+          commit_if(lead, &B->emptyQ[s]);
+          commit_if(lead, &B->xfree);
+          if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], (j / NS) & 1)) break;
+          fence_after_sync();
+          const uint64_t dV = dV0 + s * (G::VT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(lead, tm + cO, tm + cP + 8 * kk, dV + 128 * kk, id_x, kk > 0);
+          commit_if(lead, &B->o);
+          commit_if(lead, &B->emptyV[s]);
         }
       }
       commit_if(lead, &B->drain[0]);
@@ -410,35 +425,28 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       __syncwarp();
     }
   } else if (warp == 18) {
-    // ---- products of the state: U ----
+    // ---- products of the state: U, the parts side by side (3 x 64 columns) ----
     const uint32_t lead = (tid & 31) == 0;
-    constexpr uint32_t id_u = idesc_bf16(128, G::wide ? 192 : DV, true, true);
-    const uint64_t dT0 =
-        desc_sw128(smem_u32(sm + (G::scale_k ? G::kVo : G::kKo)), 16384, 1024);
-    const uint64_t dW0 = desc_sw128(smem_u32(sm + G::kWo), 8192, 1024);
+    constexpr uint32_t id_u = idesc_bf16(128, 3 * kV, true, true);
+    const uint64_t dK0 = desc_sw128(smem_u32(sm + G::kKo), 16384, 1024);
+    const uint64_t dW0 = desc_sw128(smem_u32(sm + G::kWo), G::WP, 1024);
+#pragma unroll 1
     for (int it = 0; it < nit; ++it) {
       const int s = it % NS;
-      const uint32_t full = (it / NS) & 1;
-      if (!all_wait(&B->fullK[s], full) || !all_wait(&B->fullV[s], full)) break;
+      if (!all_wait(&B->fullK[s], (it / NS) & 1)) break;
       if (ragged(chunk(it)) && !all_wait(&B->fix, 0)) break;
       bool go = true;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int u = 2 * it + half, wb = u % WH;
-        go = go && all_wait(&B->w[wb], (u / WH) & 1);
+      for (int piece = 0; piece < 4; ++piece) {
+        const int wb = piece % NW;
+        go = go && all_wait(&B->w[wb], (it * (4 / NW) + piece / NW) & 1);
         if (!go) break;
         fence_after_sync();
-        // rows 64 half ... of the tile that is not scaled
-        const uint64_t dT = dT0 + (s * ((G::scale_k ? G::VT : G::QT) >> 4) + half * 512);
+        const uint64_t dK = dK0 + (s * (G::QT >> 4) + piece * (kPiece * 8));
         const uint64_t dW = dW0 + wb * (3 * G::WP >> 4);
-        // dv = 64: the parts side by side, 3 x 64 columns; else one after another
 #pragma unroll
-        for (int part = 0; part < (G::wide ? 1 : 3); ++part)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t w = dW + (part * (G::WP >> 4) + kk * 128), x = dT + kk * 128;
-            mma_ss(lead, tU, G::scale_k ? w : x, G::scale_k ? x : w, id_u, half + part + kk > 0);
-          }
+        for (int kk = 0; kk < kPiece / 16; ++kk)
+          mma_ss(lead, tm + cU, dK + 128 * kk, dW + 128 * kk, id_u, piece + kk > 0);
         commit_if(lead, &B->wfree[wb]);
       }
       if (!go) break;
@@ -453,70 +461,56 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     // ---- P and o: thread = row i of the chunk and every second 32 columns ----
     const int row = tid & 127, il = row & 31, ib = warp & 3, hf = warp >> 2;
     const uint32_t lane_base = (uint32_t)(ib * 32) << 16;
-    // a^{|i-j|} inside the row's own 32 columns is 2^((i-j) la2), la2 of the walk's
-    // sign; bit j of `before`: step j has a part in the row.  (A decay below 2^-1e30 counts as that: its
-    // powers are 0 but for the power 0.)
-    const float la2 = fmaxf(la * 1.4426950408889634f, -1e30f) * (p.reverse ? -1.f : 1.f);
-    const float fil = (float)il;
-    const uint32_t before = p.reverse ? 0xffffffffu << il : 0xffffffffu >> (31 - il);
-    // (after a wait that gave up the warps still meet at their barriers, without
-    // touching the data)
+    // per turn: P of chunk it, then o of chunk it - 1.  (After a wait that gave up
+    // the warps still meet at their barriers, without touching the data.)
     bool ok = true;
 #pragma unroll 1
-    for (int it = 0; it < (kStates ? 0 : nit); ++it) {
-      const int c = chunk(it), n = valid(c), s = it % NS;
-      const uint32_t ph = it & 1;
-      if (ragged(c)) {
-        const uint32_t full = (it / NS) & 1;
-        ok = __all_sync(0xffffffffu, ok && wait(&B->fullK[s], full, B) &&
-                                         wait(&B->fullV[s], full, B) &&
-                                         wait(&B->fullQ[s], full, B));
-        if (ok) {
-          if (row >= n) clear_row(s, row, hf);
-          fence_async_smem();
-          warp_arrive(&B->fix);
+    for (int it = 0; it <= nit && !kStates && nit > 0; ++it) {
+      if (it < nit) {
+        const int c = chunk(it);
+        if (ragged(c)) {
+          const int s = it % NS;
+          const uint32_t full = (it / NS) & 1;
+          ok = __all_sync(0xffffffffu, ok && wait(&B->fullK[s], full, B) &&
+                                           wait(&B->fullV[s], full, B) &&
+                                           wait(&B->fullQ[s], full, B));
+          if (ok) {
+            if (row >= valid(c)) clear_row(s, row, hf);
+            fence_async_smem();
+            warp_arrive(&B->fix);
+          }
         }
-      }
-      ok = __all_sync(0xffffffffu, ok && wait(&B->s, ph, B));
-      // a^{|i-j|}: inside the row's own 32-column block one factor an element;
-      // elsewhere the steps between the blocks' facing edges, split into a factor
-      // of the row and one of the column.  Blocks of later steps are zero.
-      fence_after_sync();
+        ok = __all_sync(0xffffffffu, ok && wait(&B->s, it & 1, B));
+        fence_after_sync();
+        // a^{|i-j|}: on the diagonal from the table; elsewhere the steps between the
+        // blocks' facing edges, split into a factor of the row and one of the
+        // column.  Blocks of later steps are zero.
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        // (where P takes S's columns, a half's P overwrites S of its own blocks or
-        // of block 1, which the first half reads before the second half writes)
-        const int jb = G::wide ? 2 * x + hf : 2 * hf + x;
-        const int dist = p.reverse ? jb - ib : ib - jb;
-        uint32_t r[16];
+        for (int x = 0; x < 2; ++x) {
+          const int jb = 2 * x + hf, dist = p.reverse ? jb - ib : ib - jb;
+          uint32_t r[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = 0;
-        float v[32];
-        if (ok && dist >= 0) {
-          tmem_ld32(tS + lane_base + jb * 32, v);
-          tmem_wait_ld();
-        }
-        if (!G::wide && x != hf) {
-          fence_before_sync();
-          if (hf == 0) named_arrive(2, 256);
-          else named_sync(2, 256);
-          fence_after_sync();
-        }
-        if (ok) {
-          if (dist == 0) {
-            // (selected, not multiplied by zero: a later step has no part in this
-            // row whatever its product is)
-            float fi = fil;  // (opaque: 32 factors are not to be kept from chunk to chunk)
-            uint32_t bm = before;
-            asm volatile("" : "+f"(fi), "+r"(bm));
+          for (int j = 0; j < 16; ++j) r[j] = 0;
+          float v[32];
+          if (ok && dist >= 0) {
+            tmem_ld32(tm + cS + lane_base + jb * 32, v);
+            tmem_wait_ld();
+          }
+          if (x == 1 && ok) {  // all of S that this warp reads is read
+            fence_before_sync();
+            warp_arrive(&B->sfree);
+          }
+          if (ok && dist == 0) {
+            const float* g = diag + il * kDiagRow;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float e = ex2((fi - (float)j) * la2);
-              v[j] = ((bm >> j) & 1) ? v[j] * e : 0.f;
+            for (int j = 0; j < 8; ++j) {
+              const float4 e = *(const float4*)(g + 4 * j);
+              const float2 a0 = mul2(make_float2(v[4 * j], v[4 * j + 1]), make_float2(e.x, e.y));
+              const float2 a1 = mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), make_float2(e.z, e.w));
+              r[2 * j] = pack_bf16(a0.x, a0.y);
+              r[2 * j + 1] = pack_bf16(a1.x, a1.y);
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = pack_bf16(v[2 * j] * p.s_intra, v[2 * j + 1] * p.s_intra);
-          } else if (dist > 0) {
+          } else if (ok && dist > 0) {
             const float f = p.s_intra * bars.pw[(p.reverse ? 32 - il : il + 1) + 32 * (dist - 1)];
             const float2 f2 = make_float2(f, f);
 #pragma unroll
@@ -528,62 +522,73 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
               r[2 * j + 1] = pack_bf16(a1.x, a1.y);
             }
           }
-          tmem_st16(tP + lane_base + jb * 16, r);
+          // the last chunk's product has read its P (and written its O)
+          if (x == 0 && it > 0) {
+            ok = __all_sync(0xffffffffu, ok && wait(&B->o, (it - 1) & 1, B));
+            fence_after_sync();
+          }
+          if (ok) tmem_st16(tm + cP + lane_base + jb * 16, r);
         }
+        if (ok) {
+          tmem_wait_st();
+          fence_before_sync();
+          warp_arrive(&B->p);
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, ok && wait(&B->o, (it - 1) & 1, B));
+        fence_after_sync();
       }
-      if (ok) {
-        tmem_wait_st();
-        fence_before_sync();
-        warp_arrive(&B->p);
-      }
+      if (it == 0) continue;
+      const int c = chunk(it - 1), n = valid(c);
       const float lead = row < n ? p.s_carry * bars.pw[(p.reverse ? n - 1 - row : row) + p.off] : 0.f;
-      ok = __all_sync(0xffffffffu, ok && wait(&B->o, ph, B));
-      fence_after_sync();
-      // columns [c0, c0 + 16) of o
-      auto out16 = [&](int c0, float (&v)[16]) {
-        float y[16];
-        tmem_ld16(tO + lane_base + c0, v);
-        tmem_ld16(tC + lane_base + c0, y);
-        tmem_wait_ld();
-        const float2 l2 = make_float2(lead, lead);
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float2 a = fma2(l2, make_float2(y[j], y[j + 1]), make_float2(v[j], v[j + 1]));
-          v[j] = row < n ? a.x : 0.f;
-          v[j + 1] = row < n ? a.y : 0.f;
-        }
-      };
-      // staged in 128-byte rows: 64 columns of bf16 (both halves of the threads),
+      // o, staged in 128-byte rows: 64 columns of bf16 (both halves of the threads),
       // or 32 of fp32 (one half; one after the other where there is one buffer)
 #pragma unroll 1
-      for (int x = 0; x < DV * (kF32 ? 2 / G::NB : 1) / 64; ++x) {
-        uint8_t* st = sm + G::kSo + (G::NB == 1 ? 0 : kF32 ? hf : x % 2) * 16384;
-        const bool turn = !kF32 || G::NB == 2 || x % 2 == hf;
-        const int x0 = kF32 && G::NB == 1 ? x * 32 : x * 64;  // first column of the round
+      for (int x = 0; x < (kF32 && G::NB == 1 ? 2 : 1); ++x) {
+        uint8_t* st = sm + G::kSo + (kF32 && G::NB == 2 ? hf : 0) * 16384;
+        const bool turn = !kF32 || G::NB == 2 || x == hf;
         if (tid == 0) bulk_wait_read0();
         named_sync(1, 256);
         if (ok && turn) {
 #pragma unroll 1
           for (int z = 0; z < 2; ++z) {
-            float v[16];
-            const int ch = z * 16 + (kF32 && G::NB == 1 ? 0 : hf * 32);
-            out16(x0 + ch, v);
+            float v[16], y[16];
+            const int c16 = hf * 32 + z * 16;  // columns [c16, c16 + 16) of o
+            tmem_ld16(tm + cO + lane_base + c16, v);
+            tmem_ld16(tm + cC + lane_base + c16, y);
+            tmem_wait_ld();
+            const float2 l2 = make_float2(lead, lead);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float2 a = fma2(l2, make_float2(y[j], y[j + 1]), make_float2(v[j], v[j + 1]));
+              v[j] = a.x;
+              v[j + 1] = a.y;
+            }
+            if (n < kQ && row >= n) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = 0.f;
+            }
+            if (z == 1) {
+              fence_before_sync();
+              warp_arrive(&B->ofree);
+            }
             if (kF32) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 *(float4*)(st + sw128(row, z * 4 + j)) =
                     make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             } else {
-              *(uint4*)(st + sw128(row, ch / 8)) = pack8(v);
-              *(uint4*)(st + sw128(row, ch / 8 + 1)) = pack8(v + 8);
+              *(uint4*)(st + sw128(row, c16 / 8)) = pack8(v);
+              *(uint4*)(st + sw128(row, c16 / 8 + 1)) = pack8(v + 8);
             }
           }
         }
         fence_async_smem();
         named_sync(1, 256);
-        // (a box that starts past the width would start out of range)
         if (tid == 0 && ok) {
-          if (x0 < p.dv) tma_store_4d(&maps.o, sm + G::kSo + (kF32 ? 0 : G::NB == 1 ? 0 : x % 2) * 16384, x0, h, c * kQ, b);
+          // (a box that starts past the width would start out of range)
+          const int x0 = v0 + x * 32;
+          if (x0 < p.dv) tma_store_4d(&maps.o, sm + G::kSo, x0, h, c * kQ, b);
           if (kF32 && G::NB == 2 && x0 + 32 < p.dv)
             tma_store_4d(&maps.o, sm + G::kSo + 16384, x0 + 32, h, c * kQ, b);
           bulk_commit();
@@ -592,125 +597,119 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     }
     if (!kStates && tid == 0) bulk_wait0();
   } else if (warp < 16) {
-    // ---- w o V (or K): thread = row of a half and two 16-byte pieces of each 64
-    // columns; X: thread = row k of the state and every second 32 columns ----
+    // ---- w o V: thread = row of a piece and a 16-byte chunk; X: thread = row k of
+    // the state and 32 columns ----
     const int t = tid - 256, k = t & 127, hf = t >> 7;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const bool mine = k < DK;
-    constexpr int XN = DV / 2;  // column of X[i]: (i / 32) * 64 + hf * 32 + i % 32
-    float X[XN];
+    float X[32];  // columns v0 + 32 hf + i
 #pragma unroll
-    for (int i = 0; i < XN; ++i) X[i] = 0.f;
+    for (int i = 0; i < 32; ++i) X[i] = 0.f;
     const size_t sbase = (((size_t)seg * p.B + b) * p.H + h) * p.dk * p.dv;
+    const int vx = v0 + hf * 32, r = t & 31, ch = t >> 5;
+    float wt[4] = {0.f, 0.f, 0.f, 0.f};
+    int wn = -1;
     if (!kStates && p.first && k < p.dk) {
       const float* f = p.first + sbase;
 #pragma unroll
-      for (int i = 0; i < XN; ++i) {
-        const int v = (i / 32) * 64 + hf * 32 + i % 32;
-        if (v < p.dv) X[i] = f[p.first_swapped ? (size_t)k * p.dv + v : (size_t)v * p.dk + k];
-      }
+      for (int i = 0; i < 32; ++i)
+        if (vx + i < p.dv)
+          X[i] = f[p.first_swapped ? (size_t)k * p.dv + vx + i : (size_t)(vx + i) * p.dk + k];
     }
-    auto put_x = [&] {
-      if (mine)
-#pragma unroll
-        for (int i = 0; i < XN; i += 8)
-          *(uint4*)(sm + G::kXo + (i / 32) * DK * 128 + sw128(k, hf * 4 + (i & 31) / 8)) = pack8(X + i);
-      fence_async_smem();
-      warp_arrive(&B->x);
-    };
-    bool ok = true;
 #pragma unroll 1
-    for (int it = 0; it < nit && ok; ++it) {
+    for (int it = 0; it < nit; ++it) {
       const int c = chunk(it), n = valid(c), s = it % NS;
       const uint32_t full = (it / NS) & 1;
-      if (!kStates) {
-        if (it > 0 && !all_wait(&B->xfree, (it - 1) & 1)) break;
-        put_x();
-      }
-      if (!all_wait(G::scale_k ? &B->fullK[s] : &B->fullV[s], full)) break;
+      if (!all_wait(&B->fullV[s], full)) break;
       if (ragged(c)) {
         if (kStates) {  // (warps 0-7 do not follow a states walk's chunks)
-          if (!all_wait(G::scale_k ? &B->fullV[s] : &B->fullK[s], full)) break;
+          if (!all_wait(&B->fullK[s], full)) break;
           if (k >= n) clear_row(s, k, hf);
           fence_async_smem();
           warp_arrive(&B->fix);
         }
         if (!all_wait(&B->fix, 0)) break;
       }
-      const uint8_t* src = sm + (G::scale_k ? G::kKo + s * G::QT : G::kVo + s * G::VT);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int u = 2 * it + half, wb = u % WH;
-        if (!all_wait(&B->wfree[wb], ((u / WH) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        const int r = t & 63, j = half * 64 + r;
-        const float w = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
-        const float2 w2 = make_float2(w, w);
-        uint8_t* dst = sm + G::kWo + wb * 3 * G::WP;
-#pragma unroll 1
-        for (int x = 0; x < G::DS / 64; ++x)
-#pragma unroll 1
-          for (int q = 0; q < 2; ++q) {
-            const int ch = (t >> 6) * 2 + q;
-            const uint4 in = *(const uint4*)(src + x * 16384 + sw128(j, ch));
-            float2 f[4];
-            unpack8(in, (float*)f);
+      const uint8_t* src = sm + G::kVo + s * G::VT;
+      bool go = true;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
+      for (int piece = 0; piece < 4; ++piece) {
+        const int wb = piece % NW;  // (its turn: 4 / NW times a chunk)
+        go = go && all_wait(&B->wfree[wb], ((it * (4 / NW) + piece / NW) & 1) ^ 1);
+        if (!go) break;
+        if (n != wn) {  // the weights of this thread's row of each piece
+          wn = n;
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
-              const uint4 o = pack8((const float*)f);
-              *(uint4*)(dst + part * G::WP + x * 8192 + sw128(r, ch)) = o;
-              float2 m[4];
-              unpack8(o, (float*)m);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[i] = fma2(m[i], make_float2(-1.f, -1.f), f[i]);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int j = i * kPiece + r;
+            wt[i] = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
           }
+        }
+        const int j = piece * kPiece + r;
+        const float2 w2 = make_float2(wt[piece], wt[piece]);
+        uint8_t* dst = sm + G::kWo + wb * 3 * G::WP + sw128(r, ch);
+        float2 f[4];
+        unpack8(*(const uint4*)(src + sw128(j, ch)), (float*)f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const uint4 o = pack8((const float*)f);
+          *(uint4*)(dst + part * G::WP) = o;
+          float2 m[4];
+          unpack8(o, (float*)m);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = fma2(m[i], make_float2(-1.f, -1.f), f[i]);
+        }
         fence_async_smem();
         fence_before_sync();
         warp_arrive(&B->w[wb]);
       }
-      if (!ok || !all_wait(&B->u, it & 1)) break;
+      if (!go) break;
+      if (!kStates) {  // X before this chunk, for its Oc
+        if (it > 0 && !all_wait(&B->xfree, (it - 1) & 1)) break;
+        if (k < DK)
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *(uint4*)(sm + G::kXo + sw128(k, hf * 4 + i / 8)) = pack8(X + i);
+        fence_async_smem();
+        warp_arrive(&B->x);
+      }
+      if (!all_wait(&B->u, it & 1)) break;
       fence_after_sync();
       const float an = bars.pw[n];
 #pragma unroll
-      for (int x = 0; x < XN / 16; ++x) {
-        const int col = (x / 2) * 64 + hf * 32 + (x & 1) * 16;
-        float v[16];
-        tmem_ld16(tU + lane_base + col, v);
-        if constexpr (G::wide) {
-          float m[16], l[16];
-          tmem_ld16(tU + lane_base + 64 + col, m);
-          tmem_ld16(tU + lane_base + 128 + col, l);
-          tmem_wait_ld();
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t at = tm + cU + lane_base + hf * 32 + x * 8;
+        float v[8], m[8], l[8];
+        tmem_ld8(at, v);
+        tmem_ld8(at + 64, m);
+        tmem_ld8(at + 128, l);
+        tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += m[i] + l[i];
-        } else {
-          tmem_wait_ld();
+        for (int i = 0; i < 8; i += 2) {
+          const float2 y = add2(make_float2(v[i], v[i + 1]),
+                                add2(make_float2(m[i], m[i + 1]), make_float2(l[i], l[i + 1])));
+          const float2 z = fma2(make_float2(an, an), make_float2(X[8 * x + i], X[8 * x + i + 1]), y);
+          X[8 * x + i] = z.x;
+          X[8 * x + i + 1] = z.y;
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) X[16 * x + i] = fmaf(an, X[16 * x + i], v[i]);
       }
       fence_before_sync();
     }
     if (p.last && k < p.dk) {
       float* l = p.last + sbase;
 #pragma unroll
-      for (int i = 0; i < XN; ++i) {
-        const int v = (i / 32) * 64 + hf * 32 + i % 32;
-        if (v < p.dv) l[!kStates && p.first_swapped ? (size_t)k * p.dv + v : (size_t)v * p.dk + k] = X[i];
-      }
+      for (int i = 0; i < 32; ++i)
+        if (vx + i < p.dv)
+          l[!kStates && p.first_swapped ? (size_t)k * p.dv + vx + i : (size_t)(vx + i) * p.dk + k] = X[i];
     }
   }
   if (!kStates) {
     // whole chunks of the segment past the row's end
     const int z0 = max(c1, c0) * kQ, z1 = min((c0 + p.seg_chunks) * kQ, p.T);
-    const int esz = kF32 ? 4 : 2, lane = tid & 31;
-    uint8_t* o = (uint8_t*)p.o + ((size_t)b * p.T * p.H + h) * p.dv * esz + lane * 16;
-    if (lane * 16 < p.dv * esz)
+    const int esz = kF32 ? 4 : 2, at = (tid & 31) * 16, row = min(kV, p.dv - v0) * esz;
+    uint8_t* o = (uint8_t*)p.o + (((size_t)b * p.T * p.H + h) * p.dv + v0) * esz + at;
+    if (at < row)
 #pragma unroll 1
       for (int t = z0 + warp; t < z1; t += kThreads / 32)
         *(uint4*)(o + (size_t)t * p.H * p.dv * esz) = make_uint4(0, 0, 0, 0);
@@ -794,32 +793,31 @@ bool map_4d(CUtensorMap* m, const void* base, bool f32, int D, int heads, int T,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DK, int DV, bool kStates, bool kF32>
+template <int DK, bool kStates, bool kF32>
 cudaError_t launch(const Maps& m, const TcWalk& p, cudaStream_t s) {
-  constexpr size_t smem = Geom<DK, DV>::smem;
-  static_assert(smem + sizeof(Bars) <= 232448, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(k_la_walk_tc<DK, DV, kStates, kF32>,
+  constexpr size_t smem = Geom<DK, kStates>::smem;
+  static_assert(smem + sizeof(Bars) + 1024 <= 232448, "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(k_la_walk_tc<DK, kStates, kF32>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(kStates ? "linattn_states" : p.reverse ? "linattn_walk_back" : "linattn_walk", s);
-  k_la_walk_tc<DK, DV, kStates, kF32><<<dim3(p.H, p.B, p.nseg), kThreads, smem, s>>>(m, p);
+  const int vblocks = (p.dv + kV - 1) / kV;
+  k_la_walk_tc<DK, kStates, kF32><<<dim3(p.H * vblocks, p.B, p.nseg), kThreads, smem, s>>>(m, p);
   return cudaGetLastError();
 }
 
 template <bool kStates, bool kF32>
 cudaError_t launch_d(const Maps& m, const TcWalk& p, cudaStream_t s) {
-  if (p.dk <= 64)
-    return p.dv <= 64 ? launch<64, 64, kStates, kF32>(m, p, s) : launch<64, 128, kStates, kF32>(m, p, s);
-  return p.dv <= 64 ? launch<128, 64, kStates, kF32>(m, p, s) : launch<128, 128, kStates, kF32>(m, p, s);
+  return p.dk <= 64 ? launch<64, kStates, kF32>(m, p, s) : launch<128, kStates, kF32>(m, p, s);
 }
 
 }  // namespace
 
-int la_tc_segments(int B, int H, int T) {
+static int la_tc_segments(int B, int H, int T, int dv) {
   // One CTA an SM: a row's nc chunks go to one CTA unless that leaves SMs idle.
   // Splitting a row costs a pass over K and V for the segments' states (about
   // half a walk) and two more launches, so it has to pay for that.
-  const long long nc = (T + kQ - 1) / kQ, rows = (long long)B * H, sms = 152;
+  const long long nc = (T + kQ - 1) / kQ, rows = (long long)B * H * ((dv + kV - 1) / kV), sms = 152;
   auto waves = [&](long long n) { return (rows * n + sms - 1) / sms; };
   double best = (double)(waves(1) * nc);
   long long at = 1;
@@ -835,7 +833,8 @@ int la_tc_segments(int B, int H, int T) {
 }
 
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv) {
-  const int n = la_tc_segments(B, H, T);
+  // (the walks of a backward pass have dk and dv in either order)
+  const int a = la_tc_segments(B, H, T, dv), b = la_tc_segments(B, H, T, dk), n = a > b ? a : b;
   return n > 1 ? (size_t)n * B * H * dk * dv : 0;
 }
 
@@ -865,7 +864,7 @@ cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s) {
   p.off = w.off;
   p.reverse = w.reverse;
   const int nc = (w.T + kQ - 1) / kQ;
-  int n = la_tc_segments(w.B, w.H, w.T);
+  int n = la_tc_segments(w.B, w.H, w.T, w.dv);
   p.seg_chunks = (nc + n - 1) / n;
   n = (nc + p.seg_chunks - 1) / p.seg_chunks;
   p.nseg = n;

@@ -22,8 +22,8 @@
 // overlaps with the loads and with itself: warps 0-7 turn S into P and write o
 // of the chunk before (thread = row and half of the columns), warps 8-15 build
 // the parts of w o V and carry X (thread = row k and half of the columns), one
-// warp each issues the TMA loads of the next chunks, the products of the
-// output and those of the state.  128 columns of v are two CTAs, which read q
+// warp each issues the TMA loads of the next chunks, the products of S, of O
+// and Oc, and of U.  128 columns of v are two CTAs, which read q
 // and k twice (from L2) and form S twice: at 64 columns the accumulators leave
 // room for P beside S, so that S of the next chunk does not wait for P V.
 //
@@ -191,7 +191,7 @@ constexpr int cS = 0, cP = 128, cO = 192, cC = 256, cU = 320;
 
 struct Bars {
   uint64_t fullQ[3], fullK[3], fullV[3], emptyQ[3], emptyK[3], emptyV[3];
-  uint64_t w[4], wfree[4], s, sfree, p, o, ofree, x, xfree, u, fix, drain[2];
+  uint64_t w[4], wfree[4], s, sfree, p, o, ofree, x, xfree, u, fix, drain[3];
   uint32_t tmem;
   volatile int abort;
   float pw[132];  // a^0 ... a^130
@@ -245,13 +245,15 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   uint8_t* sm = align1024(raw);
   __shared__ Bars bars;
   Bars* B = &bars;
-  const int tid = threadIdx.x, warp = tid >> 5;
+  // (the shuffles tell the compiler what is the same in a warp's lanes: the roles'
+  // branches and loops and the products' operands then stay in uniform registers)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int vblocks = (p.dv + kV - 1) / kV;
   const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kV;
   const int b = blockIdx.y, seg = blockIdx.z;
   const float la = p.log_decay[h];
   int len = p.T;
-  if (p.lens) len = min(max(p.lens[b], 0), p.T);
+  if (p.lens) len = __shfl_sync(0xffffffffu, min(max(p.lens[b], 0), p.T), 0);
   const int c0 = seg * p.seg_chunks;
   const int c1 = min(c0 + p.seg_chunks, (len + kQ - 1) / kQ);
   const int nit = max(c1 - c0, 0);
@@ -300,6 +302,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     mbar_init(&B->fix, 8);
     mbar_init(&B->drain[0], 1);
     mbar_init(&B->drain[1], 1);
+    mbar_init(&B->drain[2], 1);
     B->abort = 0;
     fence_mbar_init();
   }
@@ -322,7 +325,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tm = B->tmem;
+  const uint32_t tm = __shfl_sync(0xffffffffu, B->tmem, 0);
 
   if (warp == 19) {
     // ---- loads ----
@@ -365,65 +368,67 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       }
     }
   } else if (warp == 17) {
-    // ---- products of the output: S, O, Oc ----
+    // ---- products of the scores: S (once S of the last chunk is read) ----
     // The whole warp walks the loop (so that descriptors stay warp-uniform), one
     // lane issues.  Descriptors of a tile differ in their start address alone
     // (16-byte units): K-major steps of 16 are 2 units apart and 1024 units after
     // every four, MN-major ones 128.
-    if (!kStates) {
-      const uint32_t lead = (tid & 31) == 0;
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t id_x = idesc_bf16(128, kV, false, true);
-      const uint64_t dQ0 = desc_sw128(smem_u32(sm + G::kQo), 16, 1024);
-      const uint64_t dK0 = desc_sw128(smem_u32(sm + G::kKo), 16, 1024);
-      const uint64_t dX = desc_sw128(smem_u32(sm + G::kXo), 16, 1024);
-      const uint64_t dV0 = desc_sw128(smem_u32(sm + G::kVo), 16, 1024);
-      // per turn: S of chunk it (once S of the last one is read), then Oc and O of
-      // chunk it - 1 (once those of the chunk before it are read)
+    const uint32_t lead = (tid & 31) == 0;
+    constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
+    const uint64_t dQ0 = desc_sw128(smem_u32(sm + G::kQo), 16, 1024);
+    const uint64_t dK0 = desc_sw128(smem_u32(sm + G::kKo), 16, 1024);
 #pragma unroll 1
-      for (int it = 0; it <= nit; ++it) {
-        if (it < nit) {
-          const int s = it % NS;
-          const uint32_t full = (it / NS) & 1;
-          if (!all_wait(&B->fullK[s], full) || !all_wait(&B->fullQ[s], full)) break;
-          if (ragged(chunk(it)) && !all_wait(&B->fix, 0)) break;
-          if (it > 0 && !all_wait(&B->sfree, (it - 1) & 1)) break;
-          fence_after_sync();
-          const uint64_t dQ = dQ0 + s * (G::QT >> 4), dK = dK0 + s * (G::QT >> 4);
+    for (int it = 0; it < nit && !kStates; ++it) {
+      const int s = it % NS;
+      const uint32_t full = (it / NS) & 1;
+      if (!all_wait(&B->fullK[s], full) || !all_wait(&B->fullQ[s], full)) break;
+      if (ragged(chunk(it)) && !all_wait(&B->fix, 0)) break;
+      if (it > 0 && !all_wait(&B->sfree, (it - 1) & 1)) break;
+      fence_after_sync();
+      const uint64_t dQ = dQ0 + s * (G::QT >> 4), dK = dK0 + s * (G::QT >> 4);
 #pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk) {
-            const int off = (kk >> 2) * 1024 + (kk & 3) * 2;
-            mma_ss(lead, tm + cS, dQ + off, dK + off, id_s, kk > 0);
-          }
-          commit_if(lead, &B->s);
-          commit_if(lead, &B->emptyK[s]);
-        }
-        if (it > 0) {
-          const int j = it - 1, s = j % NS;
-          const uint32_t ph = j & 1;
-          if (!all_wait(&B->x, ph)) break;
-          if (j > 0 && !all_wait(&B->ofree, ph ^ 1)) break;
-          fence_after_sync();
-          const uint64_t dQ = dQ0 + s * (G::QT >> 4);
-#pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk)
-            mma_ss(lead, tm + cC, dQ + ((kk >> 2) * 1024 + (kk & 3) * 2), dX + 128 * kk, id_x, kk > 0);
-          commit_if(lead, &B->emptyQ[s]);
-          commit_if(lead, &B->xfree);
-          if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], (j / NS) & 1)) break;
-          fence_after_sync();
-          const uint64_t dV = dV0 + s * (G::VT >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(lead, tm + cO, tm + cP + 8 * kk, dV + 128 * kk, id_x, kk > 0);
-          commit_if(lead, &B->o);
-          commit_if(lead, &B->emptyV[s]);
-        }
+      for (int kk = 0; kk < DK / 16; ++kk) {
+        const int off = (kk >> 2) * 1024 + (kk & 3) * 2;
+        mma_ss(lead, tm + cS, dQ + off, dK + off, id_s, kk > 0);
       }
-      commit_if(lead, &B->drain[0]);
-      mbar_wait(&B->drain[0], 0, kWaitNs);
-      __syncwarp();
+      commit_if(lead, &B->s);
+      commit_if(lead, &B->emptyK[s]);
     }
+    commit_if(lead, &B->drain[0]);
+    mbar_wait(&B->drain[0], 0, kWaitNs);
+    __syncwarp();
+  } else if (warp == 16) {
+    // ---- products of the output: O and Oc (once those of the last chunk are read) ----
+    const uint32_t lead = (tid & 31) == 0;
+    constexpr uint32_t id_x = idesc_bf16(128, kV, false, true);
+    const uint64_t dQ0 = desc_sw128(smem_u32(sm + G::kQo), 16, 1024);
+    const uint64_t dX = desc_sw128(smem_u32(sm + G::kXo), 16, 1024);
+    const uint64_t dV0 = desc_sw128(smem_u32(sm + G::kVo), 16, 1024);
+#pragma unroll 1
+    for (int it = 0; it < nit && !kStates; ++it) {
+      const int s = it % NS;
+      const uint32_t full = (it / NS) & 1, ph = it & 1;
+      if (it > 0 && !all_wait(&B->ofree, ph ^ 1)) break;
+      if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], full)) break;
+      fence_after_sync();
+      const uint64_t dV = dV0 + s * (G::VT >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(lead, tm + cO, tm + cP + 8 * kk, dV + 128 * kk, id_x, kk > 0);
+      commit_if(lead, &B->o);
+      commit_if(lead, &B->emptyV[s]);
+      if (!all_wait(&B->x, ph) || !all_wait(&B->fullQ[s], full)) break;
+      fence_after_sync();
+      const uint64_t dQ = dQ0 + s * (G::QT >> 4);
+#pragma unroll
+      for (int kk = 0; kk < DK / 16; ++kk)
+        mma_ss(lead, tm + cC, dQ + ((kk >> 2) * 1024 + (kk & 3) * 2), dX + 128 * kk, id_x, kk > 0);
+      commit_if(lead, &B->xfree);
+      commit_if(lead, &B->emptyQ[s]);
+    }
+    commit_if(lead, &B->drain[2]);
+    mbar_wait(&B->drain[2], 0, kWaitNs);
+    __syncwarp();
   } else if (warp == 18) {
     // ---- products of the state: U, the parts side by side (3 x 64 columns) ----
     const uint32_t lead = (tid & 31) == 0;
@@ -539,6 +544,8 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         fence_after_sync();
       }
       if (it == 0) continue;
+      ok = __all_sync(0xffffffffu, ok && wait(&B->xfree, (it - 1) & 1, B));
+      fence_after_sync();
       const int c = chunk(it - 1), n = valid(c);
       const float lead = row < n ? p.s_carry * bars.pw[(p.reverse ? n - 1 - row : row) + p.off] : 0.f;
       // o, staged in 128-byte rows: 64 columns of bf16 (both halves of the threads),

@@ -409,14 +409,6 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       const int s = it % NS;
       const uint32_t full = (it / NS) & 1, ph = it & 1;
       if (it > 0 && !all_wait(&B->ofree, ph ^ 1)) break;
-      if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], full)) break;
-      fence_after_sync();
-      const uint64_t dV = dV0 + s * (G::VT >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts(lead, tm + cO, tm + cP + 8 * kk, dV + 128 * kk, id_x, kk > 0);
-      commit_if(lead, &B->o);
-      commit_if(lead, &B->emptyV[s]);
       if (!all_wait(&B->x, ph) || !all_wait(&B->fullQ[s], full)) break;
       fence_after_sync();
       const uint64_t dQ = dQ0 + s * (G::QT >> 4);
@@ -425,6 +417,14 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         mma_ss(lead, tm + cC, dQ + ((kk >> 2) * 1024 + (kk & 3) * 2), dX + 128 * kk, id_x, kk > 0);
       commit_if(lead, &B->xfree);
       commit_if(lead, &B->emptyQ[s]);
+      if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], full)) break;
+      fence_after_sync();
+      const uint64_t dV = dV0 + s * (G::VT >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(lead, tm + cO, tm + cP + 8 * kk, dV + 128 * kk, id_x, kk > 0);
+      commit_if(lead, &B->o);
+      commit_if(lead, &B->emptyV[s]);
     }
     commit_if(lead, &B->drain[2]);
     mbar_wait(&B->drain[2], 0, kWaitNs);
@@ -466,11 +466,46 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     // ---- P and o: thread = row i of the chunk and every second 32 columns ----
     const int row = tid & 127, il = row & 31, ib = warp & 3, hf = warp >> 2;
     const uint32_t lane_base = (uint32_t)(ib * 32) << 16;
-    // per turn: P of chunk it, then o of chunk it - 1.  (After a wait that gave up
-    // the warps still meet at their barriers, without touching the data.)
+    // per turn: o of chunk it - 1 out of TMEM, P of chunk it, then the stores of
+    // that o.  (After a wait that gave up the warps still meet at their barriers,
+    // without touching the data.)
     bool ok = true;
 #pragma unroll 1
     for (int it = 0; it <= nit && !kStates && nit > 0; ++it) {
+      uint32_t y[kF32 ? 32 : 16];  // this thread's 32 columns of o, bf16 in pairs or fp32
+      if (it > 0) {
+        ok = __all_sync(0xffffffffu, ok && wait(&B->o, (it - 1) & 1, B));
+        fence_after_sync();
+        const int n = valid(chunk(it - 1));
+        const float lead =
+            row < n ? p.s_carry * bars.pw[(p.reverse ? n - 1 - row : row) + p.off] : 0.f;
+        const float2 l2 = make_float2(lead, lead);
+        if (ok) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            float u[16], w[16];
+            tmem_ld16(tm + cO + lane_base + hf * 32 + z * 16, u);
+            tmem_ld16(tm + cC + lane_base + hf * 32 + z * 16, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float2 a = fma2(l2, make_float2(w[j], w[j + 1]), make_float2(u[j], u[j + 1]));
+              if (kF32) {
+                y[(kF32 ? 16 * z : 0) + j] = __float_as_uint(a.x);
+                y[(kF32 ? 16 * z : 0) + j + 1] = __float_as_uint(a.y);
+              } else {
+                y[8 * z + j / 2] = pack_bf16(a.x, a.y);
+              }
+            }
+          }
+          if (n < kQ && row >= n) {
+#pragma unroll
+            for (int j = 0; j < (kF32 ? 32 : 16); ++j) y[j] = 0;
+          }
+          fence_before_sync();
+          warp_arrive(&B->ofree);
+        }
+      }
       if (it < nit) {
         const int c = chunk(it);
         if (ragged(c)) {
@@ -489,115 +524,74 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         fence_after_sync();
         // a^{|i-j|}: on the diagonal from the table; elsewhere the steps between the
         // blocks' facing edges, split into a factor of the row and one of the
-        // column.  Blocks of later steps are zero.
+        // column.  Blocks of later steps are zero.  (The product that read the last
+        // P is over: its o was waited for.)
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
           const int jb = 2 * x + hf, dist = p.reverse ? jb - ib : ib - jb;
           uint32_t r[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) r[j] = 0;
-          float v[32];
           if (ok && dist >= 0) {
+            float v[32];
             tmem_ld32(tm + cS + lane_base + jb * 32, v);
             tmem_wait_ld();
-          }
-          if (x == 1 && ok) {  // all of S that this warp reads is read
-            fence_before_sync();
-            warp_arrive(&B->sfree);
-          }
-          if (ok && dist == 0) {
-            const float* g = diag + il * kDiagRow;
+            if (dist == 0) {
+              const float* g = diag + il * kDiagRow;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 e = *(const float4*)(g + 4 * j);
-              const float2 a0 = mul2(make_float2(v[4 * j], v[4 * j + 1]), make_float2(e.x, e.y));
-              const float2 a1 = mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), make_float2(e.z, e.w));
-              r[2 * j] = pack_bf16(a0.x, a0.y);
-              r[2 * j + 1] = pack_bf16(a1.x, a1.y);
-            }
-          } else if (ok && dist > 0) {
-            const float f = p.s_intra * bars.pw[(p.reverse ? 32 - il : il + 1) + 32 * (dist - 1)];
-            const float2 f2 = make_float2(f, f);
+              for (int j = 0; j < 8; ++j) {
+                const float4 e = *(const float4*)(g + 4 * j);
+                const float2 a0 = mul2(make_float2(v[4 * j], v[4 * j + 1]), make_float2(e.x, e.y));
+                const float2 a1 = mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), make_float2(e.z, e.w));
+                r[2 * j] = pack_bf16(a0.x, a0.y);
+                r[2 * j + 1] = pack_bf16(a1.x, a1.y);
+              }
+            } else {
+              const float f = p.s_intra * bars.pw[(p.reverse ? 32 - il : il + 1) + 32 * (dist - 1)];
+              const float2 f2 = make_float2(f, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 g = *(const float4*)&bars.col[4 * j];
-              const float2 a0 = mul2(mul2(make_float2(v[4 * j], v[4 * j + 1]), f2), make_float2(g.x, g.y));
-              const float2 a1 = mul2(mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), f2), make_float2(g.z, g.w));
-              r[2 * j] = pack_bf16(a0.x, a0.y);
-              r[2 * j + 1] = pack_bf16(a1.x, a1.y);
+              for (int j = 0; j < 8; ++j) {
+                const float4 g = *(const float4*)&bars.col[4 * j];
+                const float2 a0 = mul2(mul2(make_float2(v[4 * j], v[4 * j + 1]), f2), make_float2(g.x, g.y));
+                const float2 a1 = mul2(mul2(make_float2(v[4 * j + 2], v[4 * j + 3]), f2), make_float2(g.z, g.w));
+                r[2 * j] = pack_bf16(a0.x, a0.y);
+                r[2 * j + 1] = pack_bf16(a1.x, a1.y);
+              }
             }
           }
-          // the last chunk's product has read its P (and written its O)
-          if (x == 0 && it > 0) {
-            ok = __all_sync(0xffffffffu, ok && wait(&B->o, (it - 1) & 1, B));
-            fence_after_sync();
+          if (ok) {
+            tmem_st16(tm + cP + lane_base + jb * 16, r);
+            if (x == 1) {
+              tmem_wait_st();
+              fence_before_sync();
+              warp_arrive(&B->sfree);
+              if ((tid & 31) == 0) mbar_arrive(&B->p);
+            }
           }
-          if (ok) tmem_st16(tm + cP + lane_base + jb * 16, r);
         }
-        if (ok) {
-          tmem_wait_st();
-          fence_before_sync();
-          warp_arrive(&B->p);
-        }
-      } else {
-        ok = __all_sync(0xffffffffu, ok && wait(&B->o, (it - 1) & 1, B));
-        fence_after_sync();
       }
       if (it == 0) continue;
-      ok = __all_sync(0xffffffffu, ok && wait(&B->xfree, (it - 1) & 1, B));
-      fence_after_sync();
-      const int c = chunk(it - 1), n = valid(c);
-      const float lead = row < n ? p.s_carry * bars.pw[(p.reverse ? n - 1 - row : row) + p.off] : 0.f;
       // o, staged in 128-byte rows: 64 columns of bf16 (both halves of the threads),
       // or 32 of fp32 (one half; one after the other where there is one buffer)
 #pragma unroll 1
       for (int x = 0; x < (kF32 && G::NB == 1 ? 2 : 1); ++x) {
         uint8_t* st = sm + G::kSo + (kF32 && G::NB == 2 ? hf : 0) * 16384;
-        const bool turn = !kF32 || G::NB == 2 || x == hf;
         if (tid == 0) bulk_wait_read0();
         named_sync(1, 256);
-        if (ok && turn) {
-#pragma unroll 1
-          for (int z = 0; z < 2; ++z) {
-            float v[16], y[16];
-            const int c16 = hf * 32 + z * 16;  // columns [c16, c16 + 16) of o
-            tmem_ld16(tm + cO + lane_base + c16, v);
-            tmem_ld16(tm + cC + lane_base + c16, y);
-            tmem_wait_ld();
-            const float2 l2 = make_float2(lead, lead);
+        if (ok && (!kF32 || G::NB == 2 || x == hf)) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float2 a = fma2(l2, make_float2(y[j], y[j + 1]), make_float2(v[j], v[j + 1]));
-              v[j] = a.x;
-              v[j + 1] = a.y;
-            }
-            if (n < kQ && row >= n) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = 0.f;
-            }
-            if (z == 1) {
-              fence_before_sync();
-              warp_arrive(&B->ofree);
-            }
-            if (kF32) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *(float4*)(st + sw128(row, z * 4 + j)) =
-                    make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            } else {
-              *(uint4*)(st + sw128(row, c16 / 8)) = pack8(v);
-              *(uint4*)(st + sw128(row, c16 / 8 + 1)) = pack8(v + 8);
-            }
-          }
+          for (int j = 0; j < (kF32 ? 8 : 4); ++j)
+            *(uint4*)(st + sw128(row, (kF32 ? 0 : hf * 4) + j)) =
+                make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
         }
         fence_async_smem();
         named_sync(1, 256);
         if (tid == 0 && ok) {
           // (a box that starts past the width would start out of range)
-          const int x0 = v0 + x * 32;
-          if (x0 < p.dv) tma_store_4d(&maps.o, sm + G::kSo, x0, h, c * kQ, b);
+          const int x0 = v0 + x * 32, t0 = chunk(it - 1) * kQ;
+          if (x0 < p.dv) tma_store_4d(&maps.o, sm + G::kSo, x0, h, t0, b);
           if (kF32 && G::NB == 2 && x0 + 32 < p.dv)
-            tma_store_4d(&maps.o, sm + G::kSo + 16384, x0 + 32, h, c * kQ, b);
+            tma_store_4d(&maps.o, sm + G::kSo + 16384, x0 + 32, h, t0, b);
           bulk_commit();
         }
       }
@@ -613,8 +607,6 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     for (int i = 0; i < 32; ++i) X[i] = 0.f;
     const size_t sbase = (((size_t)seg * p.B + b) * p.H + h) * p.dk * p.dv;
     const int vx = v0 + hf * 32, r = t & 31, ch = t >> 5;
-    float wt[4] = {0.f, 0.f, 0.f, 0.f};
-    int wn = -1;
     if (!kStates && p.first && k < p.dk) {
       const float* f = p.first + sbase;
 #pragma unroll
@@ -638,21 +630,14 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       }
       const uint8_t* src = sm + G::kVo + s * G::VT;
       bool go = true;
-#pragma unroll
+#pragma unroll 1
       for (int piece = 0; piece < 4; ++piece) {
-        const int wb = piece % NW;  // (its turn: 4 / NW times a chunk)
-        go = go && all_wait(&B->wfree[wb], ((it * (4 / NW) + piece / NW) & 1) ^ 1);
+        const int u = 4 * it + piece, wb = u % NW;
+        go = all_wait(&B->wfree[wb], ((u / NW) & 1) ^ 1);
         if (!go) break;
-        if (n != wn) {  // the weights of this thread's row of each piece
-          wn = n;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = i * kPiece + r;
-            wt[i] = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
-          }
-        }
         const int j = piece * kPiece + r;
-        const float2 w2 = make_float2(wt[piece], wt[piece]);
+        const float w = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
+        const float2 w2 = make_float2(w, w);
         uint8_t* dst = sm + G::kWo + wb * 3 * G::WP + sw128(r, ch);
         float2 f[4];
         unpack8(*(const uint4*)(src + sw128(j, ch)), (float*)f);

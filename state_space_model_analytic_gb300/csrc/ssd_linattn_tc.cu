@@ -629,29 +629,35 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         if (!all_wait(&B->fix, 0)) break;
       }
       const uint8_t* src = sm + G::kVo + s * G::VT;
+      uint4 in[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) in[i] = *(const uint4*)(src + sw128(i * kPiece + r, ch));
       bool go = true;
-#pragma unroll 1
+#pragma unroll
       for (int piece = 0; piece < 4; ++piece) {
-        const int u = 4 * it + piece, wb = u % NW;
-        go = all_wait(&B->wfree[wb], ((u / NW) & 1) ^ 1);
-        if (!go) break;
+        // the three parts, before the wait for the buffer they go to
         const int j = piece * kPiece + r;
         const float w = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
         const float2 w2 = make_float2(w, w);
-        uint8_t* dst = sm + G::kWo + wb * 3 * G::WP + sw128(r, ch);
         float2 f[4];
-        unpack8(*(const uint4*)(src + sw128(j, ch)), (float*)f);
+        unpack8(in[piece], (float*)f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
+        uint4 o[3];
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
-          const uint4 o = pack8((const float*)f);
-          *(uint4*)(dst + part * G::WP) = o;
+          o[part] = pack8((const float*)f);
           float2 m[4];
-          unpack8(o, (float*)m);
+          unpack8(o[part], (float*)m);
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = fma2(m[i], make_float2(-1.f, -1.f), f[i]);
         }
+        const int wb = piece % NW;  // (its turn: 4 / NW times a chunk)
+        go = go && all_wait(&B->wfree[wb], ((it * (4 / NW) + piece / NW) & 1) ^ 1);
+        if (!go) break;
+        uint8_t* dst = sm + G::kWo + wb * 3 * G::WP + sw128(r, ch);
+#pragma unroll
+        for (int part = 0; part < 3; ++part) *(uint4*)(dst + part * G::WP) = o[part];
         fence_async_smem();
         fence_before_sync();
         warp_arrive(&B->w[wb]);

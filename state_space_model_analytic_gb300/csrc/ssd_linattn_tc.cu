@@ -170,8 +170,8 @@ constexpr int kDiagRow = 36;  // (16-byte pieces of 8 rows fall on all 32 banks)
 // buffers that o is staged in.  The sums stay below the 227 KB of a CTA.
 template <int DK, bool kStates>
 struct Geom {
-  static constexpr int NS = kStates ? 3 : 2;
-  static constexpr int NW = kStates || DK == 64 ? 4 : 2;
+  static constexpr int NS = kStates || DK == 64 ? 3 : 2;
+  static constexpr int NW = kStates ? 4 : 2;
   static constexpr int NB = kStates ? 0 : DK == 64 ? 2 : 1;
   static constexpr int QT = DK * 256, VT = kV * 256;  // bytes of 128 rows
   static constexpr int WP = kPiece * 128;              // one part of a piece
@@ -278,7 +278,29 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     for (int x = 0; x < 4; ++x) *(uint4*)(sm + G::kVo + s * G::VT + at + x * 16) = z;
   };
 
-  if (tid == 0) {
+  // the loads of chunk `it` of the walk, each once its buffer is free
+  auto load = [&](int it) {
+    const int s = it % NS, t0 = chunk(it) * kQ;
+    const uint32_t free = ((it / NS) & 1) ^ 1;
+    if (!wait(&B->emptyK[s], free, B)) return false;
+    uint8_t* d = sm + G::kKo + s * G::QT;
+    mbar_expect_tx(&B->fullK[s], G::QT);
+    for (int x = 0; x < DK; x += 64)
+      tma_load_4d(d + x * 256, &maps.k, x, h / p.ks, t0, b, &B->fullK[s]);
+    if (!kStates) {
+      if (!wait(&B->emptyQ[s], free, B)) return false;
+      d = sm + G::kQo + s * G::QT;
+      mbar_expect_tx(&B->fullQ[s], G::QT);
+      for (int x = 0; x < DK; x += 64)
+        tma_load_4d(d + x * 256, &maps.q, x, h / p.qs, t0, b, &B->fullQ[s]);
+    }
+    if (!wait(&B->emptyV[s], free, B)) return false;
+    mbar_expect_tx(&B->fullV[s], G::VT);
+    tma_load_4d(sm + G::kVo + s * G::VT, &maps.v, v0, h / p.vs, t0, b, &B->fullV[s]);
+    return true;
+  };
+  // (the loading thread sets the barriers up and starts on the first stages at once)
+  if (tid == 19 * 32) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&B->fullQ[i], 1);
       mbar_init(&B->fullK[i], 1);
@@ -305,6 +327,11 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     mbar_init(&B->drain[2], 1);
     B->abort = 0;
     fence_mbar_init();
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.v);
+#pragma unroll 1
+    for (int it = 0; it < min(nit, NS); ++it) load(it);
   }
   for (int i = tid; i < 131; i += kThreads) bars.pw[i] = decay_pow(la, (float)i);
   if (tid >= 160 && tid < 192) {
@@ -330,30 +357,10 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   if (warp == 19) {
     // ---- loads ----
     if (tid == 19 * 32) {
-      prefetch_tmap(&maps.q);
-      prefetch_tmap(&maps.k);
-      prefetch_tmap(&maps.v);
-      int it = 0;
+      int it = min(nit, NS);
 #pragma unroll 1
-      for (; it < nit; ++it) {
-        const int s = it % NS, t0 = chunk(it) * kQ;
-        const uint32_t free = ((it / NS) & 1) ^ 1;
-        if (!wait(&B->emptyK[s], free, B)) break;
-        uint8_t* d = sm + G::kKo + s * G::QT;
-        mbar_expect_tx(&B->fullK[s], G::QT);
-        for (int x = 0; x < DK; x += 64)
-          tma_load_4d(d + x * 256, &maps.k, x, h / p.ks, t0, b, &B->fullK[s]);
-        if (!kStates) {
-          if (!wait(&B->emptyQ[s], free, B)) break;
-          d = sm + G::kQo + s * G::QT;
-          mbar_expect_tx(&B->fullQ[s], G::QT);
-          for (int x = 0; x < DK; x += 64)
-            tma_load_4d(d + x * 256, &maps.q, x, h / p.qs, t0, b, &B->fullQ[s]);
-        }
-        if (!wait(&B->emptyV[s], free, B)) break;
-        mbar_expect_tx(&B->fullV[s], G::VT);
-        tma_load_4d(sm + G::kVo + s * G::VT, &maps.v, v0, h / p.vs, t0, b, &B->fullV[s]);
-      }
+      for (; it < nit; ++it)
+        if (!load(it)) break;
       if (B->abort) {
         // no copy may be in flight when the CTA ends: those of the last stages
         // (a barrier that nothing was issued on in that phase runs out its limit)

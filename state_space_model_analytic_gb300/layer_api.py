@@ -5,6 +5,8 @@ stream.
 """
 from __future__ import annotations
 
+import array
+
 import torch
 
 from . import _native as nat
@@ -12,13 +14,32 @@ from . import _native as nat
 _IO_TYPES = {torch.float32: nat.SSD_F32, torch.bfloat16: nat.SSD_BF16}
 
 
+_entry = {}
+
+
+def _call(name):
+    """The library's entry point, looked up once."""
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(nat.lib(), name)
+    return f
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream or None
+# the current stream's handle without a Stream object around it, where this
+# torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream or None
+    if _raw_stream is not None:
+        return _raw_stream(dev.index) or None
+    return torch.cuda.current_stream(dev).cuda_stream or None
 
 
 def _keep(stream, *tensors):
@@ -28,6 +49,21 @@ def _keep(stream, *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+
+
+class _Layouts(dict):
+    """What a call derives from its operands' shapes, strides and types alone
+    (never from their addresses or values), kept for the next call with the
+    same ones."""
+
+    def keep(self, key, value):
+        if len(self) >= 1024:
+            self.clear()
+        self[key] = value
+        return value
+
+
+_layouts = _Layouts()
 
 
 def _expect(name, t, dtype, shape, device, dense=True):
@@ -58,28 +94,46 @@ def _rows_dense(name, t):
         raise ValueError(f"{name}: the last two dimensions must be contiguous")
 
 
-def _linattn_dims(q, k, v, scale, log_decay, decay_rows=False):
+def _linattn_dims(q, k, v, scale, log_decay, do, step):
+    """(dims, workspace bytes forward, backward) after the operands' checks."""
+    key = (step, q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape, v.stride(),
+           v.dtype, log_decay.shape, log_decay.dtype, log_decay.is_contiguous(), scale,
+           None if do is None else (do.shape, do.stride(), do.dtype))
+    dev = q.device
+    if not q.is_cuda:
+        raise ValueError("q: must be a CUDA tensor (no CPU path exists)")
+    for name, t in (("k", k), ("v", v), ("log_decay", log_decay), ("do", do)):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    got = _layouts.get(key)
+    if got is not None:
+        return got
     code = _io_type("q", q)
-    step = q.dim() == 3
-    if q.dim() != 4 and not (decay_rows and step):
+    if q.dim() != (3 if step else 4):
         raise ValueError(f"q: shape {tuple(q.shape)}, expected "
-                         + ("[B, G, K]" if decay_rows else "[B, T, G, K]"))
+                         + ("[B, G, K]" if step else "[B, T, G, K]"))
     if v.dim() != q.dim():
         raise ValueError(f"v: {v.dim()} dimensions, expected {q.dim()}")
     B, G, K = q.shape[0], q.shape[-2], q.shape[-1]
     T = 1 if step else q.shape[1]
     H, V = v.shape[-2], v.shape[-1]
-    dev = q.device
     _expect("k", k, q.dtype, q.shape, dev, False)
     _expect("v", v, q.dtype, (*q.shape[:-2], H, V), dev, False)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _rows_dense(name, t)
-    if not (decay_rows and log_decay.dim() == 2):
-        _expect("log_decay", log_decay, torch.float32, (H,), dev)
-    else:
-        _expect("log_decay", log_decay, torch.float32, (B, H), dev)
+    if do is not None:
+        _expect("do", do, v.dtype, v.shape, dev, False)
+    for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
+        if t is not None:
+            _rows_dense(name, t)
+    _expect("log_decay", log_decay, torch.float32,
+            (B, H) if step and log_decay.dim() == 2 else (H,), dev)
     s = (lambda t: (t.stride(0), 0)) if step else (lambda t: (t.stride(0), t.stride(1)))
-    return nat.LinattnDims(B, T, H, G, K, V, *s(q), *s(k), *s(v), 0, 0, scale, code)
+    d = nat.LinattnDims(B, T, H, G, K, V, *s(q), *s(k), *s(v), *(s(do) if do is not None else (0, 0)),
+                        scale, code)
+    size = _call("ssd_linattn_workspace_bytes")
+    need = size(d, 0), size(d, 1)
+    if not all(need):
+        raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "dims rejected")
+    return _layouts.keep(key, (d, *need))
 
 
 def _linattn_checks(d, dev, states, lens):
@@ -92,22 +146,9 @@ def _linattn_checks(d, dev, states, lens):
     return shape
 
 
-def _linattn_workspace(d, which, workspace, dev):
-    if workspace is not None:
-        return workspace
-    n = nat.lib().ssd_linattn_workspace_bytes(d, which)
-    if n == 0:
-        raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "dims rejected")
-    return torch.empty(n, dtype=torch.uint8, device=dev)
-
-
 def linattn_workspace_bytes(q, k, v, log_decay, *, backward=False) -> int:
     """Bytes of the `workspace` that linattn_forward (or _backward) takes."""
-    d = _linattn_dims(q, k, v, 1.0, log_decay)
-    n = nat.lib().ssd_linattn_workspace_bytes(d, int(backward))
-    if n == 0:
-        raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "dims rejected")
-    return n
+    return _linattn_dims(q, k, v, 1.0, log_decay, None, False)[2 if backward else 1]
 
 
 def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, want_state=True,
@@ -121,7 +162,7 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
     the device: row b has lens[b] steps (o is zero past them).  K and V are
     multiples of 8 up to 128.  Returns (o [B,T,H,V], final state [B,H,V,K] or
     None); out: dict of preallocated "o", "state"."""
-    d = _linattn_dims(q, k, v, scale, log_decay)
+    d, need, _ = _linattn_dims(q, k, v, scale, log_decay, None, False)
     dev = q.device
     out = {} if out is None else out
     o, state = out.get("o"), out.get("state")
@@ -132,12 +173,13 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
         _expect("out o", o, v.dtype, v.shape, dev)
     if state is None and want_state:
         state = torch.empty(shape, dtype=torch.float32, device=dev)
-    workspace = _linattn_workspace(d, 0, workspace, dev)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _keep(stream, o, state, workspace)
-    nat.check(nat.lib().ssd_linattn_forward(
+    nat.check(_call("ssd_linattn_forward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
         _ptr(lens), o.data_ptr(), _ptr(state), workspace.data_ptr(), workspace.numel(),
-        _stream_handle(stream)))
+        _stream_handle(stream, dev)))
     return o, state
 
 
@@ -146,11 +188,8 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
     """Gradients of sum(do * o) + sum(dstate * state) of linattn_forward: dict
     dq, dk, dv, dstate0 (or None).  do [B,T,H,V] may be strided like v;
     dstate [B,H,V,K] fp32 or None (zero)."""
-    d = _linattn_dims(q, k, v, scale, log_decay)
+    d, _, need = _linattn_dims(q, k, v, scale, log_decay, do, False)
     dev = q.device
-    _expect("do", do, v.dtype, v.shape, dev, False)
-    _rows_dense("do", do)
-    d.dout_batch, d.dout_step = do.stride(0), do.stride(1)
     g = dict(out) if out is not None else {}
     shape = _linattn_checks(d, dev, (("state0", state0), ("dstate", dstate),
                                      ("out dstate0", g.get("dstate0"))), lens)
@@ -163,13 +202,14 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
         g["dstate0"] = None
     elif g.get("dstate0") is None:
         g["dstate0"] = torch.empty(shape, dtype=torch.float32, device=dev)
-    workspace = _linattn_workspace(d, 1, workspace, dev)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _keep(stream, workspace, *g.values())
-    nat.check(nat.lib().ssd_linattn_backward(
+    nat.check(_call("ssd_linattn_backward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
         do.data_ptr(), _ptr(dstate), _ptr(lens), g["dq"].data_ptr(), g["dk"].data_ptr(),
         g["dv"].data_ptr(), _ptr(g["dstate0"]), workspace.data_ptr(), workspace.numel(),
-        _stream_handle(stream)))
+        _stream_handle(stream, dev)))
     return g
 
 
@@ -185,9 +225,7 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
 
     A step of the SSD core's recurrence is this one with v = dt x, k = B,
     q = C, log_decay = dt A, and D x added to o."""
-    d = _linattn_dims(q, k, v, scale, log_decay, True)
-    if q.dim() != 3:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected [B, G, K]")
+    d = _linattn_dims(q, k, v, scale, log_decay, None, True)[0]
     dev = q.device
     rows = state.shape[0] if state.dim() else 0
     _expect("state", state, torch.float32, (rows, d.nheads, d.dv, d.dk), dev)
@@ -204,10 +242,10 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
     else:
         _expect("out", out, v.dtype, v.shape, dev)
     _keep(stream, out, state_out)
-    nat.check(nat.lib().ssd_linattn_step(
+    nat.check(_call("ssd_linattn_step")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
         d.nheads if log_decay.dim() == 2 else 0, state.data_ptr(), state_out.data_ptr(),
-        _ptr(slots), rows, out.data_ptr(), _stream_handle(stream)))
+        _ptr(slots), rows, out.data_ptr(), _stream_handle(stream, dev)))
     return out, state_out
 
 
@@ -219,7 +257,7 @@ def _rows_of(name, t, shape, dtype, dev):
     width = shape[-1]
     if t.is_contiguous():
         return width
-    if t.stride(-1) == 1:
+    if t.dim() > 1 and t.stride(-1) == 1:
         s = t.stride(-2)
         n = s * t.shape[-2]
         for i in range(t.dim() - 3, -1, -1):
@@ -233,22 +271,37 @@ def _rows_of(name, t, shape, dtype, dev):
 
 
 def _block_norm_args(residual, y, z, w_post, res_scale, w_pre):
+    """(rows, width, dtype codes, row strides, workspace bytes) after the checks."""
+    dev = y.device
+    if not y.is_cuda:
+        raise ValueError("y: must be a CUDA tensor (no CPU path exists)")
+    key = ["norm", y.shape, y.stride(), y.dtype]
+    for t in (residual, z, w_post, res_scale, w_pre):
+        if t is not None:
+            if t.device != dev:
+                raise ValueError(f"a tensor is on {t.device}, expected {dev}")
+            key += (t.shape, t.stride(), t.dtype)
+        else:
+            key.append(None)
+    key = tuple(key)
+    got = _layouts.get(key)
+    if got is not None:
+        return got
     code = _io_type("y", y)
-    dev, width = y.device, y.shape[-1]
+    width = y.shape[-1]
     if residual.dtype not in (y.dtype, torch.float32):
         raise TypeError(f"residual: dtype {residual.dtype}, expected {y.dtype} or torch.float32")
     _expect("residual", residual, residual.dtype, y.shape, dev)
-    ys = _rows_of("y", y, y.shape, y.dtype, dev) if y.dim() > 1 else width
-    if y.dim() == 1 and not y.is_contiguous():
-        raise ValueError("y: must be contiguous")
-    zs = 0
-    if z is not None:
-        zs = _rows_of("z", z, y.shape, y.dtype, dev) if y.dim() > 1 else width
+    ys = _rows_of("y", y, y.shape, y.dtype, dev)
+    zs = 0 if z is None else _rows_of("z", z, y.shape, y.dtype, dev)
     for name, w in (("w_post", w_post), ("w_pre", w_pre), ("res_scale", res_scale)):
         if w is not None:
             _expect(name, w, torch.float32, (width,), dev)
     rows = y.numel() // width if width else 0
-    return rows, width, code, _IO_TYPES[residual.dtype], ys, zs
+    n = _call("ssd_block_norm_workspace_bytes")(rows, width)
+    if n == 0:
+        raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "shape rejected")
+    return _layouts.keep(key, (rows, width, code, _IO_TYPES[residual.dtype], ys, zs, n))
 
 
 def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_stats=True, out=None,
@@ -259,7 +312,8 @@ def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_st
     evenly spaced; residual: their type or fp32.  Weights [width] fp32.
     Returns (new residual, x, stats [..., 2] fp32 for the backward or None);
     out: dict of preallocated "residual" (may be `residual` itself), "x"."""
-    rows, width, code, rcode, ys, zs = _block_norm_args(residual, y, z, w_post, res_scale, w_pre)
+    rows, width, code, rcode, ys, zs, _ = _block_norm_args(residual, y, z, w_post, res_scale,
+                                                           w_pre)
     dev = y.device
     out = {} if out is None else out
     new, x = out.get("residual"), out.get("x")
@@ -273,10 +327,10 @@ def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_st
         _expect("out x", x, y.dtype, y.shape, dev)
     stats = torch.empty(*y.shape[:-1], 2, dtype=torch.float32, device=dev) if want_stats else None
     _keep(stream, new, x, stats)
-    nat.check(nat.lib().ssd_block_norm_forward(
+    nat.check(_call("ssd_block_norm_forward")(
         rows, width, code, rcode, residual.data_ptr(), y.data_ptr(), ys, _ptr(z), zs,
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), new.data_ptr(),
-        x.data_ptr(), _ptr(stats), _stream_handle(stream)))
+        x.data_ptr(), _ptr(stats), _stream_handle(stream, dev)))
     return new, x, stats
 
 
@@ -285,8 +339,8 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
     """Gradients of sum(dx * x) + sum(dnew * new): dict dresidual, dy, dz (None
     without z), dw_post, dres_scale, dw_pre.  new_residual is the forward's;
     stats as the forward returned them, or None (recomputed)."""
-    rows, width, code, rcode, ys, zs = _block_norm_args(new_residual, y, z, w_post, res_scale,
-                                                        w_pre)
+    rows, width, code, rcode, ys, zs, need = _block_norm_args(new_residual, y, z, w_post,
+                                                              res_scale, w_pre)
     dev = y.device
     _expect("dx", dx, y.dtype, y.shape, dev)
     if dnew is not None:
@@ -305,17 +359,14 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
         else:
             _expect("out " + name, g[name], dt, shape, dev)
     if workspace is None:
-        n = nat.lib().ssd_block_norm_workspace_bytes(rows, width)
-        if n == 0:
-            raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "shape rejected")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _keep(stream, workspace, *g.values())
-    nat.check(nat.lib().ssd_block_norm_backward(
+    nat.check(_call("ssd_block_norm_backward")(
         rows, width, code, rcode, new_residual.data_ptr(), y.data_ptr(), ys, _ptr(z), zs,
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), _ptr(stats),
         dx.data_ptr(), _ptr(dnew), g["dresidual"].data_ptr(), g["dy"].data_ptr(), _ptr(g["dz"]),
         g["dw_post"].data_ptr(), _ptr(g["dres_scale"]), g["dw_pre"].data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _stream_handle(stream)))
+        workspace.data_ptr(), workspace.numel(), _stream_handle(stream, dev)))
     return g
 
 
@@ -330,26 +381,42 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
     gradient NaN."""
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"out: {len(outs)} tensors, expected {len(grads)}")
-    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    table = (nat.ClipTensor * max(1, len(grads)))()
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        code = _io_type(f"grads[{i}]", g)
-        _expect(f"grads[{i}]", g, g.dtype, g.shape, dev)
-        if o is not g:
-            _expect(f"out[{i}]", o, g.dtype, g.shape, dev)
-        e = table[i]
-        e.g, e.out, e.numel, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), code
+    n = len(grads)
+    if len(outs) != n:
+        raise ValueError(f"out: {len(outs)} tensors, expected {n}")
+    dev = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    # one list a property: hundreds of tensors are looked through in every call
+    try:
+        codes = [_IO_TYPES[g.dtype] for g in grads]
+    except KeyError:
+        raise TypeError("grads: fp32 and bf16 tensors only") from None
+    sizes = [g.numel() for g in grads]
+    at = [g.data_ptr() for g in grads]
+    to = at
+    if any([g.device != dev for g in grads]) or dev.type != "cuda":
+        raise ValueError("grads: must be CUDA tensors on one device (no CPU path exists)")
+    if not all([g.is_contiguous() for g in grads]):
+        raise ValueError("grads: must be contiguous")
+    if out is not None:
+        if any([o.dtype != g.dtype for o, g in zip(outs, grads)]):
+            raise TypeError("out: another dtype than the gradient's")
+        if any([o.shape != g.shape or o.device != dev for o, g in zip(outs, grads)]):
+            raise ValueError("out: another shape or device than the gradient's")
+        if not all([o.is_contiguous() for o in outs]):
+            raise ValueError("out: must be contiguous")
+        to = [o.data_ptr() for o in outs]
+    flat = [0] * (4 * n)  # ssd_clip_tensor: g, out, numel, dtype (with a zero above it)
+    flat[0::4], flat[1::4], flat[2::4], flat[3::4] = at, to, sizes, codes
+    table = array.array("Q", flat)
+    rows = table.buffer_info()[0] if n else None
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    L = nat.lib()
     if workspace is None:
-        n = L.ssd_clip_workspace_bytes(table, len(grads))
-        if n == 0:
+        need = _call("ssd_clip_workspace_bytes")(rows, n)
+        if need == 0:
             raise nat.SsdError(nat.SSD_ERR_INVALID_ARG, nat.last_error() or "tensors rejected")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _keep(stream, norm, workspace)
-    nat.check(L.ssd_clip_grad_norm(table, len(grads), float(max_norm), float(eps), norm.data_ptr(),
+    nat.check(_call("ssd_clip_grad_norm")(rows, n, float(max_norm), float(eps), norm.data_ptr(),
                                    workspace.data_ptr(), workspace.numel(),
-                                   _stream_handle(stream)))
+                                   _stream_handle(stream, dev)))
     return norm

@@ -41,6 +41,19 @@ struct LaWalk {
 // scratch: la_scratch_floats() floats
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16);
 cudaError_t la_walk(const LaWalk& w, bool bf16, float* scratch, cudaStream_t s);
+// Segments of a row that is shared out over CTAs, `slots` of which run at once.
+int la_segments(long long rows, long long chunks, long long slots);
+// the states before each segment from the segments' own states (in place)
+struct LaSegments {
+  int B, H, T, dk, dv, nseg, span;  // span: steps of a segment
+  const float* log_decay;
+  const int* lens;
+  float* seg;          // [nseg][B][H][dv][dk]
+  const float* first;  // nullable; [dk][dv] instead of [dv][dk] if swapped
+  float* last;         // nullable
+  bool swapped, reverse;
+};
+cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s);
 // the bf16 walk on tensor cores (ssd_linattn_tc.cu)
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv);
 cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s);

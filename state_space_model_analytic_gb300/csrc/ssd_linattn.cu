@@ -25,88 +25,243 @@ namespace {
 // a^e for e >= 0 from log a; a^0 = 1 also where a = 0 (log a = -inf)
 __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f ? 1.f : expf(la * e); }
 
-constexpr int kC = 32;        // steps of a chunk
+// ---- the walk in fp32 on the CUDA cores ---------------------------------------
+//
+// One CTA per (h, 64 columns of v, b, segment of the row), chunks of 64 steps.
+// 256 threads as 16 x 16: thread (ty, tx) forms 4 x 4 blocks of the products
+//   P = mask(Q K^T)      rows 4 ty + a, columns tx + 16 c
+//   o = P V + lead Q X   rows 4 ty + a, columns 4 tx + b
+//   X = a^n X + K^T w V  rows 4 ty + a (+ 64), columns 4 tx + b, in registers
+// with operands in shared memory, 16 bytes at a time: eight 16-byte loads (12
+// shared-memory cycles) serve 64 FMAs of a warp (16 cycles of the SM's FMA
+// units), so the FMAs bound it; P and P V leave out the columns that the mask
+// empties for a warp's eight rows.  fp32 throughout: the operands' type leaves
+// no other choice that keeps their precision.
+constexpr int kC = 64;         // steps of a chunk
+constexpr int kB = 64;         // columns of v of a CTA
 constexpr int kThreads = 256;
 
-// One CTA per (h, b).  Shared memory (fp32): q, k [C][dk + 1], v [C][dv + 1],
-// P [C][C + 1], S [dv][dk + 1].
-__global__ void __launch_bounds__(kThreads) k_la_walk(LaWalk w) {
-  using T = float;
-  extern __shared__ float sm[];
-  const int dk = w.dk, dv = w.dv, lk = dk + 1, lv = dv + 1;
+template <int DK>
+struct Simt {
+  static constexpr int LK = DK + 4;  // rows 16 bytes apart in the banks
+  static constexpr int LP = kC + 4;
+  static constexpr int kFloats = 2 * kC * LK + kC * kB + kC * LP + DK * kB;
+  static constexpr size_t smem = kFloats * sizeof(float);
+};
+
+struct SimtWalk {
+  LaWalk w;
+  int nseg, span;  // steps of a segment
+};
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *(const float4*)p; }
+
+// kStates: only the state, each segment from zero, into w.last
+// [nseg][B][H][dv][dk].
+template <int DK, bool kStates>
+__global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ SimtWalk args) {
+  using G = Simt<DK>;
+  const LaWalk& w = args.w;
+  extern __shared__ __align__(16) float sm[];
   float* Q = sm;
-  float* K = Q + kC * lk;
-  float* V = K + kC * lk;
-  float* P = V + kC * lv;
-  float* S = P + kC * (kC + 1);
+  float* K = Q + kC * G::LK;
+  float* V = K + kC * G::LK;
+  float* P = V + kC * kB;
+  float* X = P + kC * G::LP;
   __shared__ float pw[kC + 2];
-  const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
+  const int vblocks = (w.dv + kB - 1) / kB;
+  const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kB;
+  const int b = blockIdx.y, seg = blockIdx.z, t = threadIdx.x, tx = t & 15, ty = t >> 4, wp = t >> 5;
   const float la = w.log_decay[h];
   int len = w.T;
   if (w.lens) len = min(max(w.lens[b], 0), w.T);
   if (t < kC + 2) pw[t] = decay_pow(la, (float)t);
-  const size_t sbase = ((size_t)b * w.H + h) * dv * dk;
-  for (int i = t; i < dv * dk; i += kThreads) {
-    const int v = i / dk, k = i % dk;
-    S[v * lk + k] = !w.first ? 0.f : w.first[sbase + (w.first_swapped ? (size_t)k * dv + v : i)];
-  }
-  const T* qp = (const T*)w.q.p + b * w.q.batch + (long long)(h / w.q.share) * dk;
-  const T* kp = (const T*)w.k.p + b * w.k.batch + (long long)(h / w.k.share) * dk;
-  const T* vp = (const T*)w.v.p + b * w.v.batch + (long long)(h / w.v.share) * dv;
-  T* op = (T*)w.o + ((long long)b * w.T * w.H + h) * dv;
-  const int nc = (len + kC - 1) / kC;
+  const int dv = min(kB, w.dv - v0);
+  const size_t sbase = (((size_t)seg * w.B + b) * w.H + h) * w.dv * w.dk;
+  // state element (k, v) of this thread
+  auto state_at = [&](int k, int v) {
+    return sbase + (!kStates && w.first_swapped ? (size_t)k * w.dv + v0 + v : (size_t)(v0 + v) * w.dk + k);
+  };
+  float x[DK / 16][4];
+#pragma unroll
+  for (int a = 0; a < DK / 16; ++a)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int k = 4 * ty + (a & 3) + (a >> 2) * 64, v = 4 * tx + c;
+      x[a][c] = !kStates && w.first && k < w.dk && v < dv ? w.first[state_at(k, v)] : 0.f;
+    }
+  const float* qp = (const float*)w.q.p + b * w.q.batch + (long long)(h / w.q.share) * w.dk;
+  const float* kp = (const float*)w.k.p + b * w.k.batch + (long long)(h / w.k.share) * w.dk;
+  const float* vp = (const float*)w.v.p + b * w.v.batch + (long long)(h / w.v.share) * w.dv + v0;
+  float* op = (float*)w.o + ((long long)b * w.T * w.H + h) * w.dv + v0;
+  const int s0 = seg * args.span, s1 = min(s0 + args.span, len);  // the segment's steps
+  const int nc = s1 > s0 ? (s1 - s0 + kC - 1) / kC : 0;
   for (int ci = 0; ci < nc; ++ci) {
-    const int c = w.reverse ? nc - 1 - ci : ci;
-    const int n = min(kC, len - c * kC);
-    const long long t0 = (long long)c * kC;
+    const int t0 = s0 + (w.reverse ? nc - 1 - ci : ci) * kC, n = min(kC, s1 - t0);
     __syncthreads();
-    for (int i = t; i < kC * dk; i += kThreads) {
-      const int r = i / dk, d = i % dk;
-      Q[r * lk + d] = r < n ? to_f32(qp[(t0 + r) * w.q.step + d]) : 0.f;
-      K[r * lk + d] = r < n ? to_f32(kp[(t0 + r) * w.k.step + d]) : 0.f;
+    for (int i = t; i < kC * (DK / 4); i += kThreads) {
+      const int r = i / (DK / 4), d = i % (DK / 4) * 4;
+      const bool in = r < n && d < w.dk;
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!kStates) *(float4*)(Q + r * G::LK + d) = in ? ld4(qp + (long long)(t0 + r) * w.q.step + d) : z;
+      *(float4*)(K + r * G::LK + d) = in ? ld4(kp + (long long)(t0 + r) * w.k.step + d) : z;
     }
-    for (int i = t; i < kC * dv; i += kThreads) {
-      const int r = i / dv, d = i % dv;
-      V[r * lv + d] = r < n ? to_f32(vp[(t0 + r) * w.v.step + d]) : 0.f;
+    for (int i = t; i < kC * (kB / 4); i += kThreads) {
+      const int r = i / (kB / 4), d = i % (kB / 4) * 4;
+      *(float4*)(V + r * kB + d) =
+          r < n && d < dv ? ld4(vp + (long long)(t0 + r) * w.v.step + d) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    if (!kStates)
+#pragma unroll
+      for (int a = 0; a < DK / 16; ++a)
+        *(float4*)(X + (4 * ty + (a & 3) + (a >> 2) * 64) * kB + 4 * tx) =
+            make_float4(x[a][0], x[a][1], x[a][2], x[a][3]);
     __syncthreads();
-    for (int e = t; e < kC * kC; e += kThreads) {
-      const int i = e / kC, j = e % kC;
-      const int d = w.reverse ? j - i : i - j;
-      float s = 0.f;
-      if (d >= 0 && i < n && j < n) {
-        for (int x = 0; x < dk; ++x) s = fmaf(Q[i * lk + x], K[j * lk + x], s);
-        s *= w.s_intra * pw[d];
+    if (!kStates) {
+      // columns tx + 16 c that the warp's rows 8 wp ... 8 wp + 7 need
+      const int ca = w.reverse ? wp / 2 : 0, cb = w.reverse ? 4 : wp / 2 + 1;
+#pragma unroll 1
+      for (int c = ca; c < cb; ++c) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const float* kr = K + (tx + 16 * c) * G::LK;
+#pragma unroll 8
+        for (int d = 0; d < DK; d += 4) {
+          const float4 kk = ld4(kr + d);
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const float4 q = ld4(Q + (4 * ty + a) * G::LK + d);
+            s[a] = fmaf(q.x, kk.x, fmaf(q.y, kk.y, fmaf(q.z, kk.z, fmaf(q.w, kk.w, s[a]))));
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int i = 4 * ty + a, j = tx + 16 * c, d = w.reverse ? j - i : i - j;
+          P[i * G::LP + j] = d >= 0 ? w.s_intra * pw[d] * s[a] : 0.f;
+        }
       }
-      P[i * (kC + 1) + j] = s;
+      __syncwarp();  // (a warp reads the rows of P that it wrote)
+      float o[4][4], u[4][4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[a][c] = u[a][c] = 0.f;
+      auto rank4 = [&](const float* left, int ld, const float* right, float (&acc)[4][4]) {
+        float4 l[4], r[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) l[a] = ld4(left + a * ld);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = ld4(right + e * kB);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const float f[4] = {l[a].x, l[a].y, l[a].z, l[a].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[a][0] = fmaf(f[e], r[e].x, acc[a][0]);
+            acc[a][1] = fmaf(f[e], r[e].y, acc[a][1]);
+            acc[a][2] = fmaf(f[e], r[e].z, acc[a][2]);
+            acc[a][3] = fmaf(f[e], r[e].w, acc[a][3]);
+          }
+        }
+      };
+#pragma unroll 4
+      for (int j = 16 * ca; j < 16 * cb; j += 4)
+        rank4(P + 4 * ty * G::LP + j, G::LP, V + j * kB + 4 * tx, o);
+#pragma unroll 4
+      for (int d = 0; d < DK; d += 4)
+        rank4(Q + 4 * ty * G::LK + d, G::LK, X + d * kB + 4 * tx, u);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int i = 4 * ty + a;
+        if (i < n && 4 * tx < dv) {
+          const float lead = w.s_carry * pw[(w.reverse ? n - 1 - i : i) + w.off];
+          *(float4*)(op + (long long)(t0 + i) * w.H * w.dv + 4 * tx) =
+              make_float4(fmaf(lead, u[a][0], o[a][0]), fmaf(lead, u[a][1], o[a][1]),
+                          fmaf(lead, u[a][2], o[a][2]), fmaf(lead, u[a][3], o[a][3]));
+        }
+      }
     }
-    __syncthreads();
-    for (int e = t; e < n * dv; e += kThreads) {
-      const int i = e / dv, v = e % dv;
-      float s = 0.f, u = 0.f;
-      for (int j = 0; j < kC; ++j) s = fmaf(P[i * (kC + 1) + j], V[j * lv + v], s);
-      for (int x = 0; x < dk; ++x) u = fmaf(S[v * lk + x], Q[i * lk + x], u);
-      const int lead = (w.reverse ? n - 1 - i : i) + w.off;
-      op[(t0 + i) * w.H * dv + v] = fmaf(w.s_carry * pw[lead], u, s);
-    }
-    __syncthreads();
-    const float an = decay_pow(la, (float)n);
-    for (int e = t; e < dv * dk; e += kThreads) {
-      const int v = e / dk, k = e % dk;
-      float s = 0.f;
-      for (int j = 0; j < n; ++j)
-        s = fmaf(V[j * lv + v] * pw[(w.reverse ? j : n - 1 - j) + 1 - w.off], K[j * lk + k], s);
-      S[v * lk + k] = fmaf(an, S[v * lk + k], w.s_inject * s);
+    const float an = pw[n];
+#pragma unroll
+    for (int a = 0; a < DK / 16; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[a][c] *= an;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float f = w.s_inject * pw[(w.reverse ? j : n - 1 - j) + 1 - w.off];
+      const float4 v = ld4(V + j * kB + 4 * tx);
+      const float y[4] = {f * v.x, f * v.y, f * v.z, f * v.w};
+#pragma unroll
+      for (int g = 0; g < DK / 64; ++g) {
+        const float4 k = ld4(K + j * G::LK + 4 * ty + 64 * g);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x[4 * g][c] = fmaf(k.x, y[c], x[4 * g][c]);
+          x[4 * g + 1][c] = fmaf(k.y, y[c], x[4 * g + 1][c]);
+          x[4 * g + 2][c] = fmaf(k.z, y[c], x[4 * g + 2][c]);
+          x[4 * g + 3][c] = fmaf(k.w, y[c], x[4 * g + 3][c]);
+        }
+      }
     }
   }
-  __syncthreads();
-  for (long long i = t; i < (long long)(w.T - len) * dv; i += kThreads)
-    op[(len + i / dv) * w.H * dv + i % dv] = 0.f;
-  if (w.last)
-    for (int i = t; i < dv * dk; i += kThreads) {
-      const int v = i / dk, k = i % dk;
-      w.last[sbase + (w.first_swapped ? (size_t)k * dv + v : i)] = S[v * lk + k];
+  if (!kStates) {  // past the row's end
+    const int z0 = max(s0, min(len, s0 + args.span)), z1 = min(s0 + args.span, w.T);
+    for (int i = t; i < (z1 - z0) * (kB / 4); i += kThreads) {
+      const int r = i / (kB / 4), d = i % (kB / 4) * 4;
+      if (d < dv) *(float4*)(op + (long long)(z0 + r) * w.H * w.dv + d) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+  }
+  if (w.last)
+#pragma unroll
+    for (int a = 0; a < DK / 16; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int k = 4 * ty + (a & 3) + (a >> 2) * 64, v = 4 * tx + c;
+        if (k < w.dk && v < dv) w.last[state_at(k, v)] = x[a][c];
+      }
+}
+
+// The states before each segment from the segments' own: in walk order
+//   X_0 = first, X_{s+1} = a^{steps of s} X_s + local_s;  last = X_nseg.
+// seg [nseg][B][H][dv][dk], overwritten in place.
+__global__ void __launch_bounds__(256) k_la_segments(const LaSegments p) {
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int i = blockIdx.x * 256 + threadIdx.x, n = p.dk * p.dv;
+  if (i >= n) return;
+  const float la = p.log_decay[h];
+  int len = p.T;
+  if (p.lens) len = min(max(p.lens[b], 0), p.T);
+  const size_t row = ((size_t)b * p.H + h) * n, stride = (size_t)p.B * p.H * n;
+  const size_t at = row + (p.swapped ? (size_t)(i % p.dk) * p.dv + i / p.dk : (size_t)i);
+  float x = p.first ? p.first[at] : 0.f;
+  for (int j0 = 0; j0 < p.nseg; j0 += 8) {
+    float local[8];  // read ahead: the loads do not wait for one another
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int s = p.reverse ? p.nseg - 1 - j0 - u : j0 + u;
+      local[u] = j0 + u < p.nseg ? p.seg[s * stride + row + i] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (j0 + u >= p.nseg) break;
+      const int s = p.reverse ? p.nseg - 1 - j0 - u : j0 + u;
+      const int steps = min(max(len - s * p.span, 0), p.span);
+      p.seg[s * stride + row + i] = x;
+      x = fmaf(decay_pow(la, (float)steps), x, local[u]);
+    }
+  }
+  if (p.last) p.last[at] = x;
+}
+
+template <int DK, bool kStates>
+cudaError_t walk_t(const SimtWalk& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(k_la_walk<DK, kStates>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Simt<DK>::smem);
+  if (e != cudaSuccess) return e;
+  LaunchScope ls(kStates ? "linattn_states" : a.w.reverse ? "linattn_walk_back" : "linattn_walk", s);
+  const int vblocks = (a.w.dv + kB - 1) / kB;
+  k_la_walk<DK, kStates><<<dim3(a.w.H * vblocks, a.w.B, a.nseg), kThreads, Simt<DK>::smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 // part [rows][G][share][D] fp32 -> out [rows][G][D]
@@ -182,21 +337,64 @@ cudaError_t step_t(const LaStep& p, cudaStream_t s) {
 
 }  // namespace
 
+int la_segments(long long rows, long long chunks, long long slots) {
+  // A row's chunks go to one CTA unless that leaves SMs idle.  Splitting a row
+  // costs a pass for the segments' states (about half a walk) and two more
+  // launches, so it has to pay for that.
+  auto waves = [&](long long n) { return (rows * n + slots - 1) / slots; };
+  double best = (double)(waves(1) * chunks);
+  int at = 1;
+  for (int n = 2; n <= chunks && n <= 32; ++n) {
+    const long long per = (chunks + n - 1) / n;
+    const double cost = 1.5 * (double)(waves(n) * per) + 4.0 + 0.25 * n;
+    if (cost < best) {
+      best = cost;
+      at = n;
+    }
+  }
+  return at;
+}
+
+cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s) {
+  LaunchScope ls("linattn_segments", s);
+  k_la_segments<<<dim3((p.dk * p.dv + 255) / 256, p.H, p.B), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// CTAs of the fp32 walk that run at once on 152 SMs (two of 81 KB, or one of 131)
+static int simt_segments(int B, int H, int T, int dk, int dv) {
+  return la_segments((long long)B * H * ((dv + kB - 1) / kB), (T + kC - 1) / kC,
+                     dk <= 64 ? 304 : 152);
+}
+
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16) {
-  return bf16 ? la_tc_scratch_floats(B, H, T, dk, dv) : 0;
+  if (bf16) return la_tc_scratch_floats(B, H, T, dk, dv);
+  // (the walks of a backward pass have dk and dv in either order)
+  const int a = simt_segments(B, H, T, dk, dv), b = simt_segments(B, H, T, dv, dk), n = a > b ? a : b;
+  return n > 1 ? (size_t)n * B * H * dk * dv : 0;
 }
 
 cudaError_t la_walk(const LaWalk& w, bool bf16, float* scratch, cudaStream_t s) {
   if (bf16) return la_walk_tc(w, scratch, s);
-  const size_t smem =
-      sizeof(float) * ((size_t)2 * kC * (w.dk + 1) + (size_t)kC * (w.dv + 1) + kC * (kC + 1) +
-                       (size_t)w.dv * (w.dk + 1));
-  cudaError_t e =
-      cudaFuncSetAttribute(k_la_walk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  LaunchScope ls(w.reverse ? "linattn_walk_back" : "linattn_walk", s);
-  k_la_walk<<<dim3(w.H, w.B), kThreads, smem, s>>>(w);
-  return cudaGetLastError();
+  SimtWalk a;
+  a.w = w;
+  const int nc = (w.T + kC - 1) / kC;
+  int n = simt_segments(w.B, w.H, w.T, w.dk, w.dv);
+  a.span = (nc + n - 1) / n * kC;
+  n = (w.T + a.span - 1) / a.span;
+  a.nseg = n;
+  if (n > 1) {
+    a.w.last = scratch;
+    cudaError_t e = w.dk <= 64 ? walk_t<64, true>(a, s) : walk_t<128, true>(a, s);
+    if (e != cudaSuccess) return e;
+    const LaSegments g = {w.B, w.H, w.T, w.dk, w.dv, n, a.span, w.log_decay, w.lens, scratch,
+                          w.first, w.last, w.first_swapped, w.reverse};
+    if ((e = la_segment_states(g, s)) != cudaSuccess) return e;
+    a.w.first = scratch;
+    a.w.first_swapped = false;
+    a.w.last = nullptr;
+  }
+  return w.dk <= 64 ? walk_t<64, false>(a, s) : walk_t<128, false>(a, s);
 }
 
 cudaError_t la_group_sum(long long rows, int G, int share, int D, bool bf16, const float* part,

@@ -727,40 +727,6 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   }
 }
 
-// The states before each segment from the segments' own: in walk order
-//   X_0 = first, X_{s+1} = a^{steps of s} X_s + local_s;  last = X_nseg.
-// seg [nseg][B][H][dv][dk], overwritten in place.
-__global__ void __launch_bounds__(256) k_la_segments(const TcWalk p, float* seg, const float* first,
-                                                     float* last) {
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int i = blockIdx.x * 256 + threadIdx.x, n = p.dk * p.dv;
-  if (i >= n) return;
-  const float la = p.log_decay[h];
-  int len = p.T;
-  if (p.lens) len = min(max(p.lens[b], 0), p.T);
-  const size_t row = ((size_t)b * p.H + h) * n, stride = (size_t)p.B * p.H * n;
-  const size_t at = row + (p.first_swapped ? (size_t)(i % p.dk) * p.dv + i / p.dk : (size_t)i);
-  float x = first ? first[at] : 0.f;
-  const int span = p.seg_chunks * kQ;
-  for (int j0 = 0; j0 < p.nseg; j0 += 8) {
-    float local[8];  // read ahead: the loads do not wait for one another
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int s = p.reverse ? p.nseg - 1 - j0 - u : j0 + u;
-      local[u] = j0 + u < p.nseg ? seg[s * stride + row + i] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (j0 + u >= p.nseg) break;
-      const int s = p.reverse ? p.nseg - 1 - j0 - u : j0 + u;
-      const int steps = min(max(len - s * span, 0), span);
-      seg[s * stride + row + i] = x;
-      x = fmaf(decay_pow(la, (float)steps), x, local[u]);
-    }
-  }
-  if (last) last[at] = x;
-}
-
 // ---- host --------------------------------------------------------------------------
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -818,23 +784,9 @@ cudaError_t launch_d(const Maps& m, const TcWalk& p, cudaStream_t s) {
 
 }  // namespace
 
+// one CTA an SM
 static int la_tc_segments(int B, int H, int T, int dv) {
-  // One CTA an SM: a row's nc chunks go to one CTA unless that leaves SMs idle.
-  // Splitting a row costs a pass over K and V for the segments' states (about
-  // half a walk) and two more launches, so it has to pay for that.
-  const long long nc = (T + kQ - 1) / kQ, rows = (long long)B * H * ((dv + kV - 1) / kV), sms = 152;
-  auto waves = [&](long long n) { return (rows * n + sms - 1) / sms; };
-  double best = (double)(waves(1) * nc);
-  long long at = 1;
-  for (long long n = 2; n <= nc && n <= 32; ++n) {
-    const long long per = (nc + n - 1) / n;
-    const double cost = 1.5 * (double)(waves(n) * per) + 4.0 + 0.25 * (double)n;
-    if (cost < best) {
-      best = cost;
-      at = n;
-    }
-  }
-  return (int)at;
+  return la_segments((long long)B * H * ((dv + kV - 1) / kV), (T + kQ - 1) / kQ, 152);
 }
 
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv) {
@@ -880,12 +832,9 @@ cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s) {
     p.last = scratch;
     cudaError_t e = launch_d<true, false>(m, p, s);
     if (e != cudaSuccess) return e;
-    {
-      LaunchScope ls("linattn_segments", s);
-      k_la_segments<<<dim3((w.dk * w.dv + 255) / 256, w.H, w.B), 256, 0, s>>>(p, scratch, w.first,
-                                                                              w.last);
-    }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const LaSegments g = {w.B, w.H, w.T, w.dk, w.dv, n, p.seg_chunks * kQ, w.log_decay, w.lens,
+                          scratch, w.first, w.last, w.first_swapped, w.reverse};
+    if ((e = la_segment_states(g, s)) != cudaSuccess) return e;
     p.first = scratch;
     p.first_swapped = 0;
     p.last = nullptr;

@@ -27,19 +27,22 @@ __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f 
 
 // ---- the walk in fp32 on the CUDA cores ---------------------------------------
 //
-// One CTA per (h, 64 columns of v, b, segment of the row), chunks of 64 steps.
-// 256 threads as 16 x 16: thread (ty, tx) forms 4 x 4 blocks of the products
-//   P = mask(Q K^T)      rows 4 ty + a, columns tx + 16 c
+// One CTA per (h, 32 columns of v, b, segment of the row), chunks of 64 steps.
+// 128 threads as 16 x 8: thread (ty, tx) forms 4 x 4 blocks of the products
+//   P = mask(Q K^T)      rows 4 ty + a, columns tx + 8 c
 //   o = P V + lead Q X   rows 4 ty + a, columns 4 tx + b
 //   X = a^n X + K^T w V  rows 4 ty + a (+ 64), columns 4 tx + b, in registers
 // with operands in shared memory, 16 bytes at a time: eight 16-byte loads (12
 // shared-memory cycles) serve 64 FMAs of a warp (16 cycles of the SM's FMA
 // units), so the FMAs bound it; P and P V leave out the columns that the mask
-// empties for a warp's eight rows.  fp32 throughout: the operands' type leaves
+// empties for a warp's sixteen rows.  64 columns of v form P twice, for a
+// quarter more FMAs, but three of these CTAs run on an SM and hide one
+// another's loads (64 columns in one CTA of 256 threads measured 318 us on
+// 8 x 1024 steps, 24 heads of 64/64).  fp32 throughout: the operands' type leaves
 // no other choice that keeps their precision.
 constexpr int kC = 64;         // steps of a chunk
-constexpr int kB = 64;         // columns of v of a CTA
-constexpr int kThreads = 256;
+constexpr int kB = 32;         // columns of v of a CTA
+constexpr int kThreads = 128;
 
 template <int DK>
 struct Simt {
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ Si
   __shared__ float pw[kC + 2];
   const int vblocks = (w.dv + kB - 1) / kB;
   const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kB;
-  const int b = blockIdx.y, seg = blockIdx.z, t = threadIdx.x, tx = t & 15, ty = t >> 4, wp = t >> 5;
+  const int b = blockIdx.y, seg = blockIdx.z, t = threadIdx.x, tx = t & 7, ty = t >> 3, wp = t >> 5;
   const float la = w.log_decay[h];
   int len = w.T;
   if (w.lens) len = min(max(w.lens[b], 0), w.T);
@@ -118,26 +121,37 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ Si
             make_float4(x[a][0], x[a][1], x[a][2], x[a][3]);
     __syncthreads();
     if (!kStates) {
-      // columns tx + 16 c that the warp's rows 8 wp ... 8 wp + 7 need
-      const int ca = w.reverse ? wp / 2 : 0, cb = w.reverse ? 4 : wp / 2 + 1;
+      // groups of 32 columns (tx + 8 c, c in fours) that the warp's rows 16 wp ...
+      // 16 wp + 15 need
+      const int ca = w.reverse ? wp / 2 : 0, cb = w.reverse ? 2 : wp / 2 + 1;
 #pragma unroll 1
       for (int c = ca; c < cb; ++c) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const float* kr = K + (tx + 16 * c) * G::LK;
-#pragma unroll 8
-        for (int d = 0; d < DK; d += 4) {
-          const float4 kk = ld4(kr + d);
+        float s[4][4];
 #pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const float4 q = ld4(Q + (4 * ty + a) * G::LK + d);
-            s[a] = fmaf(q.x, kk.x, fmaf(q.y, kk.y, fmaf(q.z, kk.z, fmaf(q.w, kk.w, s[a]))));
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[a][e] = 0.f;
+        const float* kr = K + (tx + 32 * c) * G::LK;
+#pragma unroll 4
+        for (int d = 0; d < DK; d += 4) {
+          float4 q[4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) q[a] = ld4(Q + (4 * ty + a) * G::LK + d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 kk = ld4(kr + 8 * e * G::LK + d);
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+              s[a][e] = fmaf(q[a].x, kk.x, fmaf(q[a].y, kk.y, fmaf(q[a].z, kk.z, fmaf(q[a].w, kk.w, s[a][e]))));
           }
         }
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int i = 4 * ty + a, j = tx + 16 * c, d = w.reverse ? j - i : i - j;
-          P[i * G::LP + j] = d >= 0 ? w.s_intra * pw[d] * s[a] : 0.f;
-        }
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * ty + a, j = tx + 32 * c + 8 * e, d = w.reverse ? j - i : i - j;
+            P[i * G::LP + j] = d >= 0 ? w.s_intra * pw[d] * s[a][e] : 0.f;
+          }
       }
       __syncwarp();  // (a warp reads the rows of P that it wrote)
       float o[4][4], u[4][4];
@@ -164,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ Si
         }
       };
 #pragma unroll 4
-      for (int j = 16 * ca; j < 16 * cb; j += 4)
+      for (int j = w.reverse ? 16 * wp : 0; j < (w.reverse ? kC : 16 * wp + 16); j += 4)
         rank4(P + 4 * ty * G::LP + j, G::LP, V + j * kB + 4 * tx, o);
 #pragma unroll 4
       for (int d = 0; d < DK; d += 4)
@@ -361,10 +375,10 @@ cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// CTAs of the fp32 walk that run at once on 152 SMs (two of 81 KB, or one of 131)
+// CTAs of the fp32 walk that run at once on 152 SMs (three of 70 KB, or two of 112)
 static int simt_segments(int B, int H, int T, int dk, int dv) {
   return la_segments((long long)B * H * ((dv + kB - 1) / kB), (T + kC - 1) / kC,
-                     dk <= 64 ? 304 : 152);
+                     dk <= 64 ? 456 : 304);
 }
 
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16) {

@@ -13,8 +13,9 @@
 //
 // Bound by memory: the forward moves r, y, z, r', x, the backward y, z, r',
 // dx, dn, dr, dy, dz, each once.  W warps hold a row, eight elements a lane in
-// registers (16-byte loads where the rows are aligned for it); a CTA of 256
-// threads or more walks groups of rows.
+// registers; a CTA of 256 threads or more walks groups of rows, the next row's
+// 16-byte pieces on their way while it works on the current one (where the rows
+// are aligned for that; else elements are loaded one by one).
 #include <cuda_bf16.h>
 
 #include "ssd_common.cuh"
@@ -137,80 +138,198 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* red, int buf, in
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
+// One operand's eight elements of a lane as they come from memory: 16-byte
+// pieces in the vector case.  The vector case copies the next row's pieces into
+// shared memory (cp.async, two stages) while the current row is worked on; a
+// thread reads back only what it copied itself.
+template <typename T, bool VEC>
+struct Pieces {
+  static constexpr int n = VEC ? kL * (int)sizeof(T) / 16 : 0;
+};
+// (a CTA of 1024 threads has too little shared memory for two stages)
+template <bool VEC, int W>
+constexpr bool kStaged = VEC && W < 32;
+
+__device__ __forceinline__ void cp_async16(uint4* smem, const void* gmem, bool in) {
+  // (0 bytes of the source: zeros are written)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (unsigned)__cvta_generic_to_shared(smem)),
+               "l"(gmem), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// The pieces of a row into slots [piece][thread]; U: the type of the column rule.
+template <typename U, int W, typename T>
+__device__ __forceinline__ void fetch(uint4* slot, const T* row, int lane, int width) {
+#pragma unroll
+  for (int i = 0; i < Pieces<T, true>::n; ++i) {
+    const int c = column<U, true, W>(lane, i * (16 / (int)sizeof(T)));
+    const bool in = c < width;
+    cp_async16(slot + i * Shape<W>::kThreads, in ? row + c : row, in);
+  }
+}
+template <typename T, int W>
+__device__ __forceinline__ void unpack(const uint4* slot, float (&v)[kL]) {
+#pragma unroll
+  for (int i = 0; i < Pieces<T, true>::n; ++i) {
+    const uint4 q = slot[i * Shape<W>::kThreads];
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162* h = (const __nv_bfloat162*)&q;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __bfloat1622float2(h[j]);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+    } else {
+      const float4 f = *(const float4*)&q;
+      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+    }
+  }
+}
+
 template <typename T, typename TR, bool VEC, int W>
-__global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_fwd(BlockNorm p) {
-  constexpr int R = Shape<W>::kRows;
+__global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_fwd(const BlockNorm p) {
+  constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads;
+  constexpr bool S = kStaged<VEC, W>;
+  constexpr int nT = Pieces<T, VEC>::n, nR = Pieces<TR, VEC>::n, nS = 2 * nT + nR;
   __shared__ float red[2 * 2 * R * W];
+  extern __shared__ uint4 stage[];  // [2][y, z, residual][piece][thread]
   const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
   const float inv_w = 1.f / (float)p.width;
   const long long steps = (p.rows + R - 1) / R;
-  for (long long i = blockIdx.x; i < steps; i += gridDim.x) {
+  auto slot = [&](int st, int at) { return stage + (st * nS + at) * NT + threadIdx.x; };
+  auto prefetch = [&](long long i, int st) {
+    const long long row = i * R + group;
+    const bool in = i < steps && row < p.rows;
+    const long long r = in ? row : 0;
+    const int width = in ? p.width : 0;
+    fetch<T, W>(slot(st, 0), (const T*)p.y + r * p.y_stride, lane, width);
+    if (p.z) fetch<T, W>(slot(st, nT), (const T*)p.z + r * p.z_stride, lane, width);
+    fetch<T, W>(slot(st, 2 * nT), (const TR*)p.residual + r * p.width, lane, width);
+    cp_commit();
+  };
+  float wa[kL], wq[kL];  // res_scale w_post, w_pre
+  load_row<T, VEC, W>(p.w_post, lane, p.width, wa);
+  if (p.res_scale) {
+    load_row<T, VEC, W>(p.res_scale, lane, p.width, wq);
+#pragma unroll
+    for (int e = 0; e < kL; ++e) wa[e] *= wq[e];
+  }
+  load_row<T, VEC, W>(p.w_pre, lane, p.width, wq);
+  int st = 0;
+  if constexpr (S) prefetch(blockIdx.x, 0);
+  for (long long i = blockIdx.x; i < steps; i += gridDim.x, st ^= 1) {
     const long long row = i * R + group;
     const bool in = row < p.rows;
     const int width = in ? p.width : 0;
-    float y[kL], z[kL], r[kL], w[kL];
-    load_row<T, VEC, W>((const T*)p.y + row * p.y_stride, lane, width, y);
-    if (p.z) load_row<T, VEC, W>((const T*)p.z + row * p.z_stride, lane, width, z);
-    load_row<T, VEC, W>((const TR*)p.residual + row * p.width, lane, width, r);
+    float y[kL], z[kL], r[kL];
+    if constexpr (S) {
+      prefetch(i + gridDim.x, st ^ 1);
+      cp_wait1();
+      unpack<T, W>(slot(st, 0), y);
+      if (p.z) unpack<T, W>(slot(st, nT), z);
+      unpack<TR, W>(slot(st, 2 * nT), r);
+    } else {
+      load_row<T, VEC, W>((const T*)p.y + row * p.y_stride, lane, width, y);
+      if (p.z) load_row<T, VEC, W>((const T*)p.z + row * p.z_stride, lane, width, z);
+      load_row<T, VEC, W>((const TR*)p.residual + row * p.width, lane, width, r);
+    }
     float s[1] = {0.f};
 #pragma unroll
     for (int e = 0; e < kL; ++e) s[0] = fmaf(y[e], y[e], s[0]);
-    row_sums<W>(s, red, 0, group);
-    const float iy = 1.f / sqrtf(s[0] * inv_w + p.eps);
-    load_row<T, VEC, W>(p.w_post, lane, width, w);
-#pragma unroll
-    for (int e = 0; e < kL; ++e) y[e] *= iy * w[e];
     if (p.z)
 #pragma unroll
       for (int e = 0; e < kL; ++e) y[e] *= z[e] * sigmoid(z[e]);
-    if (p.res_scale) {
-      load_row<T, VEC, W>(p.res_scale, lane, width, w);
-#pragma unroll
-      for (int e = 0; e < kL; ++e) y[e] *= w[e];
-    }
+    row_sums<W>(s, red, 0, group);
+    const float iy = 1.f / sqrtf(s[0] * inv_w + p.eps);
     s[0] = 0.f;
 #pragma unroll
     for (int e = 0; e < kL; ++e) {
-      r[e] += y[e];
+      r[e] = fmaf(y[e] * iy, wa[e], r[e]);
       s[0] = fmaf(r[e], r[e], s[0]);
     }
+    store_row<T, VEC, W>((TR*)p.new_residual + row * p.width, lane, width, r);
     row_sums<W>(s, red, 1, group);
     const float ir = 1.f / sqrtf(s[0] * inv_w + p.eps);
-    store_row<T, VEC, W>((TR*)p.new_residual + row * p.width, lane, width, r);
-    load_row<T, VEC, W>(p.w_pre, lane, width, w);
 #pragma unroll
-    for (int e = 0; e < kL; ++e) r[e] *= ir * w[e];
+    for (int e = 0; e < kL; ++e) r[e] *= ir * wq[e];
     store_row<T, VEC, W>((T*)p.x + row * p.width, lane, width, r);
     if (p.stats && in && lane == 0) ((float2*)p.stats)[row] = make_float2(iy, ir);
   }
+  if constexpr (S) cp_wait0();
 }
 
 // part: [grid][2][width] sums of dr n s and of dx r' ir over a CTA's rows.
 template <typename T, typename TR, bool VEC, int W>
-__global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(BlockNorm p) {
-  constexpr int R = Shape<W>::kRows;
+__global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(const BlockNorm p) {
+  constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads;
+  constexpr bool S = kStaged<VEC, W>;
+  constexpr int nT = Pieces<T, VEC>::n, nR = Pieces<TR, VEC>::n, nS = 3 * nT + 2 * nR;
   __shared__ float red[2 * 3 * R * W];
-  extern __shared__ float cols[];  // [R][2][width], R > 1
+  // [2][y, z, dx, r', dn][piece][thread]; after the rows [R][2][width] (R > 1)
+  extern __shared__ uint4 stage[];
   const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
   const float inv_w = 1.f / (float)p.width;
   const long long steps = (p.rows + R - 1) / R;
-  float cp[kL], cq[kL];
+  auto slot = [&](int st, int at) { return stage + (st * nS + at) * NT + threadIdx.x; };
+  auto prefetch = [&](long long i, int st) {
+    const long long row = i * R + group;
+    const bool in = i < steps && row < p.rows;
+    const long long r = in ? row : 0;
+    const int width = in ? p.width : 0;
+    fetch<T, W>(slot(st, 0), (const T*)p.y + r * p.y_stride, lane, width);
+    if (p.z) fetch<T, W>(slot(st, nT), (const T*)p.z + r * p.z_stride, lane, width);
+    fetch<T, W>(slot(st, 2 * nT), (const T*)p.dx + r * p.width, lane, width);
+    fetch<T, W>(slot(st, 3 * nT), (const TR*)p.residual + r * p.width, lane, width);
+    if (p.dnew) fetch<T, W>(slot(st, 3 * nT + nR), (const TR*)p.dnew + r * p.width, lane, width);
+    cp_commit();
+  };
+  // the column sums: registers, or for rows of 1024 threads (64 registers each)
+  // shared memory, [sum][element][thread]
+  constexpr int nA = W == 32 ? 1 : kL;
+  float cp[nA], cq[nA];
+  float* sums = (float*)stage + threadIdx.x;
 #pragma unroll
-  for (int e = 0; e < kL; ++e) cp[e] = cq[e] = 0.f;
-  for (long long i = blockIdx.x; i < steps; i += gridDim.x) {
+  for (int e = 0; e < kL; ++e) {
+    if constexpr (W == 32) sums[e * NT] = sums[(kL + e) * NT] = 0.f;
+    else cp[e] = cq[e] = 0.f;
+  }
+  auto add_p = [&](int e, float a, float b) {
+    if constexpr (W == 32) sums[e * NT] = fmaf(a, b, sums[e * NT]);
+    else cp[e] = fmaf(a, b, cp[e]);
+  };
+  auto add_q = [&](int e, float a, float b) {
+    if constexpr (W == 32) sums[(kL + e) * NT] = fmaf(a, b, sums[(kL + e) * NT]);
+    else cq[e] = fmaf(a, b, cq[e]);
+  };
+  int st = 0;
+  if constexpr (S) prefetch(blockIdx.x, 0);
+  for (long long i = blockIdx.x; i < steps; i += gridDim.x, st ^= 1) {
     const long long row = i * R + group;
     const bool in = row < p.rows;
     const int width = in ? p.width : 0;
-    float y[kL], z[kL], r[kL], dx[kL], dr[kL], w[kL];
-    load_row<T, VEC, W>((const T*)p.y + row * p.y_stride, lane, width, y);
-    if (p.z) load_row<T, VEC, W>((const T*)p.z + row * p.z_stride, lane, width, z);
-    load_row<T, VEC, W>((const TR*)p.residual + row * p.width, lane, width, r);
-    load_row<T, VEC, W>((const T*)p.dx + row * p.width, lane, width, dx);
-    if (p.dnew) load_row<T, VEC, W>((const TR*)p.dnew + row * p.width, lane, width, dr);
-    else
+    float y[kL], r[kL], dx[kL], dr[kL], w[kL];
+    if constexpr (S) {
+      prefetch(i + gridDim.x, st ^ 1);
+      cp_wait1();
+      unpack<T, W>(slot(st, 0), y);
+      unpack<T, W>(slot(st, 2 * nT), dx);
+      unpack<TR, W>(slot(st, 3 * nT), r);
+      if (p.dnew) unpack<TR, W>(slot(st, 3 * nT + nR), dr);
+    } else {
+      load_row<T, VEC, W>((const T*)p.y + row * p.y_stride, lane, width, y);
+      load_row<T, VEC, W>((const T*)p.dx + row * p.width, lane, width, dx);
+      load_row<T, VEC, W>((const TR*)p.residual + row * p.width, lane, width, r);
+      if (p.dnew) load_row<T, VEC, W>((const TR*)p.dnew + row * p.width, lane, width, dr);
+    }
+    if (!p.dnew)
 #pragma unroll
       for (int e = 0; e < kL; ++e) dr[e] = 0.f;
-    load_row<T, VEC, W>(p.w_pre, lane, width, w);
+    load_row<T, VEC, W>(p.w_pre, lane, p.width, w);
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < kL; ++e) {
@@ -221,9 +340,9 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(BlockNorm
     row_sums<W>(s, red, 0, group);
     float ir, iy;
     if (p.stats) {
-      const float2 st = in ? ((const float2*)p.stats)[row] : make_float2(0.f, 0.f);
-      iy = st.x;
-      ir = st.y;
+      const float2 stt = in ? ((const float2*)p.stats)[row] : make_float2(0.f, 0.f);
+      iy = stt.x;
+      ir = stt.y;
     } else {
       ir = 1.f / sqrtf(s[1] * inv_w + p.eps);
       iy = 1.f / sqrtf(s[2] * inv_w + p.eps);
@@ -232,38 +351,38 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(BlockNorm
 #pragma unroll
     for (int e = 0; e < kL; ++e) {
       dr[e] += fmaf(ir * dx[e], w[e], -kr * r[e]);
-      cq[e] = fmaf(dx[e] * ir, r[e], cq[e]);
+      add_q(e, dx[e] * ir, r[e]);
     }
     store_row<T, VEC, W>((TR*)p.dresidual + row * p.width, lane, width, dr);
-    // dx now holds dr n: n = y iy
-#pragma unroll
-    for (int e = 0; e < kL; ++e) dx[e] = dr[e] * y[e] * iy;
-    load_row<T, VEC, W>(p.w_post, lane, width, w);
+    // from here w = alpha w_post, dx = dr n with n = y iy
+    load_row<T, VEC, W>(p.w_post, lane, p.width, w);
     if (p.res_scale) {
-      float al[kL];
-      load_row<T, VEC, W>(p.res_scale, lane, width, al);
+      load_row<T, VEC, W>(p.res_scale, lane, p.width, r);
 #pragma unroll
-      for (int e = 0; e < kL; ++e) w[e] *= al[e];
+      for (int e = 0; e < kL; ++e) w[e] *= r[e];
     }
-    // w = alpha w_post
+#pragma unroll
+    for (int e = 0; e < kL; ++e) {
+      dx[e] = dr[e] * y[e] * iy;
+      dr[e] *= w[e];
+    }
     float t[1] = {0.f};
     if (p.z) {
-      float dz[kL];
+      if constexpr (S) unpack<T, W>(slot(st, nT), r);
+      else load_row<T, VEC, W>((const T*)p.z + row * p.z_stride, lane, width, r);
 #pragma unroll
       for (int e = 0; e < kL; ++e) {
-        const float sg = sigmoid(z[e]);
-        dz[e] = dx[e] * w[e] * (sg * fmaf(z[e], 1.f - sg, 1.f));
-        const float g = z[e] * sg;
-        cp[e] = fmaf(dx[e], g, cp[e]);
-        dr[e] *= g * w[e];
+        const float sg = sigmoid(r[e]), g = r[e] * sg;
+        add_p(e, dx[e], g);
+        dx[e] *= w[e] * (sg * fmaf(r[e], 1.f - sg, 1.f));
+        dr[e] *= g;
         t[0] = fmaf(dr[e], y[e], t[0]);
       }
-      store_row<T, VEC, W>((T*)p.dz + row * p.width, lane, width, dz);
+      store_row<T, VEC, W>((T*)p.dz + row * p.width, lane, width, dx);
     } else {
 #pragma unroll
       for (int e = 0; e < kL; ++e) {
-        cp[e] += dx[e];
-        dr[e] *= w[e];
+        add_p(e, dx[e], 1.f);
         t[0] = fmaf(dr[e], y[e], t[0]);
       }
     }
@@ -273,23 +392,26 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(BlockNorm
     for (int e = 0; e < kL; ++e) dr[e] = fmaf(iy, dr[e], -ky * y[e]);
     store_row<T, VEC, W>((T*)p.dy + row * p.width, lane, width, dr);
   }
+  if constexpr (S) cp_wait0();
   float* part = p.part + (size_t)blockIdx.x * 2 * p.width;
   if constexpr (R == 1) {
 #pragma unroll
     for (int e = 0; e < kL; ++e) {
       const int c = column<T, VEC, W>(lane, e);
       if (c < p.width) {
-        part[c] = cp[e];
-        part[p.width + c] = cq[e];
+        part[c] = W == 32 ? sums[e * NT] : cp[W == 32 ? 0 : e];
+        part[p.width + c] = W == 32 ? sums[(kL + e) * NT] : cq[W == 32 ? 0 : e];
       }
     }
   } else {
+    float* cols = (float*)stage;
+    __syncthreads();  // every thread has read its last row
 #pragma unroll
     for (int e = 0; e < kL; ++e) {
       const int c = column<T, VEC, W>(lane, e);
       if (c < p.width) {
-        cols[(group * 2) * p.width + c] = cp[e];
-        cols[(group * 2 + 1) * p.width + c] = cq[e];
+        cols[(group * 2) * p.width + c] = cp[W == 32 ? 0 : e];
+        cols[(group * 2 + 1) * p.width + c] = cq[W == 32 ? 0 : e];
       }
     }
     __syncthreads();
@@ -329,23 +451,49 @@ __global__ void __launch_bounds__(32 * kSlices) k_block_norm_dw(int ncta, BlockN
   }
 }
 
+// A persistent grid: the CTAs that run at once, at most `cap` (the backward's
+// partial rows).
+template <typename KernelT>
+cudaError_t grid_for(KernelT kernel, int threads, size_t smem, long long steps, int cap, int* grid) {
+  int dev = 0, nsm = 0, occ = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
+  long long g = (long long)nsm * (occ > 0 ? occ : 1);
+  if (g > cap) g = cap;
+  if (g > steps) g = steps;
+  *grid = (int)g;
+  return cudaSuccess;
+}
+
 template <typename T, typename TR, bool VEC, int W>
 cudaError_t launch(const BlockNorm& p, bool backward, int* grid_out, cudaStream_t s) {
-  constexpr int R = Shape<W>::kRows;
+  constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads;
   const long long steps = (p.rows + R - 1) / R;
+  int grid = 1;
   if (!backward) {
-    // CTAs that fit: up to 2048 threads an SM of 152
-    const long long cap = 152ll * (2048 / Shape<W>::kThreads);
+    constexpr size_t smem =
+        kStaged<VEC, W> ? (size_t)2 * (2 * Pieces<T, VEC>::n + Pieces<TR, VEC>::n) * NT * 16 : 0;
+    cudaError_t e = grid_for(k_block_norm_fwd<T, TR, VEC, W>, NT, smem, steps, 1 << 20, &grid);
+    if (e != cudaSuccess) return e;
     LaunchScope ls("block_norm_fwd", s);
-    k_block_norm_fwd<T, TR, VEC, W>
-        <<<(unsigned)(steps < cap ? steps : cap), Shape<W>::kThreads, 0, s>>>(p);
+    k_block_norm_fwd<T, TR, VEC, W><<<grid, NT, smem, s>>>(p);
     return cudaGetLastError();
   }
-  const int grid = (int)(steps < kBlockNormMaxCtas ? steps : kBlockNormMaxCtas);
+  size_t smem =
+      kStaged<VEC, W> ? (size_t)2 * (3 * Pieces<T, VEC>::n + 2 * Pieces<TR, VEC>::n) * NT * 16 : 0;
+  const size_t cols = R > 1 ? (size_t)R * 2 * p.width * sizeof(float)
+                            : W == 32 ? (size_t)2 * kL * NT * sizeof(float) : 0;
+  if (cols > smem) smem = cols;
+  cudaError_t e = grid_for(k_block_norm_bwd<T, TR, VEC, W>, NT, smem, steps, kBlockNormMaxCtas, &grid);
+  if (e != cudaSuccess) return e;
   *grid_out = grid;
-  const size_t smem = R > 1 ? (size_t)R * 2 * p.width * sizeof(float) : 0;
   LaunchScope ls("block_norm_bwd", s);
-  k_block_norm_bwd<T, TR, VEC, W><<<grid, Shape<W>::kThreads, smem, s>>>(p);
+  k_block_norm_bwd<T, TR, VEC, W><<<grid, NT, smem, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -124,19 +124,26 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* red, int buf, in
     float* r = red + ((buf * Shape<W>::kRows + group) * W) * NV;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) r[warp * NV + i] = v[i];
+      for (int i = 0; i < NV; ++i) r[i * W + warp] = v[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float t = 0.f;
 #pragma unroll
-      for (int j = 0; j < W; ++j) t += r[j * NV + i];
+      for (int j = 0; j < W; ++j) t += r[i * W + j];
       v[i] = t;
     }
   }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// 1 / (1 + 2^(-z log2 e)) from the hardware's base-2 exponential and reciprocal
+// (errors of a few 2^-23; 2^(+large) = inf gives 0, 2^(-large) = 0 gives 1)
+__device__ __forceinline__ float sigmoid(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
 // One operand's eight elements of a lane as they come from memory: 16-byte
 // pieces in the vector case.  The vector case copies the next row's pieces into
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_fwd(const Blo
   constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads;
   constexpr bool S = kStaged<VEC, W>;
   constexpr int nT = Pieces<T, VEC>::n, nR = Pieces<TR, VEC>::n, nS = 2 * nT + nR;
-  __shared__ float red[2 * 2 * R * W];
+  __shared__ __align__(16) float red[2 * 2 * R * W];
   extern __shared__ uint4 stage[];  // [2][y, z, residual][piece][thread]
   const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
   const float inv_w = 1.f / (float)p.width;
@@ -265,13 +272,17 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_fwd(const Blo
 
 // part: [grid][2][width] sums of dr n s and of dx r' ir over a CTA's rows.
 template <typename T, typename TR, bool VEC, int W>
-__global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(const BlockNorm p) {
+__global__ void __launch_bounds__(Shape<W>::kThreads, W <= 8 ? 3 : 1) k_block_norm_bwd(const BlockNorm p) {
   constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads;
   constexpr bool S = kStaged<VEC, W>;
   constexpr int nT = Pieces<T, VEC>::n, nR = Pieces<TR, VEC>::n, nS = 3 * nT + 2 * nR;
-  __shared__ float red[2 * 3 * R * W];
+  __shared__ __align__(16) float red[2 * 3 * R * W];
+  // [2][8][lane of the row]: w_pre, res_scale w_post by element, then
   // [2][y, z, dx, r', dn][piece][thread]; after the rows [R][2][width] (R > 1)
-  extern __shared__ uint4 stage[];
+  extern __shared__ uint4 shared[];
+  constexpr int NL = W * 32;
+  float* weights = (float*)shared;
+  uint4* stage = shared + 2 * kL * NL / 4;
   const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
   const float inv_w = 1.f / (float)p.width;
   const long long steps = (p.rows + R - 1) / R;
@@ -308,6 +319,18 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(const Blo
   };
   int st = 0;
   if constexpr (S) prefetch(blockIdx.x, 0);
+  if (group == 0) {
+    float a[kL], q[kL], al[kL];
+    load_row<T, VEC, W>(p.w_post, lane, p.width, a);
+    load_row<T, VEC, W>(p.w_pre, lane, p.width, q);
+    if (p.res_scale) load_row<T, VEC, W>(p.res_scale, lane, p.width, al);
+#pragma unroll
+    for (int e = 0; e < kL; ++e) {
+      weights[e * NL + lane] = q[e];
+      weights[(kL + e) * NL + lane] = p.res_scale ? a[e] * al[e] : a[e];
+    }
+  }
+  __syncthreads();
   for (long long i = blockIdx.x; i < steps; i += gridDim.x, st ^= 1) {
     const long long row = i * R + group;
     const bool in = row < p.rows;
@@ -329,7 +352,8 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(const Blo
     if (!p.dnew)
 #pragma unroll
       for (int e = 0; e < kL; ++e) dr[e] = 0.f;
-    load_row<T, VEC, W>(p.w_pre, lane, p.width, w);
+#pragma unroll
+    for (int e = 0; e < kL; ++e) w[e] = weights[e * NL + lane];
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < kL; ++e) {
@@ -354,13 +378,9 @@ __global__ void __launch_bounds__(Shape<W>::kThreads) k_block_norm_bwd(const Blo
       add_q(e, dx[e] * ir, r[e]);
     }
     store_row<T, VEC, W>((TR*)p.dresidual + row * p.width, lane, width, dr);
-    // from here w = alpha w_post, dx = dr n with n = y iy
-    load_row<T, VEC, W>(p.w_post, lane, p.width, w);
-    if (p.res_scale) {
-      load_row<T, VEC, W>(p.res_scale, lane, p.width, r);
+    // from here w = res_scale w_post, dx = dr n with n = y iy
 #pragma unroll
-      for (int e = 0; e < kL; ++e) w[e] *= r[e];
-    }
+    for (int e = 0; e < kL; ++e) w[e] = weights[(kL + e) * NL + lane];
 #pragma unroll
     for (int e = 0; e < kL; ++e) {
       dx[e] = dr[e] * y[e] * iy;
@@ -489,6 +509,7 @@ cudaError_t launch(const BlockNorm& p, bool backward, int* grid_out, cudaStream_
   const size_t cols = R > 1 ? (size_t)R * 2 * p.width * sizeof(float)
                             : W == 32 ? (size_t)2 * kL * NT * sizeof(float) : 0;
   if (cols > smem) smem = cols;
+  smem += (size_t)2 * kL * W * 32 * sizeof(float);
   cudaError_t e = grid_for(k_block_norm_bwd<T, TR, VEC, W>, NT, smem, steps, kBlockNormMaxCtas, &grid);
   if (e != cudaSuccess) return e;
   *grid_out = grid;

@@ -292,14 +292,34 @@ __global__ void k_la_group_sum(long long n, int share, int D, const float* __res
   }
 }
 
-// One token: S' = a S + v k^T, o = s S' q.  A warp takes rows v of the state,
-// 32 / LPR at a time (a row of dk floats is held by LPR lanes, four floats
-// each).
+// One token: S' = a S + v k^T, o = s S' q.  A row of the state (dk floats) is
+// held by LPR lanes, four floats each; a warp takes NR rows a lane at once, so
+// that as many 16-byte loads are in flight, and adds the NR dot products up
+// together: while a lane holds several, each exchange halves them (lanes of one
+// half keep one half of the values), nine exchanges for eight sums over 32
+// lanes instead of forty.
+//
+// Bound by the states' bytes, read and written once.  Measured on 256 rows of
+// 64 heads, 128 x 64 (1.08 GB): 191 us with one row a lane at a time and sixteen
+// rows a CTA, 160 us with eight.
 constexpr int kStepWarps = 4;
-constexpr int kStepRows = 16;  // rows of a CTA
 
-template <typename T, int LPR>
-__global__ void __launch_bounds__(kStepWarps * 32) k_la_step(LaStep p) {
+// four consecutive operands of a lane
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 f = *(const float4*)p;
+  v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 q = *(const uint2*)p;
+  const float2 a = __bfloat1622float2(*(const __nv_bfloat162*)&q.x);
+  const float2 b = __bfloat1622float2(*(const __nv_bfloat162*)&q.y);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+
+template <typename T, int LPR, int NR>
+__global__ void __launch_bounds__(kStepWarps * 32) k_la_step(const LaStep p) {
+  constexpr int RPW = 32 / LPR;                  // rows of a warp side by side
+  constexpr int kRows = kStepWarps * RPW * NR;   // rows of a CTA
   const int h = blockIdx.y, b = blockIdx.z, g = h / (p.H / p.G);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LPR, k0 = sub * 4;
@@ -309,44 +329,79 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_la_step(LaStep p) {
     row = p.slots[b];
     if (row < 0 || row >= p.nslots) row = -1;
   }
+  const int vb = blockIdx.x * kRows + warp * (RPW * NR) + lane / LPR;  // row of slot i: + i RPW
+  const long long at = ((row * p.H + h) * p.dv + vb) * p.dk + k0;
+  float4 s[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+    s[i] = kin && row >= 0 && vb + i * RPW < p.dv
+               ? *(const float4*)(p.state_in + at + (long long)i * RPW * p.dk)
+               : make_float4(0.f, 0.f, 0.f, 0.f);
   const float a = decay_pow(p.log_decay[b * p.decay_batch + h], 1.f);
-  float q[4], k[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    q[i] = kin ? to_f32(((const T*)p.q)[b * p.q_batch + (long long)g * p.dk + k0 + i]) : 0.f;
-    k[i] = kin ? to_f32(((const T*)p.k)[b * p.k_batch + (long long)g * p.dk + k0 + i]) : 0.f;
+  float q[4] = {0.f, 0.f, 0.f, 0.f}, k[4] = {0.f, 0.f, 0.f, 0.f};
+  if (kin) {
+    load4((const T*)p.q + b * p.q_batch + (long long)g * p.dk + k0, q);
+    load4((const T*)p.k + b * p.k_batch + (long long)g * p.dk + k0, k);
   }
-  constexpr int RPW = 32 / LPR;
-  for (int v0 = blockIdx.x * kStepRows + warp * RPW; v0 < min(p.dv, (int)(blockIdx.x + 1) * kStepRows);
-       v0 += kStepWarps * RPW) {
-    const int v = v0 + lane / LPR;
-    const bool in = kin && v < p.dv && row >= 0;
-    const long long at = ((row * p.H + h) * p.dv + v) * p.dk + k0;
-    float4 s = in ? *(const float4*)(p.state_in + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float x = v < p.dv ? to_f32(((const T*)p.v)[b * p.v_batch + (long long)h * p.dv + v]) : 0.f;
-    s.x = fmaf(a, s.x, x * k[0]);
-    s.y = fmaf(a, s.y, x * k[1]);
-    s.z = fmaf(a, s.z, x * k[2]);
-    s.w = fmaf(a, s.w, x * k[3]);
-    if (in) *(float4*)(p.state_out + at) = s;
-    float o = fmaf(s.x, q[0], fmaf(s.y, q[1], fmaf(s.z, q[2], s.w * q[3])));
+  const T* vp = (const T*)p.v + b * p.v_batch + (long long)h * p.dv;
+  float o[NR];
 #pragma unroll
-    for (int d = LPR / 2; d > 0; d >>= 1) o += __shfl_xor_sync(0xffffffffu, o, d);
-    if (sub == 0 && v < p.dv)
-      ((T*)p.o)[((long long)b * p.H + h) * p.dv + v] = from_f32<T>(row >= 0 ? p.scale * o : 0.f);
+  for (int i = 0; i < NR; ++i) {
+    const int v = vb + i * RPW;
+    const float x = v < p.dv ? to_f32(vp[v]) : 0.f;
+    s[i].x = fmaf(a, s[i].x, x * k[0]);
+    s[i].y = fmaf(a, s[i].y, x * k[1]);
+    s[i].z = fmaf(a, s[i].z, x * k[2]);
+    s[i].w = fmaf(a, s[i].w, x * k[3]);
+    if (kin && row >= 0 && v < p.dv) *(float4*)(p.state_out + at + (long long)i * RPW * p.dk) = s[i];
+    o[i] = fmaf(s[i].x, q[0], fmaf(s[i].y, q[1], fmaf(s[i].z, q[2], s[i].w * q[3])));
   }
+  int n = NR, first = 0;  // this lane holds the sums first ... first + n - 1
+#pragma unroll
+  for (int d = LPR / 2; d > 0; d >>= 1) {
+    if (n > 1) {
+      const bool up = (sub & d) != 0;
+      n /= 2;
+#pragma unroll
+      for (int i = 0; i < NR / 2; ++i)
+        if (i < n) {
+          const float send = up ? o[i] : o[i + n], keep = up ? o[i + n] : o[i];
+          o[i] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+        }
+      if (up) first += n;
+    } else {
+      o[0] += __shfl_xor_sync(0xffffffffu, o[0], d);
+    }
+  }
+  // lanes that differ below the exchanges that halved hold the same sums
+  if (sub % (LPR * n / NR > 1 ? LPR * n / NR : 1) == 0)
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      if (i < n && vb + (first + i) * RPW < p.dv)
+        ((T*)p.o)[((long long)b * p.H + h) * p.dv + vb + (first + i) * RPW] =
+            from_f32<T>(row >= 0 ? p.scale * o[i] : 0.f);
+}
+
+template <typename T, int LPR>
+cudaError_t step_l(const LaStep& p, cudaStream_t s) {
+  LaunchScope ls("linattn_step", s);
+  constexpr int rows = kStepWarps * (32 / LPR);
+  // eight rows a lane once that leaves work for every SM (with fewer rows the
+  // latency of one counts: 32 heads of one row ran in 8.1 us with two a lane)
+  if ((long long)p.B * p.H * ((p.dv + 8 * rows - 1) / (8 * rows)) >= 304)
+    k_la_step<T, LPR, 8><<<dim3((p.dv + 8 * rows - 1) / (8 * rows), p.H, p.B), kStepWarps * 32, 0, s>>>(p);
+  else
+    k_la_step<T, LPR, 2><<<dim3((p.dv + 2 * rows - 1) / (2 * rows), p.H, p.B), kStepWarps * 32, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t step_t(const LaStep& p, cudaStream_t s) {
-  const dim3 grid((p.dv + kStepRows - 1) / kStepRows, p.H, p.B);
   const int lanes = p.dk / 4;
-  LaunchScope ls("linattn_step", s);
-  if (lanes <= 4) k_la_step<T, 4><<<grid, kStepWarps * 32, 0, s>>>(p);
-  else if (lanes <= 8) k_la_step<T, 8><<<grid, kStepWarps * 32, 0, s>>>(p);
-  else if (lanes <= 16) k_la_step<T, 16><<<grid, kStepWarps * 32, 0, s>>>(p);
-  else k_la_step<T, 32><<<grid, kStepWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  if (lanes <= 4) return step_l<T, 4>(p, s);
+  if (lanes <= 8) return step_l<T, 8>(p, s);
+  if (lanes <= 16) return step_l<T, 16>(p, s);
+  return step_l<T, 32>(p, s);
 }
 
 }  // namespace
@@ -354,13 +409,14 @@ cudaError_t step_t(const LaStep& p, cudaStream_t s) {
 int la_segments(long long rows, long long chunks, long long slots) {
   // A row's chunks go to one CTA unless that leaves SMs idle.  Splitting a row
   // costs a pass for the segments' states (about half a walk) and two more
-  // launches, so it has to pay for that.
+  // launches, and every wave of CTAs its start (about two chunks), so it has to
+  // pay for that.
   auto waves = [&](long long n) { return (rows * n + slots - 1) / slots; };
-  double best = (double)(waves(1) * chunks);
+  double best = (double)(waves(1) * (chunks + 2));
   int at = 1;
   for (int n = 2; n <= chunks && n <= 32; ++n) {
     const long long per = (chunks + n - 1) / n;
-    const double cost = 1.5 * (double)(waves(n) * per) + 4.0 + 0.25 * n;
+    const double cost = 1.5 * (double)(waves(n) * (per + 2)) + 4.0 + 0.25 * n;
     if (cost < best) {
       best = cost;
       at = n;

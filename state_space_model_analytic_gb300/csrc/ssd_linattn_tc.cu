@@ -264,6 +264,44 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   auto all_wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity, B)) != 0;
   };
+  // w o V of pieces [first, end) of chunk `it`, by 256 threads (t): a row of the
+  // piece and one of its 16-byte chunks each
+  auto pieces = [&](int it, const int first, const int end, int t) {
+    const int r = t & 31, ch = t >> 5, n = valid(chunk(it));
+    const uint8_t* src = sm + G::kVo + (it % NS) * G::VT;
+    uint4 in[4];
+#pragma unroll
+    for (int i = first; i < end; ++i) in[i] = *(const uint4*)(src + sw128(i * kPiece + r, ch));
+#pragma unroll
+    for (int piece = first; piece < end; ++piece) {
+      // the three parts, before the wait for the buffer they go to
+      const int j = piece * kPiece + r;
+      const float w = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
+      const float2 w2 = make_float2(w, w);
+      float2 f[4];
+      unpack8(in[piece], (float*)f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
+      uint4 o[3];
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        o[part] = pack8((const float*)f);
+        float2 m[4];
+        unpack8(o[part], (float*)m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = fma2(m[i], make_float2(-1.f, -1.f), f[i]);
+      }
+      const int wb = piece % NW;  // (its turn: 4 / NW times a chunk)
+      if (!all_wait(&B->wfree[wb], ((it * (4 / NW) + piece / NW) & 1) ^ 1)) return false;
+      uint8_t* dst = sm + G::kWo + wb * 3 * G::WP + sw128(r, ch);
+#pragma unroll
+      for (int part = 0; part < 3; ++part) *(uint4*)(dst + part * G::WP) = o[part];
+      fence_async_smem();
+      fence_before_sync();
+      warp_arrive(&B->w[wb]);
+    }
+    return true;
+  };
   // zeros into a row of a stage: 64 bytes of each 128-byte row of each tile
   auto clear_row = [&](int s, int row, int hf) {
     const uint4 z = make_uint4(0, 0, 0, 0);
@@ -454,11 +492,14 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         go = go && all_wait(&B->w[wb], (it * (4 / NW) + piece / NW) & 1);
         if (!go) break;
         fence_after_sync();
+        // (two accumulators in turn in a states walk, which has the columns: the
+        // first pieces come before the last U is read)
+        const uint32_t u0 = kStates ? (it & 1) * 192 : cU;
         const uint64_t dK = dK0 + (s * (G::QT >> 4) + piece * (kPiece * 8));
         const uint64_t dW = dW0 + wb * (3 * G::WP >> 4);
 #pragma unroll
         for (int kk = 0; kk < kPiece / 16; ++kk)
-          mma_ss(lead, tm + cU, dK + 128 * kk, dW + 128 * kk, id_u, piece + kk > 0);
+          mma_ss(lead, tm + u0, dK + 128 * kk, dW + 128 * kk, id_u, piece + kk > 0);
         commit_if(lead, &B->wfree[wb]);
       }
       if (!go) break;
@@ -473,6 +514,14 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     // ---- P and o: thread = row i of the chunk and every second 32 columns ----
     const int row = tid & 127, il = row & 31, ib = warp & 3, hf = warp >> 2;
     const uint32_t lane_base = (uint32_t)(ib * 32) << 16;
+    if (kStates) {  // the first two pieces of w o V
+#pragma unroll 1
+      for (int it = 0; it < nit; ++it) {
+        if (!all_wait(&B->fullV[it % NS], (it / NS) & 1)) break;
+        if (ragged(chunk(it)) && !all_wait(&B->fix, 0)) break;
+        if (!pieces(it, 0, 2, tid)) break;
+      }
+    }
     // per turn: o of chunk it - 1 out of TMEM, P of chunk it, then the stores of
     // that o.  (After a wait that gave up the warps still meet at their barriers,
     // without touching the data.)
@@ -613,7 +662,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) X[i] = 0.f;
     const size_t sbase = (((size_t)seg * p.B + b) * p.H + h) * p.dk * p.dv;
-    const int vx = v0 + hf * 32, r = t & 31, ch = t >> 5;
+    const int vx = v0 + hf * 32;
     if (!kStates && p.first && k < p.dk) {
       const float* f = p.first + sbase;
 #pragma unroll
@@ -627,7 +676,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       const uint32_t full = (it / NS) & 1;
       if (!all_wait(&B->fullV[s], full)) break;
       if (ragged(c)) {
-        if (kStates) {  // (warps 0-7 do not follow a states walk's chunks)
+        if (kStates) {  // (where warps 0-7 do not follow K's loads)
           if (!all_wait(&B->fullK[s], full)) break;
           if (k >= n) clear_row(s, k, hf);
           fence_async_smem();
@@ -635,41 +684,8 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         }
         if (!all_wait(&B->fix, 0)) break;
       }
-      const uint8_t* src = sm + G::kVo + s * G::VT;
-      uint4 in[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) in[i] = *(const uint4*)(src + sw128(i * kPiece + r, ch));
-      bool go = true;
-#pragma unroll
-      for (int piece = 0; piece < 4; ++piece) {
-        // the three parts, before the wait for the buffer they go to
-        const int j = piece * kPiece + r;
-        const float w = j < n ? p.s_inject * bars.pw[(p.reverse ? j : n - 1 - j) + 1 - p.off] : 0.f;
-        const float2 w2 = make_float2(w, w);
-        float2 f[4];
-        unpack8(in[piece], (float*)f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
-        uint4 o[3];
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          o[part] = pack8((const float*)f);
-          float2 m[4];
-          unpack8(o[part], (float*)m);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = fma2(m[i], make_float2(-1.f, -1.f), f[i]);
-        }
-        const int wb = piece % NW;  // (its turn: 4 / NW times a chunk)
-        go = go && all_wait(&B->wfree[wb], ((it * (4 / NW) + piece / NW) & 1) ^ 1);
-        if (!go) break;
-        uint8_t* dst = sm + G::kWo + wb * 3 * G::WP + sw128(r, ch);
-#pragma unroll
-        for (int part = 0; part < 3; ++part) *(uint4*)(dst + part * G::WP) = o[part];
-        fence_async_smem();
-        fence_before_sync();
-        warp_arrive(&B->w[wb]);
-      }
-      if (!go) break;
+      // (in a states walk warps 0-7 form the first two pieces)
+      if (!pieces(it, kStates ? 2 : 0, 4, t)) break;
       if (!kStates) {  // X before this chunk, for its Oc
         if (it > 0 && !all_wait(&B->xfree, (it - 1) & 1)) break;
         if (k < DK)
@@ -684,7 +700,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       const float an = bars.pw[n];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const uint32_t at = tm + cU + lane_base + hf * 32 + x * 8;
+        const uint32_t at = tm + (kStates ? (it & 1) * 192 : cU) + lane_base + hf * 32 + x * 8;
         float v[8], m[8], l[8];
         tmem_ld8(at, v);
         tmem_ld8(at + 64, m);

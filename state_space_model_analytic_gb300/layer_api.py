@@ -6,6 +6,7 @@ stream.
 from __future__ import annotations
 
 import array
+import operator
 
 import torch
 
@@ -372,6 +373,9 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
 
 # ---- gradient clipping ---------------------------------------------------------------
 
+_Tensor = torch.Tensor
+_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
 def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, stream=None):
     """Scales the gradients by min(1, max_norm / (n + eps)), n the square root
     of the sum of all their squares; in place, or into the tensors of `out`
@@ -386,25 +390,26 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
         raise ValueError(f"out: {len(outs)} tensors, expected {n}")
     dev = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
     # one list a property: hundreds of tensors are looked through in every call
+    of = lambda f, ts: list(map(f, ts))  # noqa: E731
+    dtypes = of(_dtype, grads)
     try:
-        codes = [_IO_TYPES[g.dtype] for g in grads]
+        codes = [_IO_TYPES[t] for t in dtypes]
     except KeyError:
         raise TypeError("grads: fp32 and bf16 tensors only") from None
-    sizes = [g.numel() for g in grads]
-    at = [g.data_ptr() for g in grads]
-    to = at
-    if any([g.device != dev for g in grads]) or dev.type != "cuda":
+    if dev.type != "cuda" or of(_Tensor.get_device, grads) != [dev.index] * n:
         raise ValueError("grads: must be CUDA tensors on one device (no CPU path exists)")
-    if not all([g.is_contiguous() for g in grads]):
+    if not all(map(_Tensor.is_contiguous, grads)):
         raise ValueError("grads: must be contiguous")
+    sizes, at = of(_Tensor.numel, grads), of(_Tensor.data_ptr, grads)
+    to = at
     if out is not None:
-        if any([o.dtype != g.dtype for o, g in zip(outs, grads)]):
+        if of(_dtype, outs) != dtypes:
             raise TypeError("out: another dtype than the gradient's")
-        if any([o.shape != g.shape or o.device != dev for o, g in zip(outs, grads)]):
+        if of(_shape, outs) != of(_shape, grads) or of(_Tensor.get_device, outs) != [dev.index] * n:
             raise ValueError("out: another shape or device than the gradient's")
-        if not all([o.is_contiguous() for o in outs]):
+        if not all(map(_Tensor.is_contiguous, outs)):
             raise ValueError("out: must be contiguous")
-        to = [o.data_ptr() for o in outs]
+        to = of(_Tensor.data_ptr, outs)
     flat = [0] * (4 * n)  # ssd_clip_tensor: g, out, numel, dtype (with a zero above it)
     flat[0::4], flat[1::4], flat[2::4], flat[3::4] = at, to, sizes, codes
     table = array.array("Q", flat)

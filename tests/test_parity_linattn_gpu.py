@@ -220,7 +220,10 @@ def test_a_row_alone_is_the_row_in_a_batch():
 
 @pytest.mark.parametrize("case", [(1, 1, 1, 8, 8, "f32"), (3, 4, 2, 128, 64, "bf16"),
                                   (2, 6, 3, 80, 40, "bf16"), (5, 2, 2, 64, 128, "f32"),
-                                  (2, 2, 1, 32, 16, "bf16"), (1, 3, 1, 16, 120, "f32")])
+                                  (2, 2, 1, 32, 16, "bf16"), (1, 3, 1, 16, 120, "f32"),
+                                  # enough rows for the larger tiles
+                                  (80, 4, 2, 80, 40, "bf16"), (64, 8, 1, 64, 24, "f32"),
+                                  (160, 4, 4, 32, 72, "bf16"), (320, 2, 1, 16, 8, "f32")])
 @pytest.mark.parametrize("rows", [False, True])
 def test_step(case, rows):
     """One token: a state's element sees two rounded products and a sum, o a sum

@@ -103,7 +103,8 @@ size_t la_scratch_bytes(const ssd_linattn_dims* d) {
 
 size_t la_part_bytes(const ssd_linattn_dims* d, int which) {
   if (which == 0 || d->nheads == d->ngroups) return 0;
-  return up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
+  // dq's and dk's
+  return 2 * up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
 }
 
 int workspace_check(const char* who, const void* workspace, size_t bytes, size_t need) {
@@ -216,7 +217,7 @@ int ssd_linattn_forward(const ssd_linattn_dims* d, const void* q, const void* k,
   w.s_intra = w.s_carry = d->scale;
   w.s_inject = 1.f;
   w.off = 1;
-  const cudaError_t e = la_walk(w, d->dtype == SSD_BF16, (float*)workspace, (cudaStream_t)cuda_stream);
+  const cudaError_t e = la_walk(w, d->dtype == SSD_BF16, false, (float*)workspace, (cudaStream_t)cuda_stream);
   return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
 }
 
@@ -248,54 +249,55 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   float* scratch = (float*)workspace;
   float* part = share > 1 ? (float*)((char*)workspace + la_scratch_bytes(d)) : nullptr;
-  // dq: forward over (do, v, k), from the transposed state
-  LaWalk w = la_base(d, log_decay, lens);
-  w.dk = (int)d->dv;
-  w.dv = (int)d->dk;
-  w.q = og;
-  w.k = ov;
-  w.v = ok;
-  w.first = state0;
-  w.first_swapped = true;
-  w.o = part ? (void*)part : dq;
-  w.o_f32 = part != nullptr;
-  w.s_intra = w.s_carry = d->scale;
-  w.s_inject = 1.f;
-  w.off = 1;
-  cudaError_t e = la_walk(w, bf16, scratch, s);
-  if (e != cudaSuccess) return cuda_refuse(e, who);
-  if (part) {
-    e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk, bf16, part, dq, s);
-    if (e != cudaSuccess) return cuda_refuse(e, who);
-  }
-  // dk: backwards over (v, do, q), from the transposed gradient of the state
-  w.q = ov;
-  w.k = og;
-  w.v = oq;
-  w.first = dstate;
-  w.o = part ? (void*)part : dk;
-  w.s_carry = 1.f;
-  w.s_inject = d->scale;
-  w.off = 0;
-  w.reverse = true;
-  e = la_walk(w, bf16, scratch, s);
-  if (e != cudaSuccess) return cuda_refuse(e, who);
-  if (part) {
-    e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk, bf16, part, dk, s);
-    if (e != cudaSuccess) return cuda_refuse(e, who);
-  }
   // dv, dstate0: backwards over (k, q, do)
+  LaWalk w = la_base(d, log_decay, lens);
   w.dk = (int)d->dk;
   w.dv = (int)d->dv;
   w.q = ok;
   w.k = oq;
   w.v = og;
-  w.first_swapped = false;
+  w.first = dstate;
   w.last = dstate0;
   w.o = dv;
-  w.o_f32 = false;
-  e = la_walk(w, bf16, scratch, s);
-  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+  w.s_intra = w.s_inject = d->scale;
+  w.s_carry = 1.f;
+  w.reverse = true;
+  cudaError_t e = la_walk(w, bf16, false, scratch, s);
+  if (e != cudaSuccess) return cuda_refuse(e, who);
+  // dq: forward over (do, v, k), from the transposed state; dk: backwards over
+  // (v, do, q), from the transposed gradient of the state
+  LaWalk x[2] = {la_base(d, log_decay, lens), la_base(d, log_decay, lens)};
+  for (LaWalk& y : x) {
+    y.dk = (int)d->dv;
+    y.dv = (int)d->dk;
+    y.first_swapped = true;
+    y.o_f32 = part != nullptr;
+    y.s_intra = d->scale;
+  }
+  x[0].q = og;
+  x[0].k = ov;
+  x[0].v = ok;
+  x[0].first = state0;
+  x[0].o = part ? (void*)part : dq;
+  x[0].s_carry = d->scale;
+  x[0].s_inject = 1.f;
+  x[0].off = 1;
+  x[1].q = ov;
+  x[1].k = og;
+  x[1].v = oq;
+  x[1].first = dstate;
+  x[1].o = part ? (void*)((char*)part + la_part_bytes(d, 1) / 2) : dk;
+  x[1].s_carry = 1.f;
+  x[1].s_inject = d->scale;
+  x[1].reverse = true;
+  for (const LaWalk& y : x)
+    if ((e = la_walk(y, bf16, true, scratch, s)) != cudaSuccess) return cuda_refuse(e, who);
+  for (int i = 0; part && i < 2; ++i) {
+    e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk, bf16,
+                     (const float*)x[i].o, i ? dk : dq, s);
+    if (e != cudaSuccess) return cuda_refuse(e, who);
+  }
+  return SSD_OK;
 }
 
 int ssd_linattn_step(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,

@@ -40,7 +40,9 @@ struct LaWalk {
 
 // scratch: la_scratch_floats() floats
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16);
-cudaError_t la_walk(const LaWalk& w, bool bf16, float* scratch, cudaStream_t s);
+// `beside`: the walk needs nothing of the kernel launched before it, which is
+// another walk, and may run beside it.
+cudaError_t la_walk(const LaWalk& w, bool bf16, bool beside, float* scratch, cudaStream_t s);
 // Segments of a row that is shared out over CTAs, `slots` of which run at once.
 int la_segments(long long rows, long long chunks, long long slots);
 // the states before each segment from the segments' own states (in place)
@@ -56,7 +58,7 @@ struct LaSegments {
 cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s);
 // the bf16 walk on tensor cores (ssd_linattn_tc.cu)
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv);
-cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s);
+cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_t s);
 // reads and clears the kernels' device error word (a wait gave up)
 cudaError_t la_read_and_clear_error(unsigned int* out);
 // out[b][t][g][:] = sum over the group's heads of part[b][t][h][:], in head order

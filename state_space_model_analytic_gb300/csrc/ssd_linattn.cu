@@ -444,8 +444,8 @@ size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16) {
   return n > 1 ? (size_t)n * B * H * dk * dv : 0;
 }
 
-cudaError_t la_walk(const LaWalk& w, bool bf16, float* scratch, cudaStream_t s) {
-  if (bf16) return la_walk_tc(w, scratch, s);
+cudaError_t la_walk(const LaWalk& w, bool bf16, bool beside, float* scratch, cudaStream_t s) {
+  if (bf16) return la_walk_tc(w, beside, scratch, s);
   SimtWalk a;
   a.w = w;
   const int nc = (w.T + kC - 1) / kC;

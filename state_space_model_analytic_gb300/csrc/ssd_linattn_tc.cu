@@ -58,6 +58,7 @@ struct Maps {
   CUtensorMap q, k, v, o;
 };
 
+// What of a walk a kernel needs.
 struct TcWalk {
   int B, T, H, dk, dv;
   int qs, ks, vs;  // heads that share an operand's head
@@ -70,6 +71,7 @@ struct TcWalk {
   void* o;
   float s_intra, s_carry, s_inject;
   int off, reverse;
+  int beside;  // launched beside the kernel before it, whose end it waits for last
 };
 
 // ---- PTX that only this file uses ----------------------------------------------
@@ -251,6 +253,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   const int vblocks = (p.dv + kV - 1) / kV;
   const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kV;
   const int b = blockIdx.y, seg = blockIdx.z;
+  grid_dep_launch();  // a kernel that needs nothing of this one may start beside it
   const float la = p.log_decay[h];
   int len = p.T;
   if (p.lens) len = __shfl_sync(0xffffffffu, min(max(p.lens[b], 0), p.T), 0);
@@ -741,6 +744,8 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     __syncwarp();
     tmem_dealloc(tm, 512);
   }
+  // what follows on the stream has to find the kernel before this one finished too
+  if (p.beside && tid == 0) grid_dep_wait();
 }
 
 // ---- host --------------------------------------------------------------------------
@@ -784,13 +789,21 @@ template <int DK, bool kStates, bool kF32>
 cudaError_t launch(const Maps& m, const TcWalk& p, cudaStream_t s) {
   constexpr size_t smem = Geom<DK, kStates>::smem;
   static_assert(smem + sizeof(Bars) + 1024 <= 232448, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(k_la_walk_tc<DK, kStates, kF32>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kernel = k_la_walk_tc<DK, kStates, kF32>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(kStates ? "linattn_states" : p.reverse ? "linattn_walk_back" : "linattn_walk", s);
-  const int vblocks = (p.dv + kV - 1) / kV;
-  k_la_walk_tc<DK, kStates, kF32><<<dim3(p.H * vblocks, p.B, p.nseg), kThreads, smem, s>>>(m, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.H * ((p.dv + kV - 1) / kV), p.B, p.nseg);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, m, p);
 }
 
 template <bool kStates, bool kF32>
@@ -811,7 +824,7 @@ size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv) {
   return n > 1 ? (size_t)n * B * H * dk * dv : 0;
 }
 
-cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s) {
+cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_t s) {
   Maps m;
   if (!map_4d(&m.q, w.q.p, false, w.dk, w.H / w.q.share, w.T, w.B, w.q.step, w.q.batch) ||
       !map_4d(&m.k, w.k.p, false, w.dk, w.H / w.k.share, w.T, w.B, w.k.step, w.k.batch) ||
@@ -854,6 +867,8 @@ cudaError_t la_walk_tc(const LaWalk& w, float* scratch, cudaStream_t s) {
     p.first = scratch;
     p.first_swapped = 0;
     p.last = nullptr;
+  } else {
+    p.beside = beside;
   }
   return w.o_f32 ? launch_d<false, true>(m, p, s) : launch_d<false, false>(m, p, s);
 }

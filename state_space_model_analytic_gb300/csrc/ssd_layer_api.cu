@@ -101,9 +101,24 @@ size_t la_scratch_bytes(const ssd_linattn_dims* d) {
                                                  (int)d->dk, (int)d->dv, d->dtype == SSD_BF16));
 }
 
+// The bf16 gradients of q and k that are shared by several heads are summed over
+// the heads in one kernel, from the states before every chunk.  With one head a
+// group a CTA of that kernel would have one head's work (__RULE__).
+bool la_sums_heads(const ssd_linattn_dims* d) {
+  return d->dtype == SSD_BF16 && d->nheads > d->ngroups;
+}
+
+// One state history.
+size_t la_hist_bytes(const ssd_linattn_dims* d) {
+  return up256((size_t)128 * la_tc_hist_rows((int)d->batch, (int)d->nheads, (int)d->seqlen,
+                                             (int)d->dk, (int)d->dv));
+}
+
+// What the backward keeps between its kernels, beside the walks' scratch.
 size_t la_part_bytes(const ssd_linattn_dims* d, int which) {
   if (which == 0 || d->nheads == d->ngroups) return 0;
-  // dq's and dk's
+  if (la_sums_heads(d)) return 2 * la_hist_bytes(d);
+  // dq's and dk's parts of every head
   return 2 * up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
 }
 
@@ -262,8 +277,29 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   w.s_intra = w.s_inject = d->scale;
   w.s_carry = 1.f;
   w.reverse = true;
+  const bool sums = la_sums_heads(d);
+  char* hist = (char*)part;
+  if (sums) w.hist = hist + la_hist_bytes(d);
   cudaError_t e = la_walk(w, bf16, false, scratch, s);
   if (e != cudaSuccess) return cuda_refuse(e, who);
+  if (sums) {
+    // the forward's states, then dq and dk
+    LaWalk f = la_base(d, log_decay, lens);
+    f.dk = (int)d->dk;
+    f.dv = (int)d->dv;
+    f.q = oq;  // (not read)
+    f.k = ok;
+    f.v = ov;
+    f.first = state0;
+    f.s_inject = 1.f;
+    f.off = 1;
+    f.hist = hist;
+    if ((e = la_walk(f, bf16, true, scratch, s)) != cudaSuccess) return cuda_refuse(e, who);
+    const LaGrads x = {w.B, w.T, w.H, w.dk, w.dv, oq, ok, ov, og, log_decay, lens, hist, w.hist,
+                       dq, dk, d->scale};
+    e = la_grads_tc(x, s);
+    return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+  }
   // dq: forward over (do, v, k), from the transposed state; dk: backwards over
   // (v, do, q), from the transposed gradient of the state
   LaWalk x[2] = {la_base(d, log_decay, lens), la_base(d, log_decay, lens)};

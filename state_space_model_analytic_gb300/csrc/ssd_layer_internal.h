@@ -36,6 +36,8 @@ struct LaWalk {
   float s_intra, s_carry, s_inject;
   int off;
   bool reverse;
+  void* hist;             // bf16 walks: the states before every chunk (la_tc_hist_rows rows of
+                          // 64), nullable; with it o may be NULL (the states alone)
 };
 
 // scratch: la_scratch_floats() floats
@@ -59,6 +61,19 @@ cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s);
 // the bf16 walk on tensor cores (ssd_linattn_tc.cu)
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv);
 cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_t s);
+// dq and dk of shared q and k from the states before every chunk, forward and
+// backward (bf16)
+struct LaGrads {
+  int B, T, H, dk, dv;
+  LaOperand q, k, v, dout;
+  const float* log_decay;
+  const int* lens;
+  const void *hist_s, *hist_g;
+  void *dq, *dk_out;
+  float scale;
+};
+long long la_tc_hist_rows(int B, int H, int T, int dk, int dv);
+cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s);
 // reads and clears the kernels' device error word (a wait gave up)
 cudaError_t la_read_and_clear_error(unsigned int* out);
 // out[b][t][g][:] = sum over the group's heads of part[b][t][h][:], in head order

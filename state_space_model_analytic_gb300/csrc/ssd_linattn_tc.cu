@@ -55,7 +55,7 @@ constexpr uint64_t kWaitNs = 1000000000ull;  // at the end, for what is still in
 __device__ unsigned int g_la_error;
 
 struct Maps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v, o, hist;
 };
 
 // What of a walk a kernel needs.
@@ -71,6 +71,7 @@ struct TcWalk {
   void* o;
   float s_intra, s_carry, s_inject;
   int off, reverse;
+  int hist;    // X before every chunk goes to maps.hist (see Hist)
   int beside;  // launched beside the kernel before it, whose end it waits for last
 };
 
@@ -83,6 +84,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0,
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(mbar))
       : "memory");
+}
+// (64 columns, as many rows as the map's box has)
+__device__ __forceinline__ void tma_store_rows(const void* tmap, const void* src, long long row) {
+  tma_store_2d(tmap, src, 0, (int)row);
 }
 __device__ __forceinline__ void tma_store_4d(const void* tmap, const void* src, int c0, int c1,
                                              int c2, int c3) {
@@ -148,6 +153,11 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -182,11 +192,18 @@ struct Geom {
   static constexpr int kVo = kKo + NS * QT;
   static constexpr int kWo = kVo + NS * VT;
   static constexpr int kXo = kWo + NW * 3 * WP;
-  static constexpr int kSo = kXo + (kStates ? 0 : DK * kV * 2);
+  static constexpr int kSo = kXo + DK * kV * 2;
   static constexpr int kDo = kSo + NB * 16384;          // kDiagRow floats a row, 32 rows
   static constexpr int kBytes = kDo + (kStates ? 0 : 32 * kDiagRow * 4);
   static constexpr size_t smem = kBytes + 1024;
 };
+
+// States before every chunk, bf16: [B][chunks][H][blocks of 64 columns of v][DK]
+// rows of 64 (DK: dk rounded up to 64 or 128).
+__host__ __device__ inline long long hist_row(int B, int nc, int H, int vblocks, int DK, int b, int c,
+                                              int h, int vb) {
+  return ((((long long)b * nc + c) * H + h) * vblocks + vb) * DK;
+}
 
 // TMEM columns
 constexpr int cS = 0, cP = 128, cO = 192, cC = 256, cU = 320;
@@ -204,22 +221,23 @@ struct Bars {
 // bound is in SM clocks (about a second and a half): reading the nanosecond
 // timer takes about a microsecond, which every wait that is not over at once
 // would pay.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Bars* B) {
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const long long t0 = clock64();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (B->abort) return false;
+    if (*abort) return false;
     if (clock64() - t0 > kWaitClocks) {
-      B->abort = 1;
+      *abort = 1;
       atomicOr(&g_la_error, 1u);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* B) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, B);
+template <typename B>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, B* bars) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, &bars->abort);
 }
 
 __device__ __forceinline__ void unpack8(const uint4& q, float* f) {
@@ -266,6 +284,9 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   auto ragged = [&](int c) { return valid(c) < kQ && len < p.T; };
   auto all_wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity, B)) != 0;
+  };
+  auto history = [&](int it) {  // row of the state before chunk `it` of the walk
+    return hist_row(p.B, (p.T + kQ - 1) / kQ, p.H, vblocks, DK, b, chunk(it), h, v0 / kV);
   };
   // w o V of pieces [first, end) of chunk `it`, by 256 threads (t): a row of the
   // piece and one of its 16-byte chunks each
@@ -457,12 +478,20 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       const int s = it % NS;
       const uint32_t full = (it / NS) & 1, ph = it & 1;
       if (it > 0 && !all_wait(&B->ofree, ph ^ 1)) break;
-      if (!all_wait(&B->x, ph) || !all_wait(&B->fullQ[s], full)) break;
+      if (!all_wait(&B->x, ph)) break;
+      if (p.hist && lead) {
+        tma_store_rows(&maps.hist, sm + G::kXo, history(it));
+        bulk_commit();
+      }
+      __syncwarp();
+      if (!all_wait(&B->fullQ[s], full)) break;
       fence_after_sync();
       const uint64_t dQ = dQ0 + s * (G::QT >> 4);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk)
         mma_ss(lead, tm + cC, dQ + ((kk >> 2) * 1024 + (kk & 3) * 2), dX + 128 * kk, id_x, kk > 0);
+      if (p.hist && lead) bulk_wait_read0();
+      __syncwarp();
       commit_if(lead, &B->xfree);
       commit_if(lead, &B->emptyQ[s]);
       if (!all_wait(&B->p, ph) || !all_wait(&B->fullV[s], full)) break;
@@ -474,6 +503,19 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       commit_if(lead, &B->o);
       commit_if(lead, &B->emptyV[s]);
     }
+    if (kStates && p.hist)  // the states of a states walk, which forms no Oc
+#pragma unroll 1
+      for (int it = 0; it < nit; ++it) {
+        if (!all_wait(&B->x, it & 1)) break;
+        if (lead) {
+          tma_store_rows(&maps.hist, sm + G::kXo, history(it));
+          bulk_commit();
+          bulk_wait_read0();
+          mbar_arrive(&B->xfree);
+        }
+        __syncwarp();
+      }
+    if (p.hist && lead) bulk_wait0();
     commit_if(lead, &B->drain[2]);
     mbar_wait(&B->drain[2], 0, kWaitNs);
     __syncwarp();
@@ -666,7 +708,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     for (int i = 0; i < 32; ++i) X[i] = 0.f;
     const size_t sbase = (((size_t)seg * p.B + b) * p.H + h) * p.dk * p.dv;
     const int vx = v0 + hf * 32;
-    if (!kStates && p.first && k < p.dk) {
+    if ((!kStates || p.hist) && p.first && k < p.dk) {
       const float* f = p.first + sbase;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -689,7 +731,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
       }
       // (in a states walk warps 0-7 form the first two pieces)
       if (!pieces(it, kStates ? 2 : 0, 4, t)) break;
-      if (!kStates) {  // X before this chunk, for its Oc
+      if (!kStates || p.hist) {  // X before this chunk, for its Oc and the history
         if (it > 0 && !all_wait(&B->xfree, (it - 1) & 1)) break;
         if (k < DK)
 #pragma unroll
@@ -748,6 +790,330 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   if (p.beside && tid == 0) grid_dep_wait();
 }
 
+
+// ---- gradients of shared operands -----------------------------------------------
+//
+// dq (and with exchanged roles dk) of a group is a sum over its heads; with the
+// states before every chunk at hand the chunks are independent, and the sum is
+// formed where the products accumulate:
+//   out = sum over heads  P_h C + (lead_h o A_h) X_h^T,   P_h = mask_h(A_h B_h^T)
+// with dq: A = do, B = v, C = k, X = the forward's states, mask i >= j;
+//      dk: A = v, B = do, C = q, X = the backward's states, mask i <= j
+// (the states' rows are k, so X_h^T has the width of C).  One CTA per (group,
+// row, chunk, gradient) goes over the heads and 64-column blocks of v; out stays
+// in TMEM until the last of them and is rounded once.  A walk of every head would
+// write its part in fp32 for a second kernel to add up: 2 x 537 MB written and
+// read for 2 x 8192 steps, 64 heads in 8 groups.
+//
+// Precision: P is rounded to bf16 once, X once (in the history); lead o A is
+// carried in two bf16 parts.
+//
+// Warps as in the walk: 0-7 P, 8-15 lead o A, one each loads, forms A B^T, and
+// accumulates.  Per item 48 KB are loaded and 1430 cycles of products issued.
+struct Grad {
+  int B, T, H, dk, dv, share, nc;  // heads of a group, chunks of a row
+  const float* log_decay;
+  const int* lens;
+  struct Role {
+    void* out;              // [B][T][H / share][dk]
+    float s_intra, s_carry;
+    int off, reverse;
+  } role[2];
+};
+struct GradMaps {
+  struct Role {
+    CUtensorMap a, b, c, x, out;
+  } role[2];
+};
+
+template <int DK>
+struct GradGeom {
+  static constexpr int VT = kV * 256, CT = DK * 256, XT = DK * 128;
+  static constexpr int kCo = 0;
+  static constexpr int kSto = kCo + CT;              // two stages of A, B, X
+  static constexpr int kStage = 2 * VT + XT;
+  static constexpr int kHo = kSto + 2 * kStage;      // lead o A: two parts, two buffers
+  static constexpr int kBytes = kHo + 4 * VT;
+  static constexpr size_t smem = kBytes + 1024;      // (out is staged in the first stage)
+};
+constexpr int gT = 0, gP = 256, gOut = 384;  // TMEM: two of 128 and of 64 columns, then out
+
+struct GradBars {
+  uint64_t full[2], empty[2], c, t[2], p[2], pfree[2], hat[2], hatfree[2], out, fix[2], drain[2];
+  uint32_t tmem;
+  volatile int abort;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1)
+k_la_grad_tc(const __grid_constant__ GradMaps maps, const __grid_constant__ Grad g) {
+  using G = GradGeom<DK>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t* sm = align1024(raw);
+  __shared__ GradBars bars;
+  GradBars* B = &bars;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int c = blockIdx.x % g.nc, row_group = blockIdx.x / g.nc;
+  const int grp = row_group % (g.H / g.share), b = row_group / (g.H / g.share);
+  const Grad::Role r = g.role[blockIdx.y];
+  const GradMaps::Role& m = maps.role[blockIdx.y];
+  const int vblocks = (g.dv + kV - 1) / kV, items = g.share * vblocks, t0 = c * kQ;
+  int len = g.T;
+  if (g.lens) len = __shfl_sync(0xffffffffu, min(max(g.lens[b], 0), g.T), 0);
+  const int n = min(kQ, len - t0);
+  if (n <= 0) {  // a chunk past the row's end
+    const int groups = g.H / g.share, row16 = g.dk / 8, rows = min(kQ, g.T - t0);
+    uint8_t* o = (uint8_t*)r.out + (((size_t)b * g.T + t0) * groups + grp) * g.dk * 2;
+#pragma unroll 1
+    for (int i = tid; i < rows * row16; i += kThreads)
+      *(uint4*)(o + (size_t)(i / row16) * groups * g.dk * 2 + (i % row16) * 16) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const bool ragged = n < kQ && len < g.T;
+  auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity, B)) != 0;
+  };
+  auto load = [&](int u) {
+    const int s = u & 1, h = grp * g.share + u / vblocks, vb = u % vblocks;
+    if (!wait(&B->empty[s], ((u >> 1) & 1) ^ 1, B)) return false;
+    uint8_t* d = sm + G::kSto + s * G::kStage;
+    mbar_expect_tx(&B->full[s], G::kStage);
+    tma_load_4d(d, &m.a, vb * kV, h, t0, b, &B->full[s]);
+    tma_load_4d(d + G::VT, &m.b, vb * kV, h, t0, b, &B->full[s]);
+    tma_load_2d(d + 2 * G::VT, &m.x, 0, (int)hist_row(g.B, g.nc, g.H, vblocks, DK, b, c, h, vb),
+                &B->full[s]);
+    return true;
+  };
+  if (tid == 19 * 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->empty[i], 1);
+      mbar_init(&B->t[i], 1);
+      mbar_init(&B->p[i], 8);
+      mbar_init(&B->pfree[i], 1);
+      mbar_init(&B->hat[i], 8);
+      mbar_init(&B->hatfree[i], 1);
+      mbar_init(&B->fix[i], 8);
+      mbar_init(&B->drain[i], 1);
+    }
+    mbar_init(&B->c, 1);
+    mbar_init(&B->out, 1);
+    B->abort = 0;
+    fence_mbar_init();
+    load(0);
+    if (items > 1) load(1);
+    mbar_expect_tx(&B->c, G::CT);
+    for (int x = 0; x < DK; x += 64) tma_load_4d(sm + G::kCo + x * 256, &m.c, x, grp, t0, b, &B->c);
+  }
+  if (warp == 16) {
+    tmem_alloc(&B->tmem, 512);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tm = __shfl_sync(0xffffffffu, B->tmem, 0);
+  const uint32_t lead = (tid & 31) == 0;
+
+  if (warp == 19) {
+    // ---- loads ----
+    if (lead) {
+      int u = min(items, 2);
+#pragma unroll 1
+      for (; u < items; ++u)
+        if (!load(u)) break;
+      if (B->abort) {  // no copy may be in flight when the CTA ends
+        const uint64_t lim = 50000000ull;
+        for (int j = max(u - 2, 0); j <= u && j < items; ++j) mbar_wait(&B->full[j & 1], (j >> 1) & 1, lim);
+        mbar_wait(&B->c, 0, lim);
+      }
+    }
+  } else if (warp == 17) {
+    // ---- T = A B^T ----
+    constexpr uint32_t id_t = idesc_bf16(128, 128, false, false);
+    const uint64_t dA0 = desc_sw128(smem_u32(sm + G::kSto), 16, 1024);
+#pragma unroll 1
+    for (int u = 0; u < items; ++u) {
+      const int s = u & 1;
+      const uint32_t ph = (u >> 1) & 1;
+      if (!all_wait(&B->full[s], ph)) break;
+      if (ragged && !all_wait(&B->fix[s], ph)) break;
+      // (T two items ago has been read: its P is there)
+      if (u > 1 && !all_wait(&B->p[s], ph ^ 1)) break;
+      fence_after_sync();
+      const uint64_t dA = dA0 + s * (G::kStage >> 4), dB = dA + (G::VT >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kV / 16; ++kk)
+        mma_ss(lead, tm + gT + s * 128, dA + 2 * kk, dB + 2 * kk, id_t, kk > 0);
+      commit_if(lead, &B->t[s]);
+    }
+    commit_if(lead, &B->drain[0]);
+    mbar_wait(&B->drain[0], 0, kWaitNs);
+    __syncwarp();
+  } else if (warp == 18) {
+    // ---- out += P C + (lead o A) X^T ----
+    constexpr uint32_t id_c = idesc_bf16(128, DK, false, true), id_x = idesc_bf16(128, DK, false, false);
+    const uint64_t dC = desc_sw128(smem_u32(sm + G::kCo), 16384, 1024);
+    const uint64_t dX0 = desc_sw128(smem_u32(sm + G::kSto + 2 * G::VT), 16, 1024);
+    const uint64_t dH0 = desc_sw128(smem_u32(sm + G::kHo), 16, 1024);
+    bool go = all_wait(&B->c, 0);
+#pragma unroll 1
+    for (int u = 0; go && u < items; ++u) {
+      const int s = u & 1;
+      const uint32_t ph = (u >> 1) & 1;
+      if (!all_wait(&B->hat[s], ph) || !all_wait(&B->full[s], ph)) break;
+      fence_after_sync();
+      const uint64_t dX = dX0 + s * (G::kStage >> 4), dH = dH0 + s * (2 * G::VT >> 4);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int kk = 0; kk < kV / 16; ++kk)
+          mma_ss(lead, tm + gOut, dH + part * (G::VT >> 4) + 2 * kk, dX + 2 * kk, id_x,
+                 u > 0 || part + kk > 0);
+      commit_if(lead, &B->hatfree[s]);
+      if (!all_wait(&B->p[s], ph)) break;
+      fence_after_sync();
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(lead, tm + gOut, tm + gP + s * 64 + 8 * kk, dC + 128 * kk, id_c, 1);
+      commit_if(lead, &B->pfree[s]);
+      commit_if(lead, &B->empty[s]);
+    }
+    commit_if(lead, &B->out);
+    commit_if(lead, &B->drain[1]);
+    mbar_wait(&B->drain[1], 0, kWaitNs);
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---- P: thread = row i and every second 32 columns; out at the end ----
+    const int row = tid & 127, il = row & 31, ib = warp & 3, hf = warp >> 2;
+    const uint32_t lane_base = (uint32_t)(ib * 32) << 16;
+    const float sign = r.reverse ? -1.f : 1.f;
+    // zeros into the rows past the row's end: of C once, of A and B of every item
+    auto clear = [&](uint8_t* tile, int tiles) {
+      if (row >= n)
+#pragma unroll 1
+        for (int x = 0; x < tiles * 4; ++x)
+          *(uint4*)(tile + (x >> 2) * 16384 + row * 128 + hf * 64 + (x & 3) * 16) = make_uint4(0, 0, 0, 0);
+    };
+    bool ok = true;
+    if (ragged) {
+      ok = all_wait(&B->c, 0);
+      if (ok) clear(sm + G::kCo, DK / 64);
+    }
+#pragma unroll 1
+    for (int u = 0; ok && u < items; ++u) {
+      const int s = u & 1;
+      const uint32_t ph = (u >> 1) & 1;
+      if (ragged) {
+        if (!(ok = all_wait(&B->full[s], ph))) break;
+        clear(sm + G::kSto + s * G::kStage, 2);
+        fence_async_smem();
+        warp_arrive(&B->fix[s]);
+      }
+      // a^{|i-j|} = 2^{(i-j) la2}, la2 of the mask's sign (a decay below 2^-1e30
+      // counts as that: its powers are 0 but for the power 0)
+      const float la = g.log_decay[grp * g.share + u / vblocks];
+      const float la2 = fmaxf(la * 1.4426950408889634f, -1e30f) * sign;
+      if (!(ok = all_wait(&B->t[s], ph))) break;
+      if (u > 1 && !(ok = all_wait(&B->pfree[s], ph ^ 1))) break;
+      fence_after_sync();
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        const int jb = 2 * x + hf, dist = r.reverse ? jb - ib : ib - jb;
+        uint32_t q[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) q[j] = 0;
+        if (dist >= 0) {
+          float v[32];
+          tmem_ld32(tm + gT + s * 128 + lane_base + jb * 32, v);
+          tmem_wait_ld();
+          float d0 = (float)(32 * (ib - jb) + il);
+          asm volatile("" : "+f"(d0));
+          // (on the diagonal a later step has no part in this row, whatever its
+          // product is)
+          const uint32_t in = dist > 0 ? 0xffffffffu : r.reverse ? 0xffffffffu << il : 0xffffffffu >> (31 - il);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float f = r.s_intra * ex2((d0 - (float)j) * la2);
+            v[j] = (in >> j) & 1 ? v[j] * f : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) q[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+        }
+        tmem_st16(tm + gP + s * 64 + lane_base + jb * 16, q);
+      }
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&B->p[s]);
+    }
+    ok = __all_sync(0xffffffffu, ok && wait(&B->out, 0, B)) && !B->abort;
+    fence_after_sync();
+    // out in 64-column tiles, staged where the first items were (all are done)
+#pragma unroll 1
+    for (int x = 0; x < DK / 64; ++x) {
+      uint8_t* st = sm + G::kSto + x * 16384;
+      if (ok)
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {
+          float v[16];
+          tmem_ld16(tm + gOut + lane_base + x * 64 + hf * 32 + z * 16, v);
+          tmem_wait_ld();
+          if (row >= n)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+          *(uint4*)(st + sw128(row, hf * 4 + z * 2)) = pack8(v);
+          *(uint4*)(st + sw128(row, hf * 4 + z * 2 + 1)) = pack8(v + 8);
+        }
+    }
+    fence_async_smem();
+    named_sync(1, 256);
+    if (tid == 0 && ok) {
+      for (int x = 0; x < g.dk; x += 64)
+        tma_store_4d(&m.out, sm + G::kSto + (x >> 6) * 16384, x, grp, t0, b);
+      bulk_commit();
+      bulk_wait0();
+    }
+  } else if (warp < 16) {
+    // ---- lead o A in two parts: thread = row of A and four of its eight chunks ----
+    const int t = tid - 256, row = t & 127, hf = t >> 7;
+#pragma unroll 1
+    for (int u = 0; u < items; ++u) {
+      const int s = u & 1;
+      const uint32_t ph = (u >> 1) & 1;
+      const float la = g.log_decay[grp * g.share + u / vblocks];
+      const float w = row < n ? r.s_carry * decay_pow(la, (float)((r.reverse ? n - 1 - row : row) + r.off)) : 0.f;
+      const float2 w2 = make_float2(w, w);
+      if (!all_wait(&B->full[s], ph)) break;
+      if (ragged && !all_wait(&B->fix[s], ph)) break;
+      if (u > 1 && !all_wait(&B->hatfree[s], ph ^ 1)) break;
+      const uint8_t* src = sm + G::kSto + s * G::kStage;
+      uint8_t* dst = sm + G::kHo + s * 2 * G::VT;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t at = sw128(row, hf * 4 + q);
+        float2 f[4], e[4];
+        unpack8(*(const uint4*)(src + at), (float*)f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
+        const uint4 hi = pack8((const float*)f);
+        unpack8(hi, (float*)e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = fma2(e[i], make_float2(-1.f, -1.f), f[i]);
+        *(uint4*)(dst + at) = hi;
+        *(uint4*)(dst + G::VT + at) = pack8((const float*)f);
+      }
+      fence_async_smem();
+      warp_arrive(&B->hat[s]);
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 16) {
+    __syncwarp();
+    tmem_dealloc(tm, 512);
+  }
+}
+
 // ---- host --------------------------------------------------------------------------
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -783,6 +1149,19 @@ bool map_4d(CUtensorMap* m, const void* base, bool f32, int D, int heads, int T,
             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// rows of 64 bf16 with {64, box_rows} boxes
+bool map_rows(CUtensorMap* m, const void* base, long long rows, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || rows > (1ll << 31) - 1) return false;
+  cuuint64_t dims[2] = {64, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DK, bool kStates, bool kF32>
@@ -824,13 +1203,59 @@ size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv) {
   return n > 1 ? (size_t)n * B * H * dk * dv : 0;
 }
 
+long long la_tc_hist_rows(int B, int H, int T, int dk, int dv) {
+  const int DK = dk <= 64 ? 64 : 128;
+  return hist_row(B, (T + kQ - 1) / kQ, H, (dv + kV - 1) / kV, DK, B, 0, 0, 0);
+}
+
+cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s) {
+  GradMaps m;
+  Grad g = {};
+  g.B = d.B;
+  g.T = d.T;
+  g.H = d.H;
+  g.dk = d.dk;
+  g.dv = d.dv;
+  g.share = d.q.share;
+  g.nc = (d.T + kQ - 1) / kQ;
+  g.log_decay = d.log_decay;
+  g.lens = d.lens;
+  g.role[0] = {d.dq, d.scale, d.scale, 1, 0};
+  g.role[1] = {d.dk_out, d.scale, 1.f, 0, 1};
+  const LaOperand* a[2] = {&d.dout, &d.v};
+  const LaOperand* b[2] = {&d.v, &d.dout};
+  const LaOperand* c[2] = {&d.k, &d.q};
+  const void* x[2] = {d.hist_s, d.hist_g};
+  const int G = d.H / g.share, DK = d.dk <= 64 ? 64 : 128;
+  const long long rows = la_tc_hist_rows(d.B, d.H, d.T, d.dk, d.dv);
+  for (int i = 0; i < 2; ++i) {
+    GradMaps::Role& r = m.role[i];
+    if (!map_4d(&r.a, a[i]->p, false, d.dv, d.H, d.T, d.B, a[i]->step, a[i]->batch) ||
+        !map_4d(&r.b, b[i]->p, false, d.dv, d.H, d.T, d.B, b[i]->step, b[i]->batch) ||
+        !map_4d(&r.c, c[i]->p, false, d.dk, G, d.T, d.B, c[i]->step, c[i]->batch) ||
+        !map_4d(&r.out, g.role[i].out, false, d.dk, G, d.T, d.B, (long long)G * d.dk,
+                (long long)d.T * G * d.dk) ||
+        !map_rows(&r.x, x[i], rows, DK))
+      return cudaErrorNotSupported;
+  }
+  auto go = [&](auto kernel, size_t smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    LaunchScope ls("linattn_grads", s);
+    kernel<<<dim3((unsigned)((long long)g.nc * d.B * G), 2), kThreads, smem, s>>>(m, g);
+    return cudaGetLastError();
+  };
+  static_assert(GradGeom<128>::smem + 2048 <= 232448, "shared memory of a CTA");
+  return DK == 64 ? go(k_la_grad_tc<64>, GradGeom<64>::smem) : go(k_la_grad_tc<128>, GradGeom<128>::smem);
+}
+
 cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_t s) {
   Maps m;
   if (!map_4d(&m.q, w.q.p, false, w.dk, w.H / w.q.share, w.T, w.B, w.q.step, w.q.batch) ||
       !map_4d(&m.k, w.k.p, false, w.dk, w.H / w.k.share, w.T, w.B, w.k.step, w.k.batch) ||
       !map_4d(&m.v, w.v.p, false, w.dv, w.H / w.v.share, w.T, w.B, w.v.step, w.v.batch) ||
-      !map_4d(&m.o, w.o, w.o_f32, w.dv, w.H, w.T, w.B, (long long)w.H * w.dv,
-              (long long)w.T * w.H * w.dv))
+      (w.o && !map_4d(&m.o, w.o, w.o_f32, w.dv, w.H, w.T, w.B, (long long)w.H * w.dv,
+                      (long long)w.T * w.H * w.dv)))
     return cudaErrorNotSupported;
   TcWalk p = {};
   p.B = w.B;
@@ -869,6 +1294,13 @@ cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_
     p.last = nullptr;
   } else {
     p.beside = beside;
+  }
+  if (w.hist) {
+    const int DK = w.dk <= 64 ? 64 : 128;
+    if (!map_rows(&m.hist, w.hist, la_tc_hist_rows(w.B, w.H, w.T, w.dk, w.dv), DK))
+      return cudaErrorNotSupported;
+    p.hist = 1;
+    if (!w.o) return launch_d<true, false>(m, p, s);  // the states alone
   }
   return w.o_f32 ? launch_d<false, true>(m, p, s) : launch_d<false, false>(m, p, s);
 }

@@ -310,7 +310,6 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
     y.dk = (int)d->dv;
     y.dv = (int)d->dk;
     y.first_swapped = true;
-    y.o_f32 = part != nullptr;
     y.s_intra = d->scale;
   }
   x[0].q = og;
@@ -332,8 +331,8 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   for (const LaWalk& y : x)
     if ((e = la_walk(y, bf16, true, scratch, s)) != cudaSuccess) return cuda_refuse(e, who);
   for (int i = 0; part && i < 2; ++i) {
-    e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk, bf16,
-                     (const float*)x[i].o, i ? dk : dq, s);
+    e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk,
+                     (const float*)x[i].o, (float*)(i ? dk : dq), s);
     if (e != cudaSuccess) return cuda_refuse(e, who);
   }
   return SSD_OK;

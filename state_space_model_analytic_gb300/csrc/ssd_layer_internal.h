@@ -32,7 +32,6 @@ struct LaWalk {
   bool first_swapped;
   const int* lens;        // [B], nullable
   void* o;                // [B][T][H][dv], dense
-  bool o_f32;             // o is fp32 whatever the operands' type
   float s_intra, s_carry, s_inject;
   int off;
   bool reverse;
@@ -76,9 +75,10 @@ long long la_tc_hist_rows(int B, int H, int T, int dk, int dv);
 cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s);
 // reads and clears the kernels' device error word (a wait gave up)
 cudaError_t la_read_and_clear_error(unsigned int* out);
-// out[b][t][g][:] = sum over the group's heads of part[b][t][h][:], in head order
-cudaError_t la_group_sum(long long rows, int G, int share, int D, bool bf16, const float* part,
-                         void* out, cudaStream_t s);
+// out[b][t][g][:] = sum over the group's heads of part[b][t][h][:], in head
+// order (fp32)
+cudaError_t la_group_sum(long long rows, int G, int share, int D, const float* part, float* out,
+                         cudaStream_t s);
 
 struct LaStep {
   int B, H, G, dk, dv;

@@ -278,17 +278,15 @@ cudaError_t walk_t(const SimtWalk& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// part [rows][G][share][D] fp32 -> out [rows][G][D]
-template <typename T>
+// part [rows][G][share][D] -> out [rows][G][D]
 __global__ void k_la_group_sum(long long n, int share, int D, const float* __restrict__ part,
-                               T* __restrict__ out) {
+                               float* __restrict__ out) {
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n;
        i += (long long)gridDim.x * blockDim.x) {
-    const long long rg = i / D;
-    const float* p = part + rg * share * D + i % D;
+    const float* p = part + i / D * share * D + i % D;
     float s = 0.f;
     for (int j = 0; j < share; ++j) s += p[(long long)j * D];
-    out[i] = from_f32<T>(s);
+    out[i] = s;
   }
 }
 
@@ -467,14 +465,12 @@ cudaError_t la_walk(const LaWalk& w, bool bf16, bool beside, float* scratch, cud
   return w.dk <= 64 ? walk_t<64, false>(a, s) : walk_t<128, false>(a, s);
 }
 
-cudaError_t la_group_sum(long long rows, int G, int share, int D, bool bf16, const float* part,
-                         void* out, cudaStream_t s) {
+cudaError_t la_group_sum(long long rows, int G, int share, int D, const float* part, float* out,
+                         cudaStream_t s) {
   const long long n = rows * G * D;
   const long long want = (n + 255) / 256;
-  const int grid = (int)(want < 8192 ? want : 8192);
   LaunchScope ls("linattn_group_sum", s);
-  if (bf16) k_la_group_sum<<<grid, 256, 0, s>>>(n, share, D, part, (__nv_bfloat16*)out);
-  else k_la_group_sum<<<grid, 256, 0, s>>>(n, share, D, part, (float*)out);
+  k_la_group_sum<<<(int)(want < 8192 ? want : 8192), 256, 0, s>>>(n, share, D, part, out);
   return cudaGetLastError();
 }
 

@@ -178,13 +178,12 @@ constexpr int kV = 64;      // columns of v of a CTA
 constexpr int kPiece = 32;  // steps of a piece of w o V
 constexpr int kDiagRow = 36;  // (16-byte pieces of 8 rows fall on all 32 banks)
 
-// NS: stages of the loads; NW: buffers of a piece's three parts; NB: 16 KB
-// buffers that o is staged in.  The sums stay below the 227 KB of a CTA.
+// NS: stages of the loads; NW: buffers of a piece's three parts.  The sums
+// stay below the 227 KB of a CTA.
 template <int DK, bool kStates>
 struct Geom {
   static constexpr int NS = kStates || DK == 64 ? 3 : 2;
-  static constexpr int NW = kStates ? 4 : 2;
-  static constexpr int NB = kStates ? 0 : DK == 64 ? 2 : 1;
+  static constexpr int NW = kStates || DK == 64 ? 4 : 2;
   static constexpr int QT = DK * 256, VT = kV * 256;  // bytes of 128 rows
   static constexpr int WP = kPiece * 128;              // one part of a piece
   static constexpr int kQo = 0;
@@ -193,8 +192,8 @@ struct Geom {
   static constexpr int kWo = kVo + NS * VT;
   static constexpr int kXo = kWo + NW * 3 * WP;
   static constexpr int kSo = kXo + DK * kV * 2;
-  static constexpr int kDo = kSo + NB * 16384;          // kDiagRow floats a row, 32 rows
-  static constexpr int kBytes = kDo + (kStates ? 0 : 32 * kDiagRow * 4);
+  static constexpr int kDo = kSo + (kStates ? 0 : 16384);  // (o is staged at kSo)
+  static constexpr int kBytes = kDo + (kStates ? 0 : 32 * kDiagRow * 4);  // kDiagRow floats a row
   static constexpr size_t smem = kBytes + 1024;
 };
 
@@ -254,9 +253,9 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     pack_bf16(f[6], f[7]));
 }
 
-// kStates: only the states (K, V, U, X), each segment from zero.  kF32: o is
-// fp32 (partial sums), else bf16.
-template <int DK, bool kStates, bool kF32>
+// kStates: only the states (K, V, U, X); each segment from zero, or with a
+// history to be written from the state before it.
+template <int DK, bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
 k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   using G = Geom<DK, kStates>;
@@ -573,7 +572,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
     bool ok = true;
 #pragma unroll 1
     for (int it = 0; it <= nit && !kStates && nit > 0; ++it) {
-      uint32_t y[kF32 ? 32 : 16];  // this thread's 32 columns of o, bf16 in pairs or fp32
+      uint32_t y[16];  // this thread's 32 columns of o, bf16 in pairs
       if (it > 0) {
         ok = __all_sync(0xffffffffu, ok && wait(&B->o, (it - 1) & 1, B));
         fence_after_sync();
@@ -591,17 +590,12 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               const float2 a = fma2(l2, make_float2(w[j], w[j + 1]), make_float2(u[j], u[j + 1]));
-              if (kF32) {
-                y[(kF32 ? 16 * z : 0) + j] = __float_as_uint(a.x);
-                y[(kF32 ? 16 * z : 0) + j + 1] = __float_as_uint(a.y);
-              } else {
-                y[8 * z + j / 2] = pack_bf16(a.x, a.y);
-              }
+              y[8 * z + j / 2] = pack_bf16(a.x, a.y);
             }
           }
           if (n < kQ && row >= n) {
 #pragma unroll
-            for (int j = 0; j < (kF32 ? 32 : 16); ++j) y[j] = 0;
+            for (int j = 0; j < 16; ++j) y[j] = 0;
           }
           fence_before_sync();
           warp_arrive(&B->ofree);
@@ -672,29 +666,20 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
         }
       }
       if (it == 0) continue;
-      // o, staged in 128-byte rows: 64 columns of bf16 (both halves of the threads),
-      // or 32 of fp32 (one half; one after the other where there is one buffer)
-#pragma unroll 1
-      for (int x = 0; x < (kF32 && G::NB == 1 ? 2 : 1); ++x) {
-        uint8_t* st = sm + G::kSo + (kF32 && G::NB == 2 ? hf : 0) * 16384;
-        if (tid == 0) bulk_wait_read0();
-        named_sync(1, 256);
-        if (ok && (!kF32 || G::NB == 2 || x == hf)) {
+      // o, staged as 128 rows of 64 columns (both halves of the threads)
+      uint8_t* st = sm + G::kSo;
+      if (tid == 0) bulk_wait_read0();
+      named_sync(1, 256);
+      if (ok)
 #pragma unroll
-          for (int j = 0; j < (kF32 ? 8 : 4); ++j)
-            *(uint4*)(st + sw128(row, (kF32 ? 0 : hf * 4) + j)) =
-                make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-        }
-        fence_async_smem();
-        named_sync(1, 256);
-        if (tid == 0 && ok) {
-          // (a box that starts past the width would start out of range)
-          const int x0 = v0 + x * 32, t0 = chunk(it - 1) * kQ;
-          if (x0 < p.dv) tma_store_4d(&maps.o, sm + G::kSo, x0, h, t0, b);
-          if (kF32 && G::NB == 2 && x0 + 32 < p.dv)
-            tma_store_4d(&maps.o, sm + G::kSo + 16384, x0 + 32, h, t0, b);
-          bulk_commit();
-        }
+        for (int j = 0; j < 4; ++j)
+          *(uint4*)(st + sw128(row, hf * 4 + j)) =
+              make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+      fence_async_smem();
+      named_sync(1, 256);
+      if (tid == 0 && ok) {
+        tma_store_4d(&maps.o, st, v0, h, chunk(it - 1) * kQ, b);
+        bulk_commit();
       }
     }
     if (!kStates && tid == 0) bulk_wait0();
@@ -773,12 +758,12 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   if (!kStates) {
     // whole chunks of the segment past the row's end
     const int z0 = max(c1, c0) * kQ, z1 = min((c0 + p.seg_chunks) * kQ, p.T);
-    const int esz = kF32 ? 4 : 2, at = (tid & 31) * 16, row = min(kV, p.dv - v0) * esz;
-    uint8_t* o = (uint8_t*)p.o + (((size_t)b * p.T * p.H + h) * p.dv + v0) * esz + at;
+    const int at = (tid & 31) * 16, row = min(kV, p.dv - v0) * 2;
+    uint8_t* o = (uint8_t*)p.o + (((size_t)b * p.T * p.H + h) * p.dv + v0) * 2 + at;
     if (at < row)
 #pragma unroll 1
       for (int t = z0 + warp; t < z1; t += kThreads / 32)
-        *(uint4*)(o + (size_t)t * p.H * p.dv * esz) = make_uint4(0, 0, 0, 0);
+        *(uint4*)(o + (size_t)t * p.H * p.dv * 2) = make_uint4(0, 0, 0, 0);
   }
   fence_before_sync();
   __syncthreads();
@@ -1136,17 +1121,17 @@ EncodeTiledFn encode_fn() {
 }
 
 // [B][T][heads][D] with {128 bytes of D, one head, 128 steps, one row} boxes.
-bool map_4d(CUtensorMap* m, const void* base, bool f32, int D, int heads, int T, int B,
+bool map_4d(CUtensorMap* m, const void* base, int D, int heads, int T, int B,
             long long step, long long batch) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t e = f32 ? 4 : 2;
+  const cuuint64_t e = 2;
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
   cuuint64_t strides[3] = {D * e, (cuuint64_t)step * e, (cuuint64_t)batch * e};
-  cuuint32_t box[4] = {f32 ? 32u : 64u, 1, kQ, 1};
+  cuuint32_t box[4] = {64, 1, kQ, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1164,11 +1149,11 @@ bool map_rows(CUtensorMap* m, const void* base, long long rows, int box_rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DK, bool kStates, bool kF32>
+template <int DK, bool kStates>
 cudaError_t launch(const Maps& m, const TcWalk& p, cudaStream_t s) {
   constexpr size_t smem = Geom<DK, kStates>::smem;
   static_assert(smem + sizeof(Bars) + 1024 <= 232448, "shared memory of a CTA");
-  auto kernel = k_la_walk_tc<DK, kStates, kF32>;
+  auto kernel = k_la_walk_tc<DK, kStates>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(kStates ? "linattn_states" : p.reverse ? "linattn_walk_back" : "linattn_walk", s);
@@ -1185,9 +1170,9 @@ cudaError_t launch(const Maps& m, const TcWalk& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, m, p);
 }
 
-template <bool kStates, bool kF32>
+template <bool kStates>
 cudaError_t launch_d(const Maps& m, const TcWalk& p, cudaStream_t s) {
-  return p.dk <= 64 ? launch<64, kStates, kF32>(m, p, s) : launch<128, kStates, kF32>(m, p, s);
+  return p.dk <= 64 ? launch<64, kStates>(m, p, s) : launch<128, kStates>(m, p, s);
 }
 
 }  // namespace
@@ -1230,10 +1215,10 @@ cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s) {
   const long long rows = la_tc_hist_rows(d.B, d.H, d.T, d.dk, d.dv);
   for (int i = 0; i < 2; ++i) {
     GradMaps::Role& r = m.role[i];
-    if (!map_4d(&r.a, a[i]->p, false, d.dv, d.H, d.T, d.B, a[i]->step, a[i]->batch) ||
-        !map_4d(&r.b, b[i]->p, false, d.dv, d.H, d.T, d.B, b[i]->step, b[i]->batch) ||
-        !map_4d(&r.c, c[i]->p, false, d.dk, G, d.T, d.B, c[i]->step, c[i]->batch) ||
-        !map_4d(&r.out, g.role[i].out, false, d.dk, G, d.T, d.B, (long long)G * d.dk,
+    if (!map_4d(&r.a, a[i]->p, d.dv, d.H, d.T, d.B, a[i]->step, a[i]->batch) ||
+        !map_4d(&r.b, b[i]->p, d.dv, d.H, d.T, d.B, b[i]->step, b[i]->batch) ||
+        !map_4d(&r.c, c[i]->p, d.dk, G, d.T, d.B, c[i]->step, c[i]->batch) ||
+        !map_4d(&r.out, g.role[i].out, d.dk, G, d.T, d.B, (long long)G * d.dk,
                 (long long)d.T * G * d.dk) ||
         !map_rows(&r.x, x[i], rows, DK))
       return cudaErrorNotSupported;
@@ -1251,10 +1236,10 @@ cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s) {
 
 cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_t s) {
   Maps m;
-  if (!map_4d(&m.q, w.q.p, false, w.dk, w.H / w.q.share, w.T, w.B, w.q.step, w.q.batch) ||
-      !map_4d(&m.k, w.k.p, false, w.dk, w.H / w.k.share, w.T, w.B, w.k.step, w.k.batch) ||
-      !map_4d(&m.v, w.v.p, false, w.dv, w.H / w.v.share, w.T, w.B, w.v.step, w.v.batch) ||
-      (w.o && !map_4d(&m.o, w.o, w.o_f32, w.dv, w.H, w.T, w.B, (long long)w.H * w.dv,
+  if (!map_4d(&m.q, w.q.p, w.dk, w.H / w.q.share, w.T, w.B, w.q.step, w.q.batch) ||
+      !map_4d(&m.k, w.k.p, w.dk, w.H / w.k.share, w.T, w.B, w.k.step, w.k.batch) ||
+      !map_4d(&m.v, w.v.p, w.dv, w.H / w.v.share, w.T, w.B, w.v.step, w.v.batch) ||
+      (w.o && !map_4d(&m.o, w.o, w.dv, w.H, w.T, w.B, (long long)w.H * w.dv,
                       (long long)w.T * w.H * w.dv)))
     return cudaErrorNotSupported;
   TcWalk p = {};
@@ -1284,7 +1269,7 @@ cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_
   p.first_swapped = w.first_swapped;
   if (n > 1) {
     p.last = scratch;
-    cudaError_t e = launch_d<true, false>(m, p, s);
+    cudaError_t e = launch_d<true>(m, p, s);
     if (e != cudaSuccess) return e;
     const LaSegments g = {w.B, w.H, w.T, w.dk, w.dv, n, p.seg_chunks * kQ, w.log_decay, w.lens,
                           scratch, w.first, w.last, w.first_swapped, w.reverse};
@@ -1300,9 +1285,9 @@ cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_
     if (!map_rows(&m.hist, w.hist, la_tc_hist_rows(w.B, w.H, w.T, w.dk, w.dv), DK))
       return cudaErrorNotSupported;
     p.hist = 1;
-    if (!w.o) return launch_d<true, false>(m, p, s);  // the states alone
+    if (!w.o) return launch_d<true>(m, p, s);  // the states alone
   }
-  return w.o_f32 ? launch_d<false, true>(m, p, s) : launch_d<false, false>(m, p, s);
+  return launch_d<false>(m, p, s);
 }
 
 cudaError_t la_read_and_clear_error(unsigned int* out) {

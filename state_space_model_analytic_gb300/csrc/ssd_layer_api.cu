@@ -101,16 +101,6 @@ size_t la_scratch_bytes(const ssd_linattn_dims* d) {
                                                  (int)d->dk, (int)d->dv, d->dtype == SSD_BF16));
 }
 
-// The bf16 gradients of q and k that are shared by several heads are summed over
-// the heads in one kernel, from the states before every chunk: 171 us against 390
-// with fp32 parts of every head and a sum (4 x 2048 steps, 32 heads in 16
-// groups), 488 against 876 (2 x 8192, 64 heads in 8).  With one head a group a
-// CTA of that kernel has too little to do: 223 us against 184 for three walks
-// (4 x 2048, 32 heads).
-bool la_sums_heads(const ssd_linattn_dims* d) {
-  return d->dtype == SSD_BF16 && d->nheads > d->ngroups;
-}
-
 // One state history.
 size_t la_hist_bytes(const ssd_linattn_dims* d) {
   return up256((size_t)128 * la_tc_hist_rows((int)d->batch, (int)d->nheads, (int)d->seqlen,
@@ -119,10 +109,11 @@ size_t la_hist_bytes(const ssd_linattn_dims* d) {
 
 // What the backward keeps between its kernels, beside the walks' scratch.
 size_t la_part_bytes(const ssd_linattn_dims* d, int which) {
-  if (which == 0 || d->nheads == d->ngroups) return 0;
-  if (la_sums_heads(d)) return 2 * la_hist_bytes(d);
-  // dq's and dk's parts of every head
-  return 2 * up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
+  if (which == 0) return 0;
+  if (d->dtype == SSD_BF16) return 2 * la_hist_bytes(d);  // the states before every chunk
+  if (d->nheads == d->ngroups) return 0;
+  // dq's, then dk's part of every head
+  return up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
 }
 
 int workspace_check(const char* who, const void* workspace, size_t bytes, size_t need) {
@@ -266,7 +257,7 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   const int share = (int)(d->nheads / d->ngroups);
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   float* scratch = (float*)workspace;
-  float* part = share > 1 ? (float*)((char*)workspace + la_scratch_bytes(d)) : nullptr;
+  char* rest = (char*)workspace + la_scratch_bytes(d);
   // dv, dstate0: backwards over (k, q, do)
   LaWalk w = la_base(d, log_decay, lens);
   w.dk = (int)d->dk;
@@ -280,13 +271,10 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   w.s_intra = w.s_inject = d->scale;
   w.s_carry = 1.f;
   w.reverse = true;
-  const bool sums = la_sums_heads(d);
-  char* hist = (char*)part;
-  if (sums) w.hist = hist + la_hist_bytes(d);
-  cudaError_t e = la_walk(w, bf16, false, scratch, s);
-  if (e != cudaSuccess) return cuda_refuse(e, who);
-  if (sums) {
-    // the forward's states, then dq and dk
+  if (bf16) {
+    // with the states before every chunk, backward and forward, dq and dk are
+    // sums over chunks and a group's heads that need no walk
+    w.hist = rest + la_hist_bytes(d);
     LaWalk f = la_base(d, log_decay, lens);
     f.dk = (int)d->dk;
     f.dv = (int)d->dv;
@@ -296,43 +284,38 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
     f.first = state0;
     f.s_inject = 1.f;
     f.off = 1;
-    f.hist = hist;
-    if ((e = la_walk(f, bf16, true, scratch, s)) != cudaSuccess) return cuda_refuse(e, who);
-    const LaGrads x = {w.B, w.T, w.H, w.dk, w.dv, oq, ok, ov, og, log_decay, lens, hist, w.hist,
+    f.hist = rest;
+    const LaGrads x = {w.B, w.T, w.H, w.dk, w.dv, oq, ok, ov, og, log_decay, lens, f.hist, w.hist,
                        dq, dk, d->scale};
-    e = la_grads_tc(x, s);
+    cudaError_t e = la_walk(w, true, false, scratch, s);
+    if (e == cudaSuccess) e = la_walk(f, true, true, scratch, s);
+    if (e == cudaSuccess) e = la_grads_tc(x, s);
     return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
   }
+  cudaError_t e = la_walk(w, false, false, scratch, s);
+  if (e != cudaSuccess) return cuda_refuse(e, who);
   // dq: forward over (do, v, k), from the transposed state; dk: backwards over
   // (v, do, q), from the transposed gradient of the state
-  LaWalk x[2] = {la_base(d, log_decay, lens), la_base(d, log_decay, lens)};
-  for (LaWalk& y : x) {
+  for (int i = 0; i < 2; ++i) {
+    LaWalk y = la_base(d, log_decay, lens);
     y.dk = (int)d->dv;
     y.dv = (int)d->dk;
+    y.q = i ? ov : og;
+    y.k = i ? og : ov;
+    y.v = i ? oq : ok;
+    y.first = i ? dstate : state0;
     y.first_swapped = true;
     y.s_intra = d->scale;
-  }
-  x[0].q = og;
-  x[0].k = ov;
-  x[0].v = ok;
-  x[0].first = state0;
-  x[0].o = part ? (void*)part : dq;
-  x[0].s_carry = d->scale;
-  x[0].s_inject = 1.f;
-  x[0].off = 1;
-  x[1].q = ov;
-  x[1].k = og;
-  x[1].v = oq;
-  x[1].first = dstate;
-  x[1].o = part ? (void*)((char*)part + la_part_bytes(d, 1) / 2) : dk;
-  x[1].s_carry = 1.f;
-  x[1].s_inject = d->scale;
-  x[1].reverse = true;
-  for (const LaWalk& y : x)
-    if ((e = la_walk(y, bf16, true, scratch, s)) != cudaSuccess) return cuda_refuse(e, who);
-  for (int i = 0; part && i < 2; ++i) {
-    e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk,
-                     (const float*)x[i].o, (float*)(i ? dk : dq), s);
+    y.s_carry = i ? 1.f : d->scale;
+    y.s_inject = i ? d->scale : 1.f;
+    y.off = i ? 0 : 1;
+    y.reverse = i == 1;
+    float* out = (float*)(i ? dk : dq);
+    y.o = share > 1 ? (float*)rest : out;
+    if ((e = la_walk(y, false, false, scratch, s)) != cudaSuccess) return cuda_refuse(e, who);
+    if (share == 1) continue;
+    e = la_group_sum(d->batch * d->seqlen, (int)d->ngroups, share, (int)d->dk, (const float*)y.o,
+                     out, s);
     if (e != cudaSuccess) return cuda_refuse(e, who);
   }
   return SSD_OK;

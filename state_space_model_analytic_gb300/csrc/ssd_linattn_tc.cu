@@ -66,7 +66,6 @@ struct TcWalk {
   const float* log_decay;
   const float* first;  // state before the row (nseg == 1) or before each segment
   float* last;         // state after it; after each segment alone in a states walk
-  int first_swapped;
   const int* lens;
   void* o;
   float s_intra, s_carry, s_inject;
@@ -698,7 +697,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (vx + i < p.dv)
-          X[i] = f[p.first_swapped ? (size_t)k * p.dv + vx + i : (size_t)(vx + i) * p.dk + k];
+          X[i] = f[(size_t)(vx + i) * p.dk + k];
     }
 #pragma unroll 1
     for (int it = 0; it < nit; ++it) {
@@ -752,7 +751,7 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (vx + i < p.dv)
-          l[!kStates && p.first_swapped ? (size_t)k * p.dv + vx + i : (size_t)(vx + i) * p.dk + k] = X[i];
+          l[(size_t)(vx + i) * p.dk + k] = X[i];
     }
   }
   if (!kStates) {
@@ -784,17 +783,20 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 //   out = sum over heads  P_h C + (lead_h o A_h) X_h^T,   P_h = mask_h(A_h B_h^T)
 // with dq: A = do, B = v, C = k, X = the forward's states, mask i >= j;
 //      dk: A = v, B = do, C = q, X = the backward's states, mask i <= j
-// (the states' rows are k, so X_h^T has the width of C).  One CTA per (group,
-// row, chunk, gradient) goes over the heads and 64-column blocks of v; out stays
-// in TMEM until the last of them and is rounded once.  A walk of every head would
-// write its part in fp32 for a second kernel to add up: 2 x 537 MB written and
-// read for 2 x 8192 steps, 64 heads in 8 groups.
+// (the states' rows are k, so X_h^T has the width of C).  A unit is a (group,
+// row, chunk, gradient); its items are the heads and 64-column blocks of v.  out
+// stays in TMEM until the last of them and is rounded once.  A walk of every head
+// would write its part in fp32 for a second kernel to add up: 2 x 537 MB written
+// and read for 2 x 8192 steps, 64 heads in 8 groups.
 //
 // Precision: P is rounded to bf16 once, X once (in the history); lead o A is
 // carried in two bf16 parts.
 //
-// Warps as in the walk: 0-7 P, 8-15 lead o A, one each loads, forms A B^T, and
-// accumulates.  Per item 48 KB are loaded and 1430 cycles of products issued.
+// One CTA an SM goes over units (the two gradients of a chunk are neighbours and
+// share v and do in L2).  Warps as in the walk: 0-7 turn T = A B^T into P, in
+// place, 8-15 form lead o A and write out of the unit before, one each loads,
+// forms T and accumulates; two stages of items, two of C and two of out keep them
+// apart.  Per item 48 KB are loaded and 1430 cycles of products issued.
 struct Grad {
   int B, T, H, dk, dv, share, nc;  // heads of a group, chunks of a row
   const float* log_decay;
@@ -814,17 +816,19 @@ struct GradMaps {
 template <int DK>
 struct GradGeom {
   static constexpr int VT = kV * 256, CT = DK * 256, XT = DK * 128;
-  static constexpr int kCo = 0;
-  static constexpr int kSto = kCo + CT;              // two stages of A, B, X
+  static constexpr int kCo = 0;                      // two stages of C
+  static constexpr int kSto = kCo + 2 * CT;          // two stages of A, B, X
   static constexpr int kStage = 2 * VT + XT;
-  static constexpr int kHo = kSto + 2 * kStage;      // lead o A: two parts, two buffers
-  static constexpr int kBytes = kHo + 4 * VT;
-  static constexpr size_t smem = kBytes + 1024;      // (out is staged in the first stage)
+  static constexpr int kHo = kSto + 2 * kStage;      // lead o A: two parts
+  static constexpr int kOo = kHo + 2 * VT;           // out is staged here
+  static constexpr int kBytes = kOo + CT;
+  static constexpr size_t smem = kBytes + 1024;
 };
-constexpr int gT = 0, gP = 256, gOut = 384;  // TMEM: two of 128 and of 64 columns, then out
+constexpr int gT = 0, gOut = 256;  // TMEM: two of 128 columns each
 
 struct GradBars {
-  uint64_t full[2], empty[2], c, t[2], p[2], pfree[2], hat[2], hatfree[2], out, fix[2], drain[2];
+  uint64_t full[2], empty[2], c[2], cempty[2], t[2], half[2], p[2], pfree[2], hat, hatfree, out[2], outfree[2],
+      fix[2], drain[2];
   uint32_t tmem;
   volatile int abort;
 };
@@ -838,57 +842,50 @@ k_la_grad_tc(const __grid_constant__ GradMaps maps, const __grid_constant__ Grad
   __shared__ GradBars bars;
   GradBars* B = &bars;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int c = blockIdx.x % g.nc, row_group = blockIdx.x / g.nc;
-  const int grp = row_group % (g.H / g.share), b = row_group / (g.H / g.share);
-  const Grad::Role r = g.role[blockIdx.y];
-  const GradMaps::Role& m = maps.role[blockIdx.y];
-  const int vblocks = (g.dv + kV - 1) / kV, items = g.share * vblocks, t0 = c * kQ;
-  int len = g.T;
-  if (g.lens) len = __shfl_sync(0xffffffffu, min(max(g.lens[b], 0), g.T), 0);
-  const int n = min(kQ, len - t0);
-  if (n <= 0) {  // a chunk past the row's end
-    const int groups = g.H / g.share, row16 = g.dk / 8, rows = min(kQ, g.T - t0);
-    uint8_t* o = (uint8_t*)r.out + (((size_t)b * g.T + t0) * groups + grp) * g.dk * 2;
-#pragma unroll 1
-    for (int i = tid; i < rows * row16; i += kThreads)
-      *(uint4*)(o + (size_t)(i / row16) * groups * g.dk * 2 + (i % row16) * 16) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const bool ragged = n < kQ && len < g.T;
+  const int vblocks = (g.dv + kV - 1) / kV, items = g.share * vblocks, groups = g.H / g.share;
+  const int units = 2 * g.nc * g.B * groups;
+  const uint32_t lead = (tid & 31) == 0;
   auto all_wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity, B)) != 0;
   };
-  auto load = [&](int u) {
-    const int s = u & 1, h = grp * g.share + u / vblocks, vb = u % vblocks;
-    if (!wait(&B->empty[s], ((u >> 1) & 1) ^ 1, B)) return false;
-    uint8_t* d = sm + G::kSto + s * G::kStage;
-    mbar_expect_tx(&B->full[s], G::kStage);
-    tma_load_4d(d, &m.a, vb * kV, h, t0, b, &B->full[s]);
-    tma_load_4d(d + G::VT, &m.b, vb * kV, h, t0, b, &B->full[s]);
-    tma_load_2d(d + 2 * G::VT, &m.x, 0, (int)hist_row(g.B, g.nc, g.H, vblocks, DK, b, c, h, vb),
-                &B->full[s]);
-    return true;
+  struct Unit {
+    int role, c, grp, b, n;  // n: steps of the chunk that the row has (<= 0: none)
+    bool ragged;             // rows past the row's end, not past T
   };
+  auto unit = [&](int w) {
+    Unit u;
+    u.role = w & 1;
+    u.c = (w >> 1) % g.nc;
+    const int rg = (w >> 1) / g.nc;
+    u.grp = rg % groups;
+    u.b = rg / groups;
+    int len = g.T;
+    if (g.lens) len = __shfl_sync(__activemask(), min(max(g.lens[u.b], 0), g.T), 0);
+    u.n = min(kQ, len - u.c * kQ);
+    u.ragged = u.n < kQ && len < g.T;
+    return u;
+  };
+  // Every role goes over the same units and items; `it` counts the items and
+  // `w` the units that have steps.
   if (tid == 19 * 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->full[i], 1);
       mbar_init(&B->empty[i], 1);
+      mbar_init(&B->c[i], 1);
+      mbar_init(&B->cempty[i], 1);
       mbar_init(&B->t[i], 1);
+      mbar_init(&B->half[i], 4);
       mbar_init(&B->p[i], 8);
       mbar_init(&B->pfree[i], 1);
-      mbar_init(&B->hat[i], 8);
-      mbar_init(&B->hatfree[i], 1);
+      mbar_init(&B->out[i], 1);
+      mbar_init(&B->outfree[i], 8);
       mbar_init(&B->fix[i], 8);
       mbar_init(&B->drain[i], 1);
     }
-    mbar_init(&B->c, 1);
-    mbar_init(&B->out, 1);
+    mbar_init(&B->hat, 8);
+    mbar_init(&B->hatfree, 1);
     B->abort = 0;
     fence_mbar_init();
-    load(0);
-    if (items > 1) load(1);
-    mbar_expect_tx(&B->c, G::CT);
-    for (int x = 0; x < DK; x += 64) tma_load_4d(sm + G::kCo + x * 256, &m.c, x, grp, t0, b, &B->c);
   }
   if (warp == 16) {
     tmem_alloc(&B->tmem, 512);
@@ -898,198 +895,311 @@ k_la_grad_tc(const __grid_constant__ GradMaps maps, const __grid_constant__ Grad
   __syncthreads();
   fence_after_sync();
   const uint32_t tm = __shfl_sync(0xffffffffu, B->tmem, 0);
-  const uint32_t lead = (tid & 31) == 0;
 
   if (warp == 19) {
     // ---- loads ----
-    if (lead) {
-      int u = min(items, 2);
+    int it = 0, w = 0;
+    bool go = true;
 #pragma unroll 1
-      for (; u < items; ++u)
-        if (!load(u)) break;
-      if (B->abort) {  // no copy may be in flight when the CTA ends
-        const uint64_t lim = 50000000ull;
-        for (int j = max(u - 2, 0); j <= u && j < items; ++j) mbar_wait(&B->full[j & 1], (j >> 1) & 1, lim);
-        mbar_wait(&B->c, 0, lim);
+    for (int x = blockIdx.x; go && x < units; x += gridDim.x) {
+      const Unit u = unit(x);
+      if (u.n <= 0) continue;
+      const GradMaps::Role& m = maps.role[u.role];
+      const int ws = w & 1, t0 = u.c * kQ;
+      go = all_wait(&B->cempty[ws], ((w >> 1) & 1) ^ 1);
+      if (!go) break;
+      if (lead) {
+        mbar_expect_tx(&B->c[ws], G::CT);
+        for (int d = 0; d < DK; d += 64)
+          tma_load_4d(sm + G::kCo + ws * G::CT + d * 256, &m.c, d, u.grp, t0, u.b, &B->c[ws]);
+      }
+      ++w;
+#pragma unroll 1
+      for (int i = 0; i < items; ++i, ++it) {
+        const int s = it & 1, h = u.grp * g.share + i / vblocks, vb = i % vblocks;
+        go = all_wait(&B->empty[s], ((it >> 1) & 1) ^ 1);
+        if (!go) break;
+        if (lead) {
+          uint8_t* d = sm + G::kSto + s * G::kStage;
+          mbar_expect_tx(&B->full[s], G::kStage);
+          tma_load_4d(d, &m.a, vb * kV, h, t0, u.b, &B->full[s]);
+          tma_load_4d(d + G::VT, &m.b, vb * kV, h, t0, u.b, &B->full[s]);
+          tma_load_2d(d + 2 * G::VT, &m.x, 0,
+                      (int)hist_row(g.B, g.nc, g.H, vblocks, DK, u.b, u.c, h, vb), &B->full[s]);
+        }
+        __syncwarp();
       }
     }
+    if (B->abort) {  // no copy may be in flight when the CTA ends
+      const uint64_t lim = 50000000ull;
+      for (int j = max(it - 2, 0); j < it; ++j) mbar_wait(&B->full[j & 1], (j >> 1) & 1, lim);
+      for (int j = max(w - 2, 0); j < w; ++j) mbar_wait(&B->c[j & 1], (j >> 1) & 1, lim);
+    }
+    __syncwarp();
   } else if (warp == 17) {
     // ---- T = A B^T ----
     constexpr uint32_t id_t = idesc_bf16(128, 128, false, false);
     const uint64_t dA0 = desc_sw128(smem_u32(sm + G::kSto), 16, 1024);
+    int it = 0;
+    uint32_t fixes = 0;
+    bool go = true;
 #pragma unroll 1
-    for (int u = 0; u < items; ++u) {
-      const int s = u & 1;
-      const uint32_t ph = (u >> 1) & 1;
-      if (!all_wait(&B->full[s], ph)) break;
-      if (ragged && !all_wait(&B->fix[s], ph)) break;
-      // (T two items ago has been read: its P is there)
-      if (u > 1 && !all_wait(&B->p[s], ph ^ 1)) break;
-      fence_after_sync();
-      const uint64_t dA = dA0 + s * (G::kStage >> 4), dB = dA + (G::VT >> 4);
+    for (int x = blockIdx.x; go && x < units; x += gridDim.x) {
+      const Unit u = unit(x);
+      if (u.n <= 0) continue;
+#pragma unroll 1
+      for (int i = 0; i < items; ++i, ++it) {
+        const int s = it & 1;
+        const uint32_t ph = (it >> 1) & 1;
+        go = all_wait(&B->full[s], ph);
+        if (go && u.ragged) {
+          go = all_wait(&B->fix[s], (fixes >> s) & 1);
+          fixes ^= 1u << s;
+        }
+        // (the P that was formed in place of T two items ago has been used)
+        if (go && it > 1) go = all_wait(&B->pfree[s], ph ^ 1);
+        if (!go) break;
+        fence_after_sync();
+        const uint64_t dA = dA0 + s * (G::kStage >> 4), dB = dA + (G::VT >> 4);
 #pragma unroll
-      for (int kk = 0; kk < kV / 16; ++kk)
-        mma_ss(lead, tm + gT + s * 128, dA + 2 * kk, dB + 2 * kk, id_t, kk > 0);
-      commit_if(lead, &B->t[s]);
+        for (int kk = 0; kk < kV / 16; ++kk)
+          mma_ss(lead, tm + gT + s * 128, dA + 2 * kk, dB + 2 * kk, id_t, kk > 0);
+        commit_if(lead, &B->t[s]);
+      }
     }
     commit_if(lead, &B->drain[0]);
     mbar_wait(&B->drain[0], 0, kWaitNs);
     __syncwarp();
   } else if (warp == 18) {
-    // ---- out += P C + (lead o A) X^T ----
+    // ---- out += (lead o A) X^T + P C ----
     constexpr uint32_t id_c = idesc_bf16(128, DK, false, true), id_x = idesc_bf16(128, DK, false, false);
-    const uint64_t dC = desc_sw128(smem_u32(sm + G::kCo), 16384, 1024);
+    const uint64_t dC0 = desc_sw128(smem_u32(sm + G::kCo), 16384, 1024);
     const uint64_t dX0 = desc_sw128(smem_u32(sm + G::kSto + 2 * G::VT), 16, 1024);
-    const uint64_t dH0 = desc_sw128(smem_u32(sm + G::kHo), 16, 1024);
-    bool go = all_wait(&B->c, 0);
+    const uint64_t dH = desc_sw128(smem_u32(sm + G::kHo), 16, 1024);
+    int it = 0, w = 0;
+    bool go = true;
 #pragma unroll 1
-    for (int u = 0; go && u < items; ++u) {
-      const int s = u & 1;
-      const uint32_t ph = (u >> 1) & 1;
-      if (!all_wait(&B->hat[s], ph) || !all_wait(&B->full[s], ph)) break;
-      fence_after_sync();
-      const uint64_t dX = dX0 + s * (G::kStage >> 4), dH = dH0 + s * (2 * G::VT >> 4);
+    for (int x = blockIdx.x; go && x < units; x += gridDim.x) {
+      const Unit u = unit(x);
+      if (u.n <= 0) continue;
+      const int ws = w & 1;
+      const uint32_t pw = (w >> 1) & 1, tO = tm + gOut + ws * 128;
+      go = all_wait(&B->c[ws], pw) && (w < 2 || all_wait(&B->outfree[ws], pw ^ 1));
+      if (!go) break;
+      const uint64_t dC = dC0 + ws * (G::CT >> 4);
+#pragma unroll 1
+      for (int i = 0; i < items; ++i, ++it) {
+        const int s = it & 1;
+        const uint32_t ph = (it >> 1) & 1;
+        go = all_wait(&B->hat, it & 1) && all_wait(&B->full[s], ph);
+        if (!go) break;
+        fence_after_sync();
+        const uint64_t dX = dX0 + s * (G::kStage >> 4);
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int kk = 0; kk < kV / 16; ++kk)
-          mma_ss(lead, tm + gOut, dH + part * (G::VT >> 4) + 2 * kk, dX + 2 * kk, id_x,
-                 u > 0 || part + kk > 0);
-      commit_if(lead, &B->hatfree[s]);
-      if (!all_wait(&B->p[s], ph)) break;
-      fence_after_sync();
+          for (int kk = 0; kk < kV / 16; ++kk)
+            mma_ss(lead, tO, dH + part * (G::VT >> 4) + 2 * kk, dX + 2 * kk, id_x, i > 0 || part + kk > 0);
+        commit_if(lead, &B->hatfree);
+        go = all_wait(&B->p[s], ph);
+        if (!go) break;
+        fence_after_sync();
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts(lead, tm + gOut, tm + gP + s * 64 + 8 * kk, dC + 128 * kk, id_c, 1);
-      commit_if(lead, &B->pfree[s]);
-      commit_if(lead, &B->empty[s]);
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(lead, tO, tm + gT + s * 128 + 8 * kk, dC + 128 * kk, id_c, 1);
+        commit_if(lead, &B->pfree[s]);
+        commit_if(lead, &B->empty[s]);
+      }
+      if (!go) break;
+      commit_if(lead, &B->out[ws]);
+      commit_if(lead, &B->cempty[ws]);
+      ++w;
     }
-    commit_if(lead, &B->out);
     commit_if(lead, &B->drain[1]);
     mbar_wait(&B->drain[1], 0, kWaitNs);
     __syncwarp();
   } else if (warp < 8) {
-    // ---- P: thread = row i and every second 32 columns; out at the end ----
+    // ---- P: thread = row i and half of the columns ----
     const int row = tid & 127, il = row & 31, ib = warp & 3, hf = warp >> 2;
     const uint32_t lane_base = (uint32_t)(ib * 32) << 16;
-    const float sign = r.reverse ? -1.f : 1.f;
-    // zeros into the rows past the row's end: of C once, of A and B of every item
-    auto clear = [&](uint8_t* tile, int tiles) {
-      if (row >= n)
-#pragma unroll 1
-        for (int x = 0; x < tiles * 4; ++x)
-          *(uint4*)(tile + (x >> 2) * 16384 + row * 128 + hf * 64 + (x & 3) * 16) = make_uint4(0, 0, 0, 0);
-    };
+    int it = 0, w = 0;
+    uint32_t wph = 0;
     bool ok = true;
-    if (ragged) {
-      ok = all_wait(&B->c, 0);
-      if (ok) clear(sm + G::kCo, DK / 64);
-    }
 #pragma unroll 1
-    for (int u = 0; ok && u < items; ++u) {
-      const int s = u & 1;
-      const uint32_t ph = (u >> 1) & 1;
-      if (ragged) {
-        if (!(ok = all_wait(&B->full[s], ph))) break;
-        clear(sm + G::kSto + s * G::kStage, 2);
-        fence_async_smem();
-        warp_arrive(&B->fix[s]);
+    for (int x = blockIdx.x; x < units; x += gridDim.x) {
+      const Unit u = unit(x);
+      const Grad::Role& r = g.role[u.role];
+      if (u.n <= 0) {  // a chunk past the row's end
+        const int row16 = g.dk / 8, rows = min(kQ, g.T - u.c * kQ);
+        uint8_t* o = (uint8_t*)r.out + (((size_t)u.b * g.T + u.c * kQ) * groups + u.grp) * g.dk * 2;
+#pragma unroll 1
+        for (int i = tid; i < rows * row16; i += 256)
+          *(uint4*)(o + (size_t)(i / row16) * groups * g.dk * 2 + (i % row16) * 16) = make_uint4(0, 0, 0, 0);
+        continue;
       }
-      // a^{|i-j|} = 2^{(i-j) la2}, la2 of the mask's sign (a decay below 2^-1e30
-      // counts as that: its powers are 0 but for the power 0)
-      const float la = g.log_decay[grp * g.share + u / vblocks];
-      const float la2 = fmaxf(la * 1.4426950408889634f, -1e30f) * sign;
-      if (!(ok = all_wait(&B->t[s], ph))) break;
-      if (u > 1 && !(ok = all_wait(&B->pfree[s], ph ^ 1))) break;
-      fence_after_sync();
+      // zeros into the rows past the row's end: of C once, of A and B of every item
+      auto clear = [&](uint8_t* tile, int tiles) {
+        if (row >= u.n)
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        const int jb = 2 * x + hf, dist = r.reverse ? jb - ib : ib - jb;
-        uint32_t q[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) q[j] = 0;
-        if (dist >= 0) {
-          float v[32];
-          tmem_ld32(tm + gT + s * 128 + lane_base + jb * 32, v);
-          tmem_wait_ld();
-          float d0 = (float)(32 * (ib - jb) + il);
-          asm volatile("" : "+f"(d0));
-          // (on the diagonal a later step has no part in this row, whatever its
-          // product is)
-          const uint32_t in = dist > 0 ? 0xffffffffu : r.reverse ? 0xffffffffu << il : 0xffffffffu >> (31 - il);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float f = r.s_intra * ex2((d0 - (float)j) * la2);
-            v[j] = (in >> j) & 1 ? v[j] * f : 0.f;
+          for (int y = 0; y < tiles * 4; ++y)
+            *(uint4*)(tile + (y >> 2) * 16384 + row * 128 + hf * 64 + (y & 3) * 16) = make_uint4(0, 0, 0, 0);
+      };
+      const int ws = w & 1;
+      wph = (w >> 1) & 1;
+      ++w;
+      if (u.ragged) {
+        ok = __all_sync(0xffffffffu, ok && wait(&B->c[ws], wph, B));
+        if (ok) clear(sm + G::kCo + ws * G::CT, DK / 64);
+      }
+#pragma unroll 1
+      for (int i = 0; i < items; ++i, ++it) {
+        const int s = it & 1;
+        const uint32_t ph = (it >> 1) & 1;
+        if (u.ragged) {
+          ok = __all_sync(0xffffffffu, ok && wait(&B->full[s], ph, B));
+          if (ok) {
+            clear(sm + G::kSto + s * G::kStage, 2);
+            fence_async_smem();
+            warp_arrive(&B->fix[s]);
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) q[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
         }
-        tmem_st16(tm + gP + s * 64 + lane_base + jb * 16, q);
+        // a^{|i-j|} = 2^{(i-j) la2}, la2 of the mask's sign (a decay below 2^-1e30
+        // counts as that: its powers are 0 but for the power 0)
+        const float la = g.log_decay[u.grp * g.share + i / vblocks];
+        const float la2 = fmaxf(la * 1.4426950408889634f, -1e30f) * (r.reverse ? -1.f : 1.f);
+        ok = __all_sync(0xffffffffu, ok && wait(&B->t[s], ph, B));
+        fence_after_sync();
+        // (P takes T's columns: a half overwrites T of its own blocks, or of block 1,
+        // which the first half reads before the second half writes)
+#pragma unroll 1
+        for (int y = 0; y < 2; ++y) {
+          const int jb = 2 * hf + y, dist = r.reverse ? jb - ib : ib - jb;
+          uint32_t q[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) q[j] = 0;
+          float v[32];
+          if (ok && dist >= 0) {
+            tmem_ld32(tm + gT + s * 128 + lane_base + jb * 32, v);
+            tmem_wait_ld();
+          }
+          if (hf == 0 && y == 1 && ok) {
+            fence_before_sync();
+            warp_arrive(&B->half[s]);
+          } else if (hf == 1 && y == 0) {
+            ok = __all_sync(0xffffffffu, ok && wait(&B->half[s], ph, B));
+            fence_after_sync();
+          }
+          if (ok && dist >= 0) {
+            float d0 = (float)(32 * (ib - jb) + il);
+            asm volatile("" : "+f"(d0));
+            // (on the diagonal a later step has no part in this row, whatever its
+            // product is)
+            const uint32_t in = dist > 0 ? 0xffffffffu : r.reverse ? 0xffffffffu << il : 0xffffffffu >> (31 - il);
+            const float si = r.s_intra;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float f = si * ex2((d0 - (float)j) * la2);
+              v[j] = (in >> j) & 1 ? v[j] * f : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) q[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+          }
+          if (ok) tmem_st16(tm + gT + s * 128 + lane_base + jb * 16, q);
+        }
+        if (ok) {
+          tmem_wait_st();
+          fence_before_sync();
+          warp_arrive(&B->p[s]);
+        }
       }
-      tmem_wait_st();
-      fence_before_sync();
-      warp_arrive(&B->p[s]);
-    }
-    ok = __all_sync(0xffffffffu, ok && wait(&B->out, 0, B)) && !B->abort;
-    fence_after_sync();
-    // out in 64-column tiles, staged where the first items were (all are done)
-#pragma unroll 1
-    for (int x = 0; x < DK / 64; ++x) {
-      uint8_t* st = sm + G::kSto + x * 16384;
-      if (ok)
-#pragma unroll 1
-        for (int z = 0; z < 2; ++z) {
-          float v[16];
-          tmem_ld16(tm + gOut + lane_base + x * 64 + hf * 32 + z * 16, v);
-          tmem_wait_ld();
-          if (row >= n)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0.f;
-          *(uint4*)(st + sw128(row, hf * 4 + z * 2)) = pack8(v);
-          *(uint4*)(st + sw128(row, hf * 4 + z * 2 + 1)) = pack8(v + 8);
-        }
-    }
-    fence_async_smem();
-    named_sync(1, 256);
-    if (tid == 0 && ok) {
-      for (int x = 0; x < g.dk; x += 64)
-        tma_store_4d(&m.out, sm + G::kSto + (x >> 6) * 16384, x, grp, t0, b);
-      bulk_commit();
-      bulk_wait0();
     }
   } else if (warp < 16) {
-    // ---- lead o A in two parts: thread = row of A and four of its eight chunks ----
+    // ---- lead o A in two parts (thread = row of A and four of its eight chunks);
+    // out of the unit before (thread = row and half of the columns) ----
     const int t = tid - 256, row = t & 127, hf = t >> 7;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    int it = 0, w = 0;
+    uint32_t fixes = 0;
+    bool ok = true;  // (after a wait that gave up the warps still meet at their barriers)
+    Unit last = {};
+    // out of unit number v, in 64-column tiles
+    auto finish = [&](int v, const Unit& u) {
+      const int ws = v & 1;
+      ok = __all_sync(0xffffffffu, ok && wait(&B->out[ws], (v >> 1) & 1, B));
+      fence_after_sync();
+      if (t == 0) bulk_wait_read0();
+      named_sync(3, 256);
+      if (ok) {
 #pragma unroll 1
-    for (int u = 0; u < items; ++u) {
-      const int s = u & 1;
-      const uint32_t ph = (u >> 1) & 1;
-      const float la = g.log_decay[grp * g.share + u / vblocks];
-      const float w = row < n ? r.s_carry * decay_pow(la, (float)((r.reverse ? n - 1 - row : row) + r.off)) : 0.f;
-      const float2 w2 = make_float2(w, w);
-      if (!all_wait(&B->full[s], ph)) break;
-      if (ragged && !all_wait(&B->fix[s], ph)) break;
-      if (u > 1 && !all_wait(&B->hatfree[s], ph ^ 1)) break;
-      const uint8_t* src = sm + G::kSto + s * G::kStage;
-      uint8_t* dst = sm + G::kHo + s * 2 * G::VT;
+        for (int z = 0; z < DK / 32; ++z) {  // 16 of this thread's columns at a time
+          const int col = (z >> 1) * 64 + hf * 32 + (z & 1) * 16;
+          float f[16];
+          tmem_ld16(tm + gOut + ws * 128 + lane_base + col, f);
+          tmem_wait_ld();
+          if (row >= u.n)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t at = sw128(row, hf * 4 + q);
-        float2 f[4], e[4];
-        unpack8(*(const uint4*)(src + at), (float*)f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], w2);
-        const uint4 hi = pack8((const float*)f);
-        unpack8(hi, (float*)e);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = fma2(e[i], make_float2(-1.f, -1.f), f[i]);
-        *(uint4*)(dst + at) = hi;
-        *(uint4*)(dst + G::VT + at) = pack8((const float*)f);
+            for (int j = 0; j < 16; ++j) f[j] = 0.f;
+          uint8_t* st = sm + G::kOo + (z >> 1) * 16384;
+          *(uint4*)(st + sw128(row, (col & 63) / 8)) = pack8(f);
+          *(uint4*)(st + sw128(row, (col & 63) / 8 + 1)) = pack8(f + 8);
+        }
+        fence_before_sync();
+        fence_async_smem();
+        warp_arrive(&B->outfree[ws]);
       }
-      fence_async_smem();
-      warp_arrive(&B->hat[s]);
+      named_sync(3, 256);
+      if (t == 0 && ok) {
+        for (int d = 0; d < g.dk; d += 64)
+          tma_store_4d(&maps.role[u.role].out, sm + G::kOo + (d >> 6) * 16384, d, u.grp, u.c * kQ, u.b);
+        bulk_commit();
+      }
+    };
+#pragma unroll 1
+    for (int x = blockIdx.x; x < units; x += gridDim.x) {
+      const Unit u = unit(x);
+      if (u.n <= 0) continue;
+      const Grad::Role& r = g.role[u.role];
+#pragma unroll 1
+      for (int i = 0; i < items; ++i, ++it) {
+        const int s = it & 1;
+        const uint32_t ph = (it >> 1) & 1;
+        const float la = g.log_decay[u.grp * g.share + i / vblocks];
+        const float wt =
+            row < u.n ? r.s_carry * decay_pow(la, (float)((r.reverse ? u.n - 1 - row : row) + r.off)) : 0.f;
+        const float2 w2 = make_float2(wt, wt);
+        bool in = ok && wait(&B->full[s], ph, B);
+        if (u.ragged) {
+          in = in && wait(&B->fix[s], (fixes >> s) & 1, B);
+          fixes ^= 1u << s;
+        }
+        ok = __all_sync(0xffffffffu, in && (it == 0 || wait(&B->hatfree, (it - 1) & 1, B)));
+        if (ok) {
+          const uint8_t* src = sm + G::kSto + s * G::kStage;
+          uint8_t* dst = sm + G::kHo;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t at = sw128(row, hf * 4 + q);
+            float2 f[4], e[4];
+            unpack8(*(const uint4*)(src + at), (float*)f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], w2);
+            const uint4 hi = pack8((const float*)f);
+            unpack8(hi, (float*)e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = fma2(e[j], make_float2(-1.f, -1.f), f[j]);
+            *(uint4*)(dst + at) = hi;
+            *(uint4*)(dst + G::VT + at) = pack8((const float*)f);
+          }
+          fence_async_smem();
+          warp_arrive(&B->hat);
+        }
+        if (i == 0 && w > 0) finish(w - 1, last);
+      }
+      last = u;
+      ++w;
     }
+    if (w > 0) finish(w - 1, last);
+    if (t == 0) bulk_wait0();
   }
   fence_before_sync();
   __syncthreads();
@@ -1183,8 +1293,7 @@ static int la_tc_segments(int B, int H, int T, int dv) {
 }
 
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv) {
-  // (the walks of a backward pass have dk and dv in either order)
-  const int a = la_tc_segments(B, H, T, dv), b = la_tc_segments(B, H, T, dk), n = a > b ? a : b;
+  const int n = la_tc_segments(B, H, T, dv);
   return n > 1 ? (size_t)n * B * H * dk * dv : 0;
 }
 
@@ -1227,10 +1336,11 @@ cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     LaunchScope ls("linattn_grads", s);
-    kernel<<<dim3((unsigned)((long long)g.nc * d.B * G), 2), kThreads, smem, s>>>(m, g);
+    const long long units = 2ll * g.nc * d.B * G;
+    kernel<<<(unsigned)(units < 152 ? units : 152), kThreads, smem, s>>>(m, g);
     return cudaGetLastError();
   };
-  static_assert(GradGeom<128>::smem + 2048 <= 232448, "shared memory of a CTA");
+  static_assert(GradGeom<128>::smem + 1024 <= 232448, "shared memory of a CTA");
   return DK == 64 ? go(k_la_grad_tc<64>, GradGeom<64>::smem) : go(k_la_grad_tc<128>, GradGeom<128>::smem);
 }
 
@@ -1266,16 +1376,14 @@ cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_
   p.nseg = n;
   p.first = w.first;
   p.last = w.last;
-  p.first_swapped = w.first_swapped;
   if (n > 1) {
     p.last = scratch;
     cudaError_t e = launch_d<true>(m, p, s);
     if (e != cudaSuccess) return e;
     const LaSegments g = {w.B, w.H, w.T, w.dk, w.dv, n, p.seg_chunks * kQ, w.log_decay, w.lens,
-                          scratch, w.first, w.last, w.first_swapped, w.reverse};
+                          scratch, w.first, w.last, false, w.reverse};
     if ((e = la_segment_states(g, s)) != cudaSuccess) return e;
     p.first = scratch;
-    p.first_swapped = 0;
     p.last = nullptr;
   } else {
     p.beside = beside;

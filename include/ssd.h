@@ -260,7 +260,10 @@ typedef struct {
 } ssd_linattn_dims;
 
 /* Bytes of workspace of ssd_linattn_forward (which = 0) or
- * ssd_linattn_backward (which = 1); 0 for dims the library rejects. */
+ * ssd_linattn_backward (which = 1); 0 for dims the library rejects, 256 where
+ * none is used (the workspace may then be NULL).  The forward uses one where
+ * rows are few and long (they are shared out over the GPU), the bf16 backward
+ * always (the states before every 128 steps). */
 SSD_API size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* dims, int which);
 
 /* state0, lens, state (the final state) may be NULL. */

@@ -116,7 +116,9 @@ size_t la_part_bytes(const ssd_linattn_dims* d, int which) {
   return up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
 }
 
+// (256 bytes stand for none)
 int workspace_check(const char* who, const void* workspace, size_t bytes, size_t need) {
+  if (!workspace && need == 256) return SSD_OK;
   if (!workspace) return refuse(SSD_ERR_INVALID_ARG, "%s: workspace is NULL", who);
   if ((uintptr_t)workspace & 255u)
     return refuse(SSD_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", who);

@@ -30,6 +30,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _size(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 # the current stream's handle without a Stream object around it, where this
 # torch has the call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -174,12 +178,12 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
         _expect("out o", o, v.dtype, v.shape, dev)
     if state is None and want_state:
         state = torch.empty(shape, dtype=torch.float32, device=dev)
-    if workspace is None:
+    if workspace is None and need > 256:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _keep(stream, o, state, workspace)
     nat.check(_call("ssd_linattn_forward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
-        _ptr(lens), o.data_ptr(), _ptr(state), workspace.data_ptr(), workspace.numel(),
+        _ptr(lens), o.data_ptr(), _ptr(state), _ptr(workspace), _size(workspace),
         _stream_handle(stream, dev)))
     return o, state
 
@@ -203,13 +207,13 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
         g["dstate0"] = None
     elif g.get("dstate0") is None:
         g["dstate0"] = torch.empty(shape, dtype=torch.float32, device=dev)
-    if workspace is None:
+    if workspace is None and need > 256:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _keep(stream, workspace, *g.values())
     nat.check(_call("ssd_linattn_backward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
         do.data_ptr(), _ptr(dstate), _ptr(lens), g["dq"].data_ptr(), g["dk"].data_ptr(),
-        g["dv"].data_ptr(), _ptr(g["dstate0"]), workspace.data_ptr(), workspace.numel(),
+        g["dv"].data_ptr(), _ptr(g["dstate0"]), _ptr(workspace), _size(workspace),
         _stream_handle(stream, dev)))
     return g
 
@@ -367,19 +371,19 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), _ptr(stats),
         dx.data_ptr(), _ptr(dnew), g["dresidual"].data_ptr(), g["dy"].data_ptr(), _ptr(g["dz"]),
         g["dw_post"].data_ptr(), _ptr(g["dres_scale"]), g["dw_pre"].data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _stream_handle(stream, dev)))
+        workspace.data_ptr(), _size(workspace), _stream_handle(stream, dev)))
     return g
 
 
 # ---- gradient clipping ---------------------------------------------------------------
 
 _Tensor = torch.Tensor
-_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_dtype = operator.attrgetter("dtype")
 
 def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, stream=None):
     """Scales the gradients by min(1, max_norm / (n + eps)), n the square root
     of the sum of all their squares; in place, or into the tensors of `out`
-    (same shapes and types).  grads: contiguous CUDA tensors, fp32 and bf16
+    (of the same sizes and types).  grads: contiguous CUDA tensors, fp32 and bf16
     mixed as they come, of any size.  Returns n, a 0-d fp32 tensor on the
     device (nothing is synchronised).  A NaN in a gradient makes n and every
     gradient NaN."""
@@ -405,8 +409,8 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
     if out is not None:
         if of(_dtype, outs) != dtypes:
             raise TypeError("out: another dtype than the gradient's")
-        if of(_shape, outs) != of(_shape, grads) or of(_Tensor.get_device, outs) != [dev.index] * n:
-            raise ValueError("out: another shape or device than the gradient's")
+        if of(_Tensor.numel, outs) != sizes or of(_Tensor.get_device, outs) != [dev.index] * n:
+            raise ValueError("out: another size or device than the gradient's")
         if not all(map(_Tensor.is_contiguous, outs)):
             raise ValueError("out: must be contiguous")
         to = of(_Tensor.data_ptr, outs)
@@ -422,6 +426,6 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _keep(stream, norm, workspace)
     nat.check(_call("ssd_clip_grad_norm")(rows, n, float(max_norm), float(eps), norm.data_ptr(),
-                                   workspace.data_ptr(), workspace.numel(),
+                                   workspace.data_ptr(), _size(workspace),
                                    _stream_handle(stream, dev)))
     return norm

@@ -66,6 +66,7 @@ def test_linattn_pointers_and_workspace(L):
     assert need >= 2 * 10 * 4 * 16 * 4 and L.ssd_linattn_workspace_bytes(d, 0) < need
     assert backward(L, d, ws=need - 1) == nat.SSD_ERR_INVALID_ARG
     assert L.ssd_linattn_workspace_bytes(d, 2) == 0
+    assert L.ssd_linattn_workspace_bytes(dims(batch=64, v_batch=960), 0) == 256  # none is used
     assert L.ssd_linattn_forward(None, F, F, F, F, None, None, F, None, F, 1 << 30, None) == \
         nat.SSD_ERR_INVALID_ARG
 

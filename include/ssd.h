@@ -266,7 +266,7 @@ typedef struct {
  * always (the states before every 128 steps). */
 SSD_API size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* dims, int which);
 
-/* state0, lens, state (the final state) may be NULL. */
+/* state0, lens, state (the final state) may be NULL; state may be state0. */
 SSD_API int ssd_linattn_forward(const ssd_linattn_dims* dims, const void* q, const void* k,
                                 const void* v, const float* log_decay, const float* state0,
                                 const int32_t* lens, void* o, float* state,

@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ Si
   }
   if (!kStates) {  // past the row's end
     const int z0 = max(s0, min(len, s0 + args.span)), z1 = min(s0 + args.span, w.T);
-    for (int i = t; i < (z1 - z0) * (kB / 4); i += kThreads) {
-      const int r = i / (kB / 4), d = i % (kB / 4) * 4;
-      if (d < dv) *(float4*)(op + (long long)(z0 + r) * w.H * w.dv + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    const int d = t % (kB / 4) * 4;
+    if (d < dv)
+      for (int r = z0 + t / (kB / 4); r < z1; r += kThreads / (kB / 4))
+        *(float4*)(op + (long long)r * w.H * w.dv + d) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   if (w.last)
 #pragma unroll

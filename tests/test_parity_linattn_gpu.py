@@ -78,6 +78,9 @@ CASES = [
     (5, 260, 2, 1, 64, 64, "bf16", (0, 1, 128, 259, 260), None),
     (4, 150, 4, 2, 128, 64, "bf16", (150, 129, 0, 2), (0.0, -0.1, -np.inf, -1e30)),
     (3, 70, 2, 2, 32, 16, "f32", (70, 0, 33), (-np.inf, -0.2)),
+    # more (row, chunk, group) units than SMs, whole and ending anywhere
+    (8, 1300, 4, 2, 64, 64, "bf16", (0, 1, 128, 129, 640, 1000, 1299, 1300), (-0.01, -0.5)),
+    (6, 1100, 3, 3, 128, 128, "bf16", None, (-0.004, -0.1, -2.0)),
     # enough steps for a row to be shared out
     (1, 4100, 1, 1, 64, 64, "bf16", None, (-0.002,)),
     (1, 3000, 2, 1, 128, 128, "bf16", (2999,), (-0.001, -0.3)),
@@ -198,6 +201,20 @@ def test_two_runs_are_equal_and_streams_are_followed():
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(o, o2) and torch.equal(S, S2)
     assert all(torch.equal(g[n], g2[n]) for n in g)
+
+
+@pytest.mark.parametrize("T", [100, 5000])
+def test_the_state_in_place(T):
+    """The final state written over the first one, rows whole and shared out."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    for dtype in ("bf16", "f32"):
+        inp = synth.linattn_inputs(1, T, 2, 1, 64, 64, dtype, 8, (-0.01, -0.002))
+        q, k, v = (dev(inp[x], dtype) for x in "qkv")
+        la, s0 = dev(inp["log_decay"]), dev(inp["state0"])
+        o, S = ssd.linattn_forward(q, k, v, la, s0.clone())
+        o2, S2 = ssd.linattn_forward(q, k, v, la, s0, out={"state": s0})
+        assert S2 is s0 and torch.equal(S, s0) and torch.equal(o, o2)
 
 
 def test_a_row_alone_is_the_row_in_a_batch():

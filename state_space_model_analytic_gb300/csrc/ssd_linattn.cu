@@ -15,6 +15,7 @@
 // i.e. the same walk with the operands' roles exchanged, the last three from
 // the last step back (off = 0: the incoming dS belongs to the last step
 // itself, not to the one before the first).
+#include "f32x2.cuh"
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
 #include "ssd_layer_internal.h"
@@ -29,26 +30,29 @@ __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f 
 //
 // One CTA per (h, 32 columns of v, b, segment of the row), chunks of 64 steps.
 // 128 threads as 16 x 8: thread (ty, tx) forms 4 x 4 blocks of the products
-//   P = mask(Q K^T)      rows 4 ty + a, columns tx + 8 c
-//   o = P V + lead Q X   rows 4 ty + a, columns 4 tx + b
-//   X = a^n X + K^T w V  rows 4 ty + a (+ 64), columns 4 tx + b, in registers
-// with operands in shared memory, 16 bytes at a time: eight 16-byte loads (12
-// shared-memory cycles) serve 64 FMAs of a warp (16 cycles of the SM's FMA
-// units), so the FMAs bound it; P and P V leave out the columns that the mask
-// empties for a warp's sixteen rows.  64 columns of v form P twice, for a
-// quarter more FMAs, but three of these CTAs run on an SM and hide one
-// another's loads (64 columns in one CTA of 256 threads measured 318 us on
-// 8 x 1024 steps, 24 heads of 64/64).  fp32 throughout: the operands' type leaves
-// no other choice that keeps their precision.
+//   u = Q X              rows 4 ty + a, columns 4 tx + e
+//   P = mask(Q K^T)      rows 4 ty + a, columns tx + 8 e
+//   o = lead u + P V     rows 4 ty + a, columns 4 tx + e
+//   X = a^n X + K^T w V  rows 4 ty + a (+ 64), columns 4 tx + e, in registers
+// two products an instruction (fma.f32x2): the first three add up even and odd
+// terms of their sums apart, from operands that lie along the sum (V and X are
+// kept transposed for that); the last forms pairs of rows k, with each w V held
+// twice.  Eight 16-byte loads then serve 32 instructions of 64 products.  P
+// replaces the rows of Q that a warp is done with, which leaves room for three
+// CTAs on an SM to hide one another's loads; P and P V leave out the columns
+// that the mask empties for a warp's sixteen rows.  fp32 throughout: the
+// operands' type leaves no other choice that keeps their precision.
 constexpr int kC = 64;         // steps of a chunk
 constexpr int kB = 32;         // columns of v of a CTA
 constexpr int kThreads = 128;
 
-template <int DK>
+template <int DK, bool kStates>
 struct Simt {
   static constexpr int LK = DK + 4;  // rows 16 bytes apart in the banks
-  static constexpr int LP = kC + 4;
-  static constexpr int kFloats = 2 * kC * LK + kC * kB + kC * LP + DK * kB;
+  static constexpr int LV = kC + 4;
+  // K and w V (twice); Q or P, V and X transposed
+  static constexpr int kFloats =
+      kC * LK + 2 * kC * kB + (kStates ? 0 : kC * LK + kB * LV + kB * LK);
   static constexpr size_t smem = kFloats * sizeof(float);
 };
 
@@ -58,19 +62,51 @@ struct SimtWalk {
 };
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *(const float4*)p; }
+// 16 bytes, or zeros
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+// acc += l . r over four terms, even and odd ones apart
+__device__ __forceinline__ float2 dot4(float4 l, float4 r, float2 acc) {
+  return fma2(make_float2(l.x, l.y), make_float2(r.x, r.y),
+              fma2(make_float2(l.z, l.w), make_float2(r.z, r.w), acc));
+}
+
+// acc[a][e] += rows a of `left` . rows 8 e of `right`, terms [from, to)
+template <int LL, int LR>
+__device__ __forceinline__ void block4x4(const float* left, const float* right, int from, int to,
+                                         float2 (&acc)[4][4]) {
+#pragma unroll 2
+  for (int d = from; d < to; d += 4) {
+    float4 l[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) l[a] = ld4(left + a * LL + d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 r = ld4(right + 8 * e * LR + d);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) acc[a][e] = dot4(l[a], r, acc[a][e]);
+    }
+  }
+}
 
 // kStates: only the state, each segment from zero, into w.last
 // [nseg][B][H][dv][dk].
 template <int DK, bool kStates>
-__global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ SimtWalk args) {
-  using G = Simt<DK>;
+__global__ void __launch_bounds__(kThreads, DK == 64 ? 3 : 2)
+k_la_walk(const __grid_constant__ SimtWalk args) {
+  using G = Simt<DK, kStates>;
+  constexpr int LK = G::LK, LV = G::LV;
   const LaWalk& w = args.w;
   extern __shared__ __align__(16) float sm[];
-  float* Q = sm;
-  float* K = Q + kC * G::LK;
-  float* V = K + kC * G::LK;
-  float* P = V + kC * kB;
-  float* X = P + kC * G::LP;
+  float* K = sm;
+  float* W = K + kC * LK;       // w V: [step][columns 4 tx, 4 tx + 1, then + 2, + 3][twice]
+  float* Q = W + 2 * kC * kB;   // P once the warp is done with its rows
+  float* V = Q + kC * LK;       // column 4 i + c in row i + 8 c
+  float* X = V + kB * LV;       // the same
   __shared__ float pw[kC + 2];
   const int vblocks = (w.dv + kB - 1) / kB;
   const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kB;
@@ -85,13 +121,15 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ Si
   auto state_at = [&](int k, int v) {
     return sbase + (!kStates && w.first_swapped ? (size_t)k * w.dv + v0 + v : (size_t)(v0 + v) * w.dk + k);
   };
-  float x[DK / 16][4];
+  float2 x[DK / 32][4];  // rows k = 4 ty + 2 (i & 1) + 64 (i >> 1) and the next
 #pragma unroll
-  for (int a = 0; a < DK / 16; ++a)
+  for (int i = 0; i < DK / 32; ++i)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int k = 4 * ty + (a & 3) + (a >> 2) * 64, v = 4 * tx + c;
-      x[a][c] = !kStates && w.first && k < w.dk && v < dv ? w.first[state_at(k, v)] : 0.f;
+      const int k = 4 * ty + 2 * (i & 1) + (i >> 1) * 64, v = 4 * tx + c;
+      const bool in = !kStates && w.first && k < w.dk && v < dv;
+      x[i][c] = in ? make_float2(w.first[state_at(k, v)], w.first[state_at(k + 1, v)])
+                   : make_float2(0.f, 0.f);
     }
   const float* qp = (const float*)w.q.p + b * w.q.batch + (long long)(h / w.q.share) * w.dk;
   const float* kp = (const float*)w.k.p + b * w.k.batch + (long long)(h / w.k.share) * w.dk;
@@ -105,114 +143,113 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ Si
     for (int i = t; i < kC * (DK / 4); i += kThreads) {
       const int r = i / (DK / 4), d = i % (DK / 4) * 4;
       const bool in = r < n && d < w.dk;
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!kStates) *(float4*)(Q + r * G::LK + d) = in ? ld4(qp + (long long)(t0 + r) * w.q.step + d) : z;
-      *(float4*)(K + r * G::LK + d) = in ? ld4(kp + (long long)(t0 + r) * w.k.step + d) : z;
+      if (!kStates) copy16(Q + r * LK + d, in ? qp + (long long)(t0 + r) * w.q.step + d : qp, in);
+      copy16(K + r * LK + d, in ? kp + (long long)(t0 + r) * w.k.step + d : kp, in);
     }
-    for (int i = t; i < kC * (kB / 4); i += kThreads) {
-      const int r = i / (kB / 4), d = i % (kB / 4) * 4;
-      *(float4*)(V + r * kB + d) =
-          r < n && d < dv ? ld4(vp + (long long)(t0 + r) * w.v.step + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 v[kC * (kB / 4) / kThreads];
+#pragma unroll
+    for (int i = 0; i < kC * (kB / 4) / kThreads; ++i) {
+      const int r = (t + i * kThreads) / (kB / 4);
+      v[i] = r < n && 4 * tx < dv ? ld4(vp + (long long)(t0 + r) * w.v.step + 4 * tx)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (!kStates)
 #pragma unroll
-      for (int a = 0; a < DK / 16; ++a)
-        *(float4*)(X + (4 * ty + (a & 3) + (a >> 2) * 64) * kB + 4 * tx) =
-            make_float4(x[a][0], x[a][1], x[a][2], x[a][3]);
+      for (int g = 0; g < DK / 64; ++g)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *(float4*)(X + (tx + 8 * c) * LK + 4 * ty + 64 * g) =
+              make_float4(x[2 * g][c].x, x[2 * g][c].y, x[2 * g + 1][c].x, x[2 * g + 1][c].y);
+#pragma unroll
+    for (int i = 0; i < kC * (kB / 4) / kThreads; ++i) {
+      const int r = (t + i * kThreads) / (kB / 4);
+      const float f = r < n ? w.s_inject * pw[(w.reverse ? r : n - 1 - r) + 1 - w.off] : 0.f;
+      const float4 y = make_float4(f * v[i].x, f * v[i].y, f * v[i].z, f * v[i].w);
+      *(float4*)(W + r * 2 * kB + 4 * tx) = make_float4(y.x, y.x, y.y, y.y);
+      *(float4*)(W + r * 2 * kB + kB + 4 * tx) = make_float4(y.z, y.z, y.w, y.w);
+      if (!kStates) {
+        V[tx * LV + r] = v[i].x;
+        V[(tx + 8) * LV + r] = v[i].y;
+        V[(tx + 16) * LV + r] = v[i].z;
+        V[(tx + 24) * LV + r] = v[i].w;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (!kStates) {
-      // groups of 32 columns (tx + 8 c, c in fours) that the warp's rows 16 wp ...
-      // 16 wp + 15 need
-      const int ca = w.reverse ? wp / 2 : 0, cb = w.reverse ? 2 : wp / 2 + 1;
-#pragma unroll 1
-      for (int c = ca; c < cb; ++c) {
-        float s[4][4];
+      float2 o[4][4];
+      auto clear = [](float2 (&acc)[4][4]) {
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[a][e] = 0.f;
-        const float* kr = K + (tx + 32 * c) * G::LK;
-#pragma unroll 4
-        for (int d = 0; d < DK; d += 4) {
-          float4 q[4];
+          for (int e = 0; e < 4; ++e) acc[a][e] = make_float2(0.f, 0.f);
+      };
+      clear(o);
+      block4x4<LK, LK>(Q + 4 * ty * LK, X + tx * LK, 0, DK, o);
 #pragma unroll
-          for (int a = 0; a < 4; ++a) q[a] = ld4(Q + (4 * ty + a) * G::LK + d);
+      for (int a = 0; a < 4; ++a) {
+        const int i = min(4 * ty + a, n - 1);  // (a row past the end is not written)
+        const float lead = w.s_carry * pw[(w.reverse ? n - 1 - i : i) + w.off];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 kk = ld4(kr + 8 * e * G::LK + d);
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-              s[a][e] = fmaf(q[a].x, kk.x, fmaf(q[a].y, kk.y, fmaf(q[a].z, kk.z, fmaf(q[a].w, kk.w, s[a][e]))));
-          }
-        }
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = 4 * ty + a, j = tx + 32 * c + 8 * e, d = w.reverse ? j - i : i - j;
-            P[i * G::LP + j] = d >= 0 ? w.s_intra * pw[d] * s[a][e] : 0.f;
-          }
+        for (int e = 0; e < 4; ++e) o[a][e] = make_float2(lead * (o[a][e].x + o[a][e].y), 0.f);
       }
-      __syncwarp();  // (a warp reads the rows of P that it wrote)
-      float o[4][4], u[4][4];
+      // groups of 32 columns (tx + 8 e) that the warp's rows 16 wp ... 16 wp + 15
+      // need: the diagonal one, and the one before (after) it for half of the warps
+      const int c0 = wp / 2;
+      const bool both = w.reverse ? c0 == 0 : c0 == 1;
+      float2 s[4][4];
+      float p[4][4];
+      if (both) {
+        clear(s);
+        block4x4<LK, LK>(Q + 4 * ty * LK, K + (tx + 32 * (1 - c0)) * LK, 0, DK, s);
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[a][e] = s[a][e].x + s[a][e].y;
+      }
+      clear(s);
+      block4x4<LK, LK>(Q + 4 * ty * LK, K + (tx + 32 * c0) * LK, 0, DK, s);
+      __syncwarp();  // (the rows of Q are the warp's own)
+      auto put = [&](int c, int a, int e, float f) {
+        const int i = 4 * ty + a, j = tx + 32 * c + 8 * e, d = w.reverse ? j - i : i - j;
+        Q[i * LK + j] = d >= 0 ? w.s_intra * pw[d] * f : 0.f;
+      };
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[a][c] = u[a][c] = 0.f;
-      auto rank4 = [&](const float* left, int ld, const float* right, float (&acc)[4][4]) {
-        float4 l[4], r[4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) l[a] = ld4(left + a * ld);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = ld4(right + e * kB);
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const float f[4] = {l[a].x, l[a].y, l[a].z, l[a].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[a][0] = fmaf(f[e], r[e].x, acc[a][0]);
-            acc[a][1] = fmaf(f[e], r[e].y, acc[a][1]);
-            acc[a][2] = fmaf(f[e], r[e].z, acc[a][2]);
-            acc[a][3] = fmaf(f[e], r[e].w, acc[a][3]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          put(c0, a, e, s[a][e].x + s[a][e].y);
+          if (both) put(1 - c0, a, e, p[a][e]);
         }
-      };
-#pragma unroll 4
-      for (int j = w.reverse ? 16 * wp : 0; j < (w.reverse ? kC : 16 * wp + 16); j += 4)
-        rank4(P + 4 * ty * G::LP + j, G::LP, V + j * kB + 4 * tx, o);
-#pragma unroll 4
-      for (int d = 0; d < DK; d += 4)
-        rank4(Q + 4 * ty * G::LK + d, G::LK, X + d * kB + 4 * tx, u);
+      __syncwarp();
+      block4x4<LK, LV>(Q + 4 * ty * LK, V + tx * LV, w.reverse ? 16 * wp : 0,
+                       w.reverse ? kC : 16 * wp + 16, o);
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         const int i = 4 * ty + a;
-        if (i < n && 4 * tx < dv) {
-          const float lead = w.s_carry * pw[(w.reverse ? n - 1 - i : i) + w.off];
+        if (i < n && 4 * tx < dv)
           *(float4*)(op + (long long)(t0 + i) * w.H * w.dv + 4 * tx) =
-              make_float4(fmaf(lead, u[a][0], o[a][0]), fmaf(lead, u[a][1], o[a][1]),
-                          fmaf(lead, u[a][2], o[a][2]), fmaf(lead, u[a][3], o[a][3]));
-        }
+              make_float4(o[a][0].x + o[a][0].y, o[a][1].x + o[a][1].y, o[a][2].x + o[a][2].y,
+                          o[a][3].x + o[a][3].y);
       }
     }
-    const float an = pw[n];
+    const float2 an = make_float2(pw[n], pw[n]);
 #pragma unroll
-    for (int a = 0; a < DK / 16; ++a)
+    for (int i = 0; i < DK / 32; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[a][c] *= an;
+      for (int c = 0; c < 4; ++c) x[i][c] = mul2(x[i][c], an);
 #pragma unroll 4
     for (int j = 0; j < n; ++j) {
-      const float f = w.s_inject * pw[(w.reverse ? j : n - 1 - j) + 1 - w.off];
-      const float4 v = ld4(V + j * kB + 4 * tx);
-      const float y[4] = {f * v.x, f * v.y, f * v.z, f * v.w};
+      const float4 ya = ld4(W + j * 2 * kB + 4 * tx), yb = ld4(W + j * 2 * kB + kB + 4 * tx);
+      const float2 y[4] = {make_float2(ya.x, ya.y), make_float2(ya.z, ya.w),
+                           make_float2(yb.x, yb.y), make_float2(yb.z, yb.w)};
 #pragma unroll
       for (int g = 0; g < DK / 64; ++g) {
-        const float4 k = ld4(K + j * G::LK + 4 * ty + 64 * g);
+        const float4 k = ld4(K + j * LK + 4 * ty + 64 * g);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          x[4 * g][c] = fmaf(k.x, y[c], x[4 * g][c]);
-          x[4 * g + 1][c] = fmaf(k.y, y[c], x[4 * g + 1][c]);
-          x[4 * g + 2][c] = fmaf(k.z, y[c], x[4 * g + 2][c]);
-          x[4 * g + 3][c] = fmaf(k.w, y[c], x[4 * g + 3][c]);
+          x[2 * g][c] = fma2(make_float2(k.x, k.y), y[c], x[2 * g][c]);
+          x[2 * g + 1][c] = fma2(make_float2(k.z, k.w), y[c], x[2 * g + 1][c]);
         }
       }
     }
@@ -226,11 +263,14 @@ __global__ void __launch_bounds__(kThreads) k_la_walk(const __grid_constant__ Si
   }
   if (w.last)
 #pragma unroll
-    for (int a = 0; a < DK / 16; ++a)
+    for (int i = 0; i < DK / 32; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int k = 4 * ty + (a & 3) + (a >> 2) * 64, v = 4 * tx + c;
-        if (k < w.dk && v < dv) w.last[state_at(k, v)] = x[a][c];
+        const int k = 4 * ty + 2 * (i & 1) + (i >> 1) * 64, v = 4 * tx + c;
+        if (k < w.dk && v < dv) {
+          w.last[state_at(k, v)] = x[i][c].x;
+          w.last[state_at(k + 1, v)] = x[i][c].y;
+        }
       }
 }
 
@@ -268,13 +308,13 @@ __global__ void __launch_bounds__(256) k_la_segments(const LaSegments p) {
 
 template <int DK, bool kStates>
 cudaError_t walk_t(const SimtWalk& a, cudaStream_t s) {
+  constexpr int smem = (int)Simt<DK, kStates>::smem;
   cudaError_t e = cudaFuncSetAttribute(k_la_walk<DK, kStates>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Simt<DK>::smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(kStates ? "linattn_states" : a.w.reverse ? "linattn_walk_back" : "linattn_walk", s);
   const int vblocks = (a.w.dv + kB - 1) / kB;
-  k_la_walk<DK, kStates><<<dim3(a.w.H * vblocks, a.w.B, a.nseg), kThreads, Simt<DK>::smem, s>>>(a);
+  k_la_walk<DK, kStates><<<dim3(a.w.H * vblocks, a.w.B, a.nseg), kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -429,7 +469,7 @@ cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// CTAs of the fp32 walk that run at once on 152 SMs (three of 70 KB, or two of 112)
+// CTAs of the fp32 walk that run at once on 152 SMs (three of 69 KB, or two of 110)
 static int simt_segments(int B, int H, int T, int dk, int dv) {
   return la_segments((long long)B * H * ((dv + kB - 1) / kB), (T + kC - 1) / kC,
                      dk <= 64 ? 456 : 304);

@@ -26,42 +26,52 @@ namespace {
 // a^e for e >= 0 from log a; a^0 = 1 also where a = 0 (log a = -inf)
 __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f ? 1.f : expf(la * e); }
 
-// ---- the walk in fp32 on the CUDA cores ---------------------------------------
+// ---- the walk in fp32 -----------------------------------------------------------
 //
-// One CTA per (h, 32 columns of v, b, segment of the row), chunks of 64 steps.
-// 128 threads as 16 x 8: thread (ty, tx) forms 4 x 4 blocks of the products
-//   u = Q X              rows 4 ty + a, columns 4 tx + e
-//   P = mask(Q K^T)      rows 4 ty + a, columns tx + 8 e
-//   o = lead u + P V     rows 4 ty + a, columns 4 tx + e
-//   X = a^n X + K^T w V  rows 4 ty + a (+ 64), columns 4 tx + e, in registers
-// two products an instruction (fma.f32x2): the first three add up even and odd
-// terms of their sums apart, from operands that lie along the sum (V and X are
-// kept transposed for that); the last forms pairs of rows k, with each w V held
-// twice.  Eight 16-byte loads then serve 32 instructions of 64 products.  P
-// replaces the rows of Q that a warp is done with, which leaves room for three
-// CTAs on an SM to hide one another's loads; P and P V leave out the columns
-// that the mask empties for a warp's sixteen rows.  fp32 throughout: the
-// operands' type leaves no other choice that keeps their precision.
+// One CTA per (h, 32 columns of v, b, segment of the row), chunks of 64 steps,
+// four warps.  Warp w forms, of the chunk's rows 16 w ... 16 w + 15,
+//   u = Q X,  S = Q K^T,  P = mask(S),  o = lead u + P V
+// and of the state's rows k its quarter of X = a^n X + K^T w V, which stays in
+// registers.  P does too: the layout in which the matrix instructions leave S is
+// the one in which they take P as a left operand, with the steps j of eight
+// taken in the order that ja, jb below give.  The columns that the mask empties
+// for all of a warp's rows are left out.
+//
+// Precision: the operands have 24 significant bits and the matrix instructions
+// take 11 (tf32), so each operand x is hi + lo, hi = x rounded to 11 bits, lo the
+// exact rest, of which the 11 leading bits count; x y is lo_x hi_y + hi_x lo_y +
+// hi_x hi_y in fp32, with an error of a few 2^-22 of the product at most.  (An
+// infinity has no such parts and gives NaN.)
+//
+// Why not on the CUDA cores: their operands come from shared memory for every
+// 4 x 4 block of products that a thread's registers hold, 16 bytes a lane and so
+// four cycles of the SM's 128 bytes each, and that bounded them: 271 us on
+// 8 x 1024 steps, 24 heads of 64/64, and 247 with two products an instruction.
+// A matrix instruction's operands are spread over the warp, an eighth of those
+// bytes: 167 us.  Taking the operands apart is half of the instructions, with ten
+// warps an SM to issue them (384 CTAs), and bounds it now; the tensor pipes are
+// 40 % busy.
+//
+// Rows of shared memory are 8 floats apart in the banks (K, Q, X: two floats a
+// lane of rows 0-3 and 4-7; V and K read across rows t, or ja and jb, and
+// eight columns), so that no access conflicts.
 constexpr int kC = 64;         // steps of a chunk
 constexpr int kB = 32;         // columns of v of a CTA
 constexpr int kThreads = 128;
 
 template <int DK, bool kStates>
-struct Simt {
-  static constexpr int LK = DK + 4;  // rows 16 bytes apart in the banks
-  static constexpr int LV = kC + 4;
-  // K and w V (twice); Q or P, V and X transposed
-  static constexpr int kFloats =
-      kC * LK + 2 * kC * kB + (kStates ? 0 : kC * LK + kB * LV + kB * LK);
+struct Walk32 {
+  static constexpr int LK = DK + 8;
+  static constexpr int LV = kB + 8;
+  static constexpr int kFloats = kC * LK + kC * LV + (kStates ? 0 : kC * LK + kB * LK);
   static constexpr size_t smem = kFloats * sizeof(float);
 };
 
-struct SimtWalk {
+struct Walk32Args {
   LaWalk w;
   int nseg, span;  // steps of a segment
 };
 
-__device__ __forceinline__ float4 ld4(const float* p) { return *(const float4*)p; }
 // 16 bytes, or zeros
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -69,68 +79,109 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
                "l"(src), "r"(in ? 16 : 0)
                : "memory");
 }
-// acc += l . r over four terms, even and odd ones apart
-__device__ __forceinline__ float2 dot4(float4 l, float4 r, float2 acc) {
-  return fma2(make_float2(l.x, l.y), make_float2(r.x, r.y),
-              fma2(make_float2(l.z, l.w), make_float2(r.z, r.w), acc));
-}
 
-// acc[a][e] += rows a of `left` . rows 8 e of `right`, terms [from, to)
-template <int LL, int LR>
-__device__ __forceinline__ void block4x4(const float* left, const float* right, int from, int to,
-                                         float2 (&acc)[4][4]) {
-#pragma unroll 2
-  for (int d = from; d < to; d += 4) {
-    float4 l[4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) l[a] = ld4(left + a * LL + d);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 r = ld4(right + 8 * e * LR + d);
-#pragma unroll
-      for (int a = 0; a < 4; ++a) acc[a][e] = dot4(l[a], r, acc[a][e]);
-    }
+// N operands of a lane as hi + lo
+template <int N>
+struct Parts {
+  uint32_t hi[N], lo[N];
+  __device__ __forceinline__ void set(int i, float x) {
+    hi[i] = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo[i] = __float_as_uint(x - __uint_as_float(hi[i]));
   }
+};
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// c[i] += a b[i] for N tiles, 16 x 8 times 8 x 8.  With g = lane / 4, t = lane %
+// 4: a holds rows g, g + 8 of terms t, then of terms t + 4; b terms t, t + 4 of
+// column g; c row g, columns 2 t and 2 t + 1, then row g + 8.  The tiles take
+// turns, since an instruction waits for the one before it on the same sum.
+//
+// The instructions round their sums toward zero, which over a long sum adds up
+// (2.6e-6 of the outputs after 1024 steps, where the plain form has 3e-7), so
+// theirs start from zero, the small terms first, and are added to c outside.
+template <int N>
+__device__ __forceinline__ void mma_fp32(float (*c)[4], const Parts<4>& a, const Parts<2> (&b)[N]) {
+  float d[N][4];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+    mma_tf32(d[i], a.lo, b[i].hi);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) mma_tf32(d[i], a.hi, b[i].lo);
+#pragma unroll
+  for (int i = 0; i < N; ++i) mma_tf32(d[i], a.hi, b[i].hi);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const float2 f = add2(make_float2(c[i][e], c[i][e + 1]), make_float2(d[i][e], d[i][e + 1]));
+      c[i][e] = f.x;
+      c[i][e + 1] = f.y;
+    }
+}
+// the same with the right operands of N tiles 8 rows apart at p: terms 2 t and
+// 2 t + 1 of a row
+template <int N>
+__device__ __forceinline__ void mma_rows(float (*c)[4], const Parts<4>& a, const float* p, int ld) {
+  Parts<2> b[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 f = *(const float2*)(p + 8 * i * ld);
+    b[i].set(0, f.x);
+    b[i].set(1, f.y);
+  }
+  mma_fp32<N>(c, a, b);
 }
 
 // kStates: only the state, each segment from zero, into w.last
 // [nseg][B][H][dv][dk].
 template <int DK, bool kStates>
-__global__ void __launch_bounds__(kThreads, DK == 64 ? 3 : 2)
-k_la_walk(const __grid_constant__ SimtWalk args) {
-  using G = Simt<DK, kStates>;
+__global__ void __launch_bounds__(kThreads, DK == 64 ? 4 : 2)
+k_la_walk(const __grid_constant__ Walk32Args args) {
+  using G = Walk32<DK, kStates>;
   constexpr int LK = G::LK, LV = G::LV;
+  constexpr int NX = DK / 32;  // eights of rows k of a warp
   const LaWalk& w = args.w;
   extern __shared__ __align__(16) float sm[];
   float* K = sm;
-  float* W = K + kC * LK;       // w V: [step][columns 4 tx, 4 tx + 1, then + 2, + 3][twice]
-  float* Q = W + 2 * kC * kB;   // P once the warp is done with its rows
-  float* V = Q + kC * LK;       // column 4 i + c in row i + 8 c
-  float* X = V + kB * LV;       // the same
+  float* V = K + kC * LK;
+  float* Q = V + kC * LV;
+  float* X = Q + kC * LK;  // [v][k]
   __shared__ float pw[kC + 2];
   const int vblocks = (w.dv + kB - 1) / kB;
   const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kB;
-  const int b = blockIdx.y, seg = blockIdx.z, t = threadIdx.x, tx = t & 7, ty = t >> 3, wp = t >> 5;
+  const int b = blockIdx.y, seg = blockIdx.z, t = threadIdx.x, wp = t >> 5;
+  const int g = (t & 31) >> 2, t4 = t & 3;
+  const int ja = 2 * t4 + (t4 >> 1), jb = 2 * t4 + 1 - (t4 >> 1);  // columns 2 t, 2 t + 1 of S
+  const int jg = g ^ (g >> 2);                                     // column g of S
   const float la = w.log_decay[h];
   int len = w.T;
   if (w.lens) len = min(max(w.lens[b], 0), w.T);
   if (t < kC + 2) pw[t] = decay_pow(la, (float)t);
   const int dv = min(kB, w.dv - v0);
   const size_t sbase = (((size_t)seg * w.B + b) * w.H + h) * w.dv * w.dk;
-  // state element (k, v) of this thread
+  // state element (k, v)
   auto state_at = [&](int k, int v) {
     return sbase + (!kStates && w.first_swapped ? (size_t)k * w.dv + v0 + v : (size_t)(v0 + v) * w.dk + k);
   };
-  float2 x[DK / 32][4];  // rows k = 4 ty + 2 (i & 1) + 64 (i >> 1) and the next
+  // x[m][i][c]: v = 16 m + g (+ 8 for c >= 2), k = kx + 8 i + 2 t4 (+ 1 for odd c)
+  const int kx = wp * (DK / 4);
+  float x[2][NX][4];
 #pragma unroll
-  for (int i = 0; i < DK / 32; ++i)
+  for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int k = 4 * ty + 2 * (i & 1) + (i >> 1) * 64, v = 4 * tx + c;
-      const bool in = !kStates && w.first && k < w.dk && v < dv;
-      x[i][c] = in ? make_float2(w.first[state_at(k, v)], w.first[state_at(k + 1, v)])
-                   : make_float2(0.f, 0.f);
-    }
+    for (int i = 0; i < NX; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int v = 16 * m + g + 8 * (c >> 1), k = kx + 8 * i + 2 * t4 + (c & 1);
+        x[m][i][c] = !kStates && w.first && k < w.dk && v < dv ? w.first[state_at(k, v)] : 0.f;
+      }
   const float* qp = (const float*)w.q.p + b * w.q.batch + (long long)(h / w.q.share) * w.dk;
   const float* kp = (const float*)w.k.p + b * w.k.batch + (long long)(h / w.k.share) * w.dk;
   const float* vp = (const float*)w.v.p + b * w.v.batch + (long long)(h / w.v.share) * w.dv + v0;
@@ -140,118 +191,128 @@ k_la_walk(const __grid_constant__ SimtWalk args) {
   for (int ci = 0; ci < nc; ++ci) {
     const int t0 = s0 + (w.reverse ? nc - 1 - ci : ci) * kC, n = min(kC, s1 - t0);
     __syncthreads();
+#pragma unroll 4
     for (int i = t; i < kC * (DK / 4); i += kThreads) {
       const int r = i / (DK / 4), d = i % (DK / 4) * 4;
       const bool in = r < n && d < w.dk;
       if (!kStates) copy16(Q + r * LK + d, in ? qp + (long long)(t0 + r) * w.q.step + d : qp, in);
       copy16(K + r * LK + d, in ? kp + (long long)(t0 + r) * w.k.step + d : kp, in);
     }
-    float4 v[kC * (kB / 4) / kThreads];
 #pragma unroll
-    for (int i = 0; i < kC * (kB / 4) / kThreads; ++i) {
-      const int r = (t + i * kThreads) / (kB / 4);
-      v[i] = r < n && 4 * tx < dv ? ld4(vp + (long long)(t0 + r) * w.v.step + 4 * tx)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = t; i < kC * (kB / 4); i += kThreads) {
+      const int r = i / (kB / 4), d = i % (kB / 4) * 4;
+      const bool in = r < n && d < dv;
+      copy16(V + r * LV + d, in ? vp + (long long)(t0 + r) * w.v.step + d : vp, in);
     }
     if (!kStates)
 #pragma unroll
-      for (int g = 0; g < DK / 64; ++g)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *(float4*)(X + (tx + 8 * c) * LK + 4 * ty + 64 * g) =
-              make_float4(x[2 * g][c].x, x[2 * g][c].y, x[2 * g + 1][c].x, x[2 * g + 1][c].y);
+        for (int i = 0; i < NX; ++i)
 #pragma unroll
-    for (int i = 0; i < kC * (kB / 4) / kThreads; ++i) {
-      const int r = (t + i * kThreads) / (kB / 4);
-      const float f = r < n ? w.s_inject * pw[(w.reverse ? r : n - 1 - r) + 1 - w.off] : 0.f;
-      const float4 y = make_float4(f * v[i].x, f * v[i].y, f * v[i].z, f * v[i].w);
-      *(float4*)(W + r * 2 * kB + 4 * tx) = make_float4(y.x, y.x, y.y, y.y);
-      *(float4*)(W + r * 2 * kB + kB + 4 * tx) = make_float4(y.z, y.z, y.w, y.w);
-      if (!kStates) {
-        V[tx * LV + r] = v[i].x;
-        V[(tx + 8) * LV + r] = v[i].y;
-        V[(tx + 16) * LV + r] = v[i].z;
-        V[(tx + 24) * LV + r] = v[i].w;
-      }
-    }
+          for (int u = 0; u < 2; ++u)
+            *(float2*)(X + (16 * m + g + 8 * u) * LK + kx + 8 * i + 2 * t4) =
+                make_float2(x[m][i][2 * u], x[m][i][2 * u + 1]);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (!kStates) {
-      float2 o[4][4];
-      auto clear = [](float2 (&acc)[4][4]) {
+      float o[4][4], s[8][4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+      for (int c = 0; c < 4; ++c) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][e] = make_float2(0.f, 0.f);
-      };
-      clear(o);
-      block4x4<LK, LK>(Q + 4 * ty * LK, X + tx * LK, 0, DK, o);
+        for (int i = 0; i < 4; ++i) o[i][c] = 0.f;
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int i = min(4 * ty + a, n - 1);  // (a row past the end is not written)
+        for (int j = 0; j < 8; ++j) s[j][c] = 0.f;
+      }
+      // 16 columns 16 j ... of S are needed by this warp
+      auto needed = [&](int j) { return w.reverse ? j >= wp : j <= wp; };
+      const float* qr = Q + (16 * wp + g) * LK + 2 * t4;
+#pragma unroll 2
+      for (int d = 0; d < DK; d += 8) {
+        const float2 q0 = *(const float2*)(qr + d), q1 = *(const float2*)(qr + 8 * LK + d);
+        Parts<4> a;
+        a.set(0, q0.x);
+        a.set(1, q1.x);
+        a.set(2, q0.y);
+        a.set(3, q1.y);
+        mma_rows<4>(o, a, X + g * LK + d + 2 * t4, LK);
+        const float* kr = K + jg * LK + d + 2 * t4;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          if (needed(j) && needed(j + 1)) mma_rows<4>(s + 2 * j, a, kr + 16 * j * LK, LK);
+          else if (needed(j)) mma_rows<2>(s + 2 * j, a, kr + 16 * j * LK, LK);
+          else if (needed(j + 1)) mma_rows<2>(s + 2 * j + 2, a, kr + 16 * (j + 1) * LK, LK);
+        }
+      }
+      const int i0 = 16 * wp + g;  // this lane's rows: i0, i0 + 8
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = min(i0 + 8 * u, n - 1);  // (a row past the end is not written)
         const float lead = w.s_carry * pw[(w.reverse ? n - 1 - i : i) + w.off];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[a][e] = make_float2(lead * (o[a][e].x + o[a][e].y), 0.f);
-      }
-      // groups of 32 columns (tx + 8 e) that the warp's rows 16 wp ... 16 wp + 15
-      // need: the diagonal one, and the one before (after) it for half of the warps
-      const int c0 = wp / 2;
-      const bool both = w.reverse ? c0 == 0 : c0 == 1;
-      float2 s[4][4];
-      float p[4][4];
-      if (both) {
-        clear(s);
-        block4x4<LK, LK>(Q + 4 * ty * LK, K + (tx + 32 * (1 - c0)) * LK, 0, DK, s);
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[a][e] = s[a][e].x + s[a][e].y;
-      }
-      clear(s);
-      block4x4<LK, LK>(Q + 4 * ty * LK, K + (tx + 32 * c0) * LK, 0, DK, s);
-      __syncwarp();  // (the rows of Q are the warp's own)
-      auto put = [&](int c, int a, int e, float f) {
-        const int i = 4 * ty + a, j = tx + 32 * c + 8 * e, d = w.reverse ? j - i : i - j;
-        Q[i * LK + j] = d >= 0 ? w.s_intra * pw[d] * f : 0.f;
-      };
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
         for (int e = 0; e < 4; ++e) {
-          put(c0, a, e, s[a][e].x + s[a][e].y);
-          if (both) put(1 - c0, a, e, p[a][e]);
+          o[e][2 * u] *= lead;
+          o[e][2 * u + 1] *= lead;
         }
-      __syncwarp();
-      block4x4<LK, LV>(Q + 4 * ty * LK, V + tx * LV, w.reverse ? 16 * wp : 0,
-                       w.reverse ? kC : 16 * wp + 16, o);
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int i = 4 * ty + a;
-        if (i < n && 4 * tx < dv)
-          *(float4*)(op + (long long)(t0 + i) * w.H * w.dv + 4 * tx) =
-              make_float4(o[a][0].x + o[a][0].y, o[a][1].x + o[a][1].y, o[a][2].x + o[a][2].y,
-                          o[a][3].x + o[a][3].y);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (needed(j >> 1)) {
+          Parts<4> a;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = i0 + 8 * (c >> 1), col = 8 * j + (c & 1 ? jb : ja);
+            const int d = w.reverse ? col - i : i - col;
+            a.set((c >> 1) + 2 * (c & 1), d >= 0 ? w.s_intra * pw[d] * s[j][c] : 0.f);
+          }
+          const float *va = V + (8 * j + ja) * LV + g, *vb = V + (8 * j + jb) * LV + g;
+          Parts<2> v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e].set(0, va[8 * e]);
+            v[e].set(1, vb[8 * e]);
+          }
+          mma_fp32<4>(o, a, v);
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (i0 + 8 * u < n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (8 * e < dv)
+              *(float2*)(op + (long long)(t0 + i0 + 8 * u) * w.H * w.dv + 8 * e + 2 * t4) =
+                  make_float2(o[e][2 * u], o[e][2 * u + 1]);
     }
-    const float2 an = make_float2(pw[n], pw[n]);
+    const float an = pw[n];
 #pragma unroll
-    for (int i = 0; i < DK / 32; ++i)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[i][c] = mul2(x[i][c], an);
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const float4 ya = ld4(W + j * 2 * kB + 4 * tx), yb = ld4(W + j * 2 * kB + kB + 4 * tx);
-      const float2 y[4] = {make_float2(ya.x, ya.y), make_float2(ya.z, ya.w),
-                           make_float2(yb.x, yb.y), make_float2(yb.z, yb.w)};
+      for (int i = 0; i < NX; ++i)
 #pragma unroll
-      for (int g = 0; g < DK / 64; ++g) {
-        const float4 k = ld4(K + j * LK + 4 * ty + 64 * g);
+        for (int c = 0; c < 4; ++c) x[m][i][c] *= an;
+#pragma unroll 2
+    for (int j = 0; j < n; j += 8) {  // (rows past n are zero)
+      Parts<4> a[2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[2 * g][c] = fma2(make_float2(k.x, k.y), y[c], x[2 * g][c]);
-          x[2 * g + 1][c] = fma2(make_float2(k.z, k.w), y[c], x[2 * g + 1][c]);
+      for (int u = 0; u < 2; ++u) {
+        const int r = j + t4 + 4 * u;
+        const float f = w.s_inject * pw[max(w.reverse ? r : n - 1 - r, 0) + 1 - w.off];
+        const float* vr = V + r * LV + g;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          a[m].set(2 * u, f * vr[16 * m]);
+          a[m].set(2 * u + 1, f * vr[16 * m + 8]);
         }
       }
+      const float* kr = K + (j + t4) * LK + kx + g;
+      Parts<2> k[NX];
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        k[i].set(0, kr[8 * i]);
+        k[i].set(1, kr[4 * LK + 8 * i]);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) mma_fp32<NX>(x[m], a[m], k);
     }
   }
   if (!kStates) {  // past the row's end
@@ -263,15 +324,14 @@ k_la_walk(const __grid_constant__ SimtWalk args) {
   }
   if (w.last)
 #pragma unroll
-    for (int i = 0; i < DK / 32; ++i)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int k = 4 * ty + 2 * (i & 1) + (i >> 1) * 64, v = 4 * tx + c;
-        if (k < w.dk && v < dv) {
-          w.last[state_at(k, v)] = x[i][c].x;
-          w.last[state_at(k + 1, v)] = x[i][c].y;
+      for (int i = 0; i < NX; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int v = 16 * m + g + 8 * (c >> 1), k = kx + 8 * i + 2 * t4 + (c & 1);
+          if (k < w.dk && v < dv) w.last[state_at(k, v)] = x[m][i][c];
         }
-      }
 }
 
 // The states before each segment from the segments' own: in walk order
@@ -307,8 +367,8 @@ __global__ void __launch_bounds__(256) k_la_segments(const LaSegments p) {
 }
 
 template <int DK, bool kStates>
-cudaError_t walk_t(const SimtWalk& a, cudaStream_t s) {
-  constexpr int smem = (int)Simt<DK, kStates>::smem;
+cudaError_t walk_t(const Walk32Args& a, cudaStream_t s) {
+  constexpr int smem = (int)Walk32<DK, kStates>::smem;
   cudaError_t e = cudaFuncSetAttribute(k_la_walk<DK, kStates>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -469,25 +529,25 @@ cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// CTAs of the fp32 walk that run at once on 152 SMs (three of 69 KB, or two of 110)
-static int simt_segments(int B, int H, int T, int dk, int dv) {
+// CTAs of the fp32 walk that run at once on 152 SMs (four of 56 KB, or two of 97)
+static int segments32(int B, int H, int T, int dk, int dv) {
   return la_segments((long long)B * H * ((dv + kB - 1) / kB), (T + kC - 1) / kC,
-                     dk <= 64 ? 456 : 304);
+                     dk <= 64 ? 608 : 304);
 }
 
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16) {
   if (bf16) return la_tc_scratch_floats(B, H, T, dk, dv);
   // (the walks of a backward pass have dk and dv in either order)
-  const int a = simt_segments(B, H, T, dk, dv), b = simt_segments(B, H, T, dv, dk), n = a > b ? a : b;
+  const int a = segments32(B, H, T, dk, dv), b = segments32(B, H, T, dv, dk), n = a > b ? a : b;
   return n > 1 ? (size_t)n * B * H * dk * dv : 0;
 }
 
 cudaError_t la_walk(const LaWalk& w, bool bf16, bool beside, float* scratch, cudaStream_t s) {
   if (bf16) return la_walk_tc(w, beside, scratch, s);
-  SimtWalk a;
+  Walk32Args a;
   a.w = w;
   const int nc = (w.T + kC - 1) / kC;
-  int n = simt_segments(w.B, w.H, w.T, w.dk, w.dv);
+  int n = segments32(w.B, w.H, w.T, w.dk, w.dv);
   a.span = (nc + n - 1) / n * kC;
   n = (w.T + a.span - 1) / a.span;
   a.nseg = n;

@@ -26,6 +26,10 @@
 // and Oc, and of U.  128 columns of v are two CTAs, which read q
 // and k twice (from L2) and form S twice: at 64 columns the accumulators leave
 // room for P beside S, so that S of the next chunk does not wait for P V.
+// Measured: 2.5 us a chunk at dk = 128, of which 1.6 us remain with the work
+// taken out, the hand-overs between the warps; 46 us for 4 x 2048 steps of 32
+// heads 128/64 (66 % of the copy rate, 128 CTAs on 152 SMs), 87 % for 4 x 8192
+// steps of 38 heads.
 //
 // Rows past the end of a batch row (its length, or T) take part as zeros: TMA
 // fills what lies past T; between a shorter row's end and T warps 0-7 clear
@@ -796,7 +800,10 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 // share v and do in L2).  Warps as in the walk: 0-7 turn T = A B^T into P, in
 // place, 8-15 form lead o A and write out of the unit before, one each loads,
 // forms T and accumulates; two stages of items, two of C and two of out keep them
-// apart.  Per item 48 KB are loaded and 1430 cycles of products issued.
+// apart.  Per item 48 KB are loaded and 1430 cycles of products issued.  Measured
+// (128/64): 89 us for 4 x 2048 steps, 32 heads of their own q and k, of 169 for
+// all gradients (three walks: 183); 233 us for 2 x 8192 steps, 64 heads in 8
+// groups, of 476 (walks of every head with a kernel for the sums: 876).
 struct Grad {
   int B, T, H, dk, dv, share, nc;  // heads of a group, chunks of a row
   const float* log_decay;

@@ -1,7 +1,8 @@
 """Python front end of the layer operators: linear attention with a decay for
-each head, norms around a block, gradient clipping.  Torch CUDA tensors in, torch tensors out; every step runs in the
-library's kernels behind the C ABI (include/ssd.h), on `stream` or the current
-stream.
+each head, norms around a block, gradient clipping.  Torch CUDA tensors in, torch
+tensors out; every step runs in the library's kernels behind the C ABI
+(include/ssd.h), on `stream` or the current stream.  A call on another stream
+than the current one starts after the work that is on the current one.
 """
 from __future__ import annotations
 
@@ -48,12 +49,17 @@ def _stream_handle(stream, dev):
 
 
 def _keep(stream, *tensors):
-    """Memory that a call made on the current stream and uses on another one
-    is not handed out again before that other stream is done with it."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    """Orders a call on another stream than the current one, where its memory
+    was allocated: that memory may have belonged to a tensor that work already
+    on the current stream still uses, so the call comes after that work; and it
+    is not handed out again before the other stream is done with it."""
+    if stream is not None:
+        current = torch.cuda.current_stream()
+        if stream != current:
+            stream.wait_stream(current)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
 
 class _Layouts(dict):

@@ -148,6 +148,24 @@ def test_equal_runs_on_another_stream():
     assert torch.equal(n1, n2) and all(torch.equal(a, b) for a, b in zip(o1, o2))
 
 
+def test_another_stream_starts_after_the_current_one():
+    """The call's memory comes from the current stream's allocator, whose earlier
+    work may still use it: here that work also writes the gradients."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    big = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    ts = [torch.zeros(1000, device="cuda") for _ in range(3)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(20):
+        big.fill_(i)
+    for t in ts:
+        t.fill_(2.0)
+    n = ssd.clip_grad_norm(ts, 1e9, stream=side)
+    torch.cuda.synchronize()
+    assert abs(float(n) - 2 * 3000 ** 0.5) < 1e-4
+
+
 def test_refusals():
     import torch
     import state_space_model_analytic_gb300 as ssd

@@ -29,13 +29,15 @@ __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f 
 // ---- the walk in fp32 -----------------------------------------------------------
 //
 // One CTA per (h, 32 columns of v, b, segment of the row), chunks of 64 steps,
-// four warps.  Warp w forms, of the chunk's rows 16 w ... 16 w + 15,
+// eight warps.  Of rows 16 w ... 16 w + 15 of a chunk, two warps form
 //   u = Q X,  S = Q K^T,  P = mask(S),  o = lead u + P V
-// and of the state's rows k its quarter of X = a^n X + K^T w V, which stays in
-// registers.  P does too: the layout in which the matrix instructions leave S is
-// the one in which they take P as a left operand, with the steps j of eight
-// taken in the order that ja, jb below give.  The columns that the mask empties
-// for all of a warp's rows are left out.
+// each for every other eight columns of S and 16 columns of u, and add up the
+// halves of P V; and of the state's rows k a quarter, 16 columns of v each, of X =
+// a^n X + K^T w V, which stays in registers.  P does too: the layout in which the
+// matrix instructions leave S is the one in which they take P as a left operand,
+// with the steps j of eight taken in the order that ja, jb below give.  Columns
+// that the mask empties for all of a warp's rows are left out; a scheduler's two
+// warps have rows w and 3 - w, with as many such columns together.
 //
 // Precision: the operands have 24 significant bits and the matrix instructions
 // take 11 (tf32), so each operand x is hi + lo, hi = x rounded to 11 bits, lo the
@@ -48,16 +50,19 @@ __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f 
 // four cycles of the SM's 128 bytes each, and that bounded them: 271 us on
 // 8 x 1024 steps, 24 heads of 64/64, and 247 with two products an instruction.
 // A matrix instruction's operands are spread over the warp, an eighth of those
-// bytes: 167 us.  Taking the operands apart is half of the instructions, with ten
-// warps an SM to issue them (384 CTAs), and bounds it now; the tensor pipes are
-// 40 % busy.
+// bytes: 170 us.  No one unit bounds it now: taking operands apart is half of the
+// instructions (they fill 58 % of the issue slots), the matrix pipes are 43 %
+// busy, and 384 CTAs put three on some SMs and two on others.  Four warps a CTA
+// that form whole rows took 168 us, but 346 us instead of 310 for heads of
+// 128/64, where fewer CTAs fit an SM, and 18.5 instead of 14.6 for 4 x 1000
+// steps of 3 heads of 32/32.
 //
 // Rows of shared memory are 8 floats apart in the banks (K, Q, X: two floats a
 // lane of rows 0-3 and 4-7; V and K read across rows t, or ja and jb, and
 // eight columns), so that no access conflicts.
 constexpr int kC = 64;         // steps of a chunk
 constexpr int kB = 32;         // columns of v of a CTA
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 
 template <int DK, bool kStates>
 struct Walk32 {
@@ -90,11 +95,14 @@ struct Parts {
   }
 };
 
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+// d = a b + c
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2],
+                                         float c0, float c1, float c2, float c3) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
-      " {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+      " {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1),
+        "f"(c2), "f"(c3));
 }
 // c[i] += a b[i] for N tiles, 16 x 8 times 8 x 8.  With g = lane / 4, t = lane %
 // 4: a holds rows g, g + 8 of terms t, then of terms t + 4; b terms t, t + 4 of
@@ -108,14 +116,11 @@ template <int N>
 __device__ __forceinline__ void mma_fp32(float (*c)[4], const Parts<4>& a, const Parts<2> (&b)[N]) {
   float d[N][4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
-    mma_tf32(d[i], a.lo, b[i].hi);
-  }
+  for (int i = 0; i < N; ++i) mma_tf32(d[i], a.lo, b[i].hi, 0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) mma_tf32(d[i], a.hi, b[i].lo);
+  for (int i = 0; i < N; ++i) mma_tf32(d[i], a.hi, b[i].lo, d[i][0], d[i][1], d[i][2], d[i][3]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) mma_tf32(d[i], a.hi, b[i].hi);
+  for (int i = 0; i < N; ++i) mma_tf32(d[i], a.hi, b[i].hi, d[i][0], d[i][1], d[i][2], d[i][3]);
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -125,14 +130,14 @@ __device__ __forceinline__ void mma_fp32(float (*c)[4], const Parts<4>& a, const
       c[i][e + 1] = f.y;
     }
 }
-// the same with the right operands of N tiles 8 rows apart at p: terms 2 t and
-// 2 t + 1 of a row
+// the same with the right operands of N tiles `step` floats apart at p: terms 2 t
+// and 2 t + 1 of a row
 template <int N>
-__device__ __forceinline__ void mma_rows(float (*c)[4], const Parts<4>& a, const float* p, int ld) {
+__device__ __forceinline__ void mma_rows(float (*c)[4], const Parts<4>& a, const float* p, int step) {
   Parts<2> b[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float2 f = *(const float2*)(p + 8 * i * ld);
+    const float2 f = *(const float2*)(p + i * step);
     b[i].set(0, f.x);
     b[i].set(1, f.y);
   }
@@ -142,11 +147,12 @@ __device__ __forceinline__ void mma_rows(float (*c)[4], const Parts<4>& a, const
 // kStates: only the state, each segment from zero, into w.last
 // [nseg][B][H][dv][dk].
 template <int DK, bool kStates>
-__global__ void __launch_bounds__(kThreads, DK == 64 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, DK == 64 ? 3 : 2)
 k_la_walk(const __grid_constant__ Walk32Args args) {
   using G = Walk32<DK, kStates>;
   constexpr int LK = G::LK, LV = G::LV;
   constexpr int NX = DK / 32;  // eights of rows k of a warp
+  constexpr int LE = 24;
   const LaWalk& w = args.w;
   extern __shared__ __align__(16) float sm[];
   float* K = sm;
@@ -156,7 +162,8 @@ k_la_walk(const __grid_constant__ Walk32Args args) {
   __shared__ float pw[kC + 2];
   const int vblocks = (w.dv + kB - 1) / kB;
   const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kB;
-  const int b = blockIdx.y, seg = blockIdx.z, t = threadIdx.x, wp = t >> 5;
+  const int b = blockIdx.y, seg = blockIdx.z, t = threadIdx.x;
+  const int half = t >> 7, wp = half ? 3 - (t >> 5 & 3) : t >> 5;
   const int g = (t & 31) >> 2, t4 = t & 3;
   const int ja = 2 * t4 + (t4 >> 1), jb = 2 * t4 + 1 - (t4 >> 1);  // columns 2 t, 2 t + 1 of S
   const int jg = g ^ (g >> 2);                                     // column g of S
@@ -170,18 +177,16 @@ k_la_walk(const __grid_constant__ Walk32Args args) {
   auto state_at = [&](int k, int v) {
     return sbase + (!kStates && w.first_swapped ? (size_t)k * w.dv + v0 + v : (size_t)(v0 + v) * w.dk + k);
   };
-  // x[m][i][c]: v = 16 m + g (+ 8 for c >= 2), k = kx + 8 i + 2 t4 (+ 1 for odd c)
-  const int kx = wp * (DK / 4);
-  float x[2][NX][4];
+  // x[i][c]: v = vx (+ 8 for c >= 2), k = kx + 8 i (+ 1 for odd c)
+  const int vx = 16 * half + g, kx = wp * (DK / 4) + 2 * t4;
+  float x[NX][4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int i = 0; i < NX; ++i)
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int v = 16 * m + g + 8 * (c >> 1), k = kx + 8 * i + 2 * t4 + (c & 1);
-        x[m][i][c] = !kStates && w.first && k < w.dk && v < dv ? w.first[state_at(k, v)] : 0.f;
-      }
+    for (int c = 0; c < 4; ++c) {
+      const int v = vx + 8 * (c >> 1), k = kx + 8 * i + (c & 1);
+      x[i][c] = !kStates && w.first && k < w.dk && v < dv ? w.first[state_at(k, v)] : 0.f;
+    }
   const float* qp = (const float*)w.q.p + b * w.q.batch + (long long)(h / w.q.share) * w.dk;
   const float* kp = (const float*)w.k.p + b * w.k.batch + (long long)(h / w.k.share) * w.dk;
   const float* vp = (const float*)w.v.p + b * w.v.batch + (long long)(h / w.v.share) * w.dv + v0;
@@ -206,25 +211,21 @@ k_la_walk(const __grid_constant__ Walk32Args args) {
     }
     if (!kStates)
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int i = 0; i < NX; ++i)
 #pragma unroll
-        for (int i = 0; i < NX; ++i)
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            *(float2*)(X + (16 * m + g + 8 * u) * LK + kx + 8 * i + 2 * t4) =
-                make_float2(x[m][i][2 * u], x[m][i][2 * u + 1]);
+        for (int u = 0; u < 2; ++u)
+          *(float2*)(X + (vx + 8 * u) * LK + kx + 8 * i) = make_float2(x[i][2 * u], x[i][2 * u + 1]);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (!kStates) {
-      float o[4][4], s[8][4];
+      // o[0], o[1]: columns 16 half ... of o, which this warp writes; o[2], o[3]:
+      // the other half's.  s[j]: columns 16 j + 8 half ... of S
+      float o[4][4], s[4][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i][c] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j][c] = 0.f;
-      }
-      // 16 columns 16 j ... of S are needed by this warp
+        for (int c = 0; c < 4; ++c) o[i][c] = s[i][c] = 0.f;
+      // columns 16 j ... of S are needed by this warp
       auto needed = [&](int j) { return w.reverse ? j >= wp : j <= wp; };
       const float* qr = Q + (16 * wp + g) * LK + 2 * t4;
 #pragma unroll 2
@@ -235,13 +236,13 @@ k_la_walk(const __grid_constant__ Walk32Args args) {
         a.set(1, q1.x);
         a.set(2, q0.y);
         a.set(3, q1.y);
-        mma_rows<4>(o, a, X + g * LK + d + 2 * t4, LK);
-        const float* kr = K + jg * LK + d + 2 * t4;
+        mma_rows<2>(o, a, X + vx * LK + d + 2 * t4, 8 * LK);
+        const float* kr = K + (8 * half + jg) * LK + d + 2 * t4;
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-          if (needed(j) && needed(j + 1)) mma_rows<4>(s + 2 * j, a, kr + 16 * j * LK, LK);
-          else if (needed(j)) mma_rows<2>(s + 2 * j, a, kr + 16 * j * LK, LK);
-          else if (needed(j + 1)) mma_rows<2>(s + 2 * j + 2, a, kr + 16 * (j + 1) * LK, LK);
+          if (needed(j) && needed(j + 1)) mma_rows<2>(s + j, a, kr + 16 * j * LK, 16 * LK);
+          else if (needed(j)) mma_rows<1>(s + j, a, kr + 16 * j * LK, 0);
+          else if (needed(j + 1)) mma_rows<1>(s + j + 1, a, kr + 16 * (j + 1) * LK, 0);
         }
       }
       const int i0 = 16 * wp + g;  // this lane's rows: i0, i0 + 8
@@ -250,69 +251,80 @@ k_la_walk(const __grid_constant__ Walk32Args args) {
         const int i = min(i0 + 8 * u, n - 1);  // (a row past the end is not written)
         const float lead = w.s_carry * pw[(w.reverse ? n - 1 - i : i) + w.off];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           o[e][2 * u] *= lead;
           o[e][2 * u + 1] *= lead;
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (needed(j >> 1)) {
+      for (int j = 0; j < 4; ++j)
+        if (needed(j)) {
+          const int j0 = 16 * j + 8 * half;
           Parts<4> a;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int i = i0 + 8 * (c >> 1), col = 8 * j + (c & 1 ? jb : ja);
+            const int i = i0 + 8 * (c >> 1), col = j0 + (c & 1 ? jb : ja);
             const int d = w.reverse ? col - i : i - col;
             a.set((c >> 1) + 2 * (c & 1), d >= 0 ? w.s_intra * pw[d] * s[j][c] : 0.f);
           }
-          const float *va = V + (8 * j + ja) * LV + g, *vb = V + (8 * j + jb) * LV + g;
-          Parts<2> v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e].set(0, va[8 * e]);
-            v[e].set(1, vb[8 * e]);
+          for (int u = 0; u < 2; ++u) {
+            const int v = 16 * (u ? 1 - half : half) + g;
+            const float *va = V + (j0 + ja) * LV + v, *vb = V + (j0 + jb) * LV + v;
+            Parts<2> p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              p[e].set(0, va[8 * e]);
+              p[e].set(1, vb[8 * e]);
+            }
+            mma_fp32<2>(o + 2 * u, a, p);
           }
-          mma_fp32<4>(o, a, v);
         }
+      // the halves' sums, exchanged in place of the rows of Q (the two warps')
+      float* E = Q + 16 * wp * LK + g * LE + 2 * t4;
+      auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + wp) : "memory"); };
+      pair_sync();
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          *(float2*)(E + (16 * half + 8 * u) * LE + 8 * e) = make_float2(o[2 + e][2 * u], o[2 + e][2 * u + 1]);
+      pair_sync();
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (i0 + 8 * u < n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (8 * e < dv)
-              *(float2*)(op + (long long)(t0 + i0 + 8 * u) * w.H * w.dv + 8 * e + 2 * t4) =
-                  make_float2(o[e][2 * u], o[e][2 * u + 1]);
+          for (int e = 0; e < 2; ++e)
+            if (16 * half + 8 * e < dv) {
+              const float2 f = *(const float2*)(E + (16 * (1 - half) + 8 * u) * LE + 8 * e);
+              *(float2*)(op + (long long)(t0 + i0 + 8 * u) * w.H * w.dv + 16 * half + 8 * e + 2 * t4) =
+                  make_float2(o[e][2 * u] + f.x, o[e][2 * u + 1] + f.y);
+            }
     }
     const float an = pw[n];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int i = 0; i < NX; ++i)
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[m][i][c] *= an;
+      for (int c = 0; c < 4; ++c) x[i][c] *= an;
 #pragma unroll 2
     for (int j = 0; j < n; j += 8) {  // (rows past n are zero)
-      Parts<4> a[2];
+      Parts<4> a;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int r = j + t4 + 4 * u;
         const float f = w.s_inject * pw[max(w.reverse ? r : n - 1 - r, 0) + 1 - w.off];
-        const float* vr = V + r * LV + g;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          a[m].set(2 * u, f * vr[16 * m]);
-          a[m].set(2 * u + 1, f * vr[16 * m + 8]);
-        }
+        const float* vr = V + r * LV + vx;
+        a.set(2 * u, f * vr[0]);
+        a.set(2 * u + 1, f * vr[8]);
       }
-      const float* kr = K + (j + t4) * LK + kx + g;
+      const float* kr = K + (j + t4) * LK + wp * (DK / 4) + g;
       Parts<2> k[NX];
 #pragma unroll
       for (int i = 0; i < NX; ++i) {
         k[i].set(0, kr[8 * i]);
         k[i].set(1, kr[4 * LK + 8 * i]);
       }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) mma_fp32<NX>(x[m], a[m], k);
+      mma_fp32<NX>(x, a, k);
     }
   }
   if (!kStates) {  // past the row's end
@@ -324,14 +336,12 @@ k_la_walk(const __grid_constant__ Walk32Args args) {
   }
   if (w.last)
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int i = 0; i < NX; ++i)
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int v = 16 * m + g + 8 * (c >> 1), k = kx + 8 * i + 2 * t4 + (c & 1);
-          if (k < w.dk && v < dv) w.last[state_at(k, v)] = x[m][i][c];
-        }
+      for (int c = 0; c < 4; ++c) {
+        const int v = vx + 8 * (c >> 1), k = kx + 8 * i + (c & 1);
+        if (k < w.dk && v < dv) w.last[state_at(k, v)] = x[i][c];
+      }
 }
 
 // The states before each segment from the segments' own: in walk order
@@ -529,10 +539,10 @@ cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// CTAs of the fp32 walk that run at once on 152 SMs (four of 56 KB, or two of 97)
+// CTAs of the fp32 walk that run at once on 152 SMs (three, or two for dk > 64)
 static int segments32(int B, int H, int T, int dk, int dv) {
   return la_segments((long long)B * H * ((dv + kB - 1) / kB), (T + kC - 1) / kC,
-                     dk <= 64 ? 608 : 304);
+                     dk <= 64 ? 456 : 304);
 }
 
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16) {

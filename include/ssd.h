@@ -266,15 +266,18 @@ typedef struct {
  * always (the states before every 128 steps). */
 SSD_API size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* dims, int which);
 
-/* state0, lens, state (the final state) may be NULL; state may be state0. */
+/* state0, lens, state (the final state) may be NULL; state may be state0, o
+ * must not overlap an input.  A step's infinite or NaN operands reach the steps
+ * before it in its chunk too (of 128 steps, or 64 in fp32). */
 SSD_API int ssd_linattn_forward(const ssd_linattn_dims* dims, const void* q, const void* k,
                                 const void* v, const float* log_decay, const float* state0,
                                 const int32_t* lens, void* o, float* state,
                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /* Gradients of L = sum(dout * o) + sum(dstate * state); dstate NULL = zero.
- * state0, lens, dstate0 may be NULL.  Past a row's length the gradients are
- * zero.  A group's dq and dk are summed over its heads in head order. */
+ * state0, lens, dstate0 may be NULL; no output may overlap an input.  Past a
+ * row's length the gradients are zero.  A group's dq and dk are summed over its
+ * heads in head order. */
 SSD_API int ssd_linattn_backward(const ssd_linattn_dims* dims, const void* q, const void* k,
                                  const void* v, const float* log_decay, const float* state0,
                                  const void* dout, const float* dstate, const int32_t* lens,

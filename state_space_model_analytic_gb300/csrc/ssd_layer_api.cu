@@ -1,7 +1,6 @@
-// C ABI of the layer operators (linear attention, norms around a block,
-// gradient clipping): argument validation,
-// workspace carve-up and the launches of each call.  Declarations and
-// contracts: include/ssd.h.
+// C ABI of the layer operators (linear attention, norms around a block, gradient
+// clipping): argument validation, workspace carve-up and the launches of each
+// call.  Declarations and contracts: include/ssd.h.
 #include <cstdarg>
 #include <cstdio>
 #include <new>

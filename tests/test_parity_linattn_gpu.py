@@ -84,6 +84,10 @@ CASES = [
     # enough steps for a row to be shared out
     (1, 4100, 1, 1, 64, 64, "bf16", None, (-0.002,)),
     (1, 3000, 2, 1, 128, 128, "bf16", (2999,), (-0.001, -0.3)),
+    # fp32: columns of v and rows k that end inside a warp's share, shared out rows
+    (3, 190, 4, 2, 80, 40, "f32", (190, 65, 129), (-0.01, -0.4, -5.0, 0.0)),
+    (2, 2100, 2, 1, 128, 96, "f32", (2100, 1999), (-0.003, -0.05)),
+    (1, 1500, 1, 1, 24, 72, "f32", None, (-0.002,)),
 ]
 ids = [f"b{c[0]}t{c[1]}h{c[2]}g{c[3]}k{c[4]}v{c[5]}{c[6]}{'lens' if c[7] else ''}" for c in CASES]
 
@@ -184,6 +188,20 @@ def test_views_of_one_projection():
     g1 = ssd.linattn_backward(q, k, v, la, None, do)
     g2 = ssd.linattn_backward(*views, la, None, dop)
     assert all(torch.equal(g1[n], g2[n]) for n in g1)
+
+
+def test_fp32_sums_keep_their_bits():
+    """Rounding errors of fp32 products and sums are of either sign and add up as
+    their squares do: an output's error stays at a few 2^-24 of the outputs'
+    size however many terms it has.  Roundings of one direction (or operands
+    of fewer bits) add up to tens of them over a thousand steps."""
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.linattn_inputs(2, 1024, 3, 3, 64, 64, "f32", 7, (-0.002, -0.004, -0.03))
+    ro, rS = linattn.forward(inp["q"], inp["k"], inp["v"], inp["log_decay"], inp["state0"], 1.0, None)
+    o, S = ssd.linattn_forward(*(dev(inp[x]) for x in ("q", "k", "v", "log_decay", "state0")))
+    for got, ref in ((host(o), ro), (host(S), rS)):
+        err = np.sqrt(np.mean((got - ref) ** 2) / np.mean(ref ** 2))
+        assert err <= 8 * 2.0 ** -24, err
 
 
 def test_two_runs_are_equal_and_streams_are_followed():

@@ -43,7 +43,8 @@ __device__ __forceinline__ float decay_pow(float la, float e) { return e == 0.f 
 // take 11 (tf32), so each operand x is hi + lo, hi = x rounded to 11 bits, lo the
 // exact rest, of which the 11 leading bits count; x y is lo_x hi_y + hi_x lo_y +
 // hi_x hi_y in fp32, with an error of a few 2^-22 of the product at most.  (An
-// infinity has no such parts and gives NaN.)
+// infinity, or a number that rounds to one in 11 bits, has no such parts and gives
+// NaN; below 2^-102 or so lo loses bits to fp32's smallest numbers.)
 //
 // Why not on the CUDA cores: their operands come from shared memory for every
 // 4 x 4 block of products that a thread's registers hold, 16 bytes a lane and so

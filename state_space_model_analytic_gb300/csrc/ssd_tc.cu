@@ -393,11 +393,12 @@ k_state_scan_tc(const __grid_constant__ ScanStateMaps maps, TcDims d, const floa
         tma_load_2d(st + Q * 128, &maps.v, g * d.N + 64, row0, &bar_load[k]);
         tma_load_2d(st + 2 * Q * 128, &maps.u, h * d.P, row0, &bar_load[k]);
       };
-      // the first tiles are inputs that no kernel of this library writes: they
-      // are fetched before waiting for the kernel launched ahead of this one
+      // This is the first kernel of a call: its inputs may be what the kernel
+      // ahead of it on the stream is still writing (a layer's dx is the next
+      // one's dy), so that even the first tiles come after the wait.
+      grid_dep_wait();
       issue(0);
       if (nc > 1) issue(1);
-      grid_dep_wait();
       int loads_issued = nc > 1 ? 2 : 1, mma_issued = 0;
       const uint32_t idesc = idesc_bf16(128, 64, true, true);
       for (int it = 0; it < nc; ++it) {
@@ -728,8 +729,9 @@ k_fwd_scan_tc(const __grid_constant__ ScanMaps maps, TcDims d, const float* __re
     tma_load_2d(sX, &maps.x, h * d.P, row0, &bar_load);
   };
   const int crow = b * d.T + c * Q;
-  // C, B, x are inputs that no kernel of this library writes: fetched before
-  // waiting for the kernel launched ahead of this one; the states after
+  // C, B, x are inputs of the call, and a kernel of the call ahead of this one
+  // has waited for whatever wrote them: fetched before waiting for that kernel;
+  // the states after
   if (tid == 0) issue_loads(crow);
   grid_dep_wait();
 
@@ -2321,6 +2323,9 @@ cudaError_t set_smem_tc(K kernel, size_t bytes) {
 // Launch with programmatic stream serialization: the kernel may start while
 // the kernel ahead of it on the stream finishes; it waits for that kernel
 // (griddepcontrol.wait) before touching anything the earlier kernels write.
+// For the first kernel of a call that is everything, inputs too: the kernel
+// ahead may belong to a call whose outputs they are.  A kernel lets the next
+// one start (griddepcontrol.launch_dependents) only after its own wait.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args... args) {

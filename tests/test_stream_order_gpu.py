@@ -1,0 +1,55 @@
+"""Calls on one stream read what the calls before them write, without a
+synchronisation between them, wherever a kernel may start before the kernel
+ahead of it has ended."""
+import pytest
+
+from state_space_model_analytic_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from state_space_model_analytic_gb300 import build
+    build()
+
+
+def core(T, seed):
+    """Inputs of the core at a size whose state scans are fused (128 heads over
+    all rows), as device tensors by name."""
+    import torch
+    inp = synth.make_inputs(synth.Dims(4, T, 32, 64, 128, 1, 256, "bf16"), seed, True, "softplus")
+    t = {n: torch.from_numpy(inp[n]).float().cuda() for n in ("x", "dt", "A", "B", "C", "D", "h0", "dy")}
+    for n in ("x", "B", "C", "dy"):
+        t[n] = t[n].bfloat16()
+    return t
+
+
+def args(t, **other):
+    return [other.get(n, t[n]) for n in ("x", "dt", "A", "B", "C", "D", "h0")]
+
+
+@pytest.mark.parametrize("history", [False, True])
+def test_two_layers_backward(history):
+    """The upper layer's dx is the lower layer's dy."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    up, low = core(1024, 1), core(1024, 2)
+    cs = [ssd.forward(*args(t), chunk=256)[2] if history else None for t in (up, low)]
+
+    def chain(synchronise, dx):
+        dx.fill_(7.0)
+        g = ssd.backward(*args(up), up["dy"], cs[0], chunk=256, out={"dx": dx})
+        if synchronise:
+            torch.cuda.synchronize()
+        return ssd.backward(*args(low), g["dx"], cs[1], chunk=256)
+
+    dx = torch.empty_like(up["x"])
+    want = chain(True, dx)
+    for _ in range(5):
+        got = chain(False, dx)
+        for n in want:
+            assert torch.equal(got[n], want[n]), n

@@ -276,6 +276,7 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
     // with the states before every chunk, backward and forward, dq and dk are
     // sums over chunks and a group's heads that need no walk
     w.hist = rest + la_hist_bytes(d);
+    w.followed = true;
     LaWalk f = la_base(d, log_decay, lens);
     f.dk = (int)d->dk;
     f.dv = (int)d->dv;

@@ -35,6 +35,7 @@ struct LaWalk {
   float s_intra, s_carry, s_inject;
   int off;
   bool reverse;
+  bool followed;          // the next launch on the stream is a walk `beside` this one
   void* hist;             // bf16 walks: the states before every chunk (la_tc_hist_rows rows of
                           // 64), nullable; with it o may be NULL (the states alone)
 };

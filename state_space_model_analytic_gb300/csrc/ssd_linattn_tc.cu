@@ -76,6 +76,7 @@ struct TcWalk {
   int off, reverse;
   int hist;    // X before every chunk goes to maps.hist (see Hist)
   int beside;  // launched beside the kernel before it, whose end it waits for last
+  int early;   // the kernel launched after it is such a one and may start with it
 };
 
 // ---- PTX that only this file uses ----------------------------------------------
@@ -273,7 +274,9 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
   const int vblocks = (p.dv + kV - 1) / kV;
   const int h = blockIdx.x / vblocks, v0 = (blockIdx.x % vblocks) * kV;
   const int b = blockIdx.y, seg = blockIdx.z;
-  grid_dep_launch();  // a kernel that needs nothing of this one may start beside it
+  // (only where the kernel behind it is known to need nothing of this one: a
+  // kernel of another call may read what this one writes)
+  if (p.early) grid_dep_launch();
   const float la = p.log_decay[h];
   int len = p.T;
   if (p.lens) len = __shfl_sync(0xffffffffu, min(max(p.lens[b], 0), p.T), 0);
@@ -1394,6 +1397,7 @@ cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_
     p.last = nullptr;
   } else {
     p.beside = beside;
+    p.early = w.followed;
   }
   if (w.hist) {
     const int DK = w.dk <= 64 ? 64 : 128;

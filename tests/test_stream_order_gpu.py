@@ -53,3 +53,29 @@ def test_two_layers_backward(history):
         got = chain(False, dx)
         for n in want:
             assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("operand", ["x", "dy"])
+def test_linear_attention_into_the_core(operand):
+    """The output of a walk is an input of the core's backward, whose first
+    kernel may start before the kernel ahead of it has ended."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    t = core(2048, 3)
+    g = torch.Generator("cuda").manual_seed(4)
+    q, k, v = (torch.randn(4, 2048, 32, d, generator=g, device="cuda").bfloat16() for d in (128, 128, 64))
+    la = torch.full((32,), -0.05, device="cuda")
+
+    def chain(synchronise, o):
+        o.fill_(7.0)
+        ssd.linattn_forward(q, k, v, la, scale=0.01, out={"o": o})
+        if synchronise:
+            torch.cuda.synchronize()
+        return ssd.backward(*args(t, **{operand: o}), o if operand == "dy" else t["dy"], None, chunk=256)
+
+    o = torch.empty_like(v)
+    want = chain(True, o)
+    for _ in range(5):
+        got = chain(False, o)
+        for n in want:
+            assert torch.equal(got[n], want[n]), n

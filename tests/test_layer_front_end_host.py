@@ -1,0 +1,109 @@
+"""The layer operators' torch front end without a GPU: which tensors a call
+keeps for another stream and what it refuses before anything is launched.
+CPU tensors stand in for CUDA ones and a recorder for the library."""
+import pytest
+import torch
+
+from state_space_model_analytic_gb300 import layer_api
+
+
+class Stream:
+    def __init__(self, handle, device=torch.device("cuda", 0)):
+        self.cuda_stream, self.device, self.waited = handle, device, []
+
+    def wait_stream(self, other):
+        self.waited.append(other)
+
+
+class Cuda:
+    """What the patched torch and library saw."""
+
+    def __init__(self):
+        self.current, self.recorded, self.calls = Stream(1), [], []
+
+    def entry(self, name):
+        if name.endswith("workspace_bytes"):
+            return lambda *a: 512
+        return lambda *a: self.calls.append((name, a)) or 0
+
+    def kept(self, t):
+        return any(s.data_ptr() == t.data_ptr() for s in self.recorded)
+
+
+@pytest.fixture
+def cuda(monkeypatch):
+    c = Cuda()
+    empty = torch.empty
+    dev = property(lambda t: torch.device("cuda", 0))
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
+    monkeypatch.setattr(torch.Tensor, "device", dev, raising=False)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0, raising=False)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: c.recorded.append(t), raising=False)
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: c.current)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(layer_api, "_raw_stream", lambda i: c.current.cuda_stream)
+    monkeypatch.setattr(layer_api, "_call", c.entry)
+    monkeypatch.setattr(layer_api, "_layouts", layer_api._Layouts())
+    return c
+
+
+def linattn(T=5):
+    z = torch.zeros
+    return {"q": z(2, T, 2, 16), "k": z(2, T, 2, 16), "v": z(2, T, 4, 8), "log_decay": z(4),
+            "state": z(2, 4, 8, 16), "do": z(2, T, 4, 8), "dstate": z(2, 4, 8, 16),
+            "lens": z(2, dtype=torch.int32)}
+
+
+def norm():
+    z = torch.zeros
+    return {"residual": z(3, 8), "y": z(3, 8), "z": z(3, 8), "w_post": z(8), "res_scale": z(8),
+            "w_pre": z(8), "dx": z(3, 8), "dnew": z(3, 8), "stats": z(3, 2)}
+
+
+def calls():
+    """(name, operands by name, the call on a stream)"""
+    f = layer_api
+    a = linattn()
+    yield "forward", {n: a[n] for n in ("q", "k", "v", "log_decay", "state", "lens")}, lambda s, a=a: \
+        f.linattn_forward(a["q"], a["k"], a["v"], a["log_decay"], a["state"], lens=a["lens"], stream=s)
+    b = linattn()
+    yield "backward", b, lambda s: f.linattn_backward(
+        b["q"], b["k"], b["v"], b["log_decay"], b["state"], b["do"], b["dstate"], lens=b["lens"], stream=s)
+    c = {n: t[:, 0].contiguous() if t.dim() == 4 and n in "qkv" else t for n, t in linattn().items()
+         if n in ("q", "k", "v", "log_decay", "state")}
+    c["slots"] = torch.zeros(2, dtype=torch.int32)
+    yield "step", c, lambda s: f.linattn_step(c["q"], c["k"], c["v"], c["log_decay"], c["state"],
+                                              slots=c["slots"], stream=s)
+    d = norm()
+    n6 = ("residual", "y", "z", "w_post", "res_scale", "w_pre")
+    yield "norm_forward", {n: d[n] for n in n6}, lambda s: f.block_norm_forward(
+        *(d[n] for n in n6), 1e-5, stream=s)
+    e = norm()
+    yield "norm_backward", e, lambda s: f.block_norm_backward(
+        *(e[n] for n in n6), 1e-5, e["dx"], e["dnew"], e["stats"], stream=s)
+    g = {"a": torch.zeros(3), "b": torch.zeros(4), "out a": torch.zeros(3), "out b": torch.zeros(4)}
+    yield "clip", g, lambda s: f.clip_grad_norm([g["a"], g["b"]], 1.0, out=[g["out a"], g["out b"]],
+                                                stream=s)
+
+
+NAMES = ["forward", "backward", "step", "norm_forward", "norm_backward", "clip"]
+
+
+@pytest.mark.parametrize("at", range(6), ids=NAMES)
+def test_every_operand_is_kept_for_another_stream(cuda, at):
+    """A temporary operand is not handed out again before the stream is done
+    with it, and the call starts after the current stream's work."""
+    _, operands, run = list(calls())[at]
+    side = Stream(2)
+    run(side)
+    assert side.waited == [cuda.current] and len(cuda.calls) == 1
+    assert [n for n, t in operands.items() if not cuda.kept(t)] == []
+
+
+@pytest.mark.parametrize("at", range(6), ids=NAMES)
+def test_nothing_is_kept_on_the_current_stream(cuda, at):
+    _, _, run = list(calls())[at]
+    run(None)
+    run(cuda.current)
+    assert not cuda.recorded and not cuda.current.waited

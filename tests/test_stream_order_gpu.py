@@ -79,3 +79,29 @@ def test_linear_attention_into_the_core(operand):
         got = chain(False, o)
         for n in want:
             assert torch.equal(got[n], want[n]), n
+
+
+def test_temporary_operands_on_another_stream():
+    """An operand dropped on return is not handed out again while the other
+    stream still has the call ahead of it."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    g = torch.Generator("cuda").manual_seed(6)
+    q, k = (torch.randn(2, 300, 2, 64, generator=g, device="cuda") for _ in range(2))
+    v = torch.randn(2, 300, 4, 64, generator=g, device="cuda")
+    la = torch.full((4,), -0.05, device="cuda")
+    grads = [torch.randn(n, generator=g, device="cuda") for n in (1000, 70001)]
+    want = ssd.linattn_forward(q, k, v, la)
+    want_n = ssd.clip_grad_norm(grads, 1.0, out=[torch.empty_like(t) for t in grads])
+    big = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(20):
+            big.fill_(i)
+    got = ssd.linattn_forward(q.clone(), k.clone(), v.clone(), la.clone(), stream=side)
+    got_n = ssd.clip_grad_norm([t.clone() for t in grads], 1.0, stream=side)
+    trash = [torch.full_like(t, float("nan")) for t in (q, k, v, la, *grads) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(got_n, want_n)
+    del trash

@@ -1,0 +1,28 @@
+"""The device and the stream of a call, for the torch front ends."""
+from __future__ import annotations
+
+import torch
+
+# the current stream's handle without a Stream object around it, where this
+# torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def check_device(dev, stream):
+    """The library launches on the current device: a call whose tensors or
+    stream belong to another one is refused."""
+    current = torch.cuda.current_device()
+    if dev.index != current:
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{current}: "
+                         "make theirs the current one (torch.cuda.device)")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, but the tensors are on {dev}")
+
+
+def handle(stream, dev):
+    """The stream's native handle, or the current one's (None: the default stream)."""
+    if stream is not None:
+        return stream.cuda_stream or None
+    if _raw_stream is not None:
+        return _raw_stream(dev.index) or None
+    return torch.cuda.current_stream(dev).cuda_stream or None

@@ -4,23 +4,21 @@ Torch provides device memory and the stream; every step of the forward and
 backward runs in the library's CUDA kernels behind the C ABI (include/ssd.h).
 Shapes: x, dy [B,T,H,P]; dt [B,T,H] fp32; A, D [H] fp32; B, C [B,T,G,N];
 h0 [B,H,P,N] fp32.  x, B, C, dy share one storage type (fp32 or bf16).
+Calls run on `stream` or the current stream of the current device, whose tensors
+they have to be.
 """
 from __future__ import annotations
 
 import torch
 
 from . import _native as nat
+from . import _streams
 
 _IO_TYPES = {torch.float32: False, torch.bfloat16: True}
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _stream_handle(stream) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream or None
 
 
 def _check(name, t, dtype, shape, device):
@@ -90,6 +88,7 @@ def forward(x, dt, A, B, C, D, h0=None, *, chunk: int, want_final=True, want_sta
     N = B.shape[3]
     nc = T // chunk
     dev = x.device
+    _streams.check_device(dev, stream)
     if out is None:
         out = {}
     y = out.get("y")
@@ -105,7 +104,7 @@ def forward(x, dt, A, B, C, D, h0=None, *, chunk: int, want_final=True, want_sta
         workspace = alloc_workspace(dims, 0, dev)
     rc = nat.lib().ssd_forward(dims, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                _ptr(h0), _ptr(y), _ptr(fs), _ptr(cs), _ptr(workspace),
-                               workspace.numel(), _stream_handle(stream))
+                               workspace.numel(), _streams.handle(stream, dev))
     nat.check(rc)
     return y, fs, cs
 
@@ -118,6 +117,7 @@ def backward(x, dt, A, B, C, D, h0, dy, chunk_states=None, *, chunk: int, want_d
     Bz, T, H, P = x.shape
     N = B.shape[3]
     dev = x.device
+    _streams.check_device(dev, stream)
     if chunk_states is not None:
         _check("chunk_states", chunk_states, torch.float32, (Bz, T // chunk, H, P, N), dev)
     g = dict(out) if out is not None else {}
@@ -137,7 +137,7 @@ def backward(x, dt, A, B, C, D, h0, dy, chunk_states=None, *, chunk: int, want_d
                                 _ptr(h0), _ptr(dy), _ptr(chunk_states), _ptr(g["dx"]),
                                 _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]),
                                 _ptr(g["dD"]), _ptr(g["dh0"]), _ptr(workspace),
-                                workspace.numel(), _stream_handle(stream))
+                                workspace.numel(), _streams.handle(stream, dev))
     nat.check(rc)
     return g
 
@@ -162,6 +162,7 @@ def forward_raw(x, dt_raw, dt_bias, a_log, B, C, D, h0=None, *, chunk: int, want
     Bz, T, H, P = x.shape
     N = B.shape[3]
     dev = x.device
+    _streams.check_device(dev, stream)
     out = {} if out is None else out
     y = out.get("y")
     if y is None:
@@ -177,7 +178,7 @@ def forward_raw(x, dt_raw, dt_bias, a_log, B, C, D, h0=None, *, chunk: int, want
     rc = nat.lib().ssd_forward_raw(dims, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(a_log),
                                    _ptr(B), _ptr(C), _ptr(D), _ptr(h0), _ptr(y), _ptr(fs),
                                    _ptr(cs), _ptr(workspace), workspace.numel(),
-                                   _stream_handle(stream))
+                                   _streams.handle(stream, dev))
     nat.check(rc)
     return y, fs, cs
 
@@ -194,6 +195,7 @@ def backward_raw(x, dt_raw, dt_bias, a_log, B, C, D, h0, dy, chunk_states=None, 
     Bz, T, H, P = x.shape
     N = B.shape[3]
     dev = x.device
+    _streams.check_device(dev, stream)
     if chunk_states is not None:
         _check("chunk_states", chunk_states, torch.float32, (Bz, T // chunk, H, P, N), dev)
     g = dict(out) if out is not None else {}
@@ -214,7 +216,7 @@ def backward_raw(x, dt_raw, dt_bias, a_log, B, C, D, h0, dy, chunk_states=None, 
         dims, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(a_log), _ptr(B), _ptr(C), _ptr(D),
         _ptr(h0), _ptr(dy), _ptr(chunk_states), _ptr(g["dx"]), _ptr(g["d_dt_raw"]),
         _ptr(g["d_dt_bias"]), _ptr(g["d_a_log"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]),
-        _ptr(g["dh0"]), _ptr(workspace), workspace.numel(), _stream_handle(stream))
+        _ptr(g["dh0"]), _ptr(workspace), workspace.numel(), _streams.handle(stream, dev))
     nat.check(rc)
     return g
 
@@ -224,6 +226,7 @@ def rmsnorm_gated_forward(y, z, weight, eps, *, want_inv_rms=True, out=None, str
     out = y * inv_rms * weight * silu(z), inv_rms = 1 / sqrt(mean(y^2) + eps)."""
     if not y.is_cuda:
         raise ValueError("inputs must be CUDA tensors (no CPU path exists)")
+    _streams.check_device(y.device, stream)
     width = y.shape[-1]
     rows = y.numel() // width
     if y.dtype not in _IO_TYPES:
@@ -236,7 +239,7 @@ def rmsnorm_gated_forward(y, z, weight, eps, *, want_inv_rms=True, out=None, str
     inv = torch.empty(y.shape[:-1], dtype=torch.float32, device=y.device) if want_inv_rms else None
     rc = nat.lib().ssd_rmsnorm_gated_forward(rows, width, int(_IO_TYPES[y.dtype]), _ptr(y), _ptr(z),
                                              _ptr(weight), float(eps), _ptr(o), _ptr(inv),
-                                             _stream_handle(stream))
+                                             _streams.handle(stream, y.device))
     nat.check(rc)
     return o, inv
 
@@ -245,6 +248,7 @@ def rmsnorm_gated_backward(y, z, weight, eps, dout, inv_rms=None, *, workspace=N
     """Gradients of sum(dout * out): dict dy, dz, dweight."""
     if not y.is_cuda:
         raise ValueError("inputs must be CUDA tensors (no CPU path exists)")
+    _streams.check_device(y.device, stream)
     width = y.shape[-1]
     rows = y.numel() // width
     if y.dtype not in _IO_TYPES:
@@ -263,7 +267,7 @@ def rmsnorm_gated_backward(y, z, weight, eps, dout, inv_rms=None, *, workspace=N
     rc = nat.lib().ssd_rmsnorm_gated_backward(
         rows, width, int(_IO_TYPES[y.dtype]), _ptr(y), _ptr(z), _ptr(weight), float(eps),
         _ptr(inv_rms), _ptr(dout), _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dweight"]),
-        _ptr(workspace), workspace.numel(), _stream_handle(stream))
+        _ptr(workspace), workspace.numel(), _streams.handle(stream, y.device))
     nat.check(rc)
     return g
 
@@ -273,6 +277,7 @@ def conv1d_silu_forward(x, weight, bias=None, init_state=None, *, out=None, stre
     bias [C] fp32, init_state [B,C,K] fp32 (None = zeros).  Returns out [B,T,C]."""
     if not x.is_cuda:
         raise ValueError("inputs must be CUDA tensors (no CPU path exists)")
+    _streams.check_device(x.device, stream)
     if x.dtype not in _IO_TYPES:
         raise TypeError(f"x: unsupported dtype {x.dtype}")
     Bz, T, C = x.shape
@@ -287,7 +292,7 @@ def conv1d_silu_forward(x, weight, bias=None, init_state=None, *, out=None, stre
     o = torch.empty_like(x) if out is None else out
     rc = nat.lib().ssd_conv1d_silu_forward(Bz, T, C, K, int(_IO_TYPES[x.dtype]), _ptr(x),
                                            _ptr(weight), _ptr(bias), _ptr(init_state), _ptr(o),
-                                           _stream_handle(stream))
+                                           _streams.handle(stream, x.device))
     nat.check(rc)
     return o
 
@@ -296,6 +301,7 @@ def conv1d_silu_backward(x, weight, bias, init_state, dout, *, workspace=None, s
     """Gradients of sum(dout * out): dict dx, dweight, dbias."""
     if not x.is_cuda:
         raise ValueError("inputs must be CUDA tensors (no CPU path exists)")
+    _streams.check_device(x.device, stream)
     if x.dtype not in _IO_TYPES:
         raise TypeError(f"x: unsupported dtype {x.dtype}")
     Bz, T, C = x.shape
@@ -316,6 +322,6 @@ def conv1d_silu_backward(x, weight, bias, init_state, dout, *, workspace=None, s
     rc = nat.lib().ssd_conv1d_silu_backward(
         Bz, T, C, K, int(_IO_TYPES[x.dtype]), _ptr(x), _ptr(weight), _ptr(bias), _ptr(init_state),
         _ptr(dout), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(workspace),
-        workspace.numel(), _stream_handle(stream))
+        workspace.numel(), _streams.handle(stream, x.device))
     nat.check(rc)
     return g

@@ -1,7 +1,8 @@
 """Python front end of the layer operators: linear attention with a decay for
 each head, norms around a block, gradient clipping.  Torch CUDA tensors in, torch
 tensors out; every step runs in the library's kernels behind the C ABI
-(include/ssd.h), on `stream` or the current stream.  A call on another stream
+(include/ssd.h), on `stream` or the current stream of the current device, whose
+tensors they have to be.  A call on another stream
 than the current one starts after the work that is on the current one, and its
 operands may be dropped as soon as it returns.
 """
@@ -13,6 +14,8 @@ import operator
 import torch
 
 from . import _native as nat
+from . import _streams
+from ._streams import check_device as _check_device
 
 _IO_TYPES = {torch.float32: nat.SSD_F32, torch.bfloat16: nat.SSD_BF16}
 
@@ -34,19 +37,6 @@ def _ptr(t):
 
 def _size(t):
     return 0 if t is None else t.numel() * t.element_size()
-
-
-# the current stream's handle without a Stream object around it, where this
-# torch has the call
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_handle(stream, dev):
-    if stream is not None:
-        return stream.cuda_stream or None
-    if _raw_stream is not None:
-        return _raw_stream(dev.index) or None
-    return torch.cuda.current_stream(dev).cuda_stream or None
 
 
 def _keep(stream, *tensors):
@@ -178,6 +168,7 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
     None); out: dict of preallocated "o", "state"."""
     d, need, _ = _linattn_dims(q, k, v, scale, log_decay, None, False)
     dev = q.device
+    _check_device(dev, stream)
     out = {} if out is None else out
     o, state = out.get("o"), out.get("state")
     shape = _linattn_checks(d, dev, (("state0", state0), ("out state", state)), lens)
@@ -193,7 +184,7 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
     nat.check(_call("ssd_linattn_forward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
         _ptr(lens), o.data_ptr(), _ptr(state), _ptr(workspace), _size(workspace),
-        _stream_handle(stream, dev)))
+        _streams.handle(stream, dev)))
     return o, state
 
 
@@ -204,6 +195,7 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
     dstate [B,H,V,K] fp32 or None (zero)."""
     d, _, need = _linattn_dims(q, k, v, scale, log_decay, do, False)
     dev = q.device
+    _check_device(dev, stream)
     g = dict(out) if out is not None else {}
     shape = _linattn_checks(d, dev, (("state0", state0), ("dstate", dstate),
                                      ("out dstate0", g.get("dstate0"))), lens)
@@ -223,7 +215,7 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
         do.data_ptr(), _ptr(dstate), _ptr(lens), g["dq"].data_ptr(), g["dk"].data_ptr(),
         g["dv"].data_ptr(), _ptr(g["dstate0"]), _ptr(workspace), _size(workspace),
-        _stream_handle(stream, dev)))
+        _streams.handle(stream, dev)))
     return g
 
 
@@ -241,6 +233,7 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
     q = C, log_decay = dt A, and D x added to o."""
     d = _linattn_dims(q, k, v, scale, log_decay, None, True)[0]
     dev = q.device
+    _check_device(dev, stream)
     rows = state.shape[0] if state.dim() else 0
     _expect("state", state, torch.float32, (rows, d.nheads, d.dv, d.dk), dev)
     if slots is not None:
@@ -259,7 +252,7 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
     nat.check(_call("ssd_linattn_step")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
         d.nheads if log_decay.dim() == 2 else 0, state.data_ptr(), state_out.data_ptr(),
-        _ptr(slots), rows, out.data_ptr(), _stream_handle(stream, dev)))
+        _ptr(slots), rows, out.data_ptr(), _streams.handle(stream, dev)))
     return out, state_out
 
 
@@ -329,6 +322,7 @@ def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_st
     rows, width, code, rcode, ys, zs, _ = _block_norm_args(residual, y, z, w_post, res_scale,
                                                            w_pre)
     dev = y.device
+    _check_device(dev, stream)
     out = {} if out is None else out
     new, x = out.get("residual"), out.get("x")
     if new is None:
@@ -344,7 +338,7 @@ def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_st
     nat.check(_call("ssd_block_norm_forward")(
         rows, width, code, rcode, residual.data_ptr(), y.data_ptr(), ys, _ptr(z), zs,
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), new.data_ptr(),
-        x.data_ptr(), _ptr(stats), _stream_handle(stream, dev)))
+        x.data_ptr(), _ptr(stats), _streams.handle(stream, dev)))
     return new, x, stats
 
 
@@ -356,6 +350,7 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
     rows, width, code, rcode, ys, zs, need = _block_norm_args(new_residual, y, z, w_post,
                                                               res_scale, w_pre)
     dev = y.device
+    _check_device(dev, stream)
     _expect("dx", dx, y.dtype, y.shape, dev)
     if dnew is not None:
         _expect("dnew", dnew, new_residual.dtype, y.shape, dev)
@@ -381,7 +376,7 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), _ptr(stats),
         dx.data_ptr(), _ptr(dnew), g["dresidual"].data_ptr(), g["dy"].data_ptr(), _ptr(g["dz"]),
         g["dw_post"].data_ptr(), _ptr(g["dres_scale"]), g["dw_pre"].data_ptr(),
-        workspace.data_ptr(), _size(workspace), _stream_handle(stream, dev)))
+        workspace.data_ptr(), _size(workspace), _streams.handle(stream, dev)))
     return g
 
 
@@ -412,6 +407,7 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
         raise TypeError("grads: fp32 and bf16 tensors only") from None
     if dev.type != "cuda" or of(_Tensor.get_device, grads) != [dev.index] * n:
         raise ValueError("grads: must be CUDA tensors on one device (no CPU path exists)")
+    _check_device(dev, stream)
     if not all(map(_Tensor.is_contiguous, grads)):
         raise ValueError("grads: must be contiguous")
     sizes, at = of(_Tensor.numel, grads), of(_Tensor.data_ptr, grads)
@@ -438,5 +434,5 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
         _keep(stream, norm, workspace, *grads, *outs)
     nat.check(_call("ssd_clip_grad_norm")(rows, n, float(max_norm), float(eps), norm.data_ptr(),
                                    workspace.data_ptr(), _size(workspace),
-                                   _stream_handle(stream, dev)))
+                                   _streams.handle(stream, dev)))
     return norm

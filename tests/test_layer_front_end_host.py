@@ -1,10 +1,10 @@
-"""The layer operators' torch front end without a GPU: which tensors a call
-keeps for another stream and what it refuses before anything is launched.
+"""The torch front ends without a GPU: which tensors a call of a layer operator
+keeps for another stream, and what every call refuses before anything is launched.
 CPU tensors stand in for CUDA ones and a recorder for the library."""
 import pytest
 import torch
 
-from state_space_model_analytic_gb300 import layer_api
+from state_space_model_analytic_gb300 import _streams, api, layer_api
 
 
 class Stream:
@@ -42,7 +42,7 @@ def cuda(monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: c.current)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(layer_api, "_raw_stream", lambda i: c.current.cuda_stream)
+    monkeypatch.setattr(_streams, "_raw_stream", lambda i: c.current.cuda_stream)
     monkeypatch.setattr(layer_api, "_call", c.entry)
     monkeypatch.setattr(layer_api, "_layouts", layer_api._Layouts())
     return c
@@ -107,3 +107,50 @@ def test_nothing_is_kept_on_the_current_stream(cuda, at):
     run(None)
     run(cuda.current)
     assert not cuda.recorded and not cuda.current.waited
+
+
+def core_calls():
+    """(name, the call on a stream) of the core's front end"""
+    z = torch.zeros
+    x, dt, h, bc = z(2, 16, 4, 16), z(2, 16, 4), z(4), z(2, 16, 2, 16)
+    core = (x, dt, h, bc, bc, h)
+    raw = (x, dt, h, h, bc, bc, h)
+    yield "forward", lambda s: api.forward(*core, chunk=16, stream=s)
+    yield "backward", lambda s: api.backward(*core, None, x, chunk=16, stream=s)
+    yield "forward_raw", lambda s: api.forward_raw(*raw, chunk=16, stream=s)
+    yield "backward_raw", lambda s: api.backward_raw(*raw, None, x, chunk=16, stream=s)
+    y, w = z(3, 8), z(8)
+    yield "rmsnorm_gated_forward", lambda s: api.rmsnorm_gated_forward(y, y, w, 1e-5, stream=s)
+    yield "rmsnorm_gated_backward", lambda s: api.rmsnorm_gated_backward(y, y, w, 1e-5, y, stream=s)
+    c, k = z(2, 5, 8), z(8, 4)
+    yield "conv1d_silu_forward", lambda s: api.conv1d_silu_forward(c, k, w, stream=s)
+    yield "conv1d_silu_backward", lambda s: api.conv1d_silu_backward(c, k, w, None, c, stream=s)
+
+
+@pytest.fixture
+def core(cuda, monkeypatch):
+    class Library:
+        def __getattr__(self, name):
+            return cuda.entry(name)
+    monkeypatch.setattr(api.nat, "lib", lambda: Library())
+    return cuda
+
+
+EVERY = [(calls, i, n) for i, n in enumerate(NAMES)] + [(core_calls, i, n) for i, (n, _) in
+                                                        enumerate(core_calls())]
+
+
+@pytest.mark.parametrize("of,at", [e[:2] for e in EVERY], ids=[e[2] for e in EVERY])
+def test_another_device_than_the_current_one_is_refused(core, monkeypatch, of, at):
+    """Tensors, or a stream, of a device that the launch would not go to."""
+    run = list(of())[at][-1]
+    run(None)
+    run(Stream(2))
+    assert len(core.calls) == 2
+    with pytest.raises(ValueError, match="cuda:1"):
+        run(Stream(3, torch.device("cuda", 1)))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for stream in (None, Stream(2)):
+        with pytest.raises(ValueError, match="current device"):
+            run(stream)
+    assert len(core.calls) == 2

@@ -26,3 +26,19 @@ def handle(stream, dev):
     if _raw_stream is not None:
         return _raw_stream(dev.index) or None
     return torch.cuda.current_stream(dev).cuda_stream or None
+
+
+def keep(stream, *tensors):
+    """Orders a call on another stream than the current one, where its memory
+    was allocated: that memory may have belonged to a tensor that work already
+    on the current stream still uses, so the call comes after that work; and no
+    memory of the call (its operands, which the caller may drop as soon as it
+    returns, its results and its workspace) is handed out again before the
+    other stream is done with it."""
+    if stream is not None:
+        current = torch.cuda.current_stream()
+        if stream != current:
+            stream.wait_stream(current)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)

@@ -5,7 +5,9 @@ backward runs in the library's CUDA kernels behind the C ABI (include/ssd.h).
 Shapes: x, dy [B,T,H,P]; dt [B,T,H] fp32; A, D [H] fp32; B, C [B,T,G,N];
 h0 [B,H,P,N] fp32.  x, B, C, dy share one storage type (fp32 or bf16).
 Calls run on `stream` or the current stream of the current device, whose tensors
-they have to be.
+they have to be.  A call on another stream than the current one starts after the
+work that is on the current one, and its operands may be dropped as soon as it
+returns.
 """
 from __future__ import annotations
 
@@ -102,6 +104,7 @@ def forward(x, dt, A, B, C, D, h0=None, *, chunk: int, want_final=True, want_sta
         cs = torch.empty(Bz, nc, H, P, N, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = alloc_workspace(dims, 0, dev)
+    _streams.keep(stream, x, dt, A, B, C, D, h0, y, fs, cs, workspace)
     rc = nat.lib().ssd_forward(dims, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                _ptr(h0), _ptr(y), _ptr(fs), _ptr(cs), _ptr(workspace),
                                workspace.numel(), _streams.handle(stream, dev))
@@ -133,6 +136,7 @@ def backward(x, dt, A, B, C, D, h0, dy, chunk_states=None, *, chunk: int, want_d
         g["dh0"] = None
     if workspace is None:
         workspace = alloc_workspace(dims, 1 if chunk_states is not None else 2, dev)
+    _streams.keep(stream, x, dt, A, B, C, D, h0, dy, chunk_states, workspace, *g.values())
     rc = nat.lib().ssd_backward(dims, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                 _ptr(h0), _ptr(dy), _ptr(chunk_states), _ptr(g["dx"]),
                                 _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]),
@@ -175,6 +179,7 @@ def forward_raw(x, dt_raw, dt_bias, a_log, B, C, D, h0=None, *, chunk: int, want
         cs = torch.empty(Bz, T // chunk, H, P, N, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = alloc_workspace(dims, 3, dev)
+    _streams.keep(stream, x, dt_raw, dt_bias, a_log, B, C, D, h0, y, fs, cs, workspace)
     rc = nat.lib().ssd_forward_raw(dims, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(a_log),
                                    _ptr(B), _ptr(C), _ptr(D), _ptr(h0), _ptr(y), _ptr(fs),
                                    _ptr(cs), _ptr(workspace), workspace.numel(),
@@ -212,6 +217,8 @@ def backward_raw(x, dt_raw, dt_bias, a_log, B, C, D, h0, dy, chunk_states=None, 
         g["dh0"] = None
     if workspace is None:
         workspace = alloc_workspace(dims, 4 if chunk_states is not None else 5, dev)
+    _streams.keep(stream, x, dt_raw, dt_bias, a_log, B, C, D, h0, dy, chunk_states, workspace,
+                  *g.values())
     rc = nat.lib().ssd_backward_raw(
         dims, _ptr(x), _ptr(dt_raw), _ptr(dt_bias), _ptr(a_log), _ptr(B), _ptr(C), _ptr(D),
         _ptr(h0), _ptr(dy), _ptr(chunk_states), _ptr(g["dx"]), _ptr(g["d_dt_raw"]),
@@ -237,6 +244,7 @@ def rmsnorm_gated_forward(y, z, weight, eps, *, want_inv_rms=True, out=None, str
         raise ValueError("y: must be contiguous")
     o = torch.empty_like(y) if out is None else out
     inv = torch.empty(y.shape[:-1], dtype=torch.float32, device=y.device) if want_inv_rms else None
+    _streams.keep(stream, y, z, weight, o, inv)
     rc = nat.lib().ssd_rmsnorm_gated_forward(rows, width, int(_IO_TYPES[y.dtype]), _ptr(y), _ptr(z),
                                              _ptr(weight), float(eps), _ptr(o), _ptr(inv),
                                              _streams.handle(stream, y.device))
@@ -264,6 +272,7 @@ def rmsnorm_gated_backward(y, z, weight, eps, dout, inv_rms=None, *, workspace=N
         if n == 0:
             raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, "width rejected")
         workspace = torch.empty(n, dtype=torch.uint8, device=y.device)
+    _streams.keep(stream, y, z, weight, inv_rms, dout, workspace, *g.values())
     rc = nat.lib().ssd_rmsnorm_gated_backward(
         rows, width, int(_IO_TYPES[y.dtype]), _ptr(y), _ptr(z), _ptr(weight), float(eps),
         _ptr(inv_rms), _ptr(dout), _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dweight"]),
@@ -290,6 +299,7 @@ def conv1d_silu_forward(x, weight, bias=None, init_state=None, *, out=None, stre
     if not x.is_contiguous():
         raise ValueError("x: must be contiguous")
     o = torch.empty_like(x) if out is None else out
+    _streams.keep(stream, x, weight, bias, init_state, o)
     rc = nat.lib().ssd_conv1d_silu_forward(Bz, T, C, K, int(_IO_TYPES[x.dtype]), _ptr(x),
                                            _ptr(weight), _ptr(bias), _ptr(init_state), _ptr(o),
                                            _streams.handle(stream, x.device))
@@ -319,6 +329,7 @@ def conv1d_silu_backward(x, weight, bias, init_state, dout, *, workspace=None, s
         if n == 0:
             raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, "shape rejected")
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _streams.keep(stream, x, weight, bias, init_state, dout, workspace, *g.values())
     rc = nat.lib().ssd_conv1d_silu_backward(
         Bz, T, C, K, int(_IO_TYPES[x.dtype]), _ptr(x), _ptr(weight), _ptr(bias), _ptr(init_state),
         _ptr(dout), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(workspace),

@@ -39,22 +39,6 @@ def _size(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _keep(stream, *tensors):
-    """Orders a call on another stream than the current one, where its memory
-    was allocated: that memory may have belonged to a tensor that work already
-    on the current stream still uses, so the call comes after that work; and no
-    memory of the call (its operands, which the caller may drop as soon as it
-    returns, its results and its workspace) is handed out again before the
-    other stream is done with it."""
-    if stream is not None:
-        current = torch.cuda.current_stream()
-        if stream != current:
-            stream.wait_stream(current)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-
-
 class _Layouts(dict):
     """What a call derives from its operands' shapes, strides and types alone
     (never from their addresses or values), kept for the next call with the
@@ -180,7 +164,7 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
         state = torch.empty(shape, dtype=torch.float32, device=dev)
     if workspace is None and need > 256:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _keep(stream, q, k, v, log_decay, state0, lens, o, state, workspace)
+    _streams.keep(stream, q, k, v, log_decay, state0, lens, o, state, workspace)
     nat.check(_call("ssd_linattn_forward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
         _ptr(lens), o.data_ptr(), _ptr(state), _ptr(workspace), _size(workspace),
@@ -210,7 +194,7 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
         g["dstate0"] = torch.empty(shape, dtype=torch.float32, device=dev)
     if workspace is None and need > 256:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _keep(stream, q, k, v, log_decay, state0, do, dstate, lens, workspace, *g.values())
+    _streams.keep(stream, q, k, v, log_decay, state0, do, dstate, lens, workspace, *g.values())
     nat.check(_call("ssd_linattn_backward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
         do.data_ptr(), _ptr(dstate), _ptr(lens), g["dq"].data_ptr(), g["dk"].data_ptr(),
@@ -248,7 +232,7 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
         out = torch.empty(v.shape, dtype=v.dtype, device=dev)
     else:
         _expect("out", out, v.dtype, v.shape, dev)
-    _keep(stream, q, k, v, log_decay, state, slots, out, state_out)
+    _streams.keep(stream, q, k, v, log_decay, state, slots, out, state_out)
     nat.check(_call("ssd_linattn_step")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
         d.nheads if log_decay.dim() == 2 else 0, state.data_ptr(), state_out.data_ptr(),
@@ -334,7 +318,7 @@ def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_st
     else:
         _expect("out x", x, y.dtype, y.shape, dev)
     stats = torch.empty(*y.shape[:-1], 2, dtype=torch.float32, device=dev) if want_stats else None
-    _keep(stream, residual, y, z, w_post, res_scale, w_pre, new, x, stats)
+    _streams.keep(stream, residual, y, z, w_post, res_scale, w_pre, new, x, stats)
     nat.check(_call("ssd_block_norm_forward")(
         rows, width, code, rcode, residual.data_ptr(), y.data_ptr(), ys, _ptr(z), zs,
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), new.data_ptr(),
@@ -369,8 +353,8 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
             _expect("out " + name, g[name], dt, shape, dev)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _keep(stream, new_residual, y, z, w_post, res_scale, w_pre, dx, dnew, stats, workspace,
-          *g.values())
+    _streams.keep(stream, new_residual, y, z, w_post, res_scale, w_pre, dx, dnew, stats,
+                  workspace, *g.values())
     nat.check(_call("ssd_block_norm_backward")(
         rows, width, code, rcode, new_residual.data_ptr(), y.data_ptr(), ys, _ptr(z), zs,
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), _ptr(stats),
@@ -431,7 +415,7 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
             raise nat.SsdError(nat.SSD_ERR_INVALID_ARG, nat.last_error() or "tensors rejected")
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if stream is not None:
-        _keep(stream, norm, workspace, *grads, *outs)
+        _streams.keep(stream, norm, workspace, *grads, *outs)
     nat.check(_call("ssd_clip_grad_norm")(rows, n, float(max_norm), float(eps), norm.data_ptr(),
                                    workspace.data_ptr(), _size(workspace),
                                    _streams.handle(stream, dev)))

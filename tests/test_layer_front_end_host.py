@@ -1,5 +1,4 @@
-"""The torch front ends without a GPU: which tensors a call of a layer operator
-keeps for another stream, and what every call refuses before anything is launched.
+"""The torch front ends without a GPU: which tensors a call keeps for another stream, and what every call refuses before anything is launched.
 CPU tensors stand in for CUDA ones and a recorder for the library."""
 import pytest
 import torch
@@ -110,21 +109,30 @@ def test_nothing_is_kept_on_the_current_stream(cuda, at):
 
 
 def core_calls():
-    """(name, the call on a stream) of the core's front end"""
+    """(name, operands by name, the call on a stream) of the core's front end"""
     z = torch.zeros
-    x, dt, h, bc = z(2, 16, 4, 16), z(2, 16, 4), z(4), z(2, 16, 2, 16)
-    core = (x, dt, h, bc, bc, h)
-    raw = (x, dt, h, h, bc, bc, h)
-    yield "forward", lambda s: api.forward(*core, chunk=16, stream=s)
-    yield "backward", lambda s: api.backward(*core, None, x, chunk=16, stream=s)
-    yield "forward_raw", lambda s: api.forward_raw(*raw, chunk=16, stream=s)
-    yield "backward_raw", lambda s: api.backward_raw(*raw, None, x, chunk=16, stream=s)
-    y, w = z(3, 8), z(8)
-    yield "rmsnorm_gated_forward", lambda s: api.rmsnorm_gated_forward(y, y, w, 1e-5, stream=s)
-    yield "rmsnorm_gated_backward", lambda s: api.rmsnorm_gated_backward(y, y, w, 1e-5, y, stream=s)
-    c, k = z(2, 5, 8), z(8, 4)
-    yield "conv1d_silu_forward", lambda s: api.conv1d_silu_forward(c, k, w, stream=s)
-    yield "conv1d_silu_backward", lambda s: api.conv1d_silu_backward(c, k, w, None, c, stream=s)
+    core = {"x": z(2, 16, 4, 16), "dt": z(2, 16, 4), "A": z(4), "B": z(2, 16, 2, 16),
+            "C": z(2, 16, 2, 16), "D": z(4), "h0": z(2, 4, 16, 16)}
+    raw = {"x": core["x"], "dt_raw": core["dt"], "dt_bias": z(4), "a_log": z(4),
+           **{n: core[n] for n in ("B", "C", "D", "h0")}}
+    more = {"dy": z(2, 16, 4, 16), "chunk_states": z(2, 1, 4, 16, 16)}
+    yield "forward", core, lambda s: api.forward(*core.values(), chunk=16, stream=s)
+    yield "backward", {**core, **more}, lambda s: api.backward(
+        *core.values(), *more.values(), chunk=16, stream=s)
+    yield "forward_raw", raw, lambda s: api.forward_raw(*raw.values(), chunk=16, stream=s)
+    yield "backward_raw", {**raw, **more}, lambda s: api.backward_raw(
+        *raw.values(), *more.values(), chunk=16, stream=s)
+    n = {"y": z(3, 8), "z": z(3, 8), "weight": z(8), "dout": z(3, 8), "inv_rms": z(3)}
+    a = [n["y"], n["z"], n["weight"], 1e-5]
+    yield "rmsnorm_gated_forward", {i: n[i] for i in ("y", "z", "weight")}, lambda s: \
+        api.rmsnorm_gated_forward(*a, stream=s)
+    yield "rmsnorm_gated_backward", n, lambda s: api.rmsnorm_gated_backward(
+        *a, n["dout"], n["inv_rms"], stream=s)
+    c = {"x": z(2, 5, 8), "weight": z(8, 4), "bias": z(8), "init_state": z(2, 8, 4)}
+    yield "conv1d_silu_forward", c, lambda s: api.conv1d_silu_forward(*c.values(), stream=s)
+    dout = z(2, 5, 8)
+    yield "conv1d_silu_backward", {**c, "dout": dout}, lambda s: api.conv1d_silu_backward(
+        *c.values(), dout, stream=s)
 
 
 @pytest.fixture
@@ -136,7 +144,7 @@ def core(cuda, monkeypatch):
     return cuda
 
 
-EVERY = [(calls, i, n) for i, n in enumerate(NAMES)] + [(core_calls, i, n) for i, (n, _) in
+EVERY = [(calls, i, n) for i, n in enumerate(NAMES)] + [(core_calls, i, n) for i, (n, _, _) in
                                                         enumerate(core_calls())]
 
 
@@ -154,3 +162,17 @@ def test_another_device_than_the_current_one_is_refused(core, monkeypatch, of, a
         with pytest.raises(ValueError, match="current device"):
             run(stream)
     assert len(core.calls) == 2
+
+
+@pytest.mark.parametrize("at", range(8), ids=[n for n, _, _ in core_calls()])
+def test_the_core_keeps_every_operand_too(core, at):
+    _, operands, run = list(core_calls())[at]
+    run(None)
+    assert not core.recorded
+    side = Stream(2)
+    run(side)
+    assert side.waited == [core.current] and len(core.calls) == 2
+    assert [n for n, t in operands.items() if not core.kept(t)] == []
+    # and its results: every pointer that the library was given, but the stream's
+    given = {p for p in core.calls[1][1] if isinstance(p, int) and p > 1 << 20}
+    assert given <= {t.data_ptr() for t in core.recorded}

@@ -105,3 +105,24 @@ def test_temporary_operands_on_another_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(got_n, want_n)
     del trash
+
+
+def test_the_core_on_another_stream():
+    """Dropped operands and the call's own workspace, behind a busy stream."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    t = core(512, 5)
+    cs = ssd.forward(*args(t), chunk=256)[2]
+    want = ssd.backward(*args(t), t["dy"], cs, chunk=256)
+    big = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(20):
+            big.fill_(i)
+    got = ssd.backward(*(a.clone() for a in args(t)), t["dy"].clone(), cs.clone(), chunk=256, stream=side)
+    trash = [torch.full_like(a, float("nan")) for a in (*t.values(), cs) for _ in range(3)]
+    torch.cuda.synchronize()
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    del trash

@@ -20,8 +20,7 @@
 // 89 us backward with its column sums (61 %).
 #include <cuda_bf16.h>
 
-#include <atomic>
-
+#include "persistent_grid.h"
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
 #include "ssd_layer_internal.h"
@@ -475,30 +474,6 @@ __global__ void __launch_bounds__(32 * kSlices) k_block_norm_dw(int ncta, BlockN
   }
 }
 
-// A persistent grid: the CTAs that run at once, at most `cap` (the backward's
-// partial rows).  *fit keeps their number (0: not yet asked for); a kernel's
-// threads and shared memory do not change from call to call.
-template <typename KernelT>
-cudaError_t grid_for(KernelT kernel, int threads, size_t smem, long long steps, int cap,
-                     std::atomic<int>* fit, int* grid) {
-  int n = fit->load(std::memory_order_relaxed);
-  if (n == 0) {
-    int dev = 0, nsm = 0, occ = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem);
-    if (e != cudaSuccess) return e;
-    n = nsm * (occ > 0 ? occ : 1);
-    fit->store(n, std::memory_order_relaxed);
-  }
-  if (n > cap) n = cap;
-  *grid = (int)(steps < n ? steps : n);
-  return cudaSuccess;
-}
-
 template <typename T, typename TR, bool VEC, int W>
 cudaError_t launch(const BlockNorm& p, bool backward, int* grid_out, cudaStream_t s) {
   constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads;
@@ -507,8 +482,9 @@ cudaError_t launch(const BlockNorm& p, bool backward, int* grid_out, cudaStream_
   if (!backward) {
     constexpr size_t smem =
         kStaged<VEC, W> ? (size_t)2 * (2 * Pieces<T, VEC>::n + Pieces<TR, VEC>::n) * NT * 16 : 0;
-    static std::atomic<int> fit{0};
-    cudaError_t e = grid_for(k_block_norm_fwd<T, TR, VEC, W>, NT, smem, steps, 1 << 20, &fit, &grid);
+    static FitOf fit;
+    cudaError_t e =
+        persistent_grid(k_block_norm_fwd<T, TR, VEC, W>, NT, smem, steps, 1 << 20, &fit, &grid);
     if (e != cudaSuccess) return e;
     LaunchScope ls("block_norm_fwd", s);
     k_block_norm_fwd<T, TR, VEC, W><<<grid, NT, smem, s>>>(p);
@@ -519,9 +495,10 @@ cudaError_t launch(const BlockNorm& p, bool backward, int* grid_out, cudaStream_
   // the widest row's column sums
   constexpr size_t cols = (R > 1 ? (size_t)R * 2 * W * 32 * kL : W == 32 ? (size_t)2 * kL * NT : 0) * sizeof(float);
   constexpr size_t smem = (staged > cols ? staged : cols) + (size_t)2 * kL * W * 32 * sizeof(float);
-  static std::atomic<int> fit{0};
+  static FitOf fit;
   cudaError_t e =
-      grid_for(k_block_norm_bwd<T, TR, VEC, W>, NT, smem, steps, kBlockNormMaxCtas, &fit, &grid);
+      persistent_grid(k_block_norm_bwd<T, TR, VEC, W>, NT, smem, steps, kBlockNormMaxCtas, &fit,
+                      &grid);
   if (e != cudaSuccess) return e;
   *grid_out = grid;
   LaunchScope ls("block_norm_bwd", s);

@@ -65,6 +65,18 @@ def _expect(name, t, dtype, shape, device, dense=True):
         raise ValueError(f"{name}: must be contiguous")
 
 
+def _workspace(workspace, need, dev):
+    """The caller's workspace after its checks (its size is the library's), or
+    `need` bytes."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace.device != dev:
+        raise ValueError(f"workspace: on {workspace.device}, expected {dev}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace
+
+
 def _io_type(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (no CPU path exists)")
@@ -162,8 +174,8 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
         _expect("out o", o, v.dtype, v.shape, dev)
     if state is None and want_state:
         state = torch.empty(shape, dtype=torch.float32, device=dev)
-    if workspace is None and need > 256:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None or need > 256:
+        workspace = _workspace(workspace, need, dev)
     _streams.keep(stream, q, k, v, log_decay, state0, lens, o, state, workspace)
     nat.check(_call("ssd_linattn_forward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
@@ -192,8 +204,8 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
         g["dstate0"] = None
     elif g.get("dstate0") is None:
         g["dstate0"] = torch.empty(shape, dtype=torch.float32, device=dev)
-    if workspace is None and need > 256:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None or need > 256:
+        workspace = _workspace(workspace, need, dev)
     _streams.keep(stream, q, k, v, log_decay, state0, do, dstate, lens, workspace, *g.values())
     nat.check(_call("ssd_linattn_backward")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state0),
@@ -351,8 +363,7 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
             g[name] = torch.empty(shape, dtype=dt, device=dev)
         else:
             _expect("out " + name, g[name], dt, shape, dev)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, need, dev)
     _streams.keep(stream, new_residual, y, z, w_post, res_scale, w_pre, dx, dnew, stats,
                   workspace, *g.values())
     nat.check(_call("ssd_block_norm_backward")(
@@ -409,11 +420,12 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
     table = array.array("Q", flat)
     rows = table.buffer_info()[0] if n else None
     norm = torch.empty((), dtype=torch.float32, device=dev)
+    need = 0
     if workspace is None:
         need = _call("ssd_clip_workspace_bytes")(rows, n)
         if need == 0:
             raise nat.SsdError(nat.SSD_ERR_INVALID_ARG, nat.last_error() or "tensors rejected")
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, need, dev)
     if stream is not None:
         _streams.keep(stream, norm, workspace, *grads, *outs)
     nat.check(_call("ssd_clip_grad_norm")(rows, n, float(max_norm), float(eps), norm.data_ptr(),

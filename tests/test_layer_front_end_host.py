@@ -33,7 +33,7 @@ class Cuda:
 def cuda(monkeypatch):
     c = Cuda()
     empty = torch.empty
-    dev = property(lambda t: torch.device("cuda", 0))
+    dev = property(lambda t: getattr(t, "elsewhere", torch.device("cuda", 0)))
     monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
     monkeypatch.setattr(torch.Tensor, "device", dev, raising=False)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0, raising=False)
@@ -176,3 +176,21 @@ def test_the_core_keeps_every_operand_too(core, at):
     # and its results: every pointer that the library was given, but the stream's
     given = {p for p in core.calls[1][1] if isinstance(p, int) and p > 1 << 20}
     assert given <= {t.data_ptr() for t in core.recorded}
+
+
+@pytest.mark.parametrize("at", [0, 1, 4, 5], ids=[NAMES[i] for i in (0, 1, 4, 5)])
+def test_a_workspace_that_is_not_the_device_s_is_refused(cuda, monkeypatch, at):
+    """The host's memory, another device's, or memory with gaps."""
+    name = ("linattn_forward", "linattn_backward", None, None, "block_norm_backward",
+            "clip_grad_norm")[at]
+    f = getattr(layer_api, name)
+    bad = [torch.zeros(512, dtype=torch.uint8) for _ in range(2)]
+    bad[0].elsewhere, bad[1].elsewhere = torch.device("cpu"), torch.device("cuda", 1)
+    bad.append(torch.zeros(1024, dtype=torch.uint8)[::2])
+    for w in bad:
+        monkeypatch.setattr(layer_api, name, lambda *a, **k: f(*a, workspace=w, **k))
+        with pytest.raises(ValueError, match="workspace"):
+            list(calls())[at][-1](None)
+    monkeypatch.setattr(layer_api, name, lambda *a, **k: f(*a, workspace=torch.zeros(512), **k))
+    list(calls())[at][-1](None)
+    assert len(cuda.calls) == 1

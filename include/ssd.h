@@ -243,9 +243,10 @@ SSD_API int ssd_conv1d_silu_backward(int64_t batch, int64_t seqlen, int64_t chan
  * dimensions of q, k, v and dout; they must be positive multiples of 16
  * bytes, so that views of one projection's output serve as operands (a
  * stride of an extent of 1 is not used).  dk, dv: multiples of 8 in [8, 128].
- * Pointers 16-byte aligned (lens 4), the workspace 256.  State and sums are
- * fp32; deterministic, asynchronous and with the errors of ssd_forward.  The
- * kernels' waits are bounded and report through ssd_device_status.
+ * Pointers 16-byte aligned (log_decay, lens and slots 4), the workspace 256.
+ * State and sums are fp32; deterministic, asynchronous and with the errors of
+ * ssd_forward.  The kernels' waits are bounded and report through
+ * ssd_device_status.
  */
 typedef struct {
   int64_t batch;    /* B in [1, 65535] */

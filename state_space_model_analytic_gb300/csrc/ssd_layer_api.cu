@@ -45,6 +45,14 @@ int check_pointers(const char* who, const Named* need, int n_need, const Named* 
   return SSD_OK;
 }
 
+// Arrays of fp32 or int32 that are read element by element.
+int check_words(const char* who, const Named* words, int n) {
+  for (int i = 0; i < n; ++i)
+    if ((uintptr_t)words[i].p & 3u)
+      return refuse(SSD_ERR_ALIGNMENT, "%s: %s is not 4-byte aligned", who, words[i].name);
+  return SSD_OK;
+}
+
 // ---- linear attention ------------------------------------------------------
 
 int la_check(const char* who, const ssd_linattn_dims* d) {
@@ -212,6 +220,8 @@ int ssd_linattn_forward(const ssd_linattn_dims* d, const void* q, const void* k,
   const Named may[] = {{"state0", state0}, {"state", state}};
   if ((rc = check_pointers(who, need, 4, may, 2))) return rc;
   if (!log_decay) return refuse(SSD_ERR_INVALID_ARG, "%s: log_decay is NULL", who);
+  const Named words[] = {{"log_decay", log_decay}, {"lens", lens}};
+  if ((rc = check_words(who, words, 2))) return rc;
   if ((rc = workspace_check(who, workspace, workspace_bytes, ssd_linattn_workspace_bytes(d, 0))))
     return rc;
   LaWalk w = la_base(d, log_decay, lens);
@@ -245,6 +255,8 @@ int ssd_linattn_backward(const ssd_linattn_dims* d, const void* q, const void* k
   const Named may[] = {{"state0", state0}, {"dstate", dstate}, {"dstate0", dstate0}};
   if ((rc = check_pointers(who, need, 7, may, 3))) return rc;
   if (!log_decay) return refuse(SSD_ERR_INVALID_ARG, "%s: log_decay is NULL", who);
+  const Named words[] = {{"log_decay", log_decay}, {"lens", lens}};
+  if ((rc = check_words(who, words, 2))) return rc;
   if ((rc = workspace_check(who, workspace, workspace_bytes, ssd_linattn_workspace_bytes(d, 1))))
     return rc;
   LaOperand oq, ok, ov, og;
@@ -336,6 +348,8 @@ int ssd_linattn_step(const ssd_linattn_dims* d, const void* q, const void* k, co
                         {"state_out", state_out}, {"o", o}};
   if ((rc = check_pointers(who, need, 6, nullptr, 0))) return rc;
   if (!log_decay) return refuse(SSD_ERR_INVALID_ARG, "%s: log_decay is NULL", who);
+  const Named words[] = {{"log_decay", log_decay}, {"slots", slots}};
+  if ((rc = check_words(who, words, 2))) return rc;
   if (decay_batch != 0 && decay_batch != d->nheads)
     return refuse(SSD_ERR_INVALID_ARG, "%s: decay_batch must be 0 or nheads", who);
   if (nslots < 1 || (!slots && nslots < d->batch) || nslots > (1ll << 31))

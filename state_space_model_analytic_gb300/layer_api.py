@@ -96,6 +96,7 @@ def _rows_dense(name, t):
 
 def _linattn_dims(q, k, v, scale, log_decay, do, step):
     """(dims, workspace bytes forward, backward) after the operands' checks."""
+    scale = float(scale)
     key = (step, q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape, v.stride(),
            v.dtype, log_decay.shape, log_decay.dtype, log_decay.is_contiguous(), scale,
            None if do is None else (do.shape, do.stride(), do.dtype))

@@ -194,3 +194,15 @@ def test_a_workspace_that_is_not_the_device_s_is_refused(cuda, monkeypatch, at):
     monkeypatch.setattr(layer_api, name, lambda *a, **k: f(*a, workspace=torch.zeros(512), **k))
     list(calls())[at][-1](None)
     assert len(cuda.calls) == 1
+
+
+def test_a_scale_that_changes_in_place_is_read_in_every_call(cuda):
+    """What a call keeps for the next one with the same operands' shapes goes by
+    the scale's value, not by the object that holds it."""
+    a, scale = linattn(), torch.tensor(0.5)
+    for want in (0.5, 2.0):
+        scale.fill_(want)
+        layer_api.linattn_forward(a["q"], a["k"], a["v"], a["log_decay"], scale=scale)
+        layer_api.linattn_backward(a["q"], a["k"], a["v"], a["log_decay"], None, a["do"], scale=scale)
+        layer_api.linattn_step(*(a[n][:, 0] for n in "qkv"), a["log_decay"], a["state"], scale=scale)
+        assert [c[1][0].scale for c in cuda.calls[-3:]] == [want] * 3

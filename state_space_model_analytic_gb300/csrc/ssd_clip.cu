@@ -9,9 +9,10 @@
 // written once.  Measured on 240 tensors, 1.2 GB: 604 us, 86 % of the copy rate
 // for those three passes (chunks of sixteen times the size were slower).
 //
-// Squares are added in fp32 over a thread's part of a chunk and in fp64 above
-// that; a part whose fp32 sum is so large or so small that squares may have
-// left fp32's range is added again in fp64.
+// Squares are added in fp32, at most eight after one another (their roundings
+// may all go the same way), and those sums over a thread's part of a chunk, of
+// any length, in two fp32 parts; above that in fp64.  A part whose sum is so large
+// or so small that squares may have left fp32's range is added again in fp64.
 #include <cuda_bf16.h>
 
 #include "ssd_common.cuh"
@@ -43,21 +44,35 @@ __device__ __forceinline__ int find(const Table<N>& t, int j) {
   return lo;
 }
 
+// The sum of a vector's squares.
 template <typename T>
-__device__ __forceinline__ void add_squares(uint4 q, float& s, unsigned& any) {
+__device__ __forceinline__ float squares(uint4 q, unsigned& any) {
   any |= q.x | q.y | q.z | q.w;
   if constexpr (sizeof(T) == 4) {
     const float4 f = *(const float4*)&q;
-    s = fmaf(f.x, f.x, fmaf(f.y, f.y, fmaf(f.z, f.z, fmaf(f.w, f.w, s))));
+    return fmaf(f.x, f.x, fmaf(f.y, f.y, fmaf(f.z, f.z, f.w * f.w)));
   } else {
     const __nv_bfloat162* h = (const __nv_bfloat162*)&q;
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = __bfloat1622float2(h[i]);
       s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
     }
+    return s;
   }
 }
+
+// A sum and, apart from it, the rounding errors of its additions (each of them
+// exactly, by Knuth's two-sum).
+struct Sum {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = hi + x, y = t - hi;
+    lo += (hi - (t - y)) + (x - y);
+    hi = t;
+  }
+};
 
 // Elements [0, n) at g: those before the first 16-byte boundary, whole
 // vectors, and the rest.
@@ -78,27 +93,27 @@ __device__ __forceinline__ double chunk_squares(const T* g, int n) {
   const Split sp = split(g, n);
   const uint4* v = (const uint4*)(g + sp.head);
   const int t = threadIdx.x;
-  float s = 0.f;
+  Sum s;
   unsigned any = 0;
   int i = t;
   for (; i + 3 * kThreads < sp.vecs; i += 4 * kThreads) {
     uint4 q[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) q[u] = v[i + u * kThreads];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) add_squares<T>(q[u], s, any);
+    s.add((squares<T>(q[0], any) + squares<T>(q[1], any)) +
+          (squares<T>(q[2], any) + squares<T>(q[3], any)));
   }
-  for (; i < sp.vecs; i += kThreads) add_squares<T>(v[i], s, any);
+  for (; i < sp.vecs; i += kThreads) s.add(squares<T>(v[i], any));
   // at most 7 elements before the vectors and 7 behind them
   const int edge = t < sp.head ? t : t >= 32 && sp.tail + t - 32 < n ? sp.tail + t - 32 : -1;
   if (edge >= 0) {
     const float f = to_f32(g[edge]);
-    s = fmaf(f, f, s);
+    s.add(f * f);
     any |= f != 0.f;
   }
   // squares of |g| in [2^-48, 2^48] and any sum of them stay well inside fp32
   // (a sign bit alone only costs the second pass)
-  if (s < 0x1p+96f && (s > 0x1p-96f || any == 0)) return (double)s;
+  if (s.hi < 0x1p+96f && (s.hi > 0x1p-96f || any == 0)) return (double)s.hi + (double)s.lo;
   double d = 0.0;
   constexpr int E = 16 / (int)sizeof(T);
   for (i = t; i < sp.vecs; i += kThreads)

@@ -256,21 +256,19 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
 # ---- norms around a block ----------------------------------------------------------
 
 def _rows_of(name, t, shape, dtype, dev):
-    """(tensor, stride of its rows): rows dense, the rows themselves evenly spaced."""
+    """The stride of its rows: rows dense, the rows themselves evenly spaced
+    (whatever the strides of extents of 1)."""
     _expect(name, t, dtype, shape, dev, False)
     width = shape[-1]
     if t.is_contiguous():
         return width
-    if t.dim() > 1 and t.stride(-1) == 1:
-        s = t.stride(-2)
-        n = s * t.shape[-2]
-        for i in range(t.dim() - 3, -1, -1):
-            if t.shape[i] > 1 and t.stride(i) != n:
-                break
-            n *= t.shape[i]
-        else:
-            if s >= width:
-                return s
+    outer = [(n, s) for n, s in zip(t.shape[:-1], t.stride()) if n > 1]
+    if t.stride(-1) == 1 or width == 1:
+        if not outer:
+            return width
+        step = outer[-1][1]
+        if step >= width and all(s == n * inner for (_, s), (n, inner) in zip(outer, outer[1:])):
+            return step
     raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
 
 

@@ -206,3 +206,24 @@ def test_a_scale_that_changes_in_place_is_read_in_every_call(cuda):
         layer_api.linattn_backward(a["q"], a["k"], a["v"], a["log_decay"], None, a["do"], scale=scale)
         layer_api.linattn_step(*(a[n][:, 0] for n in "qkv"), a["log_decay"], a["state"], scale=scale)
         assert [c[1][0].scale for c in cuda.calls[-3:]] == [want] * 3
+
+
+def test_rows_of_one_step_are_evenly_spaced(cuda):
+    """The last step of every prompt: the stride of an extent of 1 is nobody's."""
+    wide = torch.zeros(3, 5, 12)
+    views = {"last step": (wide[:, -1:, :8], 60), "one row": (wide[1:2, 2:3, :8], 8),
+             "one prompt": (wide[:1, :, :8], 12), "all": (wide[:, :, :8], 12),
+             "one of each": (wide[:, None, :1, :8], 60)}
+    for name, (y, stride) in views.items():
+        r, w = torch.zeros(y.shape), torch.zeros(8)
+        new, x, stats = layer_api.block_norm_forward(r, y, y, w, None, w, 1e-5)
+        got = cuda.calls[-1][1]
+        assert (got[0], got[1], got[6], got[8]) == (y.numel() // 8, 8, stride, stride), name
+        layer_api.block_norm_backward(r, y, y, w, None, w, 1e-5, x, None, stats)
+        got = cuda.calls[-1][1]
+        assert (got[0], got[1], got[6], got[8]) == (y.numel() // 8, 8, stride, stride), name
+    for y in (wide[:2, :3, :8], wide[:, :, :8].transpose(0, 1), wide[..., ::2], wide[:, :, :8][:, :1]
+              .expand(3, 5, 8)):
+        r, w = torch.zeros(y.shape), torch.zeros(y.shape[-1])
+        with pytest.raises(ValueError, match="evenly spaced"):
+            layer_api.block_norm_forward(r, y, y, w, None, w, 1e-5)

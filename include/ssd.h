@@ -441,9 +441,10 @@ SSD_API int ssd_force_kernel_path(int path);
  * SSD_ERR_DEVICE_TIMEOUT or SSD_ERR_CUDA. */
 SSD_API int ssd_device_status(void);
 
-/* Failure-path self test: launches one CTA whose bounded wait on an mbarrier
- * that nothing completes gives up after about one second and sets the
- * device error word; the kernel then returns normally.  After the caller
+/* Failure-path self test: launches one CTA each of the core's and of the linear
+ * attention's bounded waits, on an mbarrier that nothing completes.  It gives up
+ * after one to two seconds and sets its device error word (bit 0 and bit 24 of
+ * the flag in the message); the kernel then returns normally.  After the caller
  * synchronises, ssd_device_status() reports SSD_ERR_DEVICE_TIMEOUT (once).
  * Returns SSD_OK or SSD_ERR_CUDA (launch failure). */
 SSD_API int ssd_selftest_wait_timeout(void* cuda_stream);

@@ -378,6 +378,7 @@ int ssd_device_status(void) {
 int ssd_selftest_wait_timeout(void* cuda_stream) {
   g_err.clear();
   cudaError_t e = tc_selftest_timeout((cudaStream_t)cuda_stream);
+  if (e == cudaSuccess) e = la_selftest_timeout((cudaStream_t)cuda_stream);
   if (e != cudaSuccess) return cuda_fail(e, "ssd_selftest_wait_timeout");
   return SSD_OK;
 }

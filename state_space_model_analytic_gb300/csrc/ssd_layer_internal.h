@@ -76,6 +76,8 @@ long long la_tc_hist_rows(int B, int H, int T, int dk, int dv);
 cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s);
 // reads and clears the kernels' device error word (a wait gave up)
 cudaError_t la_read_and_clear_error(unsigned int* out);
+// a CTA whose bounded wait runs out
+cudaError_t la_selftest_timeout(cudaStream_t s);
 // out[b][t][g][:] = sum over the group's heads of part[b][t][h][:], in head
 // order (fp32)
 cudaError_t la_group_sum(long long rows, int G, int share, int D, const float* part, float* out,

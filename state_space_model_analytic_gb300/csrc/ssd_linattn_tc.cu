@@ -1409,6 +1409,28 @@ cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_
   return launch_d<false>(m, p, s);
 }
 
+// Two warps wait on a barrier that nothing arrives on: one gives up after
+// kWaitClocks and sets the error word, the other follows it by the abort word.
+static __global__ void k_la_selftest_wait() {
+  __shared__ struct {
+    uint64_t bar;
+    volatile int abort;
+  } w;
+  if (threadIdx.x == 0) {
+    mbar_init(&w.bar, 1);
+    w.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  (void)wait(&w.bar, 0, &w);
+}
+
+cudaError_t la_selftest_timeout(cudaStream_t s) {
+  LaunchScope ls("linattn_selftest_wait", s);
+  k_la_selftest_wait<<<1, 64, 0, s>>>();
+  return cudaGetLastError();
+}
+
 cudaError_t la_read_and_clear_error(unsigned int* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_la_error, sizeof(unsigned int));
   if (e != cudaSuccess) return e;

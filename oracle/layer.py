@@ -22,11 +22,12 @@ def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps):
             {"residual": m, "x": np.abs(w_pre) * m * mi})
 
 
-def block_norm_backward(new, y, z, w_post, res_scale, w_pre, eps, dx, dnew=None):
+def block_norm_backward(new, y, z, w_post, res_scale, w_pre, eps, dx, dnew=None, stats=None):
+    """stats: (inv_y, inv_r) [rows][1] in place of those of y and new"""
     al = np.ones_like(w_post) if res_scale is None else res_scale
     width = y.shape[-1]
     mean = lambda a: a.sum(-1, keepdims=True) / width  # noqa: E731
-    iy, ir = 1.0 / np.sqrt(mean(y ** 2) + eps), 1.0 / np.sqrt(mean(new ** 2) + eps)
+    iy, ir = stats or (1.0 / np.sqrt(mean(y ** 2) + eps), 1.0 / np.sqrt(mean(new ** 2) + eps))
     s, ds = (np.ones_like(y), np.zeros_like(y)) if z is None else _silu(z)
     # magnitudes of silu' (its two terms may cancel)
     ms = np.zeros_like(y) if z is None else (1.0 + np.abs(z)) / (1.0 + np.exp(-z))

@@ -142,6 +142,14 @@ cudaError_t dt_post(const Problem& p, const float* dt_raw, const float* dt_bias,
                     const float* a_log, float* d_dt_raw, float* d_dt_bias, float* d_a_log,
                     float* part);
 
+// The driver's tensor-map encoder, looked up once (no libcuda link); nullptr if
+// there is none.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // 2D row-major [rows][cols] tensor map (bf16 or fp32) with an unswizzled
 // {box_cols, box_rows} box, through the driver entry point (ssd_tc.cu);
 // false if the driver does not provide the encoder or rejects the map.

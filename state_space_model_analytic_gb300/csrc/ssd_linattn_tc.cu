@@ -37,8 +37,6 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include <mutex>
-
 #include "f32x2.cuh"
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
@@ -1220,25 +1218,6 @@ k_la_grad_tc(const __grid_constant__ GradMaps maps, const __grid_constant__ Grad
 }
 
 // ---- host --------------------------------------------------------------------------
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (EncodeTiledFn)p;
-  });
-  return fn;
-}
 
 // [B][T][heads][D] with {128 bytes of D, one head, 128 steps, one row} boxes.
 bool map_4d(CUtensorMap* m, const void* base, int D, int heads, int T, int B,

@@ -43,11 +43,6 @@ class LinattnDims(ctypes.Structure):
                 [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)])
 
 
-class ClipTensor(ctypes.Structure):
-    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
-                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
-
-
 class SsdError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"ssd error {code}: {msg}")
@@ -115,7 +110,7 @@ def lib() -> ctypes.CDLL:
             L.ssd_block_norm_backward.argtypes = ([_I64, _I64, _I32, _I32, _VP, _VP, _I64, _VP,
                                                    _I64, _VP, _VP, _VP, _F] + [_VP] * 10 +
                                                   [ctypes.c_size_t, _VP])
-            CT = ctypes.c_void_p  # a packed array of ClipTensor
+            CT = ctypes.c_void_p  # a packed array of ssd_clip_tensor
             L.ssd_clip_workspace_bytes.restype = ctypes.c_size_t
             L.ssd_clip_workspace_bytes.argtypes = [CT, _I64]
             L.ssd_clip_grad_norm.restype = ctypes.c_int

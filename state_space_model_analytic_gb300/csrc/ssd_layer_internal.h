@@ -40,6 +40,11 @@ struct LaWalk {
                           // 64), nullable; with it o may be NULL (the states alone)
 };
 
+// SMs of the GPU that the library is built for.  A constant, so that the
+// segments that a row is cut into, and with them the workspace's size and the
+// order of the sums, are the same wherever they are asked for (without a GPU too).
+constexpr int kLaSms = 152;
+
 // scratch: la_scratch_floats() floats
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16);
 // `beside`: the walk needs nothing of the kernel launched before it, which is

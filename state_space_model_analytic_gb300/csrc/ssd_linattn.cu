@@ -497,7 +497,7 @@ cudaError_t step_l(const LaStep& p, cudaStream_t s) {
   constexpr int rows = kStepWarps * (32 / LPR);
   // eight rows a lane once that leaves work for every SM (with fewer rows the
   // latency of one counts: 32 heads of one row ran in 8.1 us with two a lane)
-  if ((long long)p.B * p.H * ((p.dv + 8 * rows - 1) / (8 * rows)) >= 304)
+  if ((long long)p.B * p.H * ((p.dv + 8 * rows - 1) / (8 * rows)) >= 2 * kLaSms)
     k_la_step<T, LPR, 8><<<dim3((p.dv + 8 * rows - 1) / (8 * rows), p.H, p.B), kStepWarps * 32, 0, s>>>(p);
   else
     k_la_step<T, LPR, 2><<<dim3((p.dv + 2 * rows - 1) / (2 * rows), p.H, p.B), kStepWarps * 32, 0, s>>>(p);
@@ -540,10 +540,10 @@ cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// CTAs of the fp32 walk that run at once on 152 SMs (three, or two for dk > 64)
+// CTAs of the fp32 walk that run at once (three an SM, or two for dk > 64)
 static int segments32(int B, int H, int T, int dk, int dv) {
   return la_segments((long long)B * H * ((dv + kB - 1) / kB), (T + kC - 1) / kC,
-                     dk <= 64 ? 456 : 304);
+                     (dk <= 64 ? 3 : 2) * kLaSms);
 }
 
 size_t la_scratch_floats(int B, int H, int T, int dk, int dv, bool bf16) {

@@ -1278,7 +1278,7 @@ cudaError_t launch_d(const Maps& m, const TcWalk& p, cudaStream_t s) {
 
 // one CTA an SM
 static int la_tc_segments(int B, int H, int T, int dv) {
-  return la_segments((long long)B * H * ((dv + kV - 1) / kV), (T + kQ - 1) / kQ, 152);
+  return la_segments((long long)B * H * ((dv + kV - 1) / kV), (T + kQ - 1) / kQ, kLaSms);
 }
 
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv) {
@@ -1326,7 +1326,7 @@ cudaError_t la_grads_tc(const LaGrads& d, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     LaunchScope ls("linattn_grads", s);
     const long long units = 2ll * g.nc * d.B * G;
-    kernel<<<(unsigned)(units < 152 ? units : 152), kThreads, smem, s>>>(m, g);
+    kernel<<<(unsigned)(units < kLaSms ? units : kLaSms), kThreads, smem, s>>>(m, g);
     return cudaGetLastError();
   };
   static_assert(GradGeom<128>::smem + 1024 <= 232448, "shared memory of a CTA");

@@ -244,9 +244,18 @@ SSD_API int ssd_conv1d_silu_backward(int64_t batch, int64_t seqlen, int64_t chan
  * bytes, so that views of one projection's output serve as operands (a
  * stride of an extent of 1 is not used).  dk, dv: multiples of 8 in [8, 128].
  * Pointers 16-byte aligned (log_decay, lens and slots 4), the workspace 256.
- * State and sums are fp32; deterministic, asynchronous and with the errors of
- * ssd_forward.  The kernels' waits are bounded and report through
- * ssd_device_status.
+ * Deterministic, asynchronous and with the errors of ssd_forward.  The kernels'
+ * waits are bounded and report through ssd_device_status.  log_decay gets no
+ * gradient.
+ *
+ * Precision: the state, sums and decays are fp32 in either type.  bf16 operands:
+ * besides the outputs, what enters a second product is rounded to bf16, once:
+ * the decayed scores, and the state where it is multiplied (for dq and dk the
+ * states before every 128 steps).  o, dq, dk and dv are off by 0.0023 of their
+ * root mean square, against 0.0017 from their own rounding alone; the states,
+ * which take no such operand, by at most 2^-20.  fp32 operands: products of
+ * parts with 22 bits together, outputs within a few 2^-24 of their root mean
+ * square.
  */
 typedef struct {
   int64_t batch;    /* B in [1, 65535] */
@@ -324,6 +333,9 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
  * res_dtype: `dtype` or SSD_F32.  stats: written by the forward (NULL = not),
  * read by the backward (NULL = recomputed).  The workspace (256-byte aligned)
  * is ssd_block_norm_workspace_bytes(rows, width) bytes (0 = rejected).
+ * The statistics are those of y and of the unrounded r'; without them the
+ * backward takes those of r' as stored.  A bf16 gate's sigmoid comes from
+ * approximate functions (2^-18 at worst), an fp32 gate's from exact ones.
  * Deterministic; errors as for ssd_forward.
  */
 SSD_API size_t ssd_block_norm_workspace_bytes(int64_t rows, int64_t width);
@@ -348,7 +360,7 @@ SSD_API int ssd_block_norm_backward(int64_t rows, int64_t width, int32_t dtype, 
  * tensors: a host array, read during the call.  out = g for clipping in
  * place; otherwise the two must not overlap.  count 0 and tensors of 0
  * elements are allowed; any alignment to the elements' own size.  max_norm >=
- * 0 (infinity: out = g); eps >= 0.  n is within 8 roundings of fp32 (2^-24 each)
+ * 0 (infinity: out = g where n is finite); eps >= 0.  n is within 8 roundings of fp32 (2^-24 each)
  * for any number of gradients of any finite magnitude (no overflow or underflow
  * of the squares).
  * A NaN anywhere makes n and every out NaN; an infinity makes n infinite and

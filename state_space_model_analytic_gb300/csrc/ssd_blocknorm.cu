@@ -14,10 +14,22 @@
 // Bound by memory: the forward moves r, y, z, r', x, the backward y, z, r',
 // dx, dn, dr, dy, dz, each once.  W warps hold a row, eight elements a lane in
 // registers; a CTA of 256 threads or more walks groups of rows, the next row's
-// 16-byte pieces on their way while it works on the current one (where the rows
-// are aligned for that; else elements are loaded one by one).  Measured on
-// 8192 x 2048 bf16 with an fp32 residual: 47 us forward (73 % of the copy rate),
-// 89 us backward with its column sums (61 %).
+// 16-byte pieces on their way while it works on the current one, up to 4096
+// columns and where the rows are aligned for that; else what a row needs is
+// loaded when its turn comes, unaligned rows element by element.  Measured on
+// 8192 x 2048 bf16 with an fp32 residual: 48 us forward (72 % of the copy rate),
+// 91 us backward with its column sums (60 %).
+//
+// Device times of the other variants (bf16, fp32 residual; forward, backward;
+// 52 and 97 us for 8192 x 2048 measured so).
+//   2048 x 8192, 1024 threads without stages: 70 and 128.  Two stages of the
+//   backward do not fit beside the weights in the 227 KB of a CTA; the forward's
+//   would (56 us), it follows the same rule.  The backward, at 64 registers a
+//   thread, keeps its column sums in shared memory and spills up to 176 bytes.
+//   Unaligned rows are built for 1, 4 and 32 warps alone: 16384 x 1023 on four
+//   takes 83 and 109, 2048 x 8191 on 32 83 and 154; widths between pay for idle
+//   warps (8192 x 2047 on 32: 226 and 404, where eight would take 80 and 108;
+//   16384 x 511 on four: 74 and 85, on two 44 and 62).
 #include <cuda_bf16.h>
 
 #include "persistent_grid.h"
@@ -166,7 +178,7 @@ template <typename T, bool VEC>
 struct Pieces {
   static constexpr int n = VEC ? kL * (int)sizeof(T) / 16 : 0;
 };
-// (a CTA of 1024 threads has too little shared memory for two stages)
+// (not for CTAs of 1024 threads: see the variants' times above)
 template <bool VEC, int W>
 constexpr bool kStaged = VEC && W < 32;
 

@@ -66,8 +66,8 @@ cudaError_t la_segment_states(const LaSegments& p, cudaStream_t s);
 // the bf16 walk on tensor cores (ssd_linattn_tc.cu)
 size_t la_tc_scratch_floats(int B, int H, int T, int dk, int dv);
 cudaError_t la_walk_tc(const LaWalk& w, bool beside, float* scratch, cudaStream_t s);
-// dq and dk of shared q and k from the states before every chunk, forward and
-// backward (bf16)
+// dq and dk from the states before every chunk, forward and backward, summed
+// over the heads that share them (every bf16 backward)
 struct LaGrads {
   int B, T, H, dk, dv;
   LaOperand q, k, v, dout;

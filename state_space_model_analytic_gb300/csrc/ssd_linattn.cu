@@ -519,7 +519,7 @@ int la_segments(long long rows, long long chunks, long long slots) {
   // A row's chunks go to one CTA unless that leaves SMs idle.  Splitting a row
   // costs a pass for the segments' states (about half a walk) and two more
   // launches, and every wave of CTAs its start (about two chunks), so it has to
-  // pay for that.
+  // pay for that.  At most 32 segments: more were not measured.
   auto waves = [&](long long n) { return (rows * n + slots - 1) / slots; };
   double best = (double)(waves(1) * (chunks + 2));
   int at = 1;

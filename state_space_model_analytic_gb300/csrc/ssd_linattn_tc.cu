@@ -12,7 +12,9 @@
 // All accumulators are in TMEM (512 columns, one CTA per SM).
 //
 // Precision.  P is rounded to bf16 once (the scores are the A operand of the
-// second product) and X once as an operand; the output is bf16 itself.  The
+// second product) and X once as an operand; the output is bf16 itself.  Together
+// 0.0023 of the outputs' root mean square, 0.0017 from the last rounding alone;
+// a second part of P and of X would double the products of O and Oc.  The
 // state is an fp32 result, so w o V is carried exactly, as three bf16 parts of
 // 8 bits each, side by side in one product of 192 columns.
 //
@@ -27,8 +29,8 @@
 // and k twice (from L2) and form S twice: at 64 columns the accumulators leave
 // room for P beside S, so that S of the next chunk does not wait for P V.
 // Measured: 2.5 us a chunk at dk = 128, of which 1.6 us remain with the work
-// taken out, the hand-overs between the warps; 46 us for 4 x 2048 steps of 32
-// heads 128/64 (66 % of the copy rate, 128 CTAs on 152 SMs), 87 % for 4 x 8192
+// taken out, the hand-overs between the warps; 45 us for 4 x 2048 steps of 32
+// heads 128/64 (68 % of the copy rate, 128 CTAs on 152 SMs), 87 % for 4 x 8192
 // steps of 38 heads.
 //
 // Rows past the end of a batch row (its length, or T) take part as zeros: TMA
@@ -780,11 +782,11 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 }
 
 
-// ---- gradients of shared operands -----------------------------------------------
+// ---- dq and dk ------------------------------------------------------------------
 //
-// dq (and with exchanged roles dk) of a group is a sum over its heads; with the
-// states before every chunk at hand the chunks are independent, and the sum is
-// formed where the products accumulate:
+// dq (and with exchanged roles dk) of a group is a sum over its heads, of which
+// there may be one; with the states before every chunk at hand the chunks are
+// independent, and the sum is formed where the products accumulate:
 //   out = sum over heads  P_h C + (lead_h o A_h) X_h^T,   P_h = mask_h(A_h B_h^T)
 // with dq: A = do, B = v, C = k, X = the forward's states, mask i >= j;
 //      dk: A = v, B = do, C = q, X = the backward's states, mask i <= j
@@ -802,9 +804,9 @@ k_la_walk_tc(const __grid_constant__ Maps maps, const TcWalk p) {
 // place, 8-15 form lead o A and write out of the unit before, one each loads,
 // forms T and accumulates; two stages of items, two of C and two of out keep them
 // apart.  Per item 48 KB are loaded and 1430 cycles of products issued.  Measured
-// (128/64): 89 us for 4 x 2048 steps, 32 heads of their own q and k, of 169 for
+// (128/64): 89 us for 4 x 2048 steps, 32 heads of their own q and k, of 165 for
 // all gradients (three walks: 183); 233 us for 2 x 8192 steps, 64 heads in 8
-// groups, of 476 (walks of every head with a kernel for the sums: 876).
+// groups, of 473 (walks of every head with a kernel for the sums: 876).
 struct Grad {
   int B, T, H, dk, dv, share, nc;  // heads of a group, chunks of a row
   const float* log_decay;

@@ -162,7 +162,11 @@ def linattn_forward(q, k, v, log_decay, state0=None, *, scale=1.0, lens=None, wa
     [H] fp32, <= 0; state0 [B,H,V,K] fp32 or None (zeros); lens [B] int32 on
     the device: row b has lens[b] steps (o is zero past them).  K and V are
     multiples of 8 up to 128.  Returns (o [B,T,H,V], final state [B,H,V,K] or
-    None); out: dict of preallocated "o", "state"."""
+    None); out: dict of preallocated "o", "state".
+
+    State and sums are fp32.  bf16 operands: the decayed scores, and the state
+    where it is multiplied, are rounded to bf16 once (o is off by 0.0023 of its
+    root mean square, 0.0017 of which is its own rounding)."""
     d, need, _ = _linattn_dims(q, k, v, scale, log_decay, None, False)
     dev = q.device
     _check_device(dev, stream)
@@ -189,7 +193,8 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
                      want_dstate0=True, out=None, workspace=None, stream=None):
     """Gradients of sum(do * o) + sum(dstate * state) of linattn_forward: dict
     dq, dk, dv, dstate0 (or None).  do [B,T,H,V] may be strided like v;
-    dstate [B,H,V,K] fp32 or None (zero)."""
+    dstate [B,H,V,K] fp32 or None (zero).  log_decay gets no gradient.  Rounded
+    as the forward's; in bf16 dq and dk come from states rounded to bf16."""
     d, _, need = _linattn_dims(q, k, v, scale, log_decay, do, False)
     dev = q.device
     _check_device(dev, stream)
@@ -312,7 +317,8 @@ def block_norm_forward(residual, y, z, w_post, res_scale, w_pre, eps, *, want_st
     w_post silu(z), x = rmsnorm(new) w_pre over the last dimension (up to
     8192).  z (the gate) and res_scale may be None.  y, z: fp32 or bf16, rows
     evenly spaced; residual: their type or fp32.  Weights [width] fp32.
-    Returns (new residual, x, stats [..., 2] fp32 for the backward or None);
+    Returns (new residual, x, stats [..., 2] fp32 for the backward or None:
+    those of y and of the residual before its rounding);
     out: dict of preallocated "residual" (may be `residual` itself), "x"."""
     rows, width, code, rcode, ys, zs, _ = _block_norm_args(residual, y, z, w_post, res_scale,
                                                            w_pre)

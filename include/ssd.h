@@ -358,11 +358,12 @@ SSD_API int ssd_block_norm_backward(int64_t rows, int64_t width, int32_t dtype, 
  *     n = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (n + eps)),
  *     out = c * g
  * tensors: a host array, read during the call.  out = g for clipping in
- * place; otherwise the two must not overlap.  count 0 and tensors of 0
- * elements are allowed; any alignment to the elements' own size.  max_norm >=
- * 0 (infinity: out = g where n is finite); eps >= 0.  n is within 8 roundings of fp32 (2^-24 each)
- * for any number of gradients of any finite magnitude (no overflow or underflow
- * of the squares).
+ * place; otherwise the two must not overlap, and no two outs may (two writers
+ * of one place race).  count 0 and tensors of 0 elements are allowed; any
+ * alignment to the elements' own size.  max_norm >= 0 (infinity: out = g where n
+ * is finite); eps >= 0.  n is within 8 roundings of fp32 (2^-24 each) for any
+ * number of gradients of any finite magnitude (no overflow or underflow of the
+ * squares).
  * A NaN anywhere makes n and every out NaN; an infinity makes n infinite and
  * c = 0 (and the infinite elements NaN).  norm [1] fp32 receives n.  In place
  * nothing is written where c = 1.  The workspace (256-byte aligned) is

@@ -389,7 +389,7 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
     """Scales the gradients by min(1, max_norm / (n + eps)), n the square root
     of the sum of all their squares; in place, or into the tensors of `out`
     (of the same sizes and types).  grads: contiguous CUDA tensors, fp32 and bf16
-    mixed as they come, of any size.  Returns n, a 0-d fp32 tensor on the
+    mixed as they come, of any size; what is written must not overlap.  Returns n, a 0-d fp32 tensor on the
     device (nothing is synchronised).  A NaN in a gradient makes n and every
     gradient NaN."""
     grads = list(grads)
@@ -420,6 +420,10 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, workspace=None, strea
         if not all(map(_Tensor.is_contiguous, outs)):
             raise ValueError("out: must be contiguous")
         to = of(_Tensor.data_ptr, outs)
+    if len(set(to)) < n:  # (tensors without elements may share an address)
+        full = [p for p, size in zip(to, sizes) if size]
+        if len(set(full)) < len(full):
+            raise ValueError(("grads" if out is None else "out") + ": a tensor is there twice")
     flat = [0] * (4 * n)  # ssd_clip_tensor: g, out, numel, dtype (with a zero above it)
     flat[0::4], flat[1::4], flat[2::4], flat[3::4] = at, to, sizes, codes
     table = array.array("Q", flat)

@@ -227,3 +227,18 @@ def test_rows_of_one_step_are_evenly_spaced(cuda):
         r, w = torch.zeros(y.shape), torch.zeros(y.shape[-1])
         with pytest.raises(ValueError, match="evenly spaced"):
             layer_api.block_norm_forward(r, y, y, w, None, w, 1e-5)
+
+
+def test_a_tensor_clipped_into_twice_is_refused(cuda):
+    """Two writers of one tensor race; one tensor read twice, and tensors without
+    elements, do not."""
+    f = layer_api.clip_grad_norm
+    a, b, none = torch.ones(3), torch.ones(4), torch.ones(0)
+    for kw in (dict(grads=[a, b, a]), dict(grads=[a, a], out=[b[:3], b[:3]])):
+        with pytest.raises(ValueError, match="twice"):
+            f(kw["grads"], 1.0, out=kw.get("out"))
+    assert not cuda.calls
+    f([a, none, b, none], 1.0)
+    f([a, a], 1.0, out=[torch.ones(3), b[:3]])
+    f([none, none], 1.0)
+    assert len(cuda.calls) == 3

@@ -308,6 +308,63 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
                              int64_t nslots, void* o, void* cuda_stream);
 
 /*
+ * The gated delta rule: linear attention whose memory takes off what it already
+ * holds for a key before it writes.  Per batch row b and head h, which uses group
+ * h / (H/G) of q and k,
+ *
+ *     e_t = v_t - a_t S_{t-1} k_t          a_t = exp(log_decay[b][t][h])
+ *     S_t = a_t S_{t-1} + beta_t e_t k_t^T ([dv x dk] state)
+ *     o_t = scale * S_t q_t
+ *
+ * The dims, layouts, strides, lengths (lens), alignments and errors are those of
+ * the linear attention above (ssd_linattn_dims), and besides
+ *
+ *   log_decay, beta, dlog_decay, dbeta   [B][T][H]  fp32, dense
+ *
+ * log_decay <= 0 (-inf: all is forgotten; below -200 it counts as such); beta may
+ * be any number, in [0, 1] it moves the memory part of the way to v (keys of length
+ * 1; a step with beta |k|^2 > 2 amplifies).  Past a row's length o and every
+ * gradient is zero.  The kernels have no waits that could run out.
+ *
+ * Precision: states, sums and decays are fp32 in either type; everything held in
+ * 32 bits enters a product as three bf16 parts (24 bits), bf16 operands as they are.
+ * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.
+ * A bf16 o takes the state and the scores as two parts (16 bits); o, dq, dk and dv
+ * are off by their own rounding alone, 0.0017 of their root mean square.
+ */
+
+/* Bytes of workspace of ssd_delta_rule_forward (which = 0) or
+ * ssd_delta_rule_backward (which = 1); 0 for dims the library rejects, 256 where
+ * none is used (the workspace may then be NULL). */
+SSD_API size_t ssd_delta_rule_workspace_bytes(const ssd_linattn_dims* dims, int which);
+
+/* state0, lens, state (the final state) may be NULL; state may be state0, o must
+ * not overlap an input.  A step's infinite or NaN operands reach the steps before
+ * it in its chunk too (of 64 steps, or 32 in fp32). */
+SSD_API int ssd_delta_rule_forward(const ssd_linattn_dims* dims, const void* q, const void* k,
+                                   const void* v, const float* log_decay, const float* beta,
+                                   const float* state0, const int32_t* lens, void* o, float* state,
+                                   void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* Gradients of L = sum(dout * o) + sum(dstate * state); dstate NULL = zero.
+ * state0, lens, dstate0 may be NULL; no output may overlap an input.  A group's dq
+ * and dk are summed over its heads in head order. */
+SSD_API int ssd_delta_rule_backward(const ssd_linattn_dims* dims, const void* q, const void* k,
+                                    const void* v, const float* log_decay, const float* beta,
+                                    const float* state0, const void* dout, const float* dstate,
+                                    const int32_t* lens, void* dq, void* dk, void* dv,
+                                    float* dlog_decay, float* dbeta, float* dstate0,
+                                    void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* The recurrence for one token of every row (dims->seqlen = 1; the step strides
+ * are not used): q, k [B][G][dk], v [B][H][dv], log_decay, beta [B][H], o
+ * [B][H][dv]; states, slots and idle rows as in ssd_linattn_step. */
+SSD_API int ssd_delta_rule_step(const ssd_linattn_dims* dims, const void* q, const void* k,
+                                const void* v, const float* log_decay, const float* beta,
+                                const float* state_in, float* state_out, const int32_t* slots,
+                                int64_t nslots, void* o, void* cuda_stream);
+
+/*
  * Norms before and after a block, with its gate and residual scale: after a
  * block whose output is y,
  *
@@ -352,6 +409,35 @@ SSD_API int ssd_block_norm_backward(int64_t rows, int64_t width, int32_t dtype, 
                                     void* dresidual, void* dy, void* dz, float* dw_post,
                                     float* dres_scale, float* dw_pre,
                                     void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * Layer norm over the rows of a matrix:
+ *
+ *     y = (x - mean) * inv * weight + bias     inv = 1 / sqrt(mean((x - mean)^2) + eps)
+ *
+ * in fp32, rounded once; the backward returns dx and, summed over the rows in an
+ * order that the sizes alone decide, dweight = sum dy (x - mean) inv and dbias =
+ * sum dy.  weight NULL = 1, bias NULL = 0; dweight and dbias may be NULL.
+ *   x, y, dy, dx                       [rows][width]  `dtype`
+ *   weight, bias, dweight, dbias       [width]        fp32
+ *   stats                              [rows][2]      fp32: mean, inv
+ * x may be strided over the rows (x_stride elements, at least width); everything
+ * else is dense.  width in [1, 8192]; any alignment to the elements' own size is
+ * accepted (16-byte aligned rows run fastest).  stats (8-byte aligned): written by
+ * the forward (NULL = not), read by the backward (NULL = recomputed).  y may be x
+ * and dx may be x or dy where they are dense.  The backward's workspace (256-byte
+ * aligned) is ssd_layer_norm_workspace_bytes(rows, width) bytes (0 = rejected).
+ * Deterministic; errors as for ssd_forward.
+ */
+SSD_API size_t ssd_layer_norm_workspace_bytes(int64_t rows, int64_t width);
+SSD_API int ssd_layer_norm_forward(int64_t rows, int64_t width, int32_t dtype, const void* x,
+                                   int64_t x_stride, const float* weight, const float* bias,
+                                   float eps, void* y, float* stats, void* cuda_stream);
+SSD_API int ssd_layer_norm_backward(int64_t rows, int64_t width, int32_t dtype, const void* x,
+                                    int64_t x_stride, const float* weight, float eps,
+                                    const float* stats, const void* dy, void* dx, float* dweight,
+                                    float* dbias, void* workspace, size_t workspace_bytes,
+                                    void* cuda_stream);
 
 /*
  * Global gradient norm over many tensors, and clipping by it:

@@ -12,10 +12,14 @@ __all__ = ["build", "forward", "backward", "forward_raw", "backward_raw",
            "rmsnorm_gated_forward", "rmsnorm_gated_backward", "conv1d_silu_forward",
            "conv1d_silu_backward", "workspace_bytes", "kernel_path", "launch_count",
            "linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes",
-           "block_norm_forward", "block_norm_backward", "clip_grad_norm"]
+           "block_norm_forward", "block_norm_backward", "clip_grad_norm",
+           "delta_rule_forward", "delta_rule_backward", "delta_rule_step",
+           "delta_rule_workspace_bytes", "layer_norm_forward", "layer_norm_backward"]
 
 _LAYER = ("linattn_forward", "linattn_backward", "linattn_step", "linattn_workspace_bytes",
-          "block_norm_forward", "block_norm_backward", "clip_grad_norm")
+          "block_norm_forward", "block_norm_backward", "clip_grad_norm",
+          "delta_rule_forward", "delta_rule_backward", "delta_rule_step",
+          "delta_rule_workspace_bytes", "layer_norm_forward", "layer_norm_backward")
 
 
 def __getattr__(name):

@@ -25,7 +25,9 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_forward", "ssd_backward", "ssd_last_error
            "ssd_conv1d_silu_backward", "ssd_linattn_workspace_bytes", "ssd_linattn_forward",
            "ssd_linattn_backward", "ssd_linattn_step", "ssd_block_norm_workspace_bytes",
            "ssd_block_norm_forward", "ssd_block_norm_backward", "ssd_clip_workspace_bytes",
-           "ssd_clip_grad_norm")
+           "ssd_clip_grad_norm", "ssd_delta_rule_workspace_bytes", "ssd_delta_rule_forward",
+           "ssd_delta_rule_backward", "ssd_delta_rule_step", "ssd_layer_norm_workspace_bytes",
+           "ssd_layer_norm_forward", "ssd_layer_norm_backward")
 
 
 class SsdDims(ctypes.Structure):
@@ -115,6 +117,22 @@ def lib() -> ctypes.CDLL:
             L.ssd_clip_workspace_bytes.argtypes = [CT, _I64]
             L.ssd_clip_grad_norm.restype = ctypes.c_int
             L.ssd_clip_grad_norm.argtypes = [CT, _I64, _F, _F, _VP, _VP, ctypes.c_size_t, _VP]
+            L.ssd_delta_rule_workspace_bytes.restype = ctypes.c_size_t
+            L.ssd_delta_rule_workspace_bytes.argtypes = [LD, ctypes.c_int]
+            L.ssd_delta_rule_forward.restype = ctypes.c_int
+            L.ssd_delta_rule_forward.argtypes = [LD] + [_VP] * 10 + [ctypes.c_size_t, _VP]
+            L.ssd_delta_rule_backward.restype = ctypes.c_int
+            L.ssd_delta_rule_backward.argtypes = [LD] + [_VP] * 16 + [ctypes.c_size_t, _VP]
+            L.ssd_delta_rule_step.restype = ctypes.c_int
+            L.ssd_delta_rule_step.argtypes = [LD] + [_VP] * 8 + [_I64, _VP, _VP]
+            L.ssd_layer_norm_workspace_bytes.restype = ctypes.c_size_t
+            L.ssd_layer_norm_workspace_bytes.argtypes = [_I64, _I64]
+            L.ssd_layer_norm_forward.restype = ctypes.c_int
+            L.ssd_layer_norm_forward.argtypes = [_I64, _I64, _I32, _VP, _I64, _VP, _VP, _F, _VP,
+                                                 _VP, _VP]
+            L.ssd_layer_norm_backward.restype = ctypes.c_int
+            L.ssd_layer_norm_backward.argtypes = ([_I64, _I64, _I32, _VP, _I64, _VP, _F] +
+                                                  [_VP] * 6 + [ctypes.c_size_t, _VP])
             L.ssd_last_error.restype = ctypes.c_char_p
             L.ssd_last_error.argtypes = []
             L.ssd_kernel_launch_count.restype = ctypes.c_uint64

@@ -19,7 +19,8 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libssd_gb300.so")
 SOURCES = ["ssd_api.cu", "ssd_simt.cu", "ssd_tc.cu", "ssd_tc64.cu", "ssd_noalloc.cu",
            "ssd_dtprep.cu", "ssd_norm.cu", "ssd_conv.cu", "ssd_layer_api.cu", "ssd_linattn.cu",
-           "ssd_linattn_tc.cu", "ssd_blocknorm.cu", "ssd_clip.cu"]
+           "ssd_linattn_tc.cu", "ssd_blocknorm.cu", "ssd_clip.cu", "ssd_delta.cu", "ssd_delta_grads.cu",
+           "ssd_layernorm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

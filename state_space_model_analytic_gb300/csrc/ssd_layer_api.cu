@@ -1,5 +1,5 @@
-// C ABI of the layer operators (linear attention, norms around a block, gradient
-// clipping): argument validation, workspace carve-up and the launches of each
+// C ABI of the layer operators (linear attention, the gated delta rule, norms
+// around a block, layer norm, gradient clipping): argument validation, workspace carve-up and the launches of each
 // call.  Declarations and contracts: include/ssd.h.
 #include <cstdarg>
 #include <cstdio>
@@ -121,6 +121,36 @@ size_t la_part_bytes(const ssd_linattn_dims* d, int which) {
   if (d->nheads == d->ngroups) return 0;
   // dq's, then dk's part of every head
   return up256(sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
+}
+
+// ---- the gated delta rule ------------------------------------------------------
+
+// What the backward keeps between its kernels, in this order: the states before
+// every chunk and the gradients of those after it, E and y, and where heads share q
+// and k their own dq and dk.
+struct DeltaKept {
+  size_t state, steps, part;
+  size_t total() const { return 2 * state + 2 * steps + part; }
+};
+DeltaKept delta_kept(const ssd_linattn_dims* d) {
+  const size_t c = (size_t)delta_chunk(d->dtype == SSD_BF16);
+  const size_t units = (size_t)d->batch * d->nheads * (((size_t)d->seqlen + c - 1) / c);
+  DeltaKept k;
+  k.state = up256(sizeof(float) * units * d->dv * d->dk);
+  k.steps = up256(sizeof(float) * units * c * d->dv);
+  k.part = d->nheads == d->ngroups
+               ? 0
+               : up256(2 * sizeof(float) * (size_t)d->batch * d->seqlen * d->nheads * d->dk);
+  return k;
+}
+
+// log_decay and beta are given and aligned
+int gates_check(const char* who, const float* log_decay, const float* beta, const int32_t* ints,
+                const char* ints_name) {
+  if (!log_decay) return refuse(SSD_ERR_INVALID_ARG, "%s: log_decay is NULL", who);
+  if (!beta) return refuse(SSD_ERR_INVALID_ARG, "%s: beta is NULL", who);
+  const Named words[] = {{"log_decay", log_decay}, {"beta", beta}, {ints_name, ints}};
+  return check_words(who, words, 3);
 }
 
 // (256 bytes stand for none)
@@ -383,6 +413,130 @@ int ssd_linattn_step(const ssd_linattn_dims* d, const void* q, const void* k, co
   return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
 }
 
+// ---- the gated delta rule ------------------------------------------------------
+
+size_t ssd_delta_rule_workspace_bytes(const ssd_linattn_dims* d, int which) {
+  set_last_error("");
+  if (la_check("ssd_delta_rule_workspace_bytes", d)) return 0;
+  if (which != 0 && which != 1) {
+    refuse(SSD_ERR_INVALID_ARG, "ssd_delta_rule_workspace_bytes: which must be 0 or 1");
+    return 0;
+  }
+  return 256 + (which ? delta_kept(d).total() : 0);
+}
+
+int ssd_delta_rule_forward(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                           const float* log_decay, const float* beta, const float* state0,
+                           const int32_t* lens, void* o, float* state, void* workspace,
+                           size_t workspace_bytes, void* cuda_stream) {
+  const char* who = "ssd_delta_rule_forward";
+  set_last_error("");
+  int rc = la_check(who, d);
+  if (rc) return rc;
+  const Named need[] = {{"q", q}, {"k", k}, {"v", v}, {"o", o}};
+  const Named may[] = {{"state0", state0}, {"state", state}};
+  if ((rc = check_pointers(who, need, 4, may, 2))) return rc;
+  if ((rc = gates_check(who, log_decay, beta, lens, "lens"))) return rc;
+  if ((rc = workspace_check(who, workspace, workspace_bytes, ssd_delta_rule_workspace_bytes(d, 0))))
+    return rc;
+  DeltaWalk w = {};
+  w.B = (int)d->batch;
+  w.T = (int)d->seqlen;
+  w.H = (int)d->nheads;
+  w.dk = (int)d->dk;
+  w.dv = (int)d->dv;
+  if ((rc = la_operand(who, "q", d, q, d->q_batch, d->q_step, d->ngroups, d->dk, false, &w.q)) ||
+      (rc = la_operand(who, "k", d, k, d->k_batch, d->k_step, d->ngroups, d->dk, false, &w.k)) ||
+      (rc = la_operand(who, "v", d, v, d->v_batch, d->v_step, d->nheads, d->dv, false, &w.v)))
+    return rc;
+  w.log_decay = log_decay;
+  w.beta = beta;
+  w.first = state0;
+  w.last = state;
+  w.lens = lens;
+  w.o = o;
+  w.scale = d->scale;
+  const cudaError_t e = delta_walk(w, d->dtype == SSD_BF16, (cudaStream_t)cuda_stream);
+  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
+int ssd_delta_rule_backward(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                            const float* log_decay, const float* beta, const float* state0,
+                            const void* dout, const float* dstate, const int32_t* lens, void* dq,
+                            void* dk, void* dv, float* dlog_decay, float* dbeta, float* dstate0,
+                            void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  const char* who = "ssd_delta_rule_backward";
+  set_last_error("");
+  int rc = la_check(who, d);
+  if (rc) return rc;
+  const Named need[] = {{"q", q},   {"k", k},   {"v", v},   {"dout", dout},
+                        {"dq", dq}, {"dk", dk}, {"dv", dv}};
+  const Named may[] = {{"state0", state0}, {"dstate", dstate}, {"dstate0", dstate0}};
+  if ((rc = check_pointers(who, need, 7, may, 3))) return rc;
+  if ((rc = gates_check(who, log_decay, beta, lens, "lens"))) return rc;
+  if (!dlog_decay) return refuse(SSD_ERR_INVALID_ARG, "%s: dlog_decay is NULL", who);
+  if (!dbeta) return refuse(SSD_ERR_INVALID_ARG, "%s: dbeta is NULL", who);
+  const Named words[] = {{"dlog_decay", dlog_decay}, {"dbeta", dbeta}};
+  if ((rc = check_words(who, words, 2))) return rc;
+  if ((rc = workspace_check(who, workspace, workspace_bytes, ssd_delta_rule_workspace_bytes(d, 1))))
+    return rc;
+  LaOperand oq, ok, ov, og;
+  if ((rc = la_operand(who, "q", d, q, d->q_batch, d->q_step, d->ngroups, d->dk, false, &oq)) ||
+      (rc = la_operand(who, "k", d, k, d->k_batch, d->k_step, d->ngroups, d->dk, false, &ok)) ||
+      (rc = la_operand(who, "v", d, v, d->v_batch, d->v_step, d->nheads, d->dv, false, &ov)) ||
+      (rc = la_operand(who, "dout", d, dout, d->dout_batch, d->dout_step, d->nheads, d->dv, false,
+                       &og)))
+    return rc;
+  const bool bf16 = d->dtype == SSD_BF16;
+  const cudaStream_t s = (cudaStream_t)cuda_stream;
+  const DeltaKept kept = delta_kept(d);
+  char* at = (char*)workspace;
+  float* hist_s = (float*)at;
+  float* hist_d = (float*)(at += kept.state);
+  float* err = (float*)(at += kept.state);
+  float* y = (float*)(at += kept.steps);
+  float* part = (float*)(at += kept.steps);
+  const int B = (int)d->batch, T = (int)d->seqlen, H = (int)d->nheads, G = (int)d->ngroups;
+  const int K = (int)d->dk, V = (int)d->dv;
+  const DeltaWalk w = {B, T, H, K, V, oq, ok, ov, log_decay, beta, state0, nullptr, lens, nullptr,
+                       hist_s, err, d->scale};
+  cudaError_t e = delta_walk(w, bf16, s);
+  const DeltaBack r = {B, T, H, K, V, oq, ok, og, log_decay, beta, dstate, dstate0, lens, dv,
+                       hist_d, y, d->scale};
+  if (e == cudaSuccess) e = delta_back(r, bf16, s);
+  const DeltaGrads x = {B, T, H, G, K, V, oq, ok, og, log_decay, beta, lens, hist_s, hist_d, err, y,
+                        dq, dk, dlog_decay, dbeta, d->scale};
+  if (e == cudaSuccess) e = delta_grads(x, part, bf16, s);
+  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
+int ssd_delta_rule_step(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                        const float* log_decay, const float* beta, const float* state_in,
+                        float* state_out, const int32_t* slots, int64_t nslots, void* o,
+                        void* cuda_stream) {
+  const char* who = "ssd_delta_rule_step";
+  set_last_error("");
+  int rc = la_check(who, d);
+  if (rc) return rc;
+  if (d->seqlen != 1) return refuse(SSD_ERR_INVALID_ARG, "%s: seqlen must be 1", who);
+  const Named need[] = {{"q", q}, {"k", k}, {"v", v}, {"state_in", state_in},
+                        {"state_out", state_out}, {"o", o}};
+  if ((rc = check_pointers(who, need, 6, nullptr, 0))) return rc;
+  if ((rc = gates_check(who, log_decay, beta, slots, "slots"))) return rc;
+  if (nslots < 1 || (!slots && nslots < d->batch) || nslots > (1ll << 31))
+    return refuse(SSD_ERR_INVALID_ARG, "%s: nslots must be in [1, 2^31], and at least batch without slots", who);
+  LaOperand oq, ok, ov;
+  if ((rc = la_operand(who, "q", d, q, d->q_batch, 0, d->ngroups, d->dk, true, &oq)) ||
+      (rc = la_operand(who, "k", d, k, d->k_batch, 0, d->ngroups, d->dk, true, &ok)) ||
+      (rc = la_operand(who, "v", d, v, d->v_batch, 0, d->nheads, d->dv, true, &ov)))
+    return rc;
+  const DeltaStep p = {(int)d->batch, (int)d->nheads, (int)d->ngroups, (int)d->dk, (int)d->dv,
+                       q, k, v, oq.batch, ok.batch, ov.batch, log_decay, beta, state_in, state_out,
+                       slots, nslots, o, d->scale};
+  const cudaError_t e = delta_step(p, d->dtype == SSD_BF16, (cudaStream_t)cuda_stream);
+  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
 // ---- norms around a block ------------------------------------------------------
 
 size_t ssd_block_norm_workspace_bytes(int64_t rows, int64_t width) {
@@ -478,6 +632,77 @@ int ssd_block_norm_backward(int64_t rows, int64_t width, int32_t dtype, int32_t 
   p.part = (float*)workspace;
   const cudaError_t e =
       block_norm_backward(p, dtype == SSD_BF16, res_dtype == SSD_BF16, (cudaStream_t)cuda_stream);
+  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
+// ---- layer norm ------------------------------------------------------------------
+
+size_t ssd_layer_norm_workspace_bytes(int64_t rows, int64_t width) {
+  set_last_error("");
+  if (rows < 1 || width < 1 || width > 8192) {
+    refuse(SSD_ERR_INVALID_ARG, "ssd_layer_norm_workspace_bytes: rows >= 1 and width in [1, 8192]");
+    return 0;
+  }
+  return up256((size_t)kLayerNormMaxCtas * 2 * width * sizeof(float));
+}
+
+int ssd_layer_norm_forward(int64_t rows, int64_t width, int32_t dtype, const void* x,
+                           int64_t x_stride, const float* weight, const float* bias, float eps,
+                           void* y, float* stats, void* cuda_stream) {
+  const char* who = "ssd_layer_norm_forward";
+  set_last_error("");
+  int rc = norm_check(who, rows, width, dtype, dtype, x_stride, width, eps);
+  if (rc) return rc;
+  const Sized need[] = {{"x", x, dtype}, {"y", y, dtype}};
+  const Sized may[] = {{"weight", weight, SSD_F32}, {"bias", bias, SSD_F32}};
+  if ((rc = check_sized(who, need, 2, may, 2))) return rc;
+  if (stats && ((uintptr_t)stats & 7u))
+    return refuse(SSD_ERR_ALIGNMENT, "%s: stats is not 8-byte aligned", who);
+  LayerNorm p = {};
+  p.rows = rows;
+  p.width = (int)width;
+  p.x_stride = x_stride;
+  p.eps = eps;
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.y = y;
+  p.stats = stats;
+  const cudaError_t e = layer_norm_forward(p, dtype == SSD_BF16, (cudaStream_t)cuda_stream);
+  return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
+}
+
+int ssd_layer_norm_backward(int64_t rows, int64_t width, int32_t dtype, const void* x,
+                            int64_t x_stride, const float* weight, float eps, const float* stats,
+                            const void* dy, void* dx, float* dweight, float* dbias,
+                            void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  const char* who = "ssd_layer_norm_backward";
+  set_last_error("");
+  int rc = norm_check(who, rows, width, dtype, dtype, x_stride, width, eps);
+  if (rc) return rc;
+  const Sized need[] = {{"x", x, dtype}, {"dy", dy, dtype}, {"dx", dx, dtype}};
+  const Sized may[] = {{"weight", weight, SSD_F32}, {"dweight", dweight, SSD_F32},
+                       {"dbias", dbias, SSD_F32}};
+  if ((rc = check_sized(who, need, 3, may, 3))) return rc;
+  if (stats && ((uintptr_t)stats & 7u))
+    return refuse(SSD_ERR_ALIGNMENT, "%s: stats is not 8-byte aligned", who);
+  if ((rc = workspace_check(who, workspace, workspace_bytes,
+                            ssd_layer_norm_workspace_bytes(rows, width))))
+    return rc;
+  LayerNorm p = {};
+  p.rows = rows;
+  p.width = (int)width;
+  p.x_stride = x_stride;
+  p.eps = eps;
+  p.x = x;
+  p.weight = weight;
+  p.stats = const_cast<float*>(stats);
+  p.dy = dy;
+  p.dx = dx;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.part = (float*)workspace;
+  const cudaError_t e = layer_norm_backward(p, dtype == SSD_BF16, (cudaStream_t)cuda_stream);
   return e == cudaSuccess ? SSD_OK : cuda_refuse(e, who);
 }
 

@@ -103,6 +103,61 @@ struct LaStep {
 };
 cudaError_t la_step(const LaStep& p, bool bf16, cudaStream_t s);
 
+// The gated delta rule (ssd_delta.cu, ssd_delta_grads.cu).  Rows are walked in
+// chunks of delta_chunk() steps; the backward keeps, for every row and head and
+// each of the row's chunks, the state before it and the gradient of the state
+// after it [dv][dk], and E and y [steps][dv], all fp32.
+int delta_chunk(bool bf16);
+struct DeltaWalk {
+  int B, T, H, dk, dv;
+  LaOperand q, k, v;
+  const float *log_decay, *beta;  // [B][T][H]
+  const float* first;             // [B][H][dv][dk], nullable
+  float* last;                    // nullable
+  const int* lens;
+  void* o;
+  float *hist, *err;              // given: the states before every chunk and E instead of o
+  float scale;
+};
+cudaError_t delta_walk(const DeltaWalk& p, bool bf16, cudaStream_t s);
+struct DeltaBack {
+  int B, T, H, dk, dv;
+  LaOperand q, k, dout;
+  const float *log_decay, *beta;
+  const float* first;  // gradient of the final state, nullable
+  float* last;         // of the first one, nullable
+  const int* lens;
+  void* dv_out;
+  float *hist, *y;
+  float scale;
+};
+cudaError_t delta_back(const DeltaBack& p, bool bf16, cudaStream_t s);
+struct DeltaGrads {
+  int B, T, H, G, dk, dv;
+  LaOperand q, k, dout;
+  const float *log_decay, *beta;
+  const int* lens;
+  const float *hist_s, *hist_d, *err, *y;
+  void *dq, *dk_out;
+  float *dlog_decay, *dbeta;
+  float scale;
+};
+// part: for heads that share q and k, 2 B T H dk floats
+cudaError_t delta_grads(const DeltaGrads& p, float* part, bool bf16, cudaStream_t s);
+struct DeltaStep {
+  int B, H, G, dk, dv;
+  const void *q, *k, *v;
+  long long q_batch, k_batch, v_batch;
+  const float *log_decay, *beta;  // [B][H]
+  const float* state_in;
+  float* state_out;
+  const int* slots;  // nullable
+  long long nslots;
+  void* o;
+  float scale;
+};
+cudaError_t delta_step(const DeltaStep& p, bool bf16, cudaStream_t s);
+
 // Norms around a block (ssd_blocknorm.cu).  In the backward `residual` is the
 // forward's new residual.  part: [grid][2][width] column sums of the CTAs,
 // grid <= kBlockNormMaxCtas.
@@ -123,6 +178,26 @@ struct BlockNorm {
 };
 cudaError_t block_norm_forward(const BlockNorm& p, bool bf16, bool res_bf16, cudaStream_t s);
 cudaError_t block_norm_backward(const BlockNorm& p, bool bf16, bool res_bf16, cudaStream_t s);
+
+// Layer norm (ssd_layernorm.cu).  part: [grid][2][width] column sums of the CTAs,
+// grid <= kLayerNormMaxCtas.
+constexpr int kLayerNormMaxCtas = 608;
+struct LayerNorm {
+  long long rows;
+  int width;
+  long long x_stride;
+  float eps;
+  const void* x;
+  const float *weight, *bias;  // nullable
+  void* y;
+  float* stats;  // [rows][2] mean, 1 / sqrt(variance + eps); nullable
+  const void* dy;
+  void* dx;
+  float *dweight, *dbias;  // nullable
+  float* part;
+};
+cudaError_t layer_norm_forward(const LayerNorm& p, bool bf16, cudaStream_t s);
+cudaError_t layer_norm_backward(const LayerNorm& p, bool bf16, cudaStream_t s);
 
 // Gradient clipping (ssd_clip.cu): `count` tensors, none empty, cut into
 // chunks of 2^shift bytes; kClipTable tensors a launch, at most kClipMaxCtas

@@ -1,5 +1,5 @@
 """Python front end of the layer operators: linear attention with a decay for
-each head, norms around a block, gradient clipping.  Torch CUDA tensors in, torch
+each head, the gated delta rule, norms around a block, layer norm, gradient clipping.  Torch CUDA tensors in, torch
 tensors out; every step runs in the library's kernels behind the C ABI
 (include/ssd.h), on `stream` or the current stream of the current device, whose
 tensors they have to be.  A call on another stream
@@ -94,16 +94,18 @@ def _rows_dense(name, t):
         raise ValueError(f"{name}: the last two dimensions must be contiguous")
 
 
-def _linattn_dims(q, k, v, scale, log_decay, do, step):
-    """(dims, workspace bytes forward, backward) after the operands' checks."""
+def _qkv_dims(q, k, v, scale, gates, do, step, check_gates, size):
+    """(dims, workspace bytes forward, backward) after the operands' checks.
+    gates: (name, tensor) of those that go with the heads; check_gates(B, T, H,
+    device) looks at their shapes; size: the library's function for the bytes."""
     scale = float(scale)
-    key = (step, q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape, v.stride(),
-           v.dtype, log_decay.shape, log_decay.dtype, log_decay.is_contiguous(), scale,
-           None if do is None else (do.shape, do.stride(), do.dtype))
+    key = (size, step, q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape,
+           v.stride(), v.dtype, scale, None if do is None else (do.shape, do.stride(), do.dtype),
+           *((t.shape, t.dtype, t.is_contiguous()) for _, t in gates))
     dev = q.device
     if not q.is_cuda:
         raise ValueError("q: must be a CUDA tensor (no CPU path exists)")
-    for name, t in (("k", k), ("v", v), ("log_decay", log_decay), ("do", do)):
+    for name, t in (("k", k), ("v", v), *gates, ("do", do)):
         if t is not None and t.device != dev:
             raise ValueError(f"{name}: on {t.device}, expected {dev}")
     got = _layouts.get(key)
@@ -125,16 +127,23 @@ def _linattn_dims(q, k, v, scale, log_decay, do, step):
     for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
         if t is not None:
             _rows_dense(name, t)
-    _expect("log_decay", log_decay, torch.float32,
-            (B, H) if step and log_decay.dim() == 2 else (H,), dev)
+    check_gates(B, T, H, dev)
     s = (lambda t: (t.stride(0), 0)) if step else (lambda t: (t.stride(0), t.stride(1)))
     d = nat.LinattnDims(B, T, H, G, K, V, *s(q), *s(k), *s(v), *(s(do) if do is not None else (0, 0)),
                         scale, code)
-    size = _call("ssd_linattn_workspace_bytes")
-    need = size(d, 0), size(d, 1)
+    need = _call(size)(d, 0), _call(size)(d, 1)
     if not all(need):
         raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "dims rejected")
     return _layouts.keep(key, (d, *need))
+
+
+def _linattn_dims(q, k, v, scale, log_decay, do, step):
+    """(dims, workspace bytes forward, backward) after the operands' checks."""
+    def gates(B, T, H, dev):
+        _expect("log_decay", log_decay, torch.float32,
+                (B, H) if step and log_decay.dim() == 2 else (H,), dev)
+    return _qkv_dims(q, k, v, scale, (("log_decay", log_decay),), do, step, gates,
+                     "ssd_linattn_workspace_bytes")
 
 
 def _linattn_checks(d, dev, states, lens):
@@ -221,6 +230,26 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
     return g
 
 
+def _step_out(d, v, state, slots, state_out, out):
+    """(o, new states, rows of the states) of one token's call after the checks."""
+    dev = v.device
+    rows = state.shape[0] if state.dim() else 0
+    _expect("state", state, torch.float32, (rows, d.nheads, d.dv, d.dk), dev)
+    if slots is not None:
+        _expect("slots", slots, torch.int32, (d.batch,), dev)
+    elif rows != d.batch:
+        raise ValueError(f"state: {rows} rows, expected {d.batch}")
+    if state_out is None:
+        state_out = torch.empty_like(state) if slots is None else state
+    else:
+        _expect("state_out", state_out, torch.float32, state.shape, dev)
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    else:
+        _expect("out", out, v.dtype, v.shape, dev)
+    return out, state_out, rows
+
+
 def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=None, out=None,
                  stream=None):
     """One token of every row: q, k [B,G,K], v [B,H,V]; log_decay [H], or
@@ -236,25 +265,114 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
     d = _linattn_dims(q, k, v, scale, log_decay, None, True)[0]
     dev = q.device
     _check_device(dev, stream)
-    rows = state.shape[0] if state.dim() else 0
-    _expect("state", state, torch.float32, (rows, d.nheads, d.dv, d.dk), dev)
-    if slots is not None:
-        _expect("slots", slots, torch.int32, (d.batch,), dev)
-    elif rows != d.batch:
-        raise ValueError(f"state: {rows} rows, expected {d.batch}")
-    if state_out is None:
-        state_out = torch.empty_like(state) if slots is None else state
-    else:
-        _expect("state_out", state_out, torch.float32, state.shape, dev)
-    if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    else:
-        _expect("out", out, v.dtype, v.shape, dev)
+    out, state_out, rows = _step_out(d, v, state, slots, state_out, out)
     _streams.keep(stream, q, k, v, log_decay, state, slots, out, state_out)
     nat.check(_call("ssd_linattn_step")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
         d.nheads if log_decay.dim() == 2 else 0, state.data_ptr(), state_out.data_ptr(),
         _ptr(slots), rows, out.data_ptr(), _streams.handle(stream, dev)))
+    return out, state_out
+
+
+# ---- the gated delta rule ------------------------------------------------------------
+
+def _delta_dims(q, k, v, scale, log_decay, beta, do, step):
+    """(dims, workspace bytes forward, backward) after the operands' checks."""
+    def gates(B, T, H, dev):
+        shape = (B, H) if step else (B, T, H)
+        _expect("log_decay", log_decay, torch.float32, shape, dev)
+        _expect("beta", beta, torch.float32, shape, dev)
+    return _qkv_dims(q, k, v, scale, (("log_decay", log_decay), ("beta", beta)), do, step, gates,
+                     "ssd_delta_rule_workspace_bytes")
+
+
+def delta_rule_workspace_bytes(q, k, v, log_decay, beta, *, backward=False) -> int:
+    """Bytes of the `workspace` that delta_rule_forward (or _backward) takes."""
+    return _delta_dims(q, k, v, 1.0, log_decay, beta, None, False)[2 if backward else 1]
+
+
+def delta_rule_forward(q, k, v, log_decay, beta, state0=None, *, scale=1.0, lens=None,
+                       want_state=True, out=None, workspace=None, stream=None):
+    """The gated delta rule over [B, T] steps: with a_t = exp(log_decay_t),
+    e_t = v_t - a_t S_{t-1} k_t, S_t = a_t S_{t-1} + beta_t e_t k_t^T,
+    o_t = scale S_t q_t.
+
+    q, k [B,T,G,K], v [B,T,H,V] (fp32 or bf16; head h uses group h // (H/G);
+    the last two dimensions contiguous, the others may be strided); log_decay
+    (<= 0), beta [B,T,H] fp32; state0 [B,H,V,K] fp32 or None (zeros); lens [B]
+    int32 on the device: row b has lens[b] steps (o is zero past them).  K and V
+    are multiples of 8 up to 128.  Returns (o [B,T,H,V], final state [B,H,V,K]
+    or None); out: dict of preallocated "o", "state".
+
+    State, sums and decays are fp32; a bf16 o is off by its own rounding alone
+    (0.0017 of its root mean square)."""
+    d, need, _ = _delta_dims(q, k, v, scale, log_decay, beta, None, False)
+    dev = q.device
+    _check_device(dev, stream)
+    out = {} if out is None else out
+    o, state = out.get("o"), out.get("state")
+    shape = _linattn_checks(d, dev, (("state0", state0), ("out state", state)), lens)
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    else:
+        _expect("out o", o, v.dtype, v.shape, dev)
+    if state is None and want_state:
+        state = torch.empty(shape, dtype=torch.float32, device=dev)
+    if workspace is not None or need > 256:
+        workspace = _workspace(workspace, need, dev)
+    _streams.keep(stream, q, k, v, log_decay, beta, state0, lens, o, state, workspace)
+    nat.check(_call("ssd_delta_rule_forward")(
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
+        _ptr(state0), _ptr(lens), o.data_ptr(), _ptr(state), _ptr(workspace), _size(workspace),
+        _streams.handle(stream, dev)))
+    return o, state
+
+
+def delta_rule_backward(q, k, v, log_decay, beta, state0, do, dstate=None, *, scale=1.0, lens=None,
+                        want_dstate0=True, out=None, workspace=None, stream=None):
+    """Gradients of sum(do * o) + sum(dstate * state) of delta_rule_forward: dict
+    dq, dk, dv, dlog_decay, dbeta (fp32), dstate0 (or None).  do [B,T,H,V] may be
+    strided like v; dstate [B,H,V,K] fp32 or None (zero).  dq, dk and dv are
+    rounded once."""
+    d, _, need = _delta_dims(q, k, v, scale, log_decay, beta, do, False)
+    dev = q.device
+    _check_device(dev, stream)
+    g = dict(out) if out is not None else {}
+    shape = _linattn_checks(d, dev, (("state0", state0), ("dstate", dstate),
+                                     ("out dstate0", g.get("dstate0"))), lens)
+    for name, t in (("dq", q), ("dk", k), ("dv", v), ("dlog_decay", log_decay), ("dbeta", beta)):
+        if g.get(name) is None:
+            g[name] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+        else:
+            _expect("out " + name, g[name], t.dtype, t.shape, dev)
+    if not want_dstate0:
+        g["dstate0"] = None
+    elif g.get("dstate0") is None:
+        g["dstate0"] = torch.empty(shape, dtype=torch.float32, device=dev)
+    workspace = _workspace(workspace, need, dev)
+    _streams.keep(stream, q, k, v, log_decay, beta, state0, do, dstate, lens, workspace, *g.values())
+    nat.check(_call("ssd_delta_rule_backward")(
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
+        _ptr(state0), do.data_ptr(), _ptr(dstate), _ptr(lens), g["dq"].data_ptr(),
+        g["dk"].data_ptr(), g["dv"].data_ptr(), g["dlog_decay"].data_ptr(), g["dbeta"].data_ptr(),
+        _ptr(g["dstate0"]), _ptr(workspace), _size(workspace), _streams.handle(stream, dev)))
+    return g
+
+
+def delta_rule_step(q, k, v, log_decay, beta, state, *, scale=1.0, slots=None, state_out=None,
+                    out=None, stream=None):
+    """One token of every row: q, k [B,G,K], v [B,H,V], log_decay, beta [B,H]
+    fp32; state [rows,H,V,K] fp32, slots and state_out as in linattn_step.
+    Returns (o [B,H,V], state_out)."""
+    d = _delta_dims(q, k, v, scale, log_decay, beta, None, True)[0]
+    dev = q.device
+    _check_device(dev, stream)
+    out, state_out, rows = _step_out(d, v, state, slots, state_out, out)
+    _streams.keep(stream, q, k, v, log_decay, beta, state, slots, out, state_out)
+    nat.check(_call("ssd_delta_rule_step")(
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
+        state.data_ptr(), state_out.data_ptr(), _ptr(slots), rows, out.data_ptr(),
+        _streams.handle(stream, dev)))
     return out, state_out
 
 
@@ -376,6 +494,90 @@ def block_norm_backward(new_residual, y, z, w_post, res_scale, w_pre, eps, dx, d
         w_post.data_ptr(), _ptr(res_scale), w_pre.data_ptr(), float(eps), _ptr(stats),
         dx.data_ptr(), _ptr(dnew), g["dresidual"].data_ptr(), g["dy"].data_ptr(), _ptr(g["dz"]),
         g["dw_post"].data_ptr(), _ptr(g["dres_scale"]), g["dw_pre"].data_ptr(),
+        workspace.data_ptr(), _size(workspace), _streams.handle(stream, dev)))
+    return g
+
+
+# ---- layer norm ------------------------------------------------------------------------
+
+def _layer_norm_args(x, weight, bias):
+    """(rows, width, dtype code, row stride, workspace bytes) after the checks."""
+    dev = x.device
+    if not x.is_cuda:
+        raise ValueError("x: must be a CUDA tensor (no CPU path exists)")
+    key = ["layer norm", x.shape, x.stride(), x.dtype]
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            if t.device != dev:
+                raise ValueError(f"{name}: on {t.device}, expected {dev}")
+            key += (t.shape, t.stride(), t.dtype)
+        else:
+            key.append(None)
+    key = tuple(key)
+    got = _layouts.get(key)
+    if got is not None:
+        return got
+    code = _io_type("x", x)
+    if x.dim() == 0:
+        raise ValueError("x: must have a dimension")
+    width = x.shape[-1]
+    stride = _rows_of("x", x, x.shape, x.dtype, dev)
+    for name, w in (("weight", weight), ("bias", bias)):
+        if w is not None:
+            _expect(name, w, torch.float32, (width,), dev)
+    rows = x.numel() // width if width else 0
+    n = _call("ssd_layer_norm_workspace_bytes")(rows, width)
+    if n == 0:
+        raise nat.SsdError(nat.SSD_ERR_UNSUPPORTED, nat.last_error() or "shape rejected")
+    return _layouts.keep(key, (rows, width, code, stride, n))
+
+
+def layer_norm_forward(x, weight, bias, eps, *, want_stats=True, out=None, stream=None):
+    """y = (x - mean) / sqrt(variance + eps) * weight + bias over the last
+    dimension (up to 8192).  x: fp32 or bf16, rows evenly spaced; weight, bias
+    [width] fp32 or None (1, 0).  Returns (y, stats [..., 2] fp32 for the
+    backward or None); out: a preallocated y (may be `x` itself)."""
+    rows, width, code, stride, _ = _layer_norm_args(x, weight, bias)
+    dev = x.device
+    _check_device(dev, stream)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _expect("out", out, x.dtype, x.shape, dev)
+    stats = torch.empty(*x.shape[:-1], 2, dtype=torch.float32, device=dev) if want_stats else None
+    _streams.keep(stream, x, weight, bias, out, stats)
+    nat.check(_call("ssd_layer_norm_forward")(
+        rows, width, code, x.data_ptr(), stride, _ptr(weight), _ptr(bias), float(eps),
+        out.data_ptr(), _ptr(stats), _streams.handle(stream, dev)))
+    return out, stats
+
+
+def layer_norm_backward(x, weight, dy, eps, stats=None, *, want_dweight=True, want_dbias=True,
+                        out=None, workspace=None, stream=None):
+    """Gradients of sum(dy * y) of layer_norm_forward: dict dx, dweight, dbias
+    (fp32; None where not wanted).  stats as the forward returned them, or None
+    (recomputed); out: dict of preallocated gradients (dx may be `x` or `dy`)."""
+    rows, width, code, stride, need = _layer_norm_args(x, weight, None)
+    dev = x.device
+    _check_device(dev, stream)
+    _expect("dy", dy, x.dtype, x.shape, dev)
+    if stats is not None:
+        _expect("stats", stats, torch.float32, (*x.shape[:-1], 2), dev)
+    g = dict(out) if out is not None else {}
+    for name, dt, shape, want in (("dx", x.dtype, x.shape, True),
+                                  ("dweight", torch.float32, (width,), want_dweight),
+                                  ("dbias", torch.float32, (width,), want_dbias)):
+        if not want:
+            g[name] = None
+        elif g.get(name) is None:
+            g[name] = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _expect("out " + name, g[name], dt, shape, dev)
+    workspace = _workspace(workspace, need, dev)
+    _streams.keep(stream, x, weight, dy, stats, workspace, *g.values())
+    nat.check(_call("ssd_layer_norm_backward")(
+        rows, width, code, x.data_ptr(), stride, _ptr(weight), float(eps), _ptr(stats),
+        dy.data_ptr(), g["dx"].data_ptr(), _ptr(g["dweight"]), _ptr(g["dbias"]),
         workspace.data_ptr(), _size(workspace), _streams.handle(stream, dev)))
     return g
 

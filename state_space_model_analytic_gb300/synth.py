@@ -225,3 +225,22 @@ def linattn_inputs(batch: int, seqlen: int, heads: int, groups: int, dk: int, dv
     f = lambda a: round_to(a, "f32")
     return {"q": r(q), "k": r(k), "v": r(v), "do": r(do), "state0": f(s0), "dstate": f(ds),
             "log_decay": f(la)}
+
+
+def delta_inputs(batch: int, seqlen: int, heads: int, groups: int, dk: int, dv: int, dtype: str,
+                 seed: int, decays=None) -> dict:
+    """Delta-rule inputs: those of linear attention with the rows of q and k
+    silu(N(0, 1)) scaled to length 1 (keys of different steps are alike);
+    log_decay [B,T,H]: `decays` repeated over the steps, or -U[0, 1] r with r of
+    2^U[-8, 0] a head; beta [B,T,H] ~ U[0, 1]."""
+    inp = linattn_inputs(batch, seqlen, heads, groups, dk, dv, dtype, seed)
+    rng = np.random.Generator(np.random.PCG64(seed + 1000))
+    for n in "qk":
+        x = inp[n] / (1.0 + np.exp(-inp[n]))
+        inp[n] = round_to(x / np.sqrt((x * x).sum(-1, keepdims=True) + 1e-6), dtype)
+    shape = (batch, seqlen, heads)
+    rate = np.exp2(rng.uniform(-8.0, 0.0, size=(heads,)))
+    la = (-rng.uniform(0.0, 1.0, size=shape) * rate if decays is None else
+          np.resize(np.asarray(decays, float), shape))
+    return {**inp, "log_decay": round_to(la, "f32"),
+            "beta": round_to(rng.uniform(0.0, 1.0, size=shape), "f32")}

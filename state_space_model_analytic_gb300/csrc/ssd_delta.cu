@@ -46,9 +46,8 @@ struct Geom {
   static constexpr int MT = kParts * C * PB, PT = PP * C * PB;
   static constexpr int kStage = 2 * KT + VT;
   static constexpr int kM = NS * kStage, kP = kM + 2 * MT;
-  static constexpr int kG = kP + 2 * PT, kS = kG + 2 * (int)sizeof(Gates<C>);
+  static constexpr int kG = kP + 2 * PT, kS = kG + 3 * (int)sizeof(Gates<C>);
   static constexpr size_t smem = kS + sizeof(Scratch<C>);
-  static_assert(sizeof(Gates<C>) % 4 == 0, "");
 };
 
 // fp32 rows of v: C x kVB floats
@@ -127,21 +126,34 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
   }
 }
 
-// acc[n] += X K^T for the C steps of a tile whose rows are steps: X the state's
-// PS parts.
-template <int NI, int PS, int DK, int NK, int NC>
-__device__ __forceinline__ void state_times(float (&acc)[NC][4], const float (&x)[NK][4],
-                                            uint32_t tile, int lane) {
+// f[n] += X K^T for the C steps of a tile whose rows are steps, X the state with all
+// its parts; and with PO > 0 o[n] += X Q^T with PO of them.
+template <int NI, int PO, int DK, int NK, int NC>
+__device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
+                                            const float (&x)[NK][4], uint32_t K, uint32_t Q, int lane) {
   constexpr int C = kSteps<NI>, RB = DK * 2;
 #pragma unroll
   for (int k = 0; k < NK; k += 2) {
-    uint32_t a[PS][4];
-    as_left<PS>(a, x[k], x[k + 1]);
+    uint32_t a[kParts][4];
+    as_left<kParts>(a, x[k], x[k + 1]);
 #pragma unroll
     for (int n = 0; n < NC; n += 4) {
       uint32_t b[NI][4][2];
-      load_right<RB, NI, 4>(b, tile, C * RB, lane, 8 * n, 8 * k);
-      mma_parts<PS, NI, 4>(acc + n, a, b);
+      load_right<RB, NI, 4>(b, K, C * RB, lane, 8 * n, 8 * k);
+      mma_parts<kParts, NI, 4>(f + n, a, b);
+    }
+    if constexpr (PO > 0) {
+      uint32_t ao[PO][4];
+#pragma unroll
+      for (int q = 0; q < PO; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ao[q][e] = a[q][e];
+#pragma unroll
+      for (int n = 0; n < NC; n += 4) {
+        uint32_t b[NI][4][2];
+        load_right<RB, NI, 4>(b, Q, C * RB, lane, 8 * n, 8 * k);
+        mma_parts<PO, NI, 4>(o + n, ao, b);
+      }
     }
   }
 }
@@ -210,21 +222,30 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
         load_floats<C, G::LV>(st + 2 * G::KT, (const float*)vp + t0 * p.v.step, p.v.step, n,
                               p.dv - v0, tid);
     };
-    NextGates ng;
+    // the gates of chunk c + 1 are made ready beside the preparation of chunk c, by
+    // the last warp, which has loaded them one chunk earlier
+    RawGates<C> raw;
+    auto load_raw = [&](int c) {
+      load_gates<C>(raw, p.log_decay, p.beta, gate0 + (long long)c * C * p.H, p.H, len - c * C, lane);
+    };
     auto prep = [&](int c) {
-      const int i = c & 1;
-      const NextGates now = ng;
-      ng = load_gates<C>(p.log_decay, p.beta, gate0 + (long long)(c + 1) * C * p.H, p.H,
-                         len - (c + 1) * C, tid);
-      prepare<NI, DK, PP, !kStates>(stage(c), stage(c) + G::KT, sm + G::kM + i * G::MT,
-                                    sm + G::kP + i * G::PT, gates[i], scratch, now, p.scale, tid);
+      prepare<NI, DK, PP, !kStates>(stage(c), stage(c) + G::KT, sm + G::kM + (c & 1) * G::MT,
+                                    sm + G::kP + (c & 1) * G::PT, gates[c % 3], scratch, p.scale, tid,
+                                    [&] {
+                                      scan_gates<C>(gates[(c + 1) % 3], raw, lane);
+                                      load_raw(c + 2);
+                                    });
     };
     if (nc > 0) {
-      ng = load_gates<C>(p.log_decay, p.beta, gate0, p.H, len, tid);
       load(0);
       copy_commit();
       if (G::NS > 2 && nc > 1) load(1);
       copy_commit();
+      if (warp == 3) {
+        load_raw(0);
+        scan_gates<C>(gates[0], raw, lane);
+        load_raw(1);
+      }
       copy_wait<1>();
       bar(1, kPrep);
       prep(0);
@@ -251,7 +272,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
       const uint8_t* st = stage(c);
       const uint32_t Q = smem32(st), K = Q + G::KT, V = K + G::KT;
       const uint32_t M = smem32(sm + G::kM + (c & 1) * G::MT), P = smem32(sm + G::kP + (c & 1) * G::PT);
-      const Gates<C>& g = gates[c & 1];
+      const Gates<C>& g = gates[c % 3];
       const int n = min(C, len - c * C);
       if (kStates) put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, p.dk, lane);
       // f: F^T, then U^T; o: O^T
@@ -260,8 +281,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
       for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[i][e] = o[i][e] = 0.f;
-      state_times<NI, kParts, DK, NK, NC>(f, x, K, lane);
-      if constexpr (!kStates) state_times<NI, PP, DK, NK, NC>(o, x, Q, lane);
+      state_times<NI, kStates ? 0 : PP, DK, NK, NC>(f, o, x, K, Q, lane);
 #pragma unroll
       for (int i = 0; i < NC; i += 2) {
         float val[2][4];
@@ -313,7 +333,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
           }
         }
         as_left<kParts>(a, y[0], y[1]);
-        load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
+        load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
         mma_parts<kParts, kParts, 2>(d, a, r);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -415,23 +435,29 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
       load_tile<NI, C, kVB, kPrep>(st + 2 * G::KT, gp + t0 * p.dout.step, p.dout.step, n, p.dv - v0,
                                    tid);
     };
-    NextGates ng;
-    auto gates_of = [&](int c) {
-      return load_gates<C>(p.log_decay, p.beta, gate0 + (long long)c * C * p.H, p.H, len - c * C, tid);
+    RawGates<C> raw;
+    auto load_raw = [&](int c) {  // (a chunk before the first has no steps)
+      load_gates<C>(raw, p.log_decay, p.beta, gate0 + (long long)c * C * p.H, p.H,
+                    c < 0 ? 0 : len - c * C, lane);
     };
     auto prep = [&](int c) {
-      const int i = c & 1;
-      const NextGates now = ng;
-      if (c > 0) ng = gates_of(c - 1);
-      prepare<NI, DK, kParts, true>(stage(c), stage(c) + G::KT, sm + G::kM + i * G::MT,
-                                    sm + G::kP + i * G::PT, gates[i], scratch, now, p.scale, tid);
+      prepare<NI, DK, kParts, true>(stage(c), stage(c) + G::KT, sm + G::kM + (c & 1) * G::MT,
+                                    sm + G::kP + (c & 1) * G::PT, gates[c % 3], scratch, p.scale, tid,
+                                    [&] {
+                                      scan_gates<C>(gates[(c + 2) % 3], raw, lane);  // (c - 1)
+                                      load_raw(c - 2);
+                                    });
     };
     if (nc > 0) {
-      ng = gates_of(nc - 1);
       load(nc - 1);
       copy_commit();
       if (G::NS > 2 && nc > 1) load(nc - 2);
       copy_commit();
+      if (warp == 3) {
+        load_raw(nc - 1);
+        scan_gates<C>(gates[(nc - 1) % 3], raw, lane);
+        load_raw(nc - 2);
+      }
       copy_wait<1>();
       bar(1, kPrep);
       prep(nc - 1);
@@ -456,7 +482,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
     for (int c = nc - 1; c >= 0; --c) {
       const uint32_t Q = smem32(stage(c)), K = Q + G::KT, dO = K + G::KT;
       const uint32_t M = smem32(sm + G::kM + (c & 1) * G::MT), P = smem32(sm + G::kP + (c & 1) * G::PT);
-      const Gates<C>& g = gates[c & 1];
+      const Gates<C>& g = gates[c % 3];
       const int n = min(C, len - c * C);
       put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, p.dk, lane);
       float f[NC][4];  // dU^T, then dv^T
@@ -464,7 +490,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
       for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[i][e] = 0.f;
-      state_times<NI, kParts, DK, NK, NC>(f, x, K, lane);
+      state_times<NI, 0, DK, NK, NC>(f, f, x, K, K, lane);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const float2 t = *(const float2*)&g.tail[8 * i + c2];
@@ -503,7 +529,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
           }
         }
         as_left<kParts>(a, y[0], y[1]);
-        load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
+        load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
         mma_parts<kParts, kParts, 2>(d, a, r);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {

@@ -243,188 +243,241 @@ __device__ __forceinline__ void load_tile(uint8_t* tile, const void* src, long l
   }
 }
 
-// Per step of a chunk: the sum of the log decays as two floats (a difference of
-// two sums is then good to its own last bit however long they have grown), the
-// write strength, and e^g, e^{G-g}.
+// Per step of a chunk: the sum g of the log decays (of base 2), as two floats, so that
+// a difference of two sums is good to its own last bit however long they have grown;
+// the write strength; and e^g, e^{G-g}.
 template <int C>
 struct alignas(16) Gates {
   float hi[C], lo[C], beta[C], lead[C], tail[C];
   float last;  // e^G
 };
 
-// log_decay below -200 is as good as -inf (e^-104 is the smallest float) and keeps
-// sums finite; NaN stays
-__device__ __forceinline__ float clamp_decay(float x) { return x < -200.f ? -200.f : x; }
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+  const float hi = s + e;
+  return {hi, e - (hi - s)};
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^x: the hardware's (2^-22) with the second float's share
+__device__ __forceinline__ float exp2_of(Two x) {
+  const float e = exp2_fast(x.hi);
+  return fmaf(e, x.lo * 0.693147181f, e);
+}
 
-// One warp; raw: C log decays (zero past the chunk's end).
+// A warp's gates of a chunk on their way: C / 32 steps a lane.
 template <int C>
-__device__ __forceinline__ void scan_gates(Gates<C>& g, const float* raw, int lane) {
-  constexpr int N = C / 32;
-  double s[N];
+struct RawGates {
+  float decay[C / 32], beta[C / 32];
+};
+// (log decays of base 2; below -200 a log decay is as good as -inf, as e^-104 is the
+// smallest float, and keeps sums finite; NaN stays; past n 0)
+template <int C>
+__device__ __forceinline__ void load_gates(RawGates<C>& x, const float* log_decay, const float* beta,
+                                           long long at, long long stride, int n, int lane) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = raw[lane * N + i] + (i ? s[i ? i - 1 : 0] : 0.0);
-  double before = s[N - 1];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
+  for (int i = 0; i < C / 32; ++i) {
+    const int r = lane * (C / 32) + i;
+    float d = 0.f, b = 0.f;
+    if (r < n) {
+      d = log_decay[at + r * stride];
+      b = beta[at + r * stride];
+    }
+    x.decay[i] = d < -200.f ? -200.f : d;
+    x.beta[i] = b;
   }
-  const double total = __shfl_sync(0xffffffffu, before, 31);
-  before = __shfl_up_sync(0xffffffffu, before, 1);
-  if (lane == 0) before = 0.0;
+}
+template <int C>
+__device__ __forceinline__ void scan_gates(Gates<C>& g, const RawGates<C>& raw, int lane) {
+  constexpr int N = C / 32;
+  constexpr float kLog2e = 1.44269504f, kLog2eLo = 1.92596303e-8f;  // their sum: 48 bits
+  Two s[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const double x = before + s[i];
-    const float hi = (float)x;
-    g.hi[lane * N + i] = hi;
-    g.lo[lane * N + i] = (float)(x - hi);
-    g.lead[lane * N + i] = expf(hi);
-    g.tail[lane * N + i] = expf((float)(total - x));
+    const float d = raw.decay[i], hi = d * kLog2e;
+    s[i] = {hi, fmaf(d, kLog2e, -hi) + d * kLog2eLo};
+    if (i) s[i] = add(s[i ? i - 1 : 0], s[i]);
   }
-  if (lane == 0) g.last = expf((float)total);
+  Two before = s[N - 1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two x = {__shfl_up_sync(0xffffffffu, before.hi, o), __shfl_up_sync(0xffffffffu, before.lo, o)};
+    if (lane >= o) before = add(x, before);
+  }
+  const Two total = {__shfl_sync(0xffffffffu, before.hi, 31), __shfl_sync(0xffffffffu, before.lo, 31)};
+  before = {__shfl_up_sync(0xffffffffu, before.hi, 1), __shfl_up_sync(0xffffffffu, before.lo, 1)};
+  if (lane == 0) before = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const Two x = add(before, s[i]), rest = add(total, {-x.hi, -x.lo});
+    const int r = lane * N + i;
+    g.hi[r] = x.hi;
+    g.lo[r] = x.lo;
+    g.beta[r] = raw.beta[i];
+    g.lead[r] = exp2_of(x);
+    g.tail[r] = exp2_of(rest);
+  }
+  if (lane == 0) g.last = exp2_of(total);
 }
 // Gamma_ij
-template <int C>
-__device__ __forceinline__ float decay(const Gates<C>& g, int i, int j) {
-  return expf((g.hi[i] - g.hi[j]) + (g.lo[i] - g.lo[j]));
+__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
+  return exp2_fast((hi_i - hi_j) + (lo_i - lo_j));
 }
 
-// What the walks read of a chunk besides its operands: -X in the blocks of 16 on
-// the diagonal and -L below them, and P, in parts (tiles [C][C]).
-constexpr int kDiag = 20;  // floats of a row of a diagonal block
+// What the walks read of a chunk besides its operands, in parts (tiles [C][C]): in M
+// -L below the blocks of 16 on the diagonal and in them -X^T, and P.
+constexpr int kDiag = 20;  // floats of a column of a diagonal block
 template <int C>
 struct alignas(16) Scratch {
-  float raw[C];
-  float diag[C / 16][16][kDiag];
+  float diag[C / 16][16][kDiag];  // L[i][j] at [j][i]
 };
 
-// Rows 16 s ... 16 s + 15 of A K^T, columns up to the diagonal block's end, times
-// the decays: -L (below the diagonal blocks to `out`, in them to the scratch), or
-// factor * (values on and below the diagonal) to `out`.
-template <int NI, int DK, int PO, bool kL>
-__device__ __forceinline__ void scores(uint32_t A, uint32_t K, uint8_t* out, int s,
+// Rows 16 S0 ... 16 S0 + 15 and, for S1 > S0, 16 S1 ... of A K^T, columns up to the
+// diagonal block's end, times the decays: -L (below the diagonal blocks to `out`, in
+// them to the scratch), or factor * (values on and below the diagonal) to `out`.
+template <int NI, int DK, int PO, bool kL, int S0, int S1>
+__device__ __forceinline__ void scores(uint32_t A, uint32_t K, uint8_t* out,
                                        const Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc,
-                                       float factor, int lane, int wait_bar) {
-  constexpr int C = kSteps<NI>, RB = DK * 2, OB = C * 2, NT = C / 8;
-  float acc[NT][4];
+                                       float factor, int lane) {
+  constexpr int C = kSteps<NI>, RB = DK * 2, OB = C * 2;
+  constexpr int N0 = 2 * S0 + 2, N1 = S1 > S0 ? 2 * S1 + 2 : 0, N = N1 > N0 ? N1 : N0;
+  float acc[N0 + N1][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int n = 0; n < N0 + N1; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll 2
+#pragma unroll(NI == 1 ? 2 : 1)
   for (int k = 0; k < DK; k += 16) {
-    uint32_t a[NI][4];
+    uint32_t a0[NI][4], a1[NI][4];
 #pragma unroll
-    for (int p = 0; p < NI; ++p) ldm4(a[p], A + p * C * RB + left<RB>(lane, 16 * s, k));
+    for (int p = 0; p < NI; ++p) {
+      ldm4(a0[p], A + p * C * RB + left<RB>(lane, 16 * S0, k));
+      if (N1) ldm4(a1[p], A + p * C * RB + left<RB>(lane, 16 * S1, k));
+    }
+    uint32_t b[NI][N][2];
+    load_right<RB, NI, N>(b, K, C * RB, lane, 0, k);
+    if constexpr (N1 > 0) mma_parts<NI, NI, N>(acc + N0, a1, b);
 #pragma unroll
-    for (int n = 0; n < NT; n += 2)
-      if (n <= 2 * s) {
-        uint32_t b[NI][2][2];
-        load_right<RB, NI, 2>(b, K, C * RB, lane, 8 * n, k);
-        mma_parts<NI, NI, 2>(acc + n, a, b);
-      }
+    for (int n = 0; n < N0; n += 2) {
+      uint32_t b2[NI][2][2];
+#pragma unroll
+      for (int p = 0; p < NI; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b2[p][i >> 1][i & 1] = b[p][n + (i >> 1)][i & 1];
+      mma_parts<NI, NI, 2>(acc + n, a0, b2);
+    }
   }
-  if (wait_bar) bar(wait_bar, kPrep);  // the gates are there
-  const int r0 = 16 * s + (lane >> 2), c0 = (lane & 3) * 2;
+  const int c0 = (lane & 3) * 2;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-    if (n <= 2 * s + 1) {
-      const bool diag = n >= 2 * s;
+  for (int strip = 0; strip < (N1 ? 2 : 1); ++strip) {
+    const int S = strip ? S1 : S0;
+    const int r0 = 16 * S + (lane >> 2);
+    const float hi0 = g.hi[r0], lo0 = g.lo[r0], hi1 = g.hi[r0 + 8], lo1 = g.lo[r0 + 8];
+#pragma unroll
+    for (int n = 0; n < (strip ? N1 : N0); ++n) {
+      const float* v = acc[strip ? N0 + n : n];
+      const bool diag = n >= 2 * S;
+      const float2 hj = *(const float2*)&g.hi[8 * n + c0], lj = *(const float2*)&g.lo[8 * n + c0];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = r0 + 8 * u, j = 8 * n + c0;
-        float x[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          x[e] = (kL ? j + e < i : j + e <= i) ? acc[n][2 * u + e] * factor * decay(g, i, j + e) : 0.f;
+        const float hi = u ? hi1 : hi0, lo = u ? lo1 : lo0;
+        float x = v[2 * u] * factor * decay(hi, lo, hj.x, lj.x);
+        float y = v[2 * u + 1] * factor * decay(hi, lo, hj.y, lj.y);
+        if (diag) {
+          if (kL ? j >= i : j > i) x = 0.f;
+          if (kL ? j + 1 >= i : j + 1 > i) y = 0.f;
+        }
         if (kL && diag) {
-          float* d = &sc.diag[s][i & 15][j & 15];
-          d[0] = x[0];
-          d[1] = x[1];
+          sc.diag[S][j & 15][i & 15] = x;
+          sc.diag[S][(j & 15) + 1][i & 15] = y;
         } else {
           uint32_t p[PO];
-          split2<PO>(kL ? -x[0] : x[0], kL ? -x[1] : x[1], p);
+          split2<PO>(kL ? -x : x, kL ? -y : y, p);
           uint8_t* at = out + at16<OB>(i, n) + c0 * 2;
 #pragma unroll
           for (int q = 0; q < PO; ++q) *(uint32_t*)(at + q * C * OB) = p[q];
         }
       }
     }
+  }
 }
 
-// One thread a column of a diagonal block: with T = (I + beta L)^-1 column j by
-// forward substitution, X_ij = sum_m L_im T_mj and T_ij = -beta_i X_ij.
+// One thread a column j of a diagonal block: with T = (I + beta L)^-1, X = L T and
+// T = I - beta X, so once X_mj is whole, T_mj = -beta_m X_mj (1 for m = j) adds
+// L_im T_mj to every later X_ij.
 template <int C>
 __device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, const Scratch<C>& sc,
                                             int tid) {
   constexpr int OB = C * 2;
   const int s = tid >> 4, j = tid & 15;
-  float t[16];
+  float x[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float x = 0.f;
+  for (int i = 0; i < 16; ++i) x[i] = 0.f;
 #pragma unroll
-    for (int m = 0; m < i; m += 4) {
-      const float4 l = *(const float4*)&sc.diag[s][i][m];
-      x = fmaf(l.x, t[m], x);
-      if (m + 1 < i) x = fmaf(l.y, t[m + 1 < 16 ? m + 1 : 0], x);
-      if (m + 2 < i) x = fmaf(l.z, t[m + 2 < 16 ? m + 2 : 0], x);
-      if (m + 3 < i) x = fmaf(l.w, t[m + 3 < 16 ? m + 3 : 0], x);
+  for (int m = 0; m < 15; ++m) {
+    const float t = m == j ? 1.f : -g.beta[16 * s + m] * x[m];
+#pragma unroll
+    for (int i = (m + 1) / 4 * 4; i < 16; i += 4) {
+      const float4 l = *(const float4*)&sc.diag[s][m][i];
+      if (i > m) x[i] = fmaf(l.x, t, x[i]);
+      if (i + 1 > m) x[i + 1] = fmaf(l.y, t, x[i + 1]);
+      if (i + 2 > m) x[i + 2] = fmaf(l.z, t, x[i + 2]);
+      if (i + 3 > m) x[i + 3] = fmaf(l.w, t, x[i + 3]);
     }
-    t[i] = i == j ? 1.f : -g.beta[16 * s + i] * x;
-    uint32_t p[kParts];
-    split2<kParts>(i > j ? -x : 0.f, 0.f, p);
-    uint8_t* at = out + at16<OB>(16 * s + i, 2 * s + (j >> 3)) + (j & 7) * 2;
+  }
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) *(uint16_t*)(at + q * C * OB) = (uint16_t)p[q];
+  for (int h = 0; h < 2; ++h) {
+    uint32_t p[4][kParts];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2<kParts>(-x[8 * h + 2 * i], -x[8 * h + 2 * i + 1], p[i]);
+    uint8_t* at = out + at16<OB>(16 * s + j, 2 * s + h);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      *(uint4*)(at + q * C * OB) = make_uint4(p[0][q], p[1][q], p[2][q], p[3][q]);
   }
 }
 
-// The gates' next values of a thread (one step a thread).
-struct NextGates {
-  float decay = 0.f, beta = 0.f;
-};
-template <int C>
-__device__ __forceinline__ NextGates load_gates(const float* log_decay, const float* beta,
-                                                long long at, long long stride, int n, int tid) {
-  NextGates x;
-  if (tid < C && tid < n) {
-    x.decay = clamp_decay(log_decay[at + tid * stride]);
-    x.beta = beta[at + tid * stride];
-  }
-  return x;
-}
-
-// Everything of a chunk whose operands are in shared memory, by the kPrep threads
-// (bar 1); kP: P too, times `scale`.
-template <int NI, int DK, int PP, bool kP>
+// M and, with kP, P times `scale` of a chunk whose operands and gates are in shared
+// memory, by the kPrep threads.  The last warp has `aside` to do as well (the gates
+// of a later chunk).
+template <int NI, int DK, int PP, bool kP, typename F>
 __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, uint8_t* M, uint8_t* P,
-                                        Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc, NextGates ng,
-                                        float scale, int tid) {
-  constexpr int C = kSteps<NI>, NB = C / 16;
+                                        const Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc,
+                                        float scale, int tid, F aside) {
+  constexpr int C = kSteps<NI>;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  if (tid < C) {
-    sc.raw[tid] = ng.decay;
-    g.beta[tid] = ng.beta;
-  }
-  bar(1, kPrep);
-  if (warp == 3) scan_gates<C>(g, sc.raw, lane);
   const uint32_t K = smem32(Kt), Q = smem32(Qt);
-  if constexpr (kP) {
+  if (warp < 2) {
     // strips of 2, 4, 6, 8 columns of eight: the first with the last
-    if (warp < 2) {
-      scores<NI, DK, kParts, true>(K, K, M, warp, g, sc, 1.f, lane, 1);
-      if constexpr (NB == 4) scores<NI, DK, kParts, true>(K, K, M, 3 - warp, g, sc, 1.f, lane, 0);
+    if constexpr (C == 64) {
+      if (warp == 0) scores<NI, DK, kParts, true, 0, 3>(K, K, M, g, sc, 1.f, lane);
+      else scores<NI, DK, kParts, true, 1, 2>(K, K, M, g, sc, 1.f, lane);
     } else {
-      scores<NI, DK, PP, false>(Q, K, P, warp - 2, g, sc, scale, lane, 1);
-      if constexpr (NB == 4) scores<NI, DK, PP, false>(Q, K, P, 5 - warp, g, sc, scale, lane, 0);
+      if (warp == 0) scores<NI, DK, kParts, true, 0, 0>(K, K, M, g, sc, 1.f, lane);
+      else scores<NI, DK, kParts, true, 1, 1>(K, K, M, g, sc, 1.f, lane);
     }
+    bar(2, 64);
+    if (tid < C) invert_diag<C>(M, g, sc, tid);
   } else {
-    if (warp < NB) scores<NI, DK, kParts, true>(K, K, M, warp, g, sc, 1.f, lane, 1);
-    else bar(1, kPrep);
+    if (kP) {
+      if constexpr (C == 64) {
+        if (warp == 2) scores<NI, DK, PP, false, 0, 3>(Q, K, P, g, sc, scale, lane);
+        else scores<NI, DK, PP, false, 1, 2>(Q, K, P, g, sc, scale, lane);
+      } else {
+        if (warp == 2) scores<NI, DK, PP, false, 0, 0>(Q, K, P, g, sc, scale, lane);
+        else scores<NI, DK, PP, false, 1, 1>(Q, K, P, g, sc, scale, lane);
+      }
+    }
+    if (warp == 3) aside();
   }
-  bar(1, kPrep);
-  if (tid < C) invert_diag<C>(M, g, sc, tid);
 }
 
 }  // namespace delta

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const DeltaGrads p,
   constexpr int C = G::C, RB = G::RB, VR = G::VR, PB = G::PB, NK = G::NK, NM = G::NM, NB = C / 16;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ Gates<C> g;
-  __shared__ float raw[C], dbeta[C], red[G::WC][C], sums[2][8];
+  __shared__ float dbeta[C], red[G::WC][C], sums[2][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int h = blockIdx.y, b = blockIdx.z, t0 = blockIdx.x * C;
   int len = p.T;
@@ -120,14 +120,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const DeltaGrads p,
   const T* gp = (const T*)p.dout.p + b * p.dout.batch + t0 * p.dout.step + (long long)h * p.dv;
   load_tile<NI, C, DK, kThreads>(sm, qp, p.q.step, n, p.dk, tid);
   load_tile<NI, C, DK, kThreads>(sm + G::kK, kp, p.k.step, n, p.dk, tid);
-  const NextGates ng = load_gates<C>(p.log_decay, p.beta, gate0, p.H, n, tid);
-  if (tid < C) {
-    raw[tid] = ng.decay;
-    g.beta[tid] = ng.beta;
-    dbeta[tid] = 0.f;
+  if (tid < C) dbeta[tid] = 0.f;
+  if (warp == 0) {
+    RawGates<C> raw;
+    load_gates<C>(raw, p.log_decay, p.beta, gate0, p.H, n, lane);
+    scan_gates<C>(g, raw, lane);
   }
   __syncthreads();
-  if (warp == 0) scan_gates<C>(g, raw, lane);
   const int strip = warp % G::WR, group = warp / G::WR;
   const bool is_l = group >= G::WC / 2;        // this warp's scores: ML's, else MP's
   const int mg = group % (G::WC / 2);
@@ -228,14 +227,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const DeltaGrads p,
 #pragma unroll
   for (int i = 0; i < NM; ++i)
     if (m0 + i <= 2 * strip + 1) {
+      const int col = 8 * (m0 + i) + c2;
+      const float2 hj = *(const float2*)&g.hi[col], lj = *(const float2*)&g.lo[col];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int row = i0 + 8 * u, col = 8 * (m0 + i) + c2;
+        const int row = i0 + 8 * u;
         float x[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const bool in = is_l ? col + e < row : col + e <= row;
-          x[e] = in ? mm[i][2 * u + e] * (is_l ? -1.f : p.scale) * decay(g, row, col + e) : 0.f;
+          x[e] = in ? mm[i][2 * u + e] * (is_l ? -1.f : p.scale) *
+                          decay(g.hi[row], g.lo[row], e ? hj.y : hj.x, e ? lj.y : lj.x)
+                    : 0.f;
         }
         uint32_t a[kParts];
         split2<kParts>(x[0], x[1], a);

@@ -127,41 +127,73 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
 }
 
 // f[n] += X K^T for the C steps of a tile whose rows are steps, X the state with all
-// its parts; and with PO > 0 o[n] += X Q^T with PO of them.
+// its parts; and with PO > 0 o[n] += X Q^T with PO of them.  The right operands of a
+// group of columns are loaded while the group before is multiplied.
 template <int NI, int PO, int DK, int NK, int NC>
 __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
                                             const float (&x)[NK][4], uint32_t K, uint32_t Q, int lane) {
   constexpr int C = kSteps<NI>, RB = DK * 2;
+  constexpr int GN = NI == 1 ? 4 : 2;                   // columns of eight of a group
+  constexpr int GF = NC / GN, GK = PO > 0 ? 2 * GF : GF;  // groups of 16 terms
+  constexpr int NG = NK / 2 * GK;
+  uint32_t a[2][kParts][4], b[2][NI][GN][2];
+  auto load = [&](int s) {
+    const int k = s / GK, g = s % GK;
+    load_right<RB, NI, GN>(b[s & 1], g < GF ? K : Q, C * RB, lane, 8 * GN * (g % GF), 16 * k);
+  };
+  as_left<kParts>(a[0], x[0], x[1]);
+  load(0);
 #pragma unroll
-  for (int k = 0; k < NK; k += 2) {
-    uint32_t a[kParts][4];
-    as_left<kParts>(a, x[k], x[k + 1]);
-#pragma unroll
-    for (int n = 0; n < NC; n += 4) {
-      uint32_t b[NI][4][2];
-      load_right<RB, NI, 4>(b, K, C * RB, lane, 8 * n, 8 * k);
-      mma_parts<kParts, NI, 4>(f + n, a, b);
-    }
-    if constexpr (PO > 0) {
+  for (int s = 0; s < NG; ++s) {
+    const int k = s / GK, g = s % GK;
+    if (s + 1 < NG) load(s + 1);
+    if (g == 0 && 2 * k + 2 < NK) as_left<kParts>(a[(k + 1) & 1], x[2 * k + 2], x[2 * k + 3]);
+    if (g < GF) {
+      mma_parts<kParts, NI, GN>(f + GN * g, a[k & 1], b[s & 1]);
+    } else if constexpr (PO > 0) {
       uint32_t ao[PO][4];
 #pragma unroll
       for (int q = 0; q < PO; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ao[q][e] = a[q][e];
-#pragma unroll
-      for (int n = 0; n < NC; n += 4) {
-        uint32_t b[NI][4][2];
-        load_right<RB, NI, 4>(b, Q, C * RB, lane, 8 * n, 8 * k);
-        mma_parts<PO, NI, 4>(o + n, ao, b);
-      }
+        for (int e = 0; e < 4; ++e) ao[q][e] = a[k & 1][q][e];
+      mma_parts<PO, NI, GN>(o + GN * (g - GF), ao, b[s & 1]);
     }
   }
 }
 
-// x <- scale x + Y tile, Y (rows v, C steps) as parts of left operands.
-template <int NI, int DK, int NK, int NB>
+// d += a b for two columns of eight, all parts of both; the products of one order of
+// size go to a sum of their own, so that fewer wait for one another.
+__device__ __forceinline__ void mma_short(float (&d)[2][4], const uint32_t (&a)[kParts][4],
+                                          const uint32_t (&b)[kParts][2][2]) {
+  float e[2][2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) e[i][n][c] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) mma(e[0][n], a[i], b[2 - i][n][0], b[2 - i][n][1]);
+    if (i < 2)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) mma(e[1][n], a[i], b[1 - i][n][0], b[1 - i][n][1]);
+    if (i == 0)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) mma(d[n], a[0], b[0][n][0], b[0][n][1]);
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) d[n][c] += e[0][n][c] + e[1][n][c];
+}
+
+// x <- scale x + Y tile, Y (rows v, C steps) as parts of left operands.  beside(i),
+// i < NK / 4: work that is issued between the products.
+template <int NI, int DK, int NK, int NB, typename F>
 __device__ __forceinline__ void state_add(float (&x)[NK][4], float scale, const uint32_t (*y)[kParts][4],
-                                          uint32_t tile, int lane) {
+                                          uint32_t tile, int lane, F beside) {
   constexpr int C = kSteps<NI>, RB = DK * 2;
 #pragma unroll
   for (int n = 0; n < NK; n += 4) {
@@ -175,6 +207,7 @@ __device__ __forceinline__ void state_add(float (&x)[NK][4], float scale, const 
       uint32_t r[NI][4][2];
       load_right_t<RB, NI, 4>(r, tile, C * RB, lane, 8 * n, 16 * b);
       mma_parts<kParts, NI, 4>(d, y[b], r);
+      if (b == 0) beside(n / 4);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -318,11 +351,36 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
           }
         }
       }
+      // block by block: E = F - X beta F, U = beta E, and what U takes off F of the
+      // later blocks and adds to O.  The next block waits for its own share alone; the
+      // rest is issued while the next one's first product is on its way.
+      uint32_t au[kParts][4];
+      auto rest = [&](int k) {
+#pragma unroll
+        for (int i = 2 * k + 4; i < NC; i += 2) {
+          uint32_t r[kParts][2][2];
+          load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
+          mma_parts<kParts, kParts, 2>(f + i, au, r);
+        }
+        if constexpr (!kStates) {
+          uint32_t ao[PP][4];
+#pragma unroll
+          for (int q = 0; q < PP; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ao[q][e] = au[q][e];
+#pragma unroll
+          for (int i = 2 * k; i < NC; i += 2) {
+            uint32_t rp[PP][2][2];
+            load_right<G::PB, PP, 2>(rp, P, C * G::PB, lane, 8 * i, 16 * k);
+            mma_parts<PP, PP, 2>(o + i, ao, rp);
+          }
+        }
+      };
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        // E of steps 16 k ...: F - X beta F
         uint32_t a[kParts][4], r[kParts][2][2];
         float d[2][4], y[2][4];
+        load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
@@ -333,8 +391,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
           }
         }
         as_left<kParts>(a, y[0], y[1]);
-        load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
-        mma_parts<kParts, kParts, 2>(d, a, r);
+        mma_short(d, a, r);
+        if (k > 0) rest(k - 1);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
@@ -353,33 +411,21 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
             }
           }
         }
-        // what U of these steps takes off F of the later ones, and adds to O
-        as_left<kParts>(a, f[2 * k], f[2 * k + 1]);
+        as_left<kParts>(au, f[2 * k], f[2 * k + 1]);
+        if (k + 1 < NB) {
+          load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k + 16, 16 * k);
 #pragma unroll
-        for (int i = 2 * k + 2; i < NC; i += 2) {
-          load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
-          mma_parts<kParts, kParts, 2>(f + i, a, r);
-        }
-        if constexpr (!kStates) {
-          uint32_t au[PP][4];
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int q = 0; q < PP; ++q)
+            for (int e = 0; e < 4; ++e) d[q][e] = f[2 * k + 2 + q][e];
+          mma_short(d, au, r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) au[q][e] = a[q][e];
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 2 * k; i < NC; i += 2) {
-            uint32_t rp[PP][2][2];
-            load_right<G::PB, PP, 2>(rp, P, C * G::PB, lane, 8 * i, 16 * k);
-            mma_parts<PP, PP, 2>(o + i, au, rp);
-          }
+            for (int e = 0; e < 4; ++e) f[2 * k + 2 + q][e] = d[q][e];
         }
       }
-      if constexpr (!kStates) {
-        T* at = out + (long long)c * C * out_step + w0;
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-          put_steps<T>(o[i], at, out_step, 8 * i, n, v0 + w0, p.dv, lane);
-      }
+      rest(NB - 1);
       uint32_t y[NB][kParts][4];
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
@@ -391,7 +437,16 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
         }
         as_left<kParts>(y[k], f[2 * k], f[2 * k + 1]);
       }
-      state_add<NI, DK, NK, NB>(x, g.last, y, K, lane);
+      state_add<NI, DK, NK, NB>(x, g.last, y, K, lane, [&](int i) {
+        if constexpr (!kStates) {  // o's columns, shared out over the products
+          constexpr int per = NC / (NK / 4) > 0 ? NC / (NK / 4) : 1;
+#pragma unroll
+          for (int j = 0; j < per; ++j)
+            if (i * per + j < NC)
+              put_steps<T>(o[i * per + j], out + (long long)c * C * out_step + w0, out_step,
+                           8 * (i * per + j), n, v0 + w0, p.dv, lane);
+        }
+      });
       __syncthreads();
     }
     if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, p.dk, lane);
@@ -503,22 +558,33 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
         for (int q = 0; q < NI; ++q)
           ldm4t(a[q], dO + q * C * kVB * 2 + left_t<kVB * 2>(lane, w0, 16 * k));
       };
+      // P^T dO for the steps of block k
+      auto from_out = [&](int k) {
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        uint32_t a[NI][4];
-        dout_left(a, k);
-#pragma unroll
-        for (int i = 0; i <= 2 * k; i += 2) {
-          uint32_t r[kParts][2][2];
-          load_right_t<G::PB, kParts, 2>(r, P, C * G::PB, lane, 8 * i, 16 * k);
-          mma_parts<NI, kParts, 2>(f + i, a, r);
+        for (int i = k; i < NB; ++i) {
+          uint32_t a[NI][4], r[kParts][2][2];
+          dout_left(a, i);
+          load_right_t<G::PB, kParts, 2>(r, P, C * G::PB, lane, 16 * k, 16 * i);
+          mma_parts<NI, kParts, 2>(f + 2 * k, a, r);
         }
-      }
+      };
+      // from the last block back: y = dU - X^T beta dU, dv = beta y, and what dv takes
+      // off dU of the earlier blocks (the order of issue as in the walk)
+      uint32_t av[kParts][4];
+      auto rest = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 2 * k - 2; i += 2) {
+          uint32_t r[kParts][2][2];
+          load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
+          mma_parts<kParts, kParts, 2>(f + i, av, r);
+        }
+      };
+      from_out(NB - 1);
 #pragma unroll
       for (int k = NB - 1; k >= 0; --k) {
-        // y of steps 16 k ...: dU - X^T beta dU
         uint32_t a[kParts][4], r[kParts][2][2];
         float d[2][4], y[2][4];
+        load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
@@ -529,8 +595,9 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
           }
         }
         as_left<kParts>(a, y[0], y[1]);
-        load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
-        mma_parts<kParts, kParts, 2>(d, a, r);
+        mma_short(d, a, r);
+        if (k + 1 < NB) rest(k + 1);
+        if (k > 0) from_out(k - 1);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
@@ -543,11 +610,18 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
             f[2 * k + q][e] = yv * (e & 1 ? be.y : be.x);
           }
         }
-        as_left<kParts>(a, f[2 * k], f[2 * k + 1]);
+        as_left<kParts>(av, f[2 * k], f[2 * k + 1]);
+        if (k > 0) {
+          load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k - 16, 16 * k);
 #pragma unroll
-        for (int i = 0; i < 2 * k; i += 2) {
-          load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
-          mma_parts<kParts, kParts, 2>(f + i, a, r);
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[q][e] = f[2 * k - 2 + q][e];
+          mma_short(d, av, r);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[2 * k - 2 + q][e] = d[q][e];
         }
       }
       T* at = out + (long long)c * C * out_step + w0;
@@ -564,7 +638,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
         }
         as_left<kParts>(y[k], f[2 * k], f[2 * k + 1]);
       }
-      state_add<NI, DK, NK, NB>(x, g.last, y, K, lane);
+      state_add<NI, DK, NK, NB>(x, g.last, y, K, lane, [](int) {});
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         uint32_t a[NI][4];
@@ -585,7 +659,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
         }
         as_left<kParts>(y[k], d[0], d[1]);
       }
-      state_add<NI, DK, NK, NB>(x, 1.f, y, Q, lane);
+      state_add<NI, DK, NK, NB>(x, 1.f, y, Q, lane, [](int) {});
       __syncthreads();
     }
     if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, p.dk, lane);

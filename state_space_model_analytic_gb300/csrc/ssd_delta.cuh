@@ -336,88 +336,66 @@ __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float
 constexpr int kDiag = 20;  // floats of a column of a diagonal block
 template <int C>
 struct alignas(16) Scratch {
-  float diag[C / 16][16][kDiag];  // L[i][j] at [j][i]
+  float diag[C / 16][16][kDiag];  // L[i][j] at [j][i], a warp each
 };
 
-// Rows 16 S0 ... 16 S0 + 15 and, for S1 > S0, 16 S1 ... of A K^T, columns up to the
-// diagonal block's end, times the decays: -L (below the diagonal blocks to `out`, in
-// them to the scratch), or factor * (values on and below the diagonal) to `out`.
-template <int NI, int DK, int PO, bool kL, int S0, int S1>
-__device__ __forceinline__ void scores(uint32_t A, uint32_t K, uint8_t* out,
-                                       const Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc,
-                                       float factor, int lane) {
+// One block of 16 x 16 of A K^T, rows 16 bi ..., columns 16 bj ..., times the decays
+// and `factor`: to the tile `out` in PO parts, or to `diag`, transposed.  On the
+// diagonal what lies above it is zero (kL: and on it).
+template <int NI, int DK, int PO, bool kDiagL>
+__device__ __forceinline__ void score_block(uint32_t A, uint32_t K, uint8_t* out,
+                                            const Gates<kSteps<NI>>& g, float (*diag)[kDiag], int bi,
+                                            int bj, float factor, int lane) {
   constexpr int C = kSteps<NI>, RB = DK * 2, OB = C * 2;
-  constexpr int N0 = 2 * S0 + 2, N1 = S1 > S0 ? 2 * S1 + 2 : 0, N = N1 > N0 ? N1 : N0;
-  float acc[N0 + N1][4];
+  float acc[2][4];
 #pragma unroll
-  for (int n = 0; n < N0 + N1; ++n)
+  for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll(NI == 1 ? 2 : 1)
+  constexpr int U = NI == 1 ? DK / 16 : 2;  // (every operand of a bf16 block on its way at once)
+#pragma unroll(U)
   for (int k = 0; k < DK; k += 16) {
-    uint32_t a0[NI][4], a1[NI][4];
+    uint32_t a[NI][4], b[NI][2][2];
 #pragma unroll
-    for (int p = 0; p < NI; ++p) {
-      ldm4(a0[p], A + p * C * RB + left<RB>(lane, 16 * S0, k));
-      if (N1) ldm4(a1[p], A + p * C * RB + left<RB>(lane, 16 * S1, k));
-    }
-    uint32_t b[NI][N][2];
-    load_right<RB, NI, N>(b, K, C * RB, lane, 0, k);
-    if constexpr (N1 > 0) mma_parts<NI, NI, N>(acc + N0, a1, b);
-#pragma unroll
-    for (int n = 0; n < N0; n += 2) {
-      uint32_t b2[NI][2][2];
-#pragma unroll
-      for (int p = 0; p < NI; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b2[p][i >> 1][i & 1] = b[p][n + (i >> 1)][i & 1];
-      mma_parts<NI, NI, 2>(acc + n, a0, b2);
-    }
+    for (int p = 0; p < NI; ++p) ldm4(a[p], A + p * C * RB + left<RB>(lane, 16 * bi, k));
+    load_right<RB, NI, 2>(b, K, C * RB, lane, 16 * bj, k);
+    mma_parts<NI, NI, 2>(acc, a, b);
   }
-  const int c0 = (lane & 3) * 2;
+  const int c0 = (lane & 3) * 2, i0 = 16 * bi + (lane >> 2);
+  const float hi0 = g.hi[i0], lo0 = g.lo[i0], hi1 = g.hi[i0 + 8], lo1 = g.lo[i0 + 8];
 #pragma unroll
-  for (int strip = 0; strip < (N1 ? 2 : 1); ++strip) {
-    const int S = strip ? S1 : S0;
-    const int r0 = 16 * S + (lane >> 2);
-    const float hi0 = g.hi[r0], lo0 = g.lo[r0], hi1 = g.hi[r0 + 8], lo1 = g.lo[r0 + 8];
+  for (int n = 0; n < 2; ++n) {
+    const int j = 16 * bj + 8 * n + c0;
+    const float2 hj = *(const float2*)&g.hi[j], lj = *(const float2*)&g.lo[j];
 #pragma unroll
-    for (int n = 0; n < (strip ? N1 : N0); ++n) {
-      const float* v = acc[strip ? N0 + n : n];
-      const bool diag = n >= 2 * S;
-      const float2 hj = *(const float2*)&g.hi[8 * n + c0], lj = *(const float2*)&g.lo[8 * n + c0];
+    for (int u = 0; u < 2; ++u) {
+      const int i = i0 + 8 * u;
+      const float hi = u ? hi1 : hi0, lo = u ? lo1 : lo0;
+      float x = acc[n][2 * u] * factor * decay(hi, lo, hj.x, lj.x);
+      float y = acc[n][2 * u + 1] * factor * decay(hi, lo, hj.y, lj.y);
+      if (kDiagL ? j >= i : j > i) x = 0.f;
+      if (kDiagL ? j + 1 >= i : j + 1 > i) y = 0.f;
+      if constexpr (kDiagL) {
+        diag[j & 15][i & 15] = x;
+        diag[(j & 15) + 1][i & 15] = y;
+      } else {
+        uint32_t p[PO];
+        split2<PO>(x, y, p);
+        uint8_t* at = out + at16<OB>(i, 2 * bj + n) + c0 * 2;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = r0 + 8 * u, j = 8 * n + c0;
-        const float hi = u ? hi1 : hi0, lo = u ? lo1 : lo0;
-        float x = v[2 * u] * factor * decay(hi, lo, hj.x, lj.x);
-        float y = v[2 * u + 1] * factor * decay(hi, lo, hj.y, lj.y);
-        if (diag) {
-          if (kL ? j >= i : j > i) x = 0.f;
-          if (kL ? j + 1 >= i : j + 1 > i) y = 0.f;
-        }
-        if (kL && diag) {
-          sc.diag[S][j & 15][i & 15] = x;
-          sc.diag[S][(j & 15) + 1][i & 15] = y;
-        } else {
-          uint32_t p[PO];
-          split2<PO>(kL ? -x : x, kL ? -y : y, p);
-          uint8_t* at = out + at16<OB>(i, n) + c0 * 2;
-#pragma unroll
-          for (int q = 0; q < PO; ++q) *(uint32_t*)(at + q * C * OB) = p[q];
-        }
+        for (int q = 0; q < PO; ++q) *(uint32_t*)(at + q * C * OB) = p[q];
       }
     }
   }
 }
 
-// One thread a column j of a diagonal block: with T = (I + beta L)^-1, X = L T and
-// T = I - beta X, so once X_mj is whole, T_mj = -beta_m X_mj (1 for m = j) adds
+// Lanes 0 - 15, a column j each of diagonal block s: with T = (I + beta L)^-1, X = L T
+// and T = I - beta X, so once X_mj is whole, T_mj = -beta_m X_mj (1 for m = j) adds
 // L_im T_mj to every later X_ij.
 template <int C>
-__device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, const Scratch<C>& sc,
-                                            int tid) {
+__device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, const float (*diag)[kDiag],
+                                            int s, int j) {
   constexpr int OB = C * 2;
-  const int s = tid >> 4, j = tid & 15;
   float x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = 0.f;
@@ -426,7 +404,7 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, con
     const float t = m == j ? 1.f : -g.beta[16 * s + m] * x[m];
 #pragma unroll
     for (int i = (m + 1) / 4 * 4; i < 16; i += 4) {
-      const float4 l = *(const float4*)&sc.diag[s][m][i];
+      const float4 l = *(const float4*)&diag[m][i];
       if (i > m) x[i] = fmaf(l.x, t, x[i]);
       if (i + 1 > m) x[i + 1] = fmaf(l.y, t, x[i + 1]);
       if (i + 2 > m) x[i + 2] = fmaf(l.z, t, x[i + 2]);
@@ -446,38 +424,41 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, con
 }
 
 // M and, with kP, P times `scale` of a chunk whose operands and gates are in shared
-// memory, by the kPrep threads.  The last warp has `aside` to do as well (the gates
-// of a later chunk).
+// memory, by the kPrep threads: a warp takes one of L's diagonal blocks and inverts
+// it, then its share of the other blocks of L and of P.  (The blocks go through one
+// loop: as straight code with the strips known at compile time the four warps' code
+// and the walk's did not fit the instruction caches together, and waiting for
+// instructions was the largest of all stalls.)  The last warp has `aside` to do as
+// well (the gates of a later chunk).
 template <int NI, int DK, int PP, bool kP, typename F>
 __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, uint8_t* M, uint8_t* P,
                                         const Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc,
                                         float scale, int tid, F aside) {
-  constexpr int C = kSteps<NI>;
+  constexpr int C = kSteps<NI>, NB = C / 16, W = kPrep / 32;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t K = smem32(Kt), Q = smem32(Qt);
-  if (warp < 2) {
-    // strips of 2, 4, 6, 8 columns of eight: the first with the last
-    if constexpr (C == 64) {
-      if (warp == 0) scores<NI, DK, kParts, true, 0, 3>(K, K, M, g, sc, 1.f, lane);
-      else scores<NI, DK, kParts, true, 1, 2>(K, K, M, g, sc, 1.f, lane);
-    } else {
-      if (warp == 0) scores<NI, DK, kParts, true, 0, 0>(K, K, M, g, sc, 1.f, lane);
-      else scores<NI, DK, kParts, true, 1, 1>(K, K, M, g, sc, 1.f, lane);
-    }
-    bar(2, 64);
-    if (tid < C) invert_diag<C>(M, g, sc, tid);
-  } else {
-    if (kP) {
-      if constexpr (C == 64) {
-        if (warp == 2) scores<NI, DK, PP, false, 0, 3>(Q, K, P, g, sc, scale, lane);
-        else scores<NI, DK, PP, false, 1, 2>(Q, K, P, g, sc, scale, lane);
-      } else {
-        if (warp == 2) scores<NI, DK, PP, false, 0, 0>(Q, K, P, g, sc, scale, lane);
-        else scores<NI, DK, PP, false, 1, 1>(Q, K, P, g, sc, scale, lane);
-      }
-    }
-    if (warp == 3) aside();
+  if (warp < NB) {
+    score_block<NI, DK, kParts, true>(K, K, nullptr, g, sc.diag[warp], warp, warp, 1.f, lane);
+    __syncwarp();
+    if (lane < 16) invert_diag<C>(M, g, sc.diag[warp], warp, lane);
+    __syncwarp();
   }
+  // L's blocks below the diagonal, rows and columns (hexadecimal digits, the first one last)
+  constexpr uint32_t kLi = NB == 4 ? 0x333221 : 0x1, kLj = NB == 4 ? 0x210100 : 0x0;
+  constexpr uint64_t kPi = NB == 4 ? 0x3333222110ull : 0x110, kPj = NB == 4 ? 0x3210210100ull : 0x100;
+  constexpr int nL = NB * (NB - 1) / 2, nP = NB * (NB + 1) / 2;
+#pragma unroll 1
+  for (int r = warp; r < nL; r += W)
+    score_block<NI, DK, kParts, false>(K, K, M, g, nullptr, kLi >> 4 * r & 15, kLj >> 4 * r & 15, -1.f,
+                                       lane);
+  if constexpr (kP) {
+    // (in the order that leaves every warp the same number of blocks)
+#pragma unroll 1
+    for (int r = (warp + W - nL % W) % W; r < nP; r += W)
+      score_block<NI, DK, PP, false>(Q, K, P, g, nullptr, kPi >> 4 * r & 15, kPj >> 4 * r & 15, scale,
+                                     lane);
+  }
+  if (warp == W - 1) aside();
 }
 
 }  // namespace delta

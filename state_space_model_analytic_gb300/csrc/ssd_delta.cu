@@ -3,19 +3,22 @@
 // states and of v), and the step of one token.  The formulas of a chunk stand in
 // ssd_delta.cuh; the gradients of L = sum(do . o) + sum(dS . S_T) are, with D the
 // gradient of the state after a chunk,
-//   dU = P^T dO + e^{G-g} K D^T,  (I + L^T beta) y = dU,  dv = beta y,
+//   dU = s P^T dO + e^{G-g} K D^T,  (I + L^T beta) y = dU,  dv = beta y,
 //   dbeta_i = E_i . y_i,  D <- e^G D + (s e^g dO)^T Q - (e^g dv)^T K
 // and those of q, k and the decays need no walk (ssd_delta_grads.cu).
 //
-// One CTA per (head, 64 columns of v, row): the rows of the state are independent
-// of each other.  Four warps hold 16 rows of the state each, in registers, in the
-// layout in which matrix instructions leave their results.  That is also the layout
-// in which they take a left operand, and every product of the chain that one chunk
-// has to pass on to the next has such a one: F^T = V^T - H K^T from the state, E^T
-// from F^T, the new state from U^T.  So that chain runs within a warp, without a
-// word through shared memory; four other warps meanwhile prepare the next chunk (L,
-// X, P: all that does not depend on the state) and load the one after it, and one
-// barrier a chunk hands over.
+// One CTA per (head, columns of v, row): the rows of the state are independent of each
+// other.  Four warps hold 16 rows of the state each, in registers, in the layout in
+// which matrix instructions leave their results.  That is also the layout in which
+// they take a left operand, and every product of the chain that one chunk has to pass
+// on to the next has such a one: F^T = V^T - H K^T from the state, E^T from F^T, the
+// new state from U^T.  So that chain runs within a warp, without a word through shared
+// memory; eight other warps meanwhile prepare the next chunk (L, X, P: all that does not
+// depend on the state) and load the one after it, and one barrier a chunk hands over.
+//
+// Where rows are few, WK = 2 or 4 warps share 16 rows of the state, a part of dk each:
+// the products with the state are split, F's parts added up through shared memory, and
+// the solution of the triangular system, which all of them need, is found by each.
 #include <cuda_bf16.h>
 
 #include "ssd_delta.cuh"
@@ -26,28 +29,34 @@ namespace {
 
 using namespace delta;
 
-// Parts of the state, P and U where they make o alone.  A bf16 o has 8 bits: two
-// parts (16) leave it its own rounding, 0.0017 of its root mean square; with one
-// part of the state and of P it was off by 0.0028 where o is small beside its terms.
+// Parts of the state, P and U where they make o alone: a bf16 o has 8 bits.
 template <int NI>
-constexpr int kOutParts = NI == 1 ? 2 : 3;
+constexpr int kOutParts = NI == 1 ? 1 : 2;
 
-template <int NI, int DK, int PP>
+constexpr int kWalkers = 4;  // warps of a walk
+// Registers of the two kinds of threads: 256 * 128 + 128 * 240 of the 384 * 168 that a
+// CTA starts with.
+constexpr int kPrepRegs = 128, kWalkRegs = 240;
+static_assert(kPrep * kPrepRegs + 32 * kWalkers * kWalkRegs <= (kPrep + 32 * kWalkers) * 168, "");
+
+template <int NI, int DK, int PP, int WK, int kExchanged>
 struct Geom {
-  static constexpr int C = kSteps<NI>;
+  static constexpr int C = kSteps<NI>, NC = C / 8;
   static constexpr int RB = DK * 2, PB = C * 2;      // bytes of a row of K, of M
   static constexpr int KT = NI * C * RB;             // K's or Q's tile, all parts
   // V in the walk (bf16 as it is, fp32 as floats whose rows are 4 banks apart),
   // dO in the walk back (parts)
   static constexpr int LV = kVB + 4;
-  static constexpr int VT = NI == 1 ? C * kVB * 2 : C * kVB * 2 * NI;
-  static_assert(NI == 1 || C * LV * 4 <= VT, "");
+  static constexpr int VT = NI == 1 ? C * kVB * 2 : C * LV * 4;
+  static_assert(VT >= NI * C * kVB * 2, "");
   static constexpr int NS = NI == 1 ? 3 : 2;         // stages of the operands
   static constexpr int MT = kParts * C * PB, PT = PP * C * PB;
   static constexpr int kStage = 2 * KT + VT;
   static constexpr int kM = NS * kStage, kP = kM + 2 * MT;
   static constexpr int kG = kP + 2 * PT, kS = kG + 3 * (int)sizeof(Gates<C>);
-  static constexpr size_t smem = kS + sizeof(Scratch<C>);
+  static constexpr int kX = kS + (int)sizeof(Scratch<C>);  // sums of WK warps on their way
+  static constexpr size_t smem = kX + (WK > 1 ? kExchanged * kWalkers * NC * 512 : 0);
+  static_assert(kStage % 16 == 0 && kX % 16 == 0, "");
 };
 
 // fp32 rows of v: C x kVB floats
@@ -63,32 +72,51 @@ __device__ __forceinline__ void load_floats(uint8_t* tile, const float* src, lon
   }
 }
 
-// A warp's rows of a state [dv][dk]: x[j]: row v (+ 8 for e >= 2), column 8 j + 2 t
-// (+ 1 for odd e), from or to memory.
+// A warp's rows of a state [dv][dk], from column k0: x[j]: row v (+ 8 for e >= 2),
+// column k0 + 8 j + 2 t (+ 1 for odd e), from or to memory.
 template <int NK>
-__device__ __forceinline__ void get_state(float (&x)[NK][4], const float* p, int v, int dv, int dk,
-                                          int lane) {
-  const int c = (lane & 3) * 2;
+__device__ __forceinline__ void get_state(float (&x)[NK][4], const float* p, int v, int dv, int k0,
+                                          int dk, int lane) {
+  const int c = k0 + (lane & 3) * 2;
 #pragma unroll
   for (int j = 0; j < NK; ++j)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float2 f = make_float2(0.f, 0.f);
-      if (p && v + 8 * u < dv && 8 * j < dk) f = *(const float2*)(p + (v + 8 * u) * dk + 8 * j + c);
+      if (p && v + 8 * u < dv && k0 + 8 * j < dk) f = *(const float2*)(p + (v + 8 * u) * dk + 8 * j + c);
       x[j][2 * u] = f.x;
       x[j][2 * u + 1] = f.y;
     }
 }
 template <int NK>
-__device__ __forceinline__ void put_state(const float (&x)[NK][4], float* p, int v, int dv, int dk,
-                                          int lane) {
-  const int c = (lane & 3) * 2;
+__device__ __forceinline__ void put_state(const float (&x)[NK][4], float* p, int v, int dv, int k0,
+                                          int dk, int lane) {
+  const int c = k0 + (lane & 3) * 2;
 #pragma unroll
   for (int j = 0; j < NK; ++j)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (v + 8 * u < dv && 8 * j < dk)
+      if (v + 8 * u < dv && k0 + 8 * j < dk)
         *(float2*)(p + (v + 8 * u) * dk + 8 * j + c) = make_float2(x[j][2 * u], x[j][2 * u + 1]);
+}
+// the largest of a lane's values in its rows g and g + 8
+template <int N>
+__device__ __forceinline__ float2 row_max(const float (*x)[4]) {
+  float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    m.x = fmaxf(m.x, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
+    m.y = fmaxf(m.y, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+  }
+  return m;
+}
+// the scales of a warp's rows from its lanes' largest values
+struct RowScales {
+  float up0, down0, up1, down1;
+};
+__device__ __forceinline__ RowScales row_scales(float2 m) {
+  const Scale a = scale_to<10>(quad_max(m.x)), b = scale_to<10>(quad_max(m.y));
+  return {a.up, a.down, b.up, b.down};
 }
 
 // x (rows v, columns c0 ... of steps, eight) transposed to rows of memory: row i of
@@ -98,7 +126,7 @@ __device__ __forceinline__ void put_steps(const float (&x)[4], T* at, long long 
                                           int v0, int dv, int lane) {
   const int g = lane >> 2, c = (lane & 3) * 2;
   if constexpr (sizeof(T) == 2) {
-    const uint32_t a = transpose8(pack2(x[0], x[1])), b = transpose8(pack2(x[2], x[3]));
+    const uint32_t a = transpose8(pack_bf(x[0], x[1])), b = transpose8(pack_bf(x[2], x[3]));
     if (c0 + g < n) {
       T* row = at + (c0 + g) * step + c;
       if (v0 < dv) *(uint32_t*)row = a;
@@ -126,108 +154,128 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
   }
 }
 
-// f[n] += X K^T for the C steps of a tile whose rows are steps, X the state with all
-// its parts; and with PO > 0 o[n] += X Q^T with PO of them.  The right operands of a
-// group of columns are loaded while the group before is multiplied.
+// f[n] = X K^T for the C steps of a tile whose rows are steps, X the warp's columns k0
+// ... of the state, scaled; and with PO > 0 o[n] = X Q^T with PO parts of it.  The right
+// operands of a group of columns are loaded while the group before is multiplied.
 template <int NI, int PO, int DK, int NK, int NC>
 __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
-                                            const float (&x)[NK][4], uint32_t K, uint32_t Q, int lane) {
+                                            const float (&x)[NK][4], const RowScales& s, uint32_t K,
+                                            uint32_t Q, int k0, int lane) {
   constexpr int C = kSteps<NI>, RB = DK * 2;
-  constexpr int GN = NI == 1 ? 4 : 2;                   // columns of eight of a group
+  constexpr int GN = NC < 4 ? NC : 4;                     // columns of eight of a group
   constexpr int GF = NC / GN, GK = PO > 0 ? 2 * GF : GF;  // groups of 16 terms
   constexpr int NG = NK / 2 * GK;
   uint32_t a[2][kParts][4], b[2][NI][GN][2];
-  auto load = [&](int s) {
-    const int k = s / GK, g = s % GK;
-    load_right<RB, NI, GN>(b[s & 1], g < GF ? K : Q, C * RB, lane, 8 * GN * (g % GF), 16 * k);
+  auto load = [&](int i) {
+    const int k = i / GK, g = i % GK;
+    load_right<RB, NI, GN>(b[i & 1], g < GF ? K : Q, C * RB, lane, 8 * GN * (g % GF), k0 + 16 * k);
   };
-  as_left<kParts>(a[0], x[0], x[1]);
+  zero(f);
+  if (PO > 0) zero(o);
+  as_left<kParts>(a[0], x[0], x[1], s.up0, s.up1);
   load(0);
 #pragma unroll
-  for (int s = 0; s < NG; ++s) {
-    const int k = s / GK, g = s % GK;
-    if (s + 1 < NG) load(s + 1);
-    if (g == 0 && 2 * k + 2 < NK) as_left<kParts>(a[(k + 1) & 1], x[2 * k + 2], x[2 * k + 3]);
+  for (int i = 0; i < NG; ++i) {
+    const int k = i / GK, g = i % GK;
+    if (i + 1 < NG) load(i + 1);
+    if (g == 0 && 2 * k + 2 < NK)
+      as_left<kParts>(a[(k + 1) & 1], x[2 * k + 2], x[2 * k + 3], s.up0, s.up1);
     if (g < GF) {
-      mma_parts<kParts, NI, GN>(f + GN * g, a[k & 1], b[s & 1]);
+      mma_parts<kParts, NI, GN>(f + GN * g, a[k & 1], b[i & 1]);
     } else if constexpr (PO > 0) {
       uint32_t ao[PO][4];
 #pragma unroll
       for (int q = 0; q < PO; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) ao[q][e] = a[k & 1][q][e];
-      mma_parts<PO, NI, GN>(o + GN * (g - GF), ao, b[s & 1]);
+      mma_parts<PO, NI, GN>(o + GN * (g - GF), ao, b[i & 1]);
     }
   }
 }
 
-// d += a b for two columns of eight, all parts of both; the products of one order of
-// size go to a sum of their own, so that fewer wait for one another.
+// d = a b for two columns of eight, all parts of both; the small products go to a sum
+// of their own, so that fewer wait for one another.
 __device__ __forceinline__ void mma_short(float (&d)[2][4], const uint32_t (&a)[kParts][4],
                                           const uint32_t (&b)[kParts][2][2]) {
-  float e[2][2][4];
+  float e[2][4];
+  zero(d);
+  zero(e);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int n = 0; n < 2; ++n) mma(e[n], a[0], b[1][n][0], b[1][n][1]);
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+  for (int n = 0; n < 2; ++n) mma(d[n], a[0], b[0][n][0], b[0][n][1]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) e[i][n][c] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n) mma(e[0][n], a[i], b[2 - i][n][0], b[2 - i][n][1]);
-    if (i < 2)
-#pragma unroll
-      for (int n = 0; n < 2; ++n) mma(e[1][n], a[i], b[1 - i][n][0], b[1 - i][n][1]);
-    if (i == 0)
-#pragma unroll
-      for (int n = 0; n < 2; ++n) mma(d[n], a[0], b[0][n][0], b[0][n][1]);
-  }
+  for (int n = 0; n < 2; ++n) mma(e[n], a[1], b[0][n][0], b[0][n][1]);
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) d[n][c] += e[0][n][c] + e[1][n][c];
+    for (int c = 0; c < 4; ++c) d[n][c] += e[n][c];
 }
 
-// x <- scale x + Y tile, Y (rows v, C steps) as parts of left operands.  beside(i),
-// i < NK / 4: work that is issued between the products.
+// x <- scale x + Y tile, Y (rows v, C steps) as parts of left operands that were scaled
+// by s; x: columns k0 ... of the state.  Returns the largest values of the lane's rows.
+// beside(i), i < ceil(NK / 4): work that is issued between the products.
 template <int NI, int DK, int NK, int NB, typename F>
-__device__ __forceinline__ void state_add(float (&x)[NK][4], float scale, const uint32_t (*y)[kParts][4],
-                                          uint32_t tile, int lane, F beside) {
-  constexpr int C = kSteps<NI>, RB = DK * 2;
+__device__ __forceinline__ float2 state_add(float (&x)[NK][4], float scale, const uint32_t (*y)[kParts][4],
+                                            const RowScales& s, uint32_t tile, int k0, int lane, F beside) {
+  constexpr int C = kSteps<NI>, RB = DK * 2, GN = NK < 4 ? NK : 4;
+  float2 m = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int n = 0; n < NK; n += 4) {
-    float d[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
+  for (int n = 0; n < NK; n += GN) {
+    float d[GN][4];
+    zero(d);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      uint32_t r[NI][4][2];
-      load_right_t<RB, NI, 4>(r, tile, C * RB, lane, 8 * n, 16 * b);
-      mma_parts<kParts, NI, 4>(d, y[b], r);
-      if (b == 0) beside(n / 4);
+      uint32_t r[NI][GN][2];
+      load_right_t<RB, NI, GN>(r, tile, C * RB, lane, k0 + 8 * n, 16 * b);
+      mma_parts<kParts, NI, GN>(d, y[b], r);
+      if (b == 0) beside(n / GN);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < GN; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[n + i][e] = fmaf(scale, x[n + i][e], d[i][e]);
+      for (int e = 0; e < 4; ++e)
+        x[n + i][e] = fmaf(e < 2 ? s.down0 : s.down1, d[i][e], scale * x[n + i][e]);
+      const float2 r = row_max<1>(x + n + i);
+      m.x = fmaxf(m.x, r.x);
+      m.y = fmaxf(m.y, r.y);
+    }
+  }
+  return m;
+}
+
+// The sum over WK warps of t[n], in the same order for each; ex: the warps' NC * 32
+// float4, from the first warp of the group.
+template <int WK, int NC>
+__device__ __forceinline__ void add_warps(float (&t)[NC][4], const float4* ex, int kg, int lane) {
+#pragma unroll
+  for (int n = 0; n < NC; ++n) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < WK; ++q) {
+      const float4 f = q == kg ? make_float4(t[n][0], t[n][1], t[n][2], t[n][3])
+                               : ex[(q * NC + n) * 32 + lane];
+      s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
+    }
+    t[n][0] = s.x; t[n][1] = s.y; t[n][2] = s.z; t[n][3] = s.w;
   }
 }
 
-template <int NI, int DK, bool kStates>
-__global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
+template <int NI, int DK, int WK, bool kStates>
+__global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const DeltaWalk p) {
   constexpr int PP = kOutParts<NI>;
-  using G = Geom<NI, DK, PP>;
+  using G = Geom<NI, DK, PP, WK, kStates ? 1 : 2>;
   using T = typename std::conditional<NI == 1, __nv_bfloat16, float>::type;
-  constexpr int C = G::C, NC = C / 8, NB = C / 16, NK = DK / 8;
+  constexpr int C = G::C, NC = G::NC, NB = C / 16, NK = DK / 8 / WK, VB = kVB / WK;
+  // blocks of 16 steps of o and E that a warp writes
+  constexpr int OB = NB / WK > 0 ? NB / WK : 1;
   extern __shared__ __align__(1024) uint8_t sm[];
   Gates<C>* gates = (Gates<C>*)(sm + G::kG);
   Scratch<C>& scratch = *(Scratch<C>*)(sm + G::kS);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int vblocks = (p.dv + kVB - 1) / kVB;
-  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * kVB, b = blockIdx.y;
+  const int vblocks = (p.dv + VB - 1) / VB;
+  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = blockIdx.y;
+  const int width = min(VB, p.dv - v0);
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
   const int nc = (len + C - 1) / C;
@@ -240,20 +288,22 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
   float* err = kStates ? p.err + unit * chunks * C * p.dv + v0 : nullptr;
   auto stage = [&](int c) { return sm + c % G::NS * G::kStage; };  // Q, K, V
   if (warp < kPrep / 32) {
+    fewer_registers<kPrepRegs>();
     const T* qp = (const T*)p.q.p + b * p.q.batch + (long long)(h / p.q.share) * p.dk;
     const T* kp = (const T*)p.k.p + b * p.k.batch + (long long)(h / p.k.share) * p.dk;
     const T* vp = (const T*)p.v.p + b * p.v.batch + (long long)h * p.dv + v0;
+    // what is copied asynchronously
     auto load = [&](int c) {
       const int n = len - c * C;
       const long long t0 = (long long)c * C;
       uint8_t* st = stage(c);
-      load_tile<NI, C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
-      if (!kStates) load_tile<NI, C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
-      if constexpr (NI == 1)
-        load_tile<1, C, kVB, kPrep>(st + 2 * G::KT, vp + t0 * p.v.step, p.v.step, n, p.dv - v0, tid);
-      else
-        load_floats<C, G::LV>(st + 2 * G::KT, (const float*)vp + t0 * p.v.step, p.v.step, n,
-                              p.dv - v0, tid);
+      if constexpr (NI == 1) {
+        load_tile<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
+        if (!kStates) load_tile<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
+        load_tile<C, kVB, kPrep>(st + 2 * G::KT, vp + t0 * p.v.step, p.v.step, n, width, tid);
+      } else {
+        load_floats<C, G::LV>(st + 2 * G::KT, vp + t0 * p.v.step, p.v.step, n, width, tid);
+      }
     };
     // the gates of chunk c + 1 are made ready beside the preparation of chunk c, by
     // the last warp, which has loaded them one chunk earlier
@@ -262,9 +312,27 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
       load_gates<C>(raw, p.log_decay, p.beta, gate0 + (long long)c * C * p.H, p.H, len - c * C, lane);
     };
     auto prep = [&](int c) {
-      prepare<NI, DK, PP, !kStates>(stage(c), stage(c) + G::KT, sm + G::kM + (c & 1) * G::MT,
-                                    sm + G::kP + (c & 1) * G::PT, gates[c % 3], scratch, p.scale, tid,
-                                    [&] {
+      Gates<C>& g = gates[c % 3];
+      uint8_t* st = stage(c);
+      auto k_done = [&](int r, float s) {
+        g.kup[r] = s;
+        const float d = inverse_pow2(s);
+        g.beta[r] *= d * d;
+      };
+      auto q_done = [&](int r, float s) { g.qup[r] = s; };
+      if constexpr (NI == 1) {
+        scale_rows<C, DK, kPrep>(st + G::KT, tid, k_done);
+        if (!kStates) scale_rows<C, DK, kPrep>(st, tid, q_done);
+      } else {
+        const long long t0 = (long long)c * C;
+        load_scaled_rows<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, len - c * C, p.dk, tid,
+                                       k_done);
+        if (!kStates)
+          load_scaled_rows<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, len - c * C, p.dk, tid, q_done);
+      }
+      bar(1, kPrep);
+      prepare<NI, DK, PP, !kStates>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
+                                    sm + G::kP + (c & 1) * G::PT, g, scratch, tid, [&] {
                                       scan_gates<C>(gates[(c + 1) % 3], raw, lane);
                                       load_raw(c + 2);
                                     });
@@ -274,7 +342,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
       copy_commit();
       if (G::NS > 2 && nc > 1) load(1);
       copy_commit();
-      if (warp == 3) {
+      if (warp == 0) {
         load_raw(0);
         scan_gates<C>(gates[0], raw, lane);
         load_raw(1);
@@ -296,25 +364,71 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
       __syncthreads();
     }
   } else {
-    const int w0 = (warp - kPrep / 32) * 16;  // this warp's columns of v in the block
+    more_registers<kWalkRegs>();
+    const int wi = warp - kPrep / 32, vg = wi / WK, kg = wi % WK;
+    const int w0 = vg * 16;        // this warp's columns of v in the block
+    const int k0 = kg * (DK / WK);  // and its columns of the state
     const int v = v0 + w0 + (lane >> 2), c2 = (lane & 3) * 2;
+    auto owns = [&](int block) { return WK == 1 || block / OB == kg; };
+    float4* ex = (float4*)(sm + G::kX) + (long long)vg * WK * NC * 32;
+    const bool idle = w0 >= width;  // (fewer columns than warps for them)
     float x[NK][4];
-    get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, p.dk, lane);
+    get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, k0, p.dk, lane);
+    float2 most = row_max<NK>(x);
     __syncthreads();
     for (int c = 0; c < nc; ++c) {
+      if (idle) {
+        __syncthreads();
+        continue;
+      }
       const uint8_t* st = stage(c);
       const uint32_t Q = smem32(st), K = Q + G::KT, V = K + G::KT;
       const uint32_t M = smem32(sm + G::kM + (c & 1) * G::MT), P = smem32(sm + G::kP + (c & 1) * G::PT);
       const Gates<C>& g = gates[c % 3];
       const int n = min(C, len - c * C);
-      if (kStates) put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, p.dk, lane);
-      // f: F^T, then U^T; o: O^T
-      float f[NC][4], o[NC][4];
+      if (kStates) put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, k0, p.dk, lane);
+      // f: F^T, then U^T.  o: O^T of the blocks that this warp writes, without s and of
+      // q's scale
+      float f[NC][4], o[2 * OB][4];
+      const RowScales sx = row_scales(most);
+      {
+        float qx[WK == 1 ? 2 * OB : NC][4];
+        state_times<NI, kStates ? 0 : PP, DK, NK, NC>(f, qx, x, sx, K, Q, k0, lane);
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[i][e] = o[i][e] = 0.f;
-      state_times<NI, kStates ? 0 : PP, DK, NK, NC>(f, o, x, K, Q, lane);
+          for (int e = 0; e < 4; ++e) {
+            f[i][e] *= e < 2 ? sx.down0 : sx.down1;
+            if (!kStates) qx[i][e] *= e < 2 ? sx.down0 : sx.down1;
+          }
+        if constexpr (WK > 1) {
+          float4* mine = ex + kg * NC * 32 + lane;
+          constexpr int kO = kWalkers * NC * 32;  // o's after f's
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            mine[i * 32] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+            if (!kStates) mine[kO + i * 32] = make_float4(qx[i][0], qx[i][1], qx[i][2], qx[i][3]);
+          }
+          bar(3 + vg, 32 * WK);
+          add_warps<WK, NC>(f, ex, kg, lane);
+          if constexpr (!kStates) {
+            zero(o);
+            if (kg * OB < NB)
+#pragma unroll
+              for (int i = 0; i < 2 * OB; ++i)
+#pragma unroll
+                for (int q = 0; q < WK; ++q) {
+                  const float4 t = ex[kO + (q * NC + kg * 2 * OB + i) * 32 + lane];
+                  o[i][0] += t.x; o[i][1] += t.y; o[i][2] += t.z; o[i][3] += t.w;
+                }
+          }
+        } else if constexpr (!kStates) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = qx[i][e];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < NC; i += 2) {
         float val[2][4];
@@ -326,8 +440,9 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              val[q][2 * u] = __uint_as_float(r[2 * q + u] << 16);
-              val[q][2 * u + 1] = __uint_as_float(r[2 * q + u] & 0xffff0000u);
+              const float2 t = unpack_bf(r[2 * q + u]);
+              val[q][2 * u] = t.x;
+              val[q][2 * u + 1] = t.y;
             }
         } else {
           const float* vf = (const float*)(st + 2 * G::KT);
@@ -340,27 +455,41 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 l = *(const float2*)&g.lead[8 * (i + q) + c2];
+          const float2 ku = *(const float2*)&g.kup[8 * (i + q) + c2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            f[i + q][2 * u] = fmaf(-l.x, f[i + q][2 * u], val[q][2 * u]);
-            f[i + q][2 * u + 1] = fmaf(-l.y, f[i + q][2 * u + 1], val[q][2 * u + 1]);
-            if (!kStates) {
-              o[i + q][2 * u] *= l.x * p.scale;
-              o[i + q][2 * u + 1] *= l.y * p.scale;
-            }
+            f[i + q][2 * u] = fmaf(-l.x, f[i + q][2 * u], ku.x * val[q][2 * u]);
+            f[i + q][2 * u + 1] = fmaf(-l.y, f[i + q][2 * u + 1], ku.y * val[q][2 * u + 1]);
           }
+        }
+      }
+      if constexpr (!kStates) {
+#pragma unroll
+        for (int i = 0; i < 2 * OB; ++i) {
+          const float2 l = *(const float2*)&g.lead[(WK == 1 ? 0 : min(kg * OB, NB - OB) * 16) + 8 * i + c2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= e & 1 ? l.y : l.x;
         }
       }
       // block by block: E = F - X beta F, U = beta E, and what U takes off F of the
       // later blocks and adds to O.  The next block waits for its own share alone; the
       // rest is issued while the next one's first product is on its way.
       uint32_t au[kParts][4];
+      RowScales su;
+      auto add_scaled = [&](float (*to)[4], const float (&d)[2][4]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[q][e] = fmaf(e < 2 ? su.down0 : su.down1, d[q][e], to[q][e]);
+      };
       auto rest = [&](int k) {
 #pragma unroll
         for (int i = 2 * k + 4; i < NC; i += 2) {
           uint32_t r[kParts][2][2];
+          float d[2][4];
           load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
-          mma_parts<kParts, kParts, 2>(f + i, au, r);
+          mma_short(d, au, r);
+          add_scaled(f + i, d);
         }
         if constexpr (!kStates) {
           uint32_t ao[PP][4];
@@ -369,10 +498,16 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) ao[q][e] = au[q][e];
 #pragma unroll
-          for (int i = 2 * k; i < NC; i += 2) {
-            uint32_t rp[PP][2][2];
-            load_right<G::PB, PP, 2>(rp, P, C * G::PB, lane, 8 * i, 16 * k);
-            mma_parts<PP, PP, 2>(o + i, ao, rp);
+          for (int j = 0; j < OB; ++j) {
+            const int i = WK == 1 ? j : kg * OB + j;  // block
+            if (i >= k && (WK == 1 || i < NB)) {
+              uint32_t rp[PP][2][2];
+              float d[2][4];
+              load_right<G::PB, PP, 2>(rp, P, C * G::PB, lane, 16 * i, 16 * k);
+              zero(d);
+              mma_parts<PP, PP, 2>(d, ao, rp);
+              add_scaled(o + 2 * j, d);
+            }
           }
         }
       };
@@ -383,89 +518,97 @@ __global__ void __launch_bounds__(256, 1) k_delta_walk(const DeltaWalk p) {
         load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
+          const int at = 16 * k + 8 * q + c2;
+          const float2 be = *(const float2*)&g.beta[at], xs = *(const float2*)&g.xs[at];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            d[q][e] = 0.f;
-            y[q][e] = f[2 * k + q][e] * (e & 1 ? be.y : be.x);
-          }
+          for (int e = 0; e < 4; ++e) y[q][e] = f[2 * k + q][e] * (e & 1 ? be.y * xs.y : be.x * xs.x);
         }
-        as_left<kParts>(a, y[0], y[1]);
+        const RowScales sy = row_scales(row_max<2>(y));
+        as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
         mma_short(d, a, r);
         if (k > 0) rest(k - 1);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
+          const int at = 16 * k + 8 * q + c2;
+          const float2 be = *(const float2*)&g.beta[at];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float ev = f[2 * k + q][e] + d[q][e];
+            const float ev = fmaf(e < 2 ? sy.down0 : sy.down1, d[q][e], f[2 * k + q][e]);
             if (kStates) d[q][e] = ev;
             f[2 * k + q][e] = ev * (e & 1 ? be.y : be.x);
           }
           if constexpr (kStates) {
+            const float2 ku = *(const float2*)&g.kup[at];
             float* ep = err + (long long)c * C * p.dv;
+            if (owns(k))
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 16 * k + 8 * q + c2 + (e & 1), vv = w0 + (lane >> 2) + 8 * (e >> 1);
-              if (v0 + vv < p.dv) ep[(long long)i * p.dv + vv] = d[q][e];
-            }
+              for (int e = 0; e < 4; ++e) {
+                const int i = at + (e & 1), vv = w0 + (lane >> 2) + 8 * (e >> 1);
+                if (vv < width) ep[(long long)i * p.dv + vv] = d[q][e] * inverse_pow2(e & 1 ? ku.y : ku.x);
+              }
           }
         }
-        as_left<kParts>(au, f[2 * k], f[2 * k + 1]);
+        su = row_scales(row_max<2>(f + 2 * k));
+        as_left<kParts>(au, f[2 * k], f[2 * k + 1], su.up0, su.up1);
         if (k + 1 < NB) {
           load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k + 16, 16 * k);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[q][e] = f[2 * k + 2 + q][e];
           mma_short(d, au, r);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[2 * k + 2 + q][e] = d[q][e];
+          add_scaled(f + 2 * k + 2, d);
         }
       }
       rest(NB - 1);
       uint32_t y[NB][kParts][4];
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
+      for (int i = 0; i < NC; ++i) {
+        const float2 t = *(const float2*)&g.tail[8 * i + c2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float2 t = *(const float2*)&g.tail[16 * k + 8 * q + c2];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[2 * k + q][e] *= e & 1 ? t.y : t.x;
-        }
-        as_left<kParts>(y[k], f[2 * k], f[2 * k + 1]);
+        for (int e = 0; e < 4; ++e) f[i][e] *= e & 1 ? t.y : t.x;
       }
-      state_add<NI, DK, NK, NB>(x, g.last, y, K, lane, [&](int i) {
-        if constexpr (!kStates) {  // o's columns, shared out over the products
-          constexpr int per = NC / (NK / 4) > 0 ? NC / (NK / 4) : 1;
+      const RowScales sw = row_scales(row_max<NC>(f));
 #pragma unroll
-          for (int j = 0; j < per; ++j)
-            if (i * per + j < NC)
-              put_steps<T>(o[i * per + j], out + (long long)c * C * out_step + w0, out_step,
-                           8 * (i * per + j), n, v0 + w0, p.dv, lane);
+      for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
+      constexpr int kGroups = NK < 4 ? 1 : NK / 4;
+      most = state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, lane, [&](int i) {
+        if constexpr (!kStates) {  // o's columns, shared out over the products
+          constexpr int per = (2 * OB + kGroups - 1) / kGroups;
+#pragma unroll
+          for (int j = 0; j < per; ++j) {
+            const int m = i * per + j;
+            if (m < 2 * OB) {
+              const int first = (WK == 1 ? 0 : kg * OB * 16) + 8 * m;  // step
+              if (WK == 1 || first < C) {
+                const float2 qu = *(const float2*)&g.qup[first + c2];
+                const float s0 = p.scale * inverse_pow2(qu.x), s1 = p.scale * inverse_pow2(qu.y);
+                const float r[4] = {o[m][0] * s0, o[m][1] * s1, o[m][2] * s0, o[m][3] * s1};
+                put_steps<T>(r, out + (long long)c * C * out_step + w0, out_step, first, n, v0 + w0, p.dv,
+                             lane);
+              }
+            }
+          }
         }
       });
       __syncthreads();
     }
-    if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, p.dk, lane);
+    if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, k0, p.dk, lane);
   }
-  if (!kStates) clear_rows<T>(out, out_step, len, p.T, min(kVB, p.dv - v0), tid, blockDim.x);
+  if (!kStates) clear_rows<T>(out, out_step, len, p.T, width, tid, blockDim.x);
 }
 
-// The walk back.
-template <int NI, int DK>
-__global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
-  using G = Geom<NI, DK, kParts>;
+// The walk back.  The sums are those of k's and q's scales: dU and y of 2^-n, dv of 2^n
+// times theirs, and dO's rows are divided by q's.
+template <int NI, int DK, int WK>
+__global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const DeltaBack p) {
+  using G = Geom<NI, DK, kParts, WK, 1>;
   using T = typename std::conditional<NI == 1, __nv_bfloat16, float>::type;
-  constexpr int C = G::C, NC = C / 8, NB = C / 16, NK = DK / 8;
+  constexpr int C = G::C, NC = G::NC, NB = C / 16, NK = DK / 8 / WK, VB = kVB / WK;
+  constexpr int OB = NB / WK > 0 ? NB / WK : 1;
   extern __shared__ __align__(1024) uint8_t sm[];
   Gates<C>* gates = (Gates<C>*)(sm + G::kG);
   Scratch<C>& scratch = *(Scratch<C>*)(sm + G::kS);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int vblocks = (p.dv + kVB - 1) / kVB;
-  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * kVB, b = blockIdx.y;
+  const int vblocks = (p.dv + VB - 1) / VB;
+  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = blockIdx.y;
+  const int width = min(VB, p.dv - v0);
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
   const int nc = (len + C - 1) / C;
@@ -478,17 +621,19 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
   float* ys = p.y + unit * chunks * C * p.dv + v0;
   auto stage = [&](int c) { return sm + c % G::NS * G::kStage; };  // Q, K, dO
   if (warp < kPrep / 32) {
+    fewer_registers<kPrepRegs>();
     const T* qp = (const T*)p.q.p + b * p.q.batch + (long long)(h / p.q.share) * p.dk;
     const T* kp = (const T*)p.k.p + b * p.k.batch + (long long)(h / p.k.share) * p.dk;
     const T* gp = (const T*)p.dout.p + b * p.dout.batch + (long long)h * p.dv + v0;
     auto load = [&](int c) {
-      const int n = len - c * C;
-      const long long t0 = (long long)c * C;
-      uint8_t* st = stage(c);
-      load_tile<NI, C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
-      load_tile<NI, C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
-      load_tile<NI, C, kVB, kPrep>(st + 2 * G::KT, gp + t0 * p.dout.step, p.dout.step, n, p.dv - v0,
-                                   tid);
+      if constexpr (NI == 1) {
+        const int n = len - c * C;
+        const long long t0 = (long long)c * C;
+        uint8_t* st = stage(c);
+        load_tile<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
+        load_tile<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
+        load_tile<C, kVB, kPrep>(st + 2 * G::KT, gp + t0 * p.dout.step, p.dout.step, n, width, tid);
+      }
     };
     RawGates<C> raw;
     auto load_raw = [&](int c) {  // (a chunk before the first has no steps)
@@ -496,9 +641,82 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
                     c < 0 ? 0 : len - c * C, lane);
     };
     auto prep = [&](int c) {
-      prepare<NI, DK, kParts, true>(stage(c), stage(c) + G::KT, sm + G::kM + (c & 1) * G::MT,
-                                    sm + G::kP + (c & 1) * G::PT, gates[c % 3], scratch, p.scale, tid,
-                                    [&] {
+      Gates<C>& g = gates[c % 3];
+      uint8_t* st = stage(c);
+      auto k_done = [&](int r, float s) {
+        g.kup[r] = s;
+        const float d = inverse_pow2(s);
+        g.beta[r] *= d * d;
+      };
+      auto q_done = [&](int r, float s) { g.qup[r] = s; };
+      const int n = len - c * C;
+      const long long t0 = (long long)c * C;
+      // dO: a thread's eights (NI == 1) or fours of elements, scaled by 2^n of all the
+      // tile's rows together
+      constexpr int E = NI == 1 ? 8 : 4, ND = C * kVB / E / kPrep;
+      static_assert(C * kVB / E % kPrep == 0, "");
+      float d[ND][E];
+      if constexpr (NI == 1) {
+        scale_rows<C, DK, kPrep>(st + G::KT, tid, k_done);
+        scale_rows<C, DK, kPrep>(st, tid, q_done);
+      } else {
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+          const int at = i * kPrep + tid, r = at / (kVB / E), x = at % (kVB / E) * E;
+          const float4 f = r < n && x < width ? *(const float4*)(gp + (t0 + r) * p.dout.step + x)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+          d[i][0] = f.x; d[i][1] = f.y; d[i][2] = f.z; d[i][3] = f.w;
+        }
+        load_scaled_rows<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid, k_done);
+        load_scaled_rows<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid, q_done);
+      }
+      bar(1, kPrep);
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const int at = i * kPrep + tid, r = at / (kVB / E);
+        if constexpr (NI == 1) {
+          const uint4 q = *(const uint4*)(st + 2 * G::KT + at16<kVB * 2>(r, at % (kVB / E)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf((&q.x)[e]);
+            d[i][2 * e] = f.x;
+            d[i][2 * e + 1] = f.y;
+          }
+        }
+        const float s = inverse_pow2(g.qup[r]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          d[i][e] *= s;
+          m = fmaxf(m, fabsf(d[i][e]));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane == 0) scratch.most[warp] = m;
+      bar(1, kPrep);
+#pragma unroll
+      for (int i = 0; i < kPrep / 32; ++i) m = fmaxf(m, scratch.most[i]);
+      const Scale so = scale_to<10>(m);
+      if (tid == 0) g.dout = so.down;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const int at = i * kPrep + tid, r = at / (kVB / E);
+        uint32_t q[E / 2][NI];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) split2<NI>(d[i][e] * so.up, d[i][e + 1] * so.up, q[e / 2]);
+        if constexpr (NI == 1) {
+          *(uint4*)(st + 2 * G::KT + at16<kVB * 2>(r, at % (kVB / E))) =
+              make_uint4(q[0][0], q[1][0], q[2][0], q[3][0]);
+        } else {
+          const int x = at % (kVB / E);
+          uint8_t* to = st + 2 * G::KT + at16<kVB * 2>(r, x >> 1) + (x & 1) * 8;
+#pragma unroll
+          for (int k = 0; k < NI; ++k) *(uint2*)(to + k * C * kVB * 2) = make_uint2(q[0][k], q[1][k]);
+        }
+      }
+      prepare<NI, DK, kParts, true>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
+                                    sm + G::kP + (c & 1) * G::PT, g, scratch, tid, [&] {
                                       scan_gates<C>(gates[(c + 2) % 3], raw, lane);  // (c - 1)
                                       load_raw(c - 2);
                                     });
@@ -508,7 +726,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
       copy_commit();
       if (G::NS > 2 && nc > 1) load(nc - 2);
       copy_commit();
-      if (warp == 3) {
+      if (warp == 0) {
         load_raw(nc - 1);
         scan_gates<C>(gates[(nc - 1) % 3], raw, lane);
         load_raw(nc - 2);
@@ -529,29 +747,50 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
       __syncthreads();
     }
   } else {
-    const int w0 = (warp - kPrep / 32) * 16;
+    more_registers<kWalkRegs>();
+    const int wi = warp - kPrep / 32, vg = wi / WK, kg = wi % WK;
+    const int w0 = vg * 16, k0 = kg * (DK / WK);
     const int v = v0 + w0 + (lane >> 2), c2 = (lane & 3) * 2;
+    auto owns = [&](int block) { return WK == 1 || block / OB == kg; };
+    float4* ex = (float4*)(sm + G::kX) + (long long)vg * WK * NC * 32;
+    const bool idle = w0 >= width;
     float x[NK][4];  // D
-    get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, p.dk, lane);
+    get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, k0, p.dk, lane);
+    float2 most = row_max<NK>(x);
     __syncthreads();
     for (int c = nc - 1; c >= 0; --c) {
+      if (idle) {
+        __syncthreads();
+        continue;
+      }
       const uint32_t Q = smem32(stage(c)), K = Q + G::KT, dO = K + G::KT;
       const uint32_t M = smem32(sm + G::kM + (c & 1) * G::MT), P = smem32(sm + G::kP + (c & 1) * G::PT);
       const Gates<C>& g = gates[c % 3];
       const int n = min(C, len - c * C);
-      put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, p.dk, lane);
+      put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, k0, p.dk, lane);
       float f[NC][4];  // dU^T, then dv^T
+      {
+        const RowScales sx = row_scales(most);
+        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, lane);
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[i][e] = 0.f;
-      state_times<NI, 0, DK, NK, NC>(f, f, x, K, K, lane);
+          for (int e = 0; e < 4; ++e) f[i][e] *= e < 2 ? sx.down0 : sx.down1;
+        if constexpr (WK > 1) {
+          float4* mine = ex + kg * NC * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) mine[i * 32] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+          bar(3 + vg, 32 * WK);
+          add_warps<WK, NC>(f, ex, kg, lane);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const float2 t = *(const float2*)&g.tail[8 * i + c2];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[i][e] *= e & 1 ? t.y : t.x;
       }
+      const float so = p.scale * g.dout;
       // dO's rows v, steps 16 k ... as a left operand
       auto dout_left = [&](uint32_t (&a)[NI][4], int k) {
 #pragma unroll
@@ -560,23 +799,38 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
       };
       // P^T dO for the steps of block k
       auto from_out = [&](int k) {
+        float d[2][4];
+        zero(d);
 #pragma unroll
         for (int i = k; i < NB; ++i) {
           uint32_t a[NI][4], r[kParts][2][2];
           dout_left(a, i);
           load_right_t<G::PB, kParts, 2>(r, P, C * G::PB, lane, 16 * k, 16 * i);
-          mma_parts<NI, kParts, 2>(f + 2 * k, a, r);
+          mma_parts<NI, kParts, 2>(d, a, r);
         }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[2 * k + q][e] = fmaf(so, d[q][e], f[2 * k + q][e]);
       };
       // from the last block back: y = dU - X^T beta dU, dv = beta y, and what dv takes
       // off dU of the earlier blocks (the order of issue as in the walk)
       uint32_t av[kParts][4];
+      RowScales su;
+      auto add_scaled = [&](float (*to)[4], const float (&d)[2][4]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[q][e] = fmaf(e < 2 ? su.down0 : su.down1, d[q][e], to[q][e]);
+      };
       auto rest = [&](int k) {
 #pragma unroll
         for (int i = 0; i < 2 * k - 2; i += 2) {
           uint32_t r[kParts][2][2];
+          float d[2][4];
           load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
-          mma_parts<kParts, kParts, 2>(f + i, av, r);
+          mma_short(d, av, r);
+          add_scaled(f + i, d);
         }
       };
       from_out(NB - 1);
@@ -589,109 +843,135 @@ __global__ void __launch_bounds__(256, 1) k_delta_back(const DeltaBack p) {
         for (int q = 0; q < 2; ++q) {
           const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            d[q][e] = 0.f;
-            y[q][e] = f[2 * k + q][e] * (e & 1 ? be.y : be.x);
-          }
+          for (int e = 0; e < 4; ++e) y[q][e] = f[2 * k + q][e] * (e & 1 ? be.y : be.x);
         }
-        as_left<kParts>(a, y[0], y[1]);
+        const RowScales sy = row_scales(row_max<2>(y));
+        as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
         mma_short(d, a, r);
         if (k + 1 < NB) rest(k + 1);
         if (k > 0) from_out(k - 1);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
+          const int at = 16 * k + 8 * q + c2;
+          const float2 be = *(const float2*)&g.beta[at], xs = *(const float2*)&g.xs[at];
+          const float2 ku = *(const float2*)&g.kup[at];
           float* yp = ys + (long long)c * C * p.dv;
+          float yv[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float yv = f[2 * k + q][e] + d[q][e];
-            const int i = 16 * k + 8 * q + c2 + (e & 1), vv = w0 + (lane >> 2) + 8 * (e >> 1);
-            if (v0 + vv < p.dv) yp[(long long)i * p.dv + vv] = yv;
-            f[2 * k + q][e] = yv * (e & 1 ? be.y : be.x);
+            yv[e] = fmaf((e < 2 ? sy.down0 : sy.down1) * (e & 1 ? xs.y : xs.x), d[q][e], f[2 * k + q][e]);
+            f[2 * k + q][e] = yv[e] * (e & 1 ? be.y : be.x);
+          }
+          if (owns(k)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = at + (e & 1), vv = w0 + (lane >> 2) + 8 * (e >> 1);
+              if (vv < width) yp[(long long)i * p.dv + vv] = yv[e] * inverse_pow2(e & 1 ? ku.y : ku.x);
+            }
+            const float* z = f[2 * k + q];
+            const float r4[4] = {z[0] * ku.x, z[1] * ku.y, z[2] * ku.x, z[3] * ku.y};
+            put_steps<T>(r4, out + (long long)c * C * out_step + w0, out_step, 16 * k + 8 * q, n, v0 + w0,
+                         p.dv, lane);
           }
         }
-        as_left<kParts>(av, f[2 * k], f[2 * k + 1]);
+        su = row_scales(row_max<2>(f + 2 * k));
+        as_left<kParts>(av, f[2 * k], f[2 * k + 1], su.up0, su.up1);
         if (k > 0) {
           load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k - 16, 16 * k);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[q][e] = f[2 * k - 2 + q][e];
           mma_short(d, av, r);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[2 * k - 2 + q][e] = d[q][e];
+          add_scaled(f + 2 * k - 2, d);
         }
       }
-      T* at = out + (long long)c * C * out_step + w0;
-#pragma unroll
-      for (int i = 0; i < NC; ++i) put_steps<T>(f[i], at, out_step, 8 * i, n, v0 + w0, p.dv, lane);
       uint32_t y[NB][kParts][4];
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
+      for (int i = 0; i < NC; ++i) {
+        const float2 l = *(const float2*)&g.lead[8 * i + c2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float2 l = *(const float2*)&g.lead[16 * k + 8 * q + c2];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[2 * k + q][e] *= -(e & 1 ? l.y : l.x);
-        }
-        as_left<kParts>(y[k], f[2 * k], f[2 * k + 1]);
+        for (int e = 0; e < 4; ++e) f[i][e] *= -(e & 1 ? l.y : l.x);
       }
-      state_add<NI, DK, NK, NB>(x, g.last, y, K, lane, [](int) {});
+      {
+        const RowScales sw = row_scales(row_max<NC>(f));
+#pragma unroll
+        for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
+        state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, lane, [](int) {});
+      }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         uint32_t a[NI][4];
         dout_left(a, k);
-        float d[2][4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float2 l = *(const float2*)&g.lead[16 * k + 8 * q + c2];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int w = 2 * q + (e >> 1);
-            float s = 0.f;
-#pragma unroll
-            for (int i = NI - 1; i >= 0; --i)
-              s += __uint_as_float(e & 1 ? a[i][w] & 0xffff0000u : a[i][w] << 16);
-            d[q][e] = s * p.scale * (e & 1 ? l.y : l.x);
+        for (int w = 0; w < 4; ++w) {
+          float2 s = unpack_half(a[0][w]);
+          if (NI == 2) {
+            const float2 t = unpack_half(a[NI - 1][w]);
+            s.x += t.x;
+            s.y += t.y;
           }
+          // registers 0, 1: rows g, g + 8 of the first eight steps; 2, 3: of the others
+          const float2 l = *(const float2*)&g.lead[16 * k + 8 * (w >> 1) + c2];
+          f[2 * k + (w >> 1)][2 * (w & 1)] = s.x * so * l.x;
+          f[2 * k + (w >> 1)][2 * (w & 1) + 1] = s.y * so * l.y;
         }
-        as_left<kParts>(y[k], d[0], d[1]);
       }
-      state_add<NI, DK, NK, NB>(x, 1.f, y, Q, lane, [](int) {});
+      const RowScales sw = row_scales(row_max<NC>(f));
+#pragma unroll
+      for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
+      most = state_add<NI, DK, NK, NB>(x, 1.f, y, sw, Q, k0, lane, [](int) {});
       __syncthreads();
     }
-    if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, p.dk, lane);
+    if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, k0, p.dk, lane);
   }
-  clear_rows<T>(out, out_step, len, p.T, min(kVB, p.dv - v0), tid, blockDim.x);
+  clear_rows<T>(out, out_step, len, p.T, width, tid, blockDim.x);
 }
 
-// CTAs of a walk: four warps that prepare, and one for 16 columns of v.
-dim3 walk_grid(int H, int B, int dv) { return dim3(H * ((dv + kVB - 1) / kVB), B); }
-int walk_threads(int dv) { return kPrep + 32 * ((min(dv, kVB) + 15) / 16); }
+// CTAs of a walk
+dim3 walk_grid(int H, int B, int dv, int wk) { return dim3(H * ((dv + kVB / wk - 1) / (kVB / wk)), B); }
+constexpr int kThreads = kPrep + 32 * kWalkers;
 
-template <int NI, int DK, bool kStates>
+template <int NI, int DK, int WK, bool kStates>
 cudaError_t walk_t(const DeltaWalk& p, cudaStream_t s) {
-  constexpr size_t smem = Geom<NI, DK, kOutParts<NI>>::smem;
+  constexpr size_t smem = Geom<NI, DK, kOutParts<NI>, WK, kStates ? 1 : 2>::smem;
   static_assert(smem <= 232448, "");
-  const cudaError_t e = cudaFuncSetAttribute(k_delta_walk<NI, DK, kStates>,
+  const cudaError_t e = cudaFuncSetAttribute(k_delta_walk<NI, DK, WK, kStates>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(kStates ? "delta_states" : "delta_walk", s);
-  k_delta_walk<NI, DK, kStates><<<walk_grid(p.H, p.B, p.dv), walk_threads(p.dv), smem, s>>>(p);
+  k_delta_walk<NI, DK, WK, kStates>
+      <<<walk_grid(p.H, p.B, p.dv, WK), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
-template <int NI, int DK>
+template <int NI, int DK, int WK>
 cudaError_t back_t(const DeltaBack& p, cudaStream_t s) {
-  constexpr size_t smem = Geom<NI, DK, kParts>::smem;
+  constexpr size_t smem = Geom<NI, DK, kParts, WK, 1>::smem;
   static_assert(smem <= 232448, "");
-  const cudaError_t e = cudaFuncSetAttribute(k_delta_back<NI, DK>,
+  const cudaError_t e = cudaFuncSetAttribute(k_delta_back<NI, DK, WK>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls("delta_back", s);
-  k_delta_back<NI, DK><<<walk_grid(p.H, p.B, p.dv), walk_threads(p.dv), smem, s>>>(p);
+  k_delta_back<NI, DK, WK><<<walk_grid(p.H, p.B, p.dv, WK), kThreads, smem, s>>>(p);
   return cudaGetLastError();
+}
+
+// Warps that share 16 columns of v.
+int warps_per_rows(int B, int H, int dv) {
+  // one CTA an SM: as many as leave every CTA a SM of its own
+  for (int wk = 4; wk > 1; wk /= 2) {
+    const dim3 g = walk_grid(H, B, dv, wk);
+    if ((long long)g.x * g.y <= kLaSms) return wk;
+  }
+  return 1;
+}
+template <int NI, int DK, bool kStates>
+cudaError_t walk_k(const DeltaWalk& p, cudaStream_t s) {
+  const int wk = warps_per_rows(p.B, p.H, p.dv);
+  return wk == 4   ? walk_t<NI, DK, 4, kStates>(p, s)
+         : wk == 2 ? walk_t<NI, DK, 2, kStates>(p, s)
+                   : walk_t<NI, DK, 1, kStates>(p, s);
+}
+template <int NI, int DK>
+cudaError_t back_k(const DeltaBack& p, cudaStream_t s) {
+  const int wk = warps_per_rows(p.B, p.H, p.dv);
+  return wk == 4 ? back_t<NI, DK, 4>(p, s) : wk == 2 ? back_t<NI, DK, 2>(p, s) : back_t<NI, DK, 1>(p, s);
 }
 
 // One token: A = a S, e = v - A k, S' = A + beta e k^T, o = s S' q.  A row of the
@@ -803,22 +1083,22 @@ cudaError_t step_t(const DeltaStep& p, cudaStream_t s) {
 
 cudaError_t delta_walk(const DeltaWalk& p, bool bf16, cudaStream_t s) {
   if (p.hist) {
-    if (bf16) return p.dk <= 64 ? walk_t<1, 64, true>(p, s) : walk_t<1, 128, true>(p, s);
-    return p.dk <= 64 ? walk_t<3, 64, true>(p, s) : walk_t<3, 128, true>(p, s);
+    if (bf16) return p.dk <= 64 ? walk_k<1, 64, true>(p, s) : walk_k<1, 128, true>(p, s);
+    return p.dk <= 64 ? walk_k<2, 64, true>(p, s) : walk_k<2, 128, true>(p, s);
   }
-  if (bf16) return p.dk <= 64 ? walk_t<1, 64, false>(p, s) : walk_t<1, 128, false>(p, s);
-  return p.dk <= 64 ? walk_t<3, 64, false>(p, s) : walk_t<3, 128, false>(p, s);
+  if (bf16) return p.dk <= 64 ? walk_k<1, 64, false>(p, s) : walk_k<1, 128, false>(p, s);
+  return p.dk <= 64 ? walk_k<2, 64, false>(p, s) : walk_k<2, 128, false>(p, s);
 }
 
 cudaError_t delta_back(const DeltaBack& p, bool bf16, cudaStream_t s) {
-  if (bf16) return p.dk <= 64 ? back_t<1, 64>(p, s) : back_t<1, 128>(p, s);
-  return p.dk <= 64 ? back_t<3, 64>(p, s) : back_t<3, 128>(p, s);
+  if (bf16) return p.dk <= 64 ? back_k<1, 64>(p, s) : back_k<1, 128>(p, s);
+  return p.dk <= 64 ? back_k<2, 64>(p, s) : back_k<2, 128>(p, s);
 }
 
 cudaError_t delta_step(const DeltaStep& p, bool bf16, cudaStream_t s) {
   return bf16 ? step_t<__nv_bfloat16>(p, s) : step_t<float>(p, s);
 }
 
-int delta_chunk(bool bf16) { return bf16 ? kSteps<1> : kSteps<3>; }
+int delta_chunk(bool bf16) { return bf16 ? kSteps<1> : kSteps<2>; }
 
 }  // namespace ssd

@@ -1,13 +1,12 @@
 // What the kernels of the gated delta rule share: products of operands that are
-// carried as several bf16 parts, and what a chunk of steps needs besides its
-// operands.
+// carried as fp16 parts, and what a chunk of steps needs besides its operands.
 //
 // The rule: e_t = v_t - a_t S_{t-1} k_t, S_t = a_t S_{t-1} + beta_t e_t k_t^T,
 // o_t = s S_t q_t, with a_t = e^{log_decay_t}.  In a chunk of C steps, with g_i
 // the sum of the log decays up to step i, Gamma_ij = e^{g_i - g_j} for j <= i, H
 // the state before the chunk ([dv][dk]) and L_ij = Gamma_ij k_i . k_j for j < i,
 //   F = V - e^g K H^T,  (I + L beta) E = F,  U = beta E
-//   O = s e^g Q H^T + P U,  P_ij = s Gamma_ij q_i . k_j for j <= i
+//   O = s e^g Q H^T + s P U,  P_ij = Gamma_ij q_i . k_j for j <= i
 //   H <- e^G H + U^T (e^{G-g} K),  G = g at the last step
 // E is found by forward substitution over blocks of 16 steps: inside a block
 // (I + L beta)^-1 = I - X beta, X = L (I + beta L)^-1 (strictly lower), and what a
@@ -15,13 +14,23 @@
 // chunk by repeated squaring would lose everything to cancellation where keys are
 // alike: powers of L grow like binomials.)
 //
-// Precision: every operand of a matrix instruction is a sum of bf16 parts of 8
-// significant bits, exact for bf16 tensors and three parts for everything held in
-// 32 bits; of the products of parts those up to 2^-16 are formed, what is left out
-// is below 2^-24 of the product.  Sums are fp32.
+// Precision: a matrix instruction takes fp16 operands of 11 significant bits and
+// sums in fp32.  A value held in 32 bits is two such parts, hi + lo (22 bits), and a
+// product of two of them hi hi + hi lo + lo hi; what is left out is below 2^-22 of
+// it.  A bf16 element is one part.  Three bf16 parts (24 bits) need six products
+// instead of three, and one more a product with a bf16 tensor; two (16 bits) left
+// 4e-6 of the states and 9e-5 of dlog_decay.
+//
+// fp16 has few powers of two, so every operand is scaled by one.  Keys: the rule does
+// not change with k 2^n, v 2^n, beta 2^-2n in place of k, v, beta for a step, and n is
+// taken such that the largest element of k is in [1, 2); L, X, E and U below are those
+// of the rows so scaled ("of k's scale").  Queries the same way, 2^-n going into the
+// output.  Left operands (the state, U and so on) are scaled row by row, by the
+// largest element; what is 2^-24 of that and less loses bits, as it would in a sum.
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -31,9 +40,9 @@
 namespace ssd {
 namespace delta {
 
-constexpr int kPrep = 128;   // threads that prepare the next chunk
-constexpr int kVB = 64;      // columns of v of a CTA: up to four warps of 16
-constexpr int kParts = 3;    // parts of a value held in 32 bits
+constexpr int kPrep = 256;   // threads that prepare the next chunk
+constexpr int kVB = 64;      // columns of v of a tile
+constexpr int kParts = 2;    // parts of a value held in 32 bits
 
 // Byte offset of a 16-byte piece of a tile whose rows are RB bytes: pieces of
 // eight consecutive rows fall on all 32 banks.
@@ -44,20 +53,56 @@ __device__ __forceinline__ uint32_t at16(int row, int piece) {
   return row * RB + ((piece ^ ((row >> 2) & 1)) << 4);
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// two values as N bf16 parts each
+__device__ __forceinline__ float2 unpack_half(uint32_t x) {
+  return __half22float2(*(const __half2*)&x);
+}
+__device__ __forceinline__ float2 unpack_bf(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+// two values as N fp16 parts each
 template <int N>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    p[i] = pack2(x, y);
-    x -= __uint_as_float(p[i] << 16);
-    y -= __uint_as_float(p[i] & 0xffff0000u);
+  p[0] = pack_half(x, y);
+  if constexpr (N == 2) {
+    const float2 f = unpack_half(p[0]);
+    p[1] = pack_half(x - f.x, y - f.y);
   }
+}
+
+// The power of two that brings m > 0 into [2^T, 2^{T+1}), and its inverse; infinities
+// and NaN stay what they are.
+struct Scale {
+  float up, down;
+};
+template <int T>
+__device__ __forceinline__ Scale scale_to(float m) {
+  int e = (int)(__float_as_uint(m) >> 23);  // (m >= 0)
+  e = e < 40 ? 40 : e > 250 ? 250 : e;
+  return {__uint_as_float((uint32_t)(254 + T - e) << 23), __uint_as_float((uint32_t)(e - T) << 23)};
+}
+// The same for a row of k or q: into [1, 2), by 2^-63 to 2^63, rows of zeros as they are.
+__device__ __forceinline__ float row_exponent(float m) {
+  int e = (int)(__float_as_uint(m) >> 23);
+  e = m == 0.f ? 127 : e < 64 ? 64 : e > 190 ? 190 : e;
+  return __uint_as_float((uint32_t)(254 - e) << 23);
+}
+__device__ __forceinline__ float inverse_pow2(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+// the largest over the four lanes that hold a row of a product
+__device__ __forceinline__ float quad_max(float m) {
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
 __device__ __forceinline__ uint32_t smem32(const void* p) {
@@ -84,10 +129,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // 8 x 8 of 16 bit
 // columns 2 t and 2 t + 1, then row g + 8; a row g, terms 2 t and 2 t + 1, row
 // g + 8, then both at terms + 8; b terms 2 t and 2 t + 1 of column g, then + 8.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
       " {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int N>
+__device__ __forceinline__ void zero(float (&d)[N][4]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
 }
 
 // Where lane `lane` points for the four 8 x 8 pieces of ldmatrix, in a tile with
@@ -162,17 +214,19 @@ __device__ __forceinline__ void load_right_t(uint32_t (&b)[PB][N][2], uint32_t t
       b[p][i + 1][1] = r[3];
     }
 }
-// Two columns of eight of a product's result as the left operand of 16 terms of
-// the next one.
+// Two columns of eight of a product's result, rows g times s0 and g + 8 times s1, as
+// the left operand of 16 terms of the next one.
 template <int P>
-__device__ __forceinline__ void as_left(uint32_t (&a)[P][4], const float (&x)[4], const float (&y)[4]) {
+__device__ __forceinline__ void as_left(uint32_t (&a)[P][4], const float (&x)[4], const float (&y)[4],
+                                        float s0, float s1) {
   uint32_t r[P];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    split2<P>(x[2 * e], x[2 * e + 1], r);
+    const float s = e ? s1 : s0;
+    split2<P>(x[2 * e] * s, x[2 * e + 1] * s, r);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][e] = r[p];
-    split2<P>(y[2 * e], y[2 * e + 1], r);
+    split2<P>(y[2 * e] * s, y[2 * e + 1] * s, r);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][2 + e] = r[p];
   }
@@ -188,68 +242,132 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Registers of a warp group from here on (kernels of 384 threads start with 168).
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // ---- a chunk's tiles ------------------------------------------------------------
 
-// NI: parts of an element of q, k, v (bf16: one; fp32: three).  fp32 takes chunks
-// of 32 steps, since three parts of 64 would not fit beside each other.
+// NI: parts of an element of q, k, v (bf16: one; fp32: two).  fp32 takes chunks of 32
+// steps.
 template <int NI>
 constexpr int kSteps = NI == 1 ? 64 : 32;
 
-// C rows of D elements (a multiple of 64) as NI part tiles `C * D * 2` bytes apart,
-// from rows `stride` elements apart; past row n and past `width` (a multiple of 8)
-// zeros.  bf16: asynchronous copies, to be committed by the caller.
-template <int NI, int C, int D, int NT>
-__device__ __forceinline__ void load_tile(uint8_t* tile, const void* src, long long stride, int n,
-                                          int width, int tid) {
-  constexpr int RB = D * 2;
-  if constexpr (NI == 1) {
-    const __nv_bfloat16* s = (const __nv_bfloat16*)src;
-#pragma unroll 4
-    for (int i = tid; i < C * (D / 8); i += NT) {
-      const int r = i / (D / 8), x = i % (D / 8);
-      const bool in = r < n && x * 8 < width;
-      copy16(tile + at16<RB>(r, x), in ? s + r * stride + x * 8 : s, in);
-    }
-  } else {
-    const float* s = (const float*)src;
-    constexpr int per = C * (D / 4) / NT;
-    static_assert(C * (D / 4) % NT == 0, "");
+// bf16: C rows of D elements from rows `stride` elements apart, as asynchronous copies
+// to be committed by the caller; past row n and past `width` (a multiple of 8) zeros.
+template <int C, int D, int NT>
+__device__ __forceinline__ void load_tile(uint8_t* tile, const __nv_bfloat16* s, long long stride,
+                                          int n, int width, int tid) {
+  constexpr int RB = D * 2, LPR = D / 8, R = NT / LPR;  // R rows at a time
+  static_assert(C % R == 0 && R % 8 == 0, "");
+  const int r = tid / LPR, x = tid % LPR;
+  const uint32_t to = smem32(tile) + at16<RB>(r, x);
+  const __nv_bfloat16* from = s + r * stride + x * 8;
+  const bool in = x * 8 < width;
 #pragma unroll
-    for (int b = 0; b < per; b += 8) {  // eight 16-byte loads on their way at a time
-      float4 f[8];
+  for (int i = 0; i < C / R; ++i) {  // (the pieces' places repeat every eight rows)
+    const bool here = in && r + i * R < n;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * R * RB),
+                 "l"(here ? from : s), "r"(here ? 16 : 0)
+                 : "memory");
+    from += R * stride;
+  }
+}
+// The largest magnitude of eight bf16 (one of the two halves' bits; NaN is passed over).
+__device__ __forceinline__ float max_bf(const uint4& q) {
+  const __nv_bfloat162* h = (const __nv_bfloat162*)&q;
+  const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ uint4 bf_to_half(const uint4& q, float s) {
+  uint4 r;
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (b + u < per) {
-          const int i = tid + (b + u) * NT, r = i / (D / 4), x = i % (D / 4);
-          f[u] = r < n && x * 4 < width ? *(const float4*)(s + r * stride + x * 4)
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_bf((&q.x)[i]);
+    (&r.x)[i] = pack_half(f.x * s, f.y * s);
+  }
+  return r;
+}
+// A bf16 tile to fp16 in place, row by row, each scaled into [1, 2); done(row, scale)
+// by one lane a row.
+template <int C, int DK, int NT, typename F>
+__device__ __forceinline__ void scale_rows(uint8_t* tile, int tid, F done) {
+  constexpr int RB = DK * 2, LPR = DK / 8, N = C * LPR / NT;
+  static_assert(C * LPR % NT == 0, "");
+  uint4 q[N];
+  float m[N];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (b + u < per) {
-          const int i = tid + (b + u) * NT, r = i / (D / 4), x = i % (D / 4);
-          uint32_t p[NI], q[NI];
-          split2<NI>(f[u].x, f[u].y, p);
-          split2<NI>(f[u].z, f[u].w, q);
-          uint8_t* at = tile + at16<RB>(r, x >> 1) + (x & 1) * 8;
+  for (int i = 0; i < N; ++i) {
+    const int at = i * NT + tid;
+    q[i] = *(const uint4*)(tile + at16<RB>(at / LPR, at % LPR));
+  }
 #pragma unroll
-          for (int k = 0; k < NI; ++k) *(uint2*)(at + k * C * RB) = make_uint2(p[k], q[k]);
-        }
-    }
+  for (int i = 0; i < N; ++i) m[i] = max_bf(q[i]);
+#pragma unroll
+  for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = i * NT + tid, r = at / LPR, x = at % LPR;
+    const float s = row_exponent(m[i]);
+    *(uint4*)(tile + at16<RB>(r, x)) = bf_to_half(q[i], s);
+    if (x == 0) done(r, s);
+  }
+}
+// The same for fp32 rows in global memory: two fp16 parts, C * DK * 2 bytes apart.
+template <int C, int DK, int NT, typename F>
+__device__ __forceinline__ void load_scaled_rows(uint8_t* tile, const float* src, long long stride,
+                                                 int n, int width, int tid, F done) {
+  constexpr int RB = DK * 2, LPR = DK / 4, N = C * LPR / NT;
+  static_assert(C * LPR % NT == 0 && LPR <= 32, "");
+#pragma unroll
+  for (int b = 0; b < N; b += 8) {  // up to eight 16-byte loads on their way at a time
+    float4 f[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (b + u < N) {
+        const int at = (b + u) * NT + tid, r = at / LPR, x = at % LPR;
+        f[u] = r < n && x * 4 < width ? *(const float4*)(src + r * stride + x * 4)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (b + u < N) {
+        const int at = (b + u) * NT + tid, r = at / LPR, x = at % LPR;
+        float m = fmaxf(fmaxf(fabsf(f[u].x), fabsf(f[u].y)), fmaxf(fabsf(f[u].z), fabsf(f[u].w)));
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = row_exponent(m);
+        uint32_t p[2], q[2];
+        split2<2>(f[u].x * s, f[u].y * s, p);
+        split2<2>(f[u].z * s, f[u].w * s, q);
+        uint8_t* to = tile + at16<RB>(r, x >> 1) + (x & 1) * 8;
+        *(uint2*)to = make_uint2(p[0], q[0]);
+        *(uint2*)(to + C * RB) = make_uint2(p[1], q[1]);
+        if (x == 0) done(r, s);
+      }
   }
 }
 
 // Per step of a chunk: the sum g of the log decays (of base 2), as two floats, so that
 // a difference of two sums is good to its own last bit however long they have grown;
-// the write strength; and e^g, e^{G-g}.
+// e^g, e^{G-g}; the write strength, of k's scale; the powers of two that k and q were
+// multiplied by; and X's columns': what its column was divided by.
 template <int C>
 struct alignas(16) Gates {
-  float hi[C], lo[C], beta[C], lead[C], tail[C];
-  float last;  // e^G
+  float hi[C], lo[C], lead[C], tail[C], beta[C], kup[C], qup[C], xs[C];
+  float last;    // e^G
+  float dout;    // the walk back: what dO's tile was divided by
 };
 
 struct Two {
@@ -277,8 +395,8 @@ template <int C>
 struct RawGates {
   float decay[C / 32], beta[C / 32];
 };
-// (log decays of base 2; below -200 a log decay is as good as -inf, as e^-104 is the
-// smallest float, and keeps sums finite; NaN stays; past n 0)
+// (log decays below -200 are as good as -inf, as e^-104 is the smallest float, and keep
+// sums finite; NaN stays; past n 0)
 template <int C>
 __device__ __forceinline__ void load_gates(RawGates<C>& x, const float* log_decay, const float* beta,
                                            long long at, long long stride, int n, int lane) {
@@ -332,11 +450,12 @@ __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float
 }
 
 // What the walks read of a chunk besides its operands, in parts (tiles [C][C]): in M
-// -L below the blocks of 16 on the diagonal and in them -X^T, and P.
+// -L below the blocks of 16 on the diagonal and in them -X^T, its rows scaled, and P.
 constexpr int kDiag = 20;  // floats of a column of a diagonal block
 template <int C>
 struct alignas(16) Scratch {
   float diag[C / 16][16][kDiag];  // L[i][j] at [j][i], a warp each
+  float most[kPrep / 32];
 };
 
 // One block of 16 x 16 of A K^T, rows 16 bi ..., columns 16 bj ..., times the decays
@@ -348,10 +467,7 @@ __device__ __forceinline__ void score_block(uint32_t A, uint32_t K, uint8_t* out
                                             int bj, float factor, int lane) {
   constexpr int C = kSteps<NI>, RB = DK * 2, OB = C * 2;
   float acc[2][4];
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  zero(acc);
   constexpr int U = NI == 1 ? DK / 16 : 2;  // (every operand of a bf16 block on its way at once)
 #pragma unroll(U)
   for (int k = 0; k < DK; k += 16) {
@@ -393,7 +509,7 @@ __device__ __forceinline__ void score_block(uint32_t A, uint32_t K, uint8_t* out
 // and T = I - beta X, so once X_mj is whole, T_mj = -beta_m X_mj (1 for m = j) adds
 // L_im T_mj to every later X_ij.
 template <int C>
-__device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, const float (*diag)[kDiag],
+__device__ __forceinline__ void invert_diag(uint8_t* out, Gates<C>& g, const float (*diag)[kDiag],
                                             int s, int j) {
   constexpr int OB = C * 2;
   float x[16];
@@ -411,11 +527,17 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, con
       if (i + 3 > m) x[i + 3] = fmaf(l.w, t, x[i + 3]);
     }
   }
+  float m = 0.f;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+  const Scale sx = scale_to<8>(m);
+  g.xs[16 * s + j] = sx.down;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t p[4][kParts];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split2<kParts>(-x[8 * h + 2 * i], -x[8 * h + 2 * i + 1], p[i]);
+    for (int i = 0; i < 4; ++i)
+      split2<kParts>(-x[8 * h + 2 * i] * sx.up, -x[8 * h + 2 * i + 1] * sx.up, p[i]);
     uint8_t* at = out + at16<OB>(16 * s + j, 2 * s + h);
 #pragma unroll
     for (int q = 0; q < kParts; ++q)
@@ -423,18 +545,18 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, const Gates<C>& g, con
   }
 }
 
-// M and, with kP, P times `scale` of a chunk whose operands and gates are in shared
-// memory, by the kPrep threads: a warp takes one of L's diagonal blocks and inverts
-// it, then its share of the other blocks of L and of P.  (The blocks go through one
-// loop: as straight code with the strips known at compile time the four warps' code
-// and the walk's did not fit the instruction caches together, and waiting for
-// instructions was the largest of all stalls.)  The last warp has `aside` to do as
-// well (the gates of a later chunk).
+// M and, with kP, P of a chunk whose operands and gates are in shared memory, by the
+// kPrep threads: a warp takes one of L's diagonal blocks and inverts it, the others the
+// blocks below the diagonal and those of P.  (The blocks go through one loop: as
+// straight code, with the strips of a warp known at compile time, the warps' code and
+// the walk's did not fit the instruction caches together, and waiting for instructions
+// was the largest of all stalls.)  Warp 0 has `aside` to do as well (the gates of a
+// later chunk).
 template <int NI, int DK, int PP, bool kP, typename F>
 __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, uint8_t* M, uint8_t* P,
-                                        const Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc,
-                                        float scale, int tid, F aside) {
-  constexpr int C = kSteps<NI>, NB = C / 16, W = kPrep / 32;
+                                        Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc, int tid,
+                                        F aside) {
+  constexpr int C = kSteps<NI>, NB = C / 16, W = kPrep / 32 - NB;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t K = smem32(Kt), Q = smem32(Qt);
   if (warp < NB) {
@@ -442,23 +564,25 @@ __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, ui
     __syncwarp();
     if (lane < 16) invert_diag<C>(M, g, sc.diag[warp], warp, lane);
     __syncwarp();
-  }
-  // L's blocks below the diagonal, rows and columns (hexadecimal digits, the first one last)
-  constexpr uint32_t kLi = NB == 4 ? 0x333221 : 0x1, kLj = NB == 4 ? 0x210100 : 0x0;
-  constexpr uint64_t kPi = NB == 4 ? 0x3333222110ull : 0x110, kPj = NB == 4 ? 0x3210210100ull : 0x100;
-  constexpr int nL = NB * (NB - 1) / 2, nP = NB * (NB + 1) / 2;
+    if (warp == 0) aside();
+  } else {
+    // L's blocks below the diagonal, rows and columns (hexadecimal digits, the first last)
+    constexpr uint32_t kLi = NB == 4 ? 0x333221 : 0x1, kLj = NB == 4 ? 0x210100 : 0x0;
+    constexpr uint64_t kPi = NB == 4 ? 0x3333222110ull : 0x110, kPj = NB == 4 ? 0x3210210100ull : 0x100;
+    constexpr int nL = NB * (NB - 1) / 2, nP = NB * (NB + 1) / 2;
+    const int w = warp - NB;
 #pragma unroll 1
-  for (int r = warp; r < nL; r += W)
-    score_block<NI, DK, kParts, false>(K, K, M, g, nullptr, kLi >> 4 * r & 15, kLj >> 4 * r & 15, -1.f,
+    for (int r = w; r < nL; r += W)
+      score_block<NI, DK, kParts, false>(K, K, M, g, nullptr, kLi >> 4 * r & 15, kLj >> 4 * r & 15, -1.f,
+                                         lane);
+    if constexpr (kP) {
+      // (in the order that leaves every warp the same number of blocks)
+#pragma unroll 1
+      for (int r = (w + W - nL % W) % W; r < nP; r += W)
+        score_block<NI, DK, PP, false>(Q, K, P, g, nullptr, kPi >> 4 * r & 15, kPj >> 4 * r & 15, 1.f,
                                        lane);
-  if constexpr (kP) {
-    // (in the order that leaves every warp the same number of blocks)
-#pragma unroll 1
-    for (int r = (warp + W - nL % W) % W; r < nP; r += W)
-      score_block<NI, DK, PP, false>(Q, K, P, g, nullptr, kPi >> 4 * r & 15, kPj >> 4 * r & 15, scale,
-                                     lane);
+    }
   }
-  if (warp == W - 1) aside();
 }
 
 }  // namespace delta

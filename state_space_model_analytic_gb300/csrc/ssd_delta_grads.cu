@@ -19,13 +19,13 @@
 // write their own gradients in fp32, summed in head order by a second kernel.
 #include <cuda_bf16.h>
 
-#include "ssd_delta.cuh"
+#include "ssd_delta3.cuh"
 #include "ssd_internal.h"
 
 namespace ssd {
 namespace {
 
-using namespace delta;
+using namespace delta3;
 
 constexpr int kThreads = 256;
 

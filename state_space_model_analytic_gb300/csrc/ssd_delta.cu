@@ -49,7 +49,7 @@ struct Geom {
   static constexpr int LV = kVB + 4;
   static constexpr int VT = NI == 1 ? C * kVB * 2 : C * LV * 4;
   static_assert(VT >= NI * C * kVB * 2, "");
-  static constexpr int NS = NI == 1 ? 3 : 2;         // stages of the operands
+  static constexpr int NS = 3;                       // stages of the operands
   static constexpr int MT = kParts * C * PB, PT = PP * C * PB;
   static constexpr int kStage = 2 * KT + VT;
   static constexpr int kM = NS * kStage, kP = kM + 2 * MT;
@@ -99,16 +99,20 @@ __device__ __forceinline__ void put_state(const float (&x)[NK][4], float* p, int
       if (v + 8 * u < dv && k0 + 8 * j < dk)
         *(float2*)(p + (v + 8 * u) * dk + 8 * j + c) = make_float2(x[j][2 * u], x[j][2 * u + 1]);
 }
-// the largest of a lane's values in its rows g and g + 8
+// the largest magnitudes of a lane's values in its rows g and g + 8
 template <int N>
-__device__ __forceinline__ float2 row_max(const float (*x)[4]) {
-  float2 m = make_float2(0.f, 0.f);
+__device__ __forceinline__ float2 row_max(const float (*x)[4], float2 m = make_float2(0.f, 0.f)) {
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    m.x = fmaxf(m.x, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
-    m.y = fmaxf(m.y, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+    m.x = max3_abs(m.x, x[j][0], x[j][1]);
+    m.y = max3_abs(m.y, x[j][2], x[j][3]);
   }
   return m;
+}
+// x times the factors of its columns
+__device__ __forceinline__ void times(float (&x)[4], float2 f) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) set_pair(x, u, mul2(pair(x, u), f));
 }
 // the scales of a warp's rows from its lanes' largest values
 struct RowScales {
@@ -117,6 +121,16 @@ struct RowScales {
 __device__ __forceinline__ RowScales row_scales(float2 m) {
   const Scale a = scale_to<10>(quad_max(m.x)), b = scale_to<10>(quad_max(m.y));
   return {a.up, a.down, b.up, b.down};
+}
+
+// x <- x + d, d's rows scaled back
+__device__ __forceinline__ void add_rows(float (&x)[4], const float (&d)[4], const RowScales& s) {
+  set_pair(x, 0, fma2(pair(d, 0), both(s.down0), pair(x, 0)));
+  set_pair(x, 1, fma2(pair(d, 1), both(s.down1), pair(x, 1)));
+}
+__device__ __forceinline__ void scale_back(float (&x)[4], const RowScales& s) {
+  set_pair(x, 0, mul2(pair(x, 0), both(s.down0)));
+  set_pair(x, 1, mul2(pair(x, 1), both(s.down1)));
 }
 
 // x (rows v, columns c0 ... of steps, eight) transposed to rows of memory: row i of
@@ -160,7 +174,7 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
 template <int NI, int PO, int DK, int NK, int NC>
 __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
                                             const float (&x)[NK][4], const RowScales& s, uint32_t K,
-                                            uint32_t Q, int k0, int lane) {
+                                            uint32_t Q, int k0, const Lane<DK * 2>& at) {
   constexpr int C = kSteps<NI>, RB = DK * 2;
   constexpr int GN = NC < 4 ? NC : 4;                     // columns of eight of a group
   constexpr int GF = NC / GN, GK = PO > 0 ? 2 * GF : GF;  // groups of 16 terms
@@ -168,10 +182,8 @@ __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4]
   uint32_t a[2][kParts][4], b[2][NI][GN][2];
   auto load = [&](int i) {
     const int k = i / GK, g = i % GK;
-    load_right<RB, NI, GN>(b[i & 1], g < GF ? K : Q, C * RB, lane, 8 * GN * (g % GF), k0 + 16 * k);
+    load_right<NI, GN>(b[i & 1], g < GF ? K : Q, C * RB, at, 8 * GN * (g % GF), k0 + 16 * k);
   };
-  zero(f);
-  if (PO > 0) zero(o);
   as_left<kParts>(a[0], x[0], x[1], s.up0, s.up1);
   load(0);
 #pragma unroll
@@ -181,14 +193,16 @@ __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4]
     if (g == 0 && 2 * k + 2 < NK)
       as_left<kParts>(a[(k + 1) & 1], x[2 * k + 2], x[2 * k + 3], s.up0, s.up1);
     if (g < GF) {
-      mma_parts<kParts, NI, GN>(f + GN * g, a[k & 1], b[i & 1]);
+      if (k == 0) mma_parts0<kParts, NI, GN>(f + GN * g, a[0], b[i & 1]);
+      else mma_parts<kParts, NI, GN>(f + GN * g, a[k & 1], b[i & 1]);
     } else if constexpr (PO > 0) {
       uint32_t ao[PO][4];
 #pragma unroll
       for (int q = 0; q < PO; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) ao[q][e] = a[k & 1][q][e];
-      mma_parts<PO, NI, GN>(o + GN * (g - GF), ao, b[i & 1]);
+      if (k == 0) mma_parts0<PO, NI, GN>(o + GN * (g - GF), ao, b[i & 1]);
+      else mma_parts<PO, NI, GN>(o + GN * (g - GF), ao, b[i & 1]);
     }
   }
 }
@@ -198,18 +212,16 @@ __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4]
 __device__ __forceinline__ void mma_short(float (&d)[2][4], const uint32_t (&a)[kParts][4],
                                           const uint32_t (&b)[kParts][2][2]) {
   float e[2][4];
-  zero(d);
-  zero(e);
 #pragma unroll
-  for (int n = 0; n < 2; ++n) mma(e[n], a[0], b[1][n][0], b[1][n][1]);
+  for (int n = 0; n < 2; ++n) mma0(e[n], a[0], b[1][n][0], b[1][n][1]);
 #pragma unroll
-  for (int n = 0; n < 2; ++n) mma(d[n], a[0], b[0][n][0], b[0][n][1]);
+  for (int n = 0; n < 2; ++n) mma0(d[n], a[0], b[0][n][0], b[0][n][1]);
 #pragma unroll
   for (int n = 0; n < 2; ++n) mma(e[n], a[1], b[0][n][0], b[0][n][1]);
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) d[n][c] += e[n][c];
+    for (int u = 0; u < 2; ++u) set_pair(d[n], u, add2(pair(d[n], u), pair(e[n], u)));
 }
 
 // x <- scale x + Y tile, Y (rows v, C steps) as parts of left operands that were scaled
@@ -217,29 +229,27 @@ __device__ __forceinline__ void mma_short(float (&d)[2][4], const uint32_t (&a)[
 // beside(i), i < ceil(NK / 4): work that is issued between the products.
 template <int NI, int DK, int NK, int NB, typename F>
 __device__ __forceinline__ float2 state_add(float (&x)[NK][4], float scale, const uint32_t (*y)[kParts][4],
-                                            const RowScales& s, uint32_t tile, int k0, int lane, F beside) {
+                                            const RowScales& s, uint32_t tile, int k0, const Lane<DK * 2>& at,
+                                            F beside) {
   constexpr int C = kSteps<NI>, RB = DK * 2, GN = NK < 4 ? NK : 4;
   float2 m = make_float2(0.f, 0.f);
 #pragma unroll
   for (int n = 0; n < NK; n += GN) {
     float d[GN][4];
-    zero(d);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       uint32_t r[NI][GN][2];
-      load_right_t<RB, NI, GN>(r, tile, C * RB, lane, k0 + 8 * n, 16 * b);
-      mma_parts<kParts, NI, GN>(d, y[b], r);
+      load_right_t<NI, GN>(r, tile, C * RB, at, k0 + 8 * n, 16 * b);
+      if (b == 0) mma_parts0<kParts, NI, GN>(d, y[b], r);
+      else mma_parts<kParts, NI, GN>(d, y[b], r);
       if (b == 0) beside(n / GN);
     }
 #pragma unroll
     for (int i = 0; i < GN; ++i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[n + i][e] = fmaf(e < 2 ? s.down0 : s.down1, d[i][e], scale * x[n + i][e]);
-      const float2 r = row_max<1>(x + n + i);
-      m.x = fmaxf(m.x, r.x);
-      m.y = fmaxf(m.y, r.y);
+      times(x[n + i], both(scale));
+      add_rows(x[n + i], d[i], s);
     }
+    m = row_max<GN>(x + n, m);
   }
   return m;
 }
@@ -297,13 +307,12 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       const int n = len - c * C;
       const long long t0 = (long long)c * C;
       uint8_t* st = stage(c);
-      if constexpr (NI == 1) {
-        load_tile<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
-        if (!kStates) load_tile<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
+      load_tile<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
+      if (!kStates) load_tile<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
+      if constexpr (NI == 1)
         load_tile<C, kVB, kPrep>(st + 2 * G::KT, vp + t0 * p.v.step, p.v.step, n, width, tid);
-      } else {
+      else
         load_floats<C, G::LV>(st + 2 * G::KT, vp + t0 * p.v.step, p.v.step, n, width, tid);
-      }
     };
     // the gates of chunk c + 1 are made ready beside the preparation of chunk c, by
     // the last warp, which has loaded them one chunk earlier
@@ -319,16 +328,17 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
         const float d = inverse_pow2(s);
         g.beta[r] *= d * d;
       };
-      auto q_done = [&](int r, float s) { g.qup[r] = s; };
+      auto q_done = [&](int r, float s) { g.qdown[r] = p.scale * inverse_pow2(s); };
       if constexpr (NI == 1) {
         scale_rows<C, DK, kPrep>(st + G::KT, tid, k_done);
         if (!kStates) scale_rows<C, DK, kPrep>(st, tid, q_done);
       } else {
-        const long long t0 = (long long)c * C;
-        load_scaled_rows<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, len - c * C, p.dk, tid,
-                                       k_done);
-        if (!kStates)
-          load_scaled_rows<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, len - c * C, p.dk, tid, q_done);
+        FloatRows<C, DK, kPrep> k, q;
+        k.read(st + G::KT, tid);
+        if (!kStates) q.read(st, tid);
+        bar(1, kPrep);
+        k.write(st + G::KT, tid, k_done);
+        if (!kStates) q.write(st, tid, q_done);
       }
       bar(1, kPrep);
       prepare<NI, DK, PP, !kStates>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
@@ -340,7 +350,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
     if (nc > 0) {
       load(0);
       copy_commit();
-      if (G::NS > 2 && nc > 1) load(1);
+      if (nc > 1) load(1);
       copy_commit();
       if (warp == 0) {
         load_raw(0);
@@ -355,9 +365,9 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
     for (int c = 0; c < nc; ++c) {
       if (c + 1 < nc) {
         // (the stage that the walk has left)
-        if (G::NS > 2 ? c + 2 < nc : true) load(G::NS > 2 ? c + 2 : c + 1);
+        if (c + 2 < nc) load(c + 2);
         copy_commit();
-        copy_wait<G::NS - 2>();
+        copy_wait<1>();
         bar(1, kPrep);
         prep(c + 1);
       }
@@ -372,6 +382,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
     auto owns = [&](int block) { return WK == 1 || block / OB == kg; };
     float4* ex = (float4*)(sm + G::kX) + (long long)vg * WK * NC * 32;
     const bool idle = w0 >= width;  // (fewer columns than warps for them)
+    const Lane<G::RB> la(lane);
+    const Lane<G::PB> lm(lane);
     float x[NK][4];
     get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, k0, p.dk, lane);
     float2 most = row_max<NK>(x);
@@ -393,14 +405,12 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       const RowScales sx = row_scales(most);
       {
         float qx[WK == 1 ? 2 * OB : NC][4];
-        state_times<NI, kStates ? 0 : PP, DK, NK, NC>(f, qx, x, sx, K, Q, k0, lane);
+        state_times<NI, kStates ? 0 : PP, DK, NK, NC>(f, qx, x, sx, K, Q, k0, la);
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[i][e] *= e < 2 ? sx.down0 : sx.down1;
-            if (!kStates) qx[i][e] *= e < 2 ? sx.down0 : sx.down1;
-          }
+        for (int i = 0; i < NC; ++i) {
+          scale_back(f[i], sx);
+          if (!kStates) scale_back(qx[i], sx);
+        }
         if constexpr (WK > 1) {
           float4* mine = ex + kg * NC * 32 + lane;
           constexpr int kO = kWalkers * NC * 32;  // o's after f's
@@ -456,19 +466,16 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
         for (int q = 0; q < 2; ++q) {
           const float2 l = *(const float2*)&g.lead[8 * (i + q) + c2];
           const float2 ku = *(const float2*)&g.kup[8 * (i + q) + c2];
+          const float2 minus = make_float2(-l.x, -l.y);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            f[i + q][2 * u] = fmaf(-l.x, f[i + q][2 * u], ku.x * val[q][2 * u]);
-            f[i + q][2 * u + 1] = fmaf(-l.y, f[i + q][2 * u + 1], ku.y * val[q][2 * u + 1]);
-          }
+          for (int u = 0; u < 2; ++u)
+            set_pair(f[i + q], u, fma2(minus, pair(f[i + q], u), mul2(ku, pair(val[q], u))));
         }
       }
       if constexpr (!kStates) {
 #pragma unroll
         for (int i = 0; i < 2 * OB; ++i) {
-          const float2 l = *(const float2*)&g.lead[(WK == 1 ? 0 : min(kg * OB, NB - OB) * 16) + 8 * i + c2];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= e & 1 ? l.y : l.x;
+          times(o[i], *(const float2*)&g.lead[(WK == 1 ? 0 : min(kg * OB, NB - OB) * 16) + 8 * i + c2]);
         }
       }
       // block by block: E = F - X beta F, U = beta E, and what U takes off F of the
@@ -477,17 +484,15 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       uint32_t au[kParts][4];
       RowScales su;
       auto add_scaled = [&](float (*to)[4], const float (&d)[2][4]) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[q][e] = fmaf(e < 2 ? su.down0 : su.down1, d[q][e], to[q][e]);
+        add_rows(to[0], d[0], su);
+        add_rows(to[1], d[1], su);
       };
       auto rest = [&](int k) {
 #pragma unroll
         for (int i = 2 * k + 4; i < NC; i += 2) {
           uint32_t r[kParts][2][2];
           float d[2][4];
-          load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
+          load_right<kParts, 2>(r, M, C * G::PB, lm, 8 * i, 16 * k);
           mma_short(d, au, r);
           add_scaled(f + i, d);
         }
@@ -503,9 +508,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
             if (i >= k && (WK == 1 || i < NB)) {
               uint32_t rp[PP][2][2];
               float d[2][4];
-              load_right<G::PB, PP, 2>(rp, P, C * G::PB, lane, 16 * i, 16 * k);
-              zero(d);
-              mma_parts<PP, PP, 2>(d, ao, rp);
+              load_right<PP, 2>(rp, P, C * G::PB, lm, 16 * i, 16 * k);
+              mma_parts0<PP, PP, 2>(d, ao, rp);
               add_scaled(o + 2 * j, d);
             }
           }
@@ -515,13 +519,13 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       for (int k = 0; k < NB; ++k) {
         uint32_t a[kParts][4], r[kParts][2][2];
         float d[2][4], y[2][4];
-        load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
+        load_right_t<kParts, 2>(r, M, C * G::PB, lm, 16 * k, 16 * k);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int at = 16 * k + 8 * q + c2;
-          const float2 be = *(const float2*)&g.beta[at], xs = *(const float2*)&g.xs[at];
+          const float2 bx = *(const float2*)&g.bx[at];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[q][e] = f[2 * k + q][e] * (e & 1 ? be.y * xs.y : be.x * xs.x);
+          for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), bx));
         }
         const RowScales sy = row_scales(row_max<2>(y));
         as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
@@ -531,12 +535,11 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
         for (int q = 0; q < 2; ++q) {
           const int at = 16 * k + 8 * q + c2;
           const float2 be = *(const float2*)&g.beta[at];
+          add_rows(f[2 * k + q], d[q], sy);
+          if (kStates)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float ev = fmaf(e < 2 ? sy.down0 : sy.down1, d[q][e], f[2 * k + q][e]);
-            if (kStates) d[q][e] = ev;
-            f[2 * k + q][e] = ev * (e & 1 ? be.y : be.x);
-          }
+            for (int e = 0; e < 4; ++e) d[q][e] = f[2 * k + q][e];
+          times(f[2 * k + q], be);
           if constexpr (kStates) {
             const float2 ku = *(const float2*)&g.kup[at];
             float* ep = err + (long long)c * C * p.dv;
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
         su = row_scales(row_max<2>(f + 2 * k));
         as_left<kParts>(au, f[2 * k], f[2 * k + 1], su.up0, su.up1);
         if (k + 1 < NB) {
-          load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k + 16, 16 * k);
+          load_right<kParts, 2>(r, M, C * G::PB, lm, 16 * k + 16, 16 * k);
           mma_short(d, au, r);
           add_scaled(f + 2 * k + 2, d);
         }
@@ -559,16 +562,12 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       rest(NB - 1);
       uint32_t y[NB][kParts][4];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const float2 t = *(const float2*)&g.tail[8 * i + c2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[i][e] *= e & 1 ? t.y : t.x;
-      }
+      for (int i = 0; i < NC; ++i) times(f[i], *(const float2*)&g.tail[8 * i + c2]);
       const RowScales sw = row_scales(row_max<NC>(f));
 #pragma unroll
       for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
       constexpr int kGroups = NK < 4 ? 1 : NK / 4;
-      most = state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, lane, [&](int i) {
+      most = state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, la, [&](int i) {
         if constexpr (!kStates) {  // o's columns, shared out over the products
           constexpr int per = (2 * OB + kGroups - 1) / kGroups;
 #pragma unroll
@@ -577,10 +576,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
             if (m < 2 * OB) {
               const int first = (WK == 1 ? 0 : kg * OB * 16) + 8 * m;  // step
               if (WK == 1 || first < C) {
-                const float2 qu = *(const float2*)&g.qup[first + c2];
-                const float s0 = p.scale * inverse_pow2(qu.x), s1 = p.scale * inverse_pow2(qu.y);
-                const float r[4] = {o[m][0] * s0, o[m][1] * s1, o[m][2] * s0, o[m][3] * s1};
-                put_steps<T>(r, out + (long long)c * C * out_step + w0, out_step, first, n, v0 + w0, p.dv,
+                times(o[m], *(const float2*)&g.qdown[first + c2]);
+                put_steps<T>(o[m], out + (long long)c * C * out_step + w0, out_step, first, n, v0 + w0, p.dv,
                              lane);
               }
             }
@@ -626,14 +623,12 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
     const T* kp = (const T*)p.k.p + b * p.k.batch + (long long)(h / p.k.share) * p.dk;
     const T* gp = (const T*)p.dout.p + b * p.dout.batch + (long long)h * p.dv + v0;
     auto load = [&](int c) {
-      if constexpr (NI == 1) {
-        const int n = len - c * C;
-        const long long t0 = (long long)c * C;
-        uint8_t* st = stage(c);
-        load_tile<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
-        load_tile<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
-        load_tile<C, kVB, kPrep>(st + 2 * G::KT, gp + t0 * p.dout.step, p.dout.step, n, width, tid);
-      }
+      const int n = len - c * C;
+      const long long t0 = (long long)c * C;
+      uint8_t* st = stage(c);
+      load_tile<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid);
+      load_tile<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid);
+      load_tile<C, kVB, kPrep>(st + 2 * G::KT, gp + t0 * p.dout.step, p.dout.step, n, width, tid);
     };
     RawGates<C> raw;
     auto load_raw = [&](int c) {  // (a chunk before the first has no steps)
@@ -648,9 +643,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         const float d = inverse_pow2(s);
         g.beta[r] *= d * d;
       };
-      auto q_done = [&](int r, float s) { g.qup[r] = s; };
-      const int n = len - c * C;
-      const long long t0 = (long long)c * C;
+      auto q_done = [&](int r, float s) { g.qdown[r] = inverse_pow2(s); };
       // dO: a thread's eights (NI == 1) or fours of elements, scaled by 2^n of all the
       // tile's rows together
       constexpr int E = NI == 1 ? 8 : 4, ND = C * kVB / E / kPrep;
@@ -660,15 +653,17 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         scale_rows<C, DK, kPrep>(st + G::KT, tid, k_done);
         scale_rows<C, DK, kPrep>(st, tid, q_done);
       } else {
+        FloatRows<C, DK, kPrep> k, q;
+        k.read(st + G::KT, tid);
+        q.read(st, tid);
 #pragma unroll
         for (int i = 0; i < ND; ++i) {
-          const int at = i * kPrep + tid, r = at / (kVB / E), x = at % (kVB / E) * E;
-          const float4 f = r < n && x < width ? *(const float4*)(gp + (t0 + r) * p.dout.step + x)
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 f = ((const float4*)(st + 2 * G::KT))[i * kPrep + tid];
           d[i][0] = f.x; d[i][1] = f.y; d[i][2] = f.z; d[i][3] = f.w;
         }
-        load_scaled_rows<C, DK, kPrep>(st + G::KT, kp + t0 * p.k.step, p.k.step, n, p.dk, tid, k_done);
-        load_scaled_rows<C, DK, kPrep>(st, qp + t0 * p.q.step, p.q.step, n, p.dk, tid, q_done);
+        bar(1, kPrep);
+        k.write(st + G::KT, tid, k_done);
+        q.write(st, tid, q_done);
       }
       bar(1, kPrep);
       float m = 0.f;
@@ -684,7 +679,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
             d[i][2 * e + 1] = f.y;
           }
         }
-        const float s = inverse_pow2(g.qup[r]);
+        const float s = g.qdown[r];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           d[i][e] *= s;
@@ -724,7 +719,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
     if (nc > 0) {
       load(nc - 1);
       copy_commit();
-      if (G::NS > 2 && nc > 1) load(nc - 2);
+      if (nc > 1) load(nc - 2);
       copy_commit();
       if (warp == 0) {
         load_raw(nc - 1);
@@ -738,9 +733,9 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
     __syncthreads();
     for (int c = nc - 1; c >= 0; --c) {
       if (c > 0) {
-        if (G::NS > 2 ? c > 1 : true) load(G::NS > 2 ? c - 2 : c - 1);
+        if (c > 1) load(c - 2);
         copy_commit();
-        copy_wait<G::NS - 2>();
+        copy_wait<1>();
         bar(1, kPrep);
         prep(c - 1);
       }
@@ -754,6 +749,9 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
     auto owns = [&](int block) { return WK == 1 || block / OB == kg; };
     float4* ex = (float4*)(sm + G::kX) + (long long)vg * WK * NC * 32;
     const bool idle = w0 >= width;
+    const Lane<G::RB> la(lane);
+    const Lane<G::PB> lm(lane);
+    const Lane<kVB * 2> lv(lane);
     float x[NK][4];  // D
     get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, k0, p.dk, lane);
     float2 most = row_max<NK>(x);
@@ -771,11 +769,9 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       float f[NC][4];  // dU^T, then dv^T
       {
         const RowScales sx = row_scales(most);
-        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, lane);
+        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, la);
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[i][e] *= e < 2 ? sx.down0 : sx.down1;
+        for (int i = 0; i < NC; ++i) scale_back(f[i], sx);
         if constexpr (WK > 1) {
           float4* mine = ex + kg * NC * 32 + lane;
 #pragma unroll
@@ -785,50 +781,45 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         }
       }
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const float2 t = *(const float2*)&g.tail[8 * i + c2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[i][e] *= e & 1 ? t.y : t.x;
-      }
+      for (int i = 0; i < NC; ++i) times(f[i], *(const float2*)&g.tail[8 * i + c2]);
       const float so = p.scale * g.dout;
       // dO's rows v, steps 16 k ... as a left operand
       auto dout_left = [&](uint32_t (&a)[NI][4], int k) {
 #pragma unroll
         for (int q = 0; q < NI; ++q)
-          ldm4t(a[q], dO + q * C * kVB * 2 + left_t<kVB * 2>(lane, w0, 16 * k));
+          ldm4t(a[q], lv.left_t(dO, w0, 16 * k) + q * C * kVB * 2);
       };
       // P^T dO for the steps of block k
       auto from_out = [&](int k) {
         float d[2][4];
-        zero(d);
 #pragma unroll
         for (int i = k; i < NB; ++i) {
           uint32_t a[NI][4], r[kParts][2][2];
           dout_left(a, i);
-          load_right_t<G::PB, kParts, 2>(r, P, C * G::PB, lane, 16 * k, 16 * i);
-          mma_parts<NI, kParts, 2>(d, a, r);
+          load_right_t<kParts, 2>(r, P, C * G::PB, lm, 16 * k, 16 * i);
+          if (i == k) mma_parts0<NI, kParts, 2>(d, a, r);
+          else mma_parts<NI, kParts, 2>(d, a, r);
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[2 * k + q][e] = fmaf(so, d[q][e], f[2 * k + q][e]);
+          for (int u = 0; u < 2; ++u)
+            set_pair(f[2 * k + q], u, fma2(both(so), pair(d[q], u), pair(f[2 * k + q], u)));
       };
       // from the last block back: y = dU - X^T beta dU, dv = beta y, and what dv takes
       // off dU of the earlier blocks (the order of issue as in the walk)
       uint32_t av[kParts][4];
       RowScales su;
       auto add_scaled = [&](float (*to)[4], const float (&d)[2][4]) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[q][e] = fmaf(e < 2 ? su.down0 : su.down1, d[q][e], to[q][e]);
+        add_rows(to[0], d[0], su);
+        add_rows(to[1], d[1], su);
       };
       auto rest = [&](int k) {
 #pragma unroll
         for (int i = 0; i < 2 * k - 2; i += 2) {
           uint32_t r[kParts][2][2];
           float d[2][4];
-          load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 8 * i, 16 * k);
+          load_right_t<kParts, 2>(r, M, C * G::PB, lm, 8 * i, 16 * k);
           mma_short(d, av, r);
           add_scaled(f + i, d);
         }
@@ -838,12 +829,12 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       for (int k = NB - 1; k >= 0; --k) {
         uint32_t a[kParts][4], r[kParts][2][2];
         float d[2][4], y[2][4];
-        load_right<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k, 16 * k);
+        load_right<kParts, 2>(r, M, C * G::PB, lm, 16 * k, 16 * k);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 be = *(const float2*)&g.beta[16 * k + 8 * q + c2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[q][e] = f[2 * k + q][e] * (e & 1 ? be.y : be.x);
+          for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), be));
         }
         const RowScales sy = row_scales(row_max<2>(y));
         as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
@@ -857,11 +848,11 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
           const float2 ku = *(const float2*)&g.kup[at];
           float* yp = ys + (long long)c * C * p.dv;
           float yv[4];
+          times(d[q], xs);
+          add_rows(f[2 * k + q], d[q], sy);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            yv[e] = fmaf((e < 2 ? sy.down0 : sy.down1) * (e & 1 ? xs.y : xs.x), d[q][e], f[2 * k + q][e]);
-            f[2 * k + q][e] = yv[e] * (e & 1 ? be.y : be.x);
-          }
+          for (int e = 0; e < 4; ++e) yv[e] = f[2 * k + q][e];
+          times(f[2 * k + q], be);
           if (owns(k)) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -877,7 +868,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         su = row_scales(row_max<2>(f + 2 * k));
         as_left<kParts>(av, f[2 * k], f[2 * k + 1], su.up0, su.up1);
         if (k > 0) {
-          load_right_t<G::PB, kParts, 2>(r, M, C * G::PB, lane, 16 * k - 16, 16 * k);
+          load_right_t<kParts, 2>(r, M, C * G::PB, lm, 16 * k - 16, 16 * k);
           mma_short(d, av, r);
           add_scaled(f + 2 * k - 2, d);
         }
@@ -886,14 +877,13 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const float2 l = *(const float2*)&g.lead[8 * i + c2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[i][e] *= -(e & 1 ? l.y : l.x);
+        times(f[i], make_float2(-l.x, -l.y));
       }
       {
         const RowScales sw = row_scales(row_max<NC>(f));
 #pragma unroll
         for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
-        state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, lane, [](int) {});
+        state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, la, [](int) {});
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
@@ -916,7 +906,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       const RowScales sw = row_scales(row_max<NC>(f));
 #pragma unroll
       for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
-      most = state_add<NI, DK, NK, NB>(x, 1.f, y, sw, Q, k0, lane, [](int) {});
+      most = state_add<NI, DK, NK, NB>(x, 1.f, y, sw, Q, k0, la, [](int) {});
       __syncthreads();
     }
     if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, k0, p.dk, lane);

@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "f32x2.cuh"
 #include "ssd_common.cuh"
 #include "ssd_layer_internal.h"
 
@@ -71,12 +72,28 @@ __device__ __forceinline__ float2 unpack_bf(uint32_t x) {
 }
 // two values as N fp16 parts each
 template <int N>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[N]) {
-  p[0] = pack_half(x, y);
+__device__ __forceinline__ void split2(float2 x, uint32_t (&p)[N]) {
+  p[0] = pack_half(x.x, x.y);
   if constexpr (N == 2) {
-    const float2 f = unpack_half(p[0]);
-    p[1] = pack_half(x - f.x, y - f.y);
+    const float2 r = fma2(unpack_half(p[0]), make_float2(-1.f, -1.f), x);
+    p[1] = pack_half(r.x, r.y);
   }
+}
+template <int N>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[N]) {
+  split2<N>(make_float2(x, y), p);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// a product's values (columns 2 t and 2 t + 1) of row g (u = 0) or g + 8
+__device__ __forceinline__ float2 pair(const float (&x)[4], int u) { return make_float2(x[2 * u], x[2 * u + 1]); }
+__device__ __forceinline__ void set_pair(float (&x)[4], int u, float2 v) {
+  x[2 * u] = v.x;
+  x[2 * u + 1] = v.y;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // The power of two that brings m > 0 into [2^T, 2^{T+1}), and its inverse; infinities
@@ -134,6 +151,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// d = a b
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 template <int N>
 __device__ __forceinline__ void zero(float (&d)[N][4]) {
 #pragma unroll
@@ -142,29 +166,34 @@ __device__ __forceinline__ void zero(float (&d)[N][4]) {
     for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
 }
 
-// Where lane `lane` points for the four 8 x 8 pieces of ldmatrix, in a tile with
-// rows of RB bytes:
-// rows m, terms along the row: a left operand of rows m ... m + 15, terms k ... k + 15
+// Where a lane points for the four 8 x 8 pieces of ldmatrix, in a tile with rows of RB
+// bytes whose address is a multiple of RB.  Both row and piece being multiples of 16
+// elements apart, an address is the tile's, whole rows, and the lane's own offset in the
+// first rows with the piece's bits exchanged: one instruction for a piece's column.
 template <int RB>
-__device__ __forceinline__ uint32_t left(int lane, int m, int k) {
-  return at16<RB>(m + (lane & 15), (k >> 3) + (lane >> 4));
-}
-// terms down the rows: the same left operand from its transpose
-template <int RB>
-__device__ __forceinline__ uint32_t left_t(int lane, int m, int k) {
-  return at16<RB>(k + (lane & 7) + (lane >> 4 << 3), (m >> 3) + (lane >> 3 & 1));
-}
-// columns n down the rows, terms along them: right operands of columns n ... n + 7
-// (r[0], r[1]) and n + 8 ... (r[2], r[3])
-template <int RB>
-__device__ __forceinline__ uint32_t right(int lane, int n, int k) {
-  return at16<RB>(n + (lane & 7) + (lane >> 4 << 3), (k >> 3) + (lane >> 3 & 1));
-}
-// terms down the rows
-template <int RB>
-__device__ __forceinline__ uint32_t right_t(int lane, int n, int k) {
-  return at16<RB>(k + (lane & 7) + ((lane >> 3 & 1) << 3), (n >> 3) + (lane >> 4));
-}
+struct Lane {
+  uint32_t a, b;
+  __device__ __forceinline__ explicit Lane(int lane)
+      : a(at16<RB>(lane & 15, lane >> 4)),
+        b(at16<RB>((lane & 7) + (lane >> 4 << 3), lane >> 3 & 1)) {}
+  // rows m, terms along the row: a left operand of rows m ... m + 15, terms k ... k + 15
+  __device__ __forceinline__ uint32_t left(uint32_t tile, int m, int k) const {
+    return tile + (a ^ (k * 2)) + m * RB;
+  }
+  // terms down the rows: the same left operand from its transpose
+  __device__ __forceinline__ uint32_t left_t(uint32_t tile, int m, int k) const {
+    return tile + (b ^ (m * 2)) + k * RB;
+  }
+  // columns n down the rows, terms along them: right operands of columns n ... n + 7
+  // (r[0], r[1]) and n + 8 ... (r[2], r[3])
+  __device__ __forceinline__ uint32_t right(uint32_t tile, int n, int k) const {
+    return tile + (b ^ (k * 2)) + n * RB;
+  }
+  // terms down the rows
+  __device__ __forceinline__ uint32_t right_t(uint32_t tile, int n, int k) const {
+    return tile + (a ^ (n * 2)) + k * RB;
+  }
+};
 
 // d[n] += a b[n] for N columns of eight, all products of parts i + j < max(PA, PB),
 // the small ones first; the columns take turns, since an instruction waits for the
@@ -183,31 +212,51 @@ __device__ __forceinline__ void mma_parts(float (*d)[4], const uint32_t (&a)[PA]
 #pragma unroll
           for (int n = 0; n < N; ++n) mma(d[n], a[i], b[j][n][0], b[j][n][1]);
 }
+// the same, the sums beginning with zero
+template <int PA, int PB, int N>
+__device__ __forceinline__ void mma_parts0(float (*d)[4], const uint32_t (&a)[PA][4],
+                                           const uint32_t (&b)[PB][N][2]) {
+  constexpr int M = PA > PB ? PA : PB;
+#pragma unroll
+  for (int s = M - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < PA; ++i)
+#pragma unroll
+      for (int j = 0; j < PB; ++j)
+        if (i + j == s) {
+          const bool first = s == M - 1 && (i == 0 || (i > 0 && s - (i - 1) >= PB));
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            if (first) mma0(d[n], a[i], b[j][n][0], b[j][n][1]);
+            else mma(d[n], a[i], b[j][n][0], b[j][n][1]);
+          }
+        }
+}
 // right operands of N (even) columns of eight, PB parts `step` bytes apart
-template <int RB, int PB, int N>
+template <int PB, int N, int RB>
 __device__ __forceinline__ void load_right(uint32_t (&b)[PB][N][2], uint32_t tile, uint32_t step,
-                                           int lane, int n, int k) {
+                                           const Lane<RB>& at, int n, int k) {
 #pragma unroll
   for (int p = 0; p < PB; ++p)
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       uint32_t r[4];
-      ldm4(r, tile + p * step + right<RB>(lane, n + 8 * i, k));
+      ldm4(r, at.right(tile, n + 8 * i, k) + p * step);
       b[p][i][0] = r[0];
       b[p][i][1] = r[1];
       b[p][i + 1][0] = r[2];
       b[p][i + 1][1] = r[3];
     }
 }
-template <int RB, int PB, int N>
+template <int PB, int N, int RB>
 __device__ __forceinline__ void load_right_t(uint32_t (&b)[PB][N][2], uint32_t tile, uint32_t step,
-                                             int lane, int n, int k) {
+                                             const Lane<RB>& at, int n, int k) {
 #pragma unroll
   for (int p = 0; p < PB; ++p)
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       uint32_t r[4];
-      ldm4t(r, tile + p * step + right_t<RB>(lane, n + 8 * i, k));
+      ldm4t(r, at.right_t(tile, n + 8 * i, k) + p * step);
       b[p][i][0] = r[0];
       b[p][i][1] = r[1];
       b[p][i + 1][0] = r[2];
@@ -222,11 +271,11 @@ __device__ __forceinline__ void as_left(uint32_t (&a)[P][4], const float (&x)[4]
   uint32_t r[P];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const float s = e ? s1 : s0;
-    split2<P>(x[2 * e] * s, x[2 * e + 1] * s, r);
+    const float2 s = both(e ? s1 : s0);
+    split2<P>(mul2(pair(x, e), s), r);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][e] = r[p];
-    split2<P>(y[2 * e] * s, y[2 * e + 1] * s, r);
+    split2<P>(mul2(pair(y, e), s), r);
 #pragma unroll
     for (int p = 0; p < P; ++p) a[p][2 + e] = r[p];
   }
@@ -282,18 +331,19 @@ __device__ __forceinline__ void load_tile(uint8_t* tile, const __nv_bfloat16* s,
     from += R * stride;
   }
 }
-// The largest magnitude of eight bf16 (one of the two halves' bits; NaN is passed over).
-__device__ __forceinline__ float max_bf(const uint4& q) {
-  const __nv_bfloat162* h = (const __nv_bfloat162*)&q;
-  const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
-  return fmaxf(__low2float(m), __high2float(m));
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *(const __nv_bfloat162*)&x; }
+// The largest magnitudes of eight bf16's even and odd elements (NaN is passed over).
+__device__ __forceinline__ __nv_bfloat162 max_bf(const uint4& q) {
+  return __hmax2(__hmax2(__habs2(as_bf2(q.x)), __habs2(as_bf2(q.y))),
+                 __hmax2(__habs2(as_bf2(q.z)), __habs2(as_bf2(q.w))));
 }
+// eight bf16 times a power of two as fp16
 __device__ __forceinline__ uint4 bf_to_half(const uint4& q, float s) {
   uint4 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_bf((&q.x)[i]);
-    (&r.x)[i] = pack_half(f.x * s, f.y * s);
+    const float2 f = mul2(unpack_bf((&q.x)[i]), both(s));
+    (&r.x)[i] = pack_half(f.x, f.y);
   }
   return r;
 }
@@ -304,7 +354,7 @@ __device__ __forceinline__ void scale_rows(uint8_t* tile, int tid, F done) {
   constexpr int RB = DK * 2, LPR = DK / 8, N = C * LPR / NT;
   static_assert(C * LPR % NT == 0, "");
   uint4 q[N];
-  float m[N];
+  __nv_bfloat162 m[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = i * NT + tid;
@@ -315,57 +365,83 @@ __device__ __forceinline__ void scale_rows(uint8_t* tile, int tid, F done) {
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+    for (int i = 0; i < N; ++i) m[i] = __hmax2(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = i * NT + tid, r = at / LPR, x = at % LPR;
-    const float s = row_exponent(m[i]);
+    const float s = row_exponent(fmaxf(__low2float(m[i]), __high2float(m[i])));
     *(uint4*)(tile + at16<RB>(r, x)) = bf_to_half(q[i], s);
     if (x == 0) done(r, s);
   }
 }
-// The same for fp32 rows in global memory: two fp16 parts, C * DK * 2 bytes apart.
-template <int C, int DK, int NT, typename F>
-__device__ __forceinline__ void load_scaled_rows(uint8_t* tile, const float* src, long long stride,
-                                                 int n, int width, int tid, F done) {
-  constexpr int RB = DK * 2, LPR = DK / 4, N = C * LPR / NT;
-  static_assert(C * LPR % NT == 0 && LPR <= 32, "");
+// fp32: C rows of D elements one behind the other, as asynchronous copies.
+template <int C, int D, int NT>
+__device__ __forceinline__ void load_tile(uint8_t* tile, const float* s, long long stride, int n,
+                                          int width, int tid) {
+  constexpr int LPR = D / 4, R = NT / LPR;
+  static_assert(C % R == 0, "");
+  const int r = tid / LPR, x = tid % LPR;
+  const uint32_t to = smem32(tile) + tid * 16;
+  const float* from = s + r * stride + x * 4;
+  const bool in = x * 4 < width;
 #pragma unroll
-  for (int b = 0; b < N; b += 8) {  // up to eight 16-byte loads on their way at a time
-    float4 f[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (b + u < N) {
-        const int at = (b + u) * NT + tid, r = at / LPR, x = at % LPR;
-        f[u] = r < n && x * 4 < width ? *(const float4*)(src + r * stride + x * 4)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (b + u < N) {
-        const int at = (b + u) * NT + tid, r = at / LPR, x = at % LPR;
-        float m = fmaxf(fmaxf(fabsf(f[u].x), fabsf(f[u].y)), fmaxf(fabsf(f[u].z), fabsf(f[u].w)));
-#pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float s = row_exponent(m);
-        uint32_t p[2], q[2];
-        split2<2>(f[u].x * s, f[u].y * s, p);
-        split2<2>(f[u].z * s, f[u].w * s, q);
-        uint8_t* to = tile + at16<RB>(r, x >> 1) + (x & 1) * 8;
-        *(uint2*)to = make_uint2(p[0], q[0]);
-        *(uint2*)(to + C * RB) = make_uint2(p[1], q[1]);
-        if (x == 0) done(r, s);
-      }
+  for (int i = 0; i < C / R; ++i) {
+    const bool here = in && r + i * R < n;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * NT * 16),
+                 "l"(here ? from : s), "r"(here ? 16 : 0)
+                 : "memory");
+    from += R * stride;
   }
 }
+// Such a tile to two fp16 parts in its place, C * DK * 2 bytes apart: a thread's
+// elements are read, and after a barrier of all threads written.
+template <int C, int DK, int NT>
+struct FloatRows {
+  static constexpr int LPR = DK / 4, N = C * LPR / NT;
+  static_assert(C * LPR % NT == 0 && LPR <= 32, "");
+  float4 f[N];
+  __device__ __forceinline__ void read(const uint8_t* tile, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = ((const float4*)tile)[i * NT + tid];
+  }
+  __device__ __forceinline__ void put(uint8_t* tile, int i, float s, int tid) const {
+    const int at = i * NT + tid, r = at / LPR, x = at % LPR;
+    uint32_t p[2], q[2];
+    split2<2>(f[i].x * s, f[i].y * s, p);
+    split2<2>(f[i].z * s, f[i].w * s, q);
+    uint8_t* to = tile + at16<DK * 2>(r, x >> 1) + (x & 1) * 8;
+    *(uint2*)to = make_uint2(p[0], q[0]);
+    *(uint2*)(to + C * DK * 2) = make_uint2(p[1], q[1]);
+  }
+  // each row scaled into [1, 2); done(row, scale) by one lane a row
+  template <typename F>
+  __device__ __forceinline__ void write(uint8_t* tile, int tid, F done) const {
+    float m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      m[i] = fmaxf(max3_abs(f[i].x, f[i].y, f[i].z), fabsf(f[i].w));
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = row_exponent(m[i]);
+      put(tile, i, s, tid);
+      const int at = i * NT + tid;
+      if (at % LPR == 0) done(at / LPR, s);
+    }
+  }
+};
 
 // Per step of a chunk: the sum g of the log decays (of base 2), as two floats, so that
 // a difference of two sums is good to its own last bit however long they have grown;
-// e^g, e^{G-g}; the write strength, of k's scale; the powers of two that k and q were
-// multiplied by; and X's columns': what its column was divided by.
+// e^g, e^{G-g}; the write strength, of k's scale; the power of two that k was multiplied
+// by; what to multiply q's results by; what X's column was divided by, and that times
+// the write strength.
 template <int C>
 struct alignas(16) Gates {
-  float hi[C], lo[C], lead[C], tail[C], beta[C], kup[C], qup[C], xs[C];
+  float hi[C], lo[C], lead[C], tail[C], beta[C], kup[C], qdown[C], xs[C], bx[C];
   float last;    // e^G
   float dout;    // the walk back: what dO's tile was divided by
 };
@@ -458,48 +534,54 @@ struct alignas(16) Scratch {
   float most[kPrep / 32];
 };
 
-// One block of 16 x 16 of A K^T, rows 16 bi ..., columns 16 bj ..., times the decays
-// and `factor`: to the tile `out` in PO parts, or to `diag`, transposed.  On the
-// diagonal what lies above it is zero (kL: and on it).
+// One block of 16 x 16 of A K^T, rows 16 bi ..., columns 16 bj ..., times the decays:
+// to the tile `out` in PO parts, their signs exchanged with `flip` (the sign bits of two
+// fp16), or to `diag`, transposed.  On the diagonal what lies above it is zero (kDiagL:
+// and on it).
 template <int NI, int DK, int PO, bool kDiagL>
 __device__ __forceinline__ void score_block(uint32_t A, uint32_t K, uint8_t* out,
                                             const Gates<kSteps<NI>>& g, float (*diag)[kDiag], int bi,
-                                            int bj, float factor, int lane) {
+                                            int bj, uint32_t flip, int lane) {
   constexpr int C = kSteps<NI>, RB = DK * 2, OB = C * 2;
+  const Lane<RB> at(lane);
   float acc[2][4];
   zero(acc);
   constexpr int U = NI == 1 ? DK / 16 : 2;  // (every operand of a bf16 block on its way at once)
+  A += bi * 16 * RB;
+  const uint32_t B = K + bj * 16 * RB;
 #pragma unroll(U)
   for (int k = 0; k < DK; k += 16) {
     uint32_t a[NI][4], b[NI][2][2];
 #pragma unroll
-    for (int p = 0; p < NI; ++p) ldm4(a[p], A + p * C * RB + left<RB>(lane, 16 * bi, k));
-    load_right<RB, NI, 2>(b, K, C * RB, lane, 16 * bj, k);
+    for (int p = 0; p < NI; ++p) ldm4(a[p], at.left(A, 0, k) + p * C * RB);
+    load_right<NI, 2>(b, B, C * RB, at, 0, k);
     mma_parts<NI, NI, 2>(acc, a, b);
   }
-  const int c0 = (lane & 3) * 2, i0 = 16 * bi + (lane >> 2);
-  const float hi0 = g.hi[i0], lo0 = g.lo[i0], hi1 = g.hi[i0 + 8], lo1 = g.lo[i0 + 8];
+  const int c0 = (lane & 3) * 2, r0 = lane >> 2, i0 = 16 * bi + r0;
+  const float* gi = &g.hi[i0];
+  const float* gj = &g.hi[16 * bj + c0];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    const int j = 16 * bj + 8 * n + c0;
-    const float2 hj = *(const float2*)&g.hi[j], lj = *(const float2*)&g.lo[j];
+    const float2 hj = *(const float2*)(gj + 8 * n), lj = *(const float2*)(gj + C + 8 * n);
+    const int j = 16 * (bj - bi) + 8 * n + c0;  // (beside the block's first row)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int i = i0 + 8 * u;
-      const float hi = u ? hi1 : hi0, lo = u ? lo1 : lo0;
-      float x = acc[n][2 * u] * factor * decay(hi, lo, hj.x, lj.x);
-      float y = acc[n][2 * u + 1] * factor * decay(hi, lo, hj.y, lj.y);
-      if (kDiagL ? j >= i : j > i) x = 0.f;
-      if (kDiagL ? j + 1 >= i : j + 1 > i) y = 0.f;
+      const int i = r0 + 8 * u;
+      // Gamma_ij = 2^((hi_i - hi_j) + (lo_i - lo_j))
+      const float2 minus = both(-1.f);
+      const float2 t = add2(fma2(hj, minus, both(gi[8 * u])), fma2(lj, minus, both(gi[C + 8 * u])));
+      float2 x = mul2(pair(acc[n], u), make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+      if (kDiagL ? j >= i : j > i) x.x = 0.f;
+      if (kDiagL ? j + 1 >= i : j + 1 > i) x.y = 0.f;
       if constexpr (kDiagL) {
-        diag[j & 15][i & 15] = x;
-        diag[(j & 15) + 1][i & 15] = y;
+        diag[8 * n + c0][i] = x.x;
+        diag[8 * n + c0 + 1][i] = x.y;
       } else {
         uint32_t p[PO];
-        split2<PO>(x, y, p);
-        uint8_t* at = out + at16<OB>(i, 2 * bj + n) + c0 * 2;
+        split2<PO>(x, p);
+        uint8_t* to = out + at16<OB>(16 * bi + i, 2 * bj + n) + c0 * 2;
 #pragma unroll
-        for (int q = 0; q < PO; ++q) *(uint32_t*)(at + q * C * OB) = p[q];
+        for (int q = 0; q < PO; ++q) *(uint32_t*)(to + q * C * OB) = p[q] ^ flip;
       }
     }
   }
@@ -532,6 +614,7 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, Gates<C>& g, const flo
   for (int i = 1; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
   const Scale sx = scale_to<8>(m);
   g.xs[16 * s + j] = sx.down;
+  g.bx[16 * s + j] = sx.down * g.beta[16 * s + j];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t p[4][kParts];
@@ -560,7 +643,7 @@ __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, ui
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t K = smem32(Kt), Q = smem32(Qt);
   if (warp < NB) {
-    score_block<NI, DK, kParts, true>(K, K, nullptr, g, sc.diag[warp], warp, warp, 1.f, lane);
+    score_block<NI, DK, kParts, true>(K, K, nullptr, g, sc.diag[warp], warp, warp, 0u, lane);
     __syncwarp();
     if (lane < 16) invert_diag<C>(M, g, sc.diag[warp], warp, lane);
     __syncwarp();
@@ -573,13 +656,13 @@ __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, ui
     const int w = warp - NB;
 #pragma unroll 1
     for (int r = w; r < nL; r += W)
-      score_block<NI, DK, kParts, false>(K, K, M, g, nullptr, kLi >> 4 * r & 15, kLj >> 4 * r & 15, -1.f,
-                                         lane);
+      score_block<NI, DK, kParts, false>(K, K, M, g, nullptr, kLi >> 4 * r & 15, kLj >> 4 * r & 15,
+                                         0x80008000u, lane);
     if constexpr (kP) {
       // (in the order that leaves every warp the same number of blocks)
 #pragma unroll 1
       for (int r = (w + W - nL % W) % W; r < nP; r += W)
-        score_block<NI, DK, PP, false>(Q, K, P, g, nullptr, kPi >> 4 * r & 15, kPj >> 4 * r & 15, 1.f,
+        score_block<NI, DK, PP, false>(Q, K, P, g, nullptr, kPi >> 4 * r & 15, kPj >> 4 * r & 15, 0u,
                                        lane);
     }
   }

@@ -323,22 +323,22 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
     auto prep = [&](int c) {
       Gates<C>& g = gates[c % 3];
       uint8_t* st = stage(c);
-      auto k_done = [&](int r, float s) {
+      auto k_done = [&](int r, float s, float) {
         g.kup[r] = s;
         const float d = inverse_pow2(s);
         g.beta[r] *= d * d;
       };
-      auto q_done = [&](int r, float s) { g.qdown[r] = p.scale * inverse_pow2(s); };
+      auto q_done = [&](int r, float s, float) { g.qdown[r] = p.scale * inverse_pow2(s); };
       if constexpr (NI == 1) {
-        scale_rows<C, DK, kPrep>(st + G::KT, tid, k_done);
-        if (!kStates) scale_rows<C, DK, kPrep>(st, tid, q_done);
+        scale_rows<C, DK, kPrep>(st + G::KT, tid, no_least, k_done);
+        if (!kStates) scale_rows<C, DK, kPrep>(st, tid, no_least, q_done);
       } else {
         FloatRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
         if (!kStates) q.read(st, tid);
         bar(1, kPrep);
-        k.write(st + G::KT, tid, k_done);
-        if (!kStates) q.write(st, tid, q_done);
+        k.write(st + G::KT, tid, no_least, k_done);
+        if (!kStates) q.write(st, tid, no_least, q_done);
       }
       bar(1, kPrep);
       prepare<NI, DK, PP, !kStates>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
@@ -638,20 +638,20 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
     auto prep = [&](int c) {
       Gates<C>& g = gates[c % 3];
       uint8_t* st = stage(c);
-      auto k_done = [&](int r, float s) {
+      auto k_done = [&](int r, float s, float) {
         g.kup[r] = s;
         const float d = inverse_pow2(s);
         g.beta[r] *= d * d;
       };
-      auto q_done = [&](int r, float s) { g.qdown[r] = inverse_pow2(s); };
+      auto q_done = [&](int r, float s, float) { g.qdown[r] = inverse_pow2(s); };
       // dO: a thread's eights (NI == 1) or fours of elements, scaled by 2^n of all the
       // tile's rows together
       constexpr int E = NI == 1 ? 8 : 4, ND = C * kVB / E / kPrep;
       static_assert(C * kVB / E % kPrep == 0, "");
       float d[ND][E];
       if constexpr (NI == 1) {
-        scale_rows<C, DK, kPrep>(st + G::KT, tid, k_done);
-        scale_rows<C, DK, kPrep>(st, tid, q_done);
+        scale_rows<C, DK, kPrep>(st + G::KT, tid, no_least, k_done);
+        scale_rows<C, DK, kPrep>(st, tid, no_least, q_done);
       } else {
         FloatRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
@@ -662,8 +662,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
           d[i][0] = f.x; d[i][1] = f.y; d[i][2] = f.z; d[i][3] = f.w;
         }
         bar(1, kPrep);
-        k.write(st + G::KT, tid, k_done);
-        q.write(st, tid, q_done);
+        k.write(st + G::KT, tid, no_least, k_done);
+        q.write(st, tid, no_least, q_done);
       }
       bar(1, kPrep);
       float m = 0.f;

@@ -347,10 +347,11 @@ __device__ __forceinline__ uint4 bf_to_half(const uint4& q, float s) {
   }
   return r;
 }
-// A bf16 tile to fp16 in place, row by row, each scaled into [1, 2); done(row, scale)
-// by one lane a row.
-template <int C, int DK, int NT, typename F>
-__device__ __forceinline__ void scale_rows(uint8_t* tile, int tid, F done) {
+__device__ __forceinline__ float no_least(int) { return 0.f; }
+// A bf16 tile to fp16 in place, row by row, each scaled into [1, 2), or by no more than
+// `least(row)` would be; done(row, scale, largest) by one lane a row.
+template <int C, int DK, int NT, typename F, typename L>
+__device__ __forceinline__ void scale_rows(uint8_t* tile, int tid, L least, F done) {
   constexpr int RB = DK * 2, LPR = DK / 8, N = C * LPR / NT;
   static_assert(C * LPR % NT == 0, "");
   uint4 q[N];
@@ -369,9 +370,10 @@ __device__ __forceinline__ void scale_rows(uint8_t* tile, int tid, F done) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = i * NT + tid, r = at / LPR, x = at % LPR;
-    const float s = row_exponent(fmaxf(__low2float(m[i]), __high2float(m[i])));
+    const float most = fmaxf(fmaxf(__low2float(m[i]), __high2float(m[i])), least(r));
+    const float s = row_exponent(most);
     *(uint4*)(tile + at16<RB>(r, x)) = bf_to_half(q[i], s);
-    if (x == 0) done(r, s);
+    if (x == 0) done(r, s, most);
   }
 }
 // fp32: C rows of D elements one behind the other, as asynchronous copies.
@@ -413,9 +415,10 @@ struct FloatRows {
     *(uint2*)to = make_uint2(p[0], q[0]);
     *(uint2*)(to + C * DK * 2) = make_uint2(p[1], q[1]);
   }
-  // each row scaled into [1, 2); done(row, scale) by one lane a row
-  template <typename F>
-  __device__ __forceinline__ void write(uint8_t* tile, int tid, F done) const {
+  // each row scaled into [1, 2), or by no more than `least(row)` would be; done(row,
+  // scale, largest) by one lane a row
+  template <typename F, typename L>
+  __device__ __forceinline__ void write(uint8_t* tile, int tid, L least, F done) const {
     float m[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -426,10 +429,11 @@ struct FloatRows {
       for (int i = 0; i < N; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      const int at = i * NT + tid;
+      m[i] = fmaxf(m[i], least(at / LPR));
       const float s = row_exponent(m[i]);
       put(tile, i, s, tid);
-      const int at = i * NT + tid;
-      if (at % LPR == 0) done(at / LPR, s);
+      if (at % LPR == 0) done(at / LPR, s, m[i]);
     }
   }
 };

@@ -1,363 +1,577 @@
 // Gated delta rule: the gradients of q, k, the decays and the write strengths of
 // every chunk, from the state H before it, the gradient D of the state after it, E
 // and y (ssd_delta.cuh, ssd_delta.cu have the formulas), no chunk waiting for
-// another.  With dv = beta y, U = beta E,
+// another.  With dv = beta y, U = beta E, (Q K^T) and (K K^T) the plain scores,
 //   MP_ij = s Gamma_ij dO_i . U_j (j <= i),  ML_ij = -Gamma_ij dv_i . U_j (j < i)
-//   dq = s e^g dO H + MP K
-//   dk = r + w,  r = ML K - e^g dv H,  w = MP^T Q + ML^T K + e^{G-g} U D
+//   dq = a + MP K,      a = s e^g dO H
+//   dk = r + w,         r = b + ML K, b = -e^g dv H,  w = MP^T Q + ML^T K + c, c = e^{G-g} U D
 //   dbeta_i = E_i . y_i
-// e^{g_i} stands with q_i and with k_i where it is read, e^{-g_i} with k_i where it
-// is written, and e^G with the state that is handed on, so
-//   dg_i = q_i . dq_i + k_i . r_i - k_i . w_i,  dG = <H', D>
-//   <H', D> = e^G <H, D> + sum_j k_j . (e^{G-g} U D)_j
-// and a step's log decay gets the sum of dg from it to the chunk's end.  These terms
-// cancel to a thirtieth of their size or less, which is why every operand here has
-// all its parts; two parts (2^-17) gave 9e-5 of dlog_decay.
+// A step's log decay acts on everything that is written before it and read from it on:
+// with m_ij = MP_ij (q_i . k_j) + ML_ij (k_i . k_j), what a pair of steps contributes,
+//   dlog_decay_t = sum_{i >= t > j} m_ij + sum_{i >= t} (q_i . a_i + k_i . b_i)
+//                + sum_{j < t} k_j . c_j + e^G <H, D>
+// found as the sums from the chunk's end of rows minus columns of m and so on, in two floats.  (Rows
+// and columns are sums of the same m_ij, whose errors then cancel like the pairs within
+// [t, C) do.  With q . dq - k . w in their place, from products of their own, what
+// should cancel was thirty times the result.)
 //
-// One CTA per (chunk, head, row), eight warps: 16 rows (steps) and a share of the
-// columns each; operands of 64 columns of v at a time.  Heads that share q and k
+// One persistent CTA an SM walks over (chunk, head, row); a warp has 16 rows (steps) and
+// a share of the columns, operands come 64 columns of v at a time and are split into
+// parts in the place where they arrive.  H and D of the next piece are on their way
+// while this one is multiplied, E, y and dO of the next chunk while MP and ML are; K and
+// Q come during the first products, which need neither.  Heads that share q and k
 // write their own gradients in fp32, summed in head order by a second kernel.
 #include <cuda_bf16.h>
 
-#include "ssd_delta3.cuh"
+#include "persistent_grid.h"
+#include "ssd_delta.cuh"
 #include "ssd_internal.h"
 
 namespace ssd {
 namespace {
 
-using namespace delta3;
+using namespace delta;
 
-constexpr int kThreads = 256;
+// bf16 results take MP and ML as one part (11 bits): they feed dq and dk alone.
+template <int NI>
+constexpr int kMaskParts = NI == 1 ? 1 : 2;
 
 template <int NI, int DK>
 struct Geom {
-  static constexpr int C = kSteps<NI>;
+  static constexpr int C = kSteps<NI>, NT = C * 8;       // threads
   static constexpr int RB = DK * 2, VR = kVB * 2, PB = C * 2;
   static constexpr int KT = NI * C * RB;                 // Q, K
   static constexpr int OT = NI * C * VR;                 // dO
   static constexpr int HT = kParts * kVB * RB;           // H, D
   static constexpr int UT = kParts * C * VR;             // U, dv
-  static constexpr int MT = kParts * C * PB;             // MP, ML: in the place of H, D
+  static constexpr int MT = kMaskParts<NI> * C * PB;     // MP, ML: in the place of H, D
   static_assert(MT <= HT, "");
-  static constexpr int kK = KT, kO = 2 * KT, kH = kO + OT, kD = kH + HT, kU = kD + HT, kV = kU + UT;
-  static constexpr size_t smem = kV + UT;
-  static constexpr int WR = C / 16, WC = 8 / WR;         // strips of rows, groups of columns
+  static constexpr int kK = KT, kO = 2 * KT, kU = kO + OT, kV = kU + UT, kH = kV + UT;
+  static constexpr size_t smem = kH + 4 * HT;            // H, D; the next ones
+  static constexpr int WR = C / 16, WC = 4;              // strips of rows, groups of columns
   static constexpr int NK = DK / 8 / WC;                 // eights of columns of dq, dk of a warp
-  static constexpr int NM = C / 8 / (WC / 2);            // of MP or ML
+  static constexpr int NM = C / 16;                      // of MP or ML
+  static_assert(WR * WC * 32 == NT && NK % 2 == 0 && NM % 2 == 0, "");
 };
 
 // a row-major tile's two elements at (row, column c, c + 1)
 template <int NI, int RB, int C>
 __device__ __forceinline__ float2 pair_at(const uint8_t* tile, int row, int c) {
   const uint8_t* at = tile + at16<RB>(row, c >> 3) + (c & 7) * 2;
-  float2 f = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int p = NI - 1; p >= 0; --p) {
-    const uint32_t x = *(const uint32_t*)(at + p * C * RB);
-    f.x += __uint_as_float(x << 16);
-    f.y += __uint_as_float(x & 0xffff0000u);
-  }
+  float2 f = unpack_half(*(const uint32_t*)at);
+  if (NI == 2) f = add2(f, unpack_half(*(const uint32_t*)(at + C * RB)));
   return f;
 }
-
-// sum over 16 lanes
-__device__ __forceinline__ float sum16(float x) {
+template <typename T>
+__device__ __forceinline__ void put_pair(T* at, float2 x) {
+  if constexpr (sizeof(T) == 2) *(uint32_t*)at = pack_bf(x.x, x.y);
+  else *(float2*)at = x;
+}
+template <int N>
+__device__ __forceinline__ float sum_lanes(float x) {
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  for (int d = N / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
   return x;
 }
-
-template <typename T>
-__device__ __forceinline__ void put_pair(T* at, float x, float y) {
-  if constexpr (sizeof(T) == 2) *(uint32_t*)at = pack2(x, y);
-  else *(float2*)at = make_float2(x, y);
+__device__ __forceinline__ float max_warp(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
 }
 
 // kShared: dq, dk of the head in fp32 to part (dq's, then dk's, [B][T][H][dk])
 template <int NI, int DK, bool kShared>
-__global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const DeltaGrads p, float* part) {
+__global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const DeltaGrads p, float* part,
+                                                                    uint32_t items) {
   using G = Geom<NI, DK>;
   using T = typename std::conditional<NI == 1, __nv_bfloat16, float>::type;
   using TO = typename std::conditional<kShared, float, T>::type;
-  constexpr int C = G::C, RB = G::RB, VR = G::VR, PB = G::PB, NK = G::NK, NM = G::NM, NB = C / 16;
+  constexpr int C = G::C, NT = G::NT, NW = NT / 32, RB = G::RB, VR = G::VR, PB = G::PB, NK = G::NK,
+                NM = G::NM, NB = C / 16, PM = kMaskParts<NI>;
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ Gates<C> g;
-  __shared__ float dbeta[C], red[G::WC][C], sums[2][8];
+  __shared__ Gates<C> gates[2];
+  // Of the steps: the largest of U, dv and dO and what they were divided by (of this
+  // piece and the one before), what q and k were; dbeta; sums over columns and rows.
+  __shared__ float most[2][3][C], down[2][3][C], qdown[C], kdown[C], dbeta[C];
+  __shared__ float rows_of[G::WC][C], cols_of[2][G::WR][C], reads[G::WC][C], writes[G::WC][C];
+  __shared__ float red[3][NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int h = blockIdx.y, b = blockIdx.z, t0 = blockIdx.x * C;
-  int len = p.T;
-  if (p.lens) len = min(max(p.lens[b], 0), p.T);
-  const int n = min(C, len - t0), rows = min(C, p.T - t0);
-  const long long token = (long long)b * p.T + t0;
-  // where dq and dk go: rows of `heads` heads
-  const int heads = kShared ? p.H : p.G;
-  TO* dq_out = (kShared ? (TO*)part : (TO*)p.dq) + (token * heads + h) * p.dk;
-  TO* dk_out = (kShared ? (TO*)(part + (long long)p.B * p.T * p.H * p.dk) : (TO*)p.dk_out) +
-               (token * heads + h) * p.dk;
-  const long long out_step = (long long)heads * p.dk;
-  // past the row's end: zeros
-  const int z0 = max(n, 0);
-  for (int i = tid; i < (rows - z0) * (p.dk / 8); i += kThreads) {
-    const int r = z0 + i / (p.dk / 8), c = i % (p.dk / 8) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; e += 16 / (int)sizeof(TO)) {
-      *(uint4*)(dq_out + r * out_step + c + e) = make_uint4(0, 0, 0, 0);
-      *(uint4*)(dk_out + r * out_step + c + e) = make_uint4(0, 0, 0, 0);
-    }
-  }
-  const long long gate0 = token * p.H + h;
-  for (int r = z0 + tid; r < rows; r += kThreads)
-    p.dlog_decay[gate0 + (long long)r * p.H] = p.dbeta[gate0 + (long long)r * p.H] = 0.f;
-  if (n <= 0) return;
-  const int chunks = (p.T + C - 1) / C;
-  const long long unit = ((long long)b * p.H + h) * chunks + blockIdx.x;
-  const float* hs = p.hist_s + unit * p.dv * p.dk;
-  const float* hd = p.hist_d + unit * p.dv * p.dk;
-  const float* ep = p.err + unit * C * p.dv;
-  const float* yp = p.y + unit * C * p.dv;
-  const T* qp = (const T*)p.q.p + b * p.q.batch + t0 * p.q.step + (long long)(h / p.q.share) * p.dk;
-  const T* kp = (const T*)p.k.p + b * p.k.batch + t0 * p.k.step + (long long)(h / p.k.share) * p.dk;
-  const T* gp = (const T*)p.dout.p + b * p.dout.batch + t0 * p.dout.step + (long long)h * p.dv;
-  load_tile<NI, C, DK, kThreads>(sm, qp, p.q.step, n, p.dk, tid);
-  load_tile<NI, C, DK, kThreads>(sm + G::kK, kp, p.k.step, n, p.dk, tid);
-  if (tid < C) dbeta[tid] = 0.f;
-  if (warp == 0) {
-    RawGates<C> raw;
-    load_gates<C>(raw, p.log_decay, p.beta, gate0, p.H, n, lane);
-    scan_gates<C>(g, raw, lane);
-  }
-  __syncthreads();
   const int strip = warp % G::WR, group = warp / G::WR;
-  const bool is_l = group >= G::WC / 2;        // this warp's scores: ML's, else MP's
-  const int mg = group % (G::WC / 2);
-  const int m0 = mg * NM;                      // their first eight of columns
-  const uint32_t sQ = smem32(sm), sK = sQ + G::kK, sO = sQ + G::kO, sH = sQ + G::kH,
-                 sD = sQ + G::kD, sU = sQ + G::kU, sV = sQ + G::kV;
-  float dq[NK][4], rd[NK][4], wr[NK][4], mm[NM][4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-#pragma unroll
-    for (int i = 0; i < NK; ++i) dq[i][e] = rd[i][e] = wr[i][e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NM; ++i) mm[i][e] = 0.f;
-  }
-  float hdot = 0.f;  // <H, D>
-  for (int v0 = 0; v0 < p.dv; v0 += kVB) {
-    const int width = min(kVB, p.dv - v0);
-    if (v0) __syncthreads();
-    load_tile<NI, C, kVB, kThreads>(sm + G::kO, gp + v0, p.dout.step, n, width, tid);
-    if (NI == 1) copy_commit();
-#pragma unroll 2
-    for (int i = tid; i < kVB * (DK / 4); i += kThreads) {
-      const int r = i / (DK / 4), x = i % (DK / 4);
-      const bool in = r < width && x * 4 < p.dk;
-      const long long at = (long long)(v0 + r) * p.dk + x * 4;
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 s = in ? *(const float4*)(hs + at) : z, d = in ? *(const float4*)(hd + at) : z;
-      hdot = fmaf(s.x, d.x, fmaf(s.y, d.y, fmaf(s.z, d.z, fmaf(s.w, d.w, hdot))));
-      uint8_t* to = sm + G::kH + at16<RB>(r, x >> 1) + (x & 1) * 8;
-      uint32_t a[kParts], c[kParts];
-      split2<kParts>(s.x, s.y, a);
-      split2<kParts>(s.z, s.w, c);
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) *(uint2*)(to + q * kVB * RB) = make_uint2(a[q], c[q]);
-      split2<kParts>(d.x, d.y, a);
-      split2<kParts>(d.z, d.w, c);
-      to += G::HT;
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) *(uint2*)(to + q * kVB * RB) = make_uint2(a[q], c[q]);
+  const bool is_l = group >= 2;   // this warp's scores: ML's, else MP's
+  const int m0 = (group & 1) * NM;  // their first eight of columns
+  const uint32_t sQ = smem32(sm), sK = sQ + G::kK, sO = sQ + G::kO, sU = sQ + G::kU, sV = sQ + G::kV;
+  const Lane<RB> lk(lane);
+  const Lane<VR> lv(lane);
+  const Lane<PB> lm(lane);
+  const int chunks = (p.T + C - 1) / C, vblocks = (p.dv + kVB - 1) / kVB;
+  const long long out_step = (long long)(kShared ? p.H : p.G) * p.dk;
+
+  struct Item {
+    int b, h, t0, n, rows;  // n: steps, `rows` up to T
+    long long unit;
+  };
+  auto item_of = [&](uint32_t i) {
+    Item x;
+    const uint32_t bh = i / (uint32_t)chunks, c = i - bh * chunks;
+    x.b = (int)(bh / (uint32_t)p.H);
+    x.h = (int)(bh - x.b * p.H);
+    x.t0 = (int)c * C;
+    int len = p.T;
+    if (p.lens) len = min(max(p.lens[x.b], 0), p.T);
+    x.n = min(C, len - x.t0);
+    x.rows = min(C, p.T - x.t0);
+    x.unit = i;
+    return x;
+  };
+  auto load_state = [&](const Item& x, int vb, int buf) {
+    const int v0 = vb * kVB, width = p.dv - v0;
+    const long long at = (x.unit * p.dv + v0) * p.dk;
+    uint8_t* to = sm + G::kH + buf * 2 * G::HT;
+    load_tile<kVB, DK, NT>(to, p.hist_s + at, p.dk, width, p.dk, tid);
+    load_tile<kVB, DK, NT>(to + G::HT, p.hist_d + at, p.dk, width, p.dk, tid);
+  };
+  auto load_steps = [&](const Item& x, int vb) {
+    const int v0 = vb * kVB, width = p.dv - v0;
+    const long long at = x.unit * C * p.dv + v0;
+    load_tile<C, kVB, NT>(sm + G::kU, p.err + at, p.dv, C, width, tid);
+    load_tile<C, kVB, NT>(sm + G::kV, p.y + at, p.dv, C, width, tid);
+    load_tile<C, kVB, NT>(sm + G::kO,
+                          (const T*)p.dout.p + x.b * p.dout.batch + x.t0 * p.dout.step + (long long)x.h * p.dv + v0,
+                          p.dout.step, x.n, width, tid);
+  };
+  auto next_of = [&](uint32_t i, Item& x) {  // the first item with steps from i on
+    for (; i < items; i += gridDim.x) {
+      x = item_of(i);
+      if (x.n > 0) break;
     }
+    return i;
+  };
+
+  // past the rows' ends: zeros, and nothing else to do
+  for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const Item x = item_of(i);
+    const int z0 = max(x.n, 0);
+    if (z0 >= x.rows) continue;
+    const long long token = (long long)x.b * p.T + x.t0;
+    TO* dq_out = (kShared ? (TO*)part : (TO*)p.dq) + token * out_step + (long long)x.h * p.dk;
+    TO* dk_out = (kShared ? (TO*)(part + (long long)p.B * p.T * p.H * p.dk) : (TO*)p.dk_out) +
+                 token * out_step + (long long)x.h * p.dk;
+    for (int e = tid; e < (x.rows - z0) * (p.dk / 8); e += NT) {
+      const int r = z0 + e / (p.dk / 8), c = e % (p.dk / 8) * 8;
 #pragma unroll
-    for (int i0 = 0; i0 < C * (kVB / 4); i0 += kThreads) {
-      const int i = i0 + tid, r = i / (kVB / 4), x = i % (kVB / 4);
-      float4 e = make_float4(0.f, 0.f, 0.f, 0.f), y = e;
-      if (x * 4 < width) {
-        e = *(const float4*)(ep + (long long)r * p.dv + v0 + x * 4);
-        y = *(const float4*)(yp + (long long)r * p.dv + v0 + x * 4);
+      for (int k = 0; k < 8; k += 16 / (int)sizeof(TO)) {
+        *(uint4*)(dq_out + r * out_step + c + k) = make_uint4(0, 0, 0, 0);
+        *(uint4*)(dk_out + r * out_step + c + k) = make_uint4(0, 0, 0, 0);
       }
-      const float d = sum16(fmaf(e.x, y.x, fmaf(e.y, y.y, fmaf(e.z, y.z, e.w * y.w))));
-      if (x == 0) dbeta[r] += d;
-      const float be = g.beta[r];
-      uint8_t* to = sm + G::kU + at16<VR>(r, x >> 1) + (x & 1) * 8;
-      uint32_t a[kParts], c[kParts];
-      split2<kParts>(be * e.x, be * e.y, a);
-      split2<kParts>(be * e.z, be * e.w, c);
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) *(uint2*)(to + q * C * VR) = make_uint2(a[q], c[q]);
-      split2<kParts>(be * y.x, be * y.y, a);
-      split2<kParts>(be * y.z, be * y.w, c);
-      to += G::UT;
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) *(uint2*)(to + q * C * VR) = make_uint2(a[q], c[q]);
     }
-    copy_wait<0>();
-    __syncthreads();
+    for (int r = z0 + tid; r < x.rows; r += NT)
+      p.dlog_decay[(token + r) * p.H + x.h] = p.dbeta[(token + r) * p.H + x.h] = 0.f;
+  }
+
+  Item x, nx;
+  nx.n = 0;
+  uint32_t i = next_of(blockIdx.x, x);
+  int buf = 0, turn = 0;
+  RawGates<C> raw;  // warp 1: the next item's gates
+  auto load_raw = [&](const Item& x) {
+    load_gates<C>(raw, p.log_decay, p.beta, ((long long)x.b * p.T + x.t0) * p.H + x.h, p.H, x.n, lane);
+  };
+  if (i < items) {
+    load_state(x, 0, 0);
+    load_steps(x, 0);
+    copy_commit();
+    if (warp == 1) {
+      load_raw(x);
+      scan_gates<C>(gates[0], raw, lane);
+    }
+  }
+  while (i < items) {
+    const uint32_t in = next_of(i + gridDim.x, nx);
+    const long long token = (long long)x.b * p.T + x.t0;
+    const T* qp = (const T*)p.q.p + x.b * p.q.batch + x.t0 * p.q.step + (long long)(x.h / p.q.share) * p.dk;
+    const T* kp = (const T*)p.k.p + x.b * p.k.batch + x.t0 * p.k.step + (long long)(x.h / p.k.share) * p.dk;
+    load_tile<C, DK, NT>(sm, qp, p.q.step, x.n, p.dk, tid);
+    load_tile<C, DK, NT>(sm + G::kK, kp, p.k.step, x.n, p.dk, tid);
+    copy_commit();
+    const Gates<C>& g = gates[turn];
+    if (tid < C) dbeta[tid] = 0.f;
+    float dq[NK][4], rd[NK][4], wr[NK][4], mm[NM][4];
+    zero(dq);
+    zero(rd);
+    zero(wr);
+    zero(mm);
+    float hdot = 0.f;  // <H, D>
+    float hs = 0.f, ds = 0.f, mh = 0.f, md = 0.f;  // H's, D's divisors, largest elements
+    const int i0 = 16 * strip + (lane >> 2), c2 = (lane & 3) * 2;
 #pragma unroll 1
-    for (int k = 0; k < width; k += 16) {
-      uint32_t ao[NI][4], au[kParts][4], av[kParts][4];
-#pragma unroll
-      for (int q = 0; q < NI; ++q) ldm4(ao[q], sO + q * C * VR + left<VR>(lane, 16 * strip, k));
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        ldm4(au[q], sU + q * C * VR + left<VR>(lane, 16 * strip, k));
-        ldm4(av[q], sV + q * C * VR + left<VR>(lane, 16 * strip, k));
+    for (int vb = 0; vb < vblocks; ++vb) {
+      const int width = min(kVB, p.dv - vb * kVB), now = vb & 1;
+      uint8_t* Ht = sm + G::kH + buf * 2 * G::HT;
+      if (vb == 0) {
+        copy_wait<1>();  // (all but K and Q)
+      } else {
+        __syncthreads();
+        load_steps(x, vb);
+        copy_commit();
+        copy_wait<0>();
       }
+      __syncthreads();
+      // the pieces into parts, in their place
+      const float hs0 = hs, ds0 = ds;
+      {
+        FloatRows<kVB, DK, NT> fh, fd;
+        FloatRows<C, kVB, NT> fe, fy, fo;
+        fh.read(Ht, tid);
+        fd.read(Ht + G::HT, tid);
+        fe.read(sm + G::kU, tid);
+        fy.read(sm + G::kV, tid);
+        if constexpr (NI == 2) fo.read(sm + G::kO, tid);
+        // (later pieces are not scaled up by more than the earlier ones, so that sums of
+        // these may be scaled to them)
 #pragma unroll
-      for (int i = 0; i < NK; i += 2) {
-        const int c = (group * NK + i) * 8;
-        uint32_t r[kParts][2][2];
-        load_right_t<RB, kParts, 2>(r, sH, kVB * RB, lane, c, k);
-        mma_parts<NI, kParts, 2>(dq + i, ao, r);
-        mma_parts<kParts, kParts, 2>(rd + i, av, r);
-        load_right_t<RB, kParts, 2>(r, sD, kVB * RB, lane, c, k);
-        mma_parts<kParts, kParts, 2>(wr + i, au, r);
-      }
-#pragma unroll
-      for (int i = 0; i < NM; i += 2)
-        if (m0 + i <= 2 * strip) {
-          uint32_t r[kParts][2][2];
-          load_right<VR, kParts, 2>(r, sU, C * VR, lane, 8 * (m0 + i), k);
-          if (is_l) mma_parts<kParts, kParts, 2>(mm + i, av, r);
-          else mma_parts<NI, kParts, 2>(mm + i, ao, r);
+        for (int k = 0; k < fh.N; ++k) {
+          const float4 s = fh.f[k], d = fd.f[k];
+          mh = max3_abs(max3_abs(mh, s.x, s.y), s.z, s.w);
+          md = max3_abs(max3_abs(md, d.x, d.y), d.z, d.w);
+          hdot = fmaf(s.x, d.x, fmaf(s.y, d.y, fmaf(s.z, d.z, fmaf(s.w, d.w, hdot))));
         }
-    }
-  }
-  __syncthreads();  // H and D have been read
-  const int i0 = 16 * strip + (lane >> 2), c2 = (lane & 3) * 2;
+        mh = max_warp(mh);
+        md = max_warp(md);
+        if (lane == 0) {
+          red[0][warp] = mh;
+          red[1][warp] = md;
+        }
 #pragma unroll
-  for (int i = 0; i < NM; ++i)
-    if (m0 + i <= 2 * strip + 1) {
-      const int col = 8 * (m0 + i) + c2;
-      const float2 hj = *(const float2*)&g.hi[col], lj = *(const float2*)&g.lo[col];
+        for (int k = 0; k < fe.N; ++k) {
+          const int at = k * NT + tid, r = at / fe.LPR;
+          float4 &e = fe.f[k], &y = fy.f[k];
+          const float d = sum_lanes<fe.LPR>(fmaf(e.x, y.x, fmaf(e.y, y.y, fmaf(e.z, y.z, e.w * y.w))));
+          if (at % fe.LPR == 0) dbeta[r] += d;
+          const float be = g.beta[r];
+          e.x *= be; e.y *= be; e.z *= be; e.w *= be;
+          y.x *= be; y.y *= be; y.z *= be; y.w *= be;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+          mh = fmaxf(mh, red[0][k]);
+          md = fmaxf(md, red[1][k]);
+        }
+        const Scale sh = scale_to<10>(mh), sd = scale_to<10>(md);
+        hs = sh.down;
+        ds = sd.down;
+#pragma unroll
+        for (int k = 0; k < fh.N; ++k) {
+          fh.put(Ht, k, sh.up, tid);
+          fd.put(Ht + G::HT, k, sd.up, tid);
+        }
+        auto least = [&](int which) {
+          return [=](int r) { return vb ? most[now ^ 1][which][r] : 0.f; };
+        };
+        auto done = [&](int which) {
+          return [=](int r, float s, float m) {
+            most[now][which][r] = m;
+            down[now][which][r] = inverse_pow2(s);
+          };
+        };
+        fe.write(sm + G::kU, tid, least(0), done(0));
+        fy.write(sm + G::kV, tid, least(1), done(1));
+        if constexpr (NI == 2) fo.write(sm + G::kO, tid, least(2), done(2));
+        else scale_rows<C, kVB, NT>(sm + G::kO, tid, least(2), done(2));
+      }
+      __syncthreads();
+      if (vb + 1 < vblocks) load_state(x, vb + 1, buf ^ 1);
+      else if (in < items) load_state(nx, 0, buf ^ 1);
+      copy_commit();
+      if (vb > 0) {
+        const float fh = hs0 / hs, fd = ds0 / ds;
+        const auto ratio = [&](int which, int r) { return down[now ^ 1][which][r] / down[now][which][r]; };
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = i0 + 8 * u;
+          const float fu = ratio(0, r), fv = ratio(1, r), fo = ratio(2, r);
+#pragma unroll
+          for (int e = 0; e < NK; ++e) {
+            set_pair(dq[e], u, mul2(pair(dq[e], u), both(fo * fh)));
+            set_pair(rd[e], u, mul2(pair(rd[e], u), both(fv * fh)));
+            set_pair(wr[e], u, mul2(pair(wr[e], u), both(fu * fd)));
+          }
+#pragma unroll
+          for (int e = 0; e < NM; ++e) {
+            const int c = 8 * (m0 + e) + c2;
+            const float f = is_l ? fv : fo;
+            set_pair(mm[e], u, mul2(pair(mm[e], u), make_float2(f * ratio(0, c), f * ratio(0, c + 1))));
+          }
+        }
+      }
+      const uint32_t sH = smem32(Ht), sD = sH + G::HT;
+#pragma unroll 1
+      for (int k = 0; k < width; k += 16) {
+        uint32_t ao[NI][4], au[kParts][4], av[kParts][4];
+#pragma unroll
+        for (int q = 0; q < NI; ++q) ldm4(ao[q], lv.left(sO, 16 * strip, k) + q * C * VR);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          ldm4(au[q], lv.left(sU, 16 * strip, k) + q * C * VR);
+          ldm4(av[q], lv.left(sV, 16 * strip, k) + q * C * VR);
+        }
+#pragma unroll
+        for (int e = 0; e < NK; e += 2) {
+          const int c = (group * NK + e) * 8;
+          uint32_t r[kParts][2][2];
+          load_right_t<kParts, 2>(r, sH, kVB * RB, lk, c, k);
+          mma_parts<NI, kParts, 2>(dq + e, ao, r);
+          mma_parts<kParts, kParts, 2>(rd + e, av, r);
+          load_right_t<kParts, 2>(r, sD, kVB * RB, lk, c, k);
+          mma_parts<kParts, kParts, 2>(wr + e, au, r);
+        }
+#pragma unroll
+        for (int e = 0; e < NM; e += 2)
+          if (m0 + e <= 2 * strip) {
+            uint32_t r[kParts][2][2];
+            load_right<kParts, 2>(r, sU, C * VR, lv, 8 * (m0 + e), k);
+            if (is_l) mma_parts<kParts, kParts, 2>(mm + e, av, r);
+            else mma_parts<NI, kParts, 2>(mm + e, ao, r);
+          }
+      }
+      buf ^= 1;
+    }
+    copy_wait<1>();  // K and Q (not the next H and D)
+    __syncthreads();
+    if (in < items) {
+      load_steps(nx, 0);
+      if (warp == 1) load_raw(nx);
+    }
+    copy_commit();
+    {
+      auto q_done = [&](int r, float s, float) { qdown[r] = inverse_pow2(s); };
+      auto k_done = [&](int r, float s, float) { kdown[r] = inverse_pow2(s); };
+      if constexpr (NI == 2) {
+        FloatRows<C, DK, NT> q, k;
+        q.read(sm, tid);
+        k.read(sm + G::kK, tid);
+        __syncthreads();
+        q.write(sm, tid, no_least, q_done);
+        k.write(sm + G::kK, tid, no_least, k_done);
+      } else {
+        scale_rows<C, DK, NT>(sm, tid, no_least, q_done);
+        scale_rows<C, DK, NT>(sm + G::kK, tid, no_least, k_done);
+      }
+    }
+    __syncthreads();
+    const int last = (vblocks - 1) & 1;
+    const float *udown = down[last][0], *vdown = down[last][1], *odown = down[last][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = i0 + 8 * u;
+      const float fq = p.scale * g.lead[r] * odown[r] * hs, fr = -g.lead[r] * vdown[r] * hs,
+                  fw = g.tail[r] * udown[r] * ds;
+      float read_q = 0.f, read_k = 0.f, write = 0.f;
+#pragma unroll
+      for (int e = 0; e < NK; ++e) {
+        const int c = (group * NK + e) * 8 + c2;
+        const float2 q = pair_at<NI, RB, C>(sm, r, c), k = pair_at<NI, RB, C>(sm + G::kK, r, c);
+        const float2 a = mul2(pair(dq[e], u), both(fq)), b = mul2(pair(rd[e], u), both(fr)),
+                     w = mul2(pair(wr[e], u), both(fw));
+        set_pair(dq[e], u, a);
+        set_pair(rd[e], u, b);
+        set_pair(wr[e], u, w);
+        read_q = fmaf(q.x, a.x, fmaf(q.y, a.y, read_q));
+        read_k = fmaf(k.x, b.x, fmaf(k.y, b.y, read_k));
+        write = fmaf(k.x, w.x, fmaf(k.y, w.y, write));
+      }
+      const float s = sum_lanes<4>(read_q * qdown[r] + read_k * kdown[r]);
+      write = sum_lanes<4>(write * kdown[r]);
+      if ((lane & 3) == 0) {
+        reads[group][r] = s;
+        writes[group][r] = write;
+      }
+    }
+    // MP or ML, of q's and k's scales, and their products with the scores
+    float largest = 0.f;
+    {
+      const uint32_t A = is_l ? sK : sQ;
+      float row[2] = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < NM; e += 2) {
+        float s[2][4];
+        zero(s);
+        if (m0 + e <= 2 * strip) {
+#pragma unroll 2
+          for (int k = 0; k < DK; k += 16) {
+            uint32_t a[NI][4], r[NI][2][2];
+#pragma unroll
+            for (int q = 0; q < NI; ++q) ldm4(a[q], lk.left(A, 16 * strip, k) + q * C * RB);
+            load_right<NI, 2>(r, sK, C * RB, lk, 8 * (m0 + e), k);
+            mma_parts<NI, NI, 2>(s, a, r);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int j = 8 * (m0 + e + q) + c2;
+          float (&m)[4] = mm[e + q];
+          float2 col = make_float2(0.f, 0.f);
+          if (m0 + e <= 2 * strip) {
+            const float2 hj = *(const float2*)&g.hi[j], lj = *(const float2*)&g.lo[j];
+            const float2 fj = mul2(*(const float2*)&udown[j], *(const float2*)&kdown[j]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int i = i0 + 8 * u;
+              const float f = is_l ? -vdown[i] * kdown[i] : p.scale * odown[i] * qdown[i];
+              float2 v = mul2(mul2(pair(m, u), both(f)), fj);
+              v.x *= decay(g.hi[i], g.lo[i], hj.x, lj.x);
+              v.y *= decay(g.hi[i], g.lo[i], hj.y, lj.y);
+              if (is_l ? j >= i : j > i) v.x = 0.f;
+              if (is_l ? j + 1 >= i : j + 1 > i) v.y = 0.f;
+              set_pair(m, u, v);
+              largest = max3_abs(largest, v.x, v.y);
+              const float2 c = mul2(v, pair(s[q], u));
+              row[u] += c.x + c.y;
+              col = add2(col, c);
+            }
+          }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            col.x += __shfl_xor_sync(0xffffffffu, col.x, d);
+            col.y += __shfl_xor_sync(0xffffffffu, col.y, d);
+          }
+          if (lane < 4) *(float2*)&cols_of[is_l][strip][j] = col;
+        }
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int row = i0 + 8 * u;
-        float x[2];
+        row[u] = sum_lanes<4>(row[u]);
+        if ((lane & 3) == 0) rows_of[group][i0 + 8 * u] = row[u];
+      }
+    }
+    largest = max_warp(largest);
+    hdot = sum_lanes<32>(hdot);
+    if (lane == 0) {
+      red[0][warp] = largest;
+      red[2][warp] = hdot;
+    }
+    __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool in = is_l ? col + e < row : col + e <= row;
-          x[e] = in ? mm[i][2 * u + e] * (is_l ? -1.f : p.scale) *
-                          decay(g.hi[row], g.lo[row], e ? hj.y : hj.x, e ? lj.y : lj.x)
-                    : 0.f;
+    for (int k = 0; k < NW; ++k) largest = fmaxf(largest, red[0][k]);
+    const Scale smask = scale_to<10>(largest);
+    uint8_t* Mt = sm + G::kH + (buf ^ 1) * 2 * G::HT;  // the last piece's H and D
+    {
+      uint8_t* out = Mt + (is_l ? G::HT : 0);
+#pragma unroll
+      for (int e = 0; e < NM; ++e)
+        if (m0 + e <= 2 * strip + 1) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t a[PM];
+            split2<PM>(mul2(pair(mm[e], u), both(smask.up)), a);
+            uint8_t* at = out + at16<PB>(i0 + 8 * u, m0 + e) + c2 * 2;
+#pragma unroll
+            for (int q = 0; q < PM; ++q) *(uint32_t*)(at + q * C * PB) = a[q];
+          }
         }
-        uint32_t a[kParts];
-        split2<kParts>(x[0], x[1], a);
-        uint8_t* at = sm + (is_l ? G::kD : G::kH) + at16<PB>(row, m0 + i) + c2 * 2;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // dg, and its sums from each step to the end, in two floats
+      constexpr int N = C / 32;
+      Two d[N], total = {0.f, 0.f};
+      float tails = 0.f, hd = 0.f;
+      for (int k = lane; k < NW; k += 32) hd += red[2][k];
+      hd = sum_lanes<32>(hd);
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) *(uint32_t*)(at + q * C * PB) = a[q];
+      for (int k = N - 1; k >= 0; --k) {
+        const int r = lane * N + k;
+        float w = 0.f;
+#pragma unroll
+        for (int c = 0; c < G::WC; ++c) {
+          total = add(add(total, {rows_of[c][r], 0.f}), {reads[c][r], 0.f});
+          w += writes[c][r];
+        }
+#pragma unroll
+        for (int c = 0; c < G::WR; ++c) {
+          total = add(total, {-cols_of[0][c][r], 0.f});
+          total = add(total, {-cols_of[1][c][r], 0.f});
+        }
+        tails += w;
+        total = add(total, {-w, 0.f});
+        d[k] = total;
+      }
+      tails = sum_lanes<32>(tails);
+      Two after = total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const Two y = {__shfl_down_sync(0xffffffffu, after.hi, o), __shfl_down_sync(0xffffffffu, after.lo, o)};
+        if (lane + o < 32) after = add(after, y);
+      }
+      after = {__shfl_down_sync(0xffffffffu, after.hi, 1), __shfl_down_sync(0xffffffffu, after.lo, 1)};
+      if (lane == 31) after = {0.f, 0.f};
+      after = add(after, {fmaf(g.last, hd, tails), 0.f});
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int r = lane * N + k;
+        const Two t = add(d[k], after);
+        if (r < x.n) p.dlog_decay[(token + r) * p.H + x.h] = t.hi + t.lo;
       }
     }
-  float state_dot = 0.f;  // sum over this warp's rows and columns of k . (e^{G-g} U D)
+    if (warp == 1 && in < items) scan_gates<C>(gates[turn ^ 1], raw, lane);
+    if (tid < x.n) p.dbeta[(token + tid) * p.H + x.h] = dbeta[tid];
+    // the products with MP and ML, and the results
+    TO* dq_out = (kShared ? (TO*)part : (TO*)p.dq) + token * out_step + (long long)x.h * p.dk;
+    TO* dk_out = (kShared ? (TO*)(part + (long long)p.B * p.T * p.H * p.dk) : (TO*)p.dk_out) +
+                 token * out_step + (long long)x.h * p.dk;
+    const uint32_t sP = smem32(Mt), sL = sP + G::HT;
+    const float up_q[2] = {smask.down * inverse_pow2(qdown[i0]), smask.down * inverse_pow2(qdown[i0 + 8])};
+    const float up_k[2] = {smask.down * inverse_pow2(kdown[i0]), smask.down * inverse_pow2(kdown[i0 + 8])};
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const float l = g.lead[i0 + 8 * u], t = g.tail[i0 + 8 * u];
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const float2 kk = pair_at<NI, RB, C>(sm + G::kK, i0 + 8 * u, (group * NK + i) * 8 + c2);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        dq[i][2 * u + e] *= p.scale * l;
-        rd[i][2 * u + e] *= -l;
-        wr[i][2 * u + e] *= t;
-        state_dot = fmaf(e ? kk.y : kk.x, wr[i][2 * u + e], state_dot);
-      }
-    }
-  }
-  __syncthreads();
+    for (int e = 0; e < NK; e += 2) {
+      const int c = (group * NK + e) * 8;
+      float d[3][2][4];
+      zero(d[0]);
+      zero(d[1]);
+      zero(d[2]);
 #pragma unroll 1
-  for (int k = 0; k < NB; ++k) {
-    if (k <= strip) {  // columns 16 k ... of MP, ML
-      uint32_t ap[kParts][4], al[kParts][4];
+      for (int k = 0; k < NB; ++k) {
+        uint32_t a[PM][4], rk[NI][2][2];
+        load_right_t<NI, 2>(rk, sK, C * RB, lk, c, 16 * k);
+        if (k <= strip) {  // columns 16 k ... of MP, ML
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        ldm4(ap[q], sH + q * C * PB + left<PB>(lane, 16 * strip, 16 * k));
-        ldm4(al[q], sD + q * C * PB + left<PB>(lane, 16 * strip, 16 * k));
+          for (int q = 0; q < PM; ++q) ldm4(a[q], lm.left(sP, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<PM, NI, 2>(d[0], a, rk);
+#pragma unroll
+          for (int q = 0; q < PM; ++q) ldm4(a[q], lm.left(sL, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<PM, NI, 2>(d[1], a, rk);
+        }
+        if (k >= strip) {  // rows 16 k ...
+          uint32_t rq[NI][2][2];
+          load_right_t<NI, 2>(rq, sQ, C * RB, lk, c, 16 * k);
+#pragma unroll
+          for (int q = 0; q < PM; ++q) ldm4t(a[q], lm.left_t(sP, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<PM, NI, 2>(d[2], a, rq);
+#pragma unroll
+          for (int q = 0; q < PM; ++q) ldm4t(a[q], lm.left_t(sL, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<PM, NI, 2>(d[2], a, rk);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < NK; i += 2) {
-        uint32_t r[NI][2][2];
-        load_right_t<RB, NI, 2>(r, sK, C * RB, lane, (group * NK + i) * 8, 16 * k);
-        mma_parts<kParts, NI, 2>(dq + i, ap, r);
-        mma_parts<kParts, NI, 2>(rd + i, al, r);
-      }
-    }
-    if (k >= strip) {  // rows 16 k ...
-      uint32_t ap[kParts][4], al[kParts][4];
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        ldm4t(ap[q], sH + q * C * PB + left_t<PB>(lane, 16 * strip, 16 * k));
-        ldm4t(al[q], sD + q * C * PB + left_t<PB>(lane, 16 * strip, 16 * k));
-      }
-#pragma unroll
-      for (int i = 0; i < NK; i += 2) {
-        uint32_t r[NI][2][2];
-        load_right_t<RB, NI, 2>(r, sQ, C * RB, lane, (group * NK + i) * 8, 16 * k);
-        mma_parts<kParts, NI, 2>(wr + i, ap, r);
-        load_right_t<RB, NI, 2>(r, sK, C * RB, lane, (group * NK + i) * 8, 16 * k);
-        mma_parts<kParts, NI, 2>(wr + i, al, r);
-      }
+        for (int u = 0; u < 2; ++u) {
+          const int r = i0 + 8 * u, cc = c + 8 * q + c2;
+          if (r < x.n && cc < p.dk) {
+            put_pair(dq_out + r * out_step + cc,
+                     fma2(pair(d[0][q], u), both(up_q[u]), pair(dq[e + q], u)));
+            const float2 dk = fma2(add2(pair(d[1][q], u), pair(d[2][q], u)), both(up_k[u]),
+                                   add2(pair(rd[e + q], u), pair(wr[e + q], u)));
+            put_pair(dk_out + r * out_step + cc, dk);
+          }
+        }
     }
+    __syncthreads();
+    x = nx;
+    i = in;
+    turn ^= 1;
   }
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int row = i0 + 8 * u;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int c = (group * NK + i) * 8 + c2;
-      const float2 q = pair_at<NI, RB, C>(sm, row, c), k = pair_at<NI, RB, C>(sm + G::kK, row, c);
-      const float *x = &dq[i][2 * u], *r = &rd[i][2 * u], *w = &wr[i][2 * u];
-      s += fmaf(q.x, x[0], k.x * (r[0] - w[0])) + fmaf(q.y, x[1], k.y * (r[1] - w[1]));
-      if (row < n && c < p.dk) {
-        put_pair(dq_out + row * out_step + c, x[0], x[1]);
-        put_pair(dk_out + row * out_step + c, r[0] + w[0], r[1] + w[1]);
-      }
-    }
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    if ((lane & 3) == 0) red[group][row] = s;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    hdot += __shfl_xor_sync(0xffffffffu, hdot, d);
-    state_dot += __shfl_xor_sync(0xffffffffu, state_dot, d);
-  }
-  if (lane == 0) {
-    sums[0][warp] = hdot;
-    sums[1][warp] = state_dot;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    // dg, and its sums from each step to the end, in 64 bits (they cancel)
-    constexpr int N = C / 32;
-    double x[N], total = 0.0, last = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) last += (double)g.last * sums[0][i] + sums[1][i];
-#pragma unroll
-    for (int i = N - 1; i >= 0; --i) {
-      const int r = lane * N + i;
-      double d = 0.0;
-#pragma unroll
-      for (int c = 0; c < G::WC; ++c) d += red[c][r];
-      if (r == C - 1) d += last;
-      total += d;
-      x[i] = total;
-    }
-    double after = total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_down_sync(0xffffffffu, after, o);
-      if (lane + o < 32) after += y;
-    }
-    after = __shfl_down_sync(0xffffffffu, after, 1);
-    if (lane == 31) after = 0.0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = lane * N + i;
-      if (r < n) p.dlog_decay[gate0 + (long long)r * p.H] = (float)(x[i] + after);
-    }
-  }
-  if (tid < n) p.dbeta[gate0 + (long long)tid * p.H] = dbeta[tid];
+  copy_wait<0>();
 }
 
 // part [2][rows][G][share][D] -> dq, dk [rows][G][D], a group's heads in order;
@@ -375,21 +589,24 @@ __global__ void __launch_bounds__(256) k_delta_group_sum(long long n, int share,
       s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
     }
     T* to = (i < n ? dq : dk) + e;
-    put_pair(to, s.x, s.y);
-    put_pair(to + 2, s.z, s.w);
+    put_pair(to, make_float2(s.x, s.y));
+    put_pair(to + 2, make_float2(s.z, s.w));
   }
 }
 
 template <int NI, int DK, bool kShared>
 cudaError_t grads_s(const DeltaGrads& p, float* part, cudaStream_t s) {
   using G = Geom<NI, DK>;
-  static_assert(G::smem + 4096 <= 232448, "");
-  const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<NI, DK, kShared>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem);
+  static_assert(G::smem + 16384 <= 232448, "");
+  // (B T H is at most 4e10, and an item 32 steps or more)
+  const long long items = (long long)p.B * p.H * ((p.T + G::C - 1) / G::C);
+  int grid = 1;
+  static FitOf fit;
+  const cudaError_t e = persistent_grid(k_delta_grads<NI, DK, kShared>, G::NT, G::smem, items, 1 << 16,
+                                        &fit, &grid);
   if (e != cudaSuccess) return e;
   LaunchScope ls("delta_grads", s);
-  k_delta_grads<NI, DK, kShared>
-      <<<dim3((p.T + G::C - 1) / G::C, p.H, p.B), kThreads, G::smem, s>>>(p, part);
+  k_delta_grads<NI, DK, kShared><<<grid, G::NT, G::smem, s>>>(p, part, (uint32_t)items);
   return cudaGetLastError();
 }
 
@@ -410,7 +627,7 @@ cudaError_t grads_t(const DeltaGrads& p, float* part, cudaStream_t s) {
 
 cudaError_t delta_grads(const DeltaGrads& p, float* part, bool bf16, cudaStream_t s) {
   if (bf16) return p.dk <= 64 ? grads_t<1, 64>(p, part, s) : grads_t<1, 128>(p, part, s);
-  return p.dk <= 64 ? grads_t<3, 64>(p, part, s) : grads_t<3, 128>(p, part, s);
+  return p.dk <= 64 ? grads_t<2, 64>(p, part, s) : grads_t<2, 128>(p, part, s);
 }
 
 }  // namespace ssd

@@ -26,9 +26,11 @@ def __getattr__(name):
     if name in ("forward", "backward", "forward_raw", "backward_raw", "rmsnorm_gated_forward",
                 "rmsnorm_gated_backward", "conv1d_silu_forward", "conv1d_silu_backward",
                 "workspace_bytes", "kernel_path", "launch_count", "alloc_workspace", "dims_of"):
-        from . import api
-        return getattr(api, name)
-    if name in _LAYER:
-        from . import layer_api
-        return getattr(layer_api, name)
-    raise AttributeError(name)
+        from . import api as module
+    elif name in _LAYER:
+        from . import layer_api as module
+    else:
+        raise AttributeError(name)
+    # found without this function from now on (it took a third of a small call)
+    globals()[name] = value = getattr(module, name)
+    return value

@@ -1,4 +1,4 @@
-// Rows of a matrix held in registers by W warps each, eight elements a lane: loads,
+// Rows of a matrix held in registers by W warps each, eight elements or more a lane: loads,
 // stores, sums over a row, and the asynchronous copies of the next row.  Used by
 // the norms.
 #pragma once
@@ -11,7 +11,7 @@
 namespace ssd {
 namespace rows {
 
-constexpr int kL = 8;  // elements of a lane
+constexpr int kL = 8;  // elements of a lane where a kernel takes no other number (L)
 
 template <int W>
 struct Shape {
@@ -30,12 +30,12 @@ __device__ __forceinline__ int column(int lane, int i) {
 // v[i] = row[column(i)], zero past the width.  In the vector case the width is
 // a multiple of the vector; U: the type of the column rule (that of y), T: the
 // type of the row, whose vectors may be twice as long.
-template <typename U, bool VEC, int W, typename T>
-__device__ __forceinline__ void load_row(const T* row, int lane, int width, float (&v)[kL]) {
+template <typename U, bool VEC, int W, typename T, int L>
+__device__ __forceinline__ void load_row(const T* row, int lane, int width, float (&v)[L]) {
   if constexpr (VEC) {
     constexpr int E = 16 / (int)sizeof(U);
 #pragma unroll
-    for (int j = 0; j < kL; j += E) {
+    for (int j = 0; j < L; j += E) {
       const int c = column<U, VEC, W>(lane, j);
       if (c < width) {
         if constexpr (sizeof(T) == 2) {
@@ -61,19 +61,19 @@ __device__ __forceinline__ void load_row(const T* row, int lane, int width, floa
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kL; ++i) {
+    for (int i = 0; i < L; ++i) {
       const int c = column<U, VEC, W>(lane, i);
       v[i] = c < width ? to_f32(row[c]) : 0.f;
     }
   }
 }
 
-template <typename U, bool VEC, int W, typename T>
-__device__ __forceinline__ void store_row(T* row, int lane, int width, const float (&v)[kL]) {
+template <typename U, bool VEC, int W, typename T, int L>
+__device__ __forceinline__ void store_row(T* row, int lane, int width, const float (&v)[L]) {
   if constexpr (VEC) {
     constexpr int E = 16 / (int)sizeof(U);
 #pragma unroll
-    for (int j = 0; j < kL; j += E) {
+    for (int j = 0; j < L; j += E) {
       const int c = column<U, VEC, W>(lane, j);
       if (c >= width) continue;
       if constexpr (sizeof(T) == 2) {
@@ -90,7 +90,7 @@ __device__ __forceinline__ void store_row(T* row, int lane, int width, const flo
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kL; ++i) {
+    for (int i = 0; i < L; ++i) {
       const int c = column<U, VEC, W>(lane, i);
       if (c < width) row[c] = from_f32<T>(v[i]);
     }
@@ -126,9 +126,9 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* red, int buf, in
 // pieces in the vector case.  The vector case copies the next row's pieces into
 // shared memory (cp.async, two stages) while the current row is worked on; a
 // thread reads back only what it copied itself.
-template <typename T, bool VEC>
+template <typename T, bool VEC, int L = kL>
 struct Pieces {
-  static constexpr int n = VEC ? kL * (int)sizeof(T) / 16 : 0;
+  static constexpr int n = VEC ? L * (int)sizeof(T) / 16 : 0;
 };
 // (not for CTAs of 1024 threads: two stages of a norm's backward do not fit beside
 // the weights in a CTA's shared memory, and its forward follows the same rule)
@@ -147,27 +147,27 @@ __device__ __forceinline__ void cp_wait1() { asm volatile("cp.async.wait_group 1
 __device__ __forceinline__ void cp_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // The pieces of a row into slots [piece][thread]; U: the type of the column rule.
-template <typename U, int W, typename T>
+template <typename U, int W, int L = kL, typename T>
 __device__ __forceinline__ void fetch(uint4* slot, const T* row, int lane, int width) {
 #pragma unroll
-  for (int i = 0; i < Pieces<T, true>::n; ++i) {
+  for (int i = 0; i < Pieces<T, true, L>::n; ++i) {
     const int c = column<U, true, W>(lane, i * (16 / (int)sizeof(T)));
     const bool in = c < width;
     cp_async16(slot + i * Shape<W>::kThreads, in ? row + c : row, in);
   }
 }
-template <typename T, int W>
-__device__ __forceinline__ void unpack(const uint4* slot, float (&v)[kL]) {
+template <typename T, int W, int L>
+__device__ __forceinline__ void unpack(const uint4* slot, float (&v)[L]) {
 #pragma unroll
-  for (int i = 0; i < Pieces<T, true>::n; ++i) {
+  for (int i = 0; i < Pieces<T, true, L>::n; ++i) {
     const uint4 q = slot[i * Shape<W>::kThreads];
     if constexpr (sizeof(T) == 2) {
       const __nv_bfloat162* h = (const __nv_bfloat162*)&q;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = __bfloat1622float2(h[j]);
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
+        v[8 * i + 2 * j] = f.x;
+        v[8 * i + 2 * j + 1] = f.y;
       }
     } else {
       const float4 f = *(const float4*)&q;

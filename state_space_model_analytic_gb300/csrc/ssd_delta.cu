@@ -330,8 +330,11 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       };
       auto q_done = [&](int r, float s, float) { g.qdown[r] = p.scale * inverse_pow2(s); };
       if constexpr (NI == 1) {
-        scale_rows<C, DK, kPrep>(st + G::KT, tid, no_least, k_done);
-        if (!kStates) scale_rows<C, DK, kPrep>(st, tid, no_least, q_done);
+        HalfRows<C, DK, kPrep> k, q;
+        k.read(st + G::KT, tid);
+        if (!kStates) q.read(st, tid);
+        k.write(st + G::KT, tid, no_least, k_done);
+        if (!kStates) q.write(st, tid, no_least, q_done);
       } else {
         FloatRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       copy_commit();
       if (nc > 1) load(1);
       copy_commit();
-      if (warp == 0) {
+      if (warp == kPrep / 32 - 1) {
         load_raw(0);
         scan_gates<C>(gates[0], raw, lane);
         load_raw(1);
@@ -650,8 +653,11 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       static_assert(C * kVB / E % kPrep == 0, "");
       float d[ND][E];
       if constexpr (NI == 1) {
-        scale_rows<C, DK, kPrep>(st + G::KT, tid, no_least, k_done);
-        scale_rows<C, DK, kPrep>(st, tid, no_least, q_done);
+        HalfRows<C, DK, kPrep> k, q;
+        k.read(st + G::KT, tid);
+        q.read(st, tid);
+        k.write(st + G::KT, tid, no_least, k_done);
+        q.write(st, tid, no_least, q_done);
       } else {
         FloatRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
@@ -721,7 +727,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       copy_commit();
       if (nc > 1) load(nc - 2);
       copy_commit();
-      if (warp == 0) {
+      if (warp == kPrep / 32 - 1) {
         load_raw(nc - 1);
         scan_gates<C>(gates[(nc - 1) % 3], raw, lane);
         load_raw(nc - 2);

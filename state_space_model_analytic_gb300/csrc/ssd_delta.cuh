@@ -348,34 +348,41 @@ __device__ __forceinline__ uint4 bf_to_half(const uint4& q, float s) {
   return r;
 }
 __device__ __forceinline__ float no_least(int) { return 0.f; }
-// A bf16 tile to fp16 in place, row by row, each scaled into [1, 2), or by no more than
-// `least(row)` would be; done(row, scale, largest) by one lane a row.
-template <int C, int DK, int NT, typename F, typename L>
-__device__ __forceinline__ void scale_rows(uint8_t* tile, int tid, L least, F done) {
-  constexpr int RB = DK * 2, LPR = DK / 8, N = C * LPR / NT;
+// A bf16 tile to fp16 in its place: a thread's elements are read, and written row by
+// row, each scaled into [1, 2), or by no more than `least(row)` would be; done(row,
+// scale, largest) by one lane a row.
+template <int C, int DK, int NT>
+struct HalfRows {
+  static constexpr int LPR = DK / 8, N = C * LPR / NT;
   static_assert(C * LPR % NT == 0, "");
   uint4 q[N];
-  __nv_bfloat162 m[N];
+  __device__ __forceinline__ void read(const uint8_t* tile, int tid) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int at = i * NT + tid;
-    q[i] = *(const uint4*)(tile + at16<RB>(at / LPR, at % LPR));
+    for (int i = 0; i < N; ++i) {
+      const int at = i * NT + tid;
+      q[i] = *(const uint4*)(tile + at16<DK * 2>(at / LPR, at % LPR));
+    }
   }
+  template <typename F, typename L>
+  __device__ __forceinline__ void write(uint8_t* tile, int tid, L least, F done) const {
+    __nv_bfloat162 m[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) m[i] = max_bf(q[i]);
+    for (int i = 0; i < N; ++i) m[i] = max_bf(q[i]);
 #pragma unroll
-  for (int o = 1; o < LPR; o <<= 1)
+    for (int o = 1; o < LPR; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) m[i] = __hmax2(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+      for (int i = 0; i < N; ++i) m[i] = __hmax2(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int at = i * NT + tid, r = at / LPR, x = at % LPR;
-    const float most = fmaxf(fmaxf(__low2float(m[i]), __high2float(m[i])), least(r));
-    const float s = row_exponent(most);
-    *(uint4*)(tile + at16<RB>(r, x)) = bf_to_half(q[i], s);
-    if (x == 0) done(r, s, most);
+    for (int i = 0; i < N; ++i) {
+      const int at = i * NT + tid, r = at / LPR, x = at % LPR;
+      const float most = fmaxf(fmaxf(__low2float(m[i]), __high2float(m[i])), least(r));
+      const float s = row_exponent(most);
+      *(uint4*)(tile + at16<DK * 2>(r, x)) = bf_to_half(q[i], s);
+      if (x == 0) done(r, s, most);
+    }
   }
-}
+};
+
 // fp32: C rows of D elements one behind the other, as asynchronous copies.
 template <int C, int D, int NT>
 __device__ __forceinline__ void load_tile(uint8_t* tile, const float* s, long long stride, int n,
@@ -538,54 +545,65 @@ struct alignas(16) Scratch {
   float most[kPrep / 32];
 };
 
-// One block of 16 x 16 of A K^T, rows 16 bi ..., columns 16 bj ..., times the decays:
-// to the tile `out` in PO parts, their signs exchanged with `flip` (the sign bits of two
-// fp16), or to `diag`, transposed.  On the diagonal what lies above it is zero (kDiagL:
-// and on it).
-template <int NI, int DK, int PO, bool kDiagL>
-__device__ __forceinline__ void score_block(uint32_t A, uint32_t K, uint8_t* out,
+// One block of 16 x 16, rows 16 bi ..., columns 16 bj ..., of L and, with kP, of P, which
+// share the decays and the right operand.  -L goes to the tile M in parts, or on the
+// diagonal (kDiagonal) L to `diag`, transposed; P to its tile in PP parts.  On the
+// diagonal P is zero above it and L on it too.
+template <int NI, int DK, int PP, bool kP, bool kDiagonal>
+__device__ __forceinline__ void score_block(uint32_t Q, uint32_t K, uint8_t* M, uint8_t* P,
                                             const Gates<kSteps<NI>>& g, float (*diag)[kDiag], int bi,
-                                            int bj, uint32_t flip, int lane) {
-  constexpr int C = kSteps<NI>, RB = DK * 2, OB = C * 2;
+                                            int bj, int lane) {
+  constexpr int C = kSteps<NI>, RB = DK * 2, OB = C * 2, NA = kP ? 2 : 1;
   const Lane<RB> at(lane);
-  float acc[2][4];
-  zero(acc);
-  constexpr int U = NI == 1 ? DK / 16 : 2;  // (every operand of a bf16 block on its way at once)
-  A += bi * 16 * RB;
-  const uint32_t B = K + bj * 16 * RB;
+  float acc[NA][2][4];
+  const uint32_t A[2] = {K + bi * 16 * RB, Q + bi * 16 * RB}, B = K + bj * 16 * RB;
+#pragma unroll
+  for (int w = 0; w < NA; ++w) zero(acc[w]);
+  constexpr int U = NI == 1 ? 4 : 2;
 #pragma unroll(U)
   for (int k = 0; k < DK; k += 16) {
-    uint32_t a[NI][4], b[NI][2][2];
+    uint32_t a[NA][NI][4], b[NI][2][2];
 #pragma unroll
-    for (int p = 0; p < NI; ++p) ldm4(a[p], at.left(A, 0, k) + p * C * RB);
+    for (int w = 0; w < NA; ++w)
+#pragma unroll
+      for (int p = 0; p < NI; ++p) ldm4(a[w][p], at.left(A[w], 0, k) + p * C * RB);
     load_right<NI, 2>(b, B, C * RB, at, 0, k);
-    mma_parts<NI, NI, 2>(acc, a, b);
+#pragma unroll
+    for (int w = 0; w < NA; ++w) mma_parts<NI, NI, 2>(acc[w], a[w], b);
   }
-  const int c0 = (lane & 3) * 2, r0 = lane >> 2, i0 = 16 * bi + r0;
-  const float* gi = &g.hi[i0];
+  const int c0 = (lane & 3) * 2, r0 = lane >> 2;
+  const float* gi = &g.hi[16 * bi + r0];
   const float* gj = &g.hi[16 * bj + c0];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const float2 hj = *(const float2*)(gj + 8 * n), lj = *(const float2*)(gj + C + 8 * n);
-    const int j = 16 * (bj - bi) + 8 * n + c0;  // (beside the block's first row)
+    const int j = 8 * n + c0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int i = r0 + 8 * u;
       // Gamma_ij = 2^((hi_i - hi_j) + (lo_i - lo_j))
       const float2 minus = both(-1.f);
       const float2 t = add2(fma2(hj, minus, both(gi[8 * u])), fma2(lj, minus, both(gi[C + 8 * u])));
-      float2 x = mul2(pair(acc[n], u), make_float2(exp2_fast(t.x), exp2_fast(t.y)));
-      if (kDiagL ? j >= i : j > i) x.x = 0.f;
-      if (kDiagL ? j + 1 >= i : j + 1 > i) x.y = 0.f;
-      if constexpr (kDiagL) {
-        diag[8 * n + c0][i] = x.x;
-        diag[8 * n + c0 + 1][i] = x.y;
+      const float2 gamma = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+      float2 l = mul2(pair(acc[0][n], u), gamma);
+      const uint32_t to = at16<OB>(16 * bi + i, 2 * bj + n) + c0 * 2;
+      if constexpr (kDiagonal) {
+        diag[j][i] = j < i ? l.x : 0.f;
+        diag[j + 1][i] = j + 1 < i ? l.y : 0.f;
       } else {
-        uint32_t p[PO];
-        split2<PO>(x, p);
-        uint8_t* to = out + at16<OB>(16 * bi + i, 2 * bj + n) + c0 * 2;
+        uint32_t p[kParts];
+        split2<kParts>(make_float2(-l.x, -l.y), p);
 #pragma unroll
-        for (int q = 0; q < PO; ++q) *(uint32_t*)(to + q * C * OB) = p[q] ^ flip;
+        for (int q = 0; q < kParts; ++q) *(uint32_t*)(M + to + q * C * OB) = p[q];
+      }
+      if constexpr (kP) {
+        float2 v = mul2(pair(acc[NA - 1][n], u), gamma);
+        if (kDiagonal && j > i) v.x = 0.f;
+        if (kDiagonal && j + 1 > i) v.y = 0.f;
+        uint32_t p[PP];
+        split2<PP>(v, p);
+#pragma unroll
+        for (int q = 0; q < PP; ++q) *(uint32_t*)(P + to + q * C * OB) = p[q];
       }
     }
   }
@@ -633,12 +651,11 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, Gates<C>& g, const flo
 }
 
 // M and, with kP, P of a chunk whose operands and gates are in shared memory, by the
-// kPrep threads: a warp takes one of L's diagonal blocks and inverts it, the others the
-// blocks below the diagonal and those of P.  (The blocks go through one loop: as
-// straight code, with the strips of a warp known at compile time, the warps' code and
-// the walk's did not fit the instruction caches together, and waiting for instructions
-// was the largest of all stalls.)  Warp 0 has `aside` to do as well (the gates of a
-// later chunk).
+// kPrep threads: a warp takes a diagonal block and inverts L's, the others the blocks
+// below the diagonal.  (These go through one loop: as straight code, with the strips of
+// a warp known at compile time, the warps' code and the walk's did not fit the
+// instruction caches together, and waiting for instructions was the largest of all
+// stalls.)  The last warp has `aside` to do as well (the gates of a later chunk).
 template <int NI, int DK, int PP, bool kP, typename F>
 __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, uint8_t* M, uint8_t* P,
                                         Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc, int tid,
@@ -647,28 +664,17 @@ __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, ui
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t K = smem32(Kt), Q = smem32(Qt);
   if (warp < NB) {
-    score_block<NI, DK, kParts, true>(K, K, nullptr, g, sc.diag[warp], warp, warp, 0u, lane);
+    score_block<NI, DK, PP, kP, true>(Q, K, M, P, g, sc.diag[warp], warp, warp, lane);
     __syncwarp();
     if (lane < 16) invert_diag<C>(M, g, sc.diag[warp], warp, lane);
     __syncwarp();
-    if (warp == 0) aside();
   } else {
-    // L's blocks below the diagonal, rows and columns (hexadecimal digits, the first last)
-    constexpr uint32_t kLi = NB == 4 ? 0x333221 : 0x1, kLj = NB == 4 ? 0x210100 : 0x0;
-    constexpr uint64_t kPi = NB == 4 ? 0x3333222110ull : 0x110, kPj = NB == 4 ? 0x3210210100ull : 0x100;
-    constexpr int nL = NB * (NB - 1) / 2, nP = NB * (NB + 1) / 2;
-    const int w = warp - NB;
+    // rows and columns (hexadecimal digits, the first last)
+    constexpr uint32_t kI = NB == 4 ? 0x333221 : 0x1, kJ = NB == 4 ? 0x210100 : 0x0;
 #pragma unroll 1
-    for (int r = w; r < nL; r += W)
-      score_block<NI, DK, kParts, false>(K, K, M, g, nullptr, kLi >> 4 * r & 15, kLj >> 4 * r & 15,
-                                         0x80008000u, lane);
-    if constexpr (kP) {
-      // (in the order that leaves every warp the same number of blocks)
-#pragma unroll 1
-      for (int r = (w + W - nL % W) % W; r < nP; r += W)
-        score_block<NI, DK, PP, false>(Q, K, P, g, nullptr, kPi >> 4 * r & 15, kPj >> 4 * r & 15, 0u,
-                                       lane);
-    }
+    for (int r = warp - NB; r < NB * (NB - 1) / 2; r += W)
+      score_block<NI, DK, PP, kP, false>(Q, K, M, P, g, nullptr, kI >> 4 * r & 15, kJ >> 4 * r & 15, lane);
+    if (warp == kPrep / 32 - 1) aside();
   }
 }
 

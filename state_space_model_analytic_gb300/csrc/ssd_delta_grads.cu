@@ -220,12 +220,13 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
       const float hs0 = hs, ds0 = ds;
       {
         FloatRows<kVB, DK, NT> fh, fd;
-        FloatRows<C, kVB, NT> fe, fy, fo;
+        FloatRows<C, kVB, NT> fe, fy;
+        typename std::conditional<NI == 1, HalfRows<C, kVB, NT>, FloatRows<C, kVB, NT>>::type fo;
         fh.read(Ht, tid);
         fd.read(Ht + G::HT, tid);
         fe.read(sm + G::kU, tid);
         fy.read(sm + G::kV, tid);
-        if constexpr (NI == 2) fo.read(sm + G::kO, tid);
+        fo.read(sm + G::kO, tid);
         // (later pieces are not scaled up by more than the earlier ones, so that sums of
         // these may be scaled to them)
 #pragma unroll
@@ -276,8 +277,7 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         };
         fe.write(sm + G::kU, tid, least(0), done(0));
         fy.write(sm + G::kV, tid, least(1), done(1));
-        if constexpr (NI == 2) fo.write(sm + G::kO, tid, least(2), done(2));
-        else scale_rows<C, kVB, NT>(sm + G::kO, tid, least(2), done(2));
+        fo.write(sm + G::kO, tid, least(2), done(2));
       }
       __syncthreads();
       if (vb + 1 < vblocks) load_state(x, vb + 1, buf ^ 1);
@@ -354,8 +354,11 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         q.write(sm, tid, no_least, q_done);
         k.write(sm + G::kK, tid, no_least, k_done);
       } else {
-        scale_rows<C, DK, NT>(sm, tid, no_least, q_done);
-        scale_rows<C, DK, NT>(sm + G::kK, tid, no_least, k_done);
+        HalfRows<C, DK, NT> q, k;
+        q.read(sm, tid);
+        k.read(sm + G::kK, tid);
+        q.write(sm, tid, no_least, q_done);
+        k.write(sm + G::kK, tid, no_least, k_done);
       }
     }
     __syncthreads();

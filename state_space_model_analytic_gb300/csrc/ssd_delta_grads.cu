@@ -54,10 +54,9 @@ struct Geom {
   static_assert(WR * WC * 32 == NT && NK % 2 == 0 && NM % 2 == 0, "");
 };
 
-// a row-major tile's two elements at (row, column c, c + 1)
+// a row-major tile's two elements at `at`
 template <int NI, int RB, int C>
-__device__ __forceinline__ float2 pair_at(const uint8_t* tile, int row, int c) {
-  const uint8_t* at = tile + at16<RB>(row, c >> 3) + (c & 7) * 2;
+__device__ __forceinline__ float2 pair_at(const uint8_t* at) {
   float2 f = unpack_half(*(const uint32_t*)at);
   if (NI == 2) f = add2(f, unpack_half(*(const uint32_t*)(at + C * RB)));
   return f;
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         }
       }
       const uint32_t sH = smem32(Ht), sD = sH + G::HT;
-#pragma unroll 1
+#pragma unroll 2
       for (int k = 0; k < width; k += 16) {
         uint32_t ao[NI][4], au[kParts][4], av[kParts][4];
 #pragma unroll
@@ -369,22 +368,24 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
       const int r = i0 + 8 * u;
       const float fq = p.scale * g.lead[r] * odown[r] * hs, fr = -g.lead[r] * vdown[r] * hs,
                   fw = g.tail[r] * udown[r] * ds;
-      float read_q = 0.f, read_k = 0.f, write = 0.f;
+      float2 read_q = both(0.f), read_k = both(0.f), write2 = both(0.f);
+      // (a row's pieces: their index exchanged by r's last bits)
+      const uint8_t* row = sm + r * RB + c2 * 2;
 #pragma unroll
       for (int e = 0; e < NK; ++e) {
-        const int c = (group * NK + e) * 8 + c2;
-        const float2 q = pair_at<NI, RB, C>(sm, r, c), k = pair_at<NI, RB, C>(sm + G::kK, r, c);
+        const uint8_t* at = row + (((group * NK + e) ^ (r & 7)) << 4);
+        const float2 q = pair_at<NI, RB, C>(at), k = pair_at<NI, RB, C>(at + G::kK);
         const float2 a = mul2(pair(dq[e], u), both(fq)), b = mul2(pair(rd[e], u), both(fr)),
                      w = mul2(pair(wr[e], u), both(fw));
         set_pair(dq[e], u, a);
         set_pair(rd[e], u, b);
         set_pair(wr[e], u, w);
-        read_q = fmaf(q.x, a.x, fmaf(q.y, a.y, read_q));
-        read_k = fmaf(k.x, b.x, fmaf(k.y, b.y, read_k));
-        write = fmaf(k.x, w.x, fmaf(k.y, w.y, write));
+        read_q = fma2(q, a, read_q);
+        read_k = fma2(k, b, read_k);
+        write2 = fma2(k, w, write2);
       }
-      const float s = sum_lanes<4>(read_q * qdown[r] + read_k * kdown[r]);
-      write = sum_lanes<4>(write * kdown[r]);
+      const float s = sum_lanes<4>((read_q.x + read_q.y) * qdown[r] + (read_k.x + read_k.y) * kdown[r]);
+      const float write = sum_lanes<4>((write2.x + write2.y) * kdown[r]);
       if ((lane & 3) == 0) {
         reads[group][r] = s;
         writes[group][r] = write;
@@ -394,7 +395,14 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
     float largest = 0.f;
     {
       const uint32_t A = is_l ? sK : sQ;
-      float row[2] = {0.f, 0.f};
+      float row[2] = {0.f, 0.f}, f[2], hi[2], lo[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + 8 * u;
+        f[u] = is_l ? -vdown[i] * kdown[i] : p.scale * odown[i] * qdown[i];
+        hi[u] = g.hi[i];
+        lo[u] = g.lo[i];
+      }
 #pragma unroll
       for (int e = 0; e < NM; e += 2) {
         float s[2][4];
@@ -420,12 +428,15 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int i = i0 + 8 * u;
-              const float f = is_l ? -vdown[i] * kdown[i] : p.scale * odown[i] * qdown[i];
-              float2 v = mul2(mul2(pair(m, u), both(f)), fj);
-              v.x *= decay(g.hi[i], g.lo[i], hj.x, lj.x);
-              v.y *= decay(g.hi[i], g.lo[i], hj.y, lj.y);
-              if (is_l ? j >= i : j > i) v.x = 0.f;
-              if (is_l ? j + 1 >= i : j + 1 > i) v.y = 0.f;
+              const float2 minus = both(-1.f);
+              const float2 t = add2(fma2(hj, minus, both(hi[u])), fma2(lj, minus, both(lo[u])));
+              float2 v = mul2(mul2(mul2(pair(m, u), both(f[u])), fj),
+                              make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+              if (m0 + e == 2 * strip) {  // (the diagonal's columns)
+                const int above = is_l ? 1 : 0;
+                if (j + above > i) v.x = 0.f;
+                if (j + 1 + above > i) v.y = 0.f;
+              }
               set_pair(m, u, v);
               largest = max3_abs(largest, v.x, v.y);
               const float2 c = mul2(v, pair(s[q], u));
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
       zero(d[0]);
       zero(d[1]);
       zero(d[2]);
-#pragma unroll 1
+#pragma unroll
       for (int k = 0; k < NB; ++k) {
         uint32_t a[PM][4], rk[NI][2][2];
         load_right_t<NI, 2>(rk, sK, C * RB, lk, c, 16 * k);

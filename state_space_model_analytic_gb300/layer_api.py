@@ -230,8 +230,8 @@ def linattn_backward(q, k, v, log_decay, state0, do, dstate=None, *, scale=1.0, 
     return g
 
 
-def _step_out(d, v, state, slots, state_out, out):
-    """(o, new states, rows of the states) of one token's call after the checks."""
+def _step_rows(d, v, state, slots, state_out, out):
+    """Rows of the states of one token's call after the checks."""
     dev = v.device
     rows = state.shape[0] if state.dim() else 0
     _expect("state", state, torch.float32, (rows, d.nheads, d.dv, d.dk), dev)
@@ -239,15 +239,11 @@ def _step_out(d, v, state, slots, state_out, out):
         _expect("slots", slots, torch.int32, (d.batch,), dev)
     elif rows != d.batch:
         raise ValueError(f"state: {rows} rows, expected {d.batch}")
-    if state_out is None:
-        state_out = torch.empty_like(state) if slots is None else state
-    else:
+    if state_out is not None:
         _expect("state_out", state_out, torch.float32, state.shape, dev)
-    if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    else:
+    if out is not None:
         _expect("out", out, v.dtype, v.shape, dev)
-    return out, state_out, rows
+    return rows
 
 
 def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=None, out=None,
@@ -265,7 +261,11 @@ def linattn_step(q, k, v, log_decay, state, *, scale=1.0, slots=None, state_out=
     d = _linattn_dims(q, k, v, scale, log_decay, None, True)[0]
     dev = q.device
     _check_device(dev, stream)
-    out, state_out, rows = _step_out(d, v, state, slots, state_out, out)
+    rows = _step_rows(d, v, state, slots, state_out, out)
+    if state_out is None:
+        state_out = torch.empty_like(state) if slots is None else state
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
     _streams.keep(stream, q, k, v, log_decay, state, slots, out, state_out)
     nat.check(_call("ssd_linattn_step")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
@@ -359,15 +359,34 @@ def delta_rule_backward(q, k, v, log_decay, beta, state0, do, dstate=None, *, sc
     return g
 
 
+def _dense_key(t):
+    return None if t is None else (t.shape, t.dtype, t.is_contiguous())
+
+
 def delta_rule_step(q, k, v, log_decay, beta, state, *, scale=1.0, slots=None, state_out=None,
                     out=None, stream=None):
     """One token of every row: q, k [B,G,K], v [B,H,V], log_decay, beta [B,H]
     fp32; state [rows,H,V,K] fp32, slots and state_out as in linattn_step.
     Returns (o [B,H,V], state_out)."""
-    d = _delta_dims(q, k, v, scale, log_decay, beta, None, True)[0]
     dev = q.device
+    scale = float(scale)
+    # every check but the devices' depends on this alone: small calls are host-bound
+    key = ("delta step", scale, q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype,
+           v.shape, v.stride(), v.dtype, _dense_key(log_decay), _dense_key(beta),
+           _dense_key(state), _dense_key(slots), _dense_key(state_out), _dense_key(out))
+    got = _layouts.get(key)
+    for t in (q, k, v, log_decay, beta, state, slots, state_out, out):
+        if t is not None and (t.device != dev or not t.is_cuda):
+            got = None  # refused below
+    if got is None:
+        d = _delta_dims(q, k, v, scale, log_decay, beta, None, True)[0]
+        got = _layouts.keep(key, (d, _step_rows(d, v, state, slots, state_out, out)))
+    d, rows = got
     _check_device(dev, stream)
-    out, state_out, rows = _step_out(d, v, state, slots, state_out, out)
+    if state_out is None:
+        state_out = torch.empty_like(state) if slots is None else state
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
     _streams.keep(stream, q, k, v, log_decay, beta, state, slots, out, state_out)
     nat.check(_call("ssd_delta_rule_step")(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),

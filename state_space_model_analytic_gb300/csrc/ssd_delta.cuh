@@ -107,10 +107,12 @@ __device__ __forceinline__ Scale scale_to(float m) {
   e = e < 40 ? 40 : e > 250 ? 250 : e;
   return {__uint_as_float((uint32_t)(254 + T - e) << 23), __uint_as_float((uint32_t)(e - T) << 23)};
 }
-// The same for a row of k or q: into [1, 2), by 2^-63 to 2^63, rows of zeros as they are.
+// The same for a row of steps: into [1, 2), by 2^-kFar to 2^kFar, rows of zeros as they
+// are.  (For k and q kFar is 63: beta is divided by the square.)
+template <int kFar>
 __device__ __forceinline__ float row_exponent(float m) {
   int e = (int)(__float_as_uint(m) >> 23);
-  e = m == 0.f ? 127 : e < 64 ? 64 : e > 190 ? 190 : e;
+  e = m == 0.f ? 127 : e < 127 - kFar ? 127 - kFar : e > 127 + kFar ? 127 + kFar : e;
   return __uint_as_float((uint32_t)(254 - e) << 23);
 }
 __device__ __forceinline__ float inverse_pow2(float x) {
@@ -363,7 +365,7 @@ struct HalfRows {
       q[i] = *(const uint4*)(tile + at16<DK * 2>(at / LPR, at % LPR));
     }
   }
-  template <typename F, typename L>
+  template <int kFar = 63, typename F, typename L>
   __device__ __forceinline__ void write(uint8_t* tile, int tid, L least, F done) const {
     __nv_bfloat162 m[N];
 #pragma unroll
@@ -376,7 +378,7 @@ struct HalfRows {
     for (int i = 0; i < N; ++i) {
       const int at = i * NT + tid, r = at / LPR, x = at % LPR;
       const float most = fmaxf(fmaxf(__low2float(m[i]), __high2float(m[i])), least(r));
-      const float s = row_exponent(most);
+      const float s = row_exponent<kFar>(most);
       *(uint4*)(tile + at16<DK * 2>(r, x)) = bf_to_half(q[i], s);
       if (x == 0) done(r, s, most);
     }
@@ -424,7 +426,7 @@ struct FloatRows {
   }
   // each row scaled into [1, 2), or by no more than `least(row)` would be; done(row,
   // scale, largest) by one lane a row
-  template <typename F, typename L>
+  template <int kFar = 63, typename F, typename L>
   __device__ __forceinline__ void write(uint8_t* tile, int tid, L least, F done) const {
     float m[N];
 #pragma unroll
@@ -438,7 +440,7 @@ struct FloatRows {
     for (int i = 0; i < N; ++i) {
       const int at = i * NT + tid;
       m[i] = fmaxf(m[i], least(at / LPR));
-      const float s = row_exponent(m[i]);
+      const float s = row_exponent<kFar>(m[i]);
       put(tile, i, s, tid);
       if (at % LPR == 0) done(at / LPR, s, m[i]);
     }

@@ -274,9 +274,9 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
             down[now][which][r] = inverse_pow2(s);
           };
         };
-        fe.write(sm + G::kU, tid, least(0), done(0));
-        fy.write(sm + G::kV, tid, least(1), done(1));
-        fo.write(sm + G::kO, tid, least(2), done(2));
+        fe.template write<100>(sm + G::kU, tid, least(0), done(0));
+        fy.template write<100>(sm + G::kV, tid, least(1), done(1));
+        fo.template write<100>(sm + G::kO, tid, least(2), done(2));
       }
       __syncthreads();
       if (vb + 1 < vblocks) load_state(x, vb + 1, buf ^ 1);

@@ -326,11 +326,15 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
  * 1; a step with beta |k|^2 > 2 amplifies).  Past a row's length o and every
  * gradient is zero.  The kernels have no waits that could run out.
  *
- * Precision: states, sums and decays are fp32 in either type; everything held in
- * 32 bits enters a product as three bf16 parts (24 bits), bf16 operands as they are.
- * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.
- * A bf16 o takes the state and the scores as two parts (16 bits); o, dq, dk and dv
- * are off by their own rounding alone, 0.0017 of their root mean square.
+ * Precision: states, sums and decays are fp32 in either type.  A value held in 32
+ * bits enters a product as two fp16 parts (22 bits) of its row scaled by a power of
+ * two, a bf16 element as it is; elements below 2^-24 of the largest of their row of
+ * the state (of their step, for q, k, v and dout in fp32) lose bits.  Results do not
+ * depend on powers of two in a step's q, k or v, as long as the largest element of a
+ * key is between 2^-63 and 2^63 and beta times its square is a normal number.
+ * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.  A
+ * bf16 o takes the state and the scores as one part (11 bits); o, dq, dk and dv are
+ * off by little more than their own rounding, 0.0017 of their root mean square.
  */
 
 /* Bytes of workspace of ssd_delta_rule_forward (which = 0) or

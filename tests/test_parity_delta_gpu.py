@@ -2,12 +2,13 @@
 float64 reference.
 
 Tolerances.  The reference gives the size that an output's errors go by (products
-of norms).  Operands held in 32 bits keep 24 bits in products, whose sums pass
-through at most 8 terms x 6 products of parts that the matrix instructions round
-toward zero, 2^-23 of the sum each: 48 * 2^-23 a product, below 2^-17; three
-products follow one another in a chunk and the chunks of a row add up, 32 steps each
-at least: |error| <= 2^-16 max(1, T / 32) size.  A bf16 output is rounded by 2^-8 of
-itself; o takes the state and P as 16 bits, 2^-16 of its size once more."""
+of norms).  Operands held in 32 bits keep 22 bits in products, 2^-21 of each, whose
+sums pass through at most 8 terms x 3 products of parts that the matrix instructions
+round toward zero, 2^-23 of the sum each: 32 * 2^-23 a product in all, below 2^-17;
+three products follow one another in a chunk and the chunks of a row add up, 32 steps
+each at least: |error| <= 2^-16 max(1, T / 32) size.  A bf16 output is rounded by 2^-8
+of itself; o takes the state and P in 11 bits, 2^-12 of each term, which as signs
+differ is far less of o's size, the sum of its terms' magnitudes: 2^-15."""
 import numpy as np
 import pytest
 

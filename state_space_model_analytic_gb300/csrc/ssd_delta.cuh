@@ -468,6 +468,12 @@ __device__ __forceinline__ Two add(Two a, Two b) {
   const float hi = s + e;
   return {hi, e - (hi - s)};
 }
+// a += b, the rounding put aside (one addition waits for the one before)
+__device__ __forceinline__ void put_in(Two& a, float b) {
+  const float s = a.hi + b, t = s - a.hi;
+  a.lo += (a.hi - (s - t)) + (b - t);
+  a.hi = s;
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

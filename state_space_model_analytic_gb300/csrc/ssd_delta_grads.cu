@@ -72,10 +72,10 @@ __device__ __forceinline__ float sum_lanes(float x) {
   for (int d = N / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
   return x;
 }
-__device__ __forceinline__ float max_warp(float x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-  return x;
+// the largest of x >= 0 over a warp and *top, whose bits are in the order of the values
+__device__ __forceinline__ void max_of_all(uint32_t* top, float x, int lane) {
+  const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(x));
+  if (lane == 0) atomicMax(top, m);
 }
 
 // kShared: dq, dk of the head in fp32 to part (dq's, then dk's, [B][T][H][dk])
@@ -93,9 +93,14 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
   // piece and the one before), what q and k were; dbeta; sums over columns and rows.
   __shared__ float most[2][3][C], down[2][3][C], qdown[C], kdown[C], dbeta[C];
   __shared__ float rows_of[G::WC][C], cols_of[2][G::WR][C], reads[G::WC][C], writes[G::WC][C];
-  __shared__ float red[3][NW];
+  __shared__ float hdots[NW];
+  // the bits of the largest of H and D and of MP and ML
+  __shared__ __align__(8) uint32_t top_state[2][2];
+  __shared__ uint32_t top_mask[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int strip = warp % G::WR, group = warp / G::WR;
+  // (the warps of a sub-core, four apart, have different strips: the later ones have more
+  // of MP and ML)
+  const int strip = (warp + warp / 4) % G::WR, group = warp / G::WR;
   const bool is_l = group >= 2;   // this warp's scores: ML's, else MP's
   const int m0 = (group & 1) * NM;  // their first eight of columns
   const uint32_t sQ = smem32(sm), sK = sQ + G::kK, sO = sQ + G::kO, sU = sQ + G::kU, sV = sQ + G::kV;
@@ -167,6 +172,7 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
       p.dlog_decay[(token + r) * p.H + x.h] = p.dbeta[(token + r) * p.H + x.h] = 0.f;
   }
 
+  if (tid < 2) top_state[0][tid] = top_state[1][tid] = top_mask[tid] = 0;
   Item x, nx;
   nx.n = 0;
   uint32_t i = next_of(blockIdx.x, x);
@@ -200,7 +206,8 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
     zero(wr);
     zero(mm);
     float hdot = 0.f;  // <H, D>
-    float hs = 0.f, ds = 0.f, mh = 0.f, md = 0.f;  // H's, D's divisors, largest elements
+    // H's and D's divisors, this lane's largest elements
+    float hs = 0.f, ds = 0.f, mh = 0.f, md = 0.f;
     const int i0 = 16 * strip + (lane >> 2), c2 = (lane & 3) * 2;
 #pragma unroll 1
     for (int vb = 0; vb < vblocks; ++vb) {
@@ -235,12 +242,8 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
           md = max3_abs(max3_abs(md, d.x, d.y), d.z, d.w);
           hdot = fmaf(s.x, d.x, fmaf(s.y, d.y, fmaf(s.z, d.z, fmaf(s.w, d.w, hdot))));
         }
-        mh = max_warp(mh);
-        md = max_warp(md);
-        if (lane == 0) {
-          red[0][warp] = mh;
-          red[1][warp] = md;
-        }
+        max_of_all(&top_state[buf][0], mh, lane);
+        max_of_all(&top_state[buf][1], md, lane);
 #pragma unroll
         for (int k = 0; k < fe.N; ++k) {
           const int at = k * NT + tid, r = at / fe.LPR;
@@ -252,12 +255,8 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
           y.x *= be; y.y *= be; y.z *= be; y.w *= be;
         }
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          mh = fmaxf(mh, red[0][k]);
-          md = fmaxf(md, red[1][k]);
-        }
-        const Scale sh = scale_to<10>(mh), sd = scale_to<10>(md);
+        const uint2 top = *(const uint2*)top_state[buf];
+        const Scale sh = scale_to<10>(__uint_as_float(top.x)), sd = scale_to<10>(__uint_as_float(top.y));
         hs = sh.down;
         ds = sd.down;
 #pragma unroll
@@ -279,6 +278,7 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         fo.template write<100>(sm + G::kO, tid, least(2), done(2));
       }
       __syncthreads();
+      if (tid < 2) top_state[buf][tid] = 0;  // (all have read it)
       if (vb + 1 < vblocks) load_state(x, vb + 1, buf ^ 1);
       else if (in < items) load_state(nx, 0, buf ^ 1);
       copy_commit();
@@ -458,16 +458,11 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         if ((lane & 3) == 0) rows_of[group][i0 + 8 * u] = row[u];
       }
     }
-    largest = max_warp(largest);
+    max_of_all(&top_mask[turn], largest, lane);
     hdot = sum_lanes<32>(hdot);
-    if (lane == 0) {
-      red[0][warp] = largest;
-      red[2][warp] = hdot;
-    }
+    if (lane == 0) hdots[warp] = hdot;
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < NW; ++k) largest = fmaxf(largest, red[0][k]);
-    const Scale smask = scale_to<10>(largest);
+    const Scale smask = scale_to<10>(__uint_as_float(top_mask[turn]));
     uint8_t* Mt = sm + G::kH + (buf ^ 1) * 2 * G::HT;  // the last piece's H and D
     {
       uint8_t* out = Mt + (is_l ? G::HT : 0);
@@ -488,9 +483,10 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
     if (warp == 0) {
       // dg, and its sums from each step to the end, in two floats
       constexpr int N = C / 32;
+      if (lane == 0) top_mask[turn] = 0;
       Two d[N], total = {0.f, 0.f};
       float tails = 0.f, hd = 0.f;
-      for (int k = lane; k < NW; k += 32) hd += red[2][k];
+      for (int k = lane; k < NW; k += 32) hd += hdots[k];
       hd = sum_lanes<32>(hd);
 #pragma unroll
       for (int k = N - 1; k >= 0; --k) {
@@ -498,16 +494,17 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         float w = 0.f;
 #pragma unroll
         for (int c = 0; c < G::WC; ++c) {
-          total = add(add(total, {rows_of[c][r], 0.f}), {reads[c][r], 0.f});
+          put_in(total, rows_of[c][r]);
+          put_in(total, reads[c][r]);
           w += writes[c][r];
         }
 #pragma unroll
         for (int c = 0; c < G::WR; ++c) {
-          total = add(total, {-cols_of[0][c][r], 0.f});
-          total = add(total, {-cols_of[1][c][r], 0.f});
+          put_in(total, -cols_of[0][c][r]);
+          put_in(total, -cols_of[1][c][r]);
         }
         tails += w;
-        total = add(total, {-w, 0.f});
+        put_in(total, -w);
         d[k] = total;
       }
       tails = sum_lanes<32>(tails);

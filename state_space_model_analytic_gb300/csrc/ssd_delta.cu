@@ -34,13 +34,14 @@ template <int NI>
 constexpr int kOutParts = NI == 1 ? 1 : 2;
 
 constexpr int kWalkers = 4;  // warps of a walk
-// Registers of the two kinds of threads: 256 * 128 + 128 * 240 of the 384 * 168 that a
-// CTA starts with.
-constexpr int kPrepRegs = 128, kWalkRegs = 240;
-static_assert(kPrep * kPrepRegs + 32 * kWalkers * kWalkRegs <= (kPrep + 32 * kWalkers) * 168, "");
 
-template <int NI, int DK, int PP, int WK, int kExchanged>
+template <int NI, int DK, int PP, int WK, int kExchanged, bool kHelped = false>
 struct Geom {
+  static constexpr int kThreads = kPrep + 32 * kWalkers * (kHelped ? 2 : 1);
+  // Registers of those that walk and of the others, of what a CTA starts with.
+  static constexpr int kPrepRegs = kHelped ? 96 : 128, kWalkRegs = kHelped ? 224 : 240;
+  static_assert((kThreads - 32 * kWalkers) * kPrepRegs + 32 * kWalkers * kWalkRegs <=
+                    kThreads * (kHelped ? 128 : 168), "");
   static constexpr int C = kSteps<NI>, NC = C / 8;
   static constexpr int RB = DK * 2, PB = C * 2;      // bytes of a row of K, of M
   static constexpr int KT = NI * C * RB;             // K's or Q's tile, all parts
@@ -55,8 +56,13 @@ struct Geom {
   static constexpr int kM = NS * kStage, kP = kM + 2 * MT;
   static constexpr int kG = kP + 2 * PT, kS = kG + 3 * (int)sizeof(Gates<C>);
   static constexpr int kX = kS + (int)sizeof(Scratch<C>);  // sums of WK warps on their way
-  static constexpr size_t smem = kX + (WK > 1 ? kExchanged * kWalkers * NC * 512 : 0);
-  static_assert(kStage % 16 == 0 && kX % 16 == 0, "");
+  // of a walking warp, for those that form its o: the state and U as left operands, what
+  // their rows were multiplied by
+  static constexpr int NB = C / 16, kHS = PP * DK / 16 * 512, kUS = PP * NB * 512;
+  static constexpr int kGiven = kHS + kUS + (1 + NB) * 64;
+  static constexpr size_t smem =
+      kX + (WK > 1 ? kExchanged * kWalkers * NC * 512 : 0) + (kHelped ? kWalkers * kGiven : 0);
+  static_assert(kStage % 16 == 0 && kX % 16 == 0 && kGiven % 16 == 0, "");
 };
 
 // fp32 rows of v: C x kVB floats
@@ -171,10 +177,11 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
 // f[n] = X K^T for the C steps of a tile whose rows are steps, X the warp's columns k0
 // ... of the state, scaled; and with PO > 0 o[n] = X Q^T with PO parts of it.  The right
 // operands of a group of columns are loaded while the group before is multiplied.
-template <int NI, int PO, int DK, int NK, int NC>
+// given(k, a): the state's parts as left operands, as soon as there are any.
+template <int NI, int PO, int DK, int NK, int NC, typename F>
 __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
                                             const float (&x)[NK][4], const RowScales& s, uint32_t K,
-                                            uint32_t Q, int k0, const Lane<DK * 2>& at) {
+                                            uint32_t Q, int k0, const Lane<DK * 2>& at, F given) {
   constexpr int C = kSteps<NI>, RB = DK * 2;
   constexpr int GN = NC < 4 ? NC : 4;                     // columns of eight of a group
   constexpr int GF = NC / GN, GK = PO > 0 ? 2 * GF : GF;  // groups of 16 terms
@@ -190,8 +197,10 @@ __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4]
   for (int i = 0; i < NG; ++i) {
     const int k = i / GK, g = i % GK;
     if (i + 1 < NG) load(i + 1);
-    if (g == 0 && 2 * k + 2 < NK)
-      as_left<kParts>(a[(k + 1) & 1], x[2 * k + 2], x[2 * k + 3], s.up0, s.up1);
+    if (g == 0) {
+      given(k, a[k & 1]);
+      if (2 * k + 2 < NK) as_left<kParts>(a[(k + 1) & 1], x[2 * k + 2], x[2 * k + 3], s.up0, s.up1);
+    }
     if (g < GF) {
       if (k == 0) mma_parts0<kParts, NI, GN>(f + GN * g, a[0], b[i & 1]);
       else mma_parts<kParts, NI, GN>(f + GN * g, a[k & 1], b[i & 1]);
@@ -271,10 +280,103 @@ __device__ __forceinline__ void add_warps(float (&t)[NC][4], const float4* ex, i
   }
 }
 
+// Whether o is formed by four warps of their own.
 template <int NI, int DK, int WK, bool kStates>
-__global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const DeltaWalk p) {
+constexpr bool helped() {
+  return !kStates && WK == 1 && NI == 1 && DK == 128;
+}
+
+// What a walking warp hands to the warp that forms its o: PP parts of the state and
+// of U's blocks as left operands, with what their rows were multiplied by.
+template <int PP, typename G>
+struct Given {
+  uint8_t* at;
+  __device__ __forceinline__ uint4* state(int k, int q, int lane) const {
+    return (uint4*)(at + (k * PP + q) * 512) + lane;
+  }
+  __device__ __forceinline__ uint4* u(int k, int q, int lane) const {
+    return (uint4*)(at + G::kHS + (k * PP + q) * 512) + lane;
+  }
+  // of rows g and g + 8: the state's (0), those of U's block k (1 + k)
+  __device__ __forceinline__ float2* down(int k, int lane) const {
+    return (float2*)(at + G::kHS + G::kUS + k * 64) + (lane >> 2);
+  }
+  __device__ __forceinline__ void put(uint4* to, const uint32_t (&a)[4]) const {
+    *to = make_uint4(a[0], a[1], a[2], a[3]);
+  }
+};
+
+// o of a chunk, 16 columns of v: s e^g H q + s P U.
+template <int NI, int DK, int PP, typename G, typename T>
+__device__ __forceinline__ void form_o(const Given<PP, G>& x, int vg, uint32_t Q, uint32_t P,
+                                       const Gates<G::C>& g, T* out, long long out_step, int n, int v,
+                                       int dv, int lane) {
+  constexpr int C = G::C, NB = G::NB;
+  const Lane<G::RB> la(lane);
+  const Lane<G::PB> lm(lane);
+  const int c2 = (lane & 3) * 2;
+  auto scales = [&](int k) {
+    const float2 d = *x.down(k, lane);
+    return RowScales{0.f, d.x, 0.f, d.y};
+  };
+  auto fetch = [&](uint32_t (&a)[4], const uint4* from) {
+    const uint4 t = *from;
+    a[0] = t.x; a[1] = t.y; a[2] = t.z; a[3] = t.w;
+  };
+  float o[2 * NB][4];
+  zero(o);
+  bar(3 + vg, 64);
+#pragma unroll
+  for (int k = 0; k < DK / 16; ++k) {
+    uint32_t a[PP][4];
+#pragma unroll
+    for (int q = 0; q < PP; ++q) fetch(a[q], x.state(k, q, lane));
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      uint32_t r[NI][2][2];
+      load_right<NI, 2>(r, Q, C * G::RB, la, 16 * j, 16 * k);
+      mma_parts<PP, NI, 2>(o + 2 * j, a, r);
+    }
+  }
+  {
+    const RowScales s = scales(0);
+#pragma unroll
+    for (int j = 0; j < 2 * NB; ++j) {
+      scale_back(o[j], s);
+      times(o[j], *(const float2*)&g.lead[8 * j + c2]);
+    }
+  }
+  bar(3 + kWalkers + vg, 64);
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    uint32_t a[PP][4];
+    const RowScales s = scales(1 + k);
+#pragma unroll
+    for (int q = 0; q < PP; ++q) fetch(a[q], x.u(k, q, lane));
+#pragma unroll
+    for (int j = k; j < NB; ++j) {
+      uint32_t r[PP][2][2];
+      float d[2][4];
+      load_right<PP, 2>(r, P, C * G::PB, lm, 16 * j, 16 * k);
+      mma_parts0<PP, PP, 2>(d, a, r);
+      add_rows(o[2 * j], d[0], s);
+      add_rows(o[2 * j + 1], d[1], s);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * NB; ++j) {
+    times(o[j], *(const float2*)&g.qdown[8 * j + c2]);
+    put_steps<T>(o[j], out, out_step, 8 * j, n, v, dv, lane);
+  }
+}
+
+template <int NI, int DK, int WK, bool kStates>
+__global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kStates>() ? 2 : 1), 1)
+    k_delta_walk(const DeltaWalk p) {
   constexpr int PP = kOutParts<NI>;
-  using G = Geom<NI, DK, PP, WK, kStates ? 1 : 2>;
+  // o: formed by the preparing warps, or by the walking ones
+  constexpr bool kHelped = helped<NI, DK, WK, kStates>(), kOwn = !kStates && !kHelped;
+  using G = Geom<NI, DK, PP, WK, kStates ? 1 : 2, kHelped>;
   using T = typename std::conditional<NI == 1, __nv_bfloat16, float>::type;
   constexpr int C = G::C, NC = G::NC, NB = C / 16, NK = DK / 8 / WK, VB = kVB / WK;
   // blocks of 16 steps of o and E that a warp writes
@@ -298,7 +400,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
   float* err = kStates ? p.err + unit * chunks * C * p.dv + v0 : nullptr;
   auto stage = [&](int c) { return sm + c % G::NS * G::kStage; };  // Q, K, V
   if (warp < kPrep / 32) {
-    fewer_registers<kPrepRegs>();
+    fewer_registers<G::kPrepRegs>();
     const T* qp = (const T*)p.q.p + b * p.q.batch + (long long)(h / p.q.share) * p.dk;
     const T* kp = (const T*)p.k.p + b * p.k.batch + (long long)(h / p.k.share) * p.dk;
     const T* vp = (const T*)p.v.p + b * p.v.batch + (long long)h * p.dv + v0;
@@ -344,7 +446,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
         if (!kStates) q.write(st, tid, no_least, q_done);
       }
       bar(1, kPrep);
-      prepare<NI, DK, PP, !kStates>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
+      prepare<NI, DK, PP, !kStates, kHelped>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
                                     sm + G::kP + (c & 1) * G::PT, g, scratch, tid, [&] {
                                       scan_gates<C>(gates[(c + 1) % 3], raw, lane);
                                       load_raw(c + 2);
@@ -376,8 +478,20 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       }
       __syncthreads();
     }
+  } else if (kHelped && warp >= kPrep / 32 + kWalkers) {
+    fewer_registers<G::kPrepRegs>();
+    const int vg = warp % kWalkers, w0 = 16 * vg;
+    __syncthreads();
+    for (int c = 0; c < nc; ++c) {
+      if (w0 < width)
+        form_o<NI, DK, PP, G, T>({sm + G::kX + vg * G::kGiven}, vg, smem32(stage(c)),
+                                 smem32(sm + G::kP + (c & 1) * G::PT), gates[c % 3],
+                                 out + (long long)c * C * out_step + w0, out_step, min(C, len - c * C),
+                                 v0 + w0, p.dv, lane);
+      __syncthreads();
+    }
   } else {
-    more_registers<kWalkRegs>();
+    more_registers<G::kWalkRegs>();
     const int wi = warp - kPrep / 32, vg = wi / WK, kg = wi % WK;
     const int w0 = vg * 16;        // this warp's columns of v in the block
     const int k0 = kg * (DK / WK);  // and its columns of the state
@@ -387,6 +501,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
     const bool idle = w0 >= width;  // (fewer columns than warps for them)
     const Lane<G::RB> la(lane);
     const Lane<G::PB> lm(lane);
+    const Given<PP, G> given = {sm + G::kX + vg * G::kGiven};
     float x[NK][4];
     get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, k0, p.dk, lane);
     float2 most = row_max<NK>(x);
@@ -407,12 +522,20 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       float f[NC][4], o[2 * OB][4];
       const RowScales sx = row_scales(most);
       {
-        float qx[WK == 1 ? 2 * OB : NC][4];
-        state_times<NI, kStates ? 0 : PP, DK, NK, NC>(f, qx, x, sx, K, Q, k0, la);
+        float qx[NC][4];
+        state_times<NI, kOwn ? PP : 0, DK, NK, NC>(f, qx, x, sx, K, Q, k0, la,
+                                                   [&](int k, const uint32_t (&a)[kParts][4]) {
+          if constexpr (kHelped) {
+#pragma unroll
+            for (int q = 0; q < PP; ++q) given.put(given.state(k, q, lane), a[q]);
+            if (k == 0 && (lane & 3) == 0) *given.down(0, lane) = make_float2(sx.down0, sx.down1);
+            if (k == NK / 2 - 1) bar_arrive(3 + vg, 64);
+          }
+        });
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           scale_back(f[i], sx);
-          if (!kStates) scale_back(qx[i], sx);
+          if (kOwn) scale_back(qx[i], sx);
         }
         if constexpr (WK > 1) {
           float4* mine = ex + kg * NC * 32 + lane;
@@ -420,11 +543,11 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
             mine[i * 32] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
-            if (!kStates) mine[kO + i * 32] = make_float4(qx[i][0], qx[i][1], qx[i][2], qx[i][3]);
+            if (kOwn) mine[kO + i * 32] = make_float4(qx[i][0], qx[i][1], qx[i][2], qx[i][3]);
           }
           bar(3 + vg, 32 * WK);
           add_warps<WK, NC>(f, ex, kg, lane);
-          if constexpr (!kStates) {
+          if constexpr (kOwn) {
             zero(o);
             if (kg * OB < NB)
 #pragma unroll
@@ -435,7 +558,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
                   o[i][0] += t.x; o[i][1] += t.y; o[i][2] += t.z; o[i][3] += t.w;
                 }
           }
-        } else if constexpr (!kStates) {
+        } else if constexpr (kOwn) {
 #pragma unroll
           for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -475,94 +598,134 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
             set_pair(f[i + q], u, fma2(minus, pair(f[i + q], u), mul2(ku, pair(val[q], u))));
         }
       }
-      if constexpr (!kStates) {
+      if constexpr (kOwn) {
 #pragma unroll
-        for (int i = 0; i < 2 * OB; ++i) {
+        for (int i = 0; i < 2 * OB; ++i)
           times(o[i], *(const float2*)&g.lead[(WK == 1 ? 0 : min(kg * OB, NB - OB) * 16) + 8 * i + c2]);
-        }
       }
-      // block by block: E = F - X beta F, U = beta E, and what U takes off F of the
-      // later blocks and adds to O.  The next block waits for its own share alone; the
-      // rest is issued while the next one's first product is on its way.
-      uint32_t au[kParts][4];
-      RowScales su;
-      auto add_scaled = [&](float (*to)[4], const float (&d)[2][4]) {
-        add_rows(to[0], d[0], su);
-        add_rows(to[1], d[1], su);
-      };
-      auto rest = [&](int k) {
+      if constexpr (kHelped) {
+        // block by block, with y = beta F: E = F - X y, U = beta E, and y takes off F of the
+        // later blocks what their rows of L T say.  The next block waits for its own share
+        // alone; all else is beside the chain.
 #pragma unroll
-        for (int i = 2 * k + 4; i < NC; i += 2) {
-          uint32_t r[kParts][2][2];
-          float d[2][4];
-          load_right<kParts, 2>(r, M, C * G::PB, lm, 8 * i, 16 * k);
-          mma_short(d, au, r);
-          add_scaled(f + i, d);
+        for (int k = 0; k < NB; ++k) {
+          uint32_t a[kParts][4], r[kParts][2][2];
+          float d[2][4], y[2][4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float2 bx = *(const float2*)&g.bx[16 * k + 8 * q + c2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), bx));
+          }
+          const RowScales sy = row_scales(row_max<2>(y));
+          as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
+#pragma unroll
+          for (int i = 2 * k + 2; i < NC; i += 2) {
+            load_right<kParts, 2>(r, M, C * G::PB, lm, 8 * i, 16 * k);
+            mma_short(d, a, r);
+            add_rows(f[i], d[0], sy);
+            add_rows(f[i + 1], d[1], sy);
+          }
+          load_right_t<kParts, 2>(r, M, C * G::PB, lm, 16 * k, 16 * k);
+          mma_short(d, a, r);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int at = 16 * k + 8 * q + c2;
+            add_rows(f[2 * k + q], d[q], sy);
+            times(f[2 * k + q], *(const float2*)&g.beta[at]);
+          }
+          uint32_t ao[PP][4];  // U for o
+          const RowScales su = row_scales(row_max<2>(f + 2 * k));
+          as_left<PP>(ao, f[2 * k], f[2 * k + 1], su.up0, su.up1);
+#pragma unroll
+          for (int q = 0; q < PP; ++q) given.put(given.u(k, q, lane), ao[q]);
+          if ((lane & 3) == 0) *given.down(1 + k, lane) = make_float2(su.down0, su.down1);
         }
-        if constexpr (!kStates) {
-          uint32_t ao[PP][4];
+        bar_arrive(3 + kWalkers + vg, 64);
+      } else {
+        // block by block: E = F - X beta F, U = beta E, and what U takes off F of the
+        // later blocks and adds to O.  The next block waits for its own share alone; the
+        // rest is issued while the next one's first product is on its way.
+        uint32_t au[kParts][4];
+        RowScales su;
+        auto add_scaled = [&](float (*to)[4], const float (&d)[2][4]) {
+          add_rows(to[0], d[0], su);
+          add_rows(to[1], d[1], su);
+        };
+        auto rest = [&](int k) {
 #pragma unroll
-          for (int q = 0; q < PP; ++q)
+          for (int i = 2 * k + 4; i < NC; i += 2) {
+            uint32_t r[kParts][2][2];
+            float d[2][4];
+            load_right<kParts, 2>(r, M, C * G::PB, lm, 8 * i, 16 * k);
+            mma_short(d, au, r);
+            add_scaled(f + i, d);
+          }
+          if constexpr (kOwn) {
+            uint32_t ao[PP][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ao[q][e] = au[q][e];
+            for (int q = 0; q < PP; ++q)
 #pragma unroll
-          for (int j = 0; j < OB; ++j) {
-            const int i = WK == 1 ? j : kg * OB + j;  // block
-            if (i >= k && (WK == 1 || i < NB)) {
-              uint32_t rp[PP][2][2];
-              float d[2][4];
-              load_right<PP, 2>(rp, P, C * G::PB, lm, 16 * i, 16 * k);
-              mma_parts0<PP, PP, 2>(d, ao, rp);
-              add_scaled(o + 2 * j, d);
+              for (int e = 0; e < 4; ++e) ao[q][e] = au[q][e];
+#pragma unroll
+            for (int j = 0; j < OB; ++j) {
+              const int i = WK == 1 ? j : kg * OB + j;  // block
+              if (i >= k && (WK == 1 || i < NB)) {
+                uint32_t rp[PP][2][2];
+                float d[2][4];
+                load_right<PP, 2>(rp, P, C * G::PB, lm, 16 * i, 16 * k);
+                mma_parts0<PP, PP, 2>(d, ao, rp);
+                add_scaled(o + 2 * j, d);
+              }
             }
           }
-        }
-      };
+        };
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        uint32_t a[kParts][4], r[kParts][2][2];
-        float d[2][4], y[2][4];
-        load_right_t<kParts, 2>(r, M, C * G::PB, lm, 16 * k, 16 * k);
+        for (int k = 0; k < NB; ++k) {
+          uint32_t a[kParts][4], r[kParts][2][2];
+          float d[2][4], y[2][4];
+          load_right_t<kParts, 2>(r, M, C * G::PB, lm, 16 * k, 16 * k);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int at = 16 * k + 8 * q + c2;
-          const float2 bx = *(const float2*)&g.bx[at];
+          for (int q = 0; q < 2; ++q) {
+            const int at = 16 * k + 8 * q + c2;
+            const float2 bx = *(const float2*)&g.bx[at];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), bx));
-        }
-        const RowScales sy = row_scales(row_max<2>(y));
-        as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
-        mma_short(d, a, r);
-        if (k > 0) rest(k - 1);
+            for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), bx));
+          }
+          const RowScales sy = row_scales(row_max<2>(y));
+          as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
+          mma_short(d, a, r);
+          if (k > 0) rest(k - 1);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int at = 16 * k + 8 * q + c2;
-          const float2 be = *(const float2*)&g.beta[at];
-          add_rows(f[2 * k + q], d[q], sy);
-          if (kStates)
+          for (int q = 0; q < 2; ++q) {
+            const int at = 16 * k + 8 * q + c2;
+            const float2 be = *(const float2*)&g.beta[at];
+            add_rows(f[2 * k + q], d[q], sy);
+            if (kStates)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[q][e] = f[2 * k + q][e];
-          times(f[2 * k + q], be);
-          if constexpr (kStates) {
-            const float2 ku = *(const float2*)&g.kup[at];
-            float* ep = err + (long long)c * C * p.dv;
-            if (owns(k))
+              for (int e = 0; e < 4; ++e) d[q][e] = f[2 * k + q][e];
+            times(f[2 * k + q], be);
+            if constexpr (kStates) {
+              const float2 ku = *(const float2*)&g.kup[at];
+              float* ep = err + (long long)c * C * p.dv;
+              if (owns(k))
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = at + (e & 1), vv = w0 + (lane >> 2) + 8 * (e >> 1);
-                if (vv < width) ep[(long long)i * p.dv + vv] = d[q][e] * inverse_pow2(e & 1 ? ku.y : ku.x);
-              }
+                for (int e = 0; e < 4; ++e) {
+                  const int i = at + (e & 1), vv = w0 + (lane >> 2) + 8 * (e >> 1);
+                  if (vv < width) ep[(long long)i * p.dv + vv] = d[q][e] * inverse_pow2(e & 1 ? ku.y : ku.x);
+                }
+            }
+          }
+          su = row_scales(row_max<2>(f + 2 * k));
+          as_left<kParts>(au, f[2 * k], f[2 * k + 1], su.up0, su.up1);
+          if (k + 1 < NB) {
+            load_right<kParts, 2>(r, M, C * G::PB, lm, 16 * k + 16, 16 * k);
+            mma_short(d, au, r);
+            add_scaled(f + 2 * k + 2, d);
           }
         }
-        su = row_scales(row_max<2>(f + 2 * k));
-        as_left<kParts>(au, f[2 * k], f[2 * k + 1], su.up0, su.up1);
-        if (k + 1 < NB) {
-          load_right<kParts, 2>(r, M, C * G::PB, lm, 16 * k + 16, 16 * k);
-          mma_short(d, au, r);
-          add_scaled(f + 2 * k + 2, d);
-        }
+        rest(NB - 1);
       }
-      rest(NB - 1);
       uint32_t y[NB][kParts][4];
 #pragma unroll
       for (int i = 0; i < NC; ++i) times(f[i], *(const float2*)&g.tail[8 * i + c2]);
@@ -571,7 +734,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_walk(const D
       for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
       constexpr int kGroups = NK < 4 ? 1 : NK / 4;
       most = state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, la, [&](int i) {
-        if constexpr (!kStates) {  // o's columns, shared out over the products
+        if constexpr (kOwn) {  // o's columns, shared out over the products
           constexpr int per = (2 * OB + kGroups - 1) / kGroups;
 #pragma unroll
           for (int j = 0; j < per; ++j) {
@@ -621,7 +784,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
   float* ys = p.y + unit * chunks * C * p.dv + v0;
   auto stage = [&](int c) { return sm + c % G::NS * G::kStage; };  // Q, K, dO
   if (warp < kPrep / 32) {
-    fewer_registers<kPrepRegs>();
+    fewer_registers<G::kPrepRegs>();
     const T* qp = (const T*)p.q.p + b * p.q.batch + (long long)(h / p.q.share) * p.dk;
     const T* kp = (const T*)p.k.p + b * p.k.batch + (long long)(h / p.k.share) * p.dk;
     const T* gp = (const T*)p.dout.p + b * p.dout.batch + (long long)h * p.dv + v0;
@@ -716,7 +879,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
           for (int k = 0; k < NI; ++k) *(uint2*)(to + k * C * kVB * 2) = make_uint2(q[0][k], q[1][k]);
         }
       }
-      prepare<NI, DK, kParts, true>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
+      prepare<NI, DK, kParts, true, false>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
                                     sm + G::kP + (c & 1) * G::PT, g, scratch, tid, [&] {
                                       scan_gates<C>(gates[(c + 2) % 3], raw, lane);  // (c - 1)
                                       load_raw(c - 2);
@@ -748,7 +911,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       __syncthreads();
     }
   } else {
-    more_registers<kWalkRegs>();
+    more_registers<G::kWalkRegs>();
     const int wi = warp - kPrep / 32, vg = wi / WK, kg = wi % WK;
     const int w0 = vg * 16, k0 = kg * (DK / WK);
     const int v = v0 + w0 + (lane >> 2), c2 = (lane & 3) * 2;
@@ -775,7 +938,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       float f[NC][4];  // dU^T, then dv^T
       {
         const RowScales sx = row_scales(most);
-        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, la);
+        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, la,
+                                        [](int, const uint32_t (&)[kParts][4]) {});
 #pragma unroll
         for (int i = 0; i < NC; ++i) scale_back(f[i], sx);
         if constexpr (WK > 1) {
@@ -922,29 +1086,30 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
 
 // CTAs of a walk
 dim3 walk_grid(int H, int B, int dv, int wk) { return dim3(H * ((dv + kVB / wk - 1) / (kVB / wk)), B); }
-constexpr int kThreads = kPrep + 32 * kWalkers;
 
 template <int NI, int DK, int WK, bool kStates>
 cudaError_t walk_t(const DeltaWalk& p, cudaStream_t s) {
-  constexpr size_t smem = Geom<NI, DK, kOutParts<NI>, WK, kStates ? 1 : 2>::smem;
+  using G = Geom<NI, DK, kOutParts<NI>, WK, kStates ? 1 : 2, helped<NI, DK, WK, kStates>()>;
+  constexpr size_t smem = G::smem;
   static_assert(smem <= 232448, "");
   const cudaError_t e = cudaFuncSetAttribute(k_delta_walk<NI, DK, WK, kStates>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls(kStates ? "delta_states" : "delta_walk", s);
   k_delta_walk<NI, DK, WK, kStates>
-      <<<walk_grid(p.H, p.B, p.dv, WK), kThreads, smem, s>>>(p);
+      <<<walk_grid(p.H, p.B, p.dv, WK), G::kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 template <int NI, int DK, int WK>
 cudaError_t back_t(const DeltaBack& p, cudaStream_t s) {
-  constexpr size_t smem = Geom<NI, DK, kParts, WK, 1>::smem;
+  using G = Geom<NI, DK, kParts, WK, 1>;
+  constexpr size_t smem = G::smem;
   static_assert(smem <= 232448, "");
   const cudaError_t e = cudaFuncSetAttribute(k_delta_back<NI, DK, WK>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls("delta_back", s);
-  k_delta_back<NI, DK, WK><<<walk_grid(p.H, p.B, p.dv, WK), kThreads, smem, s>>>(p);
+  k_delta_back<NI, DK, WK><<<walk_grid(p.H, p.B, p.dv, WK), G::kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 

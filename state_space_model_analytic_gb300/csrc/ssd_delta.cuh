@@ -305,6 +305,9 @@ __device__ __forceinline__ void fewer_registers() {
 __device__ __forceinline__ void bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 // ---- a chunk's tiles ------------------------------------------------------------
 
@@ -550,6 +553,7 @@ constexpr int kDiag = 20;  // floats of a column of a diagonal block
 template <int C>
 struct alignas(16) Scratch {
   float diag[C / 16][16][kDiag];  // L[i][j] at [j][i], a warp each
+  uint8_t t[C / 16][kParts * 512];  // T of the diagonal blocks, transposed like X, in parts
   float most[kPrep / 32];
 };
 
@@ -619,17 +623,20 @@ __device__ __forceinline__ void score_block(uint32_t Q, uint32_t K, uint8_t* M, 
 
 // Lanes 0 - 15, a column j each of diagonal block s: with T = (I + beta L)^-1, X = L T
 // and T = I - beta X, so once X_mj is whole, T_mj = -beta_m X_mj (1 for m = j) adds
-// L_im T_mj to every later X_ij.
-template <int C>
-__device__ __forceinline__ void invert_diag(uint8_t* out, Gates<C>& g, const float (*diag)[kDiag],
-                                            int s, int j) {
+// L_im T_mj to every later X_ij.  kT: T to `tt` too, its columns scaled like X's, by
+// the larger of both.
+template <int C, bool kT>
+__device__ __forceinline__ void invert_diag(uint8_t* out, uint8_t* tt, Gates<C>& g,
+                                            const float (*diag)[kDiag], int s, int j) {
   constexpr int OB = C * 2;
-  float x[16];
+  float x[16], tm[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = 0.f;
 #pragma unroll
-  for (int m = 0; m < 15; ++m) {
+  for (int m = 0; m < (kT ? 16 : 15); ++m) {
     const float t = m == j ? 1.f : -g.beta[16 * s + m] * x[m];
+    tm[m] = t;
+    if (m == 15) break;
 #pragma unroll
     for (int i = (m + 1) / 4 * 4; i < 16; i += 4) {
       const float4 l = *(const float4*)&diag[m][i];
@@ -642,7 +649,11 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, Gates<C>& g, const flo
   float m = 0.f;
 #pragma unroll
   for (int i = 1; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
-  const Scale sx = scale_to<8>(m);
+  // (an element of L is at most 2^9, so one of L T, scaled, at most 2^15)
+  if (kT)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(tm[i]));
+  const Scale sx = scale_to<kT ? 1 : 8>(m);
   g.xs[16 * s + j] = sx.down;
   g.bx[16 * s + j] = sx.down * g.beta[16 * s + j];
 #pragma unroll
@@ -655,7 +666,40 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, Gates<C>& g, const flo
 #pragma unroll
     for (int q = 0; q < kParts; ++q)
       *(uint4*)(at + q * C * OB) = make_uint4(p[0][q], p[1][q], p[2][q], p[3][q]);
+    if constexpr (kT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        split2<kParts>(tm[8 * h + 2 * i] * sx.up, tm[8 * h + 2 * i + 1] * sx.up, p[i]);
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+        *(uint4*)(tt + q * 512 + at16<32>(j, h)) = make_uint4(p[0][q], p[1][q], p[2][q], p[3][q]);
+    }
   }
+}
+
+// A block of M below the diagonal, rows 16 bi ..., columns 16 bj ...: -L T in the place
+// of -L.
+template <int C>
+__device__ __forceinline__ void fold_block(uint8_t* M, const uint8_t* tt, int bi, int bj, int lane) {
+  constexpr int OB = C * 2;
+  const Lane<OB> at(lane);
+  const Lane<32> t(lane);
+  uint32_t a[kParts][4], b[kParts][2][2];
+  float d[2][4];
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) ldm4(a[q], at.left(smem32(M), 16 * bi, 16 * bj) + q * C * OB);
+  load_right<kParts, 2>(b, smem32(tt), 512, t, 0, 0);
+  mma_parts0<kParts, kParts, 2>(d, a, b);
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t p[kParts];
+      split2<kParts>(pair(d[n], u), p);
+      uint8_t* to = M + at16<OB>(16 * bi + (lane >> 2) + 8 * u, 2 * bj + n) + (lane & 3) * 4;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) *(uint32_t*)(to + q * C * OB) = p[q];
+    }
 }
 
 // M and, with kP, P of a chunk whose operands and gates are in shared memory, by the
@@ -664,25 +708,32 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, Gates<C>& g, const flo
 // a warp known at compile time, the warps' code and the walk's did not fit the
 // instruction caches together, and waiting for instructions was the largest of all
 // stalls.)  The last warp has `aside` to do as well (the gates of a later chunk).
-template <int NI, int DK, int PP, bool kP, typename F>
+template <int NI, int DK, int PP, bool kP, bool kFold, typename F>
 __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, uint8_t* M, uint8_t* P,
                                         Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc, int tid,
                                         F aside) {
   constexpr int C = kSteps<NI>, NB = C / 16, W = kPrep / 32 - NB;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t K = smem32(Kt), Q = smem32(Qt);
+  // rows and columns (hexadecimal digits, the first last)
+  constexpr uint32_t kI = NB == 4 ? 0x333221 : 0x1, kJ = NB == 4 ? 0x210100 : 0x0;
   if (warp < NB) {
     score_block<NI, DK, PP, kP, true>(Q, K, M, P, g, sc.diag[warp], warp, warp, lane);
     __syncwarp();
-    if (lane < 16) invert_diag<C>(M, g, sc.diag[warp], warp, lane);
+    if (lane < 16) invert_diag<C, kFold>(M, sc.t[warp], g, sc.diag[warp], warp, lane);
     __syncwarp();
   } else {
-    // rows and columns (hexadecimal digits, the first last)
-    constexpr uint32_t kI = NB == 4 ? 0x333221 : 0x1, kJ = NB == 4 ? 0x210100 : 0x0;
 #pragma unroll 1
     for (int r = warp - NB; r < NB * (NB - 1) / 2; r += W)
       score_block<NI, DK, PP, kP, false>(Q, K, M, P, g, nullptr, kI >> 4 * r & 15, kJ >> 4 * r & 15, lane);
     if (warp == kPrep / 32 - 1) aside();
+  }
+  if constexpr (kFold) {
+    bar(2, kPrep);
+    if (warp < NB * (NB - 1) / 2) {
+      const int bj = kJ >> 4 * warp & 15;
+      fold_block<C>(M, sc.t[bj], kI >> 4 * warp & 15, bj, lane);
+    }
   }
 }
 

@@ -127,6 +127,33 @@ def test_write_strengths_of_any_sign():
         check(host(g[n]), ref[n], size[n], 150)
 
 
+@pytest.mark.parametrize("strengths", [(0.0, -0.1, 2.0, 1.0), (1.0, 1.0, 1.0, 40.0)],
+                         ids=["signs", "once_large"])
+def test_alike_keys_of_many_heads(strengths):
+    """Keys that hardly differ, 160 (row, head) pairs of 128 columns; the last strength
+    of a head in one step alone, which multiplies the memory by 1 - 40.
+
+    o = e^g H q + P U takes H, P and U in 11 bits: H off by 2^-12, a term of P U by twice
+    that, and the reference's size is |q| times the sum of the terms' magnitudes, so o is
+    off by 2^-11 size at most.  (Where one or two terms are most of the sum, as here the
+    steps 75 and 76, 40 times the others and of opposite sign, nothing averages out.)"""
+    import state_space_model_analytic_gb300 as ssd
+    B, T, H, K = 2, 130, 80, 128
+    inp = synth.delta_inputs(B, T, H, H, K, 32, "bf16", 71)
+    k = 1.0 + 0.05 * inp["k"]
+    inp["k"] = synth.round_to(k / np.sqrt((k * k).sum(-1, keepdims=True)), "bf16")
+    be = np.ones_like(inp["beta"])
+    be[:, :, 0::2], be[:, :, 1::2] = strengths[0], strengths[1]
+    be[:, ::3, 1::2] = strengths[2]
+    be[:, 75] = strengths[3]
+    inp["beta"] = be
+    x, s0 = operands(inp, "bf16"), dev(inp["state0"])
+    o, S = ssd.delta_rule_forward(*x, s0)
+    ro, rS, mo, mS = delta.forward(*(inp[n] for n in NAMES), inp["state0"])
+    check(host(o), ro, mo, T, 2.0 ** -8, 2.0 ** -11)
+    check(host(S), rS, mS, T)
+
+
 def test_operands_shared_by_all_rows_are_refused():
     """Views whose rows are the same memory (a batch stride of zero)."""
     import state_space_model_analytic_gb300 as ssd

@@ -95,7 +95,7 @@ __device__ __forceinline__ void get_state(float (&x)[NK][4], const float* p, int
     }
 }
 template <int NK>
-__device__ __forceinline__ void put_state(const float (&x)[NK][4], float* p, int v, int dv, int k0,
+__device__ __forceinline__ void put_state(const float (*x)[4], float* p, int v, int dv, int k0,
                                           int dk, int lane) {
   const int c = k0 + (lane & 3) * 2;
 #pragma unroll
@@ -177,7 +177,8 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
 // f[n] = X K^T for the C steps of a tile whose rows are steps, X the warp's columns k0
 // ... of the state, scaled; and with PO > 0 o[n] = X Q^T with PO parts of it.  The right
 // operands of a group of columns are loaded while the group before is multiplied.
-// given(k, a): the state's parts as left operands, as soon as there are any.
+// given(k, a): the state's parts as left operands of columns 16 k ..., as soon as there
+// are any.
 template <int NI, int PO, int DK, int NK, int NC, typename F>
 __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
                                             const float (&x)[NK][4], const RowScales& s, uint32_t K,
@@ -233,31 +234,40 @@ __device__ __forceinline__ void mma_short(float (&d)[2][4], const uint32_t (&a)[
     for (int u = 0; u < 2; ++u) set_pair(d[n], u, add2(pair(d[n], u), pair(e[n], u)));
 }
 
-// x <- scale x + Y tile, Y (rows v, C steps) as parts of left operands that were scaled
-// by s; x: columns k0 ... of the state.  Returns the largest values of the lane's rows.
-// beside(i), i < ceil(NK / 4): work that is issued between the products.
+// x <- scale x + Y tile for columns n, GN eights of them, Y (rows v, C steps) as parts of
+// left operands that were scaled by s; x: columns k0 ... of the state.  beside(): work
+// that is issued between the products.
+template <int NI, int DK, int GN, int NB, typename F>
+__device__ __forceinline__ void columns_add(float (*x)[4], float scale, const uint32_t (*y)[kParts][4],
+                                            const RowScales& s, uint32_t tile, int n, const Lane<DK * 2>& at,
+                                            F beside) {
+  constexpr int C = kSteps<NI>, RB = DK * 2;
+  float d[GN][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    uint32_t r[NI][GN][2];
+    load_right_t<NI, GN>(r, tile, C * RB, at, n, 16 * b);
+    if (b == 0) mma_parts0<kParts, NI, GN>(d, y[b], r);
+    else mma_parts<kParts, NI, GN>(d, y[b], r);
+    if (b == 0) beside();
+  }
+#pragma unroll
+  for (int i = 0; i < GN; ++i) {
+    times(x[i], both(scale));
+    add_rows(x[i], d[i], s);
+  }
+}
+// The same for all columns, beside(i) beside group i of ceil(NK / 4).  Returns the
+// largest values of the lane's rows.
 template <int NI, int DK, int NK, int NB, typename F>
 __device__ __forceinline__ float2 state_add(float (&x)[NK][4], float scale, const uint32_t (*y)[kParts][4],
                                             const RowScales& s, uint32_t tile, int k0, const Lane<DK * 2>& at,
                                             F beside) {
-  constexpr int C = kSteps<NI>, RB = DK * 2, GN = NK < 4 ? NK : 4;
+  constexpr int GN = NK < 4 ? NK : 4;
   float2 m = make_float2(0.f, 0.f);
 #pragma unroll
   for (int n = 0; n < NK; n += GN) {
-    float d[GN][4];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      uint32_t r[NI][GN][2];
-      load_right_t<NI, GN>(r, tile, C * RB, at, k0 + 8 * n, 16 * b);
-      if (b == 0) mma_parts0<kParts, NI, GN>(d, y[b], r);
-      else mma_parts<kParts, NI, GN>(d, y[b], r);
-      if (b == 0) beside(n / GN);
-    }
-#pragma unroll
-    for (int i = 0; i < GN; ++i) {
-      times(x[n + i], both(scale));
-      add_rows(x[n + i], d[i], s);
-    }
+    columns_add<NI, DK, GN, NB>(x + n, scale, y, s, tile, k0 + 8 * n, at, [&] { beside(n / GN); });
     m = row_max<GN>(x + n, m);
   }
   return m;
@@ -516,7 +526,6 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
       const uint32_t M = smem32(sm + G::kM + (c & 1) * G::MT), P = smem32(sm + G::kP + (c & 1) * G::PT);
       const Gates<C>& g = gates[c % 3];
       const int n = min(C, len - c * C);
-      if (kStates) put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, k0, p.dk, lane);
       // f: F^T, then U^T.  o: O^T of the blocks that this warp writes, without s and of
       // q's scale
       float f[NC][4], o[2 * OB][4];
@@ -531,6 +540,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
             if (k == 0 && (lane & 3) == 0) *given.down(0, lane) = make_float2(sx.down0, sx.down1);
             if (k == NK / 2 - 1) bar_arrive(3 + vg, 64);
           }
+          if constexpr (kStates)
+            put_state<2>(x + 2 * k, hist + (long long)c * p.dv * p.dk, v, p.dv, k0 + 16 * k, p.dk, lane);
         });
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -934,12 +945,14 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       const uint32_t M = smem32(sm + G::kM + (c & 1) * G::MT), P = smem32(sm + G::kP + (c & 1) * G::PT);
       const Gates<C>& g = gates[c % 3];
       const int n = min(C, len - c * C);
-      put_state<NK>(x, hist + (long long)c * p.dv * p.dk, v, p.dv, k0, p.dk, lane);
       float f[NC][4];  // dU^T, then dv^T
       {
         const RowScales sx = row_scales(most);
-        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, la,
-                                        [](int, const uint32_t (&)[kParts][4]) {});
+        // (the state is stored between the products: all at once the warp waited 1400
+        // cycles for its own stores)
+        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, la, [&](int k, const uint32_t (&)[kParts][4]) {
+          put_state<2>(x + 2 * k, hist + (long long)c * p.dv * p.dk, v, p.dv, k0 + 16 * k, p.dk, lane);
+        });
 #pragma unroll
         for (int i = 0; i < NC; ++i) scale_back(f[i], sx);
         if constexpr (WK > 1) {
@@ -976,6 +989,40 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
           for (int u = 0; u < 2; ++u)
             set_pair(f[2 * k + q], u, fma2(both(so), pair(d[q], u), pair(f[2 * k + q], u)));
       };
+      // what dO adds to D waits for nothing of this chunk: its products go between the
+      // steps of the solution, each of which waits for the one before
+      uint32_t zo[NB][kParts][4];
+      RowScales sz;
+      {
+        float z[NC][4];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          uint32_t a[NI][4];
+          dout_left(a, k);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            float2 s = unpack_half(a[0][w]);
+            if (NI == 2) {
+              const float2 t = unpack_half(a[NI - 1][w]);
+              s.x += t.x;
+              s.y += t.y;
+            }
+            // registers 0, 1: rows g, g + 8 of the first eight steps; 2, 3: of the others
+            const float2 l = *(const float2*)&g.lead[16 * k + 8 * (w >> 1) + c2];
+            z[2 * k + (w >> 1)][2 * (w & 1)] = s.x * so * l.x;
+            z[2 * k + (w >> 1)][2 * (w & 1) + 1] = s.y * so * l.y;
+          }
+        }
+        sz = row_scales(row_max<NC>(z));
+#pragma unroll
+        for (int k = 0; k < NB; ++k) as_left<kParts>(zo[k], z[2 * k], z[2 * k + 1], sz.up0, sz.up1);
+      }
+      constexpr int GN = NK < 4 ? NK : 4, kGroups = NK / GN, kPer = (kGroups + NB - 1) / NB;
+      auto add_out = [&](int k) {
+#pragma unroll
+        for (int i = k * kPer; i < (k + 1) * kPer && i < kGroups; ++i)
+          columns_add<NI, DK, GN, NB>(x + i * GN, g.last, zo, sz, Q, k0 + 8 * GN * i, la, [] {});
+      };
       // from the last block back: y = dU - X^T beta dU, dv = beta y, and what dv takes
       // off dU of the earlier blocks (the order of issue as in the walk)
       uint32_t av[kParts][4];
@@ -1011,6 +1058,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         mma_short(d, a, r);
         if (k + 1 < NB) rest(k + 1);
         if (k > 0) from_out(k - 1);
+        add_out(k);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int at = 16 * k + 8 * q + c2;
@@ -1053,30 +1101,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         const RowScales sw = row_scales(row_max<NC>(f));
 #pragma unroll
         for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
-        state_add<NI, DK, NK, NB>(x, g.last, y, sw, K, k0, la, [](int) {});
+        most = state_add<NI, DK, NK, NB>(x, 1.f, y, sw, K, k0, la, [](int) {});
       }
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        uint32_t a[NI][4];
-        dout_left(a, k);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          float2 s = unpack_half(a[0][w]);
-          if (NI == 2) {
-            const float2 t = unpack_half(a[NI - 1][w]);
-            s.x += t.x;
-            s.y += t.y;
-          }
-          // registers 0, 1: rows g, g + 8 of the first eight steps; 2, 3: of the others
-          const float2 l = *(const float2*)&g.lead[16 * k + 8 * (w >> 1) + c2];
-          f[2 * k + (w >> 1)][2 * (w & 1)] = s.x * so * l.x;
-          f[2 * k + (w >> 1)][2 * (w & 1) + 1] = s.y * so * l.y;
-        }
-      }
-      const RowScales sw = row_scales(row_max<NC>(f));
-#pragma unroll
-      for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
-      most = state_add<NI, DK, NK, NB>(x, 1.f, y, sw, Q, k0, la, [](int) {});
       __syncthreads();
     }
     if (p.last) put_state<NK>(x, p.last + unit * p.dv * p.dk, v, p.dv, k0, p.dk, lane);

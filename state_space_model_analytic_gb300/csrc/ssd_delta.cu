@@ -19,6 +19,12 @@
 // Where rows are few, WK = 2 or 4 warps share 16 rows of the state, a part of dk each:
 // the products with the state are split, F's parts added up through shared memory, and
 // the solution of the triangular system, which all of them need, is found by each.
+//
+// Bound by that chain: at 4 x 2048 steps of 32 heads 128/64 (bf16, 153 us; memory alone
+// would take 31) a chunk of 64 steps takes 8.8 thousand cycles, 2.2 of them the products
+// with the state, 3.4 the system, 1.7 the new state, with the tensor pipe 42 % and the
+// issue slots 45 % busy.  The walk that keeps the states takes 140 us, the walk back 226.
+// fp32 (8 x 1024 steps of 24 heads 64/64): 155 us.
 #include <cuda_bf16.h>
 
 #include "ssd_delta.cuh"
@@ -290,7 +296,13 @@ __device__ __forceinline__ void add_warps(float (&t)[NC][4], const float4* ex, i
   }
 }
 
-// Whether o is formed by four warps of their own.
+// Whether o is formed by four warps of their own: the walking ones hand them the state and
+// U as they have them for their own products.  4 x 2048 steps of 32 heads 128/64: 153 us
+// against 173; at 64/64 there is less to take over and the four need their issue slots (16
+// rows of 1003, 24 heads: 140 against 135), in fp32 what is handed over is twice as long (188
+// against 155), and with WK > 1 the preparation is what takes longest.  Where they are, the
+// preparing warps have time to multiply the rows of later blocks by the inverse of the
+// earlier ones as well, and the chain has one product a block less (160 without).
 template <int NI, int DK, int WK, bool kStates>
 constexpr bool helped() {
   return !kStates && WK == 1 && NI == 1 && DK == 128;
@@ -1139,9 +1151,13 @@ cudaError_t back_t(const DeltaBack& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Warps that share 16 columns of v.
+// Warps that share 16 columns of v: as many as leave every CTA an SM of its own.  Below
+// that the shared rows' shorter chain gains, above it the second wave costs more (us of the
+// walk that keeps the states, one, two, four warps; CTAs with one):
+//   1 x 4096, 32 heads 128/64 (32): 322 260 235    2 x 2048, 32 heads 128/64 (64): 166 137 244
+//   1 x 4096, 16 heads 64/64 (16): 209 194 186     2 x 2048, 24 heads 64/64 (48): 109 101 189
+//   3 x 2048, 32 heads 128/64 (96): 169 266 365    8 x 1024, 24 heads 64/64 (192): 116 158 291
 int warps_per_rows(int B, int H, int dv) {
-  // one CTA an SM: as many as leave every CTA a SM of its own
   for (int wk = 4; wk > 1; wk /= 2) {
     const dim3 g = walk_grid(H, B, dv, wk);
     if ((long long)g.x * g.y <= kLaSms) return wk;
@@ -1167,7 +1183,9 @@ cudaError_t back_k(const DeltaBack& p, cudaStream_t s) {
 // are added up together (while a lane holds several sums, each exchange halves
 // them), as are those with q.  o needs no second pass: S' q = A q + beta e (k . q).
 //
-// Bound by the states' bytes, read and written once.
+// Bound by the states' bytes, read and written once: 256 rows of 64 heads 128/64 take 160
+// us, the copy rate.  Eight rows a lane where that leaves two CTAs an SM, else two, so that
+// a single row (32 heads 128/64: 6.7 us) is on 256 CTAs.
 constexpr int kStepWarps = 4;
 
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {

@@ -21,6 +21,13 @@
 // while this one is multiplied, E, y and dO of the next chunk while MP and ML are; K and
 // Q come during the first products, which need neither.  Heads that share q and k
 // write their own gradients in fp32, summed in head order by a second kernel.
+//
+// 4 x 2048 steps of 32 heads 128/64 (bf16): 388 us for 4096 items of 27 thousand cycles,
+// where the 709 MB it reads and writes take 106.  Of an item the splitting takes 6 thousand
+// cycles, the products with H and D 6 (tensor pipe and shared memory), the scores and masks
+// 4, the products with MP and ML 4.5, loads and barriers the rest.  Two CTAs an SM with
+// half the columns each: 510 us against 423, since both take E, y and dO apart; one
+// CTA an item instead of persistent ones: 543.
 #include <cuda_bf16.h>
 
 #include "persistent_grid.h"

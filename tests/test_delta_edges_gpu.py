@@ -15,6 +15,13 @@ from test_parity_delta_gpu import NAMES, _built, check, dev, host, on_device, op
 pytestmark = pytest.mark.gpu
 
 
+# o = e^g H q + P U takes H, P and U in 11 bits where it is bf16: H off by 2^-12, a term of
+# P U by twice that, and the reference's size is |q| times the sum of the terms'
+# magnitudes, so o is off by 2^-11 size at most.  (With many terms of any sign it is far
+# less: 2^-15 where keys are long.)
+O_OF_SIZE = 2.0 ** -11
+
+
 # B, T, H, G, K, V, dtype, lens: CTAs of 64, 32 or 16 columns of v, as many warps a row
 SHARES = [
     (2, 100, 36, 4, 128, 64, "bf16", None),              # 144 CTAs with two warps a row
@@ -24,6 +31,10 @@ SHARES = [
     (4, 100, 40, 8, 128, 24, "bf16", None),              # and warps without columns
     (4, 70, 40, 40, 64, 24, "f32", (0, 70, 32, 33)),
     (3, 40, 60, 20, 128, 64, "f32", None),
+    # rows of any length in any order, as many as are put in order and more
+    (256, 40, 1, 1, 16, 8, "bf16", tuple(i * 7 % 41 for i in range(256))),
+    (300, 40, 1, 1, 16, 8, "f32", tuple(i * 7 % 41 for i in range(300))),
+    (40, 130, 8, 2, 128, 16, "bf16", tuple(i * 37 % 131 for i in range(40))),
 ]
 
 
@@ -35,7 +46,7 @@ def test_warps_that_share_rows(case):
     x, s0 = operands(inp, dtype, lens), dev(inp["state0"])
     o, S = ssd.delta_rule_forward(*x, s0, scale=0.5, lens=on_device(lens))
     ro, rS, mo, mS = delta.forward(*(inp[n] for n in NAMES), inp["state0"], 0.5, lens)
-    check(host(o), ro, mo, T, rounded(dtype), 2.0 ** -15 if dtype == "bf16" else 0.0)
+    check(host(o), ro, mo, T, rounded(dtype), O_OF_SIZE if dtype == "bf16" else 0.0)
     check(host(S), rS, mS, T)
     g = ssd.delta_rule_backward(*x, s0, dev(inp["do"], dtype), dev(inp["dstate"]), scale=0.5,
                                 lens=on_device(lens))
@@ -133,10 +144,8 @@ def test_alike_keys_of_many_heads(strengths):
     """Keys that hardly differ, 160 (row, head) pairs of 128 columns; the last strength
     of a head in one step alone, which multiplies the memory by 1 - 40.
 
-    o = e^g H q + P U takes H, P and U in 11 bits: H off by 2^-12, a term of P U by twice
-    that, and the reference's size is |q| times the sum of the terms' magnitudes, so o is
-    off by 2^-11 size at most.  (Where one or two terms are most of the sum, as here the
-    steps 75 and 76, 40 times the others and of opposite sign, nothing averages out.)"""
+    (The steps 75 and 76 write 40 times what others do, and of opposite sign, so what o
+    is rounded by does not average out.)"""
     import state_space_model_analytic_gb300 as ssd
     B, T, H, K = 2, 130, 80, 128
     inp = synth.delta_inputs(B, T, H, H, K, 32, "bf16", 71)
@@ -150,7 +159,7 @@ def test_alike_keys_of_many_heads(strengths):
     x, s0 = operands(inp, "bf16"), dev(inp["state0"])
     o, S = ssd.delta_rule_forward(*x, s0)
     ro, rS, mo, mS = delta.forward(*(inp[n] for n in NAMES), inp["state0"])
-    check(host(o), ro, mo, T, 2.0 ** -8, 2.0 ** -11)
+    check(host(o), ro, mo, T, 2.0 ** -8, O_OF_SIZE)
     check(host(S), rS, mS, T)
 
 

@@ -35,13 +35,9 @@ namespace {
 
 using namespace delta;
 
-// Parts of the state, P and U where they make o alone: a bf16 o has 8 bits.
-template <int NI>
-constexpr int kOutParts = NI == 1 ? 1 : 2;
-
 constexpr int kWalkers = 4;  // warps of a walk
 
-template <int NI, int DK, int PP, int WK, int kExchanged, bool kHelped = false>
+template <int NI, int DK, int WK, int kExchanged, bool kHelped = false>
 struct Geom {
   static constexpr int kThreads = kPrep + 32 * kWalkers * (kHelped ? 2 : 1);
   // Registers of those that walk and of the others, of what a CTA starts with.
@@ -57,14 +53,14 @@ struct Geom {
   static constexpr int VT = NI == 1 ? C * kVB * 2 : C * LV * 4;
   static_assert(VT >= NI * C * kVB * 2, "");
   static constexpr int NS = 3;                       // stages of the operands
-  static constexpr int MT = kParts * C * PB, PT = PP * C * PB;
+  static constexpr int MT = kParts * C * PB, PT = kParts * C * kPRow;
   static constexpr int kStage = 2 * KT + VT;
   static constexpr int kM = NS * kStage, kP = kM + 2 * MT;
   static constexpr int kG = kP + 2 * PT, kS = kG + 3 * (int)sizeof(Gates<C>);
   static constexpr int kX = kS + (int)sizeof(Scratch<C>);  // sums of WK warps on their way
   // of a walking warp, for those that form its o: the state and U as left operands, what
   // their rows were multiplied by
-  static constexpr int NB = C / 16, kHS = PP * DK / 16 * 512, kUS = PP * NB * 512;
+  static constexpr int NB = C / 16, kHS = kParts * DK / 16 * 512, kUS = kParts * NB * 512;
   static constexpr int kGiven = kHS + kUS + (1 + NB) * 64;
   static constexpr size_t smem =
       kX + (WK > 1 ? kExchanged * kWalkers * NC * 512 : 0) + (kHelped ? kWalkers * kGiven : 0);
@@ -181,17 +177,16 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
 }
 
 // f[n] = X K^T for the C steps of a tile whose rows are steps, X the warp's columns k0
-// ... of the state, scaled; and with PO > 0 o[n] = X Q^T with PO parts of it.  The right
-// operands of a group of columns are loaded while the group before is multiplied.
+// ... of the state, scaled; and with kO o[n] = X Q^T.  The right operands of a group of columns are loaded while the group before is multiplied.
 // given(k, a): the state's parts as left operands of columns 16 k ..., as soon as there
 // are any.
-template <int NI, int PO, int DK, int NK, int NC, typename F>
+template <int NI, bool kO, int DK, int NK, int NC, typename F>
 __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
                                             const float (&x)[NK][4], const RowScales& s, uint32_t K,
                                             uint32_t Q, int k0, const Lane<DK * 2>& at, F given) {
   constexpr int C = kSteps<NI>, RB = DK * 2;
   constexpr int GN = NC < 4 ? NC : 4;                     // columns of eight of a group
-  constexpr int GF = NC / GN, GK = PO > 0 ? 2 * GF : GF;  // groups of 16 terms
+  constexpr int GF = NC / GN, GK = kO ? 2 * GF : GF;  // groups of 16 terms
   constexpr int NG = NK / 2 * GK;
   uint32_t a[2][kParts][4], b[2][NI][GN][2];
   auto load = [&](int i) {
@@ -211,16 +206,19 @@ __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4]
     if (g < GF) {
       if (k == 0) mma_parts0<kParts, NI, GN>(f + GN * g, a[0], b[i & 1]);
       else mma_parts<kParts, NI, GN>(f + GN * g, a[k & 1], b[i & 1]);
-    } else if constexpr (PO > 0) {
-      uint32_t ao[PO][4];
-#pragma unroll
-      for (int q = 0; q < PO; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ao[q][e] = a[k & 1][q][e];
-      if (k == 0) mma_parts0<PO, NI, GN>(o + GN * (g - GF), ao, b[i & 1]);
-      else mma_parts<PO, NI, GN>(o + GN * (g - GF), ao, b[i & 1]);
+    } else if constexpr (kO) {
+      if (k == 0) mma_parts0<kParts, NI, GN>(o + GN * (g - GF), a[0], b[i & 1]);
+      else mma_parts<kParts, NI, GN>(o + GN * (g - GF), a[k & 1], b[i & 1]);
     }
   }
+}
+
+// Block (i, k) of P, 16 rows and 16 columns, as a right operand: its rows as columns.
+template <int C>
+__device__ __forceinline__ void load_scores(uint32_t (&r)[kParts][2][2], uint32_t M, uint32_t P,
+                                            const Lane<C * 2>& lm, const Lane<kPRow>& lp, int i, int k) {
+  if (i == k) load_right<kParts, 2>(r, P, C * kPRow, lp, 16 * k, 0);
+  else load_right<kParts, 2>(r, M, C * C * 2, lm, 16 * k, 16 * i);
 }
 
 // d = a b for two columns of eight, all parts of both; the small products go to a sum
@@ -300,8 +298,8 @@ __device__ __forceinline__ void add_warps(float (&t)[NC][4], const float4* ex, i
 // first, so that none of them begins when the others are done (16 rows of up to 1003
 // steps, 24 heads 64/64: 118 us against 135).
 constexpr int kOrdered = 256;  // rows that are put in order
-__device__ __forceinline__ int row_of(const int* lens, int B, int T, int tid) {
-  __shared__ int len[kOrdered], row;
+// len: kOrdered + 1 words of shared memory that are free again afterwards.
+__device__ __forceinline__ int row_of(const int* lens, int B, int T, int tid, int* len) {
   if (!lens || B > kOrdered || gridDim.x * gridDim.y <= kLaSms) return blockIdx.y;
   if (tid < B) len[tid] = min(max(lens[tid], 0), T);
   __syncthreads();
@@ -309,8 +307,10 @@ __device__ __forceinline__ int row_of(const int* lens, int B, int T, int tid) {
     int before = 0;
     const int mine = len[tid];
     for (int i = 0; i < B; ++i) before += len[i] > mine || (len[i] == mine && i < tid);
-    if (before == blockIdx.y) row = tid;
+    if (before == blockIdx.y) len[kOrdered] = tid;
   }
+  __syncthreads();
+  const int row = len[kOrdered];
   __syncthreads();
   return row;
 }
@@ -327,16 +327,16 @@ constexpr bool helped() {
   return !kStates && WK == 1 && NI == 1 && DK == 128;
 }
 
-// What a walking warp hands to the warp that forms its o: PP parts of the state and
+// What a walking warp hands to the warp that forms its o: the parts of the state and
 // of U's blocks as left operands, with what their rows were multiplied by.
-template <int PP, typename G>
+template <typename G>
 struct Given {
   uint8_t* at;
   __device__ __forceinline__ uint4* state(int k, int q, int lane) const {
-    return (uint4*)(at + (k * PP + q) * 512) + lane;
+    return (uint4*)(at + (k * kParts + q) * 512) + lane;
   }
   __device__ __forceinline__ uint4* u(int k, int q, int lane) const {
-    return (uint4*)(at + G::kHS + (k * PP + q) * 512) + lane;
+    return (uint4*)(at + G::kHS + (k * kParts + q) * 512) + lane;
   }
   // of rows g and g + 8: the state's (0), those of U's block k (1 + k)
   __device__ __forceinline__ float2* down(int k, int lane) const {
@@ -348,13 +348,14 @@ struct Given {
 };
 
 // o of a chunk, 16 columns of v: s e^g H q + s P U.
-template <int NI, int DK, int PP, typename G, typename T>
-__device__ __forceinline__ void form_o(const Given<PP, G>& x, int vg, uint32_t Q, uint32_t P,
+template <int NI, int DK, typename G, typename T>
+__device__ __forceinline__ void form_o(const Given<G>& x, int vg, uint32_t Q, uint32_t M, uint32_t P,
                                        const Gates<G::C>& g, T* out, long long out_step, int n, int v,
                                        int dv, int lane) {
   constexpr int C = G::C, NB = G::NB;
   const Lane<G::RB> la(lane);
   const Lane<G::PB> lm(lane);
+  const Lane<kPRow> lp(lane);
   const int c2 = (lane & 3) * 2;
   auto scales = [&](int k) {
     const float2 d = *x.down(k, lane);
@@ -369,14 +370,14 @@ __device__ __forceinline__ void form_o(const Given<PP, G>& x, int vg, uint32_t Q
   bar(3 + vg, 64);
 #pragma unroll
   for (int k = 0; k < DK / 16; ++k) {
-    uint32_t a[PP][4];
+    uint32_t a[kParts][4];
 #pragma unroll
-    for (int q = 0; q < PP; ++q) fetch(a[q], x.state(k, q, lane));
+    for (int q = 0; q < kParts; ++q) fetch(a[q], x.state(k, q, lane));
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       uint32_t r[NI][2][2];
       load_right<NI, 2>(r, Q, C * G::RB, la, 16 * j, 16 * k);
-      mma_parts<PP, NI, 2>(o + 2 * j, a, r);
+      mma_parts<kParts, NI, 2>(o + 2 * j, a, r);
     }
   }
   {
@@ -387,19 +388,20 @@ __device__ __forceinline__ void form_o(const Given<PP, G>& x, int vg, uint32_t Q
       times(o[j], *(const float2*)&g.lead[8 * j + c2]);
     }
   }
-  bar(3 + kWalkers + vg, 64);
 #pragma unroll
   for (int k = 0; k < NB; ++k) {
-    uint32_t a[PP][4];
+    if (k == 0) bar(3 + kWalkers + vg, 64);
+    if (k == NB / 2) bar(3 + 2 * kWalkers + vg, 64);
+    uint32_t a[kParts][4];
     const RowScales s = scales(1 + k);
 #pragma unroll
-    for (int q = 0; q < PP; ++q) fetch(a[q], x.u(k, q, lane));
+    for (int q = 0; q < kParts; ++q) fetch(a[q], x.u(k, q, lane));
 #pragma unroll
     for (int j = k; j < NB; ++j) {
-      uint32_t r[PP][2][2];
+      uint32_t r[kParts][2][2];
       float d[2][4];
-      load_right<PP, 2>(r, P, C * G::PB, lm, 16 * j, 16 * k);
-      mma_parts0<PP, PP, 2>(d, a, r);
+      load_scores<C>(r, M, P, lm, lp, j, k);
+      mma_parts0<kParts, kParts, 2>(d, a, r);
       add_rows(o[2 * j], d[0], s);
       add_rows(o[2 * j + 1], d[1], s);
     }
@@ -414,10 +416,9 @@ __device__ __forceinline__ void form_o(const Given<PP, G>& x, int vg, uint32_t Q
 template <int NI, int DK, int WK, bool kStates>
 __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kStates>() ? 2 : 1), 1)
     k_delta_walk(const DeltaWalk p) {
-  constexpr int PP = kOutParts<NI>;
   // o: formed by the preparing warps, or by the walking ones
   constexpr bool kHelped = helped<NI, DK, WK, kStates>(), kOwn = !kStates && !kHelped;
-  using G = Geom<NI, DK, PP, WK, kStates ? 1 : 2, kHelped>;
+  using G = Geom<NI, DK, WK, kStates ? 1 : 2, kHelped>;
   using T = typename std::conditional<NI == 1, __nv_bfloat16, float>::type;
   constexpr int C = G::C, NC = G::NC, NB = C / 16, NK = DK / 8 / WK, VB = kVB / WK;
   // blocks of 16 steps of o and E that a warp writes
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
   Scratch<C>& scratch = *(Scratch<C>*)(sm + G::kS);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int vblocks = (p.dv + VB - 1) / VB;
-  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = row_of(p.lens, p.B, p.T, tid);
+  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = row_of(p.lens, p.B, p.T, tid, (int*)sm);
   const int width = min(VB, p.dv - v0);
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
         if (!kStates) q.write(st, tid, no_least, q_done);
       }
       bar(1, kPrep);
-      prepare<NI, DK, PP, !kStates, kHelped>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
+      prepare<NI, DK, !kStates, kHelped>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
                                     sm + G::kP + (c & 1) * G::PT, g, scratch, tid, [&] {
                                       scan_gates<C>(gates[(c + 1) % 3], raw, lane);
                                       load_raw(c + 2);
@@ -525,10 +526,10 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
     __syncthreads();
     for (int c = 0; c < nc; ++c) {
       if (w0 < width)
-        form_o<NI, DK, PP, G, T>({sm + G::kX + vg * G::kGiven}, vg, smem32(stage(c)),
-                                 smem32(sm + G::kP + (c & 1) * G::PT), gates[c % 3],
-                                 out + (long long)c * C * out_step + w0, out_step, min(C, len - c * C),
-                                 v0 + w0, p.dv, lane);
+        form_o<NI, DK, G, T>({sm + G::kX + vg * G::kGiven}, vg, smem32(stage(c)),
+                             smem32(sm + G::kM + (c & 1) * G::MT), smem32(sm + G::kP + (c & 1) * G::PT),
+                             gates[c % 3], out + (long long)c * C * out_step + w0, out_step,
+                             min(C, len - c * C), v0 + w0, p.dv, lane);
       __syncthreads();
     }
   } else {
@@ -542,7 +543,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
     const bool idle = w0 >= width;  // (fewer columns than warps for them)
     const Lane<G::RB> la(lane);
     const Lane<G::PB> lm(lane);
-    const Given<PP, G> given = {sm + G::kX + vg * G::kGiven};
+    const Lane<kPRow> lp(lane);
+    const Given<G> given = {sm + G::kX + vg * G::kGiven};
     float x[NK][4];
     get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, k0, p.dk, lane);
     float2 most = row_max<NK>(x);
@@ -563,11 +565,11 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
       const RowScales sx = row_scales(most);
       {
         float qx[NC][4];
-        state_times<NI, kOwn ? PP : 0, DK, NK, NC>(f, qx, x, sx, K, Q, k0, la,
+        state_times<NI, kOwn, DK, NK, NC>(f, qx, x, sx, K, Q, k0, la,
                                                    [&](int k, const uint32_t (&a)[kParts][4]) {
           if constexpr (kHelped) {
 #pragma unroll
-            for (int q = 0; q < PP; ++q) given.put(given.state(k, q, lane), a[q]);
+            for (int q = 0; q < kParts; ++q) given.put(given.state(k, q, lane), a[q]);
             if (k == 0 && (lane & 3) == 0) *given.down(0, lane) = make_float2(sx.down0, sx.down1);
             if (k == NK / 2 - 1) bar_arrive(3 + vg, 64);
           }
@@ -676,14 +678,16 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
             add_rows(f[2 * k + q], d[q], sy);
             times(f[2 * k + q], *(const float2*)&g.beta[at]);
           }
-          uint32_t ao[PP][4];  // U for o
+          uint32_t ao[kParts][4];  // U for o
           const RowScales su = row_scales(row_max<2>(f + 2 * k));
-          as_left<PP>(ao, f[2 * k], f[2 * k + 1], su.up0, su.up1);
+          as_left<kParts>(ao, f[2 * k], f[2 * k + 1], su.up0, su.up1);
 #pragma unroll
-          for (int q = 0; q < PP; ++q) given.put(given.u(k, q, lane), ao[q]);
+          for (int q = 0; q < kParts; ++q) given.put(given.u(k, q, lane), ao[q]);
           if ((lane & 3) == 0) *given.down(1 + k, lane) = make_float2(su.down0, su.down1);
+          // (in halves: all at once left what U adds to o to the end of the chunk)
+          if (k == NB / 2 - 1) bar_arrive(3 + kWalkers + vg, 64);
+          if (k == NB - 1) bar_arrive(3 + 2 * kWalkers + vg, 64);
         }
-        bar_arrive(3 + kWalkers + vg, 64);
       } else {
         // block by block: E = F - X beta F, U = beta E, and what U takes off F of the
         // later blocks and adds to O.  The next block waits for its own share alone; the
@@ -704,19 +708,14 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
             add_scaled(f + i, d);
           }
           if constexpr (kOwn) {
-            uint32_t ao[PP][4];
-#pragma unroll
-            for (int q = 0; q < PP; ++q)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) ao[q][e] = au[q][e];
 #pragma unroll
             for (int j = 0; j < OB; ++j) {
               const int i = WK == 1 ? j : kg * OB + j;  // block
               if (i >= k && (WK == 1 || i < NB)) {
-                uint32_t rp[PP][2][2];
+                uint32_t rp[kParts][2][2];
                 float d[2][4];
-                load_right<PP, 2>(rp, P, C * G::PB, lm, 16 * i, 16 * k);
-                mma_parts0<PP, PP, 2>(d, ao, rp);
+                load_scores<C>(rp, M, P, lm, lp, i, k);
+                mma_parts0<kParts, kParts, 2>(d, au, rp);
                 add_scaled(o + 2 * j, d);
               }
             }
@@ -803,7 +802,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
 // times theirs, and dO's rows are divided by q's.
 template <int NI, int DK, int WK>
 __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const DeltaBack p) {
-  using G = Geom<NI, DK, kParts, WK, 1>;
+  using G = Geom<NI, DK, WK, 1>;
   using T = typename std::conditional<NI == 1, __nv_bfloat16, float>::type;
   constexpr int C = G::C, NC = G::NC, NB = C / 16, NK = DK / 8 / WK, VB = kVB / WK;
   constexpr int OB = NB / WK > 0 ? NB / WK : 1;
@@ -812,7 +811,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
   Scratch<C>& scratch = *(Scratch<C>*)(sm + G::kS);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int vblocks = (p.dv + VB - 1) / VB;
-  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = row_of(p.lens, p.B, p.T, tid);
+  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = row_of(p.lens, p.B, p.T, tid, (int*)sm);
   const int width = min(VB, p.dv - v0);
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
@@ -921,7 +920,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
           for (int k = 0; k < NI; ++k) *(uint2*)(to + k * C * kVB * 2) = make_uint2(q[0][k], q[1][k]);
         }
       }
-      prepare<NI, DK, kParts, true, false>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
+      prepare<NI, DK, true, false>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
                                     sm + G::kP + (c & 1) * G::PT, g, scratch, tid, [&] {
                                       scan_gates<C>(gates[(c + 2) % 3], raw, lane);  // (c - 1)
                                       load_raw(c - 2);
@@ -962,6 +961,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
     const bool idle = w0 >= width;
     const Lane<G::RB> la(lane);
     const Lane<G::PB> lm(lane);
+    const Lane<kPRow> lp(lane);
     const Lane<kVB * 2> lv(lane);
     float x[NK][4];  // D
     get_state<NK>(x, p.first ? p.first + unit * p.dv * p.dk : nullptr, v, p.dv, k0, p.dk, lane);
@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         const RowScales sx = row_scales(most);
         // (the state is stored between the products: all at once the warp waited 1400
         // cycles for its own stores)
-        state_times<NI, 0, DK, NK, NC>(f, f, x, sx, K, K, k0, la, [&](int k, const uint32_t (&)[kParts][4]) {
+        state_times<NI, false, DK, NK, NC>(f, f, x, sx, K, K, k0, la, [&](int k, const uint32_t (&)[kParts][4]) {
           put_state<2>(x + 2 * k, hist + (long long)c * p.dv * p.dk, v, p.dv, k0 + 16 * k, p.dk, lane);
         });
 #pragma unroll
@@ -1010,7 +1010,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         for (int i = k; i < NB; ++i) {
           uint32_t a[NI][4], r[kParts][2][2];
           dout_left(a, i);
-          load_right_t<kParts, 2>(r, P, C * G::PB, lm, 16 * k, 16 * i);
+          if (i == k) load_right_t<kParts, 2>(r, P, C * kPRow, lp, 0, 16 * k);
+          else load_right_t<kParts, 2>(r, M, C * G::PB, lm, 16 * i, 16 * k);
           if (i == k) mma_parts0<NI, kParts, 2>(d, a, r);
           else mma_parts<NI, kParts, 2>(d, a, r);
         }
@@ -1146,7 +1147,7 @@ dim3 walk_grid(int H, int B, int dv, int wk) { return dim3(H * ((dv + kVB / wk -
 
 template <int NI, int DK, int WK, bool kStates>
 cudaError_t walk_t(const DeltaWalk& p, cudaStream_t s) {
-  using G = Geom<NI, DK, kOutParts<NI>, WK, kStates ? 1 : 2, helped<NI, DK, WK, kStates>()>;
+  using G = Geom<NI, DK, WK, kStates ? 1 : 2, helped<NI, DK, WK, kStates>()>;
   constexpr size_t smem = G::smem;
   static_assert(smem <= 232448, "");
   const cudaError_t e = cudaFuncSetAttribute(k_delta_walk<NI, DK, WK, kStates>,
@@ -1159,7 +1160,7 @@ cudaError_t walk_t(const DeltaWalk& p, cudaStream_t s) {
 }
 template <int NI, int DK, int WK>
 cudaError_t back_t(const DeltaBack& p, cudaStream_t s) {
-  using G = Geom<NI, DK, kParts, WK, 1>;
+  using G = Geom<NI, DK, WK, 1>;
   constexpr size_t smem = G::smem;
   static_assert(smem <= 232448, "");
   const cudaError_t e = cudaFuncSetAttribute(k_delta_back<NI, DK, WK>,

@@ -547,8 +547,11 @@ __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float
   return exp2_fast((hi_i - hi_j) + (lo_i - lo_j));
 }
 
-// What the walks read of a chunk besides its operands, in parts (tiles [C][C]): in M
-// -L below the blocks of 16 on the diagonal and in them -X^T, its rows scaled, and P.
+// What the walks read of a chunk besides its operands, in parts: a tile M [C][C] with -L
+// below the blocks of 16 on the diagonal, in them -X^T, its rows scaled, and above them
+// P, block (i, j) in the place of block (j, i), as it is; and P's diagonal blocks, a tile
+// [C][16] (kPRow bytes a row).
+constexpr int kPRow = 32;
 constexpr int kDiag = 20;  // floats of a column of a diagonal block
 template <int C>
 struct alignas(16) Scratch {
@@ -559,9 +562,9 @@ struct alignas(16) Scratch {
 
 // One block of 16 x 16, rows 16 bi ..., columns 16 bj ..., of L and, with kP, of P, which
 // share the decays and the right operand.  -L goes to the tile M in parts, or on the
-// diagonal (kDiagonal) L to `diag`, transposed; P to its tile in PP parts.  On the
+// diagonal (kDiagonal) L to `diag`, transposed; P to M's upper blocks or to P.  On the
 // diagonal P is zero above it and L on it too.
-template <int NI, int DK, int PP, bool kP, bool kDiagonal>
+template <int NI, int DK, bool kP, bool kDiagonal>
 __device__ __forceinline__ void score_block(uint32_t Q, uint32_t K, uint8_t* M, uint8_t* P,
                                             const Gates<kSteps<NI>>& g, float (*diag)[kDiag], int bi,
                                             int bj, int lane) {
@@ -612,10 +615,12 @@ __device__ __forceinline__ void score_block(uint32_t Q, uint32_t K, uint8_t* M, 
         float2 v = mul2(pair(acc[NA - 1][n], u), gamma);
         if (kDiagonal && j > i) v.x = 0.f;
         if (kDiagonal && j + 1 > i) v.y = 0.f;
-        uint32_t p[PP];
-        split2<PP>(v, p);
+        uint32_t p[kParts];
+        split2<kParts>(v, p);
+        uint8_t* at = kDiagonal ? P + at16<kPRow>(16 * bi + i, n) + c0 * 2
+                                : M + at16<OB>(16 * bj + i, 2 * bi + n) + c0 * 2;
 #pragma unroll
-        for (int q = 0; q < PP; ++q) *(uint32_t*)(P + to + q * C * OB) = p[q];
+        for (int q = 0; q < kParts; ++q) *(uint32_t*)(at + q * C * (kDiagonal ? kPRow : OB)) = p[q];
       }
     }
   }
@@ -708,7 +713,7 @@ __device__ __forceinline__ void fold_block(uint8_t* M, const uint8_t* tt, int bi
 // a warp known at compile time, the warps' code and the walk's did not fit the
 // instruction caches together, and waiting for instructions was the largest of all
 // stalls.)  The last warp has `aside` to do as well (the gates of a later chunk).
-template <int NI, int DK, int PP, bool kP, bool kFold, typename F>
+template <int NI, int DK, bool kP, bool kFold, typename F>
 __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, uint8_t* M, uint8_t* P,
                                         Gates<kSteps<NI>>& g, Scratch<kSteps<NI>>& sc, int tid,
                                         F aside) {
@@ -718,14 +723,14 @@ __device__ __forceinline__ void prepare(const uint8_t* Qt, const uint8_t* Kt, ui
   // rows and columns (hexadecimal digits, the first last)
   constexpr uint32_t kI = NB == 4 ? 0x333221 : 0x1, kJ = NB == 4 ? 0x210100 : 0x0;
   if (warp < NB) {
-    score_block<NI, DK, PP, kP, true>(Q, K, M, P, g, sc.diag[warp], warp, warp, lane);
+    score_block<NI, DK, kP, true>(Q, K, M, P, g, sc.diag[warp], warp, warp, lane);
     __syncwarp();
     if (lane < 16) invert_diag<C, kFold>(M, sc.t[warp], g, sc.diag[warp], warp, lane);
     __syncwarp();
   } else {
 #pragma unroll 1
     for (int r = warp - NB; r < NB * (NB - 1) / 2; r += W)
-      score_block<NI, DK, PP, kP, false>(Q, K, M, P, g, nullptr, kI >> 4 * r & 15, kJ >> 4 * r & 15, lane);
+      score_block<NI, DK, kP, false>(Q, K, M, P, g, nullptr, kI >> 4 * r & 15, kJ >> 4 * r & 15, lane);
     if (warp == kPrep / 32 - 1) aside();
   }
   if constexpr (kFold) {

@@ -1,0 +1,77 @@
+"""How many bits the gated delta rule's results keep: outputs that are rounded once, keys
+that are alike, operands whose elements, steps or columns differ by powers of two.
+
+Tolerances.  A value held in 32 bits enters a product with 22 bits, off by 2^-23 of
+itself at most; a sum passes through a few dozen such terms and truncations of 2^-23,
+which as signs differ leave a few 2^-22 of its root mean square: 2^-19 is allowed, a
+factor of eight.  An element of 10^5 is off by five times that root mean square, and
+gradients sum up what two walks leave: 2^-16 for single elements.  A bf16 result is
+rounded by 2^-8 of itself besides."""
+import numpy as np
+import pytest
+
+from oracle import delta
+from state_space_model_analytic_gb300 import synth
+from test_parity_delta_gpu import NAMES, _built, dev, host, operands  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+RMS, ONE = 2.0 ** -19, 2.0 ** -16
+GRADS = ("dq", "dk", "dv", "dlog_decay", "dbeta", "dstate0")
+
+
+def recurrence(inp, state0=None, scale=1.0):
+    """o and the final state in 64 bits, step by step."""
+    import torch
+    t = lambda x: torch.from_numpy(np.asarray(x, dtype=np.float64)).cuda()  # noqa: E731
+    q, k, v, la, be = (t(inp[n]) for n in NAMES)
+    B, T, H, V = v.shape
+    q, k = (x.repeat_interleave(H // x.shape[2], 2) for x in (q, k))
+    S = torch.zeros(B, H, V, k.shape[-1], dtype=torch.float64, device="cuda")
+    S = S if state0 is None else t(state0)
+    o = torch.empty(B, T, H, V, dtype=torch.float64, device="cuda")
+    for i in range(T):
+        S = S * la[:, i].exp()[..., None, None]
+        e = v[:, i] - (S @ k[:, i, :, :, None])[..., 0]
+        S = S + (be[:, i, :, None] * e)[..., None] * k[:, i, :, None, :]
+        o[:, i] = scale * (S @ q[:, i, :, :, None])[..., 0]
+    return o.cpu().numpy(), S.cpu().numpy()
+
+
+def rms(x, axes=None):
+    return np.sqrt(np.mean(x * x, axis=axes, keepdims=axes is not None))
+
+
+def close(got, ref, axes=None, most=RMS):
+    """Root mean square of the errors against that of the values, over `axes`."""
+    assert np.isfinite(got).all()
+    off = rms(got - ref, axes) / np.maximum(rms(ref, axes), 1e-300)
+    assert (off <= most).all(), float(np.log2(off.max()))
+
+
+def rounded_once(got, ref, axes):
+    """Off by the rounding to bf16 and ONE of the root mean square over `axes`."""
+    assert np.isfinite(got).all()
+    over = np.maximum(np.abs(got - ref) - 2.0 ** -8 * np.abs(ref), 0) / rms(ref, axes)
+    assert (over <= ONE).all(), float(np.log2(over.max()))
+
+
+# heads, groups, K, V: four, two and one warp to 16 rows of a state, o by the walking warps
+# and by others
+SHAPES = [(3, 3, 64, 64), (50, 50, 64, 64), (80, 80, 64, 64),
+          (3, 1, 128, 64), (50, 25, 128, 64), (80, 80, 128, 64), (40, 40, 128, 128), (160, 8, 72, 24)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_outputs_are_rounded_once(shape):
+    import state_space_model_analytic_gb300 as ssd
+    H, G, K, V = shape
+    inp = synth.delta_inputs(1, 200, H, G, K, V, "bf16", 81)
+    o, S = ssd.delta_rule_forward(*operands(inp, "bf16"), dev(inp["state0"]))
+    ro, rS = recurrence(inp, inp["state0"])
+    rounded_once(host(o), ro, (1, 3))
+    close(host(S), rS, (2, 3))
+
+
+def spread(n, least):
+    """1 ... 2^-least over n elements, in an order that is not theirs."""
+    return np.exp2(-(np.arange(n) * 7 % (least + 1.0)))

@@ -332,9 +332,9 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
  * the state (of their step, for q, k, v and dout in fp32) lose bits.  Results do not
  * depend on powers of two in a step's q, k or v, as long as the largest element of a
  * key is between 2^-63 and 2^63 and beta times its square is a normal number.
- * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.  A
- * bf16 o and dv are off by their own rounding, 0.0017 of their root mean square; bf16
- * dq and dk, which take the chunk's masked scores in 11 bits, by little more.
+ * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.  
+ * bf16 results (o, dq, dk, dv) are off by their own rounding, 0.0017 of their root mean
+ * square.
  */
 
 /* Bytes of workspace of ssd_delta_rule_forward (which = 0) or

@@ -39,10 +39,6 @@ namespace {
 
 using namespace delta;
 
-// bf16 results take MP and ML as one part (11 bits): they feed dq and dk alone.
-template <int NI>
-constexpr int kMaskParts = NI == 1 ? 1 : 2;
-
 template <int NI, int DK>
 struct Geom {
   static constexpr int C = kSteps<NI>, NT = C * 8;       // threads
@@ -51,7 +47,7 @@ struct Geom {
   static constexpr int OT = NI * C * VR;                 // dO
   static constexpr int HT = kParts * kVB * RB;           // H, D
   static constexpr int UT = kParts * C * VR;             // U, dv
-  static constexpr int MT = kMaskParts<NI> * C * PB;     // MP, ML: in the place of H, D
+  static constexpr int MT = kParts * C * PB;     // MP, ML: in the place of H, D
   static_assert(MT <= HT, "");
   static constexpr int kK = KT, kO = 2 * KT, kU = kO + OT, kV = kU + UT, kH = kV + UT;
   static constexpr size_t smem = kH + 4 * HT;            // H, D; the next ones
@@ -93,7 +89,7 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
   using T = typename std::conditional<NI == 1, __nv_bfloat16, float>::type;
   using TO = typename std::conditional<kShared, float, T>::type;
   constexpr int C = G::C, NT = G::NT, NW = NT / 32, RB = G::RB, VR = G::VR, PB = G::PB, NK = G::NK,
-                NM = G::NM, NB = C / 16, PM = kMaskParts<NI>;
+                NM = G::NM, NB = C / 16;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ Gates<C> gates[2];
   // Of the steps: the largest of U, dv and dO and what they were divided by (of this
@@ -478,11 +474,11 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         if (m0 + e <= 2 * strip + 1) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            uint32_t a[PM];
-            split2<PM>(mul2(pair(mm[e], u), both(smask.up)), a);
+            uint32_t a[kParts];
+            split2<kParts>(mul2(pair(mm[e], u), both(smask.up)), a);
             uint8_t* at = out + at16<PB>(i0 + 8 * u, m0 + e) + c2 * 2;
 #pragma unroll
-            for (int q = 0; q < PM; ++q) *(uint32_t*)(at + q * C * PB) = a[q];
+            for (int q = 0; q < kParts; ++q) *(uint32_t*)(at + q * C * PB) = a[q];
           }
         }
     }
@@ -549,25 +545,25 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
       zero(d[2]);
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        uint32_t a[PM][4], rk[NI][2][2];
+        uint32_t a[kParts][4], rk[NI][2][2];
         load_right_t<NI, 2>(rk, sK, C * RB, lk, c, 16 * k);
         if (k <= strip) {  // columns 16 k ... of MP, ML
 #pragma unroll
-          for (int q = 0; q < PM; ++q) ldm4(a[q], lm.left(sP, 16 * strip, 16 * k) + q * C * PB);
-          mma_parts<PM, NI, 2>(d[0], a, rk);
+          for (int q = 0; q < kParts; ++q) ldm4(a[q], lm.left(sP, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<kParts, NI, 2>(d[0], a, rk);
 #pragma unroll
-          for (int q = 0; q < PM; ++q) ldm4(a[q], lm.left(sL, 16 * strip, 16 * k) + q * C * PB);
-          mma_parts<PM, NI, 2>(d[1], a, rk);
+          for (int q = 0; q < kParts; ++q) ldm4(a[q], lm.left(sL, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<kParts, NI, 2>(d[1], a, rk);
         }
         if (k >= strip) {  // rows 16 k ...
           uint32_t rq[NI][2][2];
           load_right_t<NI, 2>(rq, sQ, C * RB, lk, c, 16 * k);
 #pragma unroll
-          for (int q = 0; q < PM; ++q) ldm4t(a[q], lm.left_t(sP, 16 * strip, 16 * k) + q * C * PB);
-          mma_parts<PM, NI, 2>(d[2], a, rq);
+          for (int q = 0; q < kParts; ++q) ldm4t(a[q], lm.left_t(sP, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<kParts, NI, 2>(d[2], a, rq);
 #pragma unroll
-          for (int q = 0; q < PM; ++q) ldm4t(a[q], lm.left_t(sL, 16 * strip, 16 * k) + q * C * PB);
-          mma_parts<PM, NI, 2>(d[2], a, rk);
+          for (int q = 0; q < kParts; ++q) ldm4t(a[q], lm.left_t(sL, 16 * strip, 16 * k) + q * C * PB);
+          mma_parts<kParts, NI, 2>(d[2], a, rk);
         }
       }
 #pragma unroll

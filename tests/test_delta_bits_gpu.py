@@ -72,6 +72,18 @@ def test_outputs_are_rounded_once(shape):
     close(host(S), rS, (2, 3))
 
 
+@pytest.mark.parametrize("shape", [(3, 3, 64, 64), (4, 2, 128, 128), (2, 2, 72, 40)], ids=str)
+def test_gradients_are_rounded_once(shape):
+    import state_space_model_analytic_gb300 as ssd
+    H, G, K, V = shape
+    inp = synth.delta_inputs(1, 200, H, G, K, V, "bf16", 82)
+    g = ssd.delta_rule_backward(*operands(inp, "bf16"), dev(inp["state0"]), dev(inp["do"], "bf16"),
+                                dev(inp["dstate"]))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), inp["state0"], inp["do"], inp["dstate"])
+    for n in ("dq", "dk", "dv"):
+        rounded_once(host(g[n]), ref[n], (1, 3))
+
+
 def spread(n, least):
     """1 ... 2^-least over n elements, in an order that is not theirs."""
     return np.exp2(-(np.arange(n) * 7 % (least + 1.0)))

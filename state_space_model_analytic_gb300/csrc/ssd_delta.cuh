@@ -628,8 +628,8 @@ __device__ __forceinline__ void score_block(uint32_t Q, uint32_t K, uint8_t* M, 
 
 // Lanes 0 - 15, a column j each of diagonal block s: with T = (I + beta L)^-1, X = L T
 // and T = I - beta X, so once X_mj is whole, T_mj = -beta_m X_mj (1 for m = j) adds
-// L_im T_mj to every later X_ij.  kT: T to `tt` too, its columns scaled like X's, by
-// the larger of both.
+// L_im T_mj to every later X_ij.  kT: T to `tt` too, and the columns of both scaled by T's
+// largest (X, which comes to |k|^2 times T, would leave T's second part no exponents).
 template <int C, bool kT>
 __device__ __forceinline__ void invert_diag(uint8_t* out, uint8_t* tt, Gates<C>& g,
                                             const float (*diag)[kDiag], int s, int j) {
@@ -653,11 +653,9 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, uint8_t* tt, Gates<C>&
   }
   float m = 0.f;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
-  // (an element of L is at most 2^9, so one of L T, scaled, at most 2^15)
-  if (kT)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(tm[i]));
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(kT ? tm[i] : x[i]));
+  // (an element of L is at most 2^9, so one of X = L T, and of the folded blocks, is below
+  // 2^15 where T's are below 4)
   const Scale sx = scale_to<kT ? 1 : 8>(m);
   g.xs[16 * s + j] = sx.down;
   g.bx[16 * s + j] = sx.down * g.beta[16 * s + j];

@@ -84,6 +84,28 @@ def test_gradients_are_rounded_once(shape):
         rounded_once(host(g[n]), ref[n], (1, 3))
 
 
+@pytest.mark.parametrize("kind", ["alike", "noisy", "signs"])
+@pytest.mark.parametrize("shape", [(80, 128, 64), (3, 128, 64), (80, 64, 64)], ids=str)
+def test_states_of_alike_keys(shape, kind):
+    """Keys of length 1 that hardly differ, differ by a third, or have elements of the
+    same size: the triangular system's inverse and its matrix are of very different size.
+    (Where one key's share is written over and over, what is left of it is small: the
+    errors go by the largest that the state's row has held, hence by v's size here.)"""
+    import state_space_model_analytic_gb300 as ssd
+    H, K, V = shape
+    inp = synth.delta_inputs(1, 512, H, H, K, V, "bf16", 83)
+    rng = np.random.default_rng(84)
+    k = {"alike": 1.0 + 0.05 * inp["k"], "noisy": 1.0 + 0.3 * rng.standard_normal(inp["k"].shape),
+         "signs": np.sign(rng.standard_normal(inp["k"].shape))}[kind]
+    inp["k"] = synth.round_to(k / np.sqrt((k * k).sum(-1, keepdims=True)), "bf16")
+    inp["beta"] = np.ones_like(inp["beta"])
+    inp["log_decay"] = np.zeros_like(inp["log_decay"])
+    o, S = ssd.delta_rule_forward(*operands(inp, "bf16"))
+    ro, rS = recurrence(inp)
+    close(host(S), rS, (2, 3))
+    rounded_once(host(o), ro, (1, 3))
+
+
 def spread(n, least):
     """1 ... 2^-least over n elements, in an order that is not theirs."""
     return np.exp2(-(np.arange(n) * 7 % (least + 1.0)))

@@ -799,7 +799,9 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
 }
 
 // The walk back.  The sums are those of k's and q's scales: dU and y of 2^-n, dv of 2^n
-// times theirs, and dO's rows are divided by q's.
+// times theirs, and dO's rows are divided by q's.  dO's columns are scaled each by its own
+// largest of the chunk: they are the rows of the left operands, and what is in one of
+// them, infinities too, stays in it.
 template <int NI, int DK, int WK>
 __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const DeltaBack p) {
   using G = Geom<NI, DK, WK, 1>;
@@ -809,6 +811,10 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
   extern __shared__ __align__(1024) uint8_t sm[];
   Gates<C>* gates = (Gates<C>*)(sm + G::kG);
   Scratch<C>& scratch = *(Scratch<C>*)(sm + G::kS);
+  // of dO's columns: the bits of the largest of this chunk and the next, and what they
+  // were divided by
+  __shared__ __align__(16) uint32_t top_out[2][kVB];
+  __shared__ float out_down[2][kVB];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int vblocks = (p.dv + VB - 1) / VB;
   const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = row_of(p.lens, p.B, p.T, tid, (int*)sm);
@@ -851,10 +857,10 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         g.beta[r] *= d * d;
       };
       auto q_done = [&](int r, float s, float) { g.qdown[r] = inverse_pow2(s); };
-      // dO: a thread's eights (NI == 1) or fours of elements, scaled by 2^n of all the
-      // tile's rows together
-      constexpr int E = NI == 1 ? 8 : 4, ND = C * kVB / E / kPrep;
-      static_assert(C * kVB / E % kPrep == 0, "");
+      // dO: a thread's eights (NI == 1) or fours of elements, of the same columns
+      constexpr int E = NI == 1 ? 8 : 4, LPR = kVB / E, ND = C * LPR / kPrep;
+      static_assert(C * LPR % kPrep == 0 && kPrep % LPR == 0, "");
+      const int v8 = tid % LPR * E;
       float d[ND][E];
       if constexpr (NI == 1) {
         HalfRows<C, DK, kPrep> k, q;
@@ -876,12 +882,14 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         q.write(st, tid, no_least, q_done);
       }
       bar(1, kPrep);
-      float m = 0.f;
+      float m[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) m[e] = 0.f;
 #pragma unroll
       for (int i = 0; i < ND; ++i) {
-        const int at = i * kPrep + tid, r = at / (kVB / E);
+        const int r = (i * kPrep + tid) / LPR;
         if constexpr (NI == 1) {
-          const uint4 q = *(const uint4*)(st + 2 * G::KT + at16<kVB * 2>(r, at % (kVB / E)));
+          const uint4 q = *(const uint4*)(st + 2 * G::KT + at16<kVB * 2>(r, tid % LPR));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 f = unpack_bf((&q.x)[e]);
@@ -893,28 +901,34 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           d[i][e] *= s;
-          m = fmaxf(m, fabsf(d[i][e]));
+          m[e] = fmaxf(m[e], fabsf(d[i][e]));
         }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane == 0) scratch.most[warp] = m;
-      bar(1, kPrep);
+      for (int o = 16; o >= LPR; o >>= 1)
 #pragma unroll
-      for (int i = 0; i < kPrep / 32; ++i) m = fmaxf(m, scratch.most[i]);
-      const Scale so = scale_to<10>(m);
-      if (tid == 0) g.dout = so.down;
+        for (int e = 0; e < E; ++e) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
+      if (lane < LPR)
+#pragma unroll
+        for (int e = 0; e < E; ++e) atomicMax(&top_out[c & 1][v8 + e], __float_as_uint(m[e]));
+      bar(1, kPrep);
+      if (tid < kVB) {
+        top_out[(c & 1) ^ 1][tid] = 0;  // (read a chunk ago)
+        out_down[c & 1][tid] = scale_to<10>(__uint_as_float(top_out[c & 1][tid])).down;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) m[e] = scale_to<10>(__uint_as_float(top_out[c & 1][v8 + e])).up;
 #pragma unroll
       for (int i = 0; i < ND; ++i) {
-        const int at = i * kPrep + tid, r = at / (kVB / E);
+        const int r = (i * kPrep + tid) / LPR;
         uint32_t q[E / 2][NI];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) split2<NI>(d[i][e] * so.up, d[i][e + 1] * so.up, q[e / 2]);
+        for (int e = 0; e < E; e += 2) split2<NI>(d[i][e] * m[e], d[i][e + 1] * m[e + 1], q[e / 2]);
         if constexpr (NI == 1) {
-          *(uint4*)(st + 2 * G::KT + at16<kVB * 2>(r, at % (kVB / E))) =
+          *(uint4*)(st + 2 * G::KT + at16<kVB * 2>(r, tid % LPR)) =
               make_uint4(q[0][0], q[1][0], q[2][0], q[3][0]);
         } else {
-          const int x = at % (kVB / E);
+          const int x = tid % LPR;
           uint8_t* to = st + 2 * G::KT + at16<kVB * 2>(r, x >> 1) + (x & 1) * 8;
 #pragma unroll
           for (int k = 0; k < NI; ++k) *(uint2*)(to + k * C * kVB * 2) = make_uint2(q[0][k], q[1][k]);
@@ -927,6 +941,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
                                     });
     };
     if (nc > 0) {
+      if (tid < kVB) top_out[(nc - 1) & 1][tid] = 0;
       load(nc - 1);
       copy_commit();
       if (nc > 1) load(nc - 2);
@@ -996,7 +1011,9 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) times(f[i], *(const float2*)&g.tail[8 * i + c2]);
-      const float so = p.scale * g.dout;
+      // of rows g and g + 8
+      const float so[2] = {p.scale * out_down[c & 1][w0 + (lane >> 2)],
+                           p.scale * out_down[c & 1][w0 + (lane >> 2) + 8]};
       // dO's rows v, steps 16 k ... as a left operand
       auto dout_left = [&](uint32_t (&a)[NI][4], int k) {
 #pragma unroll
@@ -1019,7 +1036,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            set_pair(f[2 * k + q], u, fma2(both(so), pair(d[q], u), pair(f[2 * k + q], u)));
+            set_pair(f[2 * k + q], u, fma2(both(so[u]), pair(d[q], u), pair(f[2 * k + q], u)));
       };
       // what dO adds to D waits for nothing of this chunk: its products go between the
       // steps of the solution, each of which waits for the one before
@@ -1041,8 +1058,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
             }
             // registers 0, 1: rows g, g + 8 of the first eight steps; 2, 3: of the others
             const float2 l = *(const float2*)&g.lead[16 * k + 8 * (w >> 1) + c2];
-            z[2 * k + (w >> 1)][2 * (w & 1)] = s.x * so * l.x;
-            z[2 * k + (w >> 1)][2 * (w & 1) + 1] = s.y * so * l.y;
+            z[2 * k + (w >> 1)][2 * (w & 1)] = s.x * so[w & 1] * l.x;
+            z[2 * k + (w >> 1)][2 * (w & 1) + 1] = s.y * so[w & 1] * l.y;
           }
         }
         sz = row_scales(row_max<NC>(z));
@@ -1162,7 +1179,7 @@ template <int NI, int DK, int WK>
 cudaError_t back_t(const DeltaBack& p, cudaStream_t s) {
   using G = Geom<NI, DK, WK, 1>;
   constexpr size_t smem = G::smem;
-  static_assert(smem <= 232448, "");
+  static_assert(smem + 16 * kVB <= 232448, "");
   const cudaError_t e = cudaFuncSetAttribute(k_delta_back<NI, DK, WK>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

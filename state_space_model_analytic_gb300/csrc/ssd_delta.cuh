@@ -459,7 +459,6 @@ template <int C>
 struct alignas(16) Gates {
   float hi[C], lo[C], lead[C], tail[C], beta[C], kup[C], qdown[C], xs[C], bx[C];
   float last;    // e^G
-  float dout;    // the walk back: what dO's tile was divided by
 };
 
 struct Two {
@@ -557,7 +556,6 @@ template <int C>
 struct alignas(16) Scratch {
   float diag[C / 16][16][kDiag];  // L[i][j] at [j][i], a warp each
   uint8_t t[C / 16][kParts * 512];  // T of the diagonal blocks, transposed like X, in parts
-  float most[kPrep / 32];
 };
 
 // One block of 16 x 16, rows 16 bi ..., columns 16 bj ..., of L and, with kP, of P, which

@@ -106,6 +106,41 @@ def test_states_of_alike_keys(shape, kind):
     rounded_once(host(o), ro, (1, 3))
 
 
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_bad_gradient_stays_in_its_column(dtype, bad):
+    """Columns of v are independent of one another on the way back too: dv and dstate0
+    are what they are without the bad value in all other columns."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(2, 200, 2, 1, 64, 64, dtype, 85)
+    x, do = operands(inp, dtype), dev(inp["do"], dtype)
+    s0, ds = dev(inp["state0"]), dev(inp["dstate"])
+    g = ssd.delta_rule_backward(*x, s0, do, ds)
+    do[0, 70, 1, 5] = bad
+    h = ssd.delta_rule_backward(*x, s0, do, ds)
+    assert not torch.isfinite(h["dv"][0, :71, 1, 5]).any()
+    assert not torch.isfinite(h["dstate0"][0, 1, 5]).any()
+    keep = torch.ones_like(g["dv"], dtype=torch.bool)
+    keep[0, :, 1, 5] = False
+    assert torch.equal(h["dv"][keep], g["dv"][keep])
+    keep = torch.ones_like(g["dstate0"], dtype=torch.bool)
+    keep[0, 1, 5] = False
+    assert torch.equal(h["dstate0"][keep], g["dstate0"][keep])
+
+
+@pytest.mark.parametrize("H", [2, 80])
+def test_columns_of_different_size(H):
+    """dout's columns from 1 to 2^-40: each column's dv and dstate0 keep their bits."""
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(1, 130, H, H, 64, 64, "f32", 86)
+    inp["do"] = inp["do"] * np.exp2(-(np.arange(64) % 41.0))
+    g = ssd.delta_rule_backward(*operands(inp, "f32"), None, dev(inp["do"]))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), None, inp["do"])
+    close(host(g["dv"]), ref["dv"], (0, 1))
+    close(host(g["dstate0"]), ref["dstate0"], (0, 3))
+
+
 def spread(n, least):
     """1 ... 2^-least over n elements, in an order that is not theirs."""
     return np.exp2(-(np.arange(n) * 7 % (least + 1.0)))

@@ -22,6 +22,14 @@
 // Q come during the first products, which need neither.  Heads that share q and k
 // write their own gradients in fp32, summed in head order by a second kernel.
 //
+// Scales.  With rows of dO, dv, U, q and k in [1, 2) times a power of two each, the tiles
+// of MP and ML hold Gamma_ij times the products of such rows: at most 2^9, whatever the
+// rows' powers are.  The power of the output's row is multiplied in at the end; the other
+// one goes by the share that a step has in the sum (what it writes, U_j k_j, for dq and
+// dk's first part; what it reads, dO_i q_i or dv_i k_i, for its second) and is multiplied
+// into the left operand's columns, relative to the chunk's largest share.  So a step's dq
+// does not depend on the size of its q, nor dk on that of k.
+//
 // 4 x 2048 steps of 32 heads 128/64 (bf16): 388 us for 4096 items of 27 thousand cycles,
 // where the 709 MB it reads and writes take 106.  Of an item the splitting takes 6 thousand
 // cycles, the products with H and D 6 (tensor pipe and shared memory), the scores and masks
@@ -75,6 +83,21 @@ __device__ __forceinline__ float sum_lanes(float x) {
   for (int d = N / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
   return x;
 }
+// the power of two below |x| (1 for zero, infinities and NaN)
+__device__ __forceinline__ float pow2_of(float x) {
+  const uint32_t e = __float_as_uint(x) & 0x7f800000u;
+  return e == 0 || e == 0x7f800000u ? 1.f : __uint_as_float(e);
+}
+// a left operand's columns (terms) 2 t, 2 t + 1 times lo, those at + 8 times hi
+__device__ __forceinline__ void times_terms(uint32_t (&a)[kParts][4], __half2 lo, __half2 hi) {
+#pragma unroll
+  for (int q = 0; q < kParts; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 x = __hmul2(*(const __half2*)&a[q][e], e < 2 ? lo : hi);
+      a[q][e] = *(const uint32_t*)&x;
+    }
+}
 // the largest of x >= 0 over a warp and *top, whose bits are in the order of the values
 __device__ __forceinline__ void max_of_all(uint32_t* top, float x, int lane) {
   const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(x));
@@ -97,9 +120,12 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
   __shared__ float most[2][3][C], down[2][3][C], qdown[C], kdown[C], dbeta[C];
   __shared__ float rows_of[G::WC][C], cols_of[2][G::WR][C], reads[G::WC][C], writes[G::WC][C];
   __shared__ float hdots[NW];
-  // the bits of the largest of H and D and of MP and ML
+  // the bits of the largest of H and D
   __shared__ __align__(8) uint32_t top_state[2][2];
-  __shared__ uint32_t top_mask[2];
+  // the largest of the steps' q and k; their shares (written; read by q and by k), as
+  // powers of two of at most 1, and what these were divided by
+  __shared__ float qmost[C], kmost[C], share_down[2];
+  __shared__ __align__(4) __half share[3][C];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // (the warps of a sub-core, four apart, have different strips: the later ones have more
   // of MP and ML)
@@ -175,7 +201,9 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
       p.dlog_decay[(token + r) * p.H + x.h] = p.dbeta[(token + r) * p.H + x.h] = 0.f;
   }
 
-  if (tid < 2) top_state[0][tid] = top_state[1][tid] = top_mask[tid] = 0;
+  if (tid < 2) top_state[0][tid] = top_state[1][tid] = 0;
+  // scale: a power of two and a factor of at most 2
+  const float s2 = pow2_of(p.scale), s1 = p.scale / s2;
   Item x, nx;
   nx.n = 0;
   uint32_t i = next_of(blockIdx.x, x);
@@ -346,8 +374,14 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
     }
     copy_commit();
     {
-      auto q_done = [&](int r, float s, float) { qdown[r] = inverse_pow2(s); };
-      auto k_done = [&](int r, float s, float) { kdown[r] = inverse_pow2(s); };
+      auto q_done = [&](int r, float s, float m) {
+        qdown[r] = inverse_pow2(s);
+        qmost[r] = m;
+      };
+      auto k_done = [&](int r, float s, float m) {
+        kdown[r] = inverse_pow2(s);
+        kmost[r] = m;
+      };
       if constexpr (NI == 2) {
         FloatRows<C, DK, NT> q, k;
         q.read(sm, tid);
@@ -394,15 +428,51 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         writes[group][r] = write;
       }
     }
-    // MP or ML, of q's and k's scales, and their products with the scores
-    float largest = 0.f;
+    uint8_t* Mt = sm + G::kH + (buf ^ 1) * 2 * G::HT;  // the last piece's H and D
+    if (group == 1 && strip == 0) {  // (a warp without columns of MP)
+      float w[C / 32], rq[C / 32], rk[C / 32], top_w = 0.f, top_r = 0.f;
+#pragma unroll
+      for (int k = 0; k < C / 32; ++k) {
+        const int r = k * 32 + lane;
+        const bool uu = most[last][0][r] > 0.f, vv = most[last][1][r] > 0.f, oo = most[last][2][r] > 0.f;
+        const bool kk = kmost[r] > 0.f, qq = qmost[r] > 0.f;
+        w[k] = uu && kk ? udown[r] * kdown[r] : 0.f;
+        rq[k] = oo && qq ? s2 * odown[r] * qdown[r] : 0.f;
+        rk[k] = vv && kk ? vdown[r] * kdown[r] : 0.f;
+        top_w = fmaxf(top_w, w[k]);
+        top_r = fmaxf(top_r, fmaxf(rq[k], rk[k]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        top_w = fmaxf(top_w, __shfl_xor_sync(0xffffffffu, top_w, o));
+        top_r = fmaxf(top_r, __shfl_xor_sync(0xffffffffu, top_r, o));
+      }
+      // (the quotient of two powers of two; of zero there is no share)
+      const auto part_of = [](float x, float top) { return __float2half_rn(top > 0.f ? x / top : 0.f); };
+#pragma unroll
+      for (int k = 0; k < C / 32; ++k) {
+        const int r = k * 32 + lane;
+        share[0][r] = part_of(w[k], top_w);
+        share[1][r] = part_of(rq[k], top_r);
+        share[2][r] = part_of(rk[k], top_r);
+      }
+      if (lane == 0) {
+        share_down[0] = top_w;
+        share_down[1] = top_r;
+      }
+    }
+    // MP or ML as their tiles hold them (times 2^kMask), and the products with the scores
+    constexpr int kMask = 5;
+    constexpr float kMaskUp = 1 << kMask, kMaskDown = 1.f / kMaskUp;
     {
       const uint32_t A = is_l ? sK : sQ;
+      uint8_t* tile = Mt + (is_l ? G::HT : 0);
+      const float held = is_l ? -kMaskUp : kMaskUp * s1;
       float row[2] = {0.f, 0.f}, f[2], hi[2], lo[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int i = i0 + 8 * u;
-        f[u] = is_l ? -vdown[i] * kdown[i] : p.scale * odown[i] * qdown[i];
+        f[u] = (is_l ? vdown[i] * kdown[i] : s2 * odown[i] * qdown[i]) * kMaskDown;
         hi[u] = g.hi[i];
         lo[u] = g.lo[i];
       }
@@ -433,16 +503,18 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
               const int i = i0 + 8 * u;
               const float2 minus = both(-1.f);
               const float2 t = add2(fma2(hj, minus, both(hi[u])), fma2(lj, minus, both(lo[u])));
-              float2 v = mul2(mul2(mul2(pair(m, u), both(f[u])), fj),
-                              make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+              float2 v = mul2(mul2(pair(m, u), both(held)), make_float2(exp2_fast(t.x), exp2_fast(t.y)));
               if (m0 + e == 2 * strip) {  // (the diagonal's columns)
                 const int above = is_l ? 1 : 0;
                 if (j + above > i) v.x = 0.f;
                 if (j + 1 + above > i) v.y = 0.f;
               }
-              set_pair(m, u, v);
-              largest = max3_abs(largest, v.x, v.y);
-              const float2 c = mul2(v, pair(s[q], u));
+              uint32_t a[kParts];
+              split2<kParts>(v, a);
+              uint8_t* at = tile + at16<PB>(i, m0 + e + q) + c2 * 2;
+#pragma unroll
+              for (int w = 0; w < kParts; ++w) *(uint32_t*)(at + w * C * PB) = a[w];
+              const float2 c = mul2(mul2(v, both(f[u])), mul2(fj, pair(s[q], u)));
               row[u] += c.x + c.y;
               col = add2(col, c);
             }
@@ -461,32 +533,12 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         if ((lane & 3) == 0) rows_of[group][i0 + 8 * u] = row[u];
       }
     }
-    max_of_all(&top_mask[turn], largest, lane);
     hdot = sum_lanes<32>(hdot);
     if (lane == 0) hdots[warp] = hdot;
-    __syncthreads();
-    const Scale smask = scale_to<10>(__uint_as_float(top_mask[turn]));
-    uint8_t* Mt = sm + G::kH + (buf ^ 1) * 2 * G::HT;  // the last piece's H and D
-    {
-      uint8_t* out = Mt + (is_l ? G::HT : 0);
-#pragma unroll
-      for (int e = 0; e < NM; ++e)
-        if (m0 + e <= 2 * strip + 1) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t a[kParts];
-            split2<kParts>(mul2(pair(mm[e], u), both(smask.up)), a);
-            uint8_t* at = out + at16<PB>(i0 + 8 * u, m0 + e) + c2 * 2;
-#pragma unroll
-            for (int q = 0; q < kParts; ++q) *(uint32_t*)(at + q * C * PB) = a[q];
-          }
-        }
-    }
     __syncthreads();
     if (warp == 0) {
       // dg, and its sums from each step to the end, in two floats
       constexpr int N = C / 32;
-      if (lane == 0) top_mask[turn] = 0;
       Two d[N], total = {0.f, 0.f};
       float tails = 0.f, hd = 0.f;
       for (int k = lane; k < NW; k += 32) hd += hdots[k];
@@ -534,8 +586,17 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
     TO* dk_out = (kShared ? (TO*)(part + (long long)p.B * p.T * p.H * p.dk) : (TO*)p.dk_out) +
                  token * out_step + (long long)x.h * p.dk;
     const uint32_t sP = smem32(Mt), sL = sP + G::HT;
-    const float up_q[2] = {smask.down * inverse_pow2(qdown[i0]), smask.down * inverse_pow2(qdown[i0 + 8])};
-    const float up_k[2] = {smask.down * inverse_pow2(kdown[i0]), smask.down * inverse_pow2(kdown[i0 + 8])};
+    // of the rows of MP K, ML K and of the sum of MP^T Q and ML^T K
+    float up_q[2], up_r[2], up_w[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = i0 + 8 * u;
+      up_q[u] = s2 * odown[r] * (share_down[0] * kMaskDown);
+      up_r[u] = vdown[r] * (share_down[0] * kMaskDown);
+      up_w[u] = udown[r] * (share_down[1] * kMaskDown);
+    }
+    // the shares of steps 16 k + 2 t, 16 k + 2 t + 1 and those at + 8
+    const auto share_of = [&](int which, int at) { return *(const __half2*)&share[which][at + c2]; };
 #pragma unroll
     for (int e = 0; e < NK; e += 2) {
       const int c = (group * NK + e) * 8;
@@ -550,9 +611,12 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         if (k <= strip) {  // columns 16 k ... of MP, ML
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4(a[q], lm.left(sP, 16 * strip, 16 * k) + q * C * PB);
+          const __half2 w0 = share_of(0, 16 * k), w1 = share_of(0, 16 * k + 8);
+          times_terms(a, w0, w1);
           mma_parts<kParts, NI, 2>(d[0], a, rk);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4(a[q], lm.left(sL, 16 * strip, 16 * k) + q * C * PB);
+          times_terms(a, w0, w1);
           mma_parts<kParts, NI, 2>(d[1], a, rk);
         }
         if (k >= strip) {  // rows 16 k ...
@@ -560,9 +624,11 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
           load_right_t<NI, 2>(rq, sQ, C * RB, lk, c, 16 * k);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4t(a[q], lm.left_t(sP, 16 * strip, 16 * k) + q * C * PB);
+          times_terms(a, share_of(1, 16 * k), share_of(1, 16 * k + 8));
           mma_parts<kParts, NI, 2>(d[2], a, rq);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4t(a[q], lm.left_t(sL, 16 * strip, 16 * k) + q * C * PB);
+          times_terms(a, share_of(2, 16 * k), share_of(2, 16 * k + 8));
           mma_parts<kParts, NI, 2>(d[2], a, rk);
         }
       }
@@ -574,8 +640,9 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
           if (r < x.n && cc < p.dk) {
             put_pair(dq_out + r * out_step + cc,
                      fma2(pair(d[0][q], u), both(up_q[u]), pair(dq[e + q], u)));
-            const float2 dk = fma2(add2(pair(d[1][q], u), pair(d[2][q], u)), both(up_k[u]),
-                                   add2(pair(rd[e + q], u), pair(wr[e + q], u)));
+            const float2 dk = fma2(pair(d[1][q], u), both(up_r[u]),
+                                   fma2(pair(d[2][q], u), both(up_w[u]),
+                                        add2(pair(rd[e + q], u), pair(wr[e + q], u))));
             put_pair(dk_out + r * out_step + cc, dk);
           }
         }

@@ -141,6 +141,41 @@ def test_columns_of_different_size(H):
     close(host(g["dstate0"]), ref["dstate0"], (0, 3))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_a_query_do_not_depend_on_it(dtype):
+    """dq is the state's product with dout: queries of any size (2^-30 ... 2^30, zero)
+    have the same, bit for bit; and dv and dk go by what the steps read."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(2, 150, 3, 3, 64, 128, dtype, 87)
+    rng = np.random.default_rng(88)
+    q, k, v, la, be = operands(inp, dtype)
+    s0, do = dev(inp["state0"]), dev(inp["do"], dtype)
+    f = np.exp2(rng.integers(-30, 31, (2, 150, 3, 1)))
+    f[:, 7] = 0
+    g = ssd.delta_rule_backward(q, k, v, la, be, s0, do)
+    h = ssd.delta_rule_backward((q.float() * dev(f)).to(q.dtype), k, v, la, be, s0, do)
+    assert torch.equal(g["dq"], h["dq"])
+    inp["q"] = inp["q"] * f
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), inp["state0"], inp["do"])
+    # (f32 results of the rows before the largest reads; a bf16 one is rounded besides)
+    for n in ("dk", "dv"):
+        close(host(h[n]), ref[n], (1, 3), 2.0 ** -9 if dtype == "bf16" else RMS)
+
+
+def test_gradients_of_short_keys():
+    """Steps whose keys are 2^-30 of the others': their dk goes by v and the state's
+    gradient, not by the key."""
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(1, 150, 2, 2, 64, 64, "f32", 89)
+    inp["k"][:, 3::7] *= 2.0 ** -30
+    g = ssd.delta_rule_backward(*operands(inp, "f32"), dev(inp["state0"]), dev(inp["do"]), dev(inp["dstate"]))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), inp["state0"], inp["do"], inp["dstate"])
+    close(host(g["dk"])[:, 3::7], ref["dk"][:, 3::7])
+    for n in GRADS[:3]:
+        close(host(g[n]), ref[n])
+
+
 def spread(n, least):
     """1 ... 2^-least over n elements, in an order that is not theirs."""
     return np.exp2(-(np.arange(n) * 7 % (least + 1.0)))

@@ -327,13 +327,21 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
  * gradient is zero.  The kernels have no waits that could run out.
  *
  * Precision: states, sums and decays are fp32 in either type.  A value held in 32
- * bits enters a product as two fp16 parts (22 bits) of its row scaled by a power of
- * two, a bf16 element as it is; elements below 2^-24 of the largest of their row of
- * the state (of their step, for q, k, v and dout in fp32) lose bits.  Results do not
- * depend on powers of two in a step's q, k or v, as long as the largest element of a
- * key is between 2^-63 and 2^63 and beta times its square is a normal number.
- * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.  
- * bf16 results (o, dq, dk, dv) are off by their own rounding, 0.0017 of their root mean
+ * bits enters a product as two fp16 parts (22 bits), a bf16 element as it is, scaled
+ * by a power of two of its row.  An element keeps its bits down to 2^-16 of the row's
+ * largest (bf16: 2^-30), from there on one less for each power of two, none below
+ * 2^-38.  Rows are: a step's q, k, v, dout over its elements; a state's rows, and 64 of
+ * them together where dq, dk and dlog_decay are formed; a column of v over a chunk (64
+ * steps, 32 in fp32) of what is written (beta e) and of dout times the largest element
+ * of the step's q.  What one step of a chunk reads of another's write counts down to
+ * 2^-30 of the product of q's or k's largest elements, and steps add to each other's
+ * gradients by their shares dout q^T and beta e k^T, relative to the chunk's largest.
+ * Results do not depend on powers of two in a step's q (and dout for its inverse), or
+ * in k and v with beta for the inverse of their square, as long as the largest element
+ * of a key is between 2^-63 and 2^63, beta times its square a normal number and v
+ * divided by it finite.  States are not scaled up further below 2^-87.
+ * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.  bf16
+ * results (o, dq, dk, dv) are off by their own rounding, 0.0017 of their root mean
  * square.
  */
 

@@ -122,12 +122,14 @@ __device__ __forceinline__ void times(float (&x)[4], float2 f) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) set_pair(x, u, mul2(pair(x, u), f));
 }
-// the scales of a warp's rows from its lanes' largest values
+// the scales of a warp's rows from its lanes' largest values, for products with a tile
+// that holds 2^kLess times its values
 struct RowScales {
   float up0, down0, up1, down1;
 };
+template <int kLess>
 __device__ __forceinline__ RowScales row_scales(float2 m) {
-  const Scale a = scale_to<10>(quad_max(m.x)), b = scale_to<10>(quad_max(m.y));
+  const Scale a = scale_to<kLift, kLess>(quad_max(m.x)), b = scale_to<kLift, kLess>(quad_max(m.y));
   return {a.up, a.down, b.up, b.down};
 }
 
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
       auto k_done = [&](int r, float s, float) {
         g.kup[r] = s;
         const float d = inverse_pow2(s);
-        g.beta[r] *= d * d;
+        g.beta[r] = g.beta[r] * d * d;
       };
       auto q_done = [&](int r, float s, float) { g.qdown[r] = p.scale * inverse_pow2(s); };
       if constexpr (NI == 1) {
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
       // f: F^T, then U^T.  o: O^T of the blocks that this warp writes, without s and of
       // q's scale
       float f[NC][4], o[2 * OB][4];
-      const RowScales sx = row_scales(most);
+      const RowScales sx = row_scales<kLift>(most);
       {
         float qx[NC][4];
         state_times<NI, kOwn, DK, NK, NC>(f, qx, x, sx, K, Q, k0, la,
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
 #pragma unroll
             for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), bx));
           }
-          const RowScales sy = row_scales(row_max<2>(y));
+          const RowScales sy = row_scales<0>(row_max<2>(y));
           as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
 #pragma unroll
           for (int i = 2 * k + 2; i < NC; i += 2) {
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
             times(f[2 * k + q], *(const float2*)&g.beta[at]);
           }
           uint32_t ao[kParts][4];  // U for o
-          const RowScales su = row_scales(row_max<2>(f + 2 * k));
+          const RowScales su = row_scales<kScore>(row_max<2>(f + 2 * k));
           as_left<kParts>(ao, f[2 * k], f[2 * k + 1], su.up0, su.up1);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) given.put(given.u(k, q, lane), ao[q]);
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
 #pragma unroll
             for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), bx));
           }
-          const RowScales sy = row_scales(row_max<2>(y));
+          const RowScales sy = row_scales<0>(row_max<2>(y));
           as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
           mma_short(d, a, r);
           if (k > 0) rest(k - 1);
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
                 }
             }
           }
-          su = row_scales(row_max<2>(f + 2 * k));
+          su = row_scales<kScore>(row_max<2>(f + 2 * k));
           as_left<kParts>(au, f[2 * k], f[2 * k + 1], su.up0, su.up1);
           if (k + 1 < NB) {
             load_right<kParts, 2>(r, M, C * G::PB, lm, 16 * k + 16, 16 * k);
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
       uint32_t y[NB][kParts][4];
 #pragma unroll
       for (int i = 0; i < NC; ++i) times(f[i], *(const float2*)&g.tail[8 * i + c2]);
-      const RowScales sw = row_scales(row_max<NC>(f));
+      const RowScales sw = row_scales<kLift>(row_max<NC>(f));
 #pragma unroll
       for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
       constexpr int kGroups = NK < 4 ? 1 : NK / 4;
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       auto k_done = [&](int r, float s, float) {
         g.kup[r] = s;
         const float d = inverse_pow2(s);
-        g.beta[r] *= d * d;
+        g.beta[r] = g.beta[r] * d * d;
       };
       auto q_done = [&](int r, float s, float) { g.qdown[r] = inverse_pow2(s); };
       // dO: a thread's eights (NI == 1) or fours of elements, of the same columns
@@ -914,10 +916,10 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       bar(1, kPrep);
       if (tid < kVB) {
         top_out[(c & 1) ^ 1][tid] = 0;  // (read a chunk ago)
-        out_down[c & 1][tid] = scale_to<10>(__uint_as_float(top_out[c & 1][tid])).down;
+        out_down[c & 1][tid] = scale_to<kLift>(__uint_as_float(top_out[c & 1][tid])).down;
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) m[e] = scale_to<10>(__uint_as_float(top_out[c & 1][v8 + e])).up;
+      for (int e = 0; e < E; ++e) m[e] = scale_to<kLift>(__uint_as_float(top_out[c & 1][v8 + e])).up;
 #pragma unroll
       for (int i = 0; i < ND; ++i) {
         const int r = (i * kPrep + tid) / LPR;
@@ -993,7 +995,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
       const int n = min(C, len - c * C);
       float f[NC][4];  // dU^T, then dv^T
       {
-        const RowScales sx = row_scales(most);
+        const RowScales sx = row_scales<kLift>(most);
         // (the state is stored between the products: all at once the warp waited 1400
         // cycles for its own stores)
         state_times<NI, false, DK, NK, NC>(f, f, x, sx, K, K, k0, la, [&](int k, const uint32_t (&)[kParts][4]) {
@@ -1036,7 +1038,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            set_pair(f[2 * k + q], u, fma2(both(so[u]), pair(d[q], u), pair(f[2 * k + q], u)));
+            set_pair(f[2 * k + q], u,
+                     fma2(both(so[u] * pow2(-kScore)), pair(d[q], u), pair(f[2 * k + q], u)));
       };
       // what dO adds to D waits for nothing of this chunk: its products go between the
       // steps of the solution, each of which waits for the one before
@@ -1062,7 +1065,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
             z[2 * k + (w >> 1)][2 * (w & 1) + 1] = s.y * so[w & 1] * l.y;
           }
         }
-        sz = row_scales(row_max<NC>(z));
+        sz = row_scales<kLift>(row_max<NC>(z));
 #pragma unroll
         for (int k = 0; k < NB; ++k) as_left<kParts>(zo[k], z[2 * k], z[2 * k + 1], sz.up0, sz.up1);
       }
@@ -1102,7 +1105,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
 #pragma unroll
           for (int u = 0; u < 2; ++u) set_pair(y[q], u, mul2(pair(f[2 * k + q], u), be));
         }
-        const RowScales sy = row_scales(row_max<2>(y));
+        const RowScales sy = row_scales<0>(row_max<2>(y));
         as_left<kParts>(a, y[0], y[1], sy.up0, sy.up1);
         mma_short(d, a, r);
         if (k + 1 < NB) rest(k + 1);
@@ -1132,7 +1135,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
                          p.dv, lane);
           }
         }
-        su = row_scales(row_max<2>(f + 2 * k));
+        su = row_scales<kScore>(row_max<2>(f + 2 * k));
         as_left<kParts>(av, f[2 * k], f[2 * k + 1], su.up0, su.up1);
         if (k > 0) {
           load_right_t<kParts, 2>(r, M, C * G::PB, lm, 16 * k - 16, 16 * k);
@@ -1147,7 +1150,7 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         times(f[i], make_float2(-l.x, -l.y));
       }
       {
-        const RowScales sw = row_scales(row_max<NC>(f));
+        const RowScales sw = row_scales<kLift>(row_max<NC>(f));
 #pragma unroll
         for (int k = 0; k < NB; ++k) as_left<kParts>(y[k], f[2 * k], f[2 * k + 1], sw.up0, sw.up1);
         most = state_add<NI, DK, NK, NB>(x, 1.f, y, sw, K, k0, la, [](int) {});

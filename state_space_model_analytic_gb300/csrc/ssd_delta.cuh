@@ -26,7 +26,12 @@
 // taken such that the largest element of k is in [1, 2); L, X, E and U below are those
 // of the rows so scaled ("of k's scale").  Queries the same way, 2^-n going into the
 // output.  Left operands (the state, U and so on) are scaled row by row, by the
-// largest element; what is 2^-24 of that and less loses bits, as it would in a sum.
+// largest element.
+//
+// Every tile and left operand holds its values times 2^kLift more than that (L and P,
+// which are below 2^9, times 2^kScore), so that the second part, whose last bit is 2^-24,
+// is whole down to 2^-16 of a row's largest element; from there on an element has a bit
+// less for each power of two, and below 2^-39 it is zero.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,6 +49,7 @@ namespace delta {
 constexpr int kPrep = 256;   // threads that prepare the next chunk
 constexpr int kVB = 64;      // columns of v of a tile
 constexpr int kParts = 2;    // parts of a value held in 32 bits
+constexpr int kLift = 14, kScore = 6;
 
 // Byte offset of a 16-byte piece of a tile whose rows are RB bytes: pieces of
 // eight consecutive rows fall on all 32 banks.
@@ -96,23 +102,28 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   return d;
 }
 
-// The power of two that brings m > 0 into [2^T, 2^{T+1}), and its inverse; infinities
-// and NaN stay what they are.
+constexpr float pow2(int n) { return n < 0 ? 0.5f * pow2(n + 1) : n ? 2.f * pow2(n - 1) : 1.f; }
+
+// The power of two that brings m > 0 into [2^T, 2^{T+1}), and the inverse of 2^kLess times
+// it (kLess: what the other operand is multiplied by); infinities and NaN stay what they
+// are, and what is below 2^-87 is multiplied as if it were that.
 struct Scale {
   float up, down;
 };
-template <int T>
+template <int T, int kLess = 0>
 __device__ __forceinline__ Scale scale_to(float m) {
+  static_assert(T + kLess < 40, "");
   int e = (int)(__float_as_uint(m) >> 23);  // (m >= 0)
-  e = e < 40 ? 40 : e > 250 ? 250 : e;
-  return {__uint_as_float((uint32_t)(254 + T - e) << 23), __uint_as_float((uint32_t)(e - T) << 23)};
+  e = e < 40 ? 40 : e > 254 ? 254 : e;
+  return {__uint_as_float((uint32_t)(254 + T - e) << 23), __uint_as_float((uint32_t)(e - T - kLess) << 23)};
 }
-// The same for a row of steps: into [1, 2), by 2^-kFar to 2^kFar, rows of zeros as they
-// are.  (For k and q kFar is 63: beta is divided by the square.)
+// The same for a row of steps: into [1, 2), by 2^kFar at most, rows of zeros as they are.
+// (For k and q kFar is 63: beta is divided by the square.)
 template <int kFar>
 __device__ __forceinline__ float row_exponent(float m) {
+  static_assert(kFar + kLift <= 127, "");
   int e = (int)(__float_as_uint(m) >> 23);
-  e = m == 0.f ? 127 : e < 127 - kFar ? 127 - kFar : e > 127 + kFar ? 127 + kFar : e;
+  e = m == 0.f ? 127 : e < 127 - kFar ? 127 - kFar : e > 253 ? 253 : e;
   return __uint_as_float((uint32_t)(254 - e) << 23);
 }
 __device__ __forceinline__ float inverse_pow2(float x) {
@@ -354,7 +365,7 @@ __device__ __forceinline__ uint4 bf_to_half(const uint4& q, float s) {
 }
 __device__ __forceinline__ float no_least(int) { return 0.f; }
 // A bf16 tile to fp16 in its place: a thread's elements are read, and written row by
-// row, each scaled into [1, 2), or by no more than `least(row)` would be; done(row,
+// row, each scaled into [1, 2) (and by 2^kLift), or by no more than `least(row)` would be; done(row,
 // scale, largest) by one lane a row.
 template <int C, int DK, int NT>
 struct HalfRows {
@@ -382,7 +393,7 @@ struct HalfRows {
       const int at = i * NT + tid, r = at / LPR, x = at % LPR;
       const float most = fmaxf(fmaxf(__low2float(m[i]), __high2float(m[i])), least(r));
       const float s = row_exponent<kFar>(most);
-      *(uint4*)(tile + at16<DK * 2>(r, x)) = bf_to_half(q[i], s);
+      *(uint4*)(tile + at16<DK * 2>(r, x)) = bf_to_half(q[i], s * pow2(kLift));
       if (x == 0) done(r, s, most);
     }
   }
@@ -427,8 +438,8 @@ struct FloatRows {
     *(uint2*)to = make_uint2(p[0], q[0]);
     *(uint2*)(to + C * DK * 2) = make_uint2(p[1], q[1]);
   }
-  // each row scaled into [1, 2), or by no more than `least(row)` would be; done(row,
-  // scale, largest) by one lane a row
+  // each row scaled into [1, 2) (and by 2^kLift), or by no more than `least(row)` would
+  // be; done(row, scale, largest) by one lane a row
   template <int kFar = 63, typename F, typename L>
   __device__ __forceinline__ void write(uint8_t* tile, int tid, L least, F done) const {
     float m[N];
@@ -444,7 +455,7 @@ struct FloatRows {
       const int at = i * NT + tid;
       m[i] = fmaxf(m[i], least(at / LPR));
       const float s = row_exponent<kFar>(m[i]);
-      put(tile, i, s, tid);
+      put(tile, i, s * pow2(kLift), tid);
       if (at % LPR == 0) done(at / LPR, s, m[i]);
     }
   }
@@ -548,7 +559,7 @@ __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float
 
 // What the walks read of a chunk besides its operands, in parts: a tile M [C][C] with -L
 // below the blocks of 16 on the diagonal, in them -X^T, its rows scaled, and above them
-// P, block (i, j) in the place of block (j, i), as it is; and P's diagonal blocks, a tile
+// P, block (i, j) in the place of block (j, i), as it is (L and P times 2^kScore); and P's diagonal blocks, a tile
 // [C][16] (kPRow bytes a row).
 constexpr int kPRow = 32;
 constexpr int kDiag = 20;  // floats of a column of a diagonal block
@@ -597,12 +608,14 @@ __device__ __forceinline__ void score_block(uint32_t Q, uint32_t K, uint8_t* M, 
       // Gamma_ij = 2^((hi_i - hi_j) + (lo_i - lo_j))
       const float2 minus = both(-1.f);
       const float2 t = add2(fma2(hj, minus, both(gi[8 * u])), fma2(lj, minus, both(gi[C + 8 * u])));
-      const float2 gamma = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+      // (the operands' factors off, the scores' on)
+      const float2 gamma = mul2(make_float2(exp2_fast(t.x), exp2_fast(t.y)),
+                                both(pow2(kScore - 2 * kLift)));
       float2 l = mul2(pair(acc[0][n], u), gamma);
       const uint32_t to = at16<OB>(16 * bi + i, 2 * bj + n) + c0 * 2;
       if constexpr (kDiagonal) {
-        diag[j][i] = j < i ? l.x : 0.f;
-        diag[j + 1][i] = j + 1 < i ? l.y : 0.f;
+        diag[j][i] = j < i ? l.x * pow2(-kScore) : 0.f;
+        diag[j + 1][i] = j + 1 < i ? l.y * pow2(-kScore) : 0.f;
       } else {
         uint32_t p[kParts];
         split2<kParts>(make_float2(-l.x, -l.y), p);
@@ -654,7 +667,7 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, uint8_t* tt, Gates<C>&
   for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(kT ? tm[i] : x[i]));
   // (an element of L is at most 2^9, so one of X = L T, and of the folded blocks, is below
   // 2^15 where T's are below 4)
-  const Scale sx = scale_to<kT ? 1 : 8>(m);
+  const Scale sx = scale_to<kT ? 1 : kLift>(m);
   g.xs[16 * s + j] = sx.down;
   g.bx[16 * s + j] = sx.down * g.beta[16 * s + j];
 #pragma unroll
@@ -679,7 +692,7 @@ __device__ __forceinline__ void invert_diag(uint8_t* out, uint8_t* tt, Gates<C>&
 }
 
 // A block of M below the diagonal, rows 16 bi ..., columns 16 bj ...: -L T in the place
-// of -L.
+// of -L (as it is: T has its own factor).
 template <int C>
 __device__ __forceinline__ void fold_block(uint8_t* M, const uint8_t* tt, int bi, int bj, int lane) {
   constexpr int OB = C * 2;
@@ -696,7 +709,7 @@ __device__ __forceinline__ void fold_block(uint8_t* M, const uint8_t* tt, int bi
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t p[kParts];
-      split2<kParts>(pair(d[n], u), p);
+      split2<kParts>(mul2(pair(d[n], u), both(pow2(-kScore))), p);
       uint8_t* to = M + at16<OB>(16 * bi + (lane >> 2) + 8 * u, 2 * bj + n) + (lane & 3) * 4;
 #pragma unroll
       for (int q = 0; q < kParts; ++q) *(uint32_t*)(to + q * C * OB) = p[q];

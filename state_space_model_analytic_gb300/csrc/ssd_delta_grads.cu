@@ -27,7 +27,7 @@
 // rows' powers are.  The power of the output's row is multiplied in at the end; the other
 // one goes by the share that a step has in the sum (what it writes, U_j k_j, for dq and
 // dk's first part; what it reads, dO_i q_i or dv_i k_i, for its second) and is multiplied
-// into the left operand's columns, relative to the chunk's largest share.  So a step's dq
+// into the right operand's rows, relative to the chunk's largest share.  So a step's dq
 // does not depend on the size of its q, nor dk on that of k.
 //
 // 4 x 2048 steps of 32 heads 128/64 (bf16): 388 us for 4096 items of 27 thousand cycles,
@@ -88,15 +88,19 @@ __device__ __forceinline__ float pow2_of(float x) {
   const uint32_t e = __float_as_uint(x) & 0x7f800000u;
   return e == 0 || e == 0x7f800000u ? 1.f : __uint_as_float(e);
 }
-// a left operand's columns (terms) 2 t, 2 t + 1 times lo, those at + 8 times hi
-__device__ __forceinline__ void times_terms(uint32_t (&a)[kParts][4], __half2 lo, __half2 hi) {
+// a right operand's terms 2 t, 2 t + 1 times lo, those at + 8 times hi
+template <int NI>
+__device__ __forceinline__ void times_terms(uint32_t (&r)[NI][2][2], const uint32_t (&b)[NI][2][2],
+                                            __half2 lo, __half2 hi) {
 #pragma unroll
-  for (int q = 0; q < kParts; ++q)
+  for (int q = 0; q < NI; ++q)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __half2 x = __hmul2(*(const __half2*)&a[q][e], e < 2 ? lo : hi);
-      a[q][e] = *(const uint32_t*)&x;
-    }
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const __half2 x = __hmul2(*(const __half2*)&b[q][n][e], e ? hi : lo);
+        r[q][n][e] = *(const uint32_t*)&x;
+      }
 }
 // the largest of x >= 0 over a warp and *top, whose bits are in the order of the values
 __device__ __forceinline__ void max_of_all(uint32_t* top, float x, int lane) {
@@ -287,7 +291,9 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         }
         __syncthreads();
         const uint2 top = *(const uint2*)top_state[buf];
-        const Scale sh = scale_to<10>(__uint_as_float(top.x)), sd = scale_to<10>(__uint_as_float(top.y));
+        // (their products are with U, dv and dO, which have kLift of their own)
+        const Scale sh = scale_to<kLift, kLift>(__uint_as_float(top.x)),
+                    sd = scale_to<kLift, kLift>(__uint_as_float(top.y));
         hs = sh.down;
         ds = sd.down;
 #pragma unroll
@@ -375,11 +381,11 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
     copy_commit();
     {
       auto q_done = [&](int r, float s, float m) {
-        qdown[r] = inverse_pow2(s);
+        qdown[r] = inverse_pow2(s) * pow2(-kLift);
         qmost[r] = m;
       };
       auto k_done = [&](int r, float s, float m) {
-        kdown[r] = inverse_pow2(s);
+        kdown[r] = inverse_pow2(s) * pow2(-kLift);
         kmost[r] = m;
       };
       if constexpr (NI == 2) {
@@ -463,11 +469,11 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
     }
     // MP or ML as their tiles hold them (times 2^kMask), and the products with the scores
     constexpr int kMask = 5;
-    constexpr float kMaskUp = 1 << kMask, kMaskDown = 1.f / kMaskUp;
+    constexpr float kMaskDown = pow2(-kMask);
     {
       const uint32_t A = is_l ? sK : sQ;
       uint8_t* tile = Mt + (is_l ? G::HT : 0);
-      const float held = is_l ? -kMaskUp : kMaskUp * s1;
+      const float held = (is_l ? -1.f : s1) * pow2(kMask - 2 * kLift);  // (the operands' factors off)
       float row[2] = {0.f, 0.f}, f[2], hi[2], lo[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -611,24 +617,23 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         if (k <= strip) {  // columns 16 k ... of MP, ML
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4(a[q], lm.left(sP, 16 * strip, 16 * k) + q * C * PB);
-          const __half2 w0 = share_of(0, 16 * k), w1 = share_of(0, 16 * k + 8);
-          times_terms(a, w0, w1);
-          mma_parts<kParts, NI, 2>(d[0], a, rk);
+          uint32_t rw[NI][2][2];
+          times_terms<NI>(rw, rk, share_of(0, 16 * k), share_of(0, 16 * k + 8));
+          mma_parts<kParts, NI, 2>(d[0], a, rw);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4(a[q], lm.left(sL, 16 * strip, 16 * k) + q * C * PB);
-          times_terms(a, w0, w1);
-          mma_parts<kParts, NI, 2>(d[1], a, rk);
+          mma_parts<kParts, NI, 2>(d[1], a, rw);
         }
         if (k >= strip) {  // rows 16 k ...
           uint32_t rq[NI][2][2];
           load_right_t<NI, 2>(rq, sQ, C * RB, lk, c, 16 * k);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4t(a[q], lm.left_t(sP, 16 * strip, 16 * k) + q * C * PB);
-          times_terms(a, share_of(1, 16 * k), share_of(1, 16 * k + 8));
+          times_terms<NI>(rq, rq, share_of(1, 16 * k), share_of(1, 16 * k + 8));
           mma_parts<kParts, NI, 2>(d[2], a, rq);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) ldm4t(a[q], lm.left_t(sL, 16 * strip, 16 * k) + q * C * PB);
-          times_terms(a, share_of(2, 16 * k), share_of(2, 16 * k + 8));
+          times_terms<NI>(rk, rk, share_of(2, 16 * k), share_of(2, 16 * k + 8));
           mma_parts<kParts, NI, 2>(d[2], a, rk);
         }
       }

@@ -179,3 +179,53 @@ def test_gradients_of_short_keys():
 def spread(n, least):
     """1 ... 2^-least over n elements, in an order that is not theirs."""
     return np.exp2(-(np.arange(n) * 7 % (least + 1.0)))
+
+
+@pytest.mark.parametrize("H", [2, 80])
+def test_elements_of_different_size(H):
+    """fp32 rows of k and q whose elements are 1 ... 2^-14 of the largest: each column
+    of the state, of dk and of dq keeps its bits."""
+    import state_space_model_analytic_gb300 as ssd
+    K = 64
+    inp = synth.delta_inputs(1, 130, H, H, K, 64, "f32", 90)
+    c = spread(K, 14)
+    for n in "qk":
+        x = inp[n] * c
+        inp[n] = synth.round_to(x / np.sqrt((x * x).sum(-1, keepdims=True)), "f32")
+    x = operands(inp, "f32")
+    o, S = ssd.delta_rule_forward(*x)
+    ro, rS = recurrence(inp)
+    close(host(o), ro, (1, 3))
+    close(host(S), rS, (1, 2))
+    if H > 2:
+        return
+    g = ssd.delta_rule_backward(*x, None, dev(inp["do"]))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), None, inp["do"])
+    for n in ("dq", "dk"):
+        close(host(g[n]), ref[n], (0, 1, 2))
+
+
+def test_columns_against_one_another():
+    """Columns of v of 1 ... 2^-12 and of dout of 1 ... 2^12: every column has the same
+    share in dq, dk and the gates' gradients."""
+    import state_space_model_analytic_gb300 as ssd
+    V = 128
+    inp = synth.delta_inputs(1, 130, 2, 2, 64, V, "f32", 91)
+    c = spread(V, 12)
+    plain = {n: np.array(inp[n]) for n in inp}
+    inp["v"], inp["do"] = inp["v"] * c, inp["do"] / c
+    g = ssd.delta_rule_backward(*operands(inp, "f32"), None, dev(inp["do"]))
+    ref, _ = delta.backward(*(plain[n] for n in NAMES), None, plain["do"])
+    for n in ("dq", "dk", "dbeta"):
+        close(host(g[n]), ref[n])
+
+
+def test_steps_of_different_size():
+    """fp32 douts of 1 ... 2^-14 by step (weighted losses): dv of every step keeps its
+    bits."""
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(1, 130, 2, 2, 64, 64, "f32", 92, (-0.5, -0.1))
+    inp["do"] = inp["do"] * np.exp2(-np.arange(130) * 14.0 / 130)[:, None, None]
+    g = ssd.delta_rule_backward(*operands(inp, "f32"), None, dev(inp["do"]))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), None, inp["do"])
+    close(host(g["dv"]), ref["dv"], (2, 3), 2.0 ** -17)  # (of 128 elements each)

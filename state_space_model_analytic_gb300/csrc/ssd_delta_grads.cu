@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         fe.read(sm + G::kU, tid);
         fy.read(sm + G::kV, tid);
         fo.read(sm + G::kO, tid);
-        // (later pieces are not scaled up by more than the earlier ones, so that sums of
-        // these may be scaled to them)
+        // (later pieces are not scaled up by more than the earlier ones, rows of zeros by the
+        // most there is, so that sums of these may be scaled to them by factors of at most 1)
 #pragma unroll
         for (int k = 0; k < fh.N; ++k) {
           const float4 s = fh.f[k], d = fd.f[k];
@@ -310,9 +310,9 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
             down[now][which][r] = inverse_pow2(s);
           };
         };
-        fe.template write<100>(sm + G::kU, tid, least(0), done(0));
-        fy.template write<100>(sm + G::kV, tid, least(1), done(1));
-        fo.template write<100>(sm + G::kO, tid, least(2), done(2));
+        fe.template write<kFarStep>(sm + G::kU, tid, least(0), done(0));
+        fy.template write<kFarStep>(sm + G::kV, tid, least(1), done(1));
+        fo.template write<kFarStep>(sm + G::kO, tid, least(2), done(2));
       }
       __syncthreads();
       if (tid < 2) top_state[buf][tid] = 0;  // (all have read it)

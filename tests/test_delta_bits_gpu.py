@@ -229,3 +229,30 @@ def test_steps_of_different_size():
     g = ssd.delta_rule_backward(*operands(inp, "f32"), None, dev(inp["do"]))
     ref, _ = delta.backward(*(inp[n] for n in NAMES), None, inp["do"])
     close(host(g["dv"]), ref["dv"], (2, 3), 2.0 ** -17)  # (of 128 elements each)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_columns_of_zeros_before_small_ones(dtype):
+    """v, the state and dout zero in the first 64 columns, 2^-70 in the others."""
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(1, 100, 2, 2, 64, 128, dtype, 93)
+    for n in ("v", "do", "state0", "dstate"):
+        x = np.array(inp[n])
+        if n in ("v", "do"):
+            x[..., :64] = 0
+        else:
+            x[..., :64, :] = 0
+        inp[n] = x
+    f = 2.0 ** -70
+    x = operands(inp, dtype)
+    a = ssd.delta_rule_backward(*x, dev(inp["state0"]), dev(inp["do"], dtype), dev(inp["dstate"]))
+    x[2] = x[2] * f
+    b = ssd.delta_rule_backward(*x, dev(inp["state0"] * f), dev(inp["do"] * f, dtype),
+                                dev(inp["dstate"] * f))
+    # dq, dk and the gates' are products of two such factors, 2^-140: zero, or of a few bits
+    tiny = 2.0 ** -139
+    for n in ("dq", "dk", "dlog_decay", "dbeta"):
+        got, most = host(b[n]), np.abs(host(a[n])).max() * tiny
+        assert np.isfinite(got).all() and np.abs(got).max() <= most, n
+    for n in ("dv", "dstate0"):
+        assert np.array_equal(host(a[n]) * f, host(b[n])), n

@@ -3,9 +3,11 @@
 //   mu = mean x,  i = 1/sqrt(mean (x - mu)^2 + eps),  n = (x - mu) i,  y = n w + b
 // backward, t = dy w:
 //   dx = i (t - mean t - n mean(t n)),  dw = sum over the rows of dy n,  db = of dy
-// A warp takes its own columns' mean off before it sums their squares (they are in
-// registers), and the warps' means and sums are joined, so that a large mean costs no
-// digits and a row takes one exchange between its warps.
+// A warp takes its own columns' mean off (they are in registers) and sums what is left
+// and its squares; the mean of what is left is what the first one was off by, and the
+// warps' means are joined as differences to one of them.  So a large mean costs n no
+// digits, and a row takes one exchange between its warps.  (From statistics, the
+// gradients' n is off by the rounding of the stored mean.)
 //
 // Bound by memory: x and y, or x, dy and dx, each once.  W warps hold a row; a CTA
 // walks groups of rows, the next three rows' 16-byte pieces on their way while it works
@@ -67,50 +69,60 @@ __device__ __forceinline__ float warp_columns(int warp, int width) {
   return (float)n;
 }
 
-// Mean and 1 / sqrt(variance + eps) of a row; x: zeros past the width, on return what
-// is left of it without the warp's own mean, `off` (zeros past the width).  red:
-// [2][R][W] float2, alternated by the caller (buf).
+__device__ __forceinline__ float sum_warp(float sum) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Of a row: mean, 1 / sqrt(variance + eps), and what is to be added to x as it is left.
+struct RowStats {
+  float mean, inv, rest;
+};
+// x: zeros past the width, on return less the mean of the warp's own columns (zeros past
+// the width).  red: [2][R][W] float4, alternated by the caller (buf).
 template <typename T, bool VEC, int W, int L>
-__device__ __forceinline__ float2 row_stats(float (&x)[L], float& off, int lane, int width, float eps,
-                                            float2* red, int buf, int group) {
+__device__ __forceinline__ RowStats row_stats(float (&x)[L], int lane, int width, float eps, float4* red,
+                                              int buf, int group) {
   const int warp = lane >> 5;
   float2 sums = both(0.f);
 #pragma unroll
   for (int e = 0; e < L; e += 2) sums = add2(sums, pair(x, e));
-  float sum = sums.x + sums.y;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float n = warp_columns<T, VEC, W, L>(warp, width);
-  float mean = n > 0.f ? sum / n : 0.f;
-  off = mean;
-  sums = both(0.f);
+  const float n = warp_columns<T, VEC, W, L>(warp, width), inv_n = n > 0.f ? 1.f / n : 0.f;
+  // The sum's rounding goes by the mean, what is left goes by the spread: its own mean is
+  // what the first one was off by.
+  const float off = sum_warp(sums.x + sums.y) * inv_n;
+  float2 squares = sums = both(0.f);
 #pragma unroll
   for (int e = 0; e < L; e += 2) {
-    const float2 d = add2(pair(x, e), inside<T, VEC, W>(-mean, lane, e, width));
+    const float2 d = add2(pair(x, e), inside<T, VEC, W>(-off, lane, e, width));
     set_pair(x, e, d);
-    sums = fma2(d, d, sums);
+    sums = add2(sums, d);
+    squares = fma2(d, d, squares);
   }
-  float m2 = sums.x + sums.y;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+  const float more = sum_warp(sums.x + sums.y) * inv_n;
+  float m2 = sum_warp(squares.x + squares.y), mean = off + more, rest = -more;
+  if (m2 < INFINITY) m2 = fmaxf(fmaf(-n * more, more, m2), 0.f);
   if constexpr (W > 1) {
-    // lane j: warp j's
-    float2* r = red + (buf * Shape<W>::kRows + group) * W;
-    if ((lane & 31) == 0) r[warp] = make_float2(mean, m2);
+    // lane j: warp j's, as differences to the first warp's mean
+    float4* r = red + (buf * Shape<W>::kRows + group) * W;
+    if ((lane & 31) == 0) r[warp] = make_float4(off, more, m2, 0.f);
     __syncthreads();
     const int j = lane & (W - 1);
-    const float2 theirs = r[j];
-    const float m = warp_columns<T, VEC, W, L>(j, width);
-    mean = m * theirs.x;
+    const float4 theirs = r[j];
+    const float first = r[0].x, m = warp_columns<T, VEC, W, L>(j, width);
+    const float diff = (theirs.x - first) + theirs.y;
+    float to = m * diff;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
-    mean /= (float)width;
-    const float d = theirs.x - mean;
-    m2 = fmaf(m * d, d, theirs.y);
+    for (int o = W / 2; o > 0; o >>= 1) to += __shfl_xor_sync(0xffffffffu, to, o);
+    to /= (float)width;
+    mean = first + to;
+    rest = (off - first) - to;
+    m2 = fmaf(m * (diff - to), diff - to, theirs.z);
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
   }
-  return make_float2(mean, 1.f / sqrtf(m2 / (float)width + eps));
+  return {mean, 1.f / sqrtf(m2 / (float)width + eps), rest};
 }
 
 template <typename T, bool VEC, int W, int L>
@@ -118,7 +130,7 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, W <= 8 ? 2 : 1) k_layer_no
   constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads, nT = Pieces<T, VEC, L>::n;
   constexpr bool S = VEC;
   constexpr int kStages = kStagesOf<T>;
-  __shared__ float2 red[2 * R * W];
+  __shared__ float4 red[2 * R * W];
   extern __shared__ uint4 stage[];  // [kStages][piece][thread]
   const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
   const long long steps = (p.rows + R - 1) / R;
@@ -152,14 +164,13 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, W <= 8 ? 2 : 1) k_layer_no
     } else {
       load_row<T, VEC, W>((const T*)p.x + row * p.x_stride, lane, width, x);
     }
-    float off;
-    const float2 m = row_stats<T, VEC, W, L>(x, off, lane, p.width, p.eps, red, buf, group);
-    const float2 rest = both((off - m.x) * m.y), inv = both(m.y);
+    const RowStats m = row_stats<T, VEC, W, L>(x, lane, p.width, p.eps, red, buf, group);
+    const float2 rest = both(m.rest * m.inv), inv = both(m.inv);
 #pragma unroll
     for (int e = 0; e < L; e += 2)
       set_pair(x, e, fma2(fma2(pair(x, e), inv, rest), pair(w, e), pair(b, e)));
     store_row<T, VEC, W>((T*)p.y + row * p.width, lane, width, x);
-    if (p.stats && in && lane == 0) ((float2*)p.stats)[row] = m;
+    if (p.stats && in && lane == 0) ((float2*)p.stats)[row] = make_float2(m.mean, m.inv);
   }
   if constexpr (S) cp_wait0();
 }
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, W <= 8 ? 2 : 1) k_layer_no
   constexpr int R = Shape<W>::kRows, NT = Shape<W>::kThreads, nT = Pieces<T, VEC, L>::n;
   constexpr bool S = VEC;
   constexpr int kStages = kStagesOf<T>;
-  __shared__ float2 red2[2 * R * W];
+  __shared__ float4 red2[2 * R * W];
   __shared__ __align__(16) float red[2 * 2 * R * W];
   extern __shared__ uint4 stage[];  // [kStages][x, dy][piece][thread]; after the rows [R][2][width]
   const int group = threadIdx.x / (W * 32), lane = threadIdx.x % (W * 32);
@@ -217,10 +228,9 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, W <= 8 ? 2 : 1) k_layer_no
     }
     float rest = 0.f;  // without statistics n = x inv + rest, x less the warp's own mean
     if (!p.stats) {
-      float off;
-      const float2 m = row_stats<T, VEC, W, L>(x, off, lane, p.width, p.eps, red2, buf, group);
-      inv = in ? m.y : 0.f;
-      rest = (off - m.x) * inv;
+      const RowStats m = row_stats<T, VEC, W, L>(x, lane, p.width, p.eps, red2, buf, group);
+      inv = in ? m.inv : 0.f;
+      rest = m.rest * inv;
     }
     const float2 inv2 = both(inv), rest2 = both(rest);
     float2 s0 = both(0.f), s1 = both(0.f);

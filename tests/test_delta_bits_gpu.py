@@ -256,3 +256,45 @@ def test_columns_of_zeros_before_small_ones(dtype):
         assert np.isfinite(got).all() and np.abs(got).max() <= most, n
     for n in ("dv", "dstate0"):
         assert np.array_equal(host(a[n]) * f, host(b[n])), n
+
+
+# as SHAPES, and groups and two pieces of v for the gradients
+PATHS = [(3, 3, 64, 64), (50, 25, 128, 64), (80, 80, 128, 64), (80, 40, 64, 64), (4, 2, 128, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", PATHS, ids=str)
+def test_sums_keep_their_bits_on_every_path(shape, dtype):
+    """Outputs and gradients by their root mean squares, head by head.  (The terms of
+    dlog_decay cancel to a thirtieth and less of their size: 2^-17.  A bf16 result
+    between 1 and 2 is rounded by up to 2^-8, 2^-8 / sqrt(3) in the root mean square, and
+    is 1.5 itself: below 2^-9.)"""
+    import state_space_model_analytic_gb300 as ssd
+    H, G, K, V = shape
+    inp = synth.delta_inputs(1, 130, H, G, K, V, dtype, 94)
+    x, s0 = operands(inp, dtype), dev(inp["state0"])
+    o, S = ssd.delta_rule_forward(*x, s0)
+    g = ssd.delta_rule_backward(*x, s0, dev(inp["do"], dtype), dev(inp["dstate"]))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), inp["state0"], inp["do"], inp["dstate"])
+    ro, rS = recurrence(inp, inp["state0"])
+    over = {"state": (2, 3), "dstate0": (2, 3), "dlog_decay": 1, "dbeta": 1}
+    for n, got, want in (("o", o, ro), ("state", S, rS), *((n, g[n], ref[n]) for n in GRADS)):
+        most = 2.0 ** -9 if dtype == "bf16" and n in ("o", "dq", "dk", "dv") else RMS
+        close(host(got), want, over.get(n, (1, 3)), 2.0 ** -17 if n == "dlog_decay" else most)
+
+
+@pytest.mark.parametrize("scale", [-3.7, 0.0, 2.0 ** -40, 1e9])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales(dtype, scale):
+    """Any scale of o: gradients against the reference; with 0 those of the state alone."""
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(1, 100, 4, 2, 64, 128, dtype, 95)
+    g = ssd.delta_rule_backward(*operands(inp, dtype), dev(inp["state0"]), dev(inp["do"], dtype),
+                                dev(inp["dstate"]), scale=scale)
+    scale = float(np.float32(scale))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), inp["state0"], inp["do"], inp["dstate"], scale)
+    if scale == 0:
+        assert not host(g["dq"]).any()
+    for n in GRADS[scale == 0:]:
+        most = 2.0 ** -9 if dtype == "bf16" and n in ("dq", "dk", "dv") else RMS
+        close(host(g[n]), ref[n], None, 2.0 ** -17 if n == "dlog_decay" else most)

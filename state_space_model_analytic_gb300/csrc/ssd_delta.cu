@@ -20,11 +20,14 @@
 // the products with the state are split, F's parts added up through shared memory, and
 // the solution of the triangular system, which all of them need, is found by each.
 //
-// Bound by that chain: at 4 x 2048 steps of 32 heads 128/64 (bf16, 153 us; memory alone
-// would take 31) a chunk of 64 steps takes 8.8 thousand cycles, 2.2 of them the products
-// with the state, 3.4 the system, 1.7 the new state, with the tensor pipe 42 % and the
-// issue slots 45 % busy.  The walk that keeps the states takes 140 us, the walk back 226.
-// fp32 (8 x 1024 steps of 24 heads 64/64): 155 us.
+// Bound by that chain and, where o is formed, by the warps that form it: at 4 x 2048 steps
+// of 32 heads 128/64 (bf16, 175 us; memory alone would take 31) a chunk of 64 steps takes
+// 10 thousand cycles.  The chain has 2.2 of them for the products with the state, 3.4 for
+// the system and 1.7 for the new state; o takes 188 matrix instructions a warp, 84 when
+// one part of the state, P and U was taken (153 us, but o off by 2^-12 of
+// |q| |S|).  Tensor pipe 45 % and issue slots 42 % busy.  The walk that keeps the states takes
+// 144 us, the walk back 232.  fp32 (8 x 1024 steps of 24 heads 64/64): 154 us.  (These and
+// the times below: events around the kernel, caches flushed.)
 #include <cuda_bf16.h>
 
 #include "ssd_delta.cuh"
@@ -298,7 +301,7 @@ __device__ __forceinline__ void add_warps(float (&t)[NC][4], const float4* ex, i
 
 // The row of a CTA.  Of rows with lengths, where the CTAs outnumber the SMs, the longest go
 // first, so that none of them begins when the others are done (16 rows of up to 1003
-// steps, 24 heads 64/64: 118 us against 135).
+// steps, 24 heads 64/64: 130 us against 151).
 constexpr int kOrdered = 256;  // rows that are put in order
 // len: kOrdered + 1 words of shared memory that are free again afterwards.
 __device__ __forceinline__ int row_of(const int* lens, int B, int T, int tid, int* len) {
@@ -318,12 +321,13 @@ __device__ __forceinline__ int row_of(const int* lens, int B, int T, int tid, in
 }
 
 // Whether o is formed by four warps of their own: the walking ones hand them the state and
-// U as they have them for their own products.  4 x 2048 steps of 32 heads 128/64: 153 us
-// against 173; at 64/64 there is less to take over and the four need their issue slots (16
-// rows of 1003, 24 heads: 140 against 135), in fp32 what is handed over is twice as long (188
-// against 155), and with WK > 1 the preparation is what takes longest.  Where they are, the
-// preparing warps have time to multiply the rows of later blocks by the inverse of the
-// earlier ones as well, and the chain has one product a block less (160 without).
+// U as they have them for their own products.  4 x 2048 steps of 32 heads 128/64: 175 us
+// against 190; at 64/64 there is less to take over and the four need their issue slots (16
+// rows of up to 1003, 24 heads: 131 against 130), in fp32, whose chunks are half as long, the
+// state is handed over twice as often (187 against 154), and with WK > 1 the preparation is
+// what takes longest.  Where they are, the preparing warps have time to multiply the rows of
+// later blocks by the inverse of the earlier ones as well, and the chain has one product a
+// block less.
 template <int NI, int DK, int WK, bool kStates>
 constexpr bool helped() {
   return !kStates && WK == 1 && NI == 1 && DK == 128;
@@ -686,7 +690,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
 #pragma unroll
           for (int q = 0; q < kParts; ++q) given.put(given.u(k, q, lane), ao[q]);
           if ((lane & 3) == 0) *given.down(1 + k, lane) = make_float2(su.down0, su.down1);
-          // (in halves: all at once left what U adds to o to the end of the chunk)
+          // (in halves: all at once left what U adds to o to the end of the chunk, 179 us
+          // against 175)
           if (k == NB / 2 - 1) bar_arrive(3 + kWalkers + vg, 64);
           if (k == NB - 1) bar_arrive(3 + 2 * kWalkers + vg, 64);
         }
@@ -1194,9 +1199,9 @@ cudaError_t back_t(const DeltaBack& p, cudaStream_t s) {
 // Warps that share 16 columns of v: as many as leave every CTA an SM of its own.  Below
 // that the shared rows' shorter chain gains, above it the second wave costs more (us of the
 // walk that keeps the states, one, two, four warps; CTAs with one):
-//   1 x 4096, 32 heads 128/64 (32): 322 260 235    2 x 2048, 32 heads 128/64 (64): 166 137 244
-//   1 x 4096, 16 heads 64/64 (16): 209 194 186     2 x 2048, 24 heads 64/64 (48): 109 101 189
-//   3 x 2048, 32 heads 128/64 (96): 169 266 365    8 x 1024, 24 heads 64/64 (192): 116 158 291
+//   1 x 4096, 32 heads 128/64 (32): 267 226 211    2 x 2048, 32 heads 128/64 (64): 142 123 222
+//   1 x 4096, 16 heads 64/64 (16): 185 178 169     2 x 2048, 24 heads 64/64 (48): 97 95 175
+//   3 x 2048, 32 heads 128/64 (96): 143 232 327    8 x 1024, 24 heads 64/64 (192): 103 144 261
 int warps_per_rows(int B, int H, int dv) {
   for (int wk = 4; wk > 1; wk /= 2) {
     const dim3 g = walk_grid(H, B, dv, wk);

@@ -30,12 +30,15 @@
 // into the right operand's rows, relative to the chunk's largest share.  So a step's dq
 // does not depend on the size of its q, nor dk on that of k.
 //
-// 4 x 2048 steps of 32 heads 128/64 (bf16): 388 us for 4096 items of 27 thousand cycles,
-// where the 709 MB it reads and writes take 106.  Of an item the splitting takes 6 thousand
+// 4 x 2048 steps of 32 heads 128/64 (bf16): 432 us for 4096 items of 30 thousand cycles,
+// where the 709 MB it reads and writes take 106 (events around the kernel, caches flushed;
+// tensor pipe 26 % and issue slots 43 % busy).  Of an item the splitting takes 6 thousand
 // cycles, the products with H and D 6 (tensor pipe and shared memory), the scores and masks
-// 4, the products with MP and ML 4.5, loads and barriers the rest.  Two CTAs an SM with
-// half the columns each: 510 us against 423, since both take E, y and dO apart; one
-// CTA an item instead of persistent ones: 543.
+// 4, the products with MP and ML 7, loads and barriers the rest.  MP and ML as one part
+// each: 24 us less, and dq and dk off by 2^-11 of their size; held in q's and k's scales: 20
+// less, and steps of short q and k without their bits.  When it took 423 us, two CTAs an SM
+// with half the columns each took 510, since both take E, y and dO apart, and one CTA an
+// item instead of persistent ones 543.
 #include <cuda_bf16.h>
 
 #include "persistent_grid.h"

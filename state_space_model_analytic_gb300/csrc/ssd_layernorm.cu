@@ -13,8 +13,9 @@
 // walks groups of rows, the next three rows' 16-byte pieces on their way while it works
 // on the current one (rows.cuh).  The backward's column sums are kept by the
 // threads over all rows of a CTA and added up, CTA by CTA in order, by a second
-// kernel.  8192 x 2048 in bf16: 16.4 us forward and 30.9 with the gradients' second kernel
-// (6), where the bytes at the copy rate take 10 and 15.
+// kernel.  8192 x 2048 in bf16: 16.6 us forward and 31.0 with the gradients' second kernel
+// (6), where the bytes at the copy rate take 10 and 15; in fp32 24.5 and 41.6 (20 and 30).
+// Figures are of calls back to back on tensors larger than the caches.
 #include <cuda_bf16.h>
 
 #include "f32x2.cuh"
@@ -29,9 +30,10 @@ namespace {
 
 using namespace rows;
 
-// Rows on their way and worked on.  With one on its way the loads in flight did not
-// cover the memory's latency (8192 x 2048 bf16: 18.7 us forward, 34 backward).
-// (Three in fp32, whose pieces are twice as long, for two CTAs an SM.)
+// Rows on their way and worked on.  From flushed caches the gradients of 8192 x 2048 in
+// bf16 take 32.4 us with four and 34.5 with two (the row kernel), the forward 18.8 with
+// either; back to back 31.0 and 31.0, 16.6 and 16.0.  (Three in fp32, whose pieces are
+// twice as long, for two CTAs an SM.)
 template <typename T>
 constexpr int kStagesOf = sizeof(T) == 2 ? 4 : 3;
 template <int N>
@@ -340,11 +342,11 @@ cudaError_t backward(const LayerNorm& p, int* grid, cudaStream_t s) {
 }
 
 // Elements of a lane and warps of a row by its width: at eight elements what a warp does
-// once a row (the sums over its lanes, the row's statistics) was more than their work
-// (8192 x 2048 bf16: 18.7 us forward, 16.4 with 32 on two warps).  The backward has five
+// once a row (the sums over its lanes, the row's statistics) is more than their work
+// (8192 x 2048 bf16: 21.2 us forward, 16.6 with 32 on two warps).  The backward has five
 // values an element in registers, the forward three.  A forward of few rows has no such
 // choice: rows on few warps leave SMs idle, and a row's own time counts (250 x 1537 in
-// fp32: 6.7 us with eight elements, 8.2 with 32).
+// fp32: 4.3 us with eight elements, 6.3 with 32).
 template <typename T, bool VEC>
 cudaError_t launch(const LayerNorm& p, bool back, int* grid, cudaStream_t s) {
   const int w = p.width;
@@ -373,7 +375,8 @@ cudaError_t launch(const LayerNorm& p, bool back, int* grid, cudaStream_t s) {
 
 cudaError_t dispatch(const LayerNorm& p, bool bf16, bool back, int* grid, cudaStream_t s) {
   // 16-byte vectors need every row of every tensor to start on such a boundary
-  // and the width to be whole vectors
+  // and the width to be whole vectors; other rows go element by element, with nothing on
+  // its way ahead (8192 x 2049: 55 us forward and 58 backward in bf16, 35 and 51 in fp32)
   const int unit = bf16 ? 8 : 4;
   bool vec = p.width % unit == 0 && p.x_stride % unit == 0;
   const void* ptrs[] = {p.x, p.weight, p.bias, p.y, p.dy, p.dx};

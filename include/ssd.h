@@ -334,12 +334,12 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
  * them together where dq, dk and dlog_decay are formed; a column of v over a chunk (64
  * steps, 32 in fp32) of what is written (beta e) and of dout times the largest element
  * of the step's q.  What one step of a chunk reads of another's write counts down to
- * 2^-30 of the product of q's or k's largest elements, and steps add to each other's
+ * 2^-29 of the product of q's or k's largest elements, and steps add to each other's
  * gradients by their shares dout q^T and beta e k^T, relative to the chunk's largest.
  * Results do not depend on powers of two in a step's q (and dout for its inverse), or
  * in k and v with beta for the inverse of their square, as long as the largest element
- * of a key is between 2^-63 and 2^63, beta times its square a normal number and v
- * divided by it finite.  States are not scaled up further below 2^-87.
+ * of a key is between 2^-63 and 2^63, of a query above 2^-110, beta times the key's
+ * square a normal number and v divided by the key's finite.  States are not scaled up further below 2^-87.
  * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.  bf16
  * results (o, dq, dk, dv) are off by their own rounding, 0.0017 of their root mean
  * square.

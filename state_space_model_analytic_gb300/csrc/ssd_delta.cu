@@ -483,15 +483,15 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
         HalfRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
         if (!kStates) q.read(st, tid);
-        k.write(st + G::KT, tid, no_least, k_done);
-        if (!kStates) q.write(st, tid, no_least, q_done);
+        k.template write<kFarKey>(st + G::KT, tid, no_least, k_done);
+        if (!kStates) q.template write<kFarStep>(st, tid, no_least, q_done);
       } else {
         FloatRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
         if (!kStates) q.read(st, tid);
         bar(1, kPrep);
-        k.write(st + G::KT, tid, no_least, k_done);
-        if (!kStates) q.write(st, tid, no_least, q_done);
+        k.template write<kFarKey>(st + G::KT, tid, no_least, k_done);
+        if (!kStates) q.template write<kFarStep>(st, tid, no_least, q_done);
       }
       bar(1, kPrep);
       prepare<NI, DK, !kStates, kHelped>(st, st + G::KT, sm + G::kM + (c & 1) * G::MT,
@@ -873,8 +873,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
         HalfRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
         q.read(st, tid);
-        k.write(st + G::KT, tid, no_least, k_done);
-        q.write(st, tid, no_least, q_done);
+        k.template write<kFarKey>(st + G::KT, tid, no_least, k_done);
+        q.template write<kFarStep>(st, tid, no_least, q_done);
       } else {
         FloatRows<C, DK, kPrep> k, q;
         k.read(st + G::KT, tid);
@@ -885,8 +885,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
           d[i][0] = f.x; d[i][1] = f.y; d[i][2] = f.z; d[i][3] = f.w;
         }
         bar(1, kPrep);
-        k.write(st + G::KT, tid, no_least, k_done);
-        q.write(st, tid, no_least, q_done);
+        k.template write<kFarKey>(st + G::KT, tid, no_least, k_done);
+        q.template write<kFarStep>(st, tid, no_least, q_done);
       }
       bar(1, kPrep);
       float m[E];

@@ -117,10 +117,10 @@ __device__ __forceinline__ Scale scale_to(float m) {
   e = e < 40 ? 40 : e > 254 ? 254 : e;
   return {__uint_as_float((uint32_t)(254 + T - e) << 23), __uint_as_float((uint32_t)(e - T - kLess) << 23)};
 }
-// The same for a row of steps: into [1, 2), by 2^kFar at most.  For k and q kFar is kFarKey
-// (beta is divided by the square) and rows of zeros stay as they are (v is multiplied by
-// k's factor).
-constexpr int kFarKey = 63, kFarStep = 100;
+// The same for a row of steps: into [1, 2), by 2^kFar at most.  For k kFar is kFarKey (beta
+// is divided by the square) and rows of zeros stay as they are (v is multiplied by k's
+// factor).
+constexpr int kFarKey = 63, kFarStep = 110;
 template <int kFar>
 __device__ __forceinline__ float row_exponent(float m) {
   static_assert(kFar + kLift <= 127, "");
@@ -381,7 +381,7 @@ struct HalfRows {
       q[i] = *(const uint4*)(tile + at16<DK * 2>(at / LPR, at % LPR));
     }
   }
-  template <int kFar = kFarKey, typename F, typename L>
+  template <int kFar, typename F, typename L>
   __device__ __forceinline__ void write(uint8_t* tile, int tid, L least, F done) const {
     __nv_bfloat162 m[N];
 #pragma unroll
@@ -442,7 +442,7 @@ struct FloatRows {
   }
   // each row scaled into [1, 2) (and by 2^kLift), or by no more than `least(row)` would
   // be; done(row, scale, largest) by one lane a row
-  template <int kFar = kFarKey, typename F, typename L>
+  template <int kFar, typename F, typename L>
   __device__ __forceinline__ void write(uint8_t* tile, int tid, L least, F done) const {
     float m[N];
 #pragma unroll

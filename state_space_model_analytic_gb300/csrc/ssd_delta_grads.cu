@@ -396,14 +396,14 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
         q.read(sm, tid);
         k.read(sm + G::kK, tid);
         __syncthreads();
-        q.write(sm, tid, no_least, q_done);
-        k.write(sm + G::kK, tid, no_least, k_done);
+        q.template write<kFarStep>(sm, tid, no_least, q_done);
+        k.template write<kFarKey>(sm + G::kK, tid, no_least, k_done);
       } else {
         HalfRows<C, DK, NT> q, k;
         q.read(sm, tid);
         k.read(sm + G::kK, tid);
-        q.write(sm, tid, no_least, q_done);
-        k.write(sm + G::kK, tid, no_least, k_done);
+        q.template write<kFarStep>(sm, tid, no_least, q_done);
+        k.template write<kFarKey>(sm + G::kK, tid, no_least, k_done);
       }
     }
     __syncthreads();
@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = i0 + 8 * u;
-      const float fq = p.scale * g.lead[r] * odown[r] * hs, fr = -g.lead[r] * vdown[r] * hs,
-                  fw = g.tail[r] * udown[r] * ds;
+      const float fq = p.scale * g.lead[r] * odown[r], fr = -g.lead[r] * vdown[r],
+                  fw = g.tail[r] * udown[r];
       float2 read_q = both(0.f), read_k = both(0.f), write2 = both(0.f);
       // (a row's pieces: their index exchanged by r's last bits)
       const uint8_t* row = sm + r * RB + c2 * 2;
@@ -421,8 +421,10 @@ __global__ void __launch_bounds__(Geom<NI, DK>::NT, 1) k_delta_grads(const Delta
       for (int e = 0; e < NK; ++e) {
         const uint8_t* at = row + (((group * NK + e) ^ (r & 7)) << 4);
         const float2 q = pair_at<NI, RB, C>(at), k = pair_at<NI, RB, C>(at + G::kK);
-        const float2 a = mul2(pair(dq[e], u), both(fq)), b = mul2(pair(rd[e], u), both(fr)),
-                     w = mul2(pair(wr[e], u), both(fw));
+        // (the state's factor first: the product of both may be below what fp32 holds)
+        const float2 a = mul2(mul2(pair(dq[e], u), both(hs)), both(fq)),
+                     b = mul2(mul2(pair(rd[e], u), both(hs)), both(fr)),
+                     w = mul2(mul2(pair(wr[e], u), both(ds)), both(fw));
         set_pair(dq[e], u, a);
         set_pair(rd[e], u, b);
         set_pair(wr[e], u, w);

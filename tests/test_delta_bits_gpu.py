@@ -298,3 +298,46 @@ def test_scales(dtype, scale):
     for n in GRADS[scale == 0:]:
         most = 2.0 ** -9 if dtype == "bf16" and n in ("dq", "dk", "dv") else RMS
         close(host(g[n]), ref[n], None, 2.0 ** -17 if n == "dlog_decay" else most)
+
+
+@pytest.mark.parametrize("f", [2.0 ** 100, 2.0 ** -100])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_and_small_queries(dtype, f):
+    """q times f and dout divided by it: o and dq change by that factor, nothing else
+    does, bit for bit."""
+    import torch
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(2, 150, 4, 2, 64, 128, dtype, 96)
+    q, k, v, la, be = operands(inp, dtype)
+    s0, do, ds = dev(inp["state0"]), dev(inp["do"], dtype), dev(inp["dstate"])
+    # (a dout that is all bits at 2^-100 too: elements below 2^-20 are left out)
+    do = torch.where(do.abs() < 2.0 ** -20, torch.zeros_like(do), do)
+    o, S = ssd.delta_rule_forward(q, k, v, la, be, s0)
+    o2, S2 = ssd.delta_rule_forward(q * f, k, v, la, be, s0)
+    assert torch.equal(o * f, o2) and torch.equal(S, S2)
+    g = ssd.delta_rule_backward(q, k, v, la, be, s0, do, ds)
+    h = ssd.delta_rule_backward(q * f, k, v, la, be, s0, do * (1 / f), ds)
+    assert torch.equal(g["dq"] * (1 / f), h["dq"])
+    for n in GRADS[1:]:
+        assert torch.equal(g[n], h[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["beta", "v", "do", "q", "k", "all"])
+def test_zeros(dtype, what):
+    """Write strengths, values, gradients, queries, keys or all of them zero."""
+    import state_space_model_analytic_gb300 as ssd
+    inp = synth.delta_inputs(2, 100, 4, 2, 64, 128, dtype, 97)
+    for n in ("beta", "v", "do", "q", "k", "state0", "dstate") if what == "all" else (what,):
+        inp[n] = np.zeros_like(inp[n])
+    x, s0 = operands(inp, dtype), dev(inp["state0"])
+    o, S = ssd.delta_rule_forward(*x, s0)
+    g = ssd.delta_rule_backward(*x, s0, dev(inp["do"], dtype), dev(inp["dstate"]))
+    ref, _ = delta.backward(*(inp[n] for n in NAMES), inp["state0"], inp["do"], inp["dstate"])
+    ro, rS = recurrence(inp, inp["state0"])
+    for n, got, want in (("o", o, ro), ("state", S, rS), *((n, g[n], ref[n]) for n in GRADS)):
+        most = 2.0 ** -9 if dtype == "bf16" and n in ("o", "dq", "dk", "dv") else RMS
+        if want.any():
+            close(host(got), want, None, 2.0 ** -17 if n == "dlog_decay" else most)
+        else:
+            assert not host(got).any(), n

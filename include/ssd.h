@@ -339,7 +339,8 @@ SSD_API int ssd_linattn_step(const ssd_linattn_dims* dims, const void* q, const 
  * Results do not depend on powers of two in a step's q (and dout for its inverse), or
  * in k and v with beta for the inverse of their square, as long as the largest element
  * of a key is between 2^-63 and 2^63, of a query above 2^-110, beta times the key's
- * square a normal number and v divided by the key's finite.  States are not scaled up further below 2^-87.
+ * square a normal number and v divided by the key's finite.  States are not scaled up
+ * further below 2^-87.
  * States, dlog_decay and dbeta are within a few 2^-22 of their root mean square.  bf16
  * results (o, dq, dk, dv) are off by their own rounding, 0.0017 of their root mean
  * square.
@@ -360,7 +361,9 @@ SSD_API int ssd_delta_rule_forward(const ssd_linattn_dims* dims, const void* q, 
 
 /* Gradients of L = sum(dout * o) + sum(dstate * state); dstate NULL = zero.
  * state0, lens, dstate0 may be NULL; no output may overlap an input.  A group's dq
- * and dk are summed over its heads in head order. */
+ * and dk are summed over its heads in head order.  Infinite or NaN operands of a step
+ * reach the gradients of its chunk and of those before it; of dout in one column of v,
+ * dv and dstate0 in that column alone. */
 SSD_API int ssd_delta_rule_backward(const ssd_linattn_dims* dims, const void* q, const void* k,
                                     const void* v, const float* log_decay, const float* beta,
                                     const float* state0, const void* dout, const float* dstate,

@@ -24,10 +24,10 @@
 // of 32 heads 128/64 (bf16, 175 us; memory alone would take 31) a chunk of 64 steps takes
 // 10 thousand cycles.  The chain has 2.2 of them for the products with the state, 3.4 for
 // the system and 1.7 for the new state; o takes 188 matrix instructions a warp, 84 when
-// one part of the state, P and U was taken (153 us, but o off by 2^-12 of
-// |q| |S|).  Tensor pipe 45 % and issue slots 42 % busy.  The walk that keeps the states takes
-// 144 us, the walk back 232.  fp32 (8 x 1024 steps of 24 heads 64/64): 154 us.  (These and
-// the times below: events around the kernel, caches flushed.)
+// one part of the state, P and U was taken (153 us, but o off by 2^-12 of |q| |S|).
+// Tensor pipe 45 % and issue slots 42 % busy.  The walk that keeps the states takes 144
+// us, the walk back 232.  fp32 (8 x 1024 steps of 24 heads 64/64): 154 us.  (These and the
+// times below: events around the kernel, caches flushed.)
 #include <cuda_bf16.h>
 
 #include "ssd_delta.cuh"
@@ -182,9 +182,9 @@ __device__ __forceinline__ void clear_rows(T* out, long long step, int from, int
 }
 
 // f[n] = X K^T for the C steps of a tile whose rows are steps, X the warp's columns k0
-// ... of the state, scaled; and with kO o[n] = X Q^T.  The right operands of a group of columns are loaded while the group before is multiplied.
-// given(k, a): the state's parts as left operands of columns 16 k ..., as soon as there
-// are any.
+// ... of the state, scaled; and with kO o[n] = X Q^T.  The right operands of a group of
+// columns are loaded while the group before is multiplied.  given(k, a): the state's
+// parts as left operands of columns 16 k ..., as soon as there are any.
 template <int NI, bool kO, int DK, int NK, int NC, typename F>
 __device__ __forceinline__ void state_times(float (&f)[NC][4], float (&o)[NC][4],
                                             const float (&x)[NK][4], const RowScales& s, uint32_t K,
@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers * (helped<NI, DK, WK, kS
   Scratch<C>& scratch = *(Scratch<C>*)(sm + G::kS);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int vblocks = (p.dv + VB - 1) / VB;
-  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = row_of(p.lens, p.B, p.T, tid, (int*)sm);
+  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB;
+  const int b = row_of(p.lens, p.B, p.T, tid, (int*)sm);
   const int width = min(VB, p.dv - v0);
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
@@ -824,7 +825,8 @@ __global__ void __launch_bounds__(kPrep + 32 * kWalkers, 1) k_delta_back(const D
   __shared__ float out_down[2][kVB];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int vblocks = (p.dv + VB - 1) / VB;
-  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB, b = row_of(p.lens, p.B, p.T, tid, (int*)sm);
+  const int h = blockIdx.x / vblocks, v0 = blockIdx.x % vblocks * VB;
+  const int b = row_of(p.lens, p.B, p.T, tid, (int*)sm);
   const int width = min(VB, p.dv - v0);
   int len = p.T;
   if (p.lens) len = min(max(p.lens[b], 0), p.T);
